@@ -31,6 +31,9 @@ Ops (names of the C entry points; aliases with the names of the page
   ``mg_angle_scan_bwd(...) -> (dtheta, dscale, dgamma, db, dh0)``: the angle-fused
   scan (aliases ``angle_scan_fwd``, ``angle_scan_bwd``)
 
+* the selective state space mixer's operators, ``causal_conv_*``, ``selective_scan_*`` and
+  ``group_norm_*`` (see ``ssm.py``)
+
 Every op accepts optional preallocated outputs (``out=(...)``), a workspace
 tensor (``ws=``, uint8, zero-filled before first use) and a stream
 (``stream=``, a ``torch.cuda.Stream``); by default outputs are allocated with
@@ -174,6 +177,8 @@ def load():
                      "mg_linear_scan_varlen_bwd", "mg_affine_scan_h0_fwd",
                      "mg_affine_scan_h0_bwd", "mg_angle_scan_fwd", "mg_angle_scan_bwd"):
             getattr(lib, name).restype = st
+        from . import ssm
+        ssm.declare(lib)
         _lib = lib
     return _lib
 
@@ -720,3 +725,10 @@ affine_scan_h0_fwd = mg_affine_scan_h0_fwd
 affine_scan_h0_bwd = mg_affine_scan_h0_bwd
 angle_scan_fwd = mg_angle_scan_fwd
 angle_scan_bwd = mg_angle_scan_bwd
+
+# The selective mixer's operators (causal_conv_*, selective_scan_*, group_norm_*).
+from . import ssm as _ssm  # noqa: E402
+from .ssm import *  # noqa: E402,F401,F403
+
+__all__ += _ssm.__all__
+SYMBOLS += _ssm.SYMBOLS

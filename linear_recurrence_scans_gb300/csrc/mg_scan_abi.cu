@@ -5,9 +5,9 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
-#include <initializer_list>
 #include <mutex>
 
+#include "abi_checks.cuh"
 #include "common.cuh"
 
 namespace mg {
@@ -25,51 +25,6 @@ mg_status fail(mg_status st, const char *fmt, ...)
 
 namespace {
 
-constexpr int64_t kMaxDim = int64_t(1) << 40;
-
-struct Buf {
-    const void *p;
-    size_t bytes;
-    const char *name;
-    bool output;
-    bool optional = false;   // NULL allowed (the buffer is then not used)
-};
-
-// NULL, alignment and overlap checks.  Outputs may overlap nothing.
-mg_status check_bufs(const char *fn, std::initializer_list<Buf> bufs)
-{
-    for (const Buf &b : bufs) {
-        if (b.p == nullptr && b.optional) continue;
-        if (b.p == nullptr) return fail(MG_ERR_INVALID_ARG, "%s: %s is NULL", fn, b.name);
-        if (reinterpret_cast<uintptr_t>(b.p) % 16 != 0)
-            return fail(MG_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", fn, b.name);
-    }
-    for (const Buf &o : bufs) {
-        if (!o.output || o.p == nullptr) continue;
-        const uintptr_t o0 = reinterpret_cast<uintptr_t>(o.p), o1 = o0 + o.bytes;
-        for (const Buf &x : bufs) {
-            if (&x == &o || x.p == nullptr) continue;
-            const uintptr_t x0 = reinterpret_cast<uintptr_t>(x.p), x1 = x0 + x.bytes;
-            if (o0 < x1 && x0 < o1)
-                return fail(MG_ERR_INVALID_ARG, "%s: output %s overlaps %s", fn, o.name, x.name);
-        }
-    }
-    return MG_OK;
-}
-
-mg_status check_dims(const char *fn, std::initializer_list<int64_t> dims)
-{
-    int64_t prod = 1;
-    for (int64_t d : dims) {
-        if (d < 0) return fail(MG_ERR_INVALID_ARG, "%s: negative size %lld", fn, (long long)d);
-        if (d > kMaxDim) return fail(MG_ERR_UNSUPPORTED, "%s: size %lld too large", fn, (long long)d);
-        if (d > 0 && prod > (int64_t(1) << 58) / d)
-            return fail(MG_ERR_UNSUPPORTED, "%s: tensor too large", fn);
-        prod *= (d > 0 ? d : 1);
-    }
-    return MG_OK;
-}
-
 // The channel-wise kernels index channels with 32-bit integers (a tile's
 // first channel plus the lane's offset): D must stay clear of 2^31.
 constexpr int64_t kMaxChannels = (int64_t(1) << 31) - (int64_t(1) << 16);
@@ -79,16 +34,6 @@ mg_status check_channels(const char *fn, int64_t D)
     if (D > kMaxChannels)
         return fail(MG_ERR_UNSUPPORTED, "%s: D = %lld channels exceeds %lld", fn, (long long)D,
                     (long long)kMaxChannels);
-    return MG_OK;
-}
-
-mg_status check_ws(const char *fn, const void *ws, size_t ws_bytes, size_t need)
-{
-    if (ws == nullptr) return fail(MG_ERR_INVALID_ARG, "%s: workspace is NULL", fn);
-    if (reinterpret_cast<uintptr_t>(ws) % 256 != 0)
-        return fail(MG_ERR_INVALID_ARG, "%s: workspace is not 256-byte aligned", fn);
-    if (ws_bytes < need)
-        return fail(MG_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
     return MG_OK;
 }
 
@@ -163,12 +108,6 @@ mg_status read_status(const char *fn, void *ws, cudaStream_t stream)
                 "a chunk look-back wait gave up (first tile %u); the outputs of that launch are "
                 "unspecified", words[1] ? words[1] - 1 : 0u);
 }
-
-#define MG_TRY(expr)                      \
-    do {                                  \
-        const mg_status st__ = (expr);    \
-        if (st__ != MG_OK) return st__;   \
-    } while (0)
 
 }  // namespace
 }  // namespace mg

@@ -1,0 +1,212 @@
+// Shared by the selective mixer's kernels (causal_conv.cu, selective_scan.cu,
+// group_norm.cu): argument blocks, launchers, sequences and small device
+// helpers.
+#pragma once
+
+#include "abi_checks.cuh"
+#include "common.cuh"
+#include "mg_ssm.h"
+
+namespace mg {
+
+// ------------------------------------------------------------ host side
+
+struct ConvArgs {
+    const void *x, *x0, *dy, *dx_last;
+    int64_t ldx, lddy;
+    const float *w, *bias;
+    const int64_t *cu;
+    int64_t nseq;
+    int silu;
+    void *y, *x_last, *dx, *dx0;
+    float *dw, *dbias;
+    int64_t B, T, D;
+    int W;
+    void *ws;
+};
+size_t conv_ws_bytes(int64_t B, int64_t T, int64_t D, int W);
+mg_status launch_conv_fwd(const ConvArgs &p, mg_dtype dt, cudaStream_t s);
+mg_status launch_conv_bwd(const ConvArgs &p, mg_dtype dt, cudaStream_t s);
+
+struct ConvStepArgs {
+    const void *x;
+    int64_t ldx;
+    const float *w, *bias;
+    void *state;
+    int64_t nslots;
+    const int64_t *slots;
+    int silu;
+    void *y;
+    int64_t B, D;
+    int W;
+};
+mg_status launch_conv_step(const ConvStepArgs &p, mg_dtype dt, cudaStream_t s);
+
+struct SsmArgs {
+    const void *x, *raw, *Bm, *Cm, *dy;
+    int64_t ldx, ldraw, ldb, ldc, lddy;
+    const float *A, *Dskip, *dt_bias, *h0, *dh_last;
+    int softplus;
+    const int64_t *cu;
+    int64_t nseq;
+    void *y;
+    float *h_last, *saved;
+    const float *saved_in;
+    void *dx, *draw, *dBm, *dCm;
+    float *dA, *dDskip, *ddt_bias, *dh0;
+    int64_t B, T, D;
+    int N, G;
+    void *ws;
+};
+constexpr int kSsmMaxN = 64;
+size_t ssm_fwd_ws_bytes(int64_t B, int64_t T, int64_t D, int N, int G, int64_t nseq);
+size_t ssm_bwd_ws_bytes(int64_t B, int64_t T, int64_t D, int N, int G, int64_t nseq);
+size_t ssm_saved_bytes(int64_t B, int64_t T, int64_t D, int N);
+int ssm_saved_rows();
+mg_status launch_ssm_fwd(const SsmArgs &p, mg_dtype dt, cudaStream_t s);
+mg_status launch_ssm_bwd(const SsmArgs &p, mg_dtype dt, cudaStream_t s);
+
+struct SsmStepArgs {
+    const void *x, *raw, *Bm, *Cm;
+    int64_t ldx, ldraw, ldb, ldc;
+    const float *A, *Dskip, *dt_bias;
+    int softplus;
+    float *state;
+    int64_t nslots;
+    const int64_t *slots;
+    void *y;
+    int64_t B, D;
+    int N, G;
+};
+mg_status launch_ssm_step(const SsmStepArgs &p, mg_dtype dt, cudaStream_t s);
+
+struct NormArgs {
+    const void *x, *z, *dy;
+    int64_t ldx, ldz, lddy;
+    const float *w, *bias;
+    float eps;
+    int rms, silu;
+    mg_gate gate;
+    void *y, *dx, *dz;
+    float *stats;
+    const float *stats_in;
+    float *dw, *dbias;
+    int64_t M, D, G;
+    void *ws;
+};
+size_t norm_ws_bytes(int64_t M, int64_t D, int64_t G);
+mg_status launch_norm_fwd(const NormArgs &p, mg_dtype dt, cudaStream_t s);
+mg_status launch_norm_bwd(const NormArgs &p, mg_dtype dt, cudaStream_t s);
+
+// out[i] = sum_j part[j * stride + i], i < n, j in order: the last step of the
+// sums over rows, in a fixed order.
+mg_status launch_sum_parts(const float *part, int64_t parts, int64_t stride, int64_t n, float *out,
+                           cudaStream_t s);
+
+inline mg_status launched(const char *what)
+{
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? MG_OK : fail(MG_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
+}
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// ---------------------------------------------------------- device side
+
+// One value of an activation tensor.
+__device__ __forceinline__ float load1(const float *p) { return *p; }
+__device__ __forceinline__ float load1(const bf16_t *p) { return bf16_bits_to_float(p->bits); }
+__device__ __forceinline__ void store1(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store1(bf16_t *p, float v)
+{
+    p->bits = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// e^x for x <= 0: 2^(x log2 e) with the product's rounding error (which at
+// |x| near 10 alone would cost a relative 3e-7) carried into the result by
+// one more multiply-add, 2^(h + l) = 2^h (1 + l ln 2) for small l.
+__device__ __forceinline__ float exp_neg(float x)
+{
+    constexpr float kLog2eLo = 1.925963033500e-8f;   // log2 e - float(log2 e)
+    const float h = x * kLog2eF;
+    const float l = fmaf(x, kLog2eLo, fmaf(x, kLog2eF, -h));
+    const float y = ex2_ftz(h);
+    // h = -inf (x = -inf, or beyond range) makes l NaN; y is then 0
+    return h < -150.f ? 0.f : fmaf(y, l * 0.69314718f, y);
+}
+
+// With e = e^-|v|: softplus(v) = max(v, 0) + log(1 + e) and sigmoid(v).
+// log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by the odd power series
+// of atanh (the first term left out is below 2e-8 of the sum): relative
+// accuracy holds for small e too, where 1 + e would round e away.
+__device__ __forceinline__ float softplus_f(float v, float &sig)
+{
+    const float e = exp_neg(-fabsf(v));
+    const float s = __fdividef(e, 2.f + e);
+    const float q = s * s;
+    float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
+    p = fmaf(q, p, 1.f / 9.f);
+    p = fmaf(q, p, 1.f / 7.f);
+    p = fmaf(q, p, 1.f / 5.f);
+    p = fmaf(q, p, 1.f / 3.f);
+    p = fmaf(q, p, 1.f);
+    const float r = __fdividef(1.f, 1.f + e);
+    sig = v >= 0.f ? r : e * r;
+    return fmaxf(v, 0.f) + 2.f * s * p;
+}
+
+// sigmoid(v) = e^min(v,0) / (1 + e^-|v|).
+__device__ __forceinline__ float sigmoid_f(float v)
+{
+    const float e = exp_neg(-fabsf(v));
+    return __fdividef(v >= 0.f ? 1.f : e, 1.f + e);
+}
+
+// The sequences of the flattened rows 0 .. B*T-1 of a batch: offsets from
+// cu_seqlens, or B sequences of T rows.
+struct Seqs {
+    const long long *cu;
+    long long T;       // rows of a dense sequence
+    long long rows;    // all rows
+    int nseq;
+    __device__ __forceinline__ long long begin(int s) const
+    {
+        return cu != nullptr ? __ldg(cu + s) : (long long)s * T;
+    }
+    // The sequence that holds row r: the last s with begin(s) <= r.
+    __device__ __forceinline__ int of(long long r) const
+    {
+        if (cu == nullptr) return int(r / T);
+        int lo = 0, hi = nseq;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (__ldg(cu + mid) <= r) lo = mid; else hi = mid;
+        }
+        return lo;
+    }
+};
+
+// Called by the threads of one block: sets the workspace's error bit if cu
+// is not non-decreasing from 0 to rows.
+__device__ __forceinline__ void check_cu(const Seqs &q, unsigned *err, int tid, int threads)
+{
+    if (q.cu == nullptr) return;
+    bool bad = false;
+    for (int s = tid; s < q.nseq; s += threads) {
+        const long long a = __ldg(q.cu + s), b = __ldg(q.cu + s + 1);
+        bad = bad || b < a || (s == 0 && a != 0) || (s + 1 == q.nseq && b != q.rows);
+    }
+    if (bad) atomicOr(err, kErrBadSeqlens);
+}
+
+inline Seqs make_seqs(const int64_t *cu, int64_t B, int64_t T, int64_t nseq)
+{
+    return Seqs{reinterpret_cast<const long long *>(cu), T, B * T, int(nseq)};
+}
+
+__device__ __forceinline__ unsigned *error_word(void *ws)
+{
+    return &static_cast<Control *>(ws)->error;
+}
+
+}  // namespace mg
