@@ -12,6 +12,13 @@
 namespace mg {
 namespace {
 
+#ifndef MG_SSM_WHOLE
+#define MG_SSM_WHOLE 256
+#endif
+#ifndef MG_SSM_BLOCKS
+#define MG_SSM_BLOCKS 608
+#endif
+
 constexpr int kS = 4;         // states of a thread
 constexpr int kSeg = 16;      // rows between two saved states
 constexpr int kThreads = 128;
@@ -46,63 +53,449 @@ struct Tile {
     int64_t width;    // channels of a group
 };
 
-template <typename T, int L>
-__global__ void __launch_bounds__(kThreads) ssm_fwd_kernel(SsmArgs p, Seqs q, Tile tl)
+// ------------------------------------------------------- pairs of floats
+// Two float32 in one 64-bit register pair: one instruction multiplies and
+// adds both.
+using pair_t = unsigned long long;
+
+__device__ __forceinline__ pair_t pack2(float a, float b)
 {
-    constexpr int kCh = kThreads / L;
+    pair_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(pair_t p, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c)
+{
+    pair_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b)
+{
+    pair_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// The decay e^(delta A) = 2^(delta A log2 e) of two states.  ex2.approx comes
+// out low by a relative 1.1e-8 on average for small exponents (measured), and
+// a state that lives for 1 / (1 - a) rows would add that up; kDecayBias in
+// the exponent, at no cost in the multiply-add, takes it out.  For larger
+// exponents it is below their last bit, and the state is short-lived.
+constexpr float kDecayBias = 1.6e-8f;
+
+__device__ __forceinline__ pair_t decay2(pair_t delta, pair_t A2)
+{
+    float a, b;
+    unpack2(fma2(delta, A2, pack2(kDecayBias, kDecayBias)), a, b);
+    return pack2(ex2_ftz(a), ex2_ftz(b));
+}
+
+// ------------------------------------------------------------ chunk geometry
+
+// Time is cut into chunks of `len` rows (a multiple of kSeg), `n` of them for
+// a batch entry; block -> (tile, chunk, entry), tiles fastest.
+struct Chunks {
+    int64_t len;
+    int64_t n;
+};
+
+constexpr int kTile = 16;   // rows of a staged tile
+
+// How a thread block covers channels: a thread has S states of C channels,
+// L lanes a channel.
+template <int S_, int L_, int C_>
+struct Cover {
+    static constexpr int S = S_, L = L_, C = C_;
+    static constexpr int NP = S * L;                       // states with padding
+    static constexpr int kGroups = 32 / L;                 // channel groups of a warp
+    static constexpr int kCh = kThreads / 32 * kGroups * C;  // channels of a block
+};
+
+// The (delta, u) pairs of a tile row lie as float4 of two channels; XORing
+// the float4's index with bits of its octet spreads the staging writes (four
+// consecutive float4 a thread) over all banks and leaves each octet's reads
+// in one row of banks.
+__device__ __forceinline__ int du_index(int ch) { return ((ch >> 1) ^ ((ch >> 4) & 3)) * 2 + (ch & 1); }
+
+// Sum over the L lanes of a channel (lane bits 32/L .. 16) of G values each,
+// G >= L: the lane of state group sl ends with values sl*G/L .. of v.
+template <int G, int L>
+__device__ __forceinline__ void spread_sum(float (&v)[G], int sl)
+{
+#pragma unroll
+    for (int m = L / 2, w = G / 2; m > 0; m >>= 1, w >>= 1) {
+        const bool up = (sl & m) != 0;
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float keep = up ? v[i + w] : v[i], give = up ? v[i] : v[i + w];
+            v[i] = keep + __shfl_xor_sync(~0u, give, m * (32 / L));
+        }
+    }
+}
+
+// A thread's S states of one channel.
+template <int S>
+__device__ __forceinline__ void load_group(const float *p, int n0, int N, float (&o)[S])
+{
+    if (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < S; i += 4) {
+            const float4 v = n0 + i < N ? *reinterpret_cast<const float4 *>(p + n0 + i)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+            o[i] = v.x, o[i + 1] = v.y, o[i + 2] = v.z, o[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < S; ++i) o[i] = n0 + i < N ? p[n0 + i] : 0.f;
+    }
+}
+template <int S>
+__device__ __forceinline__ void store_group(float *p, int n0, int N, const float (&o)[S])
+{
+    if (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < S; i += 4)
+            if (n0 + i < N)
+                *reinterpret_cast<float4 *>(p + n0 + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+            if (n0 + i < N) p[n0 + i] = o[i];
+    }
+}
+template <int S>
+__device__ __forceinline__ void store_pairs(float *p, int n0, int N, const pair_t (&h)[S / 2])
+{
+    float o[S];
+#pragma unroll
+    for (int i = 0; i < S / 2; ++i) unpack2(h[i], o[2 * i], o[2 * i + 1]);
+    store_group<S>(p, n0, N, o);
+}
+
+// ------------------------------------------------------------------ forward
+//
+// Two passes where time is cut: the first runs the recurrence of each chunk
+// from 0 (from h0 at a sequence's start) and leaves its last state and its
+// sum of delta; the second folds those of the chunks since its sequence's
+// start into its own first state,
+//   h <- exp(A sum_j delta) h + h_j,
+// and runs the recurrence again with the outputs.  No block waits for
+// another, and the order of every sum is fixed.
+//
+// A tile of kTile rows is staged at a time: the block's threads load x and
+// raw for the next tile into registers while it works on this one, turn them
+// into (delta, u) pairs in shared memory (softplus once for each row and
+// channel), and the threads' recurrences read them from there, B and C next
+// to them.  Rows past the chunk are staged as delta = u = 0, B = C = 0: the
+// state passes through them.
+//
+// Per row and state: 4 float32 multiply-adds (2 instructions for a pair's
+// 4) and one 2^x; 64 pairs and 32 2^x a clock and SM, so both pipes ask for
+// the same time, and shared memory (2.1 or 3.9 clocks for a 16-byte load of a
+// warp, by pattern) and the issue slots are close behind: a thread's S x C
+// block of 8 x 2 states loads 5 x 16 bytes for its 16 states' row.
+template <typename T, int VEC, typename CV, bool kFirst>
+__global__ void __launch_bounds__(kThreads)
+ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg_s)
+{
+    constexpr int S = CV::S, L = CV::L, C = CV::C, NP = CV::NP, CH = CV::kCh, SP = S / 2;
+    constexpr int kVecs = kTile * CH / VEC;                         // vectors of a tile
+    constexpr int kPer = (kVecs + kThreads - 1) / kThreads;         // of a thread
+    constexpr int kBc = (kTile * NP + kThreads - 1) / kThreads;     // values of B (or C) of a thread
+    constexpr int G = L > 4 ? L : 4;                                // rows between two sums over lanes
+    __shared__ __align__(16) float2 s_du[kTile][CH];
+    __shared__ __align__(16) float s_b[kTile][NP], s_c[kFirst ? 1 : kTile][NP];
+    __shared__ __align__(16) float s_y[kFirst ? 1 : kTile][CH];
+
     const int64_t all_tiles = tl.tiles * p.G;
-    const int64_t tile = blockIdx.x % all_tiles;
-    const int s = int(blockIdx.x / all_tiles);
-    if (blockIdx.x == 0) check_cu(q, error_word(p.ws), threadIdx.x, kThreads);
+    const int64_t tile = blockIdx.x % all_tiles, rest = blockIdx.x / all_tiles;
+    const int64_t nch = kFirst ? ck.n - 1 : ck.n;                   // the last chunk has no successor
+    const int64_t k = rest % nch, b = rest / nch;
+    const int64_t rowb = b * p.T;
+    const int64_t t0 = k * ck.len, t1 = t0 + ck.len < p.T ? t0 + ck.len : p.T;
     const int g = int(tile / tl.tiles);
-    const int64_t c = (tile % tl.tiles) * kCh + threadIdx.x / L;
-    const bool live = c < tl.width;
-    const int64_t d = g * tl.width + (live ? c : 0);
-    const int sl = threadIdx.x % L, n0 = sl * kS;
-    long long lo = q.begin(s), hi = q.begin(s + 1);
-    lo = lo < 0 ? 0 : lo;
-    hi = hi > q.rows ? q.rows : hi;
-    float A2[kS], h[kS];
-    load_states(p.A + d * p.N, n0, p.N, A2);
+    const int64_t c0 = (tile % tl.tiles) * CH, d0 = g * tl.width + c0;   // the tile's first channel
+    const int64_t wide = tl.width - c0 < CH ? tl.width - c0 : CH;        // its channels
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int sl = lane / CV::kGroups, n0 = sl * S;
+    const int ch = (warp * CV::kGroups + lane % CV::kGroups) * C;        // the thread's first channel
+
+    // The thread's channels.  Channels past the tile run on zeros.
+    pair_t A2[C][SP], h[C][SP];
+    float ssum[C];
 #pragma unroll
-    for (int i = 0; i < kS; ++i) A2[i] *= kLog2eF;
-    const int64_t state = (int64_t(s) * p.D + d) * p.N;
+    for (int c = 0; c < C; ++c) {
+        float a[S];
+        const bool live = ch + c < wide;
 #pragma unroll
-    for (int i = 0; i < kS; ++i) h[i] = 0.f;
-    if (p.h0 != nullptr) load_states(p.h0 + state, n0, p.N, h);
-    const float skip = p.Dskip != nullptr ? p.Dskip[d] : 0.f;
-    const float bias = p.dt_bias != nullptr ? p.dt_bias[d] : 0.f;
-    // dense batches save by their own rows, packed ones by packed rows
-    const int64_t base = q.cu != nullptr ? 0 : lo, nseg = (p.T + kSeg - 1) / kSeg;
-    const int64_t save0 = q.cu != nullptr ? 0 : int64_t(s) * nseg;
-    for (int64_t r = lo; r < hi; ++r) {
-        if (p.saved != nullptr && (r - base) % kSeg == 0 && live) {
-            float *o = p.saved + ((save0 + (r - base) / kSeg) * p.D + d) * p.N;
+        for (int i = 0; i < S; ++i) a[i] = 0.f;
+        if (live) load_group<S>(p.A + (d0 + ch + c) * p.N, n0, p.N, a);
 #pragma unroll
-            for (int i = 0; i < kS; ++i)
-                if (n0 + i < p.N) o[n0 + i] = h[i];
+        for (int i = 0; i < SP; ++i) {
+            A2[c][i] = pack2(a[2 * i] * kLog2eF, a[2 * i + 1] * kLog2eF);
+            h[c][i] = 0;
         }
-        const float x = load1(static_cast<const T *>(p.x) + r * p.ldx + d);
-        float slope;
-        const float delta = step_size(load1(static_cast<const T *>(p.raw) + r * p.ldraw + d) + bias,
-                                      p.softplus, slope);
-        const float u = delta * x;
-        float Br[kS], Cr[kS], y = 0.f;
-        load_states(static_cast<const T *>(p.Bm) + r * p.ldb + g * p.N, n0, p.N, Br);
-        load_states(static_cast<const T *>(p.Cm) + r * p.ldc + g * p.N, n0, p.N, Cr);
+        ssum[c] = 0.f;
+    }
+    auto start_state = [&](int s) {
 #pragma unroll
-        for (int i = 0; i < kS; ++i) {
-            h[i] = fmaf(ex2_sub(delta * A2[i]), h[i], u * Br[i]);
-            y = fmaf(Cr[i], h[i], y);
+        for (int c = 0; c < C; ++c) {
+            float v[S];
+#pragma unroll
+            for (int i = 0; i < S; ++i) v[i] = 0.f;
+            if (p.h0 != nullptr && ch + c < wide)
+                load_group<S>(p.h0 + (int64_t(s) * p.D + d0 + ch + c) * p.N, n0, p.N, v);
+#pragma unroll
+            for (int i = 0; i < SP; ++i) h[c][i] = pack2(v[2 * i], v[2 * i + 1]);
         }
-        y = lane_sum<L>(y);
-        if (live && sl == 0) store1(static_cast<T *>(p.y) + r * p.D + d, fmaf(skip, x, y));
-    }
-    if (p.h_last != nullptr && live) {
+    };
+    int s = q.of(rowb + t0);
+    long long next = q.begin(s + 1) - rowb;                         // where the sequence ends
+    {
+        const long long lo = q.begin(s) - rowb;
+        if (lo >= t0) {
+            start_state(s);
+        } else if (!kFirst) {
+            int64_t j = (lo < 0 ? 0 : lo) / ck.len;
+            const int64_t base = b * (ck.n - 1);
+            bool begin = true;
+            for (; j < k; ++j) {
 #pragma unroll
-        for (int i = 0; i < kS; ++i)
-            if (n0 + i < p.N) p.h_last[state + n0 + i] = h[i];
+                for (int c = 0; c < C; ++c) {
+                    if (ch + c >= wide) continue;
+                    const int64_t at = (base + j) * p.D + d0 + ch + c;
+                    float v[S];
+                    load_group<S>(agg_h + at * p.N, n0, p.N, v);
+                    const float ds = agg_s[at];
+#pragma unroll
+                    for (int i = 0; i < SP; ++i) {
+                        const pair_t hv = pack2(v[2 * i], v[2 * i + 1]);
+                        h[c][i] = begin ? hv : fma2(decay2(pack2(ds, ds), A2[c][i]), h[c][i], hv);
+                    }
+                }
+                begin = false;
+            }
+        }
     }
+
+    // Staging: the thread's vectors of x and raw, and values of B and C.
+    const T *xp = static_cast<const T *>(p.x) + rowb * p.ldx + d0;
+    const T *rp = static_cast<const T *>(p.raw) + rowb * p.ldraw + d0;
+    const T *bp = static_cast<const T *>(p.Bm) + rowb * p.ldb + int64_t(g) * p.N;
+    const T *cp = static_cast<const T *>(p.Cm) + rowb * p.ldc + int64_t(g) * p.N;
+    Raw<T, VEC> xr[kPer], rr[kPer];
+    float br[kBc], cr[kFirst ? 1 : kBc];
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int v = threadIdx.x + i * kThreads;
+            const int64_t row = t + v / (CH / VEC);
+            const int col = v % (CH / VEC) * VEC;
+            xr[i].fill(0.f);
+            rr[i].fill(0.f);
+            if (v < kVecs && row < t1 && col < wide) {
+                xr[i].load(xp + row * p.ldx + col);
+                rr[i].load(rp + row * p.ldraw + col);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBc; ++i) {
+            const int e = threadIdx.x + i * kThreads, n = e % NP;
+            const int64_t row = t + e / NP;
+            const bool in = e < kTile * NP && row < t1 && n < p.N;
+            br[i] = in ? load1(bp + row * p.ldb + n) : 0.f;
+            if (!kFirst) cr[i] = in ? load1(cp + row * p.ldc + n) : 0.f;
+        }
+    };
+
+    // One row of the recurrence from the staged tile; y (without the sum over
+    // lanes) comes back.
+    auto step = [&](int tt, float (&y)[C]) {
+        pair_t B[SP], Cw[SP];
+#pragma unroll
+        for (int i = 0; i < SP; i += 2) {
+            const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(&s_b[tt][n0 + 2 * i]);
+            B[i] = v.x, B[i + 1] = v.y;
+            if (!kFirst) {
+                const ulonglong2 w = *reinterpret_cast<const ulonglong2 *>(&s_c[tt][n0 + 2 * i]);
+                Cw[i] = w.x, Cw[i + 1] = w.y;
+            }
+        }
+        float du[2 * C];
+        if constexpr (C == 2) {
+            const float4 v = *reinterpret_cast<const float4 *>(&s_du[tt][du_index(ch)]);
+            du[0] = v.x, du[1] = v.y, du[2] = v.z, du[3] = v.w;
+        } else {
+            const float2 v = s_du[tt][du_index(ch)];
+            du[0] = v.x, du[1] = v.y;
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const pair_t dd = pack2(du[2 * c], du[2 * c]), uu = pack2(du[2 * c + 1], du[2 * c + 1]);
+            pair_t acc = 0;
+#pragma unroll
+            for (int i = 0; i < SP; ++i) {
+                h[c][i] = fma2(decay2(dd, A2[c][i]), h[c][i], mul2(uu, B[i]));
+                if (!kFirst) acc = i == 0 ? mul2(Cw[i], h[c][i]) : fma2(Cw[i], h[c][i], acc);
+            }
+            if (kFirst) {
+                ssum[c] += du[2 * c];
+            } else {
+                float a, e;
+                unpack2(acc, a, e);
+                y[c] = a + e;
+            }
+        }
+    };
+
+    fetch(t0);
+    for (int64_t t = t0; t < t1; t += kTile) {
+        // the tile's (delta, u), B and C
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int v = threadIdx.x + i * kThreads;
+            const int row = v / (CH / VEC), col = v % (CH / VEC) * VEC;
+            if (kVecs % kThreads == 0 || v < kVecs) {
+                const bool in = t + row < t1 && col < wide;
+                float2 o[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float bias = in && p.dt_bias != nullptr ? __ldg(p.dt_bias + d0 + col + e) : 0.f;
+                    const float r = rr[i][e] + bias;
+                    const float delta = !in ? 0.f : p.softplus ? softplus_f(r) : r;
+                    o[e] = make_float2(delta, delta * xr[i][e]);
+                }
+                if constexpr (VEC % 2 == 0) {
+#pragma unroll
+                    for (int e = 0; e < VEC; e += 2)
+                        *reinterpret_cast<float4 *>(&s_du[row][du_index(col + e)]) =
+                            make_float4(o[e].x, o[e].y, o[e + 1].x, o[e + 1].y);
+                } else {
+                    s_du[row][du_index(col)] = o[0];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBc; ++i) {
+            const int e = threadIdx.x + i * kThreads;
+            if (kTile * NP % kThreads == 0 || e < kTile * NP) {
+                s_b[e / NP][e % NP] = br[i];
+                if (!kFirst) s_c[e / NP][e % NP] = cr[i];
+            }
+        }
+        Raw<T, VEC> xk[kFirst ? 1 : kPer];
+        if (!kFirst) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) xk[i] = xr[i];
+        }
+        __syncthreads();
+        if (t + kTile < t1) fetch(t + kTile);
+        if (!kFirst && p.saved != nullptr && t % kSeg == 0) {
+            const int64_t at = b * ((p.T + kSeg - 1) / kSeg) + t / kSeg;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (ch + c < wide)
+                    store_pairs<S>(p.saved + (at * p.D + d0 + ch + c) * p.N, n0, p.N, h[c]);
+        }
+        const int64_t end = t + kTile < t1 ? t + kTile : t1;
+        auto last_state = [&]() {
+            if (kFirst || p.h_last == nullptr) return;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                if (ch + c < wide)
+                    store_pairs<S>(p.h_last + (int64_t(s) * p.D + d0 + ch + c) * p.N, n0, p.N, h[c]);
+        };
+        if (next >= end) {   // no sequence begins inside the tile
+#pragma unroll 1
+            for (int tt = 0; tt < kTile; tt += G) {
+                float y[C][G];
+#pragma unroll
+                for (int i = 0; i < G; ++i) {
+                    float v[C];
+                    step(tt + i, v);
+#pragma unroll
+                    for (int c = 0; c < C; ++c) y[c][i] = kFirst ? 0.f : v[c];
+                }
+                if (!kFirst) {
+#pragma unroll
+                    for (int c = 0; c < C; ++c) spread_sum<G, L>(y[c], sl);
+#pragma unroll
+                    for (int i = 0; i < G / L; ++i) {
+                        float *o = &s_y[tt + sl * (G / L) + i][ch];
+                        if constexpr (C == 2) *reinterpret_cast<float2 *>(o) = make_float2(y[0][i], y[1][i]);
+                        else o[0] = y[0][i];
+                    }
+                }
+            }
+            if (next == end) last_state();
+        } else {
+#pragma unroll 1
+            for (int tt = 0; tt < int(end - t); ++tt) {
+                if (t + tt == next) {
+                    ++s;
+                    while (s + 1 < q.nseq && q.begin(s + 1) - rowb <= t + tt) ++s;   // empty ones
+                    if (s >= q.nseq) s = q.nseq - 1;
+                    next = q.begin(s + 1) - rowb;
+                    start_state(s);
+                }
+                float y[C];
+                step(tt, y);
+                if (!kFirst) {
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        float v = y[c];
+#pragma unroll
+                        for (int m = CV::kGroups; m < 32; m <<= 1) v += __shfl_xor_sync(~0u, v, m);
+                        if (sl == 0) s_y[tt][ch + c] = v;
+                    }
+                }
+                if (t + tt + 1 == next) last_state();
+            }
+        }
+        __syncthreads();
+        if (!kFirst) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int v = threadIdx.x + i * kThreads;
+                const int row = v / (CH / VEC), col = v % (CH / VEC) * VEC;
+                if (v < kVecs && t + row < t1 && col < wide) {
+                    float o[VEC];
+                    load_vec<VEC>(&s_y[row][col], o);
+                    if (p.Dskip != nullptr) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) o[e] = fmaf(__ldg(p.Dskip + d0 + col + e), xk[i][e], o[e]);
+                    }
+                    store_out<VEC>(static_cast<T *>(p.y) + (rowb + t + row) * p.D + d0 + col, o);
+                }
+            }
+        }
+    }
+    if (kFirst) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if (ch + c < wide) {
+                const int64_t at = (b * (ck.n - 1) + k) * p.D + d0 + ch + c;
+                store_pairs<S>(agg_h + at * p.N, n0, p.N, h[c]);
+                if (sl == 0) agg_s[at] = ssum[c];
+            }
+    }
+}
+
+// Packed batches: checks cu_seqlens, and an empty sequence's last state is
+// its first (its dh0 is dh_last): dst[s] = src[s], or 0.
+__global__ void __launch_bounds__(256) empty_sequences_kernel(Seqs q, float *dst, const float *src,
+                                                              int64_t n, unsigned *err)
+{
+    if (blockIdx.x == 0) check_cu(q, err, threadIdx.x, blockDim.x);
+    if (dst == nullptr) return;
+    for (int64_t s = blockIdx.x; s < q.nseq; s += gridDim.x)
+        if (q.begin(int(s)) >= q.begin(int(s) + 1))
+            for (int64_t i = threadIdx.x; i < n; i += blockDim.x) dst[s * n + i] = src != nullptr ? src[s * n + i] : 0.f;
 }
 
 // Gradients of one sequence and tile, from its last saved segment to its
@@ -298,13 +691,84 @@ Tile tile_for(int64_t D, int N, int G)
     return t;
 }
 
-template <typename T, int L>
-mg_status fwd(const SsmArgs &p, cudaStream_t s)
+// Where the forward cuts time, and how many channels a thread has.
+struct Plan {
+    int channels;    // C
+    Chunks ck;
+};
+
+constexpr int64_t kMinChunk = 128;   // rows
+
+// Lanes of a channel: 8 states a thread, 4 for N <= 8.
+int forward_lanes(int N) { return N <= 16 ? 2 : N <= 32 ? 4 : 8; }
+
+Plan forward_plan(int64_t B, int64_t T, int64_t D, int N, int G)
 {
-    const Tile t = tile_for(p.D, p.N, p.G);
+    const int L = forward_lanes(N);
+    auto blocks = [&](int C) { return B * G * ceil_div(D / G, kThreads / L * C); };
+    Plan f;
+    f.channels = 2;
+    f.ck.n = 1;
+    if (blocks(2) < MG_SSM_WHOLE) {
+        if (blocks(1) >= MG_SSM_WHOLE) {
+            f.channels = 1;
+        } else {
+            f.ck.n = ceil_div(MG_SSM_BLOCKS, blocks(2));
+        }
+    }
+    const int64_t most = ceil_div(T, kMinChunk);
+    f.ck.n = f.ck.n < most ? f.ck.n : most;
+    f.ck.len = ceil_div(ceil_div(T, f.ck.n), kSeg) * kSeg;
+    f.ck.n = ceil_div(T, f.ck.len);
+    return f;
+}
+
+template <typename T, int VEC, typename CV>
+mg_status fwd_cover(const SsmArgs &p, const Plan &f, cudaStream_t s)
+{
+    const Tile t{ceil_div(p.D / p.G, CV::kCh), p.D / p.G};
     const Seqs q = make_seqs(p.cu, p.B, p.T, p.nseq);
-    ssm_fwd_kernel<T, L><<<unsigned(t.tiles * p.G * p.nseq), kThreads, 0, s>>>(p, q, t);
+    float *agg_h = reinterpret_cast<float *>(static_cast<char *>(p.ws) + kControlBytes);
+    float *agg_s = agg_h + p.B * (f.ck.n - 1) * p.D * p.N;
+    const int64_t tiles = t.tiles * p.G * p.B;
+    if (p.cu != nullptr) {
+        const int64_t n = p.D * p.N;
+        empty_sequences_kernel<<<unsigned(p.nseq < 1024 ? p.nseq : 1024), 256, 0, s>>>(
+            q, p.h_last, p.h0, n, &static_cast<Control *>(p.ws)->error);
+        MG_TRY(launched("mg_selective_scan_fwd"));
+    }
+    if (f.ck.n > 1) {
+        ssm_chunk_kernel<T, VEC, CV, true><<<unsigned(tiles * (f.ck.n - 1)), kThreads, 0, s>>>(
+            p, q, t, f.ck, agg_h, agg_s);
+        MG_TRY(launched("mg_selective_scan_fwd"));
+    }
+    ssm_chunk_kernel<T, VEC, CV, false><<<unsigned(tiles * f.ck.n), kThreads, 0, s>>>(p, q, t, f.ck, agg_h, agg_s);
     return launched("mg_selective_scan_fwd");
+}
+
+template <typename T, int VEC, int S, int L>
+mg_status fwd_lanes(const SsmArgs &p, cudaStream_t s)
+{
+    const Plan f = forward_plan(p.B, p.T, p.D, p.N, p.G);
+    if (f.channels == 2) return fwd_cover<T, VEC, Cover<S, L, 2>>(p, f, s);
+    return fwd_cover<T, VEC, Cover<S, L, 1>>(p, f, s);
+}
+
+template <typename T, int VEC>
+mg_status fwd_vec(const SsmArgs &p, cudaStream_t s)
+{
+    if (p.N <= 8) return fwd_lanes<T, VEC, 4, 2>(p, s);
+    switch (forward_lanes(p.N)) {
+    case 2: return fwd_lanes<T, VEC, 8, 2>(p, s);
+    case 4: return fwd_lanes<T, VEC, 8, 4>(p, s);
+    default: return fwd_lanes<T, VEC, 8, 8>(p, s);
+    }
+}
+
+// 16-byte vectors of x and raw where the rows and the groups' channels allow.
+bool wide_rows(const SsmArgs &p, int vec)
+{
+    return p.D / p.G % vec == 0 && p.ldx % vec == 0 && p.ldraw % vec == 0;
 }
 
 template <typename T, int L>
@@ -349,7 +813,11 @@ mg_status step(const SsmStepArgs &p, cudaStream_t s)
 
 }  // namespace
 
-size_t ssm_fwd_ws_bytes(int64_t, int64_t, int64_t, int, int, int64_t) { return kControlBytes; }
+size_t ssm_fwd_ws_bytes(int64_t B, int64_t T, int64_t D, int N, int G, int64_t)
+{
+    const Plan f = forward_plan(B, T, D, N, G);
+    return kControlBytes + sizeof(float) * B * (f.ck.n - 1) * D * (N + 1);
+}
 
 size_t ssm_bwd_ws_bytes(int64_t B, int64_t T, int64_t D, int N, int G, int64_t nseq)
 {
@@ -363,7 +831,11 @@ size_t ssm_saved_bytes(int64_t B, int64_t T, int64_t D, int N)
 }
 int ssm_saved_rows() { return kSeg; }
 
-mg_status launch_ssm_fwd(const SsmArgs &p, mg_dtype dt, cudaStream_t s) { MG_SSM(fwd, p, dt, s) }
+mg_status launch_ssm_fwd(const SsmArgs &p, mg_dtype dt, cudaStream_t s)
+{
+    if (dt == MG_F32) return wide_rows(p, 4) ? fwd_vec<float, 4>(p, s) : fwd_vec<float, 1>(p, s);
+    return wide_rows(p, 8) ? fwd_vec<bf16_t, 8>(p, s) : fwd_vec<bf16_t, 1>(p, s);
+}
 mg_status launch_ssm_bwd(const SsmArgs &p, mg_dtype dt, cudaStream_t s) { MG_SSM(bwd, p, dt, s) }
 mg_status launch_ssm_step(const SsmStepArgs &p, mg_dtype dt, cudaStream_t s) { MG_SSM(step, p, dt, s) }
 

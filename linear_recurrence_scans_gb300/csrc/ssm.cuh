@@ -122,44 +122,46 @@ __device__ __forceinline__ void store1(bf16_t *p, float v)
     p->bits = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
-// e^x for x <= 0: 2^(x log2 e) with the product's rounding error (which at
-// |x| near 10 alone would cost a relative 3e-7) carried into the result by
-// one more multiply-add, 2^(h + l) = 2^h (1 + l ln 2) for small l.
-__device__ __forceinline__ float exp_neg(float x)
+// e^x for x <= 0.  The rounding of x log2 e costs a relative |x| 2^-24, no
+// more than the rounding of the sum (raw + bias, a convolution) that x is.
+__device__ __forceinline__ float exp_neg(float x) { return ex2_ftz(x * kLog2eF); }
+
+// 1 / x to 1 ulp, x in [1, 2^126).
+__device__ __forceinline__ float rcp_fast(float x) { return __fdividef(1.f, x); }
+
+// log(1 + e), 0 <= e <= 1, as 2 atanh(s), s = e / (2 + e) <= 1/3: relative
+// accuracy for small e too, where 1 + e would round e away.  atanh(s) / s is
+// a polynomial in s^2, fitted at Chebyshev points of [0, 1/9] (relative error
+// 4e-9).
+__device__ __forceinline__ float log1p_unit(float e)
 {
-    constexpr float kLog2eLo = 1.925963033500e-8f;   // log2 e - float(log2 e)
-    const float h = x * kLog2eF;
-    const float l = fmaf(x, kLog2eLo, fmaf(x, kLog2eF, -h));
-    const float y = ex2_ftz(h);
-    // h = -inf (x = -inf, or beyond range) makes l NaN; y is then 0
-    return h < -150.f ? 0.f : fmaf(y, l * 0.69314718f, y);
+    const float s = e * rcp_fast(2.f + e), q = s * s;
+    float p = fmaf(q, 0.14087329f, 0.13980709f);
+    p = fmaf(q, p, 0.20012427f);
+    p = fmaf(q, p, 0.33333158f);
+    p = fmaf(q, p, 1.f);
+    return 2.f * s * p;
 }
 
-// With e = e^-|v|: softplus(v) = max(v, 0) + log(1 + e) and sigmoid(v).
-// log(1 + e) = 2 atanh(s), s = e / (2 + e) <= 1/3, by the odd power series
-// of atanh (the first term left out is below 2e-8 of the sum): relative
-// accuracy holds for small e too, where 1 + e would round e away.
+// softplus(v) = max(v, 0) + log(1 + e^-|v|).
+__device__ __forceinline__ float softplus_f(float v)
+{
+    return fmaxf(v, 0.f) + log1p_unit(exp_neg(-fabsf(v)));
+}
+
+// softplus(v) and its derivative sigmoid(v).
 __device__ __forceinline__ float softplus_f(float v, float &sig)
 {
-    const float e = exp_neg(-fabsf(v));
-    const float s = __fdividef(e, 2.f + e);
-    const float q = s * s;
-    float p = fmaf(q, 1.f / 13.f, 1.f / 11.f);
-    p = fmaf(q, p, 1.f / 9.f);
-    p = fmaf(q, p, 1.f / 7.f);
-    p = fmaf(q, p, 1.f / 5.f);
-    p = fmaf(q, p, 1.f / 3.f);
-    p = fmaf(q, p, 1.f);
-    const float r = __fdividef(1.f, 1.f + e);
+    const float e = exp_neg(-fabsf(v)), r = rcp_fast(1.f + e);
     sig = v >= 0.f ? r : e * r;
-    return fmaxf(v, 0.f) + 2.f * s * p;
+    return fmaxf(v, 0.f) + log1p_unit(e);
 }
 
 // sigmoid(v) = e^min(v,0) / (1 + e^-|v|).
 __device__ __forceinline__ float sigmoid_f(float v)
 {
     const float e = exp_neg(-fabsf(v));
-    return __fdividef(v >= 0.f ? 1.f : e, 1.f + e);
+    return (v >= 0.f ? 1.f : e) * rcp_fast(1.f + e);
 }
 
 // The sequences of the flattened rows 0 .. B*T-1 of a batch: offsets from
