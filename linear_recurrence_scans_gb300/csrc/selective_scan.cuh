@@ -1,0 +1,245 @@
+// Shared by the selective scan's kernels: pairs of floats, the decay, how
+// threads cover channels and states, and how time is cut into chunks.
+#pragma once
+
+#include "ssm.cuh"
+
+namespace mg {
+
+constexpr int kSeg = 16;      // rows between two saved states: a tile of the gradients
+constexpr int kTile = kSeg;
+constexpr int kThreads = 128;
+constexpr float kLn2 = 0.69314718f;
+
+// A block's channels: a tile of one group.
+struct Tile {
+    int64_t tiles;    // tiles of a group
+    int64_t width;    // channels of a group
+};
+
+// ------------------------------------------------------- pairs of floats
+// Two float32 in one 64-bit register pair: one instruction multiplies and
+// adds both.
+using pair_t = unsigned long long;
+
+__device__ __forceinline__ pair_t pack2(float a, float b)
+{
+    pair_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(pair_t p, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c)
+{
+    pair_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b)
+{
+    pair_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ pair_t add2(pair_t a, pair_t b)
+{
+    pair_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// softplus of two values (as softplus_f).
+__device__ __forceinline__ pair_t softplus2(pair_t v)
+{
+    float v0, v1;
+    unpack2(v, v0, v1);
+    const pair_t e = pack2(exp_neg(-fabsf(v0)), exp_neg(-fabsf(v1)));
+    pair_t c = pack2(log1p_coef(9), log1p_coef(9));
+#pragma unroll
+    for (int i = 8; i >= 0; --i) c = fma2(c, e, pack2(log1p_coef(i), log1p_coef(i)));
+    return fma2(e, c, pack2(fmaxf(v0, 0.f), fmaxf(v1, 0.f)));
+}
+
+// The decay e^(delta A) = 2^(delta A log2 e) of two states.  ex2.approx comes
+// out low by a relative 1.1e-8 on average for small exponents (measured), and
+// a state that lives for 1 / (1 - a) rows would add that up; kDecayBias in
+// the exponent, at no cost in the multiply-add, takes it out.  For larger
+// exponents it is below their last bit, and the state is short-lived.
+//
+// The exponents are single multiply-adds on purpose: the SM reads registers
+// for two operands of an instruction a clock, a multiply-add of three
+// different registers runs at 2/3 rate (measured, pairs and singles alike),
+// and a constant third operand is part of a single's instruction (26 against
+// 29 clocks for the core of a warp's row).
+constexpr float kDecayBias = 1.6e-8f;
+
+__device__ __forceinline__ pair_t decay2(float d0, float d1, pair_t A2)
+{
+    float a, b;
+    unpack2(A2, a, b);
+    return pack2(ex2_ftz(fmaf(d0, a, kDecayBias)), ex2_ftz(fmaf(d1, b, kDecayBias)));
+}
+__device__ __forceinline__ pair_t decay2(pair_t d, pair_t A2)
+{
+    float d0, d1;
+    unpack2(d, d0, d1);
+    return decay2(d0, d1, A2);
+}
+
+// ------------------------------------------------------------ chunk geometry
+
+// Time is cut into chunks of `len` rows (a multiple of kSeg), `n` of them for
+// a batch entry; block -> (tile, chunk, entry), tiles fastest.
+struct Chunks {
+    int64_t len;
+    int64_t n;
+};
+
+// How a warp covers channels: a thread has S states of C channels, L lanes a
+// channel.
+template <int S_, int L_, int C_, int THREADS_ = kThreads>
+struct Cover {
+    static constexpr int S = S_, L = L_, C = C_, THREADS = THREADS_;
+    static constexpr int NP = S * L;                         // states with padding
+    static constexpr int kGroups = 32 / L;                   // channel groups of a warp
+    static constexpr int kWarpCh = kGroups * C;              // channels of a warp
+    static constexpr int kCh = THREADS / 32 * kWarpCh;       // channels of a block
+};
+
+// Place of a row's (delta, u) of channel ch, as float2: they lie as float4 of
+// two channels, and XORing the float4's index with its octet and the row
+// spreads the staging writes (four consecutive float4 a lane, several rows an
+// octet of lanes) over the banks; a row's reads stay within their octets.
+template <int WCH>
+__device__ __forceinline__ int du_index(int row, int ch)
+{
+    const int f = ch >> 1;
+    const int x = WCH >= 32 ? ((f >> 3) & 1) | ((row & 1) << 1) : row & (WCH / 2 - 1) & 3;
+    return (f ^ x) * 2 + (ch & 1);
+}
+
+// Sum over the L lanes of a channel (lane bits 32/L .. 16) of G values each,
+// G >= L: the lane of state group sl ends with values sl*G/L .. of v.
+template <int G, int L>
+__device__ __forceinline__ void spread_sum(float (&v)[G], int sl)
+{
+#pragma unroll
+    for (int m = L / 2, w = G / 2; m > 0; m >>= 1, w >>= 1) {
+        const bool up = (sl & m) != 0;
+#pragma unroll
+        for (int i = 0; i < w; ++i) {
+            const float keep = up ? v[i + w] : v[i], give = up ? v[i] : v[i + w];
+            v[i] = keep + __shfl_xor_sync(~0u, give, m * (32 / L));
+        }
+    }
+}
+
+// A thread's S states of one channel.
+template <int S>
+__device__ __forceinline__ void load_group(const float *p, int n0, int N, float (&o)[S])
+{
+    if (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < S; i += 4) {
+            const float4 v = n0 + i < N ? *reinterpret_cast<const float4 *>(p + n0 + i)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+            o[i] = v.x, o[i + 1] = v.y, o[i + 2] = v.z, o[i + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < S; ++i) o[i] = n0 + i < N ? p[n0 + i] : 0.f;
+    }
+}
+template <int S>
+__device__ __forceinline__ void store_group(float *p, int n0, int N, const float (&o)[S])
+{
+    if (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < S; i += 4)
+            if (n0 + i < N)
+                *reinterpret_cast<float4 *>(p + n0 + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+            if (n0 + i < N) p[n0 + i] = o[i];
+    }
+}
+template <int S>
+__device__ __forceinline__ void store_pairs(float *p, int n0, int N, const pair_t (&h)[S / 2])
+{
+    float o[S];
+#pragma unroll
+    for (int i = 0; i < S / 2; ++i) unpack2(h[i], o[2 * i], o[2 * i + 1]);
+    store_group<S>(p, n0, N, o);
+}
+
+// ---------------------------------------------------------- host side
+
+constexpr int64_t kSms = 152;
+
+// The time that an SM's blocks take for a row, by how many there are; more
+// than the last go in turns.
+struct RowTime {
+    double ns[4];
+    int most;   // blocks that an SM holds
+    double first;   // the first pass's time as a part of the second's
+    double of(int64_t blocks) const
+    {
+        const int64_t m = ceil_div(blocks, kSms), rest = m % most;
+        return double(m / most) * ns[most] + ns[rest];
+    }
+};
+
+constexpr int64_t kMinChunk = 128;   // rows
+constexpr double kFoldNs = 500;      // a launch and a step of the fold over chunks
+
+// Cuts T rows into chunks for `blocks` blocks a chunk, so that the two passes
+// together take least: more chunks fill the SMs, and pay a first pass over
+// all but the last of them.
+inline Chunks cut_time(int64_t blocks, int64_t T, const RowTime &r)
+{
+    Chunks best{ceil_div(T, kSeg) * kSeg, 1};
+    double least = double(T) * r.of(blocks);
+    const int64_t most = ceil_div(T, kMinChunk);
+    for (int64_t n = 2; n <= most && blocks * (n - 1) <= 4 * r.most * kSms; ++n) {
+        Chunks ck;
+        ck.len = ceil_div(ceil_div(T, n), kSeg) * kSeg;
+        ck.n = ceil_div(T, ck.len);
+        if (ck.n != n) continue;
+        const double t = double(ck.len) * (r.of(blocks * n) + r.first * r.of(blocks * (n - 1))) + kFoldNs * double(n);
+        if (t < least) {
+            least = t;
+            best = ck;
+        }
+    }
+    return best;
+}
+
+// Dynamic shared memory beyond the default 48 KB.
+template <typename K>
+mg_status allow_shared(K kernel, size_t bytes)
+{
+    if (bytes <= 48 * 1024) return MG_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    return e == cudaSuccess ? MG_OK : fail(MG_ERR_LAUNCH, "selective scan: %s", cudaGetErrorString(e));
+}
+
+// Packed batches: checks cu_seqlens, and gives empty sequences the state that
+// they were given: dst[s] = src[s], or 0 (selective_scan.cu).
+mg_status launch_empty_sequences(const Seqs &q, float *dst, const float *src, int64_t n, void *ws, cudaStream_t s);
+
+// 16-byte vectors of x and raw where the rows and the groups' channels allow.
+inline bool wide_rows(const SsmArgs &p, int vec)
+{
+    return p.D / p.G % vec == 0 && p.ldx % vec == 0 && p.ldraw % vec == 0;
+}
+
+// The gradients by activation type (selective_scan_bwd_*.cu).
+mg_status ssm_bwd_f32(const SsmArgs &p, bool wide, cudaStream_t s);
+mg_status ssm_bwd_bf16(const SsmArgs &p, bool wide, cudaStream_t s);
+
+}  // namespace mg

@@ -1,0 +1,745 @@
+// The selective scan's gradients (see selective_scan.cu for the recurrence):
+// kernels and launchers, instantiated by activation type in
+// selective_scan_bwd_*.cu.
+#pragma once
+
+#include <type_traits>
+
+#include "selective_scan.cuh"
+
+namespace mg {
+
+// With g_r the adjoint of h_r and q_r = a_r g_r what it hands to row r - 1:
+//   g_r = C_r dy_r + q_{r+1},   w_r = g_r a_r h_{r-1},
+//   dC_r += dy_r h_r, dB_r += u_r g_r        (sums over the group's channels)
+//   s1 = sum_n g_r B_r, s2 = sum_n w_r A     (sums over the channel's states)
+//   dx_r = delta_r s1 + Dskip dy_r,  draw_r = (x_r s1 + s2) slope_r,  dA += delta_r w_r
+// Chunks go backwards: a first pass leaves each chunk's q at its first row,
+// started from 0 (from dh_last at a sequence's end), and its sum of delta; the
+// second folds its successors' up to its sequence's end and does the rest.
+//
+// A chunk's tiles of kTile rows are worked on from the last to the first.  The
+// forward saved the state before each tile.  From it one sweep leaves the
+// states before every kSub rows in shared memory; then, kSub rows at a time
+// from the last, the states are computed once more with a_r and a_r h_{r-1}
+// kept in registers for the walk back.  (Kept in shared memory for a whole
+// tile instead, they would ask for more of its bandwidth than the second
+// computation takes of the arithmetic.)
+//
+// Four states of four channels are a thread's: the sums over channels (8
+// values of dB and dC over the warp's channel lanes) and over states (s1 and
+// s2 of 4 channels) then take 13 shuffles a row, fewer than any other split
+// of 16, and are halved at each step.  Pairs are of neighbouring channels.
+// The lane that a channel's s1 and s2 end at writes its dx and draw and sums
+// its dDskip and ddt_bias.  Each warp stages its own channels; the block's
+// warps meet once a tile to add their dB and dC.
+constexpr int kSub = 4;
+
+// v over LANES lanes (bits STRIDE .. of the lane index; `id` is the lane's
+// place among them): while there are several values, each lane hands half of
+// them over.  V >= LANES: lane id ends with values id V/LANES .. of the sum in
+// v[0 .. V/LANES - 1]; else with value id V / LANES.
+template <int V, int LANES, int STRIDE>
+__device__ __forceinline__ void halve_sum(float (&v)[V], int id)
+{
+    int w = V / 2;
+#pragma unroll
+    for (int m = LANES / 2; m > 0; m >>= 1, w >>= 1) {
+        if (w > 0) {
+            const bool up = (id & m) != 0;
+#pragma unroll
+            for (int i = 0; i < w; ++i) {
+                const float keep = up ? v[i + w] : v[i], give = up ? v[i] : v[i + w];
+                v[i] = keep + __shfl_xor_sync(~0u, give, m * STRIDE);
+            }
+        } else {
+            v[0] += __shfl_xor_sync(~0u, v[0], m * STRIDE);
+        }
+    }
+}
+
+// The block's place in the gradient passes.
+template <int CH>
+struct Spot {
+    int64_t tile, k, b, rowb, t0, t1, d0, wide;
+    int g;
+    __device__ __forceinline__ Spot(const SsmArgs &p, const Tile &tl, const Chunks &ck, bool first)
+    {
+        const int64_t all_tiles = tl.tiles * p.G;
+        const int64_t at = blockIdx.x % all_tiles, rest = blockIdx.x / all_tiles;
+        const int64_t nch = first ? ck.n - 1 : ck.n;      // the first chunk has nothing before it
+        k = rest % nch + (first ? 1 : 0);
+        b = rest / nch;
+        rowb = b * p.T;
+        t0 = k * ck.len;
+        t1 = t0 + ck.len < p.T ? t0 + ck.len : p.T;
+        g = int(at / tl.tiles);
+        tile = at % tl.tiles;
+        d0 = g * tl.width + tile * CH;
+        wide = tl.width - tile * CH < CH ? tl.width - tile * CH : CH;
+    }
+};
+
+// The sequences at a tile's rows, found only for tiles that hold a first or
+// last row of one: the sequence that row starts / ends there, or -1.
+__device__ __forceinline__ void edge_rows(const Seqs &q, int64_t rowb, int64_t ta, int rows,
+                                          int (&first)[kTile], int (&last)[kTile])
+{
+    const int i = threadIdx.x;
+    if (i >= kTile) return;
+    int f = -1, e = -1;
+    if (i < rows) {
+        const long long r = rowb + ta + i;
+        const int s = q.of(r);
+        if (q.begin(s) == r) f = s;
+        if (q.begin(s + 1) == r + 1) e = s;
+    }
+    first[i] = f;
+    last[i] = e;
+}
+
+// A thread's 4 x 4 states of float arrays (.., D, N), as channel pairs.
+template <int S>
+__device__ __forceinline__ void load_block(const float *base, int64_t d, int ch, int64_t wide, int n0,
+                                           int N, pair_t (&o)[S][2])
+{
+    float v[4][S];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+#pragma unroll
+        for (int i = 0; i < S; ++i) v[c][i] = 0.f;
+        if (base != nullptr && ch + c < wide) load_group<S>(base + (d + c) * N, n0, N, v[c]);
+    }
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+        o[i][0] = pack2(v[0][i], v[1][i]);
+        o[i][1] = pack2(v[2][i], v[3][i]);
+    }
+}
+template <int S>
+__device__ __forceinline__ void store_block(float *base, int64_t d, int ch, int64_t wide, int n0, int N,
+                                            const pair_t (&o)[S][2])
+{
+    float v[4][S];
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+        unpack2(o[i][0], v[0][i], v[1][i]);
+        unpack2(o[i][1], v[2][i], v[3][i]);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (ch + c < wide) store_group<S>(base + (d + c) * N, n0, N, v[c]);
+}
+
+__device__ __forceinline__ pair_t dup2(float a) { return pack2(a, a); }
+
+// First pass: q at the first row of chunks 1 .. n-1.
+template <typename T, int VEC, typename CV>
+__global__ void __launch_bounds__(CV::THREADS)
+ssm_adjoint_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_q, float *agg_s)
+{
+    constexpr int S = CV::S, NP = CV::NP, CH = CV::kCh;
+    constexpr int kVecs = kTile * CH / VEC, kPer = (kVecs + CV::THREADS - 1) / CV::THREADS;
+    constexpr int kBc = (kTile * NP + CV::THREADS - 1) / CV::THREADS;
+    __shared__ __align__(16) float s_d[kTile][CH], s_dy[kTile][CH], s_c[kTile][NP];
+    __shared__ int s_last[kTile], s_first[kTile];
+    const Spot<CH> w(p, tl, ck, true);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int sl = lane / CV::kGroups, n0 = sl * S;
+    const int ch = (warp * CV::kGroups + lane % CV::kGroups) * 4;
+    pair_t A2[S][2], ag[S][2];
+    load_block<S>(p.A, w.d0 + ch, ch, w.wide, n0, p.N, A2);
+    float ssum[4] = {};
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            A2[i][c] = mul2(A2[i][c], dup2(kLog2eF));
+            ag[i][c] = 0;
+        }
+    const T *rp = static_cast<const T *>(p.raw) + w.rowb * p.ldraw + w.d0;
+    const T *yp = static_cast<const T *>(p.dy) + w.rowb * p.lddy + w.d0;
+    const T *cp = static_cast<const T *>(p.Cm) + w.rowb * p.ldc + int64_t(w.g) * p.N;
+    Raw<T, VEC> rr[kPer], yr[kPer];
+    float cr[kBc];
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int v = threadIdx.x + i * CV::THREADS;
+            const int64_t row = t + v / (CH / VEC);
+            const int col = v % (CH / VEC) * VEC;
+            rr[i].fill(0.f);
+            yr[i].fill(0.f);
+            if (v < kVecs && row < w.t1 && col < w.wide) {
+                rr[i].load(rp + row * p.ldraw + col);
+                yr[i].load(yp + row * p.lddy + col);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBc; ++i) {
+            const int e = threadIdx.x + i * CV::THREADS, n = e % NP;
+            const int64_t row = t + e / NP;
+            cr[i] = e < kTile * NP && row < w.t1 && n < p.N ? load1(cp + row * p.ldc + n) : 0.f;
+        }
+    };
+    int64_t t = w.t0 + (w.t1 - 1 - w.t0) / kTile * kTile;
+    int s = q.of(w.rowb + w.t1 - 1);
+    long long lo = q.begin(s) - w.rowb, hi = q.begin(s + 1) - w.rowb;
+    fetch(t);
+    for (; t >= w.t0; t -= kTile) {
+        const int64_t end = t + kTile < w.t1 ? t + kTile : w.t1;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int v = threadIdx.x + i * CV::THREADS;
+            const int row = v / (CH / VEC), col = v % (CH / VEC) * VEC;
+            if (kVecs % CV::THREADS == 0 || v < kVecs) {
+                const bool in = t + row < w.t1 && col < w.wide;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const float bias = in && p.dt_bias != nullptr ? __ldg(p.dt_bias + w.d0 + col + e) : 0.f;
+                    const float r = rr[i][e] + bias;
+                    s_d[row][col + e] = !in ? 0.f : p.softplus ? softplus_f(r) : r;
+                    s_dy[row][col + e] = yr[i][e];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kBc; ++i) {
+            const int e = threadIdx.x + i * CV::THREADS;
+            if (kTile * NP % CV::THREADS == 0 || e < kTile * NP) s_c[e / NP][e % NP] = cr[i];
+        }
+        const bool edges = lo >= t || hi == end;
+        if (edges) edge_rows(q, w.rowb, t, int(end - t), s_first, s_last);
+        __syncthreads();
+        if (t > w.t0) fetch(t - kTile);
+#pragma unroll 4
+        for (int tt = kTile - 1; tt >= 0; --tt) {
+            if (edges && s_last[tt] >= 0) {
+                load_block<S>(p.dh_last != nullptr ? p.dh_last + int64_t(s_last[tt]) * p.D * p.N : nullptr,
+                              w.d0 + ch, ch, w.wide, n0, p.N, ag);
+            }
+            const float4 d4 = *reinterpret_cast<const float4 *>(&s_d[tt][ch]);
+            const ulonglong2 y2 = *reinterpret_cast<const ulonglong2 *>(&s_dy[tt][ch]);
+            const float4 c4 = *reinterpret_cast<const float4 *>(&s_c[tt][n0]);
+            const pair_t dl[2] = {pack2(d4.x, d4.y), pack2(d4.z, d4.w)}, dy[2] = {y2.x, y2.y};
+            const float cv[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    ag[i][c] = mul2(decay2(dl[c], A2[i][c]), fma2(dup2(cv[i]), dy[c], ag[i][c]));
+            ssum[0] += d4.x, ssum[1] += d4.y, ssum[2] += d4.z, ssum[3] += d4.w;
+        }
+        if (lo >= t && t > w.t0) {
+            s = q.of(w.rowb + t - 1);
+            lo = q.begin(s) - w.rowb;
+        }
+        hi = q.begin(s + 1) - w.rowb;
+        __syncthreads();
+    }
+    const int64_t at = (w.b * (ck.n - 1) + w.k - 1) * p.D;
+    store_block<S>(agg_q + at * p.N, w.d0 + ch, ch, w.wide, n0, p.N, ag);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (sl == 0 && ch + c < w.wide) agg_s[at + w.d0 + ch + c] = ssum[c];
+}
+
+// s1 and s2 of four channels over LANES lanes (bits STRIDE ..): lane id ends
+// with the sums of channels id 4/LANES .. (or id / (LANES/4)) in a[0], b[0], ..
+template <int LANES, int STRIDE>
+__device__ __forceinline__ void halve_channels(float (&a)[4], float (&b)[4], int id)
+{
+    int w = 2;
+#pragma unroll
+    for (int m = LANES / 2; m > 0; m >>= 1, w >>= 1) {
+        if (w > 0) {
+            const bool up = (id & m) != 0;
+#pragma unroll
+            for (int i = 0; i < w; ++i) {
+                const float ka = up ? a[i + w] : a[i], ga = up ? a[i] : a[i + w];
+                const float kb = up ? b[i + w] : b[i], gb = up ? b[i] : b[i + w];
+                a[i] = ka + __shfl_xor_sync(~0u, ga, m * STRIDE);
+                b[i] = kb + __shfl_xor_sync(~0u, gb, m * STRIDE);
+            }
+        } else {
+            a[0] += __shfl_xor_sync(~0u, a[0], m * STRIDE);
+            b[0] += __shfl_xor_sync(~0u, b[0], m * STRIDE);
+        }
+    }
+}
+
+// Shared memory of the second pass: a warp's, and the block's.
+template <typename T, int VEC, typename CV>
+struct BwdWarp {
+    static constexpr int WCH = CV::kWarpCh, NP = CV::NP;
+    float d[kTile][WCH], x[kTile][WCH], dy[kTile][WCH], slope[kTile][WCH];
+    float bc[kTile][2][NP];
+    float4 ck[kTile / kSub][4][32];                // states before each kSub rows, by lane
+    float bias[WCH];
+    T raw[3][VEC > 1 ? kTile : 1][WCH];            // the next tile's x, raw, dy as loaded
+    T rawbc[VEC > 1 ? kTile : 1][2][VEC > 1 ? NP : 8];
+};
+template <typename T, int VEC, typename CV>
+struct alignas(16) BwdShared {
+    BwdWarp<T, VEC, CV> warp[CV::THREADS / 32];
+    float red[kTile][CV::THREADS / 32][2 * CV::NP];   // each warp's dB, then dC
+    int first[kTile], last[kTile];
+};
+
+template <typename T, int VEC, typename CV>
+__global__ void __launch_bounds__(CV::THREADS, 2)
+ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const float *agg_s,
+               float *partB, float *partA, float *partD, int bc_wide)
+{
+    constexpr int S = CV::S, L = CV::L, NP = CV::NP, CH = CV::kCh, WCH = CV::kWarpCh, kWarps = CV::THREADS / 32;
+    constexpr int kCols = WCH / VEC, kVecs = kTile * kCols, kPer = (kVecs + 31) / 32;
+    constexpr int kBcCols = NP >= VEC ? NP / VEC : 1;            // vectors of a row of B or C
+    constexpr int kBcVecs = VEC > 1 ? kTile * 2 * kBcCols : 0, kBcPer = (kBcVecs + 31) / 32;
+    constexpr int kG = CV::kGroups;
+    static_assert(S == 4, "four states a thread");
+    extern __shared__ __align__(16) unsigned char shared_bytes[];
+    BwdShared<T, VEC, CV> &block = *reinterpret_cast<BwdShared<T, VEC, CV> *>(shared_bytes);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    BwdWarp<T, VEC, CV> &sm = block.warp[warp];
+    const Spot<CH> w(p, tl, ck, false);
+    const int sl = lane / kG, cg = lane % kG, n0 = sl * S;
+    const int ch = cg * 4;                                       // of the warp's channels
+    const int64_t dw = w.d0 + warp * WCH;                        // the warp's first channel
+    const int wide = int(w.wide - warp * WCH < WCH ? w.wide - warp * WCH : WCH);   // its channels (may be <= 0)
+    const bool vec_n = p.N % 4 == 0;
+
+    pair_t A2[S][2], ag[S][2], dA[S][2];
+    load_block<S>(p.A, dw + ch, ch, wide, n0, p.N, A2);
+#pragma unroll
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            A2[i][c] = mul2(A2[i][c], dup2(kLog2eF));
+            ag[i][c] = dA[i][c] = 0;
+        }
+    for (int i = lane; i < WCH; i += 32)
+        sm.bias[i] = p.dt_bias != nullptr && i < wide ? p.dt_bias[dw + i] : 0.f;
+    // the channels whose outputs are this lane's (lanes that share one: the first writes)
+    constexpr int kOut = L <= 4 ? 4 / L : 1;
+    const int oc = ch + (L <= 4 ? sl * kOut : sl / (L > 4 ? L / 4 : 1));
+    const bool writes = L <= 4 || sl % (L > 4 ? L / 4 : 1) == 0;
+    float skip[kOut], sum_d[kOut], sum_b[kOut];
+#pragma unroll
+    for (int o = 0; o < kOut; ++o) {
+        skip[o] = p.Dskip != nullptr && oc + o < wide ? p.Dskip[dw + oc + o] : 0.f;
+        sum_d[o] = sum_b[o] = 0.f;
+    }
+
+    int s = q.of(w.rowb + w.t1 - 1);
+    long long lo = q.begin(s) - w.rowb, hi = q.begin(s + 1) - w.rowb;
+    if (hi > w.t1) {   // the chunk's last sequence goes on: fold its later chunks
+        int64_t j = ((hi < p.T ? hi : p.T) - 1) / ck.len;
+        bool begin = true;
+        for (; j > w.k; --j) {
+            const int64_t at = (w.b * (ck.n - 1) + j - 1) * p.D;
+            pair_t v[S][2];
+            load_block<S>(agg_q + at * p.N, dw + ch, ch, wide, n0, p.N, v);
+            float ds[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ds[c] = ch + c < wide ? agg_s[at + dw + ch + c] : 0.f;
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    ag[i][c] = begin ? v[i][c]
+                                     : fma2(decay2(ds[2 * c], ds[2 * c + 1], A2[i][c]), ag[i][c], v[i][c]);
+            begin = false;
+        }
+    }
+
+    const T *xp = static_cast<const T *>(p.x) + w.rowb * p.ldx + dw;
+    const T *rp = static_cast<const T *>(p.raw) + w.rowb * p.ldraw + dw;
+    const T *yp = static_cast<const T *>(p.dy) + w.rowb * p.lddy + dw;
+    const T *bp = static_cast<const T *>(p.Bm) + w.rowb * p.ldb + int64_t(w.g) * p.N;
+    const T *cp = static_cast<const T *>(p.Cm) + w.rowb * p.ldc + int64_t(w.g) * p.N;
+    const int64_t nseg = (p.T + kSeg - 1) / kSeg;
+    // Starts the copies of a tile's x, raw, dy, B and C: each lane its vectors.
+    auto fetch = [&](int64_t t) {
+        if constexpr (VEC > 1) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const int v = lane + i * 32, row = v / kCols, col = v % kCols * VEC;
+                if (v < kVecs && col < wide && t + row < w.t1) {
+                    cp_async16(&sm.raw[0][row][col], xp + (t + row) * p.ldx + col);
+                    cp_async16(&sm.raw[1][row][col], rp + (t + row) * p.ldraw + col);
+                    cp_async16(&sm.raw[2][row][col], yp + (t + row) * p.lddy + col);
+                }
+            }
+            if (bc_wide) {
+#pragma unroll
+                for (int i = 0; i < kBcPer; ++i) {
+                    const int v = lane + i * 32, n = v % kBcCols * VEC, which = v / kBcCols % 2;
+                    const int row = v / kBcCols / 2;
+                    if (v < kBcVecs && t + row < w.t1 && n < p.N)
+                        cp_async16(&sm.rawbc[row][which][n],
+                                   which == 0 ? bp + (t + row) * p.ldb + n : cp + (t + row) * p.ldc + n);
+                }
+            }
+        }
+    };
+    // The saved states before a tile, into the lane's first checkpoint.
+    auto fetch_state = [&](int64_t t) {
+        const float *o = p.saved_in + ((w.b * nseg + t / kSeg) * p.D + dw + ch) * p.N;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float4 *to = &sm.ck[0][c][lane];
+            if (ch + c >= wide || n0 >= p.N) {
+                *to = make_float4(0.f, 0.f, 0.f, 0.f);
+            } else if (vec_n) {
+                cp_async16(to, o + c * p.N + n0);
+            } else {
+                float v[S];
+                load_group<S>(o + c * p.N, n0, p.N, v);
+                *to = make_float4(v[0], v[1], v[2], v[3]);
+            }
+        }
+    };
+    pair_t h[S][2];
+    auto get_state = [&](int i) {
+        const float4 a = sm.ck[i][0][lane], b = sm.ck[i][1][lane], c = sm.ck[i][2][lane], d = sm.ck[i][3][lane];
+        h[0][0] = pack2(a.x, b.x), h[0][1] = pack2(c.x, d.x);
+        h[1][0] = pack2(a.y, b.y), h[1][1] = pack2(c.y, d.y);
+        h[2][0] = pack2(a.z, b.z), h[2][1] = pack2(c.z, d.z);
+        h[3][0] = pack2(a.w, b.w), h[3][1] = pack2(c.w, d.w);
+    };
+    auto put_state = [&](int i) {
+        float a[4], b[4], c[4], d[4];
+#pragma unroll
+        for (int n = 0; n < S; ++n) {
+            unpack2(h[n][0], a[n], b[n]);
+            unpack2(h[n][1], c[n], d[n]);
+        }
+        sm.ck[i][0][lane] = make_float4(a[0], a[1], a[2], a[3]);
+        sm.ck[i][1][lane] = make_float4(b[0], b[1], b[2], b[3]);
+        sm.ck[i][2][lane] = make_float4(c[0], c[1], c[2], c[3]);
+        sm.ck[i][3][lane] = make_float4(d[0], d[1], d[2], d[3]);
+    };
+
+    // A staged row's values for the thread: delta and u = delta x of its
+    // channel pairs, and B of its states.
+    auto row_in = [&](int tt, pair_t (&dl)[2], pair_t (&u)[2], float (&bv)[4]) {
+        const ulonglong2 d2 = *reinterpret_cast<const ulonglong2 *>(&sm.d[tt][ch]);
+        const ulonglong2 x2 = *reinterpret_cast<const ulonglong2 *>(&sm.x[tt][ch]);
+        const float4 b4 = *reinterpret_cast<const float4 *>(&sm.bc[tt][0][n0]);
+        dl[0] = d2.x, dl[1] = d2.y;
+        u[0] = mul2(d2.x, x2.x), u[1] = mul2(d2.y, x2.y);
+        bv[0] = b4.x, bv[1] = b4.y, bv[2] = b4.z, bv[3] = b4.w;
+    };
+
+    // One tile; kEdges: it holds a sequence's first or last row.
+    auto tile = [&](int64_t t, auto edges) {
+        constexpr bool kEdges = decltype(edges)::value;
+        auto enter = [&](int tt) {   // a sequence's first row starts from its h0
+            if constexpr (kEdges) {
+                const int f = block.first[tt];
+                if (f >= 0)
+                    load_block<S>(p.h0 != nullptr ? p.h0 + int64_t(f) * p.D * p.N : nullptr, dw + ch, ch, wide, n0,
+                                  p.N, h);
+            }
+        };
+        const int rows = int(w.t1 - t);
+        int64_t out = (w.rowb + t + kTile - 1) * p.D + dw + oc;   // of the row at hand, from the last
+        get_state(0);
+#pragma unroll 1
+        for (int sb = 1; sb < kTile / kSub; ++sb) {
+#pragma unroll
+            for (int i = 0; i < kSub; ++i) {
+                const int tt = (sb - 1) * kSub + i;
+                enter(tt);
+                pair_t dl[2], u[2];
+                float bv[4];
+                row_in(tt, dl, u, bv);
+#pragma unroll
+                for (int n = 0; n < S; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        h[n][c] = fma2(decay2(dl[c], A2[n][c]), h[n][c], mul2(u[c], dup2(bv[n])));
+            }
+            put_state(sb);
+        }
+#pragma unroll 1
+        for (int sb = kTile / kSub - 1; sb >= 0; --sb) {
+            if (sb < kTile / kSub - 1) get_state(sb);
+            if (sb == 0) {
+                if (t > w.t0) fetch_state(t - kTile);
+                cp_async_commit();
+            }
+            pair_t a[kSub][S][2], ah[kSub][S][2];
+#pragma unroll
+            for (int i = 0; i < kSub; ++i) {
+                const int tt = sb * kSub + i;
+                enter(tt);
+                pair_t dl[2], u[2];
+                float bv[4];
+                row_in(tt, dl, u, bv);
+#pragma unroll
+                for (int n = 0; n < S; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        a[i][n][c] = decay2(dl[c], A2[n][c]);
+                        ah[i][n][c] = mul2(a[i][n][c], h[n][c]);
+                        h[n][c] = fma2(u[c], dup2(bv[n]), ah[i][n][c]);
+                    }
+            }
+#pragma unroll
+            for (int i = kSub - 1; i >= 0; --i) {
+                const int tt = sb * kSub + i;
+                if constexpr (kEdges) {
+                    if (block.last[tt] >= 0)
+                        load_block<S>(p.dh_last != nullptr ? p.dh_last + int64_t(block.last[tt]) * p.D * p.N : nullptr,
+                                      dw + ch, ch, wide, n0, p.N, ag);
+                }
+                pair_t dl[2], u[2];
+                float bv[4];
+                row_in(tt, dl, u, bv);
+                const ulonglong2 y2 = *reinterpret_cast<const ulonglong2 *>(&sm.dy[tt][ch]);
+                const float4 c4 = *reinterpret_cast<const float4 *>(&sm.bc[tt][1][n0]);
+                const float cv[4] = {c4.x, c4.y, c4.z, c4.w};
+                const pair_t dy[2] = {y2.x, y2.y};
+                pair_t s1[2], s2[2];
+                float bc[2 * S];
+#pragma unroll
+                for (int n = 0; n < S; ++n) {
+                    const pair_t bn = dup2(bv[n]), cn = dup2(cv[n]);
+                    pair_t db = 0, dc = 0;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const pair_t g = fma2(cn, dy[c], ag[n][c]);
+                        const pair_t hh = fma2(u[c], bn, ah[i][n][c]);
+                        dc = c == 0 ? mul2(dy[c], hh) : fma2(dy[c], hh, dc);
+                        db = c == 0 ? mul2(u[c], g) : fma2(u[c], g, db);
+                        s1[c] = n == 0 ? mul2(g, bn) : fma2(g, bn, s1[c]);
+                        const pair_t wv = mul2(g, ah[i][n][c]);
+                        s2[c] = n == 0 ? mul2(wv, A2[n][c]) : fma2(wv, A2[n][c], s2[c]);
+                        dA[n][c] = fma2(wv, dl[c], dA[n][c]);
+                        ag[n][c] = mul2(a[i][n][c], g);
+                    }
+                    float lo2, hi2;
+                    unpack2(db, lo2, hi2);
+                    bc[n] = lo2 + hi2;
+                    unpack2(dc, lo2, hi2);
+                    bc[S + n] = lo2 + hi2;
+                }
+                if constexpr (kEdges) {
+                    if (p.dh0 != nullptr && block.first[tt] >= 0)
+                        store_block<S>(p.dh0 + int64_t(block.first[tt]) * p.D * p.N, dw + ch, ch, wide, n0, p.N, ag);
+                }
+                // dB, dC over the warp's channel lanes
+                constexpr int kBcOut = 2 * S / kG > 0 ? 2 * S / kG : 1, kShare = kG / (2 * S) > 0 ? kG / (2 * S) : 1;
+                halve_sum<2 * S, kG, 1>(bc, cg);
+                if (cg % kShare == 0) {
+                    const int v0 = cg / kShare * kBcOut;
+#pragma unroll
+                    for (int o = 0; o < kBcOut; ++o)
+                        block.red[tt][warp][(v0 + o) / S * NP + n0 + (v0 + o) % S] = bc[o];
+                }
+                // s1, s2 over the channel's state lanes, and the outputs
+                float s1v[4], s2v[4];
+                unpack2(s1[0], s1v[0], s1v[1]);
+                unpack2(s1[1], s1v[2], s1v[3]);
+                unpack2(s2[0], s2v[0], s2v[1]);
+                unpack2(s2[1], s2v[2], s2v[3]);
+                halve_channels<L, kG>(s1v, s2v, sl);
+#pragma unroll
+                for (int o = 0; o < kOut; ++o) {
+                    const float xv = sm.x[tt][oc + o], dyv = sm.dy[tt][oc + o];
+                    const float dx = fmaf(sm.d[tt][oc + o], s1v[o], skip[o] * dyv);
+                    const float dr = fmaf(xv, s1v[o], s2v[o] * kLn2) * sm.slope[tt][oc + o];
+                    sum_d[o] = fmaf(dyv, xv, sum_d[o]);
+                    sum_b[o] += dr;
+                    if (writes && tt < rows && oc + o < wide) {
+                        store1(static_cast<T *>(p.dx) + out + o, dx);
+                        store1(static_cast<T *>(p.draw) + out + o, dr);
+                    }
+                }
+                out -= p.D;
+            }
+        }
+    };
+
+    int64_t t = w.t0 + (w.t1 - 1 - w.t0) / kTile * kTile;
+    fetch(t);
+    fetch_state(t);
+    cp_async_commit();
+    for (; t >= w.t0; t -= kTile) {
+        const int64_t end = t + kTile < w.t1 ? t + kTile : w.t1;
+        cp_async_wait<0>();
+        __syncwarp();
+        // the lane's vectors as float32: delta, x, dy and the slope of delta
+#pragma unroll(VEC > 1 ? kPer : 1)
+        for (int i = 0; i < kPer; ++i) {
+            const int v = lane + i * 32, row = v / kCols, col = v % kCols * VEC;
+            if (v < kVecs) {
+                float xv[VEC], rv[VEC], yv[VEC], sv[VEC];
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) xv[e] = rv[e] = yv[e] = sv[e] = 0.f;
+                if (col < wide && t + row < w.t1) {
+                    float bias[VEC];
+                    load_vec<VEC>(&sm.bias[col], bias);
+                    if constexpr (VEC > 1) {
+                        load_vec<VEC>(&sm.raw[0][row][col], xv);
+                        load_vec<VEC>(&sm.raw[1][row][col], rv);
+                        load_vec<VEC>(&sm.raw[2][row][col], yv);
+                    } else {
+                        xv[0] = load1(xp + (t + row) * p.ldx + col);
+                        rv[0] = load1(rp + (t + row) * p.ldraw + col);
+                        yv[0] = load1(yp + (t + row) * p.lddy + col);
+                    }
+                    if (p.softplus) {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) rv[e] = softplus_f(rv[e] + bias[e], sv[e]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < VEC; ++e) rv[e] += bias[e], sv[e] = 1.f;
+                    }
+                }
+                store_vec<VEC>(&sm.d[row][col], rv);
+                store_vec<VEC>(&sm.x[row][col], xv);
+                store_vec<VEC>(&sm.dy[row][col], yv);
+                store_vec<VEC>(&sm.slope[row][col], sv);
+            }
+        }
+        if (VEC > 1 && bc_wide) {
+#pragma unroll
+            for (int i = 0; i < kBcPer; ++i) {
+                const int v = lane + i * 32, n = v % kBcCols * VEC, which = v / kBcCols % 2;
+                const int row = v / kBcCols / 2;
+                if (v < kBcVecs) {
+                    float o[VEC];
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) o[e] = 0.f;
+                    if (t + row < w.t1 && n < p.N) load_vec<VEC>(&sm.rawbc[row][which][n], o);
+                    store_vec<VEC>(&sm.bc[row][which][n], o);
+                }
+            }
+        } else {   // rows of B and C that 16-byte vectors do not fit
+            for (int e = lane; e < kTile * 2 * NP; e += 32) {
+                const int n = e % NP, which = e / NP % 2, row = e / NP / 2;
+                const bool in = t + row < w.t1 && n < p.N;
+                sm.bc[row][which][n] =
+                    !in ? 0.f : load1(which == 0 ? bp + (t + row) * p.ldb + n : cp + (t + row) * p.ldc + n);
+            }
+        }
+        const bool edges = lo >= t || hi == end;
+        if (edges) edge_rows(q, w.rowb, t, int(end - t), block.first, block.last);
+        __syncthreads();   // edges; and the block's dB and dC of the tile before are read
+        if (t > w.t0) fetch(t - kTile);
+        cp_async_commit();
+        if (edges) tile(t, std::true_type());
+        else tile(t, std::false_type());
+        if (lo >= t && t > w.t0) {
+            s = q.of(w.rowb + t - 1);
+            lo = q.begin(s) - w.rowb;
+        }
+        hi = q.begin(s + 1) - w.rowb;
+        __syncthreads();
+        for (int i = tid; i < kTile * 2 * NP; i += CV::THREADS) {
+            const int row = i / (2 * NP), v = i % (2 * NP), n = v % NP;
+            if (n < p.N && t + row < w.t1) {
+                float a = block.red[row][0][v];
+#pragma unroll
+                for (int k = 1; k < kWarps; ++k) a += block.red[row][k][v];
+                partB[((w.tile * q.rows + w.rowb + t + row) * p.G + w.g) * 2 * p.N + v / NP * p.N + n] = a;
+            }
+        }
+    }
+    const int64_t part = w.b * ck.n + w.k;
+    store_block<S>(partA + part * p.D * p.N, dw + ch, ch, wide, n0, p.N, dA);
+#pragma unroll
+    for (int o = 0; o < kOut; ++o)
+        if (writes && oc + o < wide) {
+            partD[part * 2 * p.D + dw + oc + o] = sum_d[o];
+            partD[(part * 2 + 1) * p.D + dw + oc + o] = sum_b[o];
+        }
+}
+
+// dB and dC from the tiles' parts, in order: part (tile, row, group, dB or
+// dC, N).
+template <typename T>
+__global__ void __launch_bounds__(256) sum_bc_kernel(const float *part, int64_t tiles, int64_t rows_g,
+                                                     int N, T *dB, T *dC)
+{
+    const int64_t n = rows_g * 2 * N, i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    if (i >= n) return;
+    float a = 0.f;
+    for (int64_t t = 0; t < tiles; ++t) a += part[t * n + i];
+    const int64_t rg = i / (2 * N);
+    const int v = int(i - rg * 2 * N);
+    T *o = v < N ? dB : dC;
+    store1(o + rg * N + (v < N ? v : v - N), a);
+}
+
+// The gradients' chunks: four channels a thread, two blocks for each SM.
+inline int backward_lanes(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+// Threads of a block: shared memory holds the tiles of 128 channels.
+constexpr int backward_threads(int L) { return L == 1 ? 32 : L == 2 ? 64 : kThreads; }
+inline int64_t backward_tiles(int64_t D, int N, int G)
+{
+    const int L = backward_lanes(N);
+    return ceil_div(D / G, backward_threads(L) / L * 4);
+}
+
+inline Chunks backward_chunks(int64_t B, int64_t T, int64_t D, int N, int G)
+{
+    static constexpr RowTime r{{0, 560, 1070, 0}, 2, 0.2};
+    return cut_time(B * G * backward_tiles(D, N, G), T, r);
+}
+
+template <typename T, int VEC, int L>
+mg_status bwd(const SsmArgs &p, cudaStream_t s)
+{
+    using CV = Cover<4, L, 4, backward_threads(L)>;
+    const Tile t{backward_tiles(p.D, p.N, p.G), p.D / p.G};
+    const Chunks ck = backward_chunks(p.B, p.T, p.D, p.N, p.G);
+    const Seqs q = make_seqs(p.cu, p.B, p.T, p.nseq);
+    const int64_t rows_g = q.rows * p.G, dn = p.D * p.N, parts = p.B * ck.n;
+    float *partB = reinterpret_cast<float *>(static_cast<char *>(p.ws) + kControlBytes);
+    float *partA = partB + t.tiles * rows_g * 2 * p.N;
+    float *partD = partA + parts * dn;
+    float *agg_q = partD + parts * 2 * p.D;
+    float *agg_s = agg_q + p.B * (ck.n - 1) * dn;
+    const int64_t tiles = t.tiles * p.G * p.B;
+    // 16-byte vectors of B and C
+    const int bc_wide = VEC > 1 && p.N % VEC == 0 && p.ldb % VEC == 0 && p.ldc % VEC == 0;
+    if (p.cu != nullptr) {
+        MG_TRY(launch_empty_sequences(q, p.dh0, p.dh_last, dn, p.ws, s));
+    }
+    if (ck.n > 1) {
+        ssm_adjoint_chunk_kernel<T, VEC, CV><<<unsigned(tiles * (ck.n - 1)), CV::THREADS, 0, s>>>(
+            p, q, t, ck, agg_q, agg_s);
+        MG_TRY(launched("mg_selective_scan_bwd"));
+    }
+    constexpr size_t smem = sizeof(BwdShared<T, VEC, CV>);
+    static_assert(smem <= 227 * 1024, "shared memory of a block");
+    MG_TRY(allow_shared(ssm_bwd_kernel<T, VEC, CV>, smem));
+    ssm_bwd_kernel<T, VEC, CV><<<unsigned(tiles * ck.n), CV::THREADS, smem, s>>>(p, q, t, ck, agg_q, agg_s, partB,
+                                                                             partA, partD, bc_wide);
+    MG_TRY(launched("mg_selective_scan_bwd"));
+    sum_bc_kernel<T><<<unsigned(ceil_div(rows_g * 2 * p.N, 256)), 256, 0, s>>>(
+        partB, t.tiles, rows_g, p.N, static_cast<T *>(p.dBm), static_cast<T *>(p.dCm));
+    MG_TRY(launched("mg_selective_scan_bwd"));
+    MG_TRY(launch_sum_parts(partA, parts, dn, dn, p.dA, s));
+    if (p.dDskip != nullptr) MG_TRY(launch_sum_parts(partD, parts, 2 * p.D, p.D, p.dDskip, s));
+    if (p.ddt_bias != nullptr)
+        MG_TRY(launch_sum_parts(partD + p.D, parts, 2 * p.D, p.D, p.ddt_bias, s));
+    return MG_OK;
+}
+
+template <typename T, int VEC>
+mg_status bwd_vec(const SsmArgs &p, cudaStream_t s)
+{
+    switch (backward_lanes(p.N)) {
+    case 1: return bwd<T, VEC, 1>(p, s);
+    case 2: return bwd<T, VEC, 2>(p, s);
+    case 4: return bwd<T, VEC, 4>(p, s);
+    case 8: return bwd<T, VEC, 8>(p, s);
+    default: return bwd<T, VEC, 16>(p, s);
+    }
+}
+
+}  // namespace mg

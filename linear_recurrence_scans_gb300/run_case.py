@@ -16,6 +16,10 @@ Cases (inputs seeded, resident on cuda:0 before the first launch):
   affine16_fwd / affine16_bwd    Haar affine scan, B=2 T=1024 n=32 k=v=16
   angle_fwd / angle_bwd          angle-fused scan, B=16 T=512 n=256 k=16 R=4 (a quarter of
                                  the bench's T; each input larger than L2)
+  selective_fwd / selective_bwd  selective scan, B=4 T=4096 D=2048 N=16, bf16 (forward with
+                                 the states saved for the gradients)
+  conv_fwd / conv_bwd            short causal convolution, B=8 T=4096 D=2048 W=4, bf16
+  norm_fwd / norm_bwd            group norm of 32768 rows x 2048, 16 groups, gated, bf16
 
 Every case runs its op `repeats` times (default 3) after one set-up call of
 the forward op where the backward needs the forward's outputs.  Each input is
@@ -32,7 +36,8 @@ from linear_recurrence_scans_gb300 import workloads as wl
 
 CASES = ("linear_fwd", "linear_bwd", "linear_bf16_fwd", "linear_bf16_bwd", "log_fwd", "log_bwd",
          "affine4_fwd", "affine4_bwd", "affine16_fwd", "affine16_bwd", "mingru_bf16_fwd",
-         "mingru_bf16_bwd", "varlen_fwd", "varlen_bwd", "angle_fwd", "angle_bwd")
+         "mingru_bf16_bwd", "varlen_fwd", "varlen_bwd", "angle_fwd", "angle_bwd",
+         "selective_fwd", "selective_bwd", "conv_fwd", "conv_bwd", "norm_fwd", "norm_bwd")
 
 
 def main(argv):
@@ -53,6 +58,31 @@ def main(argv):
                 mg.angle_scan_fwd(th, sc, ga, bv, h0, perm, sgn, p2p, out=h)
             else:
                 mg.angle_scan_bwd(th, sc, ga, h0, h, go, perm, sgn, p2p, out=outs)
+    elif case.startswith("selective"):
+        x, dt, A, Bm, Cm, D, bias, dy = wl.selective(4, 4096, 2048, 16, seed=0, device=dev,
+                                                     dtype=torch.bfloat16)
+        y, h_last, saved = mg.selective_scan_fwd(x, dt, A, Bm, Cm, D, bias, save=True)
+        for _ in range(reps):
+            if case.endswith("fwd"):
+                mg.selective_scan_fwd(x, dt, A, Bm, Cm, D, bias, save=True, out=(y, h_last, saved))
+            else:
+                mg.selective_scan_bwd(dy, saved, x, dt, A, Bm, Cm, D, bias)
+    elif case.startswith("conv") or case.startswith("norm"):
+        gen = torch.Generator(dev).manual_seed(0)
+        x, z, dy = (torch.randn(8, 4096, 2048, device=dev, generator=gen).to(torch.bfloat16)
+                    for _ in range(3))
+        w = torch.randn(2048, 4, device=dev, generator=gen)
+        g, b = torch.randn(2, 2048, device=dev, generator=gen)
+        y, stats = mg.group_norm_fwd(x, g, b, z, groups=16)
+        for _ in range(reps):
+            if case == "conv_fwd":
+                mg.causal_conv_fwd(x, w, b)
+            elif case == "conv_bwd":
+                mg.causal_conv_bwd(dy, x, w, b)
+            elif case == "norm_fwd":
+                mg.group_norm_fwd(x, g, b, z, groups=16, out=(y, stats))
+            else:
+                mg.group_norm_bwd(dy, stats, x, g, b, z, groups=16)
     elif case.startswith("mingru"):
         x1, x2, _, gBc = wl.mingru_x(4, 8192, 4096, seed=0, device=dev, in_dtype=torch.bfloat16)
         _, Bc = mg.mingru_scan_fwd(x1, x2, want_A=False)

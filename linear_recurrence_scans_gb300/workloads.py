@@ -154,6 +154,25 @@ def angle_inputs(B: int, T: int, n: int, R: int, k: int, seed: int = 0, device="
     return th, scale, gamma, b, h0, perm, sgn, p2p, go
 
 
+def selective(B: int, T: int, D: int, N: int, seed: int = 0, device="cpu", dtype=torch.float32):
+    """Inputs of a selective scan: (x, dt, A, Bm, Cm, D, dt_bias, dy).  x, Bm,
+    Cm (B,T,N), dy ~ N(0,1) and raw steps dt ~ N(0, 1/4), of `dtype`; A[d, n] =
+    -(n+1) e^{0.1 N(0,1)}; D ~ N(1, 0.01); dt_bias so that softplus of it is
+    log-uniform in [1e-3, 0.1].  Streams seed .. seed+6 in the order x, dt,
+    (Bm, Cm), A, D, dt_bias, dy."""
+    def randn(i, *shape):
+        return torch.randn(shape, generator=_gen(seed + i, device), device=device)
+
+    x, dt, dy = randn(0, B, T, D), 0.5 * randn(1, B, T, D), randn(6, B, T, D)
+    bc = randn(2, B, T, 2 * N).to(dtype)
+    A = -torch.arange(1, N + 1, device=device, dtype=torch.float32) * torch.exp(0.1 * randn(3, D, N))
+    skip = 1 + 0.1 * randn(4, D)
+    u = torch.rand(D, generator=_gen(seed + 5, device), device=device)
+    step = torch.exp(u * (math.log(0.1) - math.log(1e-3)) + math.log(1e-3))
+    bias = step + torch.log(-torch.expm1(-step))
+    return x.to(dtype), dt.to(dtype), A, bc[..., :N], bc[..., N:], skip, bias, dy.to(dtype)
+
+
 # The workloads the library is checked and measured on, by name.
 CONFIGS = {
     # linear_scan_fwd fp32, a ~ U(0,1), b ~ N(0,1)
