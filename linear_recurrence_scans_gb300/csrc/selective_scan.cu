@@ -20,6 +20,9 @@ namespace {
 // and runs the recurrence again with the outputs.  No block waits for
 // another, and the order of every sum is fixed.
 //
+// The gradients' first pass is the same walk backwards in time, with
+// q <- a_r (q + C_r dy_r) in the recurrence's place (ChunkPass kAdjoint).
+//
 // Each warp works by itself, on its own channels and its own copy of B and C:
 // no barrier lines up the warps of an SM.  Stages of kRows rows pass through
 // shared memory.  The rows' x, raw, B and C arrive by asynchronous copies,
@@ -40,6 +43,9 @@ namespace {
 constexpr int kRows = 8;    // rows of a stage
 constexpr int kRing = 4;    // stages in flight or in use
 
+// What a launch of ssm_chunk_kernel does.
+enum ChunkPass { kOutputs, kStates, kAdjoint };
+
 template <typename T, int VEC, int WCH, int NP, bool kFirst>
 struct alignas(16) FwdShared {   // of a warp
     static constexpr int kBc = kFirst ? 1 : 2;
@@ -59,19 +65,19 @@ __device__ __forceinline__ void cp_async16_or_zero(void *dst, const void *src, b
                  : "memory");
 }
 
-template <typename T, int VEC, typename CV, bool kFirst>
+template <typename T, int VEC, typename CV, ChunkPass kPass>
 __global__ void __launch_bounds__(kThreads, 3)
 ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg_s, int bc_wide)
 {
+    constexpr bool kFirst = kPass != kOutputs, kBack = kPass == kAdjoint;
     constexpr int S = CV::S, L = CV::L, C = CV::C, NP = CV::NP, SP = S / 2, WCH = CV::kWarpCh;
-    constexpr int G = L > 4 ? L : 4;                   // rows between two sums over lanes
     constexpr int kBc = kFirst ? 1 : 2;
     constexpr int kCols = WCH / VEC;                   // vectors of a row
     constexpr int kStep = 32 / kCols;                  // rows between a lane's vectors
     constexpr int kPer = kStep < kRows ? kRows / kStep : 1;
     constexpr int kBcVecs = VEC > 1 ? kRows * kBc * NP / VEC : 0;   // vectors of B (and C) of a stage
     constexpr int kBcPer = (kBcVecs + 31) / 32;
-    static_assert(C == 2 && WCH % VEC == 0 && NP % VEC == 0 && kCols <= 32 && kRows % G == 0, "staging");
+    static_assert(C == 2 && WCH % VEC == 0 && NP % VEC == 0 && kCols <= 32, "staging");
     using Shared = FwdShared<T, VEC, WCH, NP, kFirst>;
     extern __shared__ __align__(16) unsigned char shared_bytes[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -79,8 +85,8 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
 
     const int64_t all_tiles = tl.tiles * p.G;
     const int64_t tile = blockIdx.x % all_tiles, rest = blockIdx.x / all_tiles;
-    const int64_t nch = kFirst ? ck.n - 1 : ck.n;      // the last chunk has no successor
-    const int64_t k = rest % nch, b = rest / nch;
+    const int64_t nch = kFirst ? ck.n - 1 : ck.n;      // the last (backwards: first) chunk has no successor
+    const int64_t k = rest % nch + (kBack ? 1 : 0), b = rest / nch;
     const int64_t rowb = b * p.T;
     const int64_t t0 = k * ck.len, t1 = t0 + ck.len < p.T ? t0 + ck.len : p.T;
     const int g = int(tile / tl.tiles);
@@ -94,11 +100,16 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
     // and of B and C.
     const int row0 = lane / kCols, col = lane % kCols * VEC;
     const bool col_in = col < wide && row0 < kRows;
-    const T *xp = static_cast<const T *>(p.x) + (rowb + t0 + row0) * p.ldx + d0 + col;
-    const T *rp = static_cast<const T *>(p.raw) + (rowb + t0 + row0) * p.ldraw + d0 + col;
-    const int64_t xs = kStep * p.ldx, rs = kStep * p.ldraw;
-    const T *bp = static_cast<const T *>(p.Bm) + (rowb + t0) * p.ldb + int64_t(g) * p.N;
-    const T *cp = static_cast<const T *>(p.Cm) + (rowb + t0) * p.ldc + int64_t(g) * p.N;
+    // Backwards, rows count from the chunk's last one down: dy stands for x, C
+    // for B, and the strides are negative.
+    const int64_t ldx = kBack ? -p.lddy : p.ldx, ldr = kBack ? -p.ldraw : p.ldraw;
+    const int64_t ldb = kBack ? -p.ldc : p.ldb, ldc = p.ldc;
+    const int64_t rf = rowb + (kBack ? t1 - 1 : t0);   // the chunk's first row in that order
+    const T *xp = static_cast<const T *>(kBack ? p.dy : p.x) + rf * (kBack ? p.lddy : p.ldx) + row0 * ldx + d0 + col;
+    const T *rp = static_cast<const T *>(p.raw) + rf * p.ldraw + row0 * ldr + d0 + col;
+    const int64_t xs = kStep * ldx, rs = kStep * ldr;
+    const T *bp = static_cast<const T *>(kBack ? p.Cm : p.Bm) + rf * (kBack ? p.ldc : p.ldb) + int64_t(g) * p.N;
+    const T *cp = static_cast<const T *>(p.Cm) + rf * p.ldc + int64_t(g) * p.N;
     const int rows = int(t1 - t0);
     // Starts the copies of the rows from `at` on into ring slot `slot`.
     auto fetch = [&](int at, int slot) {
@@ -108,8 +119,8 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
                 const int row = at + row0 + i * kStep;
                 const bool in = col_in && row < rows;
                 if (row0 < kRows) {
-                    cp_async16_or_zero(&sm.raw[slot][0][row0 + i * kStep][col], in ? xp + at * p.ldx + i * xs : p.x, in);
-                    cp_async16_or_zero(&sm.raw[slot][1][row0 + i * kStep][col], in ? rp + at * p.ldraw + i * rs : p.raw, in);
+                    cp_async16_or_zero(&sm.raw[slot][0][row0 + i * kStep][col], in ? xp + at * ldx + i * xs : p.x, in);
+                    cp_async16_or_zero(&sm.raw[slot][1][row0 + i * kStep][col], in ? rp + at * ldr + i * rs : p.raw, in);
                 }
             }
             if (bc_wide) {
@@ -119,8 +130,8 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
                     const int row = v / (NP / VEC) / kBc;
                     const bool in = at + row < rows && n < p.N;
                     const void *src = !in          ? p.Bm
-                                      : which == 0 ? static_cast<const void *>(bp + (at + row) * p.ldb + n)
-                                                   : static_cast<const void *>(cp + (at + row) * p.ldc + n);
+                                      : which == 0 ? static_cast<const void *>(bp + (at + row) * ldb + n)
+                                                   : static_cast<const void *>(cp + (at + row) * ldc + n);
                     if (kBcVecs % 32 == 0 || v < kBcVecs) cp_async16_or_zero(&sm.rawbc[slot][row][which][n], src, in);
                 }
             }
@@ -152,23 +163,26 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
         sm.skip[i] = !kFirst && p.Dskip != nullptr && i < wide ? p.Dskip[d0 + i] : 0.f;
     }
     __syncwarp();
+    const float *edge = kBack ? p.dh_last : p.h0;      // the state that a sequence starts from
     auto start_state = [&](int s) {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             float v[S];
 #pragma unroll
             for (int i = 0; i < S; ++i) v[i] = 0.f;
-            if (p.h0 != nullptr && ch + c < wide)
-                load_group<S>(p.h0 + (int64_t(s) * p.D + d0 + ch + c) * p.N, n0, p.N, v);
+            if (edge != nullptr && ch + c < wide)
+                load_group<S>(edge + (int64_t(s) * p.D + d0 + ch + c) * p.N, n0, p.N, v);
 #pragma unroll
             for (int i = 0; i < SP; ++i) h[c][i] = pack2(v[2 * i], v[2 * i + 1]);
         }
     };
-    int s = q.of(rowb + t0);
-    long long next = q.begin(s + 1) - rowb;            // where the sequence ends
+    int s = q.of(rf);
+    // where the sequence ends, in rows from the chunk's first
+    auto ends = [&]() { return kBack ? rowb + t1 - q.begin(s) : q.begin(s + 1) - (rowb + t0); };
+    long long next = ends();
     {
         const long long lo = q.begin(s) - rowb;
-        if (lo >= t0) {
+        if (kBack ? q.begin(s + 1) - rowb <= t1 : lo >= t0) {
             start_state(s);
         } else if (!kFirst) {
             int64_t j = (lo < 0 ? 0 : lo) / ck.len;
@@ -211,12 +225,14 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
                     const pair_t r = add2(pack2(rv[e], rv[e + 1]), pack2(bias[e], bias[e + 1]));
                     const pair_t sp = softplus2(r);
                     dl[i][e / 2] = !in ? 0 : p.softplus ? sp : r;
-                    uu[i][e / 2] = mul2(dl[i][e / 2], pack2(xv[e], xv[e + 1]));
+                    const pair_t xx = pack2(xv[e], xv[e + 1]);
+                    uu[i][e / 2] = kBack ? xx : mul2(dl[i][e / 2], xx);
                 }
             } else {
-                const float r = in ? load1(rp + at * p.ldraw + i * rs) + sm.bias[col] : 0.f;
+                const float r = in ? load1(rp + at * ldr + i * rs) + sm.bias[col] : 0.f;
                 const float delta = !in ? 0.f : p.softplus ? softplus_f(r) : r;
-                dl[i][0] = pack2(delta, in ? delta * load1(xp + at * p.ldx + i * xs) : 0.f);
+                const float xv1 = in ? load1(xp + at * ldx + i * xs) : 0.f;
+                dl[i][0] = pack2(delta, kBack ? xv1 : delta * xv1);
             }
         }
         if constexpr (VEC > 1) {
@@ -260,7 +276,7 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
                 const int n = e % NP, which = e / NP % kBc, row = e / NP / kBc;
                 const bool in = at + row < rows && n < p.N;
                 sm.bc[to][row][which][n] =
-                    !in ? 0.f : load1(which == 0 ? bp + (at + row) * p.ldb + n : cp + (at + row) * p.ldc + n);
+                    !in ? 0.f : load1(which == 0 ? bp + (at + row) * ldb + n : cp + (at + row) * ldc + n);
             }
         }
     };
@@ -286,7 +302,8 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
             pair_t acc = 0;
 #pragma unroll
             for (int i = 0; i < SP; ++i) {
-                h[c][i] = fma2(decay2(du[2 * c], du[2 * c], A2[c][i]), h[c][i], mul2(u2, B[i]));
+                const pair_t a = decay2(du[2 * c], du[2 * c], A2[c][i]);
+                h[c][i] = kBack ? mul2(a, fma2(u2, B[i], h[c][i])) : fma2(a, h[c][i], mul2(u2, B[i]));
                 if (!kFirst) acc = i == 0 ? mul2(Cw[i], h[c][i]) : fma2(Cw[i], h[c][i], acc);
             }
             if (kFirst) {
@@ -314,7 +331,7 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
                 if (ch + c < wide)
                     store_pairs<S>(p.saved + (o * p.D + d0 + ch + c) * p.N, n0, p.N, h[c]);
         }
-        const int64_t t = t0 + at, end = t + kRows < t1 ? t + kRows : t1;
+        const int end = at + kRows < rows ? at + kRows : rows;
         auto last_state = [&]() {
             if constexpr (!kFirst) {
                 if (p.h_last == nullptr) return;
@@ -346,12 +363,10 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
             if (next == end) last_state();
         } else {
 #pragma unroll 1
-            for (int tt = 0; tt < int(end - t); ++tt) {
-                if (t + tt == next) {
-                    ++s;
-                    while (s + 1 < q.nseq && q.begin(s + 1) - rowb <= t + tt) ++s;   // empty ones
-                    if (s >= q.nseq) s = q.nseq - 1;
-                    next = q.begin(s + 1) - rowb;
+            for (int tt = 0; tt < end - at; ++tt) {
+                if (at + tt == next) {   // the next sequence that has rows
+                    s = q.of(kBack ? rf - (at + tt) : rf + at + tt);
+                    next = ends();
                     start_state(s);
                 }
                 float y[C];
@@ -365,7 +380,7 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
                         if (sl == 0) sm.y[tt][ch + c] = v;
                     }
                 }
-                if (t + tt + 1 == next) last_state();
+                if (at + tt + 1 == next) last_state();
             }
             convert(at + kRows, ns);
         }
@@ -380,7 +395,7 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
                     load_vec<VEC>(&sm.y[row % kRows][col], o);
                     load_vec<VEC>(&sm.skip[col], skip);
                     if constexpr (VEC > 1) load_vec<VEC>(&sm.raw[slot][0][row % kRows][col], x);
-                    else x[0] = load1(xp + at * p.ldx + i * xs);
+                    else x[0] = load1(xp + at * ldx + i * xs);
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) o[e] = fmaf(skip[e], x[e], o[e]);
                     store_out<VEC>(yp + (at + i * kStep) * p.D, o);
@@ -397,7 +412,7 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
 #pragma unroll
         for (int c = 0; c < C; ++c)
             if (ch + c < wide) {
-                const int64_t at = (b * (ck.n - 1) + k) * p.D + d0 + ch + c;
+                const int64_t at = (b * (ck.n - 1) + (kBack ? k - 1 : k)) * p.D + d0 + ch + c;
                 store_pairs<S>(agg_h + at * p.N, n0, p.N, h[c]);
                 if (sl == 0) agg_s[at] = ssum[c];
             }
@@ -520,27 +535,48 @@ mg_status fwd_cover(const SsmArgs &p, cudaStream_t s)
     }
     constexpr size_t sm1 = kThreads / 32 * sizeof(FwdShared<T, VEC, CV::kWarpCh, CV::NP, true>);
     constexpr size_t sm2 = kThreads / 32 * sizeof(FwdShared<T, VEC, CV::kWarpCh, CV::NP, false>);
-    MG_TRY(allow_shared(ssm_chunk_kernel<T, VEC, CV, true>, sm1));
-    MG_TRY(allow_shared(ssm_chunk_kernel<T, VEC, CV, false>, sm2));
+    MG_TRY(allow_shared(ssm_chunk_kernel<T, VEC, CV, kStates>, sm1));
+    MG_TRY(allow_shared(ssm_chunk_kernel<T, VEC, CV, kOutputs>, sm2));
     if (ck.n > 1) {
-        ssm_chunk_kernel<T, VEC, CV, true><<<unsigned(tiles * (ck.n - 1)), kThreads, sm1, s>>>(
+        ssm_chunk_kernel<T, VEC, CV, kStates><<<unsigned(tiles * (ck.n - 1)), kThreads, sm1, s>>>(
             p, q, t, ck, agg_h, agg_s, bc_wide);
         MG_TRY(launched("mg_selective_scan_fwd"));
     }
-    ssm_chunk_kernel<T, VEC, CV, false><<<unsigned(tiles * ck.n), kThreads, sm2, s>>>(p, q, t, ck, agg_h, agg_s,
+    ssm_chunk_kernel<T, VEC, CV, kOutputs><<<unsigned(tiles * ck.n), kThreads, sm2, s>>>(p, q, t, ck, agg_h, agg_s,
                                                                                     bc_wide);
     return launched("mg_selective_scan_fwd");
 }
 
+template <typename T, int VEC, typename CV>
+mg_status adjoint_cover(const SsmArgs &p, const Chunks &ck, float *agg_q, float *agg_s, cudaStream_t s)
+{
+    const Tile t{forward_tiles(p.D, p.N, p.G), p.D / p.G};
+    const int bc_wide = VEC > 1 && p.N % VEC == 0 && p.ldc % VEC == 0;
+    const Seqs q = make_seqs(p.cu, p.B, p.T, p.nseq);
+    constexpr size_t sm = kThreads / 32 * sizeof(FwdShared<T, VEC, CV::kWarpCh, CV::NP, true>);
+    MG_TRY(allow_shared(ssm_chunk_kernel<T, VEC, CV, kAdjoint>, sm));
+    ssm_chunk_kernel<T, VEC, CV, kAdjoint><<<unsigned(t.tiles * p.G * p.B * (ck.n - 1)), kThreads, sm, s>>>(
+        p, q, t, ck, agg_q, agg_s, bc_wide);
+    return launched("mg_selective_scan_bwd");
+}
+
+// F<CV>(...) for the states of the call.
+#define MG_COVER(F, T, VEC, ...)                                                     \
+    if (p.N <= 8) return F<T, VEC, Cover<4, 2, 2>>(__VA_ARGS__);                     \
+    switch (forward_lanes(p.N)) {                                                    \
+    case 2: return F<T, VEC, Cover<8, 2, 2>>(__VA_ARGS__);                           \
+    case 4: return F<T, VEC, Cover<8, 4, 2>>(__VA_ARGS__);                           \
+    default: return F<T, VEC, Cover<8, 8, 2>>(__VA_ARGS__);                          \
+    }
 template <typename T, int VEC>
 mg_status fwd_vec(const SsmArgs &p, cudaStream_t s)
 {
-    if (p.N <= 8) return fwd_cover<T, VEC, Cover<4, 2, 2>>(p, s);
-    switch (forward_lanes(p.N)) {
-    case 2: return fwd_cover<T, VEC, Cover<8, 2, 2>>(p, s);
-    case 4: return fwd_cover<T, VEC, Cover<8, 4, 2>>(p, s);
-    default: return fwd_cover<T, VEC, Cover<8, 8, 2>>(p, s);
-    }
+    MG_COVER(fwd_cover, T, VEC, p, s)
+}
+template <typename T, int VEC>
+mg_status adjoint_vec(const SsmArgs &p, const Chunks &ck, float *agg_q, float *agg_s, cudaStream_t s)
+{
+    MG_COVER(adjoint_cover, T, VEC, p, ck, agg_q, agg_s, s)
 }
 
 template <typename T, int L>
@@ -569,6 +605,14 @@ mg_status launch_empty_sequences(const Seqs &q, float *dst, const float *src, in
     empty_sequences_kernel<<<unsigned(q.nseq < 1024 ? q.nseq : 1024), 256, 0, s>>>(
         q, dst, src, n, &static_cast<Control *>(ws)->error);
     return launched("selective scan: empty sequences");
+}
+
+mg_status launch_ssm_adjoint(const SsmArgs &p, mg_dtype dt, bool wide, const Chunks &ck, float *agg_q,
+                             float *agg_s, cudaStream_t s)
+{
+    if (dt == MG_F32)
+        return wide ? adjoint_vec<float, 4>(p, ck, agg_q, agg_s, s) : adjoint_vec<float, 1>(p, ck, agg_q, agg_s, s);
+    return wide ? adjoint_vec<bf16_t, 8>(p, ck, agg_q, agg_s, s) : adjoint_vec<bf16_t, 1>(p, ck, agg_q, agg_s, s);
 }
 
 size_t ssm_fwd_ws_bytes(int64_t B, int64_t T, int64_t D, int N, int G, int64_t)

@@ -52,16 +52,33 @@ __device__ __forceinline__ pair_t add2(pair_t a, pair_t b)
     return r;
 }
 
-// softplus of two values (as softplus_f).
-__device__ __forceinline__ pair_t softplus2(pair_t v)
+// softplus of two values, from e = e^-|v| (as softplus_f).
+__device__ __forceinline__ pair_t softplus2(pair_t v, float &e0, float &e1)
 {
     float v0, v1;
     unpack2(v, v0, v1);
-    const pair_t e = pack2(exp_neg(-fabsf(v0)), exp_neg(-fabsf(v1)));
+    e0 = exp_neg(-fabsf(v0));
+    e1 = exp_neg(-fabsf(v1));
+    const pair_t e = pack2(e0, e1);
     pair_t c = pack2(log1p_coef(9), log1p_coef(9));
 #pragma unroll
     for (int i = 8; i >= 0; --i) c = fma2(c, e, pack2(log1p_coef(i), log1p_coef(i)));
     return fma2(e, c, pack2(fmaxf(v0, 0.f), fmaxf(v1, 0.f)));
+}
+__device__ __forceinline__ pair_t softplus2(pair_t v)
+{
+    float e0, e1;
+    return softplus2(v, e0, e1);
+}
+// The same, and sigmoid of both.
+__device__ __forceinline__ pair_t softplus2(pair_t v, pair_t &sig)
+{
+    float e0, e1, v0, v1;
+    const pair_t d = softplus2(v, e0, e1);
+    unpack2(v, v0, v1);
+    const float r0 = rcp_fast(1.f + e0), r1 = rcp_fast(1.f + e1);
+    sig = pack2(v0 >= 0.f ? r0 : e0 * r0, v1 >= 0.f ? r1 : e1 * r1);
+    return d;
 }
 
 // The decay e^(delta A) = 2^(delta A log2 e) of two states.  ex2.approx comes
@@ -237,6 +254,11 @@ inline bool wide_rows(const SsmArgs &p, int vec)
 {
     return p.D / p.G % vec == 0 && p.ldx % vec == 0 && p.ldraw % vec == 0;
 }
+
+// The gradients' first pass: q at the first row of chunks 1 .. ck.n-1, and
+// each one's sum of delta (selective_scan.cu).
+mg_status launch_ssm_adjoint(const SsmArgs &p, mg_dtype dt, bool wide, const Chunks &ck, float *agg_q,
+                             float *agg_s, cudaStream_t s);
 
 // The gradients by activation type (selective_scan_bwd_*.cu).
 mg_status ssm_bwd_f32(const SsmArgs &p, bool wide, cudaStream_t s);

@@ -58,18 +58,17 @@ __device__ __forceinline__ void halve_sum(float (&v)[V], int id)
     }
 }
 
-// The block's place in the gradient passes.
+// The block's place.
 template <int CH>
 struct Spot {
     int64_t tile, k, b, rowb, t0, t1, d0, wide;
     int g;
-    __device__ __forceinline__ Spot(const SsmArgs &p, const Tile &tl, const Chunks &ck, bool first)
+    __device__ __forceinline__ Spot(const SsmArgs &p, const Tile &tl, const Chunks &ck)
     {
         const int64_t all_tiles = tl.tiles * p.G;
         const int64_t at = blockIdx.x % all_tiles, rest = blockIdx.x / all_tiles;
-        const int64_t nch = first ? ck.n - 1 : ck.n;      // the first chunk has nothing before it
-        k = rest % nch + (first ? 1 : 0);
-        b = rest / nch;
+        k = rest % ck.n;
+        b = rest / ck.n;
         rowb = b * p.T;
         t0 = k * ck.len;
         t1 = t0 + ck.len < p.T ? t0 + ck.len : p.T;
@@ -133,117 +132,6 @@ __device__ __forceinline__ void store_block(float *base, int64_t d, int ch, int6
 
 __device__ __forceinline__ pair_t dup2(float a) { return pack2(a, a); }
 
-// First pass: q at the first row of chunks 1 .. n-1.
-template <typename T, int VEC, typename CV>
-__global__ void __launch_bounds__(CV::THREADS)
-ssm_adjoint_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_q, float *agg_s)
-{
-    constexpr int S = CV::S, NP = CV::NP, CH = CV::kCh;
-    constexpr int kVecs = kTile * CH / VEC, kPer = (kVecs + CV::THREADS - 1) / CV::THREADS;
-    constexpr int kBc = (kTile * NP + CV::THREADS - 1) / CV::THREADS;
-    __shared__ __align__(16) float s_d[kTile][CH], s_dy[kTile][CH], s_c[kTile][NP];
-    __shared__ int s_last[kTile], s_first[kTile];
-    const Spot<CH> w(p, tl, ck, true);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int sl = lane / CV::kGroups, n0 = sl * S;
-    const int ch = (warp * CV::kGroups + lane % CV::kGroups) * 4;
-    pair_t A2[S][2], ag[S][2];
-    load_block<S>(p.A, w.d0 + ch, ch, w.wide, n0, p.N, A2);
-    float ssum[4] = {};
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            A2[i][c] = mul2(A2[i][c], dup2(kLog2eF));
-            ag[i][c] = 0;
-        }
-    const T *rp = static_cast<const T *>(p.raw) + w.rowb * p.ldraw + w.d0;
-    const T *yp = static_cast<const T *>(p.dy) + w.rowb * p.lddy + w.d0;
-    const T *cp = static_cast<const T *>(p.Cm) + w.rowb * p.ldc + int64_t(w.g) * p.N;
-    Raw<T, VEC> rr[kPer], yr[kPer];
-    float cr[kBc];
-    auto fetch = [&](int64_t t) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int v = threadIdx.x + i * CV::THREADS;
-            const int64_t row = t + v / (CH / VEC);
-            const int col = v % (CH / VEC) * VEC;
-            rr[i].fill(0.f);
-            yr[i].fill(0.f);
-            if (v < kVecs && row < w.t1 && col < w.wide) {
-                rr[i].load(rp + row * p.ldraw + col);
-                yr[i].load(yp + row * p.lddy + col);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kBc; ++i) {
-            const int e = threadIdx.x + i * CV::THREADS, n = e % NP;
-            const int64_t row = t + e / NP;
-            cr[i] = e < kTile * NP && row < w.t1 && n < p.N ? load1(cp + row * p.ldc + n) : 0.f;
-        }
-    };
-    int64_t t = w.t0 + (w.t1 - 1 - w.t0) / kTile * kTile;
-    int s = q.of(w.rowb + w.t1 - 1);
-    long long lo = q.begin(s) - w.rowb, hi = q.begin(s + 1) - w.rowb;
-    fetch(t);
-    for (; t >= w.t0; t -= kTile) {
-        const int64_t end = t + kTile < w.t1 ? t + kTile : w.t1;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int v = threadIdx.x + i * CV::THREADS;
-            const int row = v / (CH / VEC), col = v % (CH / VEC) * VEC;
-            if (kVecs % CV::THREADS == 0 || v < kVecs) {
-                const bool in = t + row < w.t1 && col < w.wide;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const float bias = in && p.dt_bias != nullptr ? __ldg(p.dt_bias + w.d0 + col + e) : 0.f;
-                    const float r = rr[i][e] + bias;
-                    s_d[row][col + e] = !in ? 0.f : p.softplus ? softplus_f(r) : r;
-                    s_dy[row][col + e] = yr[i][e];
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kBc; ++i) {
-            const int e = threadIdx.x + i * CV::THREADS;
-            if (kTile * NP % CV::THREADS == 0 || e < kTile * NP) s_c[e / NP][e % NP] = cr[i];
-        }
-        const bool edges = lo >= t || hi == end;
-        if (edges) edge_rows(q, w.rowb, t, int(end - t), s_first, s_last);
-        __syncthreads();
-        if (t > w.t0) fetch(t - kTile);
-#pragma unroll 4
-        for (int tt = kTile - 1; tt >= 0; --tt) {
-            if (edges && s_last[tt] >= 0) {
-                load_block<S>(p.dh_last != nullptr ? p.dh_last + int64_t(s_last[tt]) * p.D * p.N : nullptr,
-                              w.d0 + ch, ch, w.wide, n0, p.N, ag);
-            }
-            const float4 d4 = *reinterpret_cast<const float4 *>(&s_d[tt][ch]);
-            const ulonglong2 y2 = *reinterpret_cast<const ulonglong2 *>(&s_dy[tt][ch]);
-            const float4 c4 = *reinterpret_cast<const float4 *>(&s_c[tt][n0]);
-            const pair_t dl[2] = {pack2(d4.x, d4.y), pack2(d4.z, d4.w)}, dy[2] = {y2.x, y2.y};
-            const float cv[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-            for (int i = 0; i < S; ++i)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    ag[i][c] = mul2(decay2(dl[c], A2[i][c]), fma2(dup2(cv[i]), dy[c], ag[i][c]));
-            ssum[0] += d4.x, ssum[1] += d4.y, ssum[2] += d4.z, ssum[3] += d4.w;
-        }
-        if (lo >= t && t > w.t0) {
-            s = q.of(w.rowb + t - 1);
-            lo = q.begin(s) - w.rowb;
-        }
-        hi = q.begin(s + 1) - w.rowb;
-        __syncthreads();
-    }
-    const int64_t at = (w.b * (ck.n - 1) + w.k - 1) * p.D;
-    store_block<S>(agg_q + at * p.N, w.d0 + ch, ch, w.wide, n0, p.N, ag);
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        if (sl == 0 && ch + c < w.wide) agg_s[at + w.d0 + ch + c] = ssum[c];
-}
-
 // s1 and s2 of four channels over LANES lanes (bits STRIDE ..): lane id ends
 // with the sums of channels id 4/LANES .. (or id / (LANES/4)) in a[0], b[0], ..
 template <int LANES, int STRIDE>
@@ -301,7 +189,7 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
     BwdShared<T, VEC, CV> &block = *reinterpret_cast<BwdShared<T, VEC, CV> *>(shared_bytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     BwdWarp<T, VEC, CV> &sm = block.warp[warp];
-    const Spot<CH> w(p, tl, ck, false);
+    const Spot<CH> w(p, tl, ck);
     const int sl = lane / kG, cg = lane % kG, n0 = sl * S;
     const int ch = cg * 4;                                       // of the warp's channels
     const int64_t dw = w.d0 + warp * WCH;                        // the warp's first channel
@@ -591,8 +479,17 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
                         yv[0] = load1(yp + (t + row) * p.lddy + col);
                     }
                     if (p.softplus) {
+                        if constexpr (VEC > 1) {
 #pragma unroll
-                        for (int e = 0; e < VEC; ++e) rv[e] = softplus_f(rv[e] + bias[e], sv[e]);
+                            for (int e = 0; e < VEC; e += 2) {
+                                pair_t sg;
+                                const pair_t r = add2(pack2(rv[e], rv[e + 1]), pack2(bias[e], bias[e + 1]));
+                                unpack2(softplus2(r, sg), rv[e], rv[e + 1]);
+                                unpack2(sg, sv[e], sv[e + 1]);
+                            }
+                        } else {
+                            rv[0] = softplus_f(rv[0] + bias[0], sv[0]);
+                        }
                     } else {
 #pragma unroll
                         for (int e = 0; e < VEC; ++e) rv[e] += bias[e], sv[e] = 1.f;
@@ -686,7 +583,8 @@ inline int64_t backward_tiles(int64_t D, int N, int G)
 
 inline Chunks backward_chunks(int64_t B, int64_t T, int64_t D, int N, int G)
 {
-    static constexpr RowTime r{{0, 560, 1070, 0}, 2, 0.2};
+    // measured: 152 blocks, and 304 blocks, a row each
+    static constexpr RowTime r{{0, 450, 714, 0}, 2, 0.2};
     return cut_time(B * G * backward_tiles(D, N, G), T, r);
 }
 
@@ -710,9 +608,8 @@ mg_status bwd(const SsmArgs &p, cudaStream_t s)
         MG_TRY(launch_empty_sequences(q, p.dh0, p.dh_last, dn, p.ws, s));
     }
     if (ck.n > 1) {
-        ssm_adjoint_chunk_kernel<T, VEC, CV><<<unsigned(tiles * (ck.n - 1)), CV::THREADS, 0, s>>>(
-            p, q, t, ck, agg_q, agg_s);
-        MG_TRY(launched("mg_selective_scan_bwd"));
+        constexpr mg_dtype dt = sizeof(T) == 4 ? MG_F32 : MG_BF16;
+        MG_TRY(launch_ssm_adjoint(p, dt, VEC > 1, ck, agg_q, agg_s, s));
     }
     constexpr size_t smem = sizeof(BwdShared<T, VEC, CV>);
     static_assert(smem <= 227 * 1024, "shared memory of a block");
