@@ -13,7 +13,94 @@
 namespace mg {
 namespace {
 
-constexpr int kUnroll = 4;   // rows loaded before the first of them is used
+// Rows of a group, and groups of a thread's ring.
+constexpr int kUnroll = 4;
+constexpr int kGroups = 3;
+constexpr int kBlock = 128;
+// Blocks that an SM holds: the registers allow 6 of the forward's and 4 of the
+// gradients'; one more or fewer of either was slower.
+constexpr int kFwdPerSm = 6, kBwdPerSm = 4;
+
+// VEC neighbouring channels of a row.
+template <typename T, int VEC>
+__device__ __forceinline__ void store_lanes(T *to, const Lanes<VEC> &v)
+{
+    float o[VEC];
+    vto<VEC>(v, o);
+    store_vec<VEC>(to, o);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Lanes<VEC> load_lanes(const T *from)
+{
+    float o[VEC];
+    load_vec<VEC>(from, o);
+    return vfrom<VEC>(o);
+}
+
+// A thread's own ring of rows in shared memory, filled by asynchronous copies
+// kGroups - 1 groups ahead of the one at hand: what is in flight takes no
+// registers, and no other thread reads it, so nothing but the thread's own
+// copies is waited for.  Rows of 2 bytes, which no asynchronous copy moves,
+// are loaded when they are needed.
+template <typename T, int VEC>
+struct Ring {
+    static constexpr int kBytes = int(sizeof(T)) * VEC;
+    static constexpr bool kAsync = kBytes >= 4;
+    static constexpr size_t bytes(int threads) { return kAsync ? size_t(kGroups) * kUnroll * threads * kBytes : 0; }
+    T *mine;            // the thread's vector of ring row 0
+    const T *next;      // the next row to be copied (or loaded)
+    int64_t ld;
+    Raw<T, VEC> here[kAsync ? 1 : kUnroll];   // the group at hand, where nothing is copied ahead
+    __device__ __forceinline__ Ring(unsigned char *base, const T *first, int64_t stride) : next(first), ld(stride)
+    {
+        mine = reinterpret_cast<T *>(base) + (threadIdx.y * blockDim.x + threadIdx.x) * VEC;
+    }
+    __device__ __forceinline__ T *at(int row) const { return mine + row * kBlock * VEC; }
+    // Starts the copies of the rows i0 .. of a run of n into ring group g.
+    __device__ __forceinline__ void fetch(int g, int i0, int n)
+    {
+        if constexpr (kAsync) {
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                if (i0 + i < n) {
+                    if constexpr (kBytes == 16)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" : : "r"(smem_addr(at(g * kUnroll + i))),
+                                     "l"(next) : "memory");
+                    else
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" : : "r"(smem_addr(at(g * kUnroll + i))),
+                                     "l"(next), "n"(kBytes) : "memory");
+                }
+                next += ld;
+            }
+        }
+    }
+    // The group at hand, rows i0 .. of a run of n.
+    __device__ __forceinline__ void open(int i0, int n)
+    {
+        if constexpr (!kAsync) {
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                if (i0 + i < n) here[i].load(next);
+                next += ld;
+            }
+        }
+    }
+    // Row i of ring group g, the group at hand.
+    __device__ __forceinline__ Lanes<VEC> get(int g, int i) const
+    {
+        if constexpr (kAsync) return load_lanes<T, VEC>(at(g * kUnroll + i));
+        else return vraw<T, VEC>(here[i]);
+    }
+    __device__ __forceinline__ Lanes<VEC> get_any(int g, int i) const   // i not known when compiled
+    {
+        if constexpr (kAsync) return load_lanes<T, VEC>(at(g * kUnroll + i));
+        Raw<T, VEC> r = here[0];
+#pragma unroll
+        for (int k = 1; k < (kAsync ? 1 : kUnroll); ++k)
+            if (i == k) r = here[k];
+        return vraw<T, VEC>(r);
+    }
+};
 
 // A thread's place: its channels and its run of rows.
 struct Place {
@@ -33,47 +120,103 @@ __device__ __forceinline__ Place place(int64_t chan_blocks, int vec, int64_t D, 
     return w;
 }
 
-// The sequence a run is in.  lo and hi are its bounds, lo kept within
-// [0, row] whatever cu holds.
+// The sequence that a run is in, its bounds counted from the run's first row
+// (a run has fewer than kFar rows; lo <= 0 whatever cu holds).
+constexpr int kFar = 1 << 30;
 struct Walk {
-    int s;
-    long long lo, hi;
-    __device__ __forceinline__ void start(const Seqs &q, long long r)
+    int s, lo, hi;
+    __device__ __forceinline__ void bounds(const Seqs &q, long long r0)
     {
-        s = q.of(r);
-        lo = q.begin(s);
-        hi = q.begin(s + 1);
-        lo = lo < 0 ? 0 : (lo > r ? r : lo);
+        const long long a = q.begin(s) - r0, b = q.begin(s + 1) - r0;
+        lo = int(a < -kFar ? -kFar : a > kFar ? kFar : a);
+        hi = int(b < -kFar ? -kFar : b > kFar ? kFar : b);
+    }
+    __device__ __forceinline__ void start(const Seqs &q, long long r0)
+    {
+        s = q.of(r0);
+        bounds(q, r0);
+        if (lo > 0 || lo < -r0) lo = 0;
     }
 };
 
 // A sequence's edge state (W-1 rows), x0 or dx_last: row j, or zero.
 template <typename T, int VEC, int W>
-__device__ __forceinline__ void load_edge(const T *edge, int s, int j, int64_t D, int64_t d,
-                                          float (&o)[VEC])
+__device__ __forceinline__ Lanes<VEC> load_edge(const T *edge, int s, int j, int64_t D, int64_t d)
 {
-    if (edge != nullptr) {
-        load_vec<VEC>(edge + (int64_t(s) * (W - 1) + j) * D + d, o);
-    } else {
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) o[v] = 0.f;
-    }
+    if (edge == nullptr) return vset<VEC>(0.f);
+    float o[VEC];
+    load_vec<VEC>(edge + (int64_t(s) * (W - 1) + j) * D + d, o);
+    return vfrom<VEC>(o);
 }
-
 // An empty sequence hands its edge state on: dst[s] = src[s] (or zero).
 template <typename T, int VEC, int W>
-__device__ __forceinline__ void copy_edge(T *dst, const T *src, int s, int64_t D, int64_t d)
+__device__ __noinline__ void copy_edge(T *dst, const T *src, int s, int64_t D, int64_t d)
 {
     if (dst == nullptr) return;
+    for (int j = 0; j < W - 1; ++j)
+        store_lanes<T, VEC>(dst + (int64_t(s) * (W - 1) + j) * D + d, load_edge<T, VEC, W>(src, s, j, D, d));
+}
+
+// The thread's taps and bias.
+template <int VEC, int W>
+__device__ __forceinline__ void load_taps(const ConvArgs &p, int64_t d, Lanes<VEC> (&w)[W], Lanes<VEC> &bias)
+{
+    float f[VEC];
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) f[v] = __ldg(p.w + (d + v) * W + k);
+        w[k] = vfrom<VEC>(f);
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) f[v] = p.bias != nullptr ? __ldg(p.bias + d + v) : 0.f;
+    bias = vfrom<VEC>(f);
+}
+
+// The inputs of rows r0-W+1 .. r0-1 into win[1 ..].
+template <typename T, int VEC, int W>
+__device__ __forceinline__ void first_window(const T *x, const T *x0, const ConvArgs &p, const Walk &k, int64_t r0,
+                                             int64_t d, Lanes<VEC> (&win)[W])
+{
+#pragma unroll
     for (int j = 0; j < W - 1; ++j) {
-        float o[VEC];
-        load_edge<T, VEC, W>(src, s, j, D, d, o);
-        store_vec<VEC>(dst + (int64_t(s) * (W - 1) + j) * D + d, o);
+        const int i = j - (W - 1);
+        win[j + 1] = i >= k.lo ? load_lanes<T, VEC>(x + (r0 + i) * p.ldx + d)
+                               : load_edge<T, VEC, W>(x0, k.s, i - k.lo + W - 1, p.D, d);
     }
 }
 
+// Moves the walk to the sequence that begins at row i of the run; empty ones
+// on the way hand their edge states on.
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs p, Seqs q, int64_t chan_blocks,
+__device__ __forceinline__ void next_sequence(const Seqs &q, Walk &k, int64_t r0, int i, T *dst, const T *src,
+                                              int64_t D, int64_t d)
+{
+    const int s = q.of(r0 + i);
+    for (++k.s; k.s < s; ++k.s) copy_edge<T, VEC, W>(dst, src, k.s, D, d);
+    k.s = s;
+    k.bounds(q, r0);
+    k.lo = i;
+}
+
+// Empty sequences that lie at the run's first row, or at the batch's end,
+// hand their edge states on.
+template <typename T, int VEC, int W>
+__device__ __forceinline__ void empty_before(const Seqs &q, const Walk &k, int64_t r0, T *dst, const T *src,
+                                             int64_t D, int64_t d)
+{
+    if (k.lo == 0)
+        for (int e = k.s - 1; e >= 0 && q.begin(e) == r0; --e) copy_edge<T, VEC, W>(dst, src, e, D, d);
+}
+template <typename T, int VEC, int W>
+__device__ __forceinline__ void empty_after(const Seqs &q, int64_t r1, T *dst, const T *src, int64_t D, int64_t d)
+{
+    if (r1 != q.rows) return;
+    for (int e = q.nseq - 1; e >= 0 && q.begin(e) >= q.rows; --e) copy_edge<T, VEC, W>(dst, src, e, D, d);
+}
+
+template <typename T, int VEC, int W>
+__global__ void __launch_bounds__(kBlock, kFwdPerSm) conv_fwd_kernel(ConvArgs p, Seqs q, int64_t chan_blocks,
                                                        int64_t run)
 {
     if (blockIdx.x == 0)
@@ -81,68 +224,69 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs p, Seqs q, int64
                  blockDim.x * blockDim.y);
     const Place at = place(chan_blocks, VEC, p.D, q.rows, run);
     if (!at.live) return;
+    extern __shared__ __align__(16) unsigned char ring_bytes[];
     const int64_t D = p.D, d = at.d;
     const T *x = static_cast<const T *>(p.x), *x0 = static_cast<const T *>(p.x0);
     T *y = static_cast<T *>(p.y), *x_last = static_cast<T *>(p.x_last);
-    float w[W][VEC], bias[VEC];
-#pragma unroll
-    for (int v = 0; v < VEC; ++v) {
-        bias[v] = p.bias != nullptr ? __ldg(p.bias + d + v) : 0.f;
-#pragma unroll
-        for (int k = 0; k < W; ++k) w[k][v] = __ldg(p.w + (d + v) * W + k);
-    }
+    Lanes<VEC> w[W], bias, win[W];   // win: inputs r-W+1 .. r
+    load_taps<VEC, W>(p, d, w, bias);
     Walk k;
     k.start(q, at.r0);
-    if (k.lo == at.r0)   // empty sequences that lie at this row
-        for (int e = k.s - 1; e >= 0 && q.begin(e) == at.r0; --e) copy_edge<T, VEC, W>(x_last, x0, e, D, d);
-    float win[W][VEC];   // inputs r-W+1 .. r
+    empty_before<T, VEC, W>(q, k, at.r0, x_last, x0, D, d);
+    first_window<T, VEC, W>(x, x0, p, k, at.r0, d, win);
+    T *yp = y + at.r0 * D + d;
+    const int n = int(at.r1 - at.r0);
+    Ring<T, VEC> ring(ring_bytes, x + at.r0 * p.ldx + d, p.ldx);
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) {
-        const int64_t r = at.r0 - (W - 1) + j;
-        if (r >= k.lo) load_vec<VEC>(x + r * p.ldx + d, win[j + 1]);
-        else load_edge<T, VEC, W>(x0, k.s, int(r - k.lo + W - 1), D, d, win[j + 1]);
+    for (int g = 0; g < kGroups - 1; ++g) {
+        ring.fetch(g, g * kUnroll, n);
+        cp_async_commit();
     }
-    for (int64_t rb = at.r0; rb < at.r1; rb += kUnroll) {
-        Raw<T, VEC> in[kUnroll];
+    auto row = [&](const Lanes<VEC> &in, T *to) {
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
-            if (rb + i < at.r1) in[i].load(x + (rb + i) * p.ldx + d);
+        for (int j = 0; j + 1 < W; ++j) win[j] = win[j + 1];
+        win[W - 1] = in;
+        Lanes<VEC> a = bias;
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const int64_t r = rb + i;
-            if (r >= at.r1) break;
-            if (r == k.hi) {   // a new sequence (empty ones on the way)
-                ++k.s;
-                while (k.s + 1 < q.nseq && q.begin(k.s + 1) <= r) {
-                    copy_edge<T, VEC, W>(x_last, x0, k.s, D, d);
-                    ++k.s;
+        for (int j = 0; j < W; ++j) a = vfma<VEC>(w[j], win[j], a);
+        if (p.silu) a = vmul<VEC>(a, vsigmoid<VEC>(a));
+        float o[VEC];
+        vto<VEC>(a, o);
+        store_out<VEC>(to, o);
+    };
+    int g = 0;
+    for (int i0 = 0; i0 < n; i0 += kUnroll) {
+        ring.fetch(g == 0 ? kGroups - 1 : g - 1, i0 + (kGroups - 1) * kUnroll, n);
+        cp_async_commit();
+        cp_async_wait<kGroups - 1>();
+        ring.open(i0, n);
+        if (i0 + kUnroll <= n && k.hi > i0 + kUnroll) {   // whole, inside one sequence
+#pragma unroll
+            for (int i = 0; i < kUnroll; ++i) {
+                row(ring.get(g, i), yp);
+                yp += D;
+            }
+        } else {
+#pragma unroll 1
+            for (int i = i0; i < i0 + kUnroll && i < n; ++i) {
+                if (i == k.hi) {
+                    next_sequence<T, VEC, W>(q, k, at.r0, i, x_last, x0, D, d);
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) win[j + 1] = load_edge<T, VEC, W>(x0, k.s, j, D, d);
                 }
-                if (k.s >= q.nseq) k.s = q.nseq - 1;
-                k.hi = q.begin(k.s + 1);
+                row(ring.get_any(g, i - i0), yp);
+                yp += D;
+                if (i + 1 == k.hi && x_last != nullptr) {
 #pragma unroll
-                for (int j = 0; j < W - 1; ++j) load_edge<T, VEC, W>(x0, k.s, j, D, d, win[j + 1]);
-            }
-            float o[VEC];
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-#pragma unroll
-                for (int j = 0; j + 1 < W; ++j) win[j][v] = win[j + 1][v];
-                win[W - 1][v] = in[i][v];
-                float a = bias[v];
-#pragma unroll
-                for (int j = 0; j < W; ++j) a = fmaf(w[j][v], win[j][v], a);
-                o[v] = p.silu ? a * sigmoid_f(a) : a;
-            }
-            store_vec<VEC>(y + r * D + d, o);
-            if (r + 1 == k.hi && x_last != nullptr) {
-#pragma unroll
-                for (int j = 0; j < W - 1; ++j)
-                    store_vec<VEC>(x_last + (int64_t(k.s) * (W - 1) + j) * D + d, win[j + 1]);
+                    for (int j = 0; j < W - 1; ++j)
+                        store_lanes<T, VEC>(x_last + (int64_t(k.s) * (W - 1) + j) * D + d, win[j + 1]);
+                }
             }
         }
+        g = g + 1 == kGroups ? 0 : g + 1;
     }
-    if (at.r1 == q.rows)   // empty sequences at the end
-        for (int e = k.s + 1; e < q.nseq; ++e) copy_edge<T, VEC, W>(x_last, x0, e, D, d);
+    cp_async_wait<0>();
+    empty_after<T, VEC, W>(q, at.r1, x_last, x0, D, d);
 }
 
 // Gradients.  The walk carries, next to the window, the sums that the rows
@@ -151,138 +295,151 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs p, Seqs q, int64
 // last rows' sums.  dw and dbias are summed over the run in registers, over
 // the block in shared memory and over the blocks by sum_parts_kernel.
 template <typename T, int VEC, int W>
-__global__ void __launch_bounds__(256) conv_bwd_kernel(ConvArgs p, Seqs q, int64_t chan_blocks,
+__global__ void __launch_bounds__(kBlock, kBwdPerSm) conv_bwd_kernel(ConvArgs p, Seqs q, int64_t chan_blocks,
                                                        int64_t run, float *part)
 {
-    extern __shared__ float sums[];   // [blockDim.y][blockDim.x][VEC * (W + 1)]
+    // the rings, and after them the sums [blockDim.y][VEC * (W + 1)][blockDim.x]
+    extern __shared__ __align__(16) unsigned char ring_bytes[];
+    float *sums = reinterpret_cast<float *>(ring_bytes);
     constexpr int NS = VEC * (W + 1);
     if (blockIdx.x == 0)
         check_cu(q, error_word(p.ws), threadIdx.y * blockDim.x + threadIdx.x,
                  blockDim.x * blockDim.y);
     const Place at = place(chan_blocks, VEC, p.D, q.rows, run);
-    const int64_t D = p.D, d = at.d, rows = q.rows;
-    float dw[W][VEC] = {}, db[VEC] = {};
+    const int64_t D = p.D, d = at.d, rows_all = q.rows;
+    Lanes<VEC> dw[W], db = vset<VEC>(0.f);
+#pragma unroll
+    for (int j = 0; j < W; ++j) dw[j] = vset<VEC>(0.f);
     if (at.live) {
         const T *x = static_cast<const T *>(p.x), *x0 = static_cast<const T *>(p.x0);
         const T *dy = static_cast<const T *>(p.dy), *dx_last = static_cast<const T *>(p.dx_last);
         T *dx = static_cast<T *>(p.dx), *dx0 = static_cast<T *>(p.dx0);
-        float w[W][VEC], bias[VEC];
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) {
-            bias[v] = p.bias != nullptr ? __ldg(p.bias + d + v) : 0.f;
-#pragma unroll
-            for (int k = 0; k < W; ++k) w[k][v] = __ldg(p.w + (d + v) * W + k);
-        }
+        Lanes<VEC> w[W], bias, win[W], acc[W];
+        load_taps<VEC, W>(p, d, w, bias);
         Walk k;
         k.start(q, at.r0);
-        if (k.lo == at.r0)
-            for (int e = k.s - 1; e >= 0 && q.begin(e) == at.r0; --e)
-                copy_edge<T, VEC, W>(dx0, dx_last, e, D, d);
-        float win[W][VEC], acc[W][VEC] = {};
+        empty_before<T, VEC, W>(q, k, at.r0, dx0, dx_last, D, d);
+        first_window<T, VEC, W>(x, x0, p, k, at.r0, d, win);
 #pragma unroll
-        for (int j = 0; j < W - 1; ++j) {
-            const int64_t r = at.r0 - (W - 1) + j;
-            if (r >= k.lo) load_vec<VEC>(x + r * p.ldx + d, win[j + 1]);
-            else load_edge<T, VEC, W>(x0, k.s, int(r - k.lo + W - 1), D, d, win[j + 1]);
-        }
-        // dx of row r, or of a row before the sequence, is complete.
-        auto emit = [&](int64_t r, const float (&v)[VEC]) {
-            if (r >= k.lo) {
-                if (r >= at.r0 && r < at.r1) store_vec<VEC>(dx + r * D + d, v);
-            } else if (dx0 != nullptr && k.lo >= at.r0 && k.lo < at.r1 && r >= k.lo - (W - 1)) {
-                store_vec<VEC>(dx0 + (int64_t(k.s) * (W - 1) + (r - k.lo + W - 1)) * D + d, v);
+        for (int j = 0; j < W; ++j) acc[j] = vset<VEC>(0.f);
+        const int own = int(at.r1 - at.r0);   // rows, and those past the end for their sums
+        const int n = int((at.r1 + W - 1 < rows_all ? at.r1 + W - 1 : rows_all) - at.r0);
+        // dx of row i of the run, or of a row before the sequence, is complete.
+        auto emit = [&](int i, const Lanes<VEC> &v) {
+            if (i >= k.lo) {
+                if (i >= 0 && i < own) store_lanes<T, VEC>(dx + (at.r0 + i) * D + d, v);
+            } else if (dx0 != nullptr && k.lo >= 0 && k.lo < own && i >= k.lo - (W - 1)) {
+                store_lanes<T, VEC>(dx0 + (int64_t(k.s) * (W - 1) + (i - k.lo + W - 1)) * D + d, v);
             }
         };
-        const int64_t stop = at.r1 + W - 1 < rows ? at.r1 + W - 1 : rows;
         bool done = false;
-        for (int64_t rb = at.r0; rb < stop && !done; rb += kUnroll) {
-            Raw<T, VEC> in[kUnroll], gy[kUnroll];
+        Ring<T, VEC> ring(ring_bytes, x + at.r0 * p.ldx + d, p.ldx);
+        Ring<T, VEC> ring_g(ring_bytes + Ring<T, VEC>::bytes(kBlock), dy + at.r0 * p.lddy + d, p.lddy);
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i)
-                if (rb + i < stop) {
-                    in[i].load(x + (rb + i) * p.ldx + d);
-                    gy[i].load(dy + (rb + i) * p.lddy + d);
-                }
+        for (int g = 0; g < kGroups - 1; ++g) {
+            ring.fetch(g, g * kUnroll, n);
+            ring_g.fetch(g, g * kUnroll, n);
+            cp_async_commit();
+        }
+        // row i of the run: acc[0] becomes what row i - (W - 1) of dx is
+        auto row = [&](const Lanes<VEC> &in_row, Lanes<VEC> dv, bool mine) {
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                const int64_t r = rb + i;
-                if (r >= stop || done) break;
-                if (r == k.hi) {
-                    ++k.s;
-                    while (k.s + 1 < q.nseq && q.begin(k.s + 1) <= r) {
-                        copy_edge<T, VEC, W>(dx0, dx_last, k.s, D, d);
-                        ++k.s;
-                    }
-                    if (k.s >= q.nseq) k.s = q.nseq - 1;
-                    k.lo = r;
-                    k.hi = q.begin(k.s + 1);
+            for (int j = 0; j + 1 < W; ++j) {
+                win[j] = win[j + 1];
+                acc[j] = acc[j + 1];
+            }
+            win[W - 1] = in_row;
+            if (p.silu) {   // silu'(v) = s (1 + v (1 - s))
+                Lanes<VEC> v = bias;
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) {
-                        load_edge<T, VEC, W>(x0, k.s, j, D, d, win[j + 1]);
+                for (int j = 0; j < W; ++j) v = vfma<VEC>(w[j], win[j], v);
+                const Lanes<VEC> s = vsigmoid<VEC>(v), one = vset<VEC>(1.f);
+                const Lanes<VEC> rest = vfma<VEC>(s, vset<VEC>(-1.f), one);
+                dv = vmul<VEC>(dv, vmul<VEC>(s, vfma<VEC>(v, rest, one)));
+            }
+            if (mine) {
+                db = vadd<VEC>(db, dv);
 #pragma unroll
-                        for (int v = 0; v < VEC; ++v) acc[j + 1][v] = 0.f;
-                    }
-                }
-                const bool own = r < at.r1;
+                for (int j = 0; j < W; ++j) dw[j] = vfma<VEC>(dv, win[j], dw[j]);
+            }
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) {
+            for (int j = 0; j + 1 < W; ++j) acc[j] = vfma<VEC>(w[j], dv, acc[j]);
+            acc[W - 1] = vmul<VEC>(w[W - 1], dv);
+        };
+        T *dxp = dx + (at.r0 - (W - 1)) * D + d;   // of the row that the next one completes
+        int g = 0;
+        for (int i0 = 0; i0 < n && !done; i0 += kUnroll) {
+            ring.fetch(g == 0 ? kGroups - 1 : g - 1, i0 + (kGroups - 1) * kUnroll, n);
+            ring_g.fetch(g == 0 ? kGroups - 1 : g - 1, i0 + (kGroups - 1) * kUnroll, n);
+            cp_async_commit();
+            cp_async_wait<kGroups - 1>();
+            ring.open(i0, n);
+            ring_g.open(i0, n);
+            // whole, inside one sequence and the run, and no row before the
+            // sequence is completed
+            if (i0 + kUnroll <= own && k.hi > i0 + kUnroll && (k.lo < 0 || i0 - (W - 1) >= k.lo)) {
 #pragma unroll
-                    for (int j = 0; j + 1 < W; ++j) {
-                        win[j][v] = win[j + 1][v];
-                        acc[j][v] = acc[j + 1][v];
-                    }
-                    win[W - 1][v] = in[i][v];
-                    acc[W - 1][v] = 0.f;
-                    float dv = gy[i][v];
-                    if (p.silu) {
-                        float a = bias[v];
-#pragma unroll
-                        for (int j = 0; j < W; ++j) a = fmaf(w[j][v], win[j][v], a);
-                        const float sg = sigmoid_f(a);
-                        dv *= sg * fmaf(a, 1.f - sg, 1.f);
-                    }
-                    if (own) db[v] += dv;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) {
-                        acc[j][v] = fmaf(w[j][v], dv, acc[j][v]);
-                        if (own) dw[j][v] = fmaf(dv, win[j][v], dw[j][v]);
-                    }
-                }
-                emit(r - (W - 1), acc[0]);
-                if (r + 1 == k.hi) {   // the sequence ends: the rest is complete too
-#pragma unroll
-                    for (int j = 0; j < W - 1; ++j) {
+                for (int i = 0; i < kUnroll; ++i) {
+                    row(ring.get(g, i), ring_g.get(g, i), true);
+                    if (i0 + i >= W - 1) {
                         float o[VEC];
-                        load_edge<T, VEC, W>(dx_last, k.s, j, D, d, o);
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v) o[v] += acc[j + 1][v];
-                        emit(r - (W - 2) + j, o);
+                        vto<VEC>(acc[0], o);
+                        store_out<VEC>(dxp, o);
                     }
-                    done = r + 1 >= at.r1;
+                    dxp += D;
+                }
+            } else {
+#pragma unroll 1
+                for (int i = i0; i < i0 + kUnroll && i < n && !done; ++i) {
+                    if (i == k.hi) {
+                        next_sequence<T, VEC, W>(q, k, at.r0, i, dx0, dx_last, D, d);
+#pragma unroll
+                        for (int j = 0; j < W - 1; ++j) {
+                            win[j + 1] = load_edge<T, VEC, W>(x0, k.s, j, D, d);
+                            acc[j + 1] = vset<VEC>(0.f);
+                        }
+                    }
+                    row(ring.get_any(g, i - i0), ring_g.get_any(g, i - i0), i < own);
+                    emit(i - (W - 1), acc[0]);
+                    dxp += D;
+                    if (i + 1 == k.hi) {   // the sequence ends: the rest is complete too
+#pragma unroll
+                        for (int j = 0; j < W - 1; ++j)
+                            emit(i - (W - 2) + j, vadd<VEC>(acc[j + 1], load_edge<T, VEC, W>(dx_last, k.s, j, D, d)));
+                        done = i + 1 >= own;
+                    }
                 }
             }
+            g = g + 1 == kGroups ? 0 : g + 1;
         }
-        if (at.r1 == rows)
-            for (int e = k.s + 1; e < q.nseq; ++e) copy_edge<T, VEC, W>(dx0, dx_last, e, D, d);
+        cp_async_wait<0>();
+        empty_after<T, VEC, W>(q, at.r1, dx0, dx_last, D, d);
     }
+    __syncthreads();   // every thread is done with its rings
     // the block's sums over its runs, in order
-    float *mine = sums + (threadIdx.y * blockDim.x + threadIdx.x) * NS;
+    const int lanes = blockDim.x;
+    float *mine = sums + threadIdx.y * lanes * NS + threadIdx.x;
+    float f[VEC];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) {
+    for (int k = 0; k < W; ++k) {
+        vto<VEC>(dw[k], f);
 #pragma unroll
-        for (int k = 0; k < W; ++k) mine[v * W + k] = dw[k][v];
-        mine[VEC * W + v] = db[v];
+        for (int v = 0; v < VEC; ++v) mine[(v * W + k) * lanes] = f[v];
     }
+    vto<VEC>(db, f);
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) mine[(VEC * W + v) * lanes] = f[v];
     __syncthreads();
-    if (threadIdx.y == 0 && d < D) {
-        const int64_t rb = blockIdx.x / chan_blocks;
-        float *out = part + rb * D * (W + 1);
-        for (int i = 0; i < NS; ++i) {
-            float a = 0.f;
-            for (int yy = 0; yy < blockDim.y; ++yy) a += sums[(yy * blockDim.x + threadIdx.x) * NS + i];
-            if (i < VEC * W) out[d * W + i] = a;
-            else out[D * W + d + (i - VEC * W)] = a;
-        }
+    const int64_t d00 = blockIdx.x % chan_blocks * lanes * VEC, rb = blockIdx.x / chan_blocks;
+    float *out = part + rb * D * (W + 1);
+    for (int e = threadIdx.y * lanes + threadIdx.x; e < lanes * NS; e += lanes * blockDim.y) {
+        const int lane = e % lanes, i = e / lanes;
+        const int64_t dd = d00 + lane * VEC;
+        if (dd >= D) continue;
+        float a = 0.f;
+        for (int yy = 0; yy < blockDim.y; ++yy) a += sums[(yy * NS + i) * lanes + lane];
+        if (i < VEC * W) out[dd * W + i] = a;
+        else out[D * W + dd + (i - VEC * W)] = a;
     }
 }
 
@@ -313,8 +470,10 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvStepArgs p)
         float a = p.bias != nullptr ? __ldg(p.bias + d + v) : 0.f;
 #pragma unroll
         for (int j = 0; j < W; ++j) a = fmaf(__ldg(p.w + (d + v) * W + j), win[j][v], a);
-        o[v] = p.silu ? a * sigmoid_f(a) : a;
+        o[v] = a;
     }
+    const Lanes<VEC> a = vfrom<VEC>(o);
+    if (p.silu) vto<VEC>(vmul<VEC>(a, vsigmoid<VEC>(a)), o);
     store_vec<VEC>(y, o);
 #pragma unroll
     for (int j = 0; j < W - 1; ++j) store_vec<VEC>(st + j * D, win[j + 1]);
@@ -345,14 +504,14 @@ struct Cut {
     int64_t chan_blocks, run, row_blocks;
 };
 
-// Lanes run over channels (a multiple of a warp, at most 128), the rest of
-// 256 threads over runs; runs of `least` rows or more, long enough for about
+// Lanes run over channels (a multiple of a warp), the rest of a block over
+// runs; runs of `least` rows or more, long enough for about
 // `blocks` blocks in all.
 Cut cut(int64_t rows, int64_t D, int vec, int64_t least, int64_t blocks)
 {
     Cut c;
     const int64_t lanes = ceil_div(D, vec);
-    const int bx = lanes <= 32 ? 32 : lanes <= 64 ? 64 : 128, by = 256 / bx;
+    const int bx = lanes <= 32 ? 32 : lanes <= 64 ? 64 : kBlock, by = kBlock / bx;
     c.block = dim3(bx, by);
     c.chan_blocks = ceil_div(lanes, bx);
     const int64_t want = ceil_div(blocks, c.chan_blocks) * by;
@@ -362,7 +521,7 @@ Cut cut(int64_t rows, int64_t D, int vec, int64_t least, int64_t blocks)
     return c;
 }
 
-constexpr int64_t kBwdBlocks = 608;   // 4 blocks for each of 152 SMs
+constexpr int64_t kBwdBlocks = 152 * kBwdPerSm;
 
 Cut cut_bwd(int64_t rows, int64_t D, int vec) { return cut(rows, D, vec, 16, kBwdBlocks); }
 
@@ -375,8 +534,8 @@ template <typename T, int VEC, int W>
 mg_status conv_fwd(const ConvArgs &p, cudaStream_t s)
 {
     const Seqs q = make_seqs(p.cu, p.B, p.T, p.nseq);
-    const Cut c = cut(q.rows, p.D, VEC, 16, 4096);
-    conv_fwd_kernel<T, VEC, W><<<unsigned(c.chan_blocks * c.row_blocks), c.block, 0, s>>>(
+    const Cut c = cut(q.rows, p.D, VEC, 16, 152 * kFwdPerSm);
+    conv_fwd_kernel<T, VEC, W><<<unsigned(c.chan_blocks * c.row_blocks), c.block, Ring<T, VEC>::bytes(kBlock), s>>>(
         p, q, c.chan_blocks, c.run);
     return launched("mg_causal_conv_fwd");
 }
@@ -387,7 +546,9 @@ mg_status conv_bwd(const ConvArgs &p, cudaStream_t s)
     const Seqs q = make_seqs(p.cu, p.B, p.T, p.nseq);
     const Cut c = cut_bwd(q.rows, p.D, VEC);
     float *part = reinterpret_cast<float *>(static_cast<char *>(p.ws) + kControlBytes);
-    const size_t smem = 256 * size_t(VEC * (W + 1)) * sizeof(float);
+    constexpr size_t sums = kBlock * size_t(VEC * (W + 1)) * sizeof(float), rings = 2 * Ring<T, VEC>::bytes(kBlock);
+    constexpr size_t smem = sums > rings ? sums : rings;
+    MG_TRY(allow_shared(conv_bwd_kernel<T, VEC, W>, smem));
     conv_bwd_kernel<T, VEC, W><<<unsigned(c.chan_blocks * c.row_blocks), c.block, smem, s>>>(
         p, q, c.chan_blocks, c.run, part);
     MG_TRY(launched("mg_causal_conv_bwd"));
@@ -426,7 +587,7 @@ size_t conv_ws_bytes(int64_t B, int64_t T, int64_t D, int W)
 {
     // the parts of either vector width
     size_t need = 0;
-    for (int vec : {1, 4}) {
+    for (int vec : {1, 2, 4}) {
         const Cut c = cut_bwd(B * T, D, vec);
         const size_t n = size_t(c.row_blocks) * D * (W + 1) * sizeof(float);
         need = n > need ? n : need;
@@ -434,26 +595,22 @@ size_t conv_ws_bytes(int64_t B, int64_t T, int64_t D, int W)
     return kControlBytes + need;
 }
 
+// The widest vectors, 4, 2 or 1 channels, that keep every row aligned.
+#define MG_CONV_VEC(F, T, p, s, ld2)                                             \
+    if (rows_aligned((p).D, (p).ldx, ld2, 4)) { MG_CONV_W(F, T, 4, p, s); }      \
+    if (rows_aligned((p).D, (p).ldx, ld2, 2)) { MG_CONV_W(F, T, 2, p, s); }      \
+    MG_CONV_W(F, T, 1, p, s)
+
 mg_status launch_conv_fwd(const ConvArgs &p, mg_dtype dt, cudaStream_t s)
 {
-    const bool wide = rows_aligned(p.D, p.ldx, p.ldx, 4);
-    if (dt == MG_F32) {
-        if (wide) { MG_CONV_W(conv_fwd, float, 4, p, s); }
-        MG_CONV_W(conv_fwd, float, 1, p, s);
-    }
-    if (wide) { MG_CONV_W(conv_fwd, bf16_t, 4, p, s); }
-    MG_CONV_W(conv_fwd, bf16_t, 1, p, s);
+    if (dt == MG_F32) { MG_CONV_VEC(conv_fwd, float, p, s, p.ldx); }
+    MG_CONV_VEC(conv_fwd, bf16_t, p, s, p.ldx);
 }
 
 mg_status launch_conv_bwd(const ConvArgs &p, mg_dtype dt, cudaStream_t s)
 {
-    const bool wide = rows_aligned(p.D, p.ldx, p.lddy, 4);
-    if (dt == MG_F32) {
-        if (wide) { MG_CONV_W(conv_bwd, float, 4, p, s); }
-        MG_CONV_W(conv_bwd, float, 1, p, s);
-    }
-    if (wide) { MG_CONV_W(conv_bwd, bf16_t, 4, p, s); }
-    MG_CONV_W(conv_bwd, bf16_t, 1, p, s);
+    if (dt == MG_F32) { MG_CONV_VEC(conv_bwd, float, p, s, p.lddy); }
+    MG_CONV_VEC(conv_bwd, bf16_t, p, s, p.lddy);
 }
 
 mg_status launch_conv_step(const ConvStepArgs &p, mg_dtype dt, cudaStream_t s)

@@ -189,6 +189,10 @@ __device__ __forceinline__ void load_vec(const bf16_t *p, float (&o)[VEC])
         o[1] = __uint_as_float(x.x & 0xffff0000u);
         o[2] = __uint_as_float(x.y << 16);
         o[3] = __uint_as_float(x.y & 0xffff0000u);
+    } else if constexpr (VEC == 2) {
+        const unsigned w = *reinterpret_cast<const unsigned *>(p);
+        o[0] = __uint_as_float(w << 16);
+        o[1] = __uint_as_float(w & 0xffff0000u);
     } else {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) o[v] = bf16_bits_to_float(p[v].bits);
@@ -311,6 +315,8 @@ __device__ __forceinline__ void store_out(float *p, const float (&x)[VEC])
         for (int q = 0; q < VEC / 4; ++q)
             __stcs(reinterpret_cast<float4 *>(p + 4 * q),
                    make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]));
+    } else if constexpr (MG_STREAM_OUT != 0 && VEC == 2) {
+        __stcs(reinterpret_cast<float2 *>(p), make_float2(x[0], x[1]));
     } else if constexpr (MG_STREAM_OUT != 0) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) __stcs(p + v, x[v]);

@@ -17,41 +17,6 @@ struct Tile {
     int64_t width;    // channels of a group
 };
 
-// ------------------------------------------------------- pairs of floats
-// Two float32 in one 64-bit register pair: one instruction multiplies and
-// adds both.
-using pair_t = unsigned long long;
-
-__device__ __forceinline__ pair_t pack2(float a, float b)
-{
-    pair_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(pair_t p, float &a, float &b)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
-}
-__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c)
-{
-    pair_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b)
-{
-    pair_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-__device__ __forceinline__ pair_t add2(pair_t a, pair_t b)
-{
-    pair_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 // softplus of two values, from e = e^-|v| (as softplus_f).
 __device__ __forceinline__ pair_t softplus2(pair_t v, float &e0, float &e1)
 {
@@ -234,15 +199,6 @@ inline Chunks cut_time(int64_t blocks, int64_t T, const RowTime &r)
         }
     }
     return best;
-}
-
-// Dynamic shared memory beyond the default 48 KB.
-template <typename K>
-mg_status allow_shared(K kernel, size_t bytes)
-{
-    if (bytes <= 48 * 1024) return MG_OK;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-    return e == cudaSuccess ? MG_OK : fail(MG_ERR_LAUNCH, "selective scan: %s", cudaGetErrorString(e));
 }
 
 // Packed batches: checks cu_seqlens, and gives empty sequences the state that

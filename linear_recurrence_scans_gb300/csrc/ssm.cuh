@@ -109,6 +109,15 @@ inline mg_status launched(const char *what)
     return e == cudaSuccess ? MG_OK : fail(MG_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Dynamic shared memory beyond the default 48 KB.
+template <typename K>
+mg_status allow_shared(K kernel, size_t bytes)
+{
+    if (bytes <= 48 * 1024) return MG_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    return e == cudaSuccess ? MG_OK : fail(MG_ERR_LAUNCH, "shared memory: %s", cudaGetErrorString(e));
+}
+
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ---------------------------------------------------------- device side
@@ -173,6 +182,134 @@ __device__ __forceinline__ float sigmoid_f(float v)
 {
     const float e = exp_neg(-fabsf(v));
     return (v >= 0.f ? 1.f : e) * rcp_fast(1.f + e);
+}
+
+// ------------------------------------------------------- pairs of floats
+// Two float32 in one 64-bit register pair: one instruction multiplies and
+// adds both.
+using pair_t = unsigned long long;
+
+__device__ __forceinline__ pair_t pack2(float a, float b)
+{
+    pair_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(pair_t p, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p));
+}
+__device__ __forceinline__ pair_t fma2(pair_t a, pair_t b, pair_t c)
+{
+    pair_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ pair_t mul2(pair_t a, pair_t b)
+{
+    pair_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ pair_t add2(pair_t a, pair_t b)
+{
+    pair_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// VEC neighbouring channels as pairs (or one float), and arithmetic on them.
+template <int VEC>
+struct Lanes {
+    pair_t p[VEC / 2];
+};
+template <>
+struct Lanes<1> {
+    float p[1];
+};
+__device__ __forceinline__ pair_t op_fma(pair_t a, pair_t b, pair_t c) { return fma2(a, b, c); }
+__device__ __forceinline__ pair_t op_mul(pair_t a, pair_t b) { return mul2(a, b); }
+__device__ __forceinline__ pair_t op_add(pair_t a, pair_t b) { return add2(a, b); }
+__device__ __forceinline__ float op_fma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float op_mul(float a, float b) { return a * b; }
+__device__ __forceinline__ float op_add(float a, float b) { return a + b; }
+#define MG_LANES_EACH for (int i_ = 0; i_ < int(sizeof(Lanes<VEC>::p) / sizeof(Lanes<VEC>::p[0])); ++i_)
+template <int VEC>
+__device__ __forceinline__ Lanes<VEC> vfma(const Lanes<VEC> &a, const Lanes<VEC> &b, const Lanes<VEC> &c)
+{
+    Lanes<VEC> r;
+#pragma unroll
+    MG_LANES_EACH r.p[i_] = op_fma(a.p[i_], b.p[i_], c.p[i_]);
+    return r;
+}
+template <int VEC>
+__device__ __forceinline__ Lanes<VEC> vmul(const Lanes<VEC> &a, const Lanes<VEC> &b)
+{
+    Lanes<VEC> r;
+#pragma unroll
+    MG_LANES_EACH r.p[i_] = op_mul(a.p[i_], b.p[i_]);
+    return r;
+}
+template <int VEC>
+__device__ __forceinline__ Lanes<VEC> vadd(const Lanes<VEC> &a, const Lanes<VEC> &b)
+{
+    Lanes<VEC> r;
+#pragma unroll
+    MG_LANES_EACH r.p[i_] = op_add(a.p[i_], b.p[i_]);
+    return r;
+}
+template <int VEC>
+__device__ __forceinline__ Lanes<VEC> vfrom(const float (&f)[VEC])
+{
+    Lanes<VEC> r;
+    if constexpr (VEC == 1) {
+        r.p[0] = f[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) r.p[i] = pack2(f[2 * i], f[2 * i + 1]);
+    }
+    return r;
+}
+template <int VEC>
+__device__ __forceinline__ void vto(const Lanes<VEC> &a, float (&f)[VEC])
+{
+    if constexpr (VEC == 1) {
+        f[0] = a.p[0];
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) unpack2(a.p[i], f[2 * i], f[2 * i + 1]);
+    }
+}
+template <int VEC>
+__device__ __forceinline__ Lanes<VEC> vset(float c)
+{
+    float f[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = c;
+    return vfrom<VEC>(f);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Lanes<VEC> vraw(const Raw<T, VEC> &x)
+{
+    float f[VEC];
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = x[i];
+    return vfrom<VEC>(f);
+}
+// sigmoid as 1 / (1 + 2^(-v log2 e)): for v far below 0 the power is infinite
+// and the quotient 0.
+template <int VEC>
+__device__ __forceinline__ Lanes<VEC> vsigmoid(const Lanes<VEC> &v)
+{
+    float f[VEC];
+    vto<VEC>(vmul<VEC>(v, vset<VEC>(-kLog2eF)), f);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = ex2_ftz(f[i]);
+    vto<VEC>(vadd<VEC>(vfrom<VEC>(f), vset<VEC>(1.f)), f);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) f[i] = rcp_fast(f[i]);
+    return vfrom<VEC>(f);
 }
 
 // The sequences of the flattened rows 0 .. B*T-1 of a batch: offsets from
