@@ -479,22 +479,37 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvStepArgs p)
     for (int j = 0; j < W - 1; ++j) store_vec<VEC>(st + j * D, win[j + 1]);
 }
 
-// out[i] = sum_j part[j * stride + i]: 8 threads take every 8th part of a
-// column, and their sums are added in order.
-__global__ void __launch_bounds__(256) sum_parts_kernel(const float *part, int64_t parts,
-                                                        int64_t stride, int64_t n, float *out)
+// Sums columns of part (see launch_sum_parts): 8 threads take every 8th part
+// of a column, four at a time, and their sums are added in order.
+struct SumOuts {
+    SumOut o[3];
+};
+__global__ void __launch_bounds__(256) sum_parts_kernel(const float *part, int64_t parts, int64_t stride,
+                                                        SumOuts outs)
 {
     __shared__ float s[8][33];
     const int64_t i = int64_t(blockIdx.x) * 32 + threadIdx.x;
     float a = 0.f;
-    if (i < n)
-        for (int64_t j = threadIdx.y; j < parts; j += 8) a += part[j * stride + i];
+    if (i < stride) {
+        const float *c = part + i;
+        int64_t j = threadIdx.y;
+        for (; j + 24 < parts; j += 32) {
+            const float v0 = c[j * stride], v1 = c[(j + 8) * stride], v2 = c[(j + 16) * stride], v3 = c[(j + 24) * stride];
+            a += (v0 + v1) + (v2 + v3);
+        }
+        for (; j < parts; j += 8) a += c[j * stride];
+    }
     s[threadIdx.y][threadIdx.x] = a;
     __syncthreads();
-    if (threadIdx.y == 0 && i < n) {
+    if (threadIdx.y == 0 && i < stride) {
         float t = 0.f;
         for (int k = 0; k < 8; ++k) t += s[k][threadIdx.x];
-        out[i] = t;
+        int64_t at = i;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            if (at >= 0 && at < outs.o[k].n && outs.o[k].out != nullptr) outs.o[k].out[at] = t;
+            at -= outs.o[k].n;
+        }
     }
 }
 
@@ -552,11 +567,7 @@ mg_status conv_bwd(const ConvArgs &p, cudaStream_t s)
     conv_bwd_kernel<T, VEC, W><<<unsigned(c.chan_blocks * c.row_blocks), c.block, smem, s>>>(
         p, q, c.chan_blocks, c.run, part);
     MG_TRY(launched("mg_causal_conv_bwd"));
-    const int64_t n = p.D * (W + 1);
-    MG_TRY(launch_sum_parts(part, c.row_blocks, n, p.D * W, p.dw, s));
-    if (p.dbias != nullptr)
-        return launch_sum_parts(part + p.D * W, c.row_blocks, n, p.D, p.dbias, s);
-    return MG_OK;
+    return launch_sum_parts(part, c.row_blocks, {{p.dw, p.D * W}, {p.dbias, p.D}}, s);
 }
 
 template <typename T, int VEC, int W>
@@ -624,10 +635,16 @@ mg_status launch_conv_step(const ConvStepArgs &p, mg_dtype dt, cudaStream_t s)
     MG_CONV_W(conv_step, bf16_t, 1, p, s);
 }
 
-mg_status launch_sum_parts(const float *part, int64_t parts, int64_t stride, int64_t n, float *out,
-                           cudaStream_t s)
+mg_status launch_sum_parts(const float *part, int64_t parts, std::initializer_list<SumOut> outs, cudaStream_t s)
 {
-    sum_parts_kernel<<<unsigned(ceil_div(n, 32)), dim3(32, 8), 0, s>>>(part, parts, stride, n, out);
+    SumOuts o{};
+    int64_t stride = 0;
+    int k = 0;
+    for (const SumOut &x : outs) {
+        o.o[k++] = x;
+        stride += x.n;
+    }
+    sum_parts_kernel<<<unsigned(ceil_div(stride, 32)), dim3(32, 8), 0, s>>>(part, parts, stride, o);
     return launched("sum over parts");
 }
 

@@ -276,9 +276,9 @@ __device__ __forceinline__ void store_vec(float *p, const float (&x)[VEC])
 // Store VEC consecutive values at p rounded to bf16 (round to nearest even).
 __device__ __forceinline__ unsigned pack_bf16x2(float lo, float hi)
 {
-    const unsigned l = __bfloat16_as_ushort(__float2bfloat16_rn(lo));
-    const unsigned h = __bfloat16_as_ushort(__float2bfloat16_rn(hi));
-    return l | (h << 16);
+    unsigned r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
 }
 
 template <int VEC>

@@ -6,7 +6,11 @@
 // group in registers: NV vectors of VEC channels a thread, read once.  The
 // mean is taken first and the variance from the differences, both in
 // registers, so there is no second pass over memory and no cancellation of
-// E[p^2] against E[p]^2.  Memory bounds the kernels.
+// E[p^2] against E[p]^2.
+//
+// A team keeps its group and walks over rows: its weights stay in registers,
+// and its next rows arrive by asynchronous copies into each thread's own slots
+// of shared memory, kAhead rows ahead.  Memory bounds the kernels.
 #include "ssm.cuh"
 
 namespace mg {
@@ -14,211 +18,358 @@ namespace {
 
 constexpr int kMaxTeam = 1024;
 
+constexpr int kAhead = 3;   // rows in flight for a thread
+
 // Sum of v over each team; every thread of the team gets it.  buf: one float
-// for each warp of the block.  All threads of the block call it.
+// for each warp of the block, and not the one of the call before (whose
+// readers this call's barrier waits for).  All threads of the block call it.
 __device__ __forceinline__ float team_sum(float v, int tpg, float *buf)
 {
-    const int in_warp = tpg < 32 ? tpg : 32;
-    for (int o = in_warp / 2; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float w = __shfl_xor_sync(~0u, v, o);
+        if (o < tpg) v += w;
+    }
     if (tpg <= 32) return v;
     const int warp = threadIdx.x >> 5, per = tpg >> 5, first = warp / per * per;
     if ((threadIdx.x & 31) == 0) buf[warp] = v;
     __syncthreads();
     v = 0.f;
     for (int i = 0; i < per; ++i) v += buf[first + i];
-    __syncthreads();
     return v;
 }
 
-__device__ __forceinline__ float act(float v, int silu) { return silu ? v * sigmoid_f(v) : v; }
-// d act / dv
-__device__ __forceinline__ float act_grad(float v, int silu)
+// The sum of a's values, and of a's values times b's.
+template <int VEC>
+__device__ __forceinline__ float vsum(const Lanes<VEC> &a)
 {
-    if (!silu) return 1.f;
-    const float s = sigmoid_f(v);
-    return s * fmaf(v, 1.f - s, 1.f);
+    if constexpr (VEC == 1) {
+        return a.p[0];
+    } else {
+        pair_t t = a.p[0];
+#pragma unroll
+        for (int i = 1; i < VEC / 2; ++i) t = add2(t, a.p[i]);
+        float x, y;
+        unpack2(t, x, y);
+        return x + y;
+    }
+}
+template <int VEC>
+__device__ __forceinline__ float vdot(const Lanes<VEC> &a, const Lanes<VEC> &b)
+{
+    if constexpr (VEC == 1) {
+        return a.p[0] * b.p[0];
+    } else {
+        pair_t t = mul2(a.p[0], b.p[0]);
+#pragma unroll
+        for (int i = 1; i < VEC / 2; ++i) t = fma2(a.p[i], b.p[i], t);
+        float x, y;
+        unpack2(t, x, y);
+        return x + y;
+    }
 }
 
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(NV == 16 ? kMaxTeam : 512)
-norm_fwd_kernel(NormArgs p, int tpg, int64_t units)
+// act(v) and, if grad, its derivative; sigmoid s: v s and s (1 + v (1 - s)).
+template <int VEC>
+__device__ __forceinline__ Lanes<VEC> vact(const Lanes<VEC> &v, int silu)
 {
-    __shared__ float buf[32];
-    const int teams = blockDim.x / tpg, lane = threadIdx.x & (tpg - 1);
-    const int64_t u = int64_t(blockIdx.x) * teams + threadIdx.x / tpg;
-    const bool live = u < units;
-    const int64_t row = live ? u / p.G : 0, g = live ? u - row * p.G : 0, gs = p.D / p.G;
-    const int64_t d0 = g * gs;
-    const T *x = static_cast<const T *>(p.x) + row * p.ldx + d0;
-    const T *z = p.gate != MG_GATE_NONE ? static_cast<const T *>(p.z) + row * p.ldz + d0 : nullptr;
-    Raw<T, VEC> xr[NV], zr[NV];
+    return silu ? vmul<VEC>(v, vsigmoid<VEC>(v)) : v;
+}
+template <int VEC>
+__device__ __forceinline__ Lanes<VEC> vact(const Lanes<VEC> &v, int silu, Lanes<VEC> &grad)
+{
+    const Lanes<VEC> one = vset<VEC>(1.f);
+    if (!silu) {
+        grad = one;
+        return v;
+    }
+    const Lanes<VEC> s = vsigmoid<VEC>(v);
+    grad = vmul<VEC>(s, vfma<VEC>(v, vfma<VEC>(s, vset<VEC>(-1.f), one), one));
+    return vmul<VEC>(v, s);
+}
+
+// A thread's vectors of the rows to come, K tensors of them: slots of shared
+// memory that only the thread's own copies fill.  Rows of 2-byte vectors,
+// which no asynchronous copy moves, are loaded when they are needed.
+template <typename T, int VEC, int NV, int K>
+struct Ahead {
+    static constexpr int kBytes = int(sizeof(T)) * VEC;
+    static constexpr bool kAsync = kBytes >= 4 && NV <= 2;
+    static size_t bytes(int threads) { return kAsync ? size_t(kAhead) * K * NV * threads * kBytes : 0; }
+    unsigned char *mine;
+    __device__ __forceinline__ T *at(int slot, int k, int i) const
+    {
+        return reinterpret_cast<T *>(mine + size_t((slot * K + k) * NV + i) * blockDim.x * kBytes);
+    }
+    __device__ __forceinline__ void fetch(int slot, int k, int i, const T *from) const
+    {
+        if constexpr (kAsync && kBytes == 16)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" : : "r"(smem_addr(at(slot, k, i))), "l"(from)
+                         : "memory");
+        else if constexpr (kAsync)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" : : "r"(smem_addr(at(slot, k, i))), "l"(from),
+                         "n"(kBytes) : "memory");
+    }
+    __device__ __forceinline__ Lanes<VEC> get(int slot, int k, int i, const T *from) const
+    {
+        float o[VEC];
+        load_vec<VEC>(kAsync ? at(slot, k, i) : from, o);
+        return vfrom<VEC>(o);
+    }
+};
+
+// The team's place: its group, its first row, and its thread's channels.
+struct Team {
+    int lane, g, slot;
+    int64_t d0;
+    bool live;
+    __device__ __forceinline__ Team(const NormArgs &p, int tpg, int row_teams)
+    {
+        const unsigned t = blockIdx.x * (blockDim.x / tpg) + threadIdx.x / tpg, G = unsigned(p.G);
+        lane = threadIdx.x & (tpg - 1);
+        g = int(t % G);
+        slot = int(t / G);
+        d0 = int64_t(g) * (p.D / p.G);
+        live = slot < row_teams;
+    }
+};
+
+template <typename T, int VEC, int NV, mg_gate GATE>
+__global__ void __launch_bounds__(NV == 16 ? kMaxTeam : 512, NV == 1 ? 2 : 1)
+norm_fwd_kernel(NormArgs p, int tpg, int row_teams)
+{
+    constexpr int K = GATE == MG_GATE_NONE ? 1 : 2;
+    __shared__ float buf[2][32];
+    extern __shared__ __align__(16) unsigned char ring[];
+    const Team team(p, tpg, row_teams);
+    const int gs = int(p.D / p.G);
+    const Ahead<T, VEC, NV, K> ahead{ring + threadIdx.x * Ahead<T, VEC, NV, K>::kBytes};
+    const T *x = static_cast<const T *>(p.x) + int64_t(team.slot) * p.ldx + team.d0;
+    const T *z = static_cast<const T *>(p.z) + int64_t(team.slot) * p.ldz + team.d0;
+    T *y = static_cast<T *>(p.y) + int64_t(team.slot) * p.D + team.d0;
+    Lanes<VEC> w[NV], b[NV];
+    int c[NV];
     bool in[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int64_t c = (int64_t(i) * tpg + lane) * VEC;
-        in[i] = live && c < gs;
+        c[i] = (i * tpg + team.lane) * VEC;
+        in[i] = team.live && c[i] < gs;
+        w[i] = b[i] = vset<VEC>(0.f);
         if (in[i]) {
-            xr[i].load(x + c);
-            if (z != nullptr) zr[i].load(z + c);
+            float f[VEC];
+            load_vec<VEC>(p.w + team.d0 + c[i], f);
+            w[i] = vfrom<VEC>(f);
+            if (p.bias != nullptr) {
+                load_vec<VEC>(p.bias + team.d0 + c[i], f);
+                b[i] = vfrom<VEC>(f);
+            }
         }
     }
+    const int64_t xs = row_teams * p.ldx, zs = row_teams * p.ldz, ys = row_teams * p.D;
+    const T *xn = x, *zn = z;   // of the next row to be fetched
+    const int M = int(p.M);   // M G < 2^31
+    int64_t row_next = team.slot;
+    auto fetch = [&](int slot) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in[i] && row_next < M) {
+                ahead.fetch(slot, 0, i, xn + c[i]);
+                if (K == 2) ahead.fetch(slot, 1, i, zn + c[i]);
+            }
+        xn += xs;
+        zn += zs;
+        row_next += row_teams;
+        cp_async_commit();
+    };
     const float inv = 1.f / float(gs);
-    float f[NV][VEC], sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (in[i]) {
+    for (int k = 0; k < kAhead - 1; ++k) fetch(k);
+    const int rounds = (M - 1) / row_teams + 1;   // the same for every team
+    int slot = 0;
+    int64_t row = team.slot;
+    for (int k = 0; k < rounds; ++k, row += row_teams) {
+        fetch(slot == 0 ? kAhead - 1 : slot - 1);
+        cp_async_wait<kAhead - 1>();
+        const bool live = row < M;
+        Lanes<VEC> f[NV], gate[NV];
+        float sum = 0.f;
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                f[i][v] = p.gate == MG_GATE_FIRST ? xr[i][v] * act(zr[i][v], p.silu) : xr[i][v];
-                sum += f[i][v];
+        for (int i = 0; i < NV; ++i) {
+            f[i] = vset<VEC>(0.f);
+            if (in[i] && live) {
+                f[i] = ahead.get(slot, 0, i, x + c[i]);
+                if (K == 2) gate[i] = vact<VEC>(ahead.get(slot, 1, i, z + c[i]), p.silu);
+                if (GATE == MG_GATE_FIRST) f[i] = vmul<VEC>(f[i], gate[i]);
+                sum += vsum<VEC>(f[i]);
             }
         }
-    float mean = 0.f;
-    if (!p.rms) mean = team_sum(sum, tpg, buf) * inv;
-    float sq = 0.f;
+        float mean = 0.f;
+        if (!p.rms) mean = team_sum(sum, tpg, buf[0]) * inv;
+        float sq = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (in[i]) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                const float e = f[i][v] - mean;
-                sq = fmaf(e, e, sq);
+        for (int i = 0; i < NV; ++i)
+            if (in[i] && live) {
+                f[i] = vadd<VEC>(f[i], vset<VEC>(-mean));
+                sq += vdot<VEC>(f[i], f[i]);
             }
+        // (one sum a row: the buffers take turns)
+        const float rstd = rsqrtf(fmaf(team_sum(sq, tpg, buf[p.rms ? k & 1 : 1]), inv, p.eps));
+        if (live && team.live) {
+            if (team.lane == 0 && p.stats != nullptr) {
+                const int64_t u = row * p.G + team.g;
+                *reinterpret_cast<float2 *>(p.stats + 2 * u) = make_float2(mean, rstd);
+            }
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (in[i]) {
+                    Lanes<VEC> o = vfma<VEC>(vmul<VEC>(f[i], vset<VEC>(rstd)), w[i], b[i]);
+                    if (GATE == MG_GATE_AFTER) o = vmul<VEC>(o, gate[i]);
+                    if (GATE == MG_GATE_NONE) o = vact<VEC>(o, p.silu);
+                    float v[VEC];
+                    vto<VEC>(o, v);
+                    store_out<VEC>(y + c[i], v);
+                }
         }
-    const float rstd = rsqrtf(fmaf(team_sum(sq, tpg, buf), inv, p.eps));
-    if (!live) return;
-    if (lane == 0 && p.stats != nullptr) {
-        p.stats[2 * u] = mean;
-        p.stats[2 * u + 1] = rstd;
+        x += xs;
+        z += zs;
+        y += ys;
+        slot = slot + 1 == kAhead ? 0 : slot + 1;
     }
-    T *y = static_cast<T *>(p.y) + row * p.D + d0;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-        if (in[i]) {
-            const int64_t c = (int64_t(i) * tpg + lane) * VEC;
-            float w[VEC], b[VEC], o[VEC];
-            load_vec<VEC>(p.w + d0 + c, w);
-            if (p.bias != nullptr) load_vec<VEC>(p.bias + d0 + c, b);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                o[v] = (f[i][v] - mean) * rstd * w[v];
-                if (p.bias != nullptr) o[v] += b[v];
-                if (p.gate == MG_GATE_AFTER) o[v] *= act(zr[i][v], p.silu);
-                if (p.gate == MG_GATE_NONE) o[v] = act(o[v], p.silu);
-            }
-            store_out<VEC>(y + c, o);
-        }
+    cp_async_wait<0>();
 }
 
 // Gradients.  With n = (p - mean) rstd and dn = do w, over a group
 //   dp = rstd (dn - mean(dn) - n mean(dn n))    (rms: without mean(dn))
-// and the gate's chain rule around it.  A team keeps its group and walks over
-// rows, so that a thread's channels stay the same and dw, dbias are summed in
-// registers; the teams' sums are added in order by sum_parts_kernel.
+// and the gate's chain rule around it.  dw and dbias are summed over a team's
+// rows in registers; the teams' sums are added in order by sum_parts_kernel.
 template <typename T, int VEC, int NV, mg_gate GATE>
 __global__ void __launch_bounds__(NV == 16 ? kMaxTeam : 512)
-norm_bwd_kernel(NormArgs p, int tpg, int64_t row_teams, float *part)
+norm_bwd_kernel(NormArgs p, int tpg, int row_teams, float *part)
 {
-    __shared__ float buf[32];
-    const int teams = blockDim.x / tpg, lane = threadIdx.x & (tpg - 1);
-    const int64_t t = int64_t(blockIdx.x) * teams + threadIdx.x / tpg;
-    const int64_t g = t % p.G, slot = t / p.G, gs = p.D / p.G, d0 = g * gs;
-    float dw[NV][VEC] = {}, db[NV][VEC] = {}, w[NV][VEC], b[NV][VEC];
+    constexpr int K = GATE == MG_GATE_NONE ? 2 : 3;
+    __shared__ float buf[2][32];
+    extern __shared__ __align__(16) unsigned char ring[];
+    const Team team(p, tpg, row_teams);
+    const int gs = int(p.D / p.G);
+    const Ahead<T, VEC, NV, K> ahead{ring + threadIdx.x * Ahead<T, VEC, NV, K>::kBytes};
+    const T *x = static_cast<const T *>(p.x) + int64_t(team.slot) * p.ldx + team.d0;
+    const T *z = static_cast<const T *>(p.z) + int64_t(team.slot) * p.ldz + team.d0;
+    const T *dy = static_cast<const T *>(p.dy) + int64_t(team.slot) * p.lddy + team.d0;
+    int64_t out = int64_t(team.slot) * p.D + team.d0;
+    Lanes<VEC> w[NV], b[NV], dw[NV], db[NV];
+    int c[NV];
     bool in[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int64_t c = (int64_t(i) * tpg + lane) * VEC;
-        in[i] = slot < row_teams && c < gs;
-#pragma unroll
-        for (int v = 0; v < VEC; ++v) w[i][v] = b[i][v] = 0.f;
+        c[i] = (i * tpg + team.lane) * VEC;
+        in[i] = team.live && c[i] < gs;
+        w[i] = b[i] = dw[i] = db[i] = vset<VEC>(0.f);
         if (in[i]) {
-            load_vec<VEC>(p.w + d0 + c, w[i]);
-            if (GATE != MG_GATE_FIRST && p.bias != nullptr) load_vec<VEC>(p.bias + d0 + c, b[i]);
+            float f[VEC];
+            load_vec<VEC>(p.w + team.d0 + c[i], f);
+            w[i] = vfrom<VEC>(f);
+            if (GATE != MG_GATE_FIRST && p.bias != nullptr) {
+                load_vec<VEC>(p.bias + team.d0 + c[i], f);
+                b[i] = vfrom<VEC>(f);
+            }
         }
     }
+    const int64_t xs = row_teams * p.ldx, zs = row_teams * p.ldz, gst = row_teams * p.lddy, os = row_teams * p.D;
+    const T *xn = x, *zn = z, *gn = dy;   // of the next row to be fetched
+    const int M = int(p.M);   // M G < 2^31
+    int64_t row_next = team.slot;
+    auto fetch = [&](int slot) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (in[i] && row_next < M) {
+                ahead.fetch(slot, 0, i, xn + c[i]);
+                ahead.fetch(slot, 1, i, gn + c[i]);
+                if (K == 3) ahead.fetch(slot, K - 1, i, zn + c[i]);
+            }
+        xn += xs;
+        zn += zs;
+        gn += gst;
+        row_next += row_teams;
+        cp_async_commit();
+    };
     const float inv = 1.f / float(gs);
-    // the same count of rounds for every team: team_sum is for whole blocks
-    const int64_t rounds = (p.M + row_teams - 1) / row_teams;
-    for (int64_t k = 0; k < rounds; ++k) {
-        const int64_t row = k * row_teams + slot;
-        const bool live = slot < row_teams && row < p.M;
-        const T *x = static_cast<const T *>(p.x) + row * p.ldx + d0;
-        const T *z = static_cast<const T *>(p.z) + row * p.ldz + d0;
-        const T *dy = static_cast<const T *>(p.dy) + row * p.lddy + d0;
-        Raw<T, VEC> xr[NV], zr[NV], yr[NV];
-        float mean = 0.f, rstd = 0.f;
-        if (live) {
-            mean = p.stats_in[2 * (row * p.G + g)];
-            rstd = p.stats_in[2 * (row * p.G + g) + 1];
-        }
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int64_t c = (int64_t(i) * tpg + lane) * VEC;
-            if (live && in[i]) {
-                xr[i].load(x + c);
-                yr[i].load(dy + c);
-                if (GATE != MG_GATE_NONE) zr[i].load(z + c);
-            }
-        }
-        float n[NV][VEC], dn[NV][VEC], m1 = 0.f, m2 = 0.f;
+    for (int k = 0; k < kAhead - 1; ++k) fetch(k);
+    const int rounds = (M - 1) / row_teams + 1;   // the same for every team
+    int slot = 0;
+    int64_t row = team.slot;
+    for (int k = 0; k < rounds; ++k, row += row_teams) {
+        fetch(slot == 0 ? kAhead - 1 : slot - 1);
+        const bool live = team.live && row < M;
+        float2 st = make_float2(0.f, 0.f);
+        if (live) st = *reinterpret_cast<const float2 *>(p.stats_in + 2 * (row * p.G + team.g));
+        cp_async_wait<kAhead - 1>();
+        const Lanes<VEC> rstd = vset<VEC>(st.y);
+        Lanes<VEC> n[NV], dn[NV], ga[NV], gg[NV];
+        float m1 = 0.f, m2 = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (live && in[i]) {
-                const int64_t c = (int64_t(i) * tpg + lane) * VEC;
-                float dz[VEC];
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const float pv = GATE == MG_GATE_FIRST ? xr[i][v] * act(zr[i][v], p.silu) : xr[i][v];
-                    n[i][v] = (pv - mean) * rstd;
-                    float dov = yr[i][v];
-                    if (GATE != MG_GATE_FIRST) {
-                        const float o = fmaf(n[i][v], w[i][v], b[i][v]);
-                        if (GATE == MG_GATE_AFTER) {
-                            dz[v] = dov * o * act_grad(zr[i][v], p.silu);
-                            dov *= act(zr[i][v], p.silu);
-                        } else {
-                            dov *= act_grad(o, p.silu);
-                        }
-                    }
-                    dw[i][v] = fmaf(dov, n[i][v], dw[i][v]);
-                    db[i][v] += dov;
-                    dn[i][v] = dov * w[i][v];
-                    m1 += dn[i][v];
-                    m2 = fmaf(dn[i][v], n[i][v], m2);
+                Lanes<VEC> pv = ahead.get(slot, 0, i, x + c[i]), dov = ahead.get(slot, 1, i, dy + c[i]);
+                if (K == 3) ga[i] = vact<VEC>(ahead.get(slot, K - 1, i, z + c[i]), p.silu, gg[i]);
+                if (GATE == MG_GATE_FIRST) {
+                    gg[i] = vmul<VEC>(gg[i], pv);
+                    pv = vmul<VEC>(pv, ga[i]);
                 }
-                if (GATE == MG_GATE_AFTER)
-                    store_out<VEC>(static_cast<T *>(p.dz) + row * p.D + d0 + c, dz);
-            }
-        m1 = p.rms ? 0.f : team_sum(m1, tpg, buf) * inv;
-        m2 = team_sum(m2, tpg, buf) * inv;
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-            if (live && in[i]) {
-                const int64_t c = (int64_t(i) * tpg + lane) * VEC;
-                float dx[VEC], dz[VEC];
-#pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    const float dp = rstd * (dn[i][v] - m1 - n[i][v] * m2);
-                    if (GATE == MG_GATE_FIRST) {
-                        dx[v] = dp * act(zr[i][v], p.silu);
-                        dz[v] = dp * xr[i][v] * act_grad(zr[i][v], p.silu);
+                // (p - mean) rstd: the difference first where the mean is not 0
+                n[i] = p.rms ? vmul<VEC>(pv, rstd) : vmul<VEC>(vadd<VEC>(pv, vset<VEC>(-st.x)), rstd);
+                if (GATE != MG_GATE_FIRST) {
+                    const Lanes<VEC> o = vfma<VEC>(n[i], w[i], b[i]);
+                    if (GATE == MG_GATE_AFTER) {
+                        float v[VEC];
+                        vto<VEC>(vmul<VEC>(vmul<VEC>(dov, o), gg[i]), v);
+                        store_out<VEC>(static_cast<T *>(p.dz) + out + c[i], v);
+                        dov = vmul<VEC>(dov, ga[i]);
                     } else {
-                        dx[v] = dp;
+                        Lanes<VEC> grad;
+                        vact<VEC>(o, p.silu, grad);
+                        dov = vmul<VEC>(dov, grad);
                     }
                 }
-                store_out<VEC>(static_cast<T *>(p.dx) + row * p.D + d0 + c, dx);
-                if (GATE == MG_GATE_FIRST)
-                    store_out<VEC>(static_cast<T *>(p.dz) + row * p.D + d0 + c, dz);
+                dw[i] = vfma<VEC>(dov, n[i], dw[i]);
+                db[i] = vadd<VEC>(db[i], dov);
+                dn[i] = vmul<VEC>(dov, w[i]);
+                m1 += vsum<VEC>(dn[i]);
+                m2 += vdot<VEC>(dn[i], n[i]);
             }
+        m1 = p.rms ? 0.f : team_sum(m1, tpg, buf[0]) * inv;
+        m2 = team_sum(m2, tpg, buf[p.rms ? k & 1 : 1]) * inv;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if (live && in[i]) {
+                Lanes<VEC> dp = vadd<VEC>(vfma<VEC>(n[i], vset<VEC>(-m2), dn[i]), vset<VEC>(-m1));
+                dp = vmul<VEC>(dp, rstd);
+                float v[VEC];
+                if (GATE == MG_GATE_FIRST) {
+                    vto<VEC>(vmul<VEC>(dp, gg[i]), v);
+                    store_out<VEC>(static_cast<T *>(p.dz) + out + c[i], v);
+                    dp = vmul<VEC>(dp, ga[i]);
+                }
+                vto<VEC>(dp, v);
+                store_out<VEC>(static_cast<T *>(p.dx) + out + c[i], v);
+            }
+        x += xs;
+        z += zs;
+        dy += gst;
+        out += os;
+        slot = slot + 1 == kAhead ? 0 : slot + 1;
     }
+    cp_async_wait<0>();
     // part: row_teams rows of dw (D) and then of dbias (D)
-    float *out = part + slot * 2 * p.D + d0;
+    float *to = part + int64_t(team.slot) * 2 * p.D + team.d0;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (in[i]) {
-            const int64_t c = (int64_t(i) * tpg + lane) * VEC;
-            store_vec<VEC>(out + c, dw[i]);
-            store_vec<VEC>(out + p.D + c, db[i]);
+            float f[VEC];
+            vto<VEC>(dw[i], f);
+            store_vec<VEC>(to + c[i], f);
+            vto<VEC>(db[i], f);
+            store_vec<VEC>(to + p.D + c[i], f);
         }
 }
 
@@ -233,12 +384,13 @@ int team_for(int64_t gs, int vec, int nv)
 
 constexpr int kNormBlock = 256;
 
-// (vector width, vectors a thread) of a call.  Vectors are 16 bytes where
-// the group's width and the rows allow, else one value.  More than one vector
-// a thread is taken only where one would need a team of more than 512
-// threads, beyond a group of 4096 bf16 channels: small teams keep more rows
-// in flight.  8 x 512 float4 and 16 x 1024 single values hold the widest
-// group, 16384 channels.
+// (vector width, vectors a thread, team) of a call.  Vectors are 16 bytes
+// where the group's width and the rows allow, else one value.  Single values
+// take the fewest a thread whose team fits a warp, whose sums need no barrier
+// (groups of 143 bf16 channels: see below), and everything else the fewest
+// whose team has at most 512 threads: one vector up to 4096 bf16 channels.
+// 8 x 512 float4 and 16 x 1024 single values hold the widest group, 16384
+// channels.
 struct Shape {
     int vec, nv, tpg;
 };
@@ -247,56 +399,70 @@ Shape shape_for(mg_dtype dt, int64_t gs, bool aligned)
     const int full = dt == MG_F32 ? 4 : 8;
     Shape c;
     c.vec = aligned && gs % full == 0 ? full : 1;
-    for (int nv : {1, 2, 4, c.vec == 1 ? 16 : 8}) {
-        c.nv = nv;
-        c.tpg = team_for(gs, c.vec, nv);
-        if (c.tpg <= 512 || (nv == 16 && c.tpg <= kMaxTeam)) return c;
-    }
+    const int most = c.vec == 1 ? 16 : 8;
+    for (int limit : {c.vec == 1 ? 32 : 512, 512, kMaxTeam})
+        for (int nv : {1, 2, 4, most}) {
+            c.nv = nv;
+            c.tpg = team_for(gs, c.vec, nv);
+            if (c.tpg <= limit && (limit <= 512 || nv == 16)) return c;
+        }
     c.tpg = 0;
     return c;
 }
 
-// Row teams of the backward: about 8 blocks of 256 threads for each SM, at
-// most one for each row.
-int64_t row_teams_for(int64_t M, int64_t G, int tpg)
+// Row teams: so many that the teams of all groups fill the SMs with `warps`
+// warps each, at most one for each row.
+int64_t row_teams_for(int64_t M, int64_t G, int tpg, int warps)
 {
     const int block = tpg > kNormBlock ? tpg : kNormBlock;
-    const int64_t all = int64_t(152) * 8 * kNormBlock / block * (block / tpg);
-    int64_t n = ceil_div(all, G);
+    const int64_t all = int64_t(152) * (warps * 32 / block > 0 ? warps * 32 / block : 1) * (block / tpg);
+    int64_t n = all / G;
     n = n < 1 ? 1 : n;
     return n < M ? n : M;
+}
+constexpr int kFwdWarps = 32, kBwdWarps = 16;   // what an SM holds by the kernels' registers
+
+template <typename T, int VEC, int NV, mg_gate GATE>
+mg_status norm_fwd_gate(const NormArgs &p, int tpg, cudaStream_t s)
+{
+    const int block = tpg > kNormBlock ? tpg : kNormBlock;
+    const int64_t rt = row_teams_for(p.M, p.G, tpg, kFwdWarps);
+    const size_t smem = Ahead<T, VEC, NV, GATE == MG_GATE_NONE ? 1 : 2>::bytes(block);
+    MG_TRY(allow_shared(norm_fwd_kernel<T, VEC, NV, GATE>, smem));
+    norm_fwd_kernel<T, VEC, NV, GATE><<<unsigned(ceil_div(rt * p.G, block / tpg)), block, smem, s>>>(p, tpg, int(rt));
+    return launched("mg_group_norm_fwd");
+}
+
+template <typename T, int VEC, int NV, mg_gate GATE>
+mg_status norm_bwd_gate(const NormArgs &p, int tpg, cudaStream_t s)
+{
+    const int block = tpg > kNormBlock ? tpg : kNormBlock;
+    const int64_t rt = row_teams_for(p.M, p.G, tpg, kBwdWarps);
+    float *part = reinterpret_cast<float *>(static_cast<char *>(p.ws) + kControlBytes);
+    const size_t smem = Ahead<T, VEC, NV, GATE == MG_GATE_NONE ? 2 : 3>::bytes(block);
+    MG_TRY(allow_shared(norm_bwd_kernel<T, VEC, NV, GATE>, smem));
+    norm_bwd_kernel<T, VEC, NV, GATE><<<unsigned(ceil_div(rt * p.G, block / tpg)), block, smem, s>>>(p, tpg, int(rt), part);
+    MG_TRY(launched("mg_group_norm_bwd"));
+    return launch_sum_parts(part, rt, {{p.dw, p.D}, {p.dbias, p.D}}, s);
 }
 
 template <typename T, int VEC, int NV>
 mg_status norm_fwd(const NormArgs &p, int tpg, cudaStream_t s)
 {
-    const int block = tpg > kNormBlock ? tpg : kNormBlock;
-    const int64_t units = p.M * p.G;
-    norm_fwd_kernel<T, VEC, NV><<<unsigned(ceil_div(units, block / tpg)), block, 0, s>>>(p, tpg, units);
-    return launched("mg_group_norm_fwd");
+    switch (p.gate) {
+    case MG_GATE_NONE: return norm_fwd_gate<T, VEC, NV, MG_GATE_NONE>(p, tpg, s);
+    case MG_GATE_AFTER: return norm_fwd_gate<T, VEC, NV, MG_GATE_AFTER>(p, tpg, s);
+    default: return norm_fwd_gate<T, VEC, NV, MG_GATE_FIRST>(p, tpg, s);
+    }
 }
-
 template <typename T, int VEC, int NV>
 mg_status norm_bwd(const NormArgs &p, int tpg, cudaStream_t s)
 {
-    const int block = tpg > kNormBlock ? tpg : kNormBlock;
-    const int64_t rt = row_teams_for(p.M, p.G, tpg);
-    const unsigned grid = unsigned(ceil_div(rt * p.G, block / tpg));
-    float *part = reinterpret_cast<float *>(static_cast<char *>(p.ws) + kControlBytes);
     switch (p.gate) {
-    case MG_GATE_NONE:
-        norm_bwd_kernel<T, VEC, NV, MG_GATE_NONE><<<grid, block, 0, s>>>(p, tpg, rt, part);
-        break;
-    case MG_GATE_AFTER:
-        norm_bwd_kernel<T, VEC, NV, MG_GATE_AFTER><<<grid, block, 0, s>>>(p, tpg, rt, part);
-        break;
-    default:
-        norm_bwd_kernel<T, VEC, NV, MG_GATE_FIRST><<<grid, block, 0, s>>>(p, tpg, rt, part);
+    case MG_GATE_NONE: return norm_bwd_gate<T, VEC, NV, MG_GATE_NONE>(p, tpg, s);
+    case MG_GATE_AFTER: return norm_bwd_gate<T, VEC, NV, MG_GATE_AFTER>(p, tpg, s);
+    default: return norm_bwd_gate<T, VEC, NV, MG_GATE_FIRST>(p, tpg, s);
     }
-    MG_TRY(launched("mg_group_norm_bwd"));
-    MG_TRY(launch_sum_parts(part, rt, 2 * p.D, p.D, p.dw, s));
-    if (p.dbias != nullptr) return launch_sum_parts(part + p.D, rt, 2 * p.D, p.D, p.dbias, s);
-    return MG_OK;
 }
 
 // Calls F<T, VEC, NV> for the call's shape.
@@ -340,7 +506,7 @@ size_t norm_ws_bytes(int64_t M, int64_t D, int64_t G)
         for (bool al : {false, true}) {
             const Shape c = shape_for(dt, D / G, al);
             if (c.tpg == 0) continue;
-            const size_t n = size_t(row_teams_for(M, G, c.tpg)) * 2 * D * sizeof(float);
+            const size_t n = size_t(row_teams_for(M, G, c.tpg, kBwdWarps)) * 2 * D * sizeof(float);
             need = n > need ? n : need;
         }
     return kControlBytes + need;

@@ -177,7 +177,7 @@ struct alignas(16) BwdShared {
 template <typename T, int VEC, typename CV>
 __global__ void __launch_bounds__(CV::THREADS, 2)
 ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const float *agg_s,
-               float *partB, float *partA, float *partD, int bc_wide)
+               float *partB, float *partA, int bc_wide)
 {
     constexpr int S = CV::S, L = CV::L, NP = CV::NP, CH = CV::kCh, WCH = CV::kWarpCh, kWarps = CV::THREADS / 32;
     constexpr int kCols = WCH / VEC, kVecs = kTile * kCols, kPer = (kVecs + 31) / 32;
@@ -545,13 +545,25 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
             }
         }
     }
-    const int64_t part = w.b * ck.n + w.k;
-    store_block<S>(partA + part * p.D * p.N, dw + ch, ch, wide, n0, p.N, dA);
+    // a part is dA, then dDskip and ddt_bias
+    float *part = partA + (w.b * ck.n + w.k) * p.D * (p.N + 2);
+    if (p.N % 4 == 0 && p.D % 2 == 0) {
+        store_block<S>(part, dw + ch, ch, wide, n0, p.N, dA);
+    } else {   // parts that are not 16-byte aligned
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                float a, b;
+                unpack2(dA[i][c / 2], a, b);
+                if (ch + c < wide && n0 + i < p.N) part[(dw + ch + c) * p.N + n0 + i] = c % 2 ? b : a;
+            }
+    }
 #pragma unroll
     for (int o = 0; o < kOut; ++o)
         if (writes && oc + o < wide) {
-            partD[part * 2 * p.D + dw + oc + o] = sum_d[o];
-            partD[(part * 2 + 1) * p.D + dw + oc + o] = sum_b[o];
+            part[p.D * p.N + dw + oc + o] = sum_d[o];
+            part[p.D * (p.N + 1) + dw + oc + o] = sum_b[o];
         }
 }
 
@@ -598,8 +610,7 @@ mg_status bwd(const SsmArgs &p, cudaStream_t s)
     const int64_t rows_g = q.rows * p.G, dn = p.D * p.N, parts = p.B * ck.n;
     float *partB = reinterpret_cast<float *>(static_cast<char *>(p.ws) + kControlBytes);
     float *partA = partB + t.tiles * rows_g * 2 * p.N;
-    float *partD = partA + parts * dn;
-    float *agg_q = partD + parts * 2 * p.D;
+    float *agg_q = partA + ceil_div(parts * p.D * (p.N + 2), 4) * 4;
     float *agg_s = agg_q + p.B * (ck.n - 1) * dn;
     const int64_t tiles = t.tiles * p.G * p.B;
     // 16-byte vectors of B and C
@@ -615,16 +626,12 @@ mg_status bwd(const SsmArgs &p, cudaStream_t s)
     static_assert(smem <= 227 * 1024, "shared memory of a block");
     MG_TRY(allow_shared(ssm_bwd_kernel<T, VEC, CV>, smem));
     ssm_bwd_kernel<T, VEC, CV><<<unsigned(tiles * ck.n), CV::THREADS, smem, s>>>(p, q, t, ck, agg_q, agg_s, partB,
-                                                                             partA, partD, bc_wide);
+                                                                             partA, bc_wide);
     MG_TRY(launched("mg_selective_scan_bwd"));
     sum_bc_kernel<T><<<unsigned(ceil_div(rows_g * 2 * p.N, 256)), 256, 0, s>>>(
         partB, t.tiles, rows_g, p.N, static_cast<T *>(p.dBm), static_cast<T *>(p.dCm));
     MG_TRY(launched("mg_selective_scan_bwd"));
-    MG_TRY(launch_sum_parts(partA, parts, dn, dn, p.dA, s));
-    if (p.dDskip != nullptr) MG_TRY(launch_sum_parts(partD, parts, 2 * p.D, p.D, p.dDskip, s));
-    if (p.ddt_bias != nullptr)
-        MG_TRY(launch_sum_parts(partD + p.D, parts, 2 * p.D, p.D, p.ddt_bias, s));
-    return MG_OK;
+    return launch_sum_parts(partA, parts, {{p.dA, dn}, {p.dDskip, p.D}, {p.ddt_bias, p.D}}, s);
 }
 
 template <typename T, int VEC>

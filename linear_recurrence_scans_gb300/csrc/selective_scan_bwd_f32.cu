@@ -7,7 +7,7 @@ size_t ssm_bwd_ws_bytes(int64_t B, int64_t T, int64_t D, int N, int G, int64_t)
 {
     const Chunks ck = backward_chunks(B, T, D, N, G);
     return kControlBytes +
-           sizeof(float) * (backward_tiles(D, N, G) * B * T * G * 2 * N + B * ck.n * (D * N + 2 * D) +
+           sizeof(float) * (backward_tiles(D, N, G) * B * T * G * 2 * N + B * ck.n * D * (N + 2) + 4 +
                             B * (ck.n - 1) * (D * N + D));
 }
 

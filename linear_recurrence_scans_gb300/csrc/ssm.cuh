@@ -98,10 +98,14 @@ size_t norm_ws_bytes(int64_t M, int64_t D, int64_t G);
 mg_status launch_norm_fwd(const NormArgs &p, mg_dtype dt, cudaStream_t s);
 mg_status launch_norm_bwd(const NormArgs &p, mg_dtype dt, cudaStream_t s);
 
-// out[i] = sum_j part[j * stride + i], i < n, j in order: the last step of the
-// sums over rows, in a fixed order.
-mg_status launch_sum_parts(const float *part, int64_t parts, int64_t stride, int64_t n, float *out,
-                           cudaStream_t s);
+// The last step of the sums over rows: each of `parts` rows of part holds the
+// outputs' values one after another; out[i] = the sum of its column, in a fixed
+// order, in one launch.  An output that is NULL is left out.
+struct SumOut {
+    float *out;
+    int64_t n;
+};
+mg_status launch_sum_parts(const float *part, int64_t parts, std::initializer_list<SumOut> outs, cudaStream_t s);
 
 inline mg_status launched(const char *what)
 {
@@ -113,7 +117,7 @@ inline mg_status launched(const char *what)
 template <typename K>
 mg_status allow_shared(K kernel, size_t bytes)
 {
-    if (bytes <= 48 * 1024) return MG_OK;
+    if (bytes <= 40 * 1024) return MG_OK;   // the default 48 KB count static shared memory too
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
     return e == cudaSuccess ? MG_OK : fail(MG_ERR_LAUNCH, "shared memory: %s", cudaGetErrorString(e));
 }
