@@ -201,6 +201,24 @@ mg_status mg_group_norm_bwd(const void *dy, int64_t lddy, const float *stats, co
                             int64_t M, int64_t D, int64_t G,
                             void *ws, size_t ws_bytes, cudaStream_t stream);
 
+/*
+ * The calls above with their arguments as an array of 64-bit words, in the
+ * declared order (integers and enums sign-extended, pointers and sizes as they
+ * are, eps as the bits of a double): one argument instead of up to 36 for
+ * bindings that pay for each.  `nargs` is the array's length.
+ */
+typedef enum mg_ssm_op {
+    MG_CAUSAL_CONV_FWD = 0,
+    MG_CAUSAL_CONV_BWD = 1,
+    MG_CAUSAL_CONV_STEP = 2,
+    MG_SELECTIVE_SCAN_FWD = 3,
+    MG_SELECTIVE_SCAN_BWD = 4,
+    MG_SELECTIVE_SCAN_STEP = 5,
+    MG_GROUP_NORM_FWD = 6,
+    MG_GROUP_NORM_BWD = 7
+} mg_ssm_op;
+mg_status mg_ssm_call(mg_ssm_op op, const uint64_t *args, int nargs);
+
 #ifdef __cplusplus
 }
 #endif

@@ -63,10 +63,10 @@ inline mg_status check_ws(const char *fn, const void *ws, size_t ws_bytes, size_
     return MG_OK;
 }
 
-#define MG_TRY(expr)                      \
-    do {                                  \
-        const mg_status st__ = (expr);    \
-        if (st__ != MG_OK) return st__;   \
+#define MG_TRY(...)                           \
+    do {                                      \
+        const mg_status st__ = (__VA_ARGS__); \
+        if (st__ != MG_OK) return st__;       \
     } while (0)
 
 }  // namespace mg

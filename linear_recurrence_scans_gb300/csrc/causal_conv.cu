@@ -563,7 +563,7 @@ mg_status conv_bwd(const ConvArgs &p, cudaStream_t s)
     float *part = reinterpret_cast<float *>(static_cast<char *>(p.ws) + kControlBytes);
     constexpr size_t sums = kBlock * size_t(VEC * (W + 1)) * sizeof(float), rings = 2 * Ring<T, VEC>::bytes(kBlock);
     constexpr size_t smem = sums > rings ? sums : rings;
-    MG_TRY(allow_shared(conv_bwd_kernel<T, VEC, W>, smem));
+    MG_TRY(allow_shared<conv_bwd_kernel<T, VEC, W>>(smem));
     conv_bwd_kernel<T, VEC, W><<<unsigned(c.chan_blocks * c.row_blocks), c.block, smem, s>>>(
         p, q, c.chan_blocks, c.run, part);
     MG_TRY(launched("mg_causal_conv_bwd"));

@@ -428,7 +428,7 @@ mg_status norm_fwd_gate(const NormArgs &p, int tpg, cudaStream_t s)
     const int block = tpg > kNormBlock ? tpg : kNormBlock;
     const int64_t rt = row_teams_for(p.M, p.G, tpg, kFwdWarps);
     const size_t smem = Ahead<T, VEC, NV, GATE == MG_GATE_NONE ? 1 : 2>::bytes(block);
-    MG_TRY(allow_shared(norm_fwd_kernel<T, VEC, NV, GATE>, smem));
+    MG_TRY(allow_shared<norm_fwd_kernel<T, VEC, NV, GATE>>(smem));
     norm_fwd_kernel<T, VEC, NV, GATE><<<unsigned(ceil_div(rt * p.G, block / tpg)), block, smem, s>>>(p, tpg, int(rt));
     return launched("mg_group_norm_fwd");
 }
@@ -440,7 +440,7 @@ mg_status norm_bwd_gate(const NormArgs &p, int tpg, cudaStream_t s)
     const int64_t rt = row_teams_for(p.M, p.G, tpg, kBwdWarps);
     float *part = reinterpret_cast<float *>(static_cast<char *>(p.ws) + kControlBytes);
     const size_t smem = Ahead<T, VEC, NV, GATE == MG_GATE_NONE ? 2 : 3>::bytes(block);
-    MG_TRY(allow_shared(norm_bwd_kernel<T, VEC, NV, GATE>, smem));
+    MG_TRY(allow_shared<norm_bwd_kernel<T, VEC, NV, GATE>>(smem));
     norm_bwd_kernel<T, VEC, NV, GATE><<<unsigned(ceil_div(rt * p.G, block / tpg)), block, smem, s>>>(p, tpg, int(rt), part);
     MG_TRY(launched("mg_group_norm_bwd"));
     return launch_sum_parts(part, rt, {{p.dw, p.D}, {p.dbias, p.D}}, s);

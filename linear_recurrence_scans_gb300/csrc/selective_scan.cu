@@ -535,8 +535,8 @@ mg_status fwd_cover(const SsmArgs &p, cudaStream_t s)
     }
     constexpr size_t sm1 = kThreads / 32 * sizeof(FwdShared<T, VEC, CV::kWarpCh, CV::NP, true>);
     constexpr size_t sm2 = kThreads / 32 * sizeof(FwdShared<T, VEC, CV::kWarpCh, CV::NP, false>);
-    MG_TRY(allow_shared(ssm_chunk_kernel<T, VEC, CV, kStates>, sm1));
-    MG_TRY(allow_shared(ssm_chunk_kernel<T, VEC, CV, kOutputs>, sm2));
+    MG_TRY(allow_shared<ssm_chunk_kernel<T, VEC, CV, kStates>>(sm1));
+    MG_TRY(allow_shared<ssm_chunk_kernel<T, VEC, CV, kOutputs>>(sm2));
     if (ck.n > 1) {
         ssm_chunk_kernel<T, VEC, CV, kStates><<<unsigned(tiles * (ck.n - 1)), kThreads, sm1, s>>>(
             p, q, t, ck, agg_h, agg_s, bc_wide);
@@ -554,7 +554,7 @@ mg_status adjoint_cover(const SsmArgs &p, const Chunks &ck, float *agg_q, float 
     const int bc_wide = VEC > 1 && p.N % VEC == 0 && p.ldc % VEC == 0;
     const Seqs q = make_seqs(p.cu, p.B, p.T, p.nseq);
     constexpr size_t sm = kThreads / 32 * sizeof(FwdShared<T, VEC, CV::kWarpCh, CV::NP, true>);
-    MG_TRY(allow_shared(ssm_chunk_kernel<T, VEC, CV, kAdjoint>, sm));
+    MG_TRY(allow_shared<ssm_chunk_kernel<T, VEC, CV, kAdjoint>>(sm));
     ssm_chunk_kernel<T, VEC, CV, kAdjoint><<<unsigned(t.tiles * p.G * p.B * (ck.n - 1)), kThreads, sm, s>>>(
         p, q, t, ck, agg_q, agg_s, bc_wide);
     return launched("mg_selective_scan_bwd");

@@ -623,8 +623,8 @@ mg_status bwd(const SsmArgs &p, cudaStream_t s)
         MG_TRY(launch_ssm_adjoint(p, dt, VEC > 1, ck, agg_q, agg_s, s));
     }
     constexpr size_t smem = sizeof(BwdShared<T, VEC, CV>);
-    static_assert(smem <= 227 * 1024, "shared memory of a block");
-    MG_TRY(allow_shared(ssm_bwd_kernel<T, VEC, CV>, smem));
+    static_assert(smem <= kMostShared, "shared memory of a block");
+    MG_TRY(allow_shared<ssm_bwd_kernel<T, VEC, CV>>(smem));
     ssm_bwd_kernel<T, VEC, CV><<<unsigned(tiles * ck.n), CV::THREADS, smem, s>>>(p, q, t, ck, agg_q, agg_s, partB,
                                                                              partA, bc_wide);
     MG_TRY(launched("mg_selective_scan_bwd"));

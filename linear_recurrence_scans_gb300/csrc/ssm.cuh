@@ -3,6 +3,8 @@
 // helpers.
 #pragma once
 
+#include <atomic>
+
 #include "abi_checks.cuh"
 #include "common.cuh"
 #include "mg_ssm.h"
@@ -113,12 +115,23 @@ inline mg_status launched(const char *what)
     return e == cudaSuccess ? MG_OK : fail(MG_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
 }
 
-// Dynamic shared memory beyond the default 48 KB.
-template <typename K>
-mg_status allow_shared(K kernel, size_t bytes)
+// Dynamic shared memory beyond the default 48 KB (which count static shared
+// memory too): allowed once for a kernel and device, up to what a block may
+// have.  The set-up costs as much as a launch.
+constexpr size_t kMostShared = 226 * 1024;
+template <auto kKernel>
+mg_status allow_shared(size_t bytes)
 {
-    if (bytes <= 40 * 1024) return MG_OK;   // the default 48 KB count static shared memory too
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+    if (bytes <= 40 * 1024) return MG_OK;
+    if (bytes > kMostShared) return fail(MG_ERR_UNSUPPORTED, "%zu bytes of shared memory", bytes);
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (e == cudaSuccess && (done.load() & bit) == 0) {
+        e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared));
+        if (e == cudaSuccess) done.fetch_or(bit);
+    }
     return e == cudaSuccess ? MG_OK : fail(MG_ERR_LAUNCH, "shared memory: %s", cudaGetErrorString(e));
 }
 

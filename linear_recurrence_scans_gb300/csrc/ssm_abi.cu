@@ -1,5 +1,9 @@
 // The C entry points of mg_ssm.h: argument validation (all of it before any
 // launch) and the calls without rows.
+#include <cstring>
+#include <type_traits>
+#include <utility>
+
 #include "ssm.cuh"
 
 using namespace mg;
@@ -123,6 +127,33 @@ mg_status check_norm(const char *fn, int64_t M, int64_t D, int64_t G, mg_gate ga
     MG_TRY(check_size(fn, M, D));
     if (M > (int64_t(1) << 31) / G) return fail(MG_ERR_UNSUPPORTED, "%s: M G beyond 2^31", fn);
     return MG_OK;
+}
+
+// Calls f with its arguments from 64-bit words.
+template <typename A>
+A from_word(uint64_t w)
+{
+    A a{};
+    if constexpr (std::is_pointer_v<A>) {
+        a = reinterpret_cast<A>(static_cast<uintptr_t>(w));
+    } else if constexpr (std::is_same_v<A, double>) {
+        memcpy(&a, &w, sizeof(a));
+    } else {
+        a = static_cast<A>(static_cast<int64_t>(w));
+    }
+    return a;
+}
+template <typename... A, size_t... I>
+mg_status call_words(mg_status (*f)(A...), const uint64_t *w, std::index_sequence<I...>)
+{
+    return f(from_word<A>(w[I])...);
+}
+template <typename... A>
+mg_status call_words(mg_status (*f)(A...), const uint64_t *w, int n)
+{
+    if (n != int(sizeof...(A)))
+        return fail(MG_ERR_INVALID_ARG, "mg_ssm_call: %d arguments, %d expected", n, int(sizeof...(A)));
+    return call_words(f, w, std::index_sequence_for<A...>());
 }
 
 }  // namespace
@@ -477,6 +508,22 @@ mg_status mg_group_norm_bwd(const void *dy, int64_t lddy, const float *stats, co
     p.w = w, p.bias = bias, p.rms = rms, p.gate = gate, p.silu = silu, p.dx = dx, p.dz = dz;
     p.dw = dw, p.dbias = dbias, p.M = M, p.D = D, p.G = G, p.ws = ws;
     return launch_norm_bwd(p, dt, stream);
+}
+
+mg_status mg_ssm_call(mg_ssm_op op, const uint64_t *args, int nargs)
+{
+    if (args == nullptr) return fail(MG_ERR_INVALID_ARG, "mg_ssm_call: args is NULL");
+    switch (op) {
+    case MG_CAUSAL_CONV_FWD: return call_words(mg_causal_conv_fwd, args, nargs);
+    case MG_CAUSAL_CONV_BWD: return call_words(mg_causal_conv_bwd, args, nargs);
+    case MG_CAUSAL_CONV_STEP: return call_words(mg_causal_conv_step, args, nargs);
+    case MG_SELECTIVE_SCAN_FWD: return call_words(mg_selective_scan_fwd, args, nargs);
+    case MG_SELECTIVE_SCAN_BWD: return call_words(mg_selective_scan_bwd, args, nargs);
+    case MG_SELECTIVE_SCAN_STEP: return call_words(mg_selective_scan_step, args, nargs);
+    case MG_GROUP_NORM_FWD: return call_words(mg_group_norm_fwd, args, nargs);
+    case MG_GROUP_NORM_BWD: return call_words(mg_group_norm_bwd, args, nargs);
+    }
+    return fail(MG_ERR_INVALID_ARG, "mg_ssm_call: op %d", int(op));
 }
 
 }  // extern "C"

@@ -23,11 +23,13 @@ then made too; a token call writes its state in place.
 from __future__ import annotations
 
 import ctypes
-import functools
+import struct
 
 import torch
+from torch import Tensor
 
-from . import _DT, _check, _cu, _out, _prep, _stream_handle, _workspace, load
+from . import (_DT, MG_ERR_INVALID_ARG, MG_OK, _check, _cu, _out, _prep, _stream_handle, _workspace,
+               load)
 
 __all__ = [
     "mg_causal_conv_fwd", "mg_causal_conv_bwd", "mg_causal_conv_step",
@@ -44,18 +46,29 @@ SYMBOLS = (
     "mg_selective_scan_bwd_workspace_size", "mg_selective_scan_saved_size",
     "mg_selective_scan_saved_rows", "mg_selective_scan_fwd", "mg_selective_scan_bwd",
     "mg_selective_scan_step", "mg_group_norm_workspace_size", "mg_group_norm_fwd",
-    "mg_group_norm_bwd",
+    "mg_group_norm_bwd", "mg_ssm_call",
 )
 
 MAX_STATES, MAX_TAPS = 64, 8
 _ACTIVATIONS = (torch.float32, torch.bfloat16)
+_F32 = torch.float32
 _CONTROL_BYTES = 256
+
+# The calls' argument blocks (mg_ssm_call): one packed argument costs a third
+# of what ctypes takes for twenty.
+_OPS = {name: (op, struct.Struct(words).pack, len(words)) for op, (name, words) in enumerate({
+    "mg_causal_conv_fwd": "q" * 18, "mg_causal_conv_bwd": "q" * 23, "mg_causal_conv_step": "q" * 14,
+    "mg_selective_scan_fwd": "q" * 27, "mg_selective_scan_bwd": "q" * 36,
+    "mg_selective_scan_step": "q" * 22,
+    "mg_group_norm_fwd": "q" * 7 + "d" + "q" * 9, "mg_group_norm_bwd": "q" * 23,
+}.items())}
+_call = None
 
 
 def declare(lib):
-    """Argument types of the entry points of mg_ssm.h."""
-    vp, i64, i32, sz, f64 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t,
-                             ctypes.c_double)
+    """Argument types of the entry points of mg_ssm.h that are called."""
+    global _call
+    i64, i32, sz = ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
     sizes = {"mg_causal_conv_workspace_size": [i64, i64, i64, i32],
              "mg_selective_scan_fwd_workspace_size": [i64] * 6,
              "mg_selective_scan_bwd_workspace_size": [i64] * 6,
@@ -64,6 +77,7 @@ def declare(lib):
     for name, args in sizes.items():
         getattr(lib, name).argtypes, getattr(lib, name).restype = args, sz
     lib.mg_selective_scan_saved_rows.argtypes, lib.mg_selective_scan_saved_rows.restype = [], i32
+    vp, f64 = ctypes.c_void_p, ctypes.c_double
     calls = {
         "mg_causal_conv_fwd": [vp, i64, i32, vp, vp, vp, vp, i64, i32, vp, vp, i64, i64, i64, i32,
                                vp, sz, vp],
@@ -84,198 +98,233 @@ def declare(lib):
     }
     for name, args in calls.items():
         getattr(lib, name).argtypes, getattr(lib, name).restype = args, i32
+    lib.mg_ssm_call.argtypes, lib.mg_ssm_call.restype = [i32, ctypes.c_char_p, i32], i32
+    _call = lib.mg_ssm_call
+
+
+def _run(name, *words):
+    """The C call `name`; `words` are its arguments."""
+    op, pack, n = _OPS[name]
+    st = (_call or load().mg_ssm_call)(op, pack(*words), n)
+    if st != MG_OK:
+        _check(st, name)
+
+
+def _run_ws(name, need, device, ws, words, sh):
+    """The C call `name` with a workspace: arguments `words`, then workspace,
+    its size and the stream.  The stream's cached workspace is tried as it is;
+    need() is asked only when the call says that it does not do."""
+    op, pack, n = _OPS[name]
+    buf = _workspace(_CONTROL_BYTES, device, sh, ws)
+    st = (_call or load().mg_ssm_call)(op, pack(*words, buf.data_ptr(), buf.numel(), sh), n)
+    if st == MG_ERR_INVALID_ARG and ws is None:
+        size = need()
+        if size > buf.numel():
+            buf = _workspace(size, device, sh, None)
+            st = _call(op, pack(*words, buf.data_ptr(), buf.numel(), sh), n)
+    if st != MG_OK:
+        _check(st, name)
 
 
 # ---------------------------------------------------------------- arguments
 
-def _on_stream(f):
-    """With stream=, everything the op does (copies of arguments and the
-    allocation of outputs too) happens on that stream."""
-    @functools.wraps(f)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return f(*args, **kw)
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
-    return call
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(x) -> int:
+    return _raw_stream(x.get_device()) if _raw_stream is not None else _stream_handle(None, x.device)
 
 
 def _rows(x, name, dtypes, inner=1):
-    """(tensor, row stride) of an activation whose rows are its last ``inner``
-    dimensions: x itself where the kernels can read its rows in place, else a
-    dense copy."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+    """(x, pointer, row stride) of an activation whose rows are its last
+    ``inner`` dimensions: x itself where the kernels can read its rows in
+    place, else a dense copy."""
+    if not isinstance(x, Tensor) or not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if x.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {x.dtype} not in {dtypes}")
-    shape, stride = x.shape, x.stride()
+    shape = x.shape
     width = shape[-1] if inner == 1 else shape[-1] * shape[-2]
-    ok, step = x.data_ptr() % 16 == 0, 1
-    for i in range(1, inner + 1):
-        ok = ok and (shape[-i] == 1 or stride[-i] == step)
-        step *= shape[-i]
-    ld, rows = 0, 1
-    for i in range(len(shape) - inner - 1, -1, -1):
-        n = shape[i]
-        if n != 1:
-            if ld == 0:
-                ld = stride[i]   # rows is still 1 here
-            elif stride[i] != ld * rows:
-                ok = False
-            rows *= n
-    if ld == 0 and rows == 1:
-        ld = width
-    if ok and ld >= width:
-        return x, ld
-    return x.clone(memory_format=torch.contiguous_format), width
+    ptr = x.data_ptr()
+    if not ptr & 15:
+        if x.is_contiguous():
+            return x, ptr, width
+        stride, ok, step = x.stride(), True, 1
+        for i in range(1, inner + 1):
+            ok = ok and (shape[-i] == 1 or stride[-i] == step)
+            step *= shape[-i]
+        ld, rows = 0, 1
+        for i in range(len(shape) - inner - 1, -1, -1):
+            n = shape[i]
+            if n != 1:
+                if rows == 1:
+                    ld = stride[i]
+                elif stride[i] != ld * rows:
+                    ok = False
+                rows *= n
+        if rows == 1:
+            ld = width
+        if ok and ld >= width:
+            return x, ptr, ld
+    x = x.clone(memory_format=torch.contiguous_format)
+    return x, x.data_ptr(), width
 
 
-def _param(x, name, shape):
-    """A float32 parameter or state of that shape, dense (None stays None)."""
+def _param(x, name, shape, dtype=_F32):
+    """(x, pointer) of a dense parameter or state of that shape (None and NULL
+    stay what they are)."""
     if x is None:
-        return None
-    x = _prep(x, name)
-    if tuple(x.shape) != shape:
-        raise ValueError(f"{name} must be {shape}")
-    return x
+        return None, 0
+    if not isinstance(x, Tensor) or x.dtype != dtype or not x.is_cuda or not x.is_contiguous() \
+            or x.data_ptr() & 15:
+        x = _prep(x, name, (dtype,))
+    if x.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}")
+    return x, x.data_ptr()
 
 
-def _ptr(x):
-    return x.data_ptr() if x is not None and x.numel() else None
+def _new(out, i, shape, like, dtype):
+    """(output i, its pointer): the caller's, or a new one."""
+    if out is None or i >= len(out) or out[i] is None:
+        o = torch.empty(shape, dtype=dtype, device=like.device)
+    else:
+        o = _out(out, i, shape, like, dtype)
+    return o, o.data_ptr()
 
 
 def _silu(act):
-    if act not in ("silu", None):
+    if act == "silu":
+        return 1
+    if act is not None:
         raise ValueError('act must be "silu" or None')
-    return int(act == "silu")
+    return 0
 
 
 def _sequences(cu_seqlens, x, B):
-    """(cu, number of sequences) of a batch of B rows of sequences."""
+    """(cu, its pointer, number of sequences) of a batch of B rows of sequences."""
     if cu_seqlens is None:
-        return None, B
+        return None, 0, B
     if B != 1:
         raise ValueError("with cu_seqlens the batch must be one packed sequence")
     cu = _cu(cu_seqlens, x)
     if cu.numel() < 2:
         raise ValueError("cu_seqlens must name at least one sequence")
-    return cu, cu.numel() - 1
+    if cu.data_ptr() & 7:
+        cu = cu.clone()
+    return cu, cu.data_ptr(), cu.numel() - 1
 
 
 def _slots(slots, state, B):
     if slots is None:
         if state.shape[0] < B:
             raise ValueError("state must have an entry for every row of the batch")
-        return None
-    if not isinstance(slots, torch.Tensor) or not slots.is_cuda or slots.dtype != torch.int64 \
-            or slots.dim() != 1 or slots.numel() != B:
+        return None, 0
+    if not isinstance(slots, Tensor) or slots.dtype != torch.int64 or not slots.is_cuda or slots.shape != (B,):
         raise ValueError("slots must be a CUDA int64 tensor with one entry for each row")
-    slots = slots.contiguous()
-    return slots.clone() if slots.data_ptr() % 16 else slots
+    if not slots.is_contiguous() or slots.data_ptr() & 15:
+        slots = slots.clone(memory_format=torch.contiguous_format)
+    return slots, slots.data_ptr()
 
 
 def _state(state, name, dtype, inner):
     """A pool of states that a call updates in place: never copied."""
-    if not isinstance(state, torch.Tensor) or not state.is_cuda or state.dtype != dtype \
-            or state.dim() != 1 + len(inner) or tuple(state.shape[1:]) != inner \
-            or not state.is_contiguous() or state.data_ptr() % 16:
+    if not isinstance(state, Tensor) or state.dtype != dtype or not state.is_cuda \
+            or state.shape[1:] != inner or state.dim() != 1 + len(inner) \
+            or not state.is_contiguous() or state.data_ptr() & 15:
         raise ValueError(f"{name} must be a dense, 16-byte aligned {dtype} CUDA tensor "
                          f"(states, {', '.join(map(str, inner))})")
-    return state
+    return state.data_ptr()
 
 
 # -------------------------------------------------------------- convolution
 
-def _conv_args(x, w, bias, x0, cu_seqlens):
-    x, ldx = _rows(x, "x", _ACTIVATIONS)
-    if x.dim() != 3:
-        raise ValueError("x must be (B, T, D)")
-    B, T, D = x.shape
-    w = _prep(w, "w")
-    if w.dim() != 2 or w.shape[0] != D or not 1 <= w.shape[1] <= MAX_TAPS:
+def _taps(w, D):
+    if not isinstance(w, Tensor) or w.dim() != 2 or w.shape[0] != D or not 1 <= w.shape[1] <= MAX_TAPS:
         raise ValueError(f"w must be (D, W) with W at most {MAX_TAPS}")
-    W = w.shape[1]
-    cu, nseq = _sequences(cu_seqlens, x, B)
-    bias = _param(bias, "bias", (D,))
-    edge = (nseq, W - 1, D)
-    if x0 is not None:
-        x0 = _prep(x0, "x0", (x.dtype,))
-        if tuple(x0.shape) != edge:
-            raise ValueError(f"x0 must be {edge}")
-    return x, ldx, w, bias, x0, cu, nseq, edge
+    return _param(w, "w", w.shape)
 
 
-@_on_stream
-def mg_causal_conv_fwd(x, w, bias=None, x0=None, *, act="silu", cu_seqlens=None, out=None, ws=None):
+def mg_causal_conv_fwd(x, w, bias=None, x0=None, *, act="silu", cu_seqlens=None, out=None, ws=None,
+                       stream=None):
     """(y (B,T,D), x_last (sequences, W-1, D)): y = act(bias + sum_k w[:, k]
     x_{t-W+1+k}), from the W-1 rows x0 before each sequence (zero without
     them); x_last holds each sequence's last W-1 inputs, the x0 of what
     follows.  w (D, W), 1 <= W <= 8; act "silu" or None."""
-    x, ldx, w, bias, x0, cu, nseq, edge = _conv_args(x, w, bias, x0, cu_seqlens)
-    B, T, D = x.shape
-    y = _out(out, 0, x.shape, x, x.dtype)
-    x_last = _out(out, 1, edge, x, x.dtype)
-    sh = _stream_handle(None, x.device)
-    wk = _workspace(_CONTROL_BYTES, x.device, sh, ws)
-    _check(load().mg_causal_conv_fwd(_ptr(x), ldx, _DT[x.dtype], _ptr(w), _ptr(bias), _ptr(x0),
-                                     _ptr(cu), nseq, _silu(act), _ptr(y), _ptr(x_last), B, T, D,
-                                     w.shape[1], wk.data_ptr(), wk.numel(), sh),
-           "mg_causal_conv_fwd")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mg_causal_conv_fwd(x, w, bias, x0, act=act, cu_seqlens=cu_seqlens, out=out, ws=ws)
+    x, px, ldx = _rows(x, "x", _ACTIVATIONS)
+    if x.dim() != 3:
+        raise ValueError("x must be (B, T, D)")
+    (B, T, D), ty = x.shape, x.dtype
+    w, pw = _taps(w, D)
+    W = w.shape[1]
+    cu, pcu, nseq = _sequences(cu_seqlens, x, B)
+    edge = (nseq, W - 1, D)
+    bias, pb = _param(bias, "bias", (D,))
+    x0, px0 = _param(x0, "x0", edge, ty)
+    y, py = _new(out, 0, (B, T, D), x, ty)
+    x_last, pl = _new(out, 1, edge, x, ty)
+    sh = _stream(x)
+    _run_ws("mg_causal_conv_fwd", lambda: _CONTROL_BYTES, x.device, ws,
+            (px, ldx, _DT[ty], pw, pb, px0, pcu, nseq, _silu(act), py, pl, B, T, D, W), sh)
     return y, x_last
 
 
-@_on_stream
 def mg_causal_conv_bwd(dy, x, w, bias=None, x0=None, dx_last=None, *, act="silu", cu_seqlens=None,
-                       out=None, ws=None):
+                       out=None, ws=None, stream=None):
     """(dx, dw, dbias, dx0): gradients of sum(dy*y) + sum(dx_last*x_last) for
     mg_causal_conv_fwd on the same inputs; dbias and dx0 are None without bias
     and x0."""
-    x, ldx, w, bias, x0, cu, nseq, edge = _conv_args(x, w, bias, x0, cu_seqlens)
-    dy, lddy = _rows(dy, "dy", (x.dtype,))
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mg_causal_conv_bwd(dy, x, w, bias, x0, dx_last, act=act, cu_seqlens=cu_seqlens,
+                                      out=out, ws=ws)
+    x, px, ldx = _rows(x, "x", _ACTIVATIONS)
+    if x.dim() != 3:
+        raise ValueError("x must be (B, T, D)")
+    (B, T, D), ty = x.shape, x.dtype
+    dy, pdy, lddy = _rows(dy, "dy", (ty,))
     if dy.shape != x.shape:
         raise ValueError("dy must have x's shape")
-    if dx_last is not None:
-        dx_last = _prep(dx_last, "dx_last", (x.dtype,))
-        if tuple(dx_last.shape) != edge:
-            raise ValueError(f"dx_last must be {edge}")
-    B, T, D = x.shape
-    dx = _out(out, 0, x.shape, x, x.dtype)
-    dw = _out(out, 1, w.shape, x)
-    dbias = _out(out, 2, (D,), x) if bias is not None else None
-    dx0 = _out(out, 3, edge, x, x.dtype) if x0 is not None else None
-    sh = _stream_handle(None, x.device)
-    lib = load()
-    wk = _workspace(lib.mg_causal_conv_workspace_size(B, T, D, w.shape[1]), x.device, sh, ws)
-    _check(lib.mg_causal_conv_bwd(_ptr(dy), lddy, _ptr(x), ldx, _DT[x.dtype], _ptr(w), _ptr(bias),
-                                  _ptr(x0), _ptr(dx_last), _ptr(cu), nseq, _silu(act), _ptr(dx),
-                                  _ptr(dw), _ptr(dbias), _ptr(dx0), B, T, D, w.shape[1],
-                                  wk.data_ptr(), wk.numel(), sh),
-           "mg_causal_conv_bwd")
+    w, pw = _taps(w, D)
+    W = w.shape[1]
+    cu, pcu, nseq = _sequences(cu_seqlens, x, B)
+    edge = (nseq, W - 1, D)
+    bias, pb = _param(bias, "bias", (D,))
+    x0, px0 = _param(x0, "x0", edge, ty)
+    dx_last, pdl = _param(dx_last, "dx_last", edge, ty)
+    dx, pdx = _new(out, 0, (B, T, D), x, ty)
+    dw, pdw = _new(out, 1, (D, W), x, _F32)
+    dbias, pdb = _new(out, 2, (D,), x, _F32) if bias is not None else (None, 0)
+    dx0, pdx0 = _new(out, 3, edge, x, ty) if x0 is not None else (None, 0)
+    sh = _stream(x)
+    _run_ws("mg_causal_conv_bwd", lambda: load().mg_causal_conv_workspace_size(B, T, D, W), x.device, ws,
+            (pdy, lddy, px, ldx, _DT[ty], pw, pb, px0, pdl, pcu, nseq, _silu(act), pdx, pdw, pdb, pdx0,
+             B, T, D, W), sh)
     return dx, dw, dbias, dx0
 
 
-@_on_stream
-def mg_causal_conv_step(x, w, state, bias=None, *, slots=None, act="silu", out=None):
+def mg_causal_conv_step(x, w, state, bias=None, *, slots=None, act="silu", out=None, stream=None):
     """y (B, D): one token x (B, D) a row through the convolution.  Row i's
     last W-1 inputs are state[slots[i]] (state[i] without slots), of x's type,
     (states, W-1, D), moved on in place; a row whose slot is not in the pool
     is idle: y 0, no state written."""
-    x, ldx = _rows(x, "x", _ACTIVATIONS)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mg_causal_conv_step(x, w, state, bias, slots=slots, act=act, out=out)
+    x, px, ldx = _rows(x, "x", _ACTIVATIONS)
     if x.dim() != 2:
         raise ValueError("x must be (B, D)")
-    B, D = x.shape
-    w = _prep(w, "w")
-    if w.dim() != 2 or w.shape[0] != D or not 1 <= w.shape[1] <= MAX_TAPS:
-        raise ValueError(f"w must be (D, W) with W at most {MAX_TAPS}")
+    (B, D), ty = x.shape, x.dtype
+    w, pw = _taps(w, D)
     W = w.shape[1]
-    state = _state(state, "state", x.dtype, (W - 1, D))
-    slots = _slots(slots, state, B)
-    bias = _param(bias, "bias", (D,))
-    y = _out(None if out is None else (out,), 0, x.shape, x, x.dtype)
-    _check(load().mg_causal_conv_step(_ptr(x), ldx, _DT[x.dtype], _ptr(w), _ptr(bias), _ptr(state),
-                                      state.shape[0], _ptr(slots), _silu(act), _ptr(y), B, D, W,
-                                      _stream_handle(None, x.device)),
-           "mg_causal_conv_step")
+    ps = _state(state, "state", ty, (W - 1, D))
+    slots, psl = _slots(slots, state, B)
+    bias, pb = _param(bias, "bias", (D,))
+    y, py = _new(None if out is None else (out,), 0, (B, D), x, ty)
+    _run("mg_causal_conv_step", px, ldx, _DT[ty], pw, pb, ps, state.shape[0], psl, _silu(act), py, B, D, W,
+         _stream(x))
     return y
 
 
@@ -283,117 +332,133 @@ def mg_causal_conv_step(x, w, state, bias=None, *, slots=None, act="silu", out=N
 
 def _scan_args(x, dt, A, B, C, D, dt_bias, lead):
     """The arguments that the scan's three calls share; x has `lead` leading
-    dimensions.  B and C may leave out the group dimension."""
-    x, ldx = _rows(x, "x", _ACTIVATIONS)
-    if x.dim() != lead + 1:
+    dimensions.  B and C may leave out the group dimension.  The tensors (kept
+    alive until the call is made), the words of the C calls from x to the
+    softplus flag, N, G and the shape of B and C."""
+    x, px, ldx = _rows(x, "x", _ACTIVATIONS)
+    shape, ty = x.shape, x.dtype
+    if len(shape) != lead + 1:
         raise ValueError("x must be (B, T, D)" if lead == 2 else "x must be (B, D)")
-    dt, ldt = _rows(dt, "dt", (x.dtype,))
-    if dt.shape != x.shape:
+    like = (ty,)
+    dt, pdt, ldt = _rows(dt, "dt", like)
+    if dt.shape != shape:
         raise ValueError("dt must have x's shape")
-    Dx = x.shape[-1]
-    A = _prep(A, "A")
-    if A.dim() != 2 or A.shape[0] != Dx or not 1 <= A.shape[1] <= MAX_STATES:
+    Dx = shape[-1]
+    if not isinstance(A, Tensor) or A.dim() != 2 or A.shape[0] != Dx or not 1 <= A.shape[1] <= MAX_STATES:
         raise ValueError(f"A must be (D, N) with N at most {MAX_STATES}")
+    A, pA = _param(A, "A", A.shape)
     N = A.shape[1]
-    bc = []
-    for m, name in ((B, "B"), (C, "C")):
-        if not isinstance(m, torch.Tensor) or m.dim() not in (lead + 1, lead + 2) \
-                or m.shape[:lead] != x.shape[:lead] or m.shape[-1] != N:
-            raise ValueError(f"{name} must be x's leading dimensions and (G, N), or (N)")
-        bc.append(_rows(m, name, (x.dtype,), m.dim() - lead))
-    (B, ldb), (C, ldc) = bc
-    if B.shape != C.shape:
-        raise ValueError("B and C must have the same shape")
-    G = B.shape[-2] if B.dim() == lead + 2 else 1
+    bshape = B.shape if isinstance(B, Tensor) else ()
+    dims = len(bshape) - lead
+    if dims not in (1, 2) or bshape[-1] != N or bshape[:lead] != shape[:lead] \
+            or not isinstance(C, Tensor) or C.shape != bshape:
+        raise ValueError("B and C must both be x's leading dimensions and (G, N), or (N)")
+    B, pB, ldb = _rows(B, "B", like, dims)
+    C, pC, ldc = _rows(C, "C", like, dims)
+    G = bshape[-2] if dims == 2 else 1
     if G < 1 or Dx % G:
         raise ValueError("D must be a multiple of the number of groups of B and C")
-    return (x, ldx, dt, ldt, A, B, ldb, C, ldc, _param(D, "D", (Dx,)),
-            _param(dt_bias, "dt_bias", (Dx,)), N, G)
+    D, pD = _param(D, "D", (Dx,))
+    dt_bias, pbias = _param(dt_bias, "dt_bias", (Dx,))
+    return ((x, dt, A, B, C, D, dt_bias), (px, ldx, pdt, ldt, pA, pB, ldb, pC, ldc, _DT[ty], pD, pbias),
+            N, G, bshape)
 
 
-@_on_stream
+_seg = 0   # rows between two saved states
+
+
+def _saved_numel(B, T, D, N):
+    global _seg
+    if _seg == 0:
+        _seg = load().mg_selective_scan_saved_rows()
+    return B * -(-T // _seg) * D * N
+
+
 def mg_selective_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, h0=None, *, softplus=True,
-                          cu_seqlens=None, save=False, out=None, ws=None):
+                          cu_seqlens=None, save=False, out=None, ws=None, stream=None):
     """(y (B,T,D), h_last (sequences, D, N), saved): the selective scan
       h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t,  y_t = C_t h_t + D x_t,
     delta = softplus(dt + dt_bias) (without softplus: dt + dt_bias), from h0.
     x, dt (B,T,D); A (D,N), N <= 64; B, C (B,T,G,N), or (B,T,N) for one group;
     channel d reads group d // (D/G).  saved, with save=True, is what
     mg_selective_scan_bwd needs of this call; else None."""
-    x, ldx, dt, ldt, A, Bm, ldb, Cm, ldc, D, dt_bias, N, G = _scan_args(x, dt, A, B, C, D, dt_bias, 2)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mg_selective_scan_fwd(x, dt, A, B, C, D, dt_bias, h0, softplus=softplus,
+                                         cu_seqlens=cu_seqlens, save=save, out=out, ws=ws)
+    keep, words, N, G, _ = _scan_args(x, dt, A, B, C, D, dt_bias, 2)
+    x = keep[0]
     Bx, T, Dx = x.shape
-    cu, nseq = _sequences(cu_seqlens, x, Bx)
-    h0 = _param(h0, "h0", (nseq, Dx, N))
-    y = _out(out, 0, x.shape, x, x.dtype)
-    h_last = _out(out, 1, (nseq, Dx, N), x)
-    lib = load()
-    saved = _out(out[2:] if out is not None and len(out) > 2 else None, 0,
-                 (lib.mg_selective_scan_saved_size(Bx, T, Dx, N) // 4,), x) if save else None
-    sh = _stream_handle(None, x.device)
-    wk = _workspace(lib.mg_selective_scan_fwd_workspace_size(Bx, T, Dx, N, G, nseq), x.device, sh, ws)
-    _check(lib.mg_selective_scan_fwd(_ptr(x), ldx, _ptr(dt), ldt, _ptr(A), _ptr(Bm), ldb, _ptr(Cm),
-                                     ldc, _DT[x.dtype], _ptr(D), _ptr(dt_bias), int(bool(softplus)),
-                                     _ptr(h0), _ptr(cu), nseq, _ptr(y), _ptr(h_last), _ptr(saved),
-                                     Bx, T, Dx, N, G, wk.data_ptr(), wk.numel(), sh),
-           "mg_selective_scan_fwd")
+    cu, pcu, nseq = _sequences(cu_seqlens, x, Bx)
+    states = (nseq, Dx, N)
+    h0, ph0 = _param(h0, "h0", states)
+    y, py = _new(out, 0, x.shape, x, x.dtype)
+    h_last, pl = _new(out, 1, states, x, _F32)
+    saved, psv = _new(out, 2, (_saved_numel(Bx, T, Dx, N),), x, _F32) if save else (None, 0)
+    sh = _stream(x)
+    _run_ws("mg_selective_scan_fwd",
+            lambda: load().mg_selective_scan_fwd_workspace_size(Bx, T, Dx, N, G, nseq), x.device, ws,
+            (*words, 1 if softplus else 0, ph0, pcu, nseq, py, pl, psv, Bx, T, Dx, N, G), sh)
     return y, h_last, saved
 
 
-@_on_stream
 def mg_selective_scan_bwd(dy, saved, x, dt, A, B, C, D=None, dt_bias=None, h0=None, dh_last=None, *,
-                          softplus=True, cu_seqlens=None, out=None, ws=None):
+                          softplus=True, cu_seqlens=None, out=None, ws=None, stream=None):
     """(dx, ddt, dA, dB, dC, dD, ddt_bias, dh0): gradients of sum(dy*y) +
     sum(dh_last*h_last) for mg_selective_scan_fwd on the same inputs, with the
     `saved` that it returned.  dD, ddt_bias and dh0 are None where their input
     is."""
-    x, ldx, dt, ldt, A, Bm, ldb, Cm, ldc, D, dt_bias, N, G = _scan_args(x, dt, A, B, C, D, dt_bias, 2)
-    dy, lddy = _rows(dy, "dy", (x.dtype,))
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mg_selective_scan_bwd(dy, saved, x, dt, A, B, C, D, dt_bias, h0, dh_last,
+                                         softplus=softplus, cu_seqlens=cu_seqlens, out=out, ws=ws)
+    keep, words, N, G, bshape = _scan_args(x, dt, A, B, C, D, dt_bias, 2)
+    x, ty = keep[0], keep[0].dtype
+    dy, pdy, lddy = _rows(dy, "dy", (ty,))
     if dy.shape != x.shape:
         raise ValueError("dy must have x's shape")
     Bx, T, Dx = x.shape
-    cu, nseq = _sequences(cu_seqlens, x, Bx)
-    h0 = _param(h0, "h0", (nseq, Dx, N))
-    dh_last = _param(dh_last, "dh_last", (nseq, Dx, N))
-    lib = load()
-    saved = _param(saved, "saved", (lib.mg_selective_scan_saved_size(Bx, T, Dx, N) // 4,))
+    cu, pcu, nseq = _sequences(cu_seqlens, x, Bx)
+    states = (nseq, Dx, N)
+    h0, ph0 = _param(h0, "h0", states)
+    dh_last, pdl = _param(dh_last, "dh_last", states)
     if saved is None:
         raise ValueError("saved must be what mg_selective_scan_fwd returned with save=True")
-    dx, ddt = _out(out, 0, x.shape, x, x.dtype), _out(out, 1, x.shape, x, x.dtype)
-    dA = _out(out, 2, A.shape, x)
-    dB, dC = _out(out, 3, Bm.shape, x, x.dtype), _out(out, 4, Cm.shape, x, x.dtype)
-    dD = _out(out, 5, (Dx,), x) if D is not None else None
-    ddt_bias = _out(out, 6, (Dx,), x) if dt_bias is not None else None
-    dh0 = _out(out, 7, (nseq, Dx, N), x) if h0 is not None else None
-    sh = _stream_handle(None, x.device)
-    wk = _workspace(lib.mg_selective_scan_bwd_workspace_size(Bx, T, Dx, N, G, nseq), x.device, sh, ws)
-    _check(lib.mg_selective_scan_bwd(_ptr(dy), lddy, _ptr(saved), _ptr(x), ldx, _ptr(dt), ldt,
-                                     _ptr(A), _ptr(Bm), ldb, _ptr(Cm), ldc, _DT[x.dtype], _ptr(D),
-                                     _ptr(dt_bias), int(bool(softplus)), _ptr(h0), _ptr(dh_last),
-                                     _ptr(cu), nseq, _ptr(dx), _ptr(ddt), _ptr(dA), _ptr(dB),
-                                     _ptr(dC), _ptr(dD), _ptr(ddt_bias), _ptr(dh0), Bx, T, Dx, N, G,
-                                     wk.data_ptr(), wk.numel(), sh),
-           "mg_selective_scan_bwd")
+    saved, psv = _param(saved, "saved", (_saved_numel(Bx, T, Dx, N),))
+    dx, pdx = _new(out, 0, x.shape, x, ty)
+    ddt, pddt = _new(out, 1, x.shape, x, ty)
+    dA, pdA = _new(out, 2, (Dx, N), x, _F32)
+    dB, pdB = _new(out, 3, bshape, x, ty)
+    dC, pdC = _new(out, 4, bshape, x, ty)
+    dD, pdD = _new(out, 5, (Dx,), x, _F32) if D is not None else (None, 0)
+    ddt_bias, pdbias = _new(out, 6, (Dx,), x, _F32) if dt_bias is not None else (None, 0)
+    dh0, pdh0 = _new(out, 7, states, x, _F32) if h0 is not None else (None, 0)
+    sh = _stream(x)
+    _run_ws("mg_selective_scan_bwd",
+            lambda: load().mg_selective_scan_bwd_workspace_size(Bx, T, Dx, N, G, nseq), x.device, ws,
+            (pdy, lddy, psv, *words, 1 if softplus else 0, ph0, pdl, pcu, nseq, pdx, pddt, pdA, pdB, pdC,
+             pdD, pdbias, pdh0, Bx, T, Dx, N, G), sh)
     return dx, ddt, dA, dB, dC, dD, ddt_bias, dh0
 
 
-@_on_stream
-def mg_selective_scan_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, slots=None,
-                           softplus=True, out=None):
+def mg_selective_scan_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, slots=None, softplus=True,
+                           out=None, stream=None):
     """y (B, D): one token a row through mg_selective_scan_fwd's recurrence.
     x, dt (B, D); B, C (B, G, N) or (B, N).  Row i's state is state[slots[i]]
     (state[i] without slots) of (states, D, N) float32, updated in place; a
     row whose slot is not in the pool is idle: y 0, no state written."""
-    x, ldx, dt, ldt, A, Bm, ldb, Cm, ldc, D, dt_bias, N, G = _scan_args(x, dt, A, B, C, D, dt_bias, 1)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mg_selective_scan_step(x, dt, A, B, C, state, D, dt_bias, slots=slots,
+                                          softplus=softplus, out=out)
+    keep, words, N, G, _ = _scan_args(x, dt, A, B, C, D, dt_bias, 1)
+    x = keep[0]
     Bx, Dx = x.shape
-    state = _state(state, "state", torch.float32, (Dx, N))
-    slots = _slots(slots, state, Bx)
-    y = _out(None if out is None else (out,), 0, x.shape, x, x.dtype)
-    _check(load().mg_selective_scan_step(_ptr(x), ldx, _ptr(dt), ldt, _ptr(A), _ptr(Bm), ldb,
-                                         _ptr(Cm), ldc, _DT[x.dtype], _ptr(D), _ptr(dt_bias),
-                                         int(bool(softplus)), _ptr(state), state.shape[0],
-                                         _ptr(slots), _ptr(y), Bx, Dx, N, G,
-                                         _stream_handle(None, x.device)),
-           "mg_selective_scan_step")
+    ps = _state(state, "state", _F32, (Dx, N))
+    slots, psl = _slots(slots, state, Bx)
+    y, py = _new(None if out is None else (out,), 0, (Bx, Dx), x, x.dtype)
+    _run("mg_selective_scan_step", *words, 1 if softplus else 0, ps, state.shape[0], psl, py, Bx, Dx, N, G,
+         _stream(x))
     return y
 
 
@@ -403,70 +468,72 @@ MG_GATE_NONE, MG_GATE_AFTER, MG_GATE_FIRST = range(3)
 
 
 def _norm_args(x, w, bias, z, groups, gate_first):
-    x, ldx = _rows(x, "x", _ACTIVATIONS)
-    if x.dim() < 1:
+    x, px, ldx = _rows(x, "x", _ACTIVATIONS)
+    shape = x.shape
+    if len(shape) < 1:
         raise ValueError("x must be (..., D)")
-    D = x.shape[-1]
+    D = shape[-1]
     if groups < 1 or D % groups:
         raise ValueError("the channels must be a multiple of groups")
-    ldz, gate = D, MG_GATE_NONE
+    pz, ldz, gate = 0, D, MG_GATE_NONE
     if z is not None:
-        z, ldz = _rows(z, "z", (x.dtype,))
-        if z.shape != x.shape:
+        z, pz, ldz = _rows(z, "z", (x.dtype,))
+        if z.shape != shape:
             raise ValueError("z must have x's shape")
         gate = MG_GATE_FIRST if gate_first else MG_GATE_AFTER
     elif gate_first:
         raise ValueError("gate_first needs z")
-    w = _param(w, "w", (D,))
+    w, pw = _param(w, "w", (D,))
     if w is None:
         raise ValueError("w must be (D,)")
-    M = x.numel() // D if D else 0
-    return x, ldx, z, ldz, w, _param(bias, "bias", (D,)), gate, M, D
+    bias, pb = _param(bias, "bias", (D,))
+    return (x, z, w, bias), (px, ldx, pz, ldz, _DT[x.dtype], pw, pb), gate, x.numel() // D if D else 0, D
 
 
-@_on_stream
 def mg_group_norm_fwd(x, w, bias=None, z=None, *, groups=1, eps=1e-5, rms=False, gate_first=False,
-                      act="silu", out=None):
+                      act="silu", out=None, stream=None):
     """(y, stats): each row of x (..., D) in `groups` groups of neighbouring
     channels, each normalised by itself (rms: without taking the mean out),
     o = n w + bias; y = o act(z), or with gate_first the norm is of x act(z)
     and y = o, or without z y = act(o).  act "silu" or None; groups of at most
     16384 channels.  stats (rows, groups, 2) is for mg_group_norm_bwd."""
-    x, ldx, z, ldz, w, bias, gate, M, D = _norm_args(x, w, bias, z, groups, gate_first)
-    y = _out(out, 0, x.shape, x, x.dtype)
-    stats = _out(out, 1, (M, groups, 2), x)
-    _check(load().mg_group_norm_fwd(_ptr(x), ldx, _ptr(z), ldz, _DT[x.dtype], _ptr(w), _ptr(bias),
-                                    float(eps), int(bool(rms)), gate, _silu(act), _ptr(y),
-                                    _ptr(stats), M, D, groups, _stream_handle(None, x.device)),
-           "mg_group_norm_fwd")
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mg_group_norm_fwd(x, w, bias, z, groups=groups, eps=eps, rms=rms,
+                                     gate_first=gate_first, act=act, out=out)
+    keep, words, gate, M, D = _norm_args(x, w, bias, z, groups, gate_first)
+    x = keep[0]
+    y, py = _new(out, 0, x.shape, x, x.dtype)
+    stats, pst = _new(out, 1, (M, groups, 2), x, _F32)
+    _run("mg_group_norm_fwd", *words, float(eps), 1 if rms else 0, gate, _silu(act), py, pst, M, D, groups,
+         _stream(x))
     return y, stats
 
 
-@_on_stream
 def mg_group_norm_bwd(dy, stats, x, w, bias=None, z=None, *, groups=1, eps=1e-5, rms=False,
-                      gate_first=False, act="silu", out=None, ws=None):
+                      gate_first=False, act="silu", out=None, ws=None, stream=None):
     """(dx, dw, dbias, dz): gradients of sum(dy*y) for mg_group_norm_fwd on the
     same inputs, with the stats that it returned (eps is in them already);
     dbias and dz are None without bias and z."""
-    x, ldx, z, ldz, w, bias, gate, M, D = _norm_args(x, w, bias, z, groups, gate_first)
-    dy, lddy = _rows(dy, "dy", (x.dtype,))
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return mg_group_norm_bwd(dy, stats, x, w, bias, z, groups=groups, eps=eps, rms=rms,
+                                     gate_first=gate_first, act=act, out=out, ws=ws)
+    keep, words, gate, M, D = _norm_args(x, w, bias, z, groups, gate_first)
+    x, ty = keep[0], keep[0].dtype
+    dy, pdy, lddy = _rows(dy, "dy", (ty,))
     if dy.shape != x.shape:
         raise ValueError("dy must have x's shape")
-    stats = _param(stats, "stats", (M, groups, 2))
     if stats is None:
         raise ValueError("stats must be what mg_group_norm_fwd returned")
-    dx = _out(out, 0, x.shape, x, x.dtype)
-    dw = _out(out, 1, (D,), x)
-    dbias = _out(out, 2, (D,), x) if bias is not None else None
-    dz = _out(out, 3, x.shape, x, x.dtype) if z is not None else None
-    sh = _stream_handle(None, x.device)
-    lib = load()
-    wk = _workspace(lib.mg_group_norm_workspace_size(M, D, groups), x.device, sh, ws)
-    _check(lib.mg_group_norm_bwd(_ptr(dy), lddy, _ptr(stats), _ptr(x), ldx, _ptr(z), ldz,
-                                 _DT[x.dtype], _ptr(w), _ptr(bias), int(bool(rms)), gate, _silu(act),
-                                 _ptr(dx), _ptr(dz), _ptr(dw), _ptr(dbias), M, D, groups,
-                                 wk.data_ptr(), wk.numel(), sh),
-           "mg_group_norm_bwd")
+    stats, pst = _param(stats, "stats", (M, groups, 2))
+    dx, pdx = _new(out, 0, x.shape, x, ty)
+    dw, pdw = _new(out, 1, (D,), x, _F32)
+    dbias, pdb = _new(out, 2, (D,), x, _F32) if bias is not None else (None, 0)
+    dz, pdz = _new(out, 3, x.shape, x, ty) if z is not None else (None, 0)
+    sh = _stream(x)
+    _run_ws("mg_group_norm_bwd", lambda: load().mg_group_norm_workspace_size(M, D, groups), x.device, ws,
+            (pdy, lddy, pst, *words, 1 if rms else 0, gate, _silu(act), pdx, pdz, pdw, pdb, M, D, groups), sh)
     return dx, dw, dbias, dz
 
 
