@@ -20,17 +20,24 @@ constexpr int kMaxTeam = 1024;
 
 constexpr int kAhead = 3;   // rows in flight for a thread
 
-// Sum of v over each team; every thread of the team gets it.  buf: one float
-// for each warp of the block, and not the one of the call before (whose
-// readers this call's barrier waits for).  All threads of the block call it.
+// Sum of v over each team; every thread of the team gets it.  TEAM: the team's
+// size where it is known when compiled, kAny for any size, kBlock for whole
+// warps.  buf: one float for each warp of the block, and not the one of the
+// call before (whose readers this call's barrier waits for).  All threads of
+// the block call it.  (With the size as an argument alone, the two sums of a
+// row took 100 of its 290 instructions.)
+constexpr int kAny = 0, kBlock = -1;
+template <int TEAM>
 __device__ __forceinline__ float team_sum(float v, int tpg, float *buf)
 {
+    if constexpr (TEAM > 0) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        const float w = __shfl_xor_sync(~0u, v, o);
-        if (o < tpg) v += w;
+        for (int o = TEAM / 2; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+        return v;
     }
-    if (tpg <= 32) return v;
+    const int in_warp = TEAM == kBlock || tpg > 32 ? 32 : tpg;
+    for (int o = in_warp / 2; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    if (TEAM == kAny && tpg <= 32) return v;
     const int warp = threadIdx.x >> 5, per = tpg >> 5, first = warp / per * per;
     if ((threadIdx.x & 31) == 0) buf[warp] = v;
     __syncthreads();
@@ -134,10 +141,12 @@ struct Team {
     }
 };
 
-template <typename T, int VEC, int NV, mg_gate GATE>
+// SILU: 1 where the activation is known to be SiLU when compiled, else -1.
+template <typename T, int VEC, int NV, mg_gate GATE, int TEAM, int SILU>
 __global__ void __launch_bounds__(NV == 16 ? kMaxTeam : 512, NV == 1 ? 2 : 1)
-norm_fwd_kernel(NormArgs p, int tpg, int row_teams)
+norm_fwd_kernel(NormArgs p, int team_size, int row_teams)
 {
+    const int tpg = TEAM > 0 ? TEAM : team_size, silu = SILU == 1 ? 1 : p.silu;
     constexpr int K = GATE == MG_GATE_NONE ? 1 : 2;
     __shared__ float buf[2][32];
     extern __shared__ __align__(16) unsigned char ring[];
@@ -182,12 +191,15 @@ norm_fwd_kernel(NormArgs p, int tpg, int row_teams)
         cp_async_commit();
     };
     const float inv = 1.f / float(gs);
+    const bool writes_stats = team.lane == 0 && p.stats != nullptr;
+    float2 *stats = reinterpret_cast<float2 *>(p.stats) + (int64_t(team.slot) * p.G + team.g);
+    const int64_t ss = row_teams * p.G;
 #pragma unroll
     for (int k = 0; k < kAhead - 1; ++k) fetch(k);
     const int rounds = (M - 1) / row_teams + 1;   // the same for every team
     int slot = 0;
     int64_t row = team.slot;
-    for (int k = 0; k < rounds; ++k, row += row_teams) {
+    for (int k = 0; k < rounds; ++k, row += row_teams, stats += ss) {
         fetch(slot == 0 ? kAhead - 1 : slot - 1);
         cp_async_wait<kAhead - 1>();
         const bool live = row < M;
@@ -198,13 +210,13 @@ norm_fwd_kernel(NormArgs p, int tpg, int row_teams)
             f[i] = vset<VEC>(0.f);
             if (in[i] && live) {
                 f[i] = ahead.get(slot, 0, i, x + c[i]);
-                if (K == 2) gate[i] = vact<VEC>(ahead.get(slot, 1, i, z + c[i]), p.silu);
+                if (K == 2) gate[i] = vact<VEC>(ahead.get(slot, 1, i, z + c[i]), silu);
                 if (GATE == MG_GATE_FIRST) f[i] = vmul<VEC>(f[i], gate[i]);
                 sum += vsum<VEC>(f[i]);
             }
         }
         float mean = 0.f;
-        if (!p.rms) mean = team_sum(sum, tpg, buf[0]) * inv;
+        if (!p.rms) mean = team_sum<TEAM>(sum, tpg, buf[0]) * inv;
         float sq = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -213,18 +225,15 @@ norm_fwd_kernel(NormArgs p, int tpg, int row_teams)
                 sq += vdot<VEC>(f[i], f[i]);
             }
         // (one sum a row: the buffers take turns)
-        const float rstd = rsqrtf(fmaf(team_sum(sq, tpg, buf[p.rms ? k & 1 : 1]), inv, p.eps));
+        const float rstd = rsqrtf(fmaf(team_sum<TEAM>(sq, tpg, buf[p.rms ? k & 1 : 1]), inv, p.eps));
         if (live && team.live) {
-            if (team.lane == 0 && p.stats != nullptr) {
-                const int64_t u = row * p.G + team.g;
-                *reinterpret_cast<float2 *>(p.stats + 2 * u) = make_float2(mean, rstd);
-            }
+            if (writes_stats) *stats = make_float2(mean, rstd);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (in[i]) {
                     Lanes<VEC> o = vfma<VEC>(vmul<VEC>(f[i], vset<VEC>(rstd)), w[i], b[i]);
                     if (GATE == MG_GATE_AFTER) o = vmul<VEC>(o, gate[i]);
-                    if (GATE == MG_GATE_NONE) o = vact<VEC>(o, p.silu);
+                    if (GATE == MG_GATE_NONE) o = vact<VEC>(o, silu);
                     float v[VEC];
                     vto<VEC>(o, v);
                     store_out<VEC>(y + c[i], v);
@@ -242,10 +251,11 @@ norm_fwd_kernel(NormArgs p, int tpg, int row_teams)
 //   dp = rstd (dn - mean(dn) - n mean(dn n))    (rms: without mean(dn))
 // and the gate's chain rule around it.  dw and dbias are summed over a team's
 // rows in registers; the teams' sums are added in order by sum_parts_kernel.
-template <typename T, int VEC, int NV, mg_gate GATE>
+template <typename T, int VEC, int NV, mg_gate GATE, int TEAM, int SILU>
 __global__ void __launch_bounds__(NV == 16 ? kMaxTeam : 512)
-norm_bwd_kernel(NormArgs p, int tpg, int row_teams, float *part)
+norm_bwd_kernel(NormArgs p, int team_size, int row_teams, float *part)
 {
+    const int tpg = TEAM > 0 ? TEAM : team_size, silu = SILU == 1 ? 1 : p.silu;
     constexpr int K = GATE == MG_GATE_NONE ? 2 : 3;
     __shared__ float buf[2][32];
     extern __shared__ __align__(16) unsigned char ring[];
@@ -296,13 +306,15 @@ norm_bwd_kernel(NormArgs p, int tpg, int row_teams, float *part)
 #pragma unroll
     for (int k = 0; k < kAhead - 1; ++k) fetch(k);
     const int rounds = (M - 1) / row_teams + 1;   // the same for every team
+    const float2 *stats = reinterpret_cast<const float2 *>(p.stats_in) + (int64_t(team.slot) * p.G + team.g);
+    const int64_t ss = row_teams * p.G;
     int slot = 0;
     int64_t row = team.slot;
-    for (int k = 0; k < rounds; ++k, row += row_teams) {
+    for (int k = 0; k < rounds; ++k, row += row_teams, stats += ss) {
         fetch(slot == 0 ? kAhead - 1 : slot - 1);
         const bool live = team.live && row < M;
         float2 st = make_float2(0.f, 0.f);
-        if (live) st = *reinterpret_cast<const float2 *>(p.stats_in + 2 * (row * p.G + team.g));
+        if (live) st = *stats;
         cp_async_wait<kAhead - 1>();
         const Lanes<VEC> rstd = vset<VEC>(st.y);
         Lanes<VEC> n[NV], dn[NV], ga[NV], gg[NV];
@@ -311,7 +323,7 @@ norm_bwd_kernel(NormArgs p, int tpg, int row_teams, float *part)
         for (int i = 0; i < NV; ++i)
             if (live && in[i]) {
                 Lanes<VEC> pv = ahead.get(slot, 0, i, x + c[i]), dov = ahead.get(slot, 1, i, dy + c[i]);
-                if (K == 3) ga[i] = vact<VEC>(ahead.get(slot, K - 1, i, z + c[i]), p.silu, gg[i]);
+                if (K == 3) ga[i] = vact<VEC>(ahead.get(slot, K - 1, i, z + c[i]), silu, gg[i]);
                 if (GATE == MG_GATE_FIRST) {
                     gg[i] = vmul<VEC>(gg[i], pv);
                     pv = vmul<VEC>(pv, ga[i]);
@@ -327,7 +339,7 @@ norm_bwd_kernel(NormArgs p, int tpg, int row_teams, float *part)
                         dov = vmul<VEC>(dov, ga[i]);
                     } else {
                         Lanes<VEC> grad;
-                        vact<VEC>(o, p.silu, grad);
+                        vact<VEC>(o, silu, grad);
                         dov = vmul<VEC>(dov, grad);
                     }
                 }
@@ -337,8 +349,8 @@ norm_bwd_kernel(NormArgs p, int tpg, int row_teams, float *part)
                 m1 += vsum<VEC>(dn[i]);
                 m2 += vdot<VEC>(dn[i], n[i]);
             }
-        m1 = p.rms ? 0.f : team_sum(m1, tpg, buf[0]) * inv;
-        m2 = team_sum(m2, tpg, buf[p.rms ? k & 1 : 1]) * inv;
+        m1 = p.rms ? 0.f : team_sum<TEAM>(m1, tpg, buf[0]) * inv;
+        m2 = team_sum<TEAM>(m2, tpg, buf[p.rms ? k & 1 : 1]) * inv;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (live && in[i]) {
@@ -422,28 +434,53 @@ int64_t row_teams_for(int64_t M, int64_t G, int tpg, int warps)
 }
 constexpr int kFwdWarps = 32, kBwdWarps = 16;   // what an SM holds by the kernels' registers
 
-template <typename T, int VEC, int NV, mg_gate GATE>
-mg_status norm_fwd_gate(const NormArgs &p, int tpg, cudaStream_t s)
+template <typename T, int VEC, int NV, mg_gate GATE, int TEAM, int SILU>
+mg_status norm_fwd_team(const NormArgs &p, int tpg, cudaStream_t s)
 {
     const int block = tpg > kNormBlock ? tpg : kNormBlock;
     const int64_t rt = row_teams_for(p.M, p.G, tpg, kFwdWarps);
     const size_t smem = Ahead<T, VEC, NV, GATE == MG_GATE_NONE ? 1 : 2>::bytes(block);
-    MG_TRY(allow_shared<norm_fwd_kernel<T, VEC, NV, GATE>>(smem));
-    norm_fwd_kernel<T, VEC, NV, GATE><<<unsigned(ceil_div(rt * p.G, block / tpg)), block, smem, s>>>(p, tpg, int(rt));
+    MG_TRY(allow_shared<norm_fwd_kernel<T, VEC, NV, GATE, TEAM, SILU>>(smem));
+    norm_fwd_kernel<T, VEC, NV, GATE, TEAM, SILU><<<unsigned(ceil_div(rt * p.G, block / tpg)), block, smem, s>>>(
+        p, tpg, int(rt));
     return launched("mg_group_norm_fwd");
 }
 
-template <typename T, int VEC, int NV, mg_gate GATE>
-mg_status norm_bwd_gate(const NormArgs &p, int tpg, cudaStream_t s)
+template <typename T, int VEC, int NV, mg_gate GATE, int TEAM, int SILU>
+mg_status norm_bwd_team(const NormArgs &p, int tpg, cudaStream_t s)
 {
     const int block = tpg > kNormBlock ? tpg : kNormBlock;
     const int64_t rt = row_teams_for(p.M, p.G, tpg, kBwdWarps);
     float *part = reinterpret_cast<float *>(static_cast<char *>(p.ws) + kControlBytes);
     const size_t smem = Ahead<T, VEC, NV, GATE == MG_GATE_NONE ? 2 : 3>::bytes(block);
-    MG_TRY(allow_shared<norm_bwd_kernel<T, VEC, NV, GATE>>(smem));
-    norm_bwd_kernel<T, VEC, NV, GATE><<<unsigned(ceil_div(rt * p.G, block / tpg)), block, smem, s>>>(p, tpg, int(rt), part);
+    MG_TRY(allow_shared<norm_bwd_kernel<T, VEC, NV, GATE, TEAM, SILU>>(smem));
+    norm_bwd_kernel<T, VEC, NV, GATE, TEAM, SILU><<<unsigned(ceil_div(rt * p.G, block / tpg)), block, smem, s>>>(
+        p, tpg, int(rt), part);
     MG_TRY(launched("mg_group_norm_bwd"));
     return launch_sum_parts(part, rt, {{p.dw, p.D}, {p.dbias, p.D}}, s);
+}
+
+// Groups of one vector a thread, gated or activated by SiLU, have kernels for
+// their team's size; the rest share one for any size.
+#define MG_NORM_TEAM(F)                                                              \
+    if constexpr (NV == 1 && VEC > 1) {                                              \
+        if (p.silu) {                                                                \
+            if (tpg == 8) return F<T, VEC, NV, GATE, 8, 1>(p, tpg, s);               \
+            if (tpg == 16) return F<T, VEC, NV, GATE, 16, 1>(p, tpg, s);             \
+            if (tpg == 32) return F<T, VEC, NV, GATE, 32, 1>(p, tpg, s);             \
+            if (tpg > 32) return F<T, VEC, NV, GATE, kBlock, 1>(p, tpg, s);          \
+        }                                                                            \
+    }                                                                                \
+    return F<T, VEC, NV, GATE, kAny, -1>(p, tpg, s);
+template <typename T, int VEC, int NV, mg_gate GATE>
+mg_status norm_fwd_gate(const NormArgs &p, int tpg, cudaStream_t s)
+{
+    MG_NORM_TEAM(norm_fwd_team)
+}
+template <typename T, int VEC, int NV, mg_gate GATE>
+mg_status norm_bwd_gate(const NormArgs &p, int tpg, cudaStream_t s)
+{
+    MG_NORM_TEAM(norm_bwd_team)
 }
 
 template <typename T, int VEC, int NV>

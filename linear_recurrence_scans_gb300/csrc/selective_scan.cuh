@@ -176,7 +176,7 @@ struct RowTime {
     }
 };
 
-constexpr int64_t kMinChunk = 128;   // rows
+constexpr int64_t kMinChunk = 32;   // rows
 constexpr double kFoldNs = 500;      // a launch and a step of the fold over chunks
 
 // Cuts T rows into chunks for `blocks` blocks a chunk, so that the two passes
