@@ -54,30 +54,24 @@ struct alignas(16) FwdShared {   // of a warp
     float y[kFirst ? 1 : kRows][kFirst ? 4 : WCH];
     float bias[WCH], skip[WCH];
     // as loaded: x, raw, and B (and C)
-    T raw[VEC > 1 ? kRing : 1][2][VEC > 1 ? kRows : 1][WCH];
-    T rawbc[VEC > 1 ? kRing : 1][VEC > 1 ? kRows : 1][kBc][VEC > 1 ? NP : VEC];
+    T raw[kRing][2][kRows][VEC > 1 ? WCH : Words<T, WCH>::kPitch];
+    alignas(16) T rawbc[kRing][kRows][kBc][NP];
 };
-
-// 16 bytes, or 16 zero bytes.
-__device__ __forceinline__ void cp_async16_or_zero(void *dst, const void *src, bool in)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" : : "r"(smem_addr(dst)), "l"(src), "r"(in ? 16 : 0)
-                 : "memory");
-}
 
 template <typename T, int VEC, typename CV, ChunkPass kPass>
 __global__ void __launch_bounds__(kThreads, 3)
-ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg_s, int bc_wide)
+ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg_s, int mode)
 {
     constexpr bool kFirst = kPass != kOutputs, kBack = kPass == kAdjoint;
     constexpr int S = CV::S, L = CV::L, C = CV::C, NP = CV::NP, SP = S / 2, WCH = CV::kWarpCh;
     constexpr int kBc = kFirst ? 1 : 2;
-    constexpr int kCols = WCH / VEC;                   // vectors of a row
-    constexpr int kStep = 32 / kCols;                  // rows between a lane's vectors
+    // A lane's part of staging: kPer pieces of VEC channels, kStep rows apart.
+    constexpr int kCols = WCH / VEC, kStep = 32 / kCols;
     constexpr int kPer = kStep < kRows ? kRows / kStep : 1;
-    constexpr int kBcVecs = VEC > 1 ? kRows * kBc * NP / VEC : 0;   // vectors of B (and C) of a stage
-    constexpr int kBcPer = (kBcVecs + 31) / 32;
-    static_assert(C == 2 && WCH % VEC == 0 && NP % VEC == 0 && kCols <= 32, "staging");
+    constexpr int kCv = 16 / int(sizeof(T));                        // values of a vector of B or C
+    constexpr int kBcCols = NP / kCv, kBcVecs = kRows * kBc * kBcCols, kBcPer = (kBcVecs + 31) / 32;
+    constexpr int kBcW = kRows * kBc * NP * int(sizeof(T)) / 4, kRowW = NP * int(sizeof(T)) / 4;
+    static_assert(C == 2 && WCH % VEC == 0 && kCols <= 32 && (VEC > 1 || kPer % 2 == 0), "staging");
     using Shared = FwdShared<T, VEC, WCH, NP, kFirst>;
     extern __shared__ __align__(16) unsigned char shared_bytes[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -105,8 +99,9 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
     const int64_t ldx = kBack ? -p.lddy : p.ldx, ldr = kBack ? -p.ldraw : p.ldraw;
     const int64_t ldb = kBack ? -p.ldc : p.ldb, ldc = p.ldc;
     const int64_t rf = rowb + (kBack ? t1 - 1 : t0);   // the chunk's first row in that order
-    const T *xp = static_cast<const T *>(kBack ? p.dy : p.x) + rf * (kBack ? p.lddy : p.ldx) + row0 * ldx + d0 + col;
-    const T *rp = static_cast<const T *>(p.raw) + rf * p.ldraw + row0 * ldr + d0 + col;
+    const T *x0p = static_cast<const T *>(kBack ? p.dy : p.x), *r0p = static_cast<const T *>(p.raw);
+    const int64_t xf = rf * (kBack ? p.lddy : p.ldx) + d0, rawf = rf * p.ldraw + d0;   // its first values
+    const T *xp = x0p + xf + row0 * ldx + col, *rp = r0p + rawf + row0 * ldr + col;
     const int64_t xs = kStep * ldx, rs = kStep * ldr;
     const T *bp = static_cast<const T *>(kBack ? p.Cm : p.Bm) + rf * (kBack ? p.ldc : p.ldb) + int64_t(g) * p.N;
     const T *cp = static_cast<const T *>(p.Cm) + rf * p.ldc + int64_t(g) * p.N;
@@ -123,17 +118,27 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
                     cp_async16_or_zero(&sm.raw[slot][1][row0 + i * kStep][col], in ? rp + at * ldr + i * rs : p.raw, in);
                 }
             }
-            if (bc_wide) {
+        } else {
+            fetch_words<T, WCH, kRows>(sm.raw[slot][0], x0p, xf + at * ldx, ldx, rows - at, wide, lane);
+            fetch_words<T, WCH, kRows>(sm.raw[slot][1], r0p, rawf + at * ldr, ldr, rows - at, wide, lane);
+        }
+        if (mode == kBcVectors) {
 #pragma unroll
-                for (int i = 0; i < kBcPer; ++i) {
-                    const int v = lane + i * 32, n = v % (NP / VEC) * VEC, which = v / (NP / VEC) % kBc;
-                    const int row = v / (NP / VEC) / kBc;
-                    const bool in = at + row < rows && n < p.N;
-                    const void *src = !in          ? p.Bm
-                                      : which == 0 ? static_cast<const void *>(bp + (at + row) * ldb + n)
-                                                   : static_cast<const void *>(cp + (at + row) * ldc + n);
-                    if (kBcVecs % 32 == 0 || v < kBcVecs) cp_async16_or_zero(&sm.rawbc[slot][row][which][n], src, in);
-                }
+            for (int i = 0; i < kBcPer; ++i) {
+                const int v = lane + i * 32, n = v % kBcCols * kCv, which = v / kBcCols % kBc, row = v / kBcCols / kBc;
+                const bool in = at + row < rows && n < p.N;
+                const void *src = !in          ? p.Bm
+                                  : which == 0 ? static_cast<const void *>(bp + (at + row) * ldb + n)
+                                               : static_cast<const void *>(cp + (at + row) * ldc + n);
+                if (kBcVecs % 32 == 0 || v < kBcVecs) cp_async16_or_zero(&sm.rawbc[slot][row][which][n], src, in);
+            }
+        } else if (mode == kBcWords) {
+#pragma unroll 4
+            for (int v = lane; v < kBcW; v += 32) {
+                const int n = v % kRowW * (4 / int(sizeof(T))), which = v / kRowW % kBc, row = v / kRowW / kBc;
+                const bool in = at + row < rows && n < p.N;
+                const T *src = which == 0 ? bp + (at + row) * ldb + n : cp + (at + row) * ldc + n;
+                cp_async4(&sm.rawbc[slot][row][which][n], in ? static_cast<const void *>(src) : p.Bm, in ? 4 : 0);
             }
         }
         cp_async_commit();
@@ -209,69 +214,94 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
 
     // The next stage's staged values, from what the copies brought: computed
     // (convert) and written to buffer `to` (put) apart from each other.
-    pair_t dl[kPer][(VEC + 1) / 2], uu[kPer][(VEC + 1) / 2];
-    float bcv[kBcPer > 0 ? kBcPer : 1][VEC];
+    constexpr int kPairs = kPer * VEC / 2;   // of channels, or (VEC = 1) of a channel's rows
+    pair_t dl[kPairs], uu[kPairs];
+    float bcv[kBcPer][kCv];
+    // parity of the rows' first values, for the words' shifts
+    const int xpar = int(xf & 1), xstep = int(ldx & 1), rpar = int(rawf & 1), rstep = int(ldr & 1);
+    auto word_value = [&](const T *row_words, int shift) { return load1(row_words + shift + col); };
     auto convert = [&](int at, int slot) {
+        if constexpr (VEC > 1) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const bool in = col_in && at + row0 + i * kStep < rows;
-            float xv[VEC], rv[VEC], bias[VEC];
-            if constexpr (VEC > 1) {
+            for (int i = 0; i < kPer; ++i) {
+                const bool in = col_in && at + row0 + i * kStep < rows;
+                float xv[VEC], rv[VEC], bias[VEC];
                 load_vec<VEC>(&sm.raw[slot][0][(row0 + i * kStep) % kRows][col], xv);
                 load_vec<VEC>(&sm.raw[slot][1][(row0 + i * kStep) % kRows][col], rv);
                 load_vec<VEC>(&sm.bias[col], bias);
 #pragma unroll
                 for (int e = 0; e < VEC; e += 2) {
                     const pair_t r = add2(pack2(rv[e], rv[e + 1]), pack2(bias[e], bias[e + 1]));
-                    const pair_t sp = softplus2(r);
-                    dl[i][e / 2] = !in ? 0 : p.softplus ? sp : r;
-                    const pair_t xx = pack2(xv[e], xv[e + 1]);
-                    uu[i][e / 2] = kBack ? xx : mul2(dl[i][e / 2], xx);
+                    const pair_t sp = softplus2(r), xx = pack2(xv[e], xv[e + 1]);
+                    const pair_t d = !in ? 0 : p.softplus ? sp : r;
+                    dl[(i * VEC + e) / 2] = d;
+                    uu[(i * VEC + e) / 2] = kBack ? xx : mul2(d, xx);
                 }
-            } else {
-                const float r = in ? load1(rp + at * ldr + i * rs) + sm.bias[col] : 0.f;
-                const float delta = !in ? 0.f : p.softplus ? softplus_f(r) : r;
-                const float xv1 = in ? load1(xp + at * ldx + i * xs) : 0.f;
-                dl[i][0] = pack2(delta, kBack ? xv1 : delta * xv1);
+            }
+        } else {
+            const float bias = sm.bias[col];
+#pragma unroll
+            for (int i = 0; i < kPer; i += 2) {
+                const int a = row0 + i * kStep, b = a + kStep;
+                const bool in0 = col_in && at + a < rows, in1 = col_in && at + b < rows;
+                const int sx = sizeof(T) == 4 ? 0 : 1, ra = at + a, rb = at + b;
+                const float r0 = word_value(sm.raw[slot][1][a % kRows], sx & (rpar ^ (ra & rstep)));
+                const float r1 = word_value(sm.raw[slot][1][b % kRows], sx & (rpar ^ (rb & rstep)));
+                const float x0 = word_value(sm.raw[slot][0][a % kRows], sx & (xpar ^ (ra & xstep)));
+                const float x1 = word_value(sm.raw[slot][0][b % kRows], sx & (xpar ^ (rb & xstep)));
+                const pair_t r = add2(pack2(r0, r1), pack2(bias, bias)), sp = softplus2(r);
+                float d0v, d1v;
+                unpack2(p.softplus ? sp : r, d0v, d1v);
+                const pair_t d = pack2(in0 ? d0v : 0.f, in1 ? d1v : 0.f);
+                // (a channel past the group reads a neighbour's or stale values)
+                const pair_t xx = pack2(in0 ? x0 : 0.f, in1 ? x1 : 0.f);
+                dl[i / 2] = d;
+                uu[i / 2] = kBack ? xx : mul2(d, xx);
             }
         }
-        if constexpr (VEC > 1) {
+        if (mode != kBcValues) {
 #pragma unroll
             for (int i = 0; i < kBcPer; ++i) {
-                const int v = lane + i * 32, n = v % (NP / VEC) * VEC, which = v / (NP / VEC) % kBc;
+                const int v = lane + i * 32;
                 if (kBcVecs % 32 == 0 || v < kBcVecs)
-                    load_vec<VEC>(&sm.rawbc[slot][v / (NP / VEC) / kBc][which][n], bcv[i]);
+                    load_vec<kCv>(&sm.rawbc[slot][v / kBcCols / kBc][v / kBcCols % kBc][v % kBcCols * kCv], bcv[i]);
             }
         }
     };
     auto put = [&](int at, int to) {
+        if (row0 < kRows) {
+            if constexpr (VEC > 1) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int row = row0 + i * kStep;
-            if (row0 < kRows) {
-                if constexpr (VEC > 1) {
+                for (int i = 0; i < kPer; ++i) {
+                    const int row = row0 + i * kStep;
 #pragma unroll
                     for (int e = 0; e < VEC; e += 2) {
                         float4 o;
-                        unpack2(dl[i][e / 2], o.x, o.z);
-                        unpack2(uu[i][e / 2], o.y, o.w);
+                        unpack2(dl[(i * VEC + e) / 2], o.x, o.z);
+                        unpack2(uu[(i * VEC + e) / 2], o.y, o.w);
                         *reinterpret_cast<float4 *>(&sm.du[to][row][du_index<WCH>(row, col + e)]) = o;
                     }
-                } else {
-                    float2 o;
-                    unpack2(dl[i][0], o.x, o.y);
-                    sm.du[to][row][du_index<WCH>(row, col)] = o;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kPer; i += 2) {
+                    const int a = row0 + i * kStep, b = a + kStep;
+                    float2 oa, ob;
+                    unpack2(dl[i / 2], oa.x, ob.x);
+                    unpack2(uu[i / 2], oa.y, ob.y);
+                    sm.du[to][a][du_index<WCH>(a, col)] = oa;
+                    sm.du[to][b][du_index<WCH>(b, col)] = ob;
                 }
             }
         }
-        if (VEC > 1 && bc_wide) {
+        if (mode != kBcValues) {
 #pragma unroll
             for (int i = 0; i < kBcPer; ++i) {
-                const int v = lane + i * 32, n = v % (NP / VEC) * VEC, which = v / (NP / VEC) % kBc;
+                const int v = lane + i * 32;
                 if (kBcVecs % 32 == 0 || v < kBcVecs)
-                    store_vec<VEC>(&sm.bc[to][v / (NP / VEC) / kBc][which][n], bcv[i]);
+                    store_vec<kCv>(&sm.bc[to][v / kBcCols / kBc][v / kBcCols % kBc][v % kBcCols * kCv], bcv[i]);
             }
-        } else {   // rows of B and C that 16-byte vectors do not fit
+        } else {
             for (int e = lane; e < kRows * kBc * NP; e += 32) {
                 const int n = e % NP, which = e / NP % kBc, row = e / NP / kBc;
                 const bool in = at + row < rows && n < p.N;
@@ -318,6 +348,7 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
 
     T *yp = static_cast<T *>(p.y) + (rowb + t0 + row0) * p.D + d0 + col;
     cp_async_wait<kRing - 1>();
+    __syncwarp();   // words are other lanes' copies
     convert(0, 0);
     put(0, 0);
     __syncwarp();
@@ -342,6 +373,7 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
             }
         };
         cp_async_wait<kRing - 2>();
+        __syncwarp();
         const int ns = slot + 1 < kRing ? slot + 1 : 0;
         if (next >= end) {   // no sequence begins inside the stage
             convert(at + kRows, ns);
@@ -395,13 +427,15 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
                     load_vec<VEC>(&sm.y[row % kRows][col], o);
                     load_vec<VEC>(&sm.skip[col], skip);
                     if constexpr (VEC > 1) load_vec<VEC>(&sm.raw[slot][0][row % kRows][col], x);
-                    else x[0] = load1(xp + at * ldx + i * xs);
+                    else x[0] = word_value(sm.raw[slot][0][row % kRows],
+                                           (sizeof(T) == 4 ? 0 : 1) & (xpar ^ ((at + row) & xstep)));
 #pragma unroll
                     for (int e = 0; e < VEC; ++e) o[e] = fmaf(skip[e], x[e], o[e]);
                     store_out<VEC>(yp + (at + i * kStep) * p.D, o);
                 }
             }
         }
+        if (VEC == 1) __syncwarp();   // the slot's x is read
         fetch(at + kRing * kRows, slot);
         __syncwarp();
         slot = ns;
@@ -546,8 +580,7 @@ mg_status fwd_cover(const SsmArgs &p, cudaStream_t s)
 {
     const Tile t{forward_tiles(p.D, p.N, p.G), p.D / p.G};
     const Chunks ck = forward_chunks(p.B, p.T, p.D, p.N, p.G);
-    // 16-byte vectors of B and C
-    const int bc_wide = VEC > 1 && p.N % VEC == 0 && p.ldb % VEC == 0 && p.ldc % VEC == 0;
+    const int mode = bc_mode<T>(p.N, p.ldb, p.ldc);
     const Seqs q = make_seqs(p.cu, p.B, p.T, p.nseq);
     float *agg_h = reinterpret_cast<float *>(static_cast<char *>(p.ws) + kControlBytes);
     float *agg_s = agg_h + p.B * (ck.n - 1) * p.D * p.N;
@@ -562,11 +595,11 @@ mg_status fwd_cover(const SsmArgs &p, cudaStream_t s)
     MG_TRY(allow_shared<ssm_chunk_kernel<T, VEC, CV, kOutputs>>(sm2));
     if (ck.n > 1) {
         ssm_chunk_kernel<T, VEC, CV, kStates><<<unsigned(tiles * (ck.n - 1)), kThreads, sm1, s>>>(
-            p, q, t, ck, agg_h, agg_s, bc_wide);
+            p, q, t, ck, agg_h, agg_s, mode);
         MG_TRY(launched("mg_selective_scan_fwd"));
     }
     ssm_chunk_kernel<T, VEC, CV, kOutputs><<<unsigned(tiles * ck.n), kThreads, sm2, s>>>(p, q, t, ck, agg_h, agg_s,
-                                                                                    bc_wide);
+                                                                                    mode);
     return launched("mg_selective_scan_fwd");
 }
 
@@ -574,12 +607,12 @@ template <typename T, int VEC, typename CV>
 mg_status adjoint_cover(const SsmArgs &p, const Chunks &ck, float *agg_q, float *agg_s, cudaStream_t s)
 {
     const Tile t{forward_tiles(p.D, p.N, p.G), p.D / p.G};
-    const int bc_wide = VEC > 1 && p.N % VEC == 0 && p.ldc % VEC == 0;
+    const int mode = bc_mode<T>(p.N, p.ldc, p.ldc);
     const Seqs q = make_seqs(p.cu, p.B, p.T, p.nseq);
     constexpr size_t sm = kThreads / 32 * sizeof(FwdShared<T, VEC, CV::kWarpCh, CV::NP, true>);
     MG_TRY(allow_shared<ssm_chunk_kernel<T, VEC, CV, kAdjoint>>(sm));
     ssm_chunk_kernel<T, VEC, CV, kAdjoint><<<unsigned(t.tiles * p.G * p.B * (ck.n - 1)), kThreads, sm, s>>>(
-        p, q, t, ck, agg_q, agg_s, bc_wide);
+        p, q, t, ck, agg_q, agg_s, mode);
     return launched("mg_selective_scan_bwd");
 }
 

@@ -159,6 +159,60 @@ __device__ __forceinline__ void store_pairs(float *p, int n0, int N, const pair_
     store_group<S>(p, n0, N, o);
 }
 
+// ------------------------------------------------- rows of any alignment
+// A row segment of WCH channels that 16-byte copies do not fit arrives as
+// 4-byte words from the one that holds its first value; with 2-byte values
+// that value may be a word's upper half (the shift).
+template <typename T, int WCH>
+struct Words {
+    static constexpr int kWords = sizeof(T) == 4 ? WCH : WCH / 2 + 1;
+    static constexpr int kPitch = kWords * 4 / int(sizeof(T));   // values
+};
+
+// `bytes` (0, 2 or 4) of a 4-byte word, the rest zero.
+__device__ __forceinline__ void cp_async4(void *dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" : : "r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+}
+
+// Starts the copies of the words of ROWS row segments: row r's first channel
+// is value first + r * ld of base, its channels `wide`, and rows from `rows`
+// on are zero.  A word past the last channel's value is not read beyond it.
+template <typename T, int WCH, int ROWS>
+__device__ __forceinline__ void fetch_words(T (*dst)[Words<T, WCH>::kPitch], const T *base, int64_t first, int64_t ld,
+                                            int rows, int wide, int lane)
+{
+    constexpr int kWords = Words<T, WCH>::kWords, kPer = (ROWS * kWords + 31) / 32;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int v = lane + i * 32, row = v / kWords, w = v % kWords;
+        if (ROWS * kWords % 32 == 0 || v < ROWS * kWords) {
+            const int64_t at = first + row * ld;
+            const int shift = sizeof(T) == 4 ? 0 : int(at & 1), per = 4 / int(sizeof(T));
+            const int c = w * per - shift;   // the word's first value, as a channel
+            const int bytes = row >= rows || c >= wide ? 0 : c + per <= wide ? 4 : int(sizeof(T));
+            cp_async4(reinterpret_cast<unsigned *>(dst[row]) + w, bytes > 0 ? base + at + c : base, bytes);
+        }
+    }
+}
+
+// How rows of B and C are read: value by value, by 4 bytes, by 16 bytes.
+enum BcMode { kBcValues, kBcWords, kBcVectors };
+template <typename T>
+inline int bc_mode(int N, int64_t ldb, int64_t ldc)
+{
+    const int per16 = 16 / int(sizeof(T)), per4 = 4 / int(sizeof(T));
+    if (N % per16 == 0 && ldb % per16 == 0 && ldc % per16 == 0) return kBcVectors;
+    return N % per4 == 0 && ldb % per4 == 0 && ldc % per4 == 0 ? kBcWords : kBcValues;
+}
+
+// 16 bytes, or 16 zero bytes.
+__device__ __forceinline__ void cp_async16_or_zero(void *dst, const void *src, bool in)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" : : "r"(smem_addr(dst)), "l"(src), "r"(in ? 16 : 0)
+                 : "memory");
+}
+
 // ---------------------------------------------------------- host side
 
 constexpr int64_t kSms = 152;

@@ -164,8 +164,8 @@ struct BwdWarp {
     float bc[kTile][2][NP];
     float4 ck[kTile / kSub][4][32];                // states before each kSub rows, by lane
     float bias[WCH];
-    T raw[3][VEC > 1 ? kTile : 1][WCH];            // the next tile's x, raw, dy as loaded
-    T rawbc[VEC > 1 ? kTile : 1][2][VEC > 1 ? NP : 8];
+    T raw[3][kTile][VEC > 1 ? WCH : Words<T, WCH>::kPitch];   // the next tile's x, raw, dy as loaded
+    alignas(16) T rawbc[kTile][2][NP];
 };
 template <typename T, int VEC, typename CV>
 struct alignas(16) BwdShared {
@@ -177,12 +177,13 @@ struct alignas(16) BwdShared {
 template <typename T, int VEC, typename CV>
 __global__ void __launch_bounds__(CV::THREADS, 2)
 ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const float *agg_s,
-               float *partB, float *partA, int bc_wide)
+               float *partB, float *partA, int mode)
 {
     constexpr int S = CV::S, L = CV::L, NP = CV::NP, CH = CV::kCh, WCH = CV::kWarpCh, kWarps = CV::THREADS / 32;
     constexpr int kCols = WCH / VEC, kVecs = kTile * kCols, kPer = (kVecs + 31) / 32;
-    constexpr int kBcCols = NP >= VEC ? NP / VEC : 1;            // vectors of a row of B or C
-    constexpr int kBcVecs = VEC > 1 ? kTile * 2 * kBcCols : 0, kBcPer = (kBcVecs + 31) / 32;
+    constexpr int kCv = NP < 16 / int(sizeof(T)) ? NP : 16 / int(sizeof(T));   // values of a vector of B or C
+    constexpr int kBcCols = NP / kCv, kBcVecs = kTile * 2 * kBcCols, kBcPer = (kBcVecs + 31) / 32;
+    constexpr int kRowW = NP * int(sizeof(T)) / 4, kBcW = kTile * 2 * kRowW;   // words
     constexpr int kG = CV::kGroups;
     static_assert(S == 4, "four states a thread");
     extern __shared__ __align__(16) unsigned char shared_bytes[];
@@ -240,9 +241,9 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
         }
     }
 
-    const T *xp = static_cast<const T *>(p.x) + w.rowb * p.ldx + dw;
-    const T *rp = static_cast<const T *>(p.raw) + w.rowb * p.ldraw + dw;
-    const T *yp = static_cast<const T *>(p.dy) + w.rowb * p.lddy + dw;
+    const T *x0p = static_cast<const T *>(p.x), *r0p = static_cast<const T *>(p.raw), *y0p = static_cast<const T *>(p.dy);
+    const int64_t xf = w.rowb * p.ldx + dw, rf = w.rowb * p.ldraw + dw, yf = w.rowb * p.lddy + dw;
+    const T *xp = x0p + xf, *rp = r0p + rf, *yp = y0p + yf;
     const T *bp = static_cast<const T *>(p.Bm) + w.rowb * p.ldb + int64_t(w.g) * p.N;
     const T *cp = static_cast<const T *>(p.Cm) + w.rowb * p.ldc + int64_t(w.g) * p.N;
     const int64_t nseg = (p.T + kSeg - 1) / kSeg;
@@ -258,15 +259,28 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
                     cp_async16(&sm.raw[2][row][col], yp + (t + row) * p.lddy + col);
                 }
             }
-            if (bc_wide) {
+        } else {
+            const int rows = wide > 0 ? int(w.t1 - t < kTile ? w.t1 - t : kTile) : 0;
+            fetch_words<T, WCH, kTile>(sm.raw[0], x0p, xf + t * p.ldx, p.ldx, rows, wide, lane);
+            fetch_words<T, WCH, kTile>(sm.raw[1], r0p, rf + t * p.ldraw, p.ldraw, rows, wide, lane);
+            fetch_words<T, WCH, kTile>(sm.raw[2], y0p, yf + t * p.lddy, p.lddy, rows, wide, lane);
+        }
+        if (mode == kBcVectors) {
 #pragma unroll
-                for (int i = 0; i < kBcPer; ++i) {
-                    const int v = lane + i * 32, n = v % kBcCols * VEC, which = v / kBcCols % 2;
-                    const int row = v / kBcCols / 2;
-                    if (v < kBcVecs && t + row < w.t1 && n < p.N)
-                        cp_async16(&sm.rawbc[row][which][n],
-                                   which == 0 ? bp + (t + row) * p.ldb + n : cp + (t + row) * p.ldc + n);
-                }
+            for (int i = 0; i < kBcPer; ++i) {
+                const int v = lane + i * 32, n = v % kBcCols * kCv, which = v / kBcCols % 2, row = v / kBcCols / 2;
+                const bool in = t + row < w.t1 && n < p.N;
+                const T *src = which == 0 ? bp + (t + row) * p.ldb + n : cp + (t + row) * p.ldc + n;
+                if (kCv * sizeof(T) == 16 && v < kBcVecs)
+                    cp_async16_or_zero(&sm.rawbc[row][which][n], in ? static_cast<const void *>(src) : p.Bm, in);
+            }
+        } else if (mode == kBcWords) {
+#pragma unroll 4
+            for (int v = lane; v < kBcW; v += 32) {
+                const int n = v % kRowW * (4 / int(sizeof(T))), which = v / kRowW % 2, row = v / kRowW / 2;
+                const bool in = t + row < w.t1 && n < p.N;
+                const T *src = which == 0 ? bp + (t + row) * p.ldb + n : cp + (t + row) * p.ldc + n;
+                cp_async4(&sm.rawbc[row][which][n], in ? static_cast<const void *>(src) : p.Bm, in ? 4 : 0);
             }
         }
     };
@@ -459,62 +473,79 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
         cp_async_wait<0>();
         __syncwarp();
         // the lane's vectors as float32: delta, x, dy and the slope of delta
-#pragma unroll(VEC > 1 ? kPer : 1)
-        for (int i = 0; i < kPer; ++i) {
-            const int v = lane + i * 32, row = v / kCols, col = v % kCols * VEC;
-            if (v < kVecs) {
-                float xv[VEC], rv[VEC], yv[VEC], sv[VEC];
+        if constexpr (VEC > 1) {
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) xv[e] = rv[e] = yv[e] = sv[e] = 0.f;
-                if (col < wide && t + row < w.t1) {
-                    float bias[VEC];
-                    load_vec<VEC>(&sm.bias[col], bias);
-                    if constexpr (VEC > 1) {
+            for (int i = 0; i < kPer; ++i) {
+                const int v = lane + i * 32, row = v / kCols, col = v % kCols * VEC;
+                if (v < kVecs) {
+                    float xv[VEC], rv[VEC], yv[VEC], sv[VEC];
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) xv[e] = rv[e] = yv[e] = sv[e] = 0.f;
+                    if (col < wide && t + row < w.t1) {
+                        float bias[VEC];
+                        load_vec<VEC>(&sm.bias[col], bias);
                         load_vec<VEC>(&sm.raw[0][row][col], xv);
                         load_vec<VEC>(&sm.raw[1][row][col], rv);
                         load_vec<VEC>(&sm.raw[2][row][col], yv);
-                    } else {
-                        xv[0] = load1(xp + (t + row) * p.ldx + col);
-                        rv[0] = load1(rp + (t + row) * p.ldraw + col);
-                        yv[0] = load1(yp + (t + row) * p.lddy + col);
-                    }
-                    if (p.softplus) {
-                        if constexpr (VEC > 1) {
 #pragma unroll
-                            for (int e = 0; e < VEC; e += 2) {
-                                pair_t sg;
-                                const pair_t r = add2(pack2(rv[e], rv[e + 1]), pack2(bias[e], bias[e + 1]));
-                                unpack2(softplus2(r, sg), rv[e], rv[e + 1]);
-                                unpack2(sg, sv[e], sv[e + 1]);
-                            }
-                        } else {
-                            rv[0] = softplus_f(rv[0] + bias[0], sv[0]);
+                        for (int e = 0; e < VEC; e += 2) {
+                            pair_t sg;
+                            const pair_t r = add2(pack2(rv[e], rv[e + 1]), pack2(bias[e], bias[e + 1]));
+                            const pair_t sp = softplus2(r, sg);
+                            unpack2(p.softplus ? sp : r, rv[e], rv[e + 1]);
+                            unpack2(p.softplus ? sg : dup2(1.f), sv[e], sv[e + 1]);
                         }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) rv[e] += bias[e], sv[e] = 1.f;
                     }
+                    store_vec<VEC>(&sm.d[row][col], rv);
+                    store_vec<VEC>(&sm.x[row][col], xv);
+                    store_vec<VEC>(&sm.dy[row][col], yv);
+                    store_vec<VEC>(&sm.slope[row][col], sv);
                 }
-                store_vec<VEC>(&sm.d[row][col], rv);
-                store_vec<VEC>(&sm.x[row][col], xv);
-                store_vec<VEC>(&sm.dy[row][col], yv);
-                store_vec<VEC>(&sm.slope[row][col], sv);
+            }
+        } else {   // single values, two at a time
+            static_assert(VEC > 1 || (kVecs % 64 == 0 && kPer % 2 == 0), "pairs");
+#pragma unroll 2
+            for (int i = 0; i < kPer; i += 2) {
+                float xv[2], rv[2], yv[2], sv[2], bias[2];
+                bool in[2];
+                int row[2], col[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int v = lane + (i + e) * 32;
+                    row[e] = v / kCols, col[e] = v % kCols;
+                    in[e] = col[e] < wide && t + row[e] < w.t1;
+                    auto shift = [&](int64_t first, int64_t ld) {   // of the row's words
+                        return sizeof(T) == 4 ? 0 : (int(first) ^ ((int(t) + row[e]) & int(ld))) & 1;
+                    };
+                    xv[e] = load1(&sm.raw[0][row[e]][col[e] + shift(xf, p.ldx)]);
+                    rv[e] = load1(&sm.raw[1][row[e]][col[e] + shift(rf, p.ldraw)]);
+                    yv[e] = load1(&sm.raw[2][row[e]][col[e] + shift(yf, p.lddy)]);
+                    bias[e] = sm.bias[col[e]];
+                }
+                pair_t sg;
+                const pair_t r = add2(pack2(rv[0], rv[1]), pack2(bias[0], bias[1])), sp = softplus2(r, sg);
+                unpack2(p.softplus ? sp : r, rv[0], rv[1]);
+                unpack2(p.softplus ? sg : dup2(1.f), sv[0], sv[1]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    sm.d[row[e]][col[e]] = in[e] ? rv[e] : 0.f;
+                    sm.x[row[e]][col[e]] = in[e] ? xv[e] : 0.f;
+                    sm.dy[row[e]][col[e]] = in[e] ? yv[e] : 0.f;
+                    sm.slope[row[e]][col[e]] = in[e] ? sv[e] : 0.f;
+                }
             }
         }
-        if (VEC > 1 && bc_wide) {
+        if (mode != kBcValues) {
 #pragma unroll
             for (int i = 0; i < kBcPer; ++i) {
-                const int v = lane + i * 32, n = v % kBcCols * VEC, which = v / kBcCols % 2;
-                const int row = v / kBcCols / 2;
+                const int v = lane + i * 32;
                 if (v < kBcVecs) {
-                    float o[VEC];
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) o[e] = 0.f;
-                    if (t + row < w.t1 && n < p.N) load_vec<VEC>(&sm.rawbc[row][which][n], o);
-                    store_vec<VEC>(&sm.bc[row][which][n], o);
+                    float o[kCv];
+                    load_vec<kCv>(&sm.rawbc[v / kBcCols / 2][v / kBcCols % 2][v % kBcCols * kCv], o);
+                    store_vec<kCv>(&sm.bc[v / kBcCols / 2][v / kBcCols % 2][v % kBcCols * kCv], o);
                 }
             }
-        } else {   // rows of B and C that 16-byte vectors do not fit
+        } else {
             for (int e = lane; e < kTile * 2 * NP; e += 32) {
                 const int n = e % NP, which = e / NP % 2, row = e / NP / 2;
                 const bool in = t + row < w.t1 && n < p.N;
@@ -613,8 +644,7 @@ mg_status bwd(const SsmArgs &p, cudaStream_t s)
     float *agg_q = partA + ceil_div(parts * p.D * (p.N + 2), 4) * 4;
     float *agg_s = agg_q + p.B * (ck.n - 1) * dn;
     const int64_t tiles = t.tiles * p.G * p.B;
-    // 16-byte vectors of B and C
-    const int bc_wide = VEC > 1 && p.N % VEC == 0 && p.ldb % VEC == 0 && p.ldc % VEC == 0;
+    const int mode = bc_mode<T>(p.N, p.ldb, p.ldc);
     if (p.cu != nullptr) {
         MG_TRY(launch_empty_sequences(q, p.dh0, p.dh_last, dn, p.ws, s));
     }
@@ -626,7 +656,7 @@ mg_status bwd(const SsmArgs &p, cudaStream_t s)
     static_assert(smem <= kMostShared, "shared memory of a block");
     MG_TRY(allow_shared<ssm_bwd_kernel<T, VEC, CV>>(smem));
     ssm_bwd_kernel<T, VEC, CV><<<unsigned(tiles * ck.n), CV::THREADS, smem, s>>>(p, q, t, ck, agg_q, agg_s, partB,
-                                                                             partA, bc_wide);
+                                                                             partA, mode);
     MG_TRY(launched("mg_selective_scan_bwd"));
     sum_bc_kernel<T><<<unsigned(ceil_div(rows_g * 2 * p.N, 256)), 256, 0, s>>>(
         partB, t.tiles, rows_g, p.N, static_cast<T *>(p.dBm), static_cast<T *>(p.dCm));
