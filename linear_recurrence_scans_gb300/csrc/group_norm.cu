@@ -10,13 +10,16 @@
 //
 // A team keeps its group and walks over rows: its weights stay in registers,
 // and its next rows arrive by asynchronous copies into each thread's own slots
-// of shared memory, kAhead rows ahead.  Memory bounds the kernels.
+// of shared memory, kAhead rows ahead.  Memory bounds the forward, 32768 x 4096
+// bf16 channels in one group in 134 us, 6.0 TB/s, and nearly the gradients of
+// groups that a warp holds (the same in 16 groups: 5.2 TB/s); in wider
+// groups they wait at the row's barriers (one group of 4096: 3.7 TB/s).
 #include "ssm.cuh"
 
 namespace mg {
 namespace {
 
-constexpr int kMaxTeam = 1024;
+constexpr int kMaxTeam = 512;
 
 constexpr int kAhead = 3;   // rows in flight for a thread
 
@@ -50,30 +53,22 @@ __device__ __forceinline__ float team_sum(float v, int tpg, float *buf)
 template <int VEC>
 __device__ __forceinline__ float vsum(const Lanes<VEC> &a)
 {
-    if constexpr (VEC == 1) {
-        return a.p[0];
-    } else {
-        pair_t t = a.p[0];
+    pair_t t = a.p[0];
 #pragma unroll
-        for (int i = 1; i < VEC / 2; ++i) t = add2(t, a.p[i]);
-        float x, y;
-        unpack2(t, x, y);
-        return x + y;
-    }
+    for (int i = 1; i < VEC / 2; ++i) t = add2(t, a.p[i]);
+    float x, y;
+    unpack2(t, x, y);
+    return x + y;
 }
 template <int VEC>
 __device__ __forceinline__ float vdot(const Lanes<VEC> &a, const Lanes<VEC> &b)
 {
-    if constexpr (VEC == 1) {
-        return a.p[0] * b.p[0];
-    } else {
-        pair_t t = mul2(a.p[0], b.p[0]);
+    pair_t t = mul2(a.p[0], b.p[0]);
 #pragma unroll
-        for (int i = 1; i < VEC / 2; ++i) t = fma2(a.p[i], b.p[i], t);
-        float x, y;
-        unpack2(t, x, y);
-        return x + y;
-    }
+    for (int i = 1; i < VEC / 2; ++i) t = fma2(a.p[i], b.p[i], t);
+    float x, y;
+    unpack2(t, x, y);
+    return x + y;
 }
 
 // act(v) and, if grad, its derivative; sigmoid s: v s and s (1 + v (1 - s)).
@@ -95,33 +90,93 @@ __device__ __forceinline__ Lanes<VEC> vact(const Lanes<VEC> &v, int silu, Lanes<
     return vmul<VEC>(v, s);
 }
 
+// Vectors of two values stand for groups and rows that 16-byte vectors do not
+// fit: they start at any value, and a group's last one may hold one value
+// (`count` of them; the other reads as 0 and is not written).
+template <int VEC, typename T>
+__device__ __forceinline__ Lanes<VEC> vload(const T *from, int count)
+{
+    float f[VEC];
+    if constexpr (VEC == 2) {
+        f[0] = load1(from);
+        f[1] = count > 1 ? load1(from + 1) : 0.f;
+    } else {
+        load_vec<VEC>(from, f);
+    }
+    return vfrom<VEC>(f);
+}
+template <int VEC, typename T>
+__device__ __forceinline__ void vstore(T *to, const Lanes<VEC> &v, int count)
+{
+    float f[VEC];
+    vto<VEC>(v, f);
+    if constexpr (VEC == 2) {
+        if (count > 1 && reinterpret_cast<uintptr_t>(to) % (2 * sizeof(T)) == 0) {
+            store_vec<2>(to, f);
+        } else {
+            store1(to, f[0]);
+            if (count > 1) store1(to + 1, f[1]);
+        }
+    } else {
+        store_out<VEC>(to, f);
+    }
+}
+
 // A thread's vectors of the rows to come, K tensors of them: slots of shared
-// memory that only the thread's own copies fill.  Rows of 2-byte vectors,
-// which no asynchronous copy moves, are loaded when they are needed.
+// memory that only the thread's own copies fill.  Two values come as the
+// 4-byte words that hold them: two bf16 that start in the middle of a word as
+// its two words, of which the value before them (never the first of a tensor)
+// is dropped.  8192 rows of 7 groups of 143 bf16 take 68 us, and the gradients
+// 92; single values, loaded where they are used, took 63 and 192, and one
+// group of 1001 136 and 157, now 62 and 86.  Instructions bound these.
 template <typename T, int VEC, int NV, int K>
 struct Ahead {
-    static constexpr int kBytes = int(sizeof(T)) * VEC;
-    static constexpr bool kAsync = kBytes >= 4 && NV <= 2;
+    static constexpr int kBytes = VEC == 2 ? 8 : int(sizeof(T)) * VEC;
+    static constexpr bool kAsync = NV <= (VEC == 2 ? 4 : 2);
     static size_t bytes(int threads) { return kAsync ? size_t(kAhead) * K * NV * threads * kBytes : 0; }
     unsigned char *mine;
-    __device__ __forceinline__ T *at(int slot, int k, int i) const
+    __device__ __forceinline__ unsigned char *at(int slot, int k, int i) const
     {
-        return reinterpret_cast<T *>(mine + size_t((slot * K + k) * NV + i) * blockDim.x * kBytes);
+        return mine + size_t((slot * K + k) * NV + i) * blockDim.x * kBytes;
     }
-    __device__ __forceinline__ void fetch(int slot, int k, int i, const T *from) const
+    static __device__ __forceinline__ bool odd(const T *from) { return reinterpret_cast<uintptr_t>(from) % 4 != 0; }
+    static __device__ __forceinline__ void word(unsigned char *to, const void *from, int bytes)
     {
-        if constexpr (kAsync && kBytes == 16)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" : : "r"(smem_addr(at(slot, k, i))), "l"(from)
-                         : "memory");
-        else if constexpr (kAsync)
-            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" : : "r"(smem_addr(at(slot, k, i))), "l"(from),
-                         "n"(kBytes) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" : : "r"(smem_addr(to)), "l"(from), "r"(bytes)
+                     : "memory");
     }
-    __device__ __forceinline__ Lanes<VEC> get(int slot, int k, int i, const T *from) const
+    __device__ __forceinline__ void fetch(int slot, int k, int i, const T *from, int count) const
     {
-        float o[VEC];
-        load_vec<VEC>(kAsync ? at(slot, k, i) : from, o);
-        return vfrom<VEC>(o);
+        unsigned char *to = at(slot, k, i);
+        if constexpr (!kAsync) {
+            return;
+        } else if constexpr (VEC > 2) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" : : "r"(smem_addr(to)), "l"(from) : "memory");
+        } else if constexpr (sizeof(T) == 4) {
+            word(to, from, 4);
+            word(to + 4, count > 1 ? from + 1 : from, count > 1 ? 4 : 0);
+        } else {
+            const T *first = reinterpret_cast<const T *>(reinterpret_cast<uintptr_t>(from) & ~uintptr_t(3));
+            const bool mid = first != from, two = count > 1;
+            word(to, first, mid || two ? 4 : 2);
+            word(to + 4, mid && two ? first + 2 : first, mid && two ? 2 : 0);
+        }
+    }
+    __device__ __forceinline__ Lanes<VEC> get(int slot, int k, int i, const T *from, int count) const
+    {
+        if constexpr (!kAsync) {
+            return vload<VEC>(from, count);
+        } else if constexpr (VEC == 2 && sizeof(T) == 2) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(at(slot, k, i));
+            const unsigned two = odd(from) ? __funnelshift_r(w.x, w.y, 16) : w.x;
+            Lanes<VEC> v;
+            v.p[0] = pack2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+            return v;
+        } else {
+            float o[VEC];
+            load_vec<VEC>(reinterpret_cast<const T *>(at(slot, k, i)), o);
+            return vfrom<VEC>(o);
+        }
     }
 };
 
@@ -143,7 +198,7 @@ struct Team {
 
 // SILU: 1 where the activation is known to be SiLU when compiled, else -1.
 template <typename T, int VEC, int NV, mg_gate GATE, int TEAM, int SILU>
-__global__ void __launch_bounds__(NV == 16 ? kMaxTeam : 512, NV == 1 ? 2 : 1)
+__global__ void __launch_bounds__(512, NV == 1 || (VEC == 2 && NV <= 4) ? 2 : 1)
 norm_fwd_kernel(NormArgs p, int team_size, int row_teams)
 {
     const int tpg = TEAM > 0 ? TEAM : team_size, silu = SILU == 1 ? 1 : p.silu;
@@ -165,13 +220,8 @@ norm_fwd_kernel(NormArgs p, int team_size, int row_teams)
         in[i] = team.live && c[i] < gs;
         w[i] = b[i] = vset<VEC>(0.f);
         if (in[i]) {
-            float f[VEC];
-            load_vec<VEC>(p.w + team.d0 + c[i], f);
-            w[i] = vfrom<VEC>(f);
-            if (p.bias != nullptr) {
-                load_vec<VEC>(p.bias + team.d0 + c[i], f);
-                b[i] = vfrom<VEC>(f);
-            }
+            w[i] = vload<VEC>(p.w + team.d0 + c[i], gs - c[i]);
+            if (p.bias != nullptr) b[i] = vload<VEC>(p.bias + team.d0 + c[i], gs - c[i]);
         }
     }
     const int64_t xs = row_teams * p.ldx, zs = row_teams * p.ldz, ys = row_teams * p.D;
@@ -182,8 +232,8 @@ norm_fwd_kernel(NormArgs p, int team_size, int row_teams)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (in[i] && row_next < M) {
-                ahead.fetch(slot, 0, i, xn + c[i]);
-                if (K == 2) ahead.fetch(slot, 1, i, zn + c[i]);
+                ahead.fetch(slot, 0, i, xn + c[i], gs - c[i]);
+                if (K == 2) ahead.fetch(slot, 1, i, zn + c[i], gs - c[i]);
             }
         xn += xs;
         zn += zs;
@@ -209,19 +259,22 @@ norm_fwd_kernel(NormArgs p, int team_size, int row_teams)
         for (int i = 0; i < NV; ++i) {
             f[i] = vset<VEC>(0.f);
             if (in[i] && live) {
-                f[i] = ahead.get(slot, 0, i, x + c[i]);
-                if (K == 2) gate[i] = vact<VEC>(ahead.get(slot, 1, i, z + c[i]), silu);
+                f[i] = ahead.get(slot, 0, i, x + c[i], gs - c[i]);
+                if (K == 2) gate[i] = vact<VEC>(ahead.get(slot, 1, i, z + c[i], gs - c[i]), silu);
                 if (GATE == MG_GATE_FIRST) f[i] = vmul<VEC>(f[i], gate[i]);
                 sum += vsum<VEC>(f[i]);
             }
         }
         float mean = 0.f;
+        Lanes<VEC> first = vset<VEC>(1.f);
+        if constexpr (VEC == 2) first.p[0] = pack2(1.f, 0.f);
         if (!p.rms) mean = team_sum<TEAM>(sum, tpg, buf[0]) * inv;
         float sq = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (in[i] && live) {
                 f[i] = vadd<VEC>(f[i], vset<VEC>(-mean));
+                if (VEC == 2 && c[i] + 1 == gs) f[i] = vmul<VEC>(f[i], first);
                 sq += vdot<VEC>(f[i], f[i]);
             }
         // (one sum a row: the buffers take turns)
@@ -234,9 +287,7 @@ norm_fwd_kernel(NormArgs p, int team_size, int row_teams)
                     Lanes<VEC> o = vfma<VEC>(vmul<VEC>(f[i], vset<VEC>(rstd)), w[i], b[i]);
                     if (GATE == MG_GATE_AFTER) o = vmul<VEC>(o, gate[i]);
                     if (GATE == MG_GATE_NONE) o = vact<VEC>(o, silu);
-                    float v[VEC];
-                    vto<VEC>(o, v);
-                    store_out<VEC>(y + c[i], v);
+                    vstore<VEC>(y + c[i], o, gs - c[i]);
                 }
         }
         x += xs;
@@ -252,7 +303,7 @@ norm_fwd_kernel(NormArgs p, int team_size, int row_teams)
 // and the gate's chain rule around it.  dw and dbias are summed over a team's
 // rows in registers; the teams' sums are added in order by sum_parts_kernel.
 template <typename T, int VEC, int NV, mg_gate GATE, int TEAM, int SILU>
-__global__ void __launch_bounds__(NV == 16 ? kMaxTeam : 512)
+__global__ void __launch_bounds__(512)
 norm_bwd_kernel(NormArgs p, int team_size, int row_teams, float *part)
 {
     const int tpg = TEAM > 0 ? TEAM : team_size, silu = SILU == 1 ? 1 : p.silu;
@@ -275,13 +326,8 @@ norm_bwd_kernel(NormArgs p, int team_size, int row_teams, float *part)
         in[i] = team.live && c[i] < gs;
         w[i] = b[i] = dw[i] = db[i] = vset<VEC>(0.f);
         if (in[i]) {
-            float f[VEC];
-            load_vec<VEC>(p.w + team.d0 + c[i], f);
-            w[i] = vfrom<VEC>(f);
-            if (GATE != MG_GATE_FIRST && p.bias != nullptr) {
-                load_vec<VEC>(p.bias + team.d0 + c[i], f);
-                b[i] = vfrom<VEC>(f);
-            }
+            w[i] = vload<VEC>(p.w + team.d0 + c[i], gs - c[i]);
+            if (GATE != MG_GATE_FIRST && p.bias != nullptr) b[i] = vload<VEC>(p.bias + team.d0 + c[i], gs - c[i]);
         }
     }
     const int64_t xs = row_teams * p.ldx, zs = row_teams * p.ldz, gst = row_teams * p.lddy, os = row_teams * p.D;
@@ -292,9 +338,9 @@ norm_bwd_kernel(NormArgs p, int team_size, int row_teams, float *part)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (in[i] && row_next < M) {
-                ahead.fetch(slot, 0, i, xn + c[i]);
-                ahead.fetch(slot, 1, i, gn + c[i]);
-                if (K == 3) ahead.fetch(slot, K - 1, i, zn + c[i]);
+                ahead.fetch(slot, 0, i, xn + c[i], gs - c[i]);
+                ahead.fetch(slot, 1, i, gn + c[i], gs - c[i]);
+                if (K == 3) ahead.fetch(slot, K - 1, i, zn + c[i], gs - c[i]);
             }
         xn += xs;
         zn += zs;
@@ -322,8 +368,8 @@ norm_bwd_kernel(NormArgs p, int team_size, int row_teams, float *part)
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (live && in[i]) {
-                Lanes<VEC> pv = ahead.get(slot, 0, i, x + c[i]), dov = ahead.get(slot, 1, i, dy + c[i]);
-                if (K == 3) ga[i] = vact<VEC>(ahead.get(slot, K - 1, i, z + c[i]), silu, gg[i]);
+                Lanes<VEC> pv = ahead.get(slot, 0, i, x + c[i], gs - c[i]), dov = ahead.get(slot, 1, i, dy + c[i], gs - c[i]);
+                if (K == 3) ga[i] = vact<VEC>(ahead.get(slot, K - 1, i, z + c[i], gs - c[i]), silu, gg[i]);
                 if (GATE == MG_GATE_FIRST) {
                     gg[i] = vmul<VEC>(gg[i], pv);
                     pv = vmul<VEC>(pv, ga[i]);
@@ -333,9 +379,7 @@ norm_bwd_kernel(NormArgs p, int team_size, int row_teams, float *part)
                 if (GATE != MG_GATE_FIRST) {
                     const Lanes<VEC> o = vfma<VEC>(n[i], w[i], b[i]);
                     if (GATE == MG_GATE_AFTER) {
-                        float v[VEC];
-                        vto<VEC>(vmul<VEC>(vmul<VEC>(dov, o), gg[i]), v);
-                        store_out<VEC>(static_cast<T *>(p.dz) + out + c[i], v);
+                        vstore<VEC>(static_cast<T *>(p.dz) + out + c[i], vmul<VEC>(vmul<VEC>(dov, o), gg[i]), gs - c[i]);
                         dov = vmul<VEC>(dov, ga[i]);
                     } else {
                         Lanes<VEC> grad;
@@ -356,14 +400,11 @@ norm_bwd_kernel(NormArgs p, int team_size, int row_teams, float *part)
             if (live && in[i]) {
                 Lanes<VEC> dp = vadd<VEC>(vfma<VEC>(n[i], vset<VEC>(-m2), dn[i]), vset<VEC>(-m1));
                 dp = vmul<VEC>(dp, rstd);
-                float v[VEC];
                 if (GATE == MG_GATE_FIRST) {
-                    vto<VEC>(vmul<VEC>(dp, gg[i]), v);
-                    store_out<VEC>(static_cast<T *>(p.dz) + out + c[i], v);
+                    vstore<VEC>(static_cast<T *>(p.dz) + out + c[i], vmul<VEC>(dp, gg[i]), gs - c[i]);
                     dp = vmul<VEC>(dp, ga[i]);
                 }
-                vto<VEC>(dp, v);
-                store_out<VEC>(static_cast<T *>(p.dx) + out + c[i], v);
+                vstore<VEC>(static_cast<T *>(p.dx) + out + c[i], dp, gs - c[i]);
             }
         x += xs;
         z += zs;
@@ -377,11 +418,8 @@ norm_bwd_kernel(NormArgs p, int team_size, int row_teams, float *part)
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (in[i]) {
-            float f[VEC];
-            vto<VEC>(dw[i], f);
-            store_vec<VEC>(to + c[i], f);
-            vto<VEC>(db[i], f);
-            store_vec<VEC>(to + p.D + c[i], f);
+            vstore<VEC>(to + c[i], dw[i], gs - c[i]);
+            vstore<VEC>(to + p.D + c[i], db[i], gs - c[i]);
         }
 }
 
@@ -394,31 +432,46 @@ int team_for(int64_t gs, int vec, int nv)
     return t;
 }
 
-constexpr int kNormBlock = 256;
+// A team of several warps has its block to itself, for its barriers.
+// (32768 rows of 4 groups of 1024 bf16: 158 -> 146 us, gradients 376 -> 333.)
+int block_for(int tpg) { return tpg > 32 ? tpg : 256; }
 
 // (vector width, vectors a thread, team) of a call.  Vectors are 16 bytes
-// where the group's width and the rows allow, else one value.  Single values
-// take the fewest a thread whose team fits a warp, whose sums need no barrier
-// (groups of 143 bf16 channels: see below), and everything else the fewest
-// whose team has at most 512 threads: one vector up to 4096 bf16 channels.
-// 8 x 512 float4 and 16 x 1024 single values hold the widest group, 16384
-// channels.
+// where the group's width and the rows allow, else two values.
+//
+// A thread takes two vectors where a group has more than 8 of them, which
+// leaves fewer threads to meet over its sums, and more only where 512 threads
+// do not cover it.  Of 32768 x 4096 bf16 channels gated first, one vector
+// against two: one group 175 us to 134, 4 groups 164 to 131, 32 groups 144 to
+// 136.  The gradients hold more of a row in registers and begin later, at more
+// than 256 (128 float32) channels: one group 397 to 366 us, 8 groups 297 to
+// 278, but 16 groups 256 to 276; 8192 rows of 32 float32 groups 135 to 118.
+//
+// Pairs take the fewest a thread whose team fits a warp, else at most
+// kPairTeam threads (8192 rows of 1001 channels: 62 us; with up to 512 87).
+// 8 x 512 float4 and 16 x 512 pairs hold the widest group, 16384 channels.
+constexpr int kPairTeam = 128;
 struct Shape {
     int vec, nv, tpg;
 };
-Shape shape_for(mg_dtype dt, int64_t gs, bool aligned)
+Shape shape_for(mg_dtype dt, int64_t gs, bool aligned, bool backward)
 {
     const int full = dt == MG_F32 ? 4 : 8;
     Shape c;
-    c.vec = aligned && gs % full == 0 ? full : 1;
-    const int most = c.vec == 1 ? 16 : 8;
-    for (int limit : {c.vec == 1 ? 32 : 512, 512, kMaxTeam})
-        for (int nv : {1, 2, 4, most}) {
-            c.nv = nv;
-            c.tpg = team_for(gs, c.vec, nv);
-            if (c.tpg <= limit && (limit <= 512 || nv == 16)) return c;
-        }
-    c.tpg = 0;
+    c.vec = aligned && gs % full == 0 ? full : 2;
+    const int most = c.vec == 2 ? 16 : 8, warp = 32, one = backward ? 4 * full : 8;
+    auto fits = [&](int nv, int limit) {
+        c.nv = nv;
+        c.tpg = team_for(gs, c.vec, nv);
+        return c.tpg <= limit;
+    };
+    if (c.vec == 2) {
+        for (int limit : {warp, kPairTeam, kMaxTeam})
+            if (fits(1, limit) || fits(2, limit) || fits(4, limit)) return c;
+    } else if (fits(1, one) || fits(2, kMaxTeam) || fits(4, kMaxTeam)) {
+        return c;
+    }
+    if (!fits(most, kMaxTeam)) c.tpg = 0;
     return c;
 }
 
@@ -426,7 +479,7 @@ Shape shape_for(mg_dtype dt, int64_t gs, bool aligned)
 // warps each, at most one for each row.
 int64_t row_teams_for(int64_t M, int64_t G, int tpg, int warps)
 {
-    const int block = tpg > kNormBlock ? tpg : kNormBlock;
+    const int block = block_for(tpg);
     const int64_t all = int64_t(152) * (warps * 32 / block > 0 ? warps * 32 / block : 1) * (block / tpg);
     int64_t n = all / G;
     n = n < 1 ? 1 : n;
@@ -437,7 +490,7 @@ constexpr int kFwdWarps = 32, kBwdWarps = 16;   // what an SM holds by the kerne
 template <typename T, int VEC, int NV, mg_gate GATE, int TEAM, int SILU>
 mg_status norm_fwd_team(const NormArgs &p, int tpg, cudaStream_t s)
 {
-    const int block = tpg > kNormBlock ? tpg : kNormBlock;
+    const int block = block_for(tpg);
     const int64_t rt = row_teams_for(p.M, p.G, tpg, kFwdWarps);
     const size_t smem = Ahead<T, VEC, NV, GATE == MG_GATE_NONE ? 1 : 2>::bytes(block);
     MG_TRY(allow_shared<norm_fwd_kernel<T, VEC, NV, GATE, TEAM, SILU>>(smem));
@@ -449,7 +502,7 @@ mg_status norm_fwd_team(const NormArgs &p, int tpg, cudaStream_t s)
 template <typename T, int VEC, int NV, mg_gate GATE, int TEAM, int SILU>
 mg_status norm_bwd_team(const NormArgs &p, int tpg, cudaStream_t s)
 {
-    const int block = tpg > kNormBlock ? tpg : kNormBlock;
+    const int block = block_for(tpg);
     const int64_t rt = row_teams_for(p.M, p.G, tpg, kBwdWarps);
     float *part = reinterpret_cast<float *>(static_cast<char *>(p.ws) + kControlBytes);
     const size_t smem = Ahead<T, VEC, NV, GATE == MG_GATE_NONE ? 2 : 3>::bytes(block);
@@ -460,10 +513,10 @@ mg_status norm_bwd_team(const NormArgs &p, int tpg, cudaStream_t s)
     return launch_sum_parts(part, rt, {{p.dw, p.D}, {p.dbias, p.D}}, s);
 }
 
-// Groups of one vector a thread, gated or activated by SiLU, have kernels for
-// their team's size; the rest share one for any size.
+// Groups of one or two 16-byte vectors a thread, gated or activated by SiLU,
+// have kernels for their team's size; the rest share one for any size.
 #define MG_NORM_TEAM(F)                                                              \
-    if constexpr (NV == 1 && VEC > 1) {                                              \
+    if constexpr (NV <= 2 && VEC > 2) {                                              \
         if (p.silu) {                                                                \
             if (tpg == 8) return F<T, VEC, NV, GATE, 8, 1>(p, tpg, s);               \
             if (tpg == 16) return F<T, VEC, NV, GATE, 16, 1>(p, tpg, s);             \
@@ -514,7 +567,7 @@ mg_status norm_bwd(const NormArgs &p, int tpg, cudaStream_t s)
     const bool al = p.D % vec == 0 && p.ldx % vec == 0 &&                                \
                     (p.z == nullptr || p.ldz % vec == 0) &&                              \
                     (p.dy == nullptr || p.lddy % vec == 0);                              \
-    const Shape c = shape_for(dt, p.D / p.G, al);                                        \
+    const Shape c = shape_for(dt, p.D / p.G, al, p.dy != nullptr);                       \
     if (c.tpg == 0)                                                                      \
         return fail(MG_ERR_UNSUPPORTED, "group of %lld channels too wide",               \
                     (long long)(p.D / p.G));                                             \
@@ -523,15 +576,15 @@ mg_status norm_bwd(const NormArgs &p, int tpg, cudaStream_t s)
             MG_NORM_NV(F, float, 4)                                                      \
             return F<float, 4, 8>(p, c.tpg, s);                                          \
         }                                                                                \
-        MG_NORM_NV(F, float, 1)                                                          \
-        return F<float, 1, 16>(p, c.tpg, s);                                             \
+        MG_NORM_NV(F, float, 2)                                                          \
+        return F<float, 2, 16>(p, c.tpg, s);                                             \
     }                                                                                    \
     if (c.vec == 8) {                                                                    \
         MG_NORM_NV(F, bf16_t, 8)                                                         \
         return fail(MG_ERR_UNSUPPORTED, "group too wide");                               \
     }                                                                                    \
-    MG_NORM_NV(F, bf16_t, 1)                                                             \
-    return F<bf16_t, 1, 16>(p, c.tpg, s);
+    MG_NORM_NV(F, bf16_t, 2)                                                             \
+    return F<bf16_t, 2, 16>(p, c.tpg, s);
 
 }  // namespace
 
@@ -541,7 +594,7 @@ size_t norm_ws_bytes(int64_t M, int64_t D, int64_t G)
     size_t need = 0;
     for (mg_dtype dt : {MG_F32, MG_BF16})
         for (bool al : {false, true}) {
-            const Shape c = shape_for(dt, D / G, al);
+            const Shape c = shape_for(dt, D / G, al, true);
             if (c.tpg == 0) continue;
             const size_t n = size_t(row_teams_for(M, G, c.tpg, kBwdWarps)) * 2 * D * sizeof(float);
             need = n > need ? n : need;
