@@ -26,13 +26,21 @@ namespace mg {
 // tile instead, they would ask for more of its bandwidth than the second
 // computation takes of the arithmetic.)
 //
-// Four states of four channels are a thread's: the sums over channels (8
-// values of dB and dC over the warp's channel lanes) and over states (s1 and
-// s2 of 4 channels) then take 13 shuffles a row, fewer than any other split
-// of 16, and are halved at each step.  Pairs are of neighbouring channels.
-// The lane that a channel's s1 and s2 end at writes its dx and draw and sums
-// its dDskip and ddt_bias.  Each warp stages its own channels; the block's
-// warps meet once a tile to add their dB and dC.
+// Four states of four channels are a thread's (of two, up to 8 states): the
+// sums over channels (8 values of dB and dC over the warp's channel lanes) and
+// over states (s1 and s2 of its channels) then take 13 shuffles a row, fewer
+// than any other split of 16 states, and are halved at each step.  Pairs are of
+// neighbouring channels.  The lane that a channel's s1 and s2 end at writes its
+// dx and draw and sums its dDskip and ddt_bias.  Each warp stages its own
+// channels, the block its B and C (staged by every warp for itself they took
+// shared memory for a second block: 2 x 4096 x 1024 channels of 64 states 1246
+// -> 838 us); the block's warps meet once a tile to add their dB and dC.
+//
+// 4 x 4096 x 2048 channels of 16 states take 780 us, 0.69e12 states a second:
+// 120 for the first pass, 630 here and 20 for the sums of the parts.  The
+// arithmetic bounds it (some 17 instructions a state, one of them an
+// exponential, twice over), at half the issue slots with two warps a
+// scheduler, which is what the registers of kSub rows leave.
 constexpr int kSub = 4;
 
 // v over LANES lanes (bits STRIDE .. of the lane index; `id` is the lane's
@@ -97,47 +105,57 @@ __device__ __forceinline__ void edge_rows(const Seqs &q, int64_t rowb, int64_t t
     last[i] = e;
 }
 
-// A thread's 4 x 4 states of float arrays (.., D, N), as channel pairs.
-template <int S>
+// A thread's states of 2 CP channels of float arrays (.., D, N), as channel
+// pairs.
+template <int S, int CP>
 __device__ __forceinline__ void load_block(const float *base, int64_t d, int ch, int64_t wide, int n0,
-                                           int N, pair_t (&o)[S][2])
+                                           int N, pair_t (&o)[S][CP])
 {
-    float v[4][S];
+    float v[2 * CP][S];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 2 * CP; ++c) {
 #pragma unroll
         for (int i = 0; i < S; ++i) v[c][i] = 0.f;
         if (base != nullptr && ch + c < wide) load_group<S>(base + (d + c) * N, n0, N, v[c]);
     }
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-        o[i][0] = pack2(v[0][i], v[1][i]);
-        o[i][1] = pack2(v[2][i], v[3][i]);
-    }
+    for (int i = 0; i < S; ++i)
+#pragma unroll
+        for (int c = 0; c < CP; ++c) o[i][c] = pack2(v[2 * c][i], v[2 * c + 1][i]);
 }
-template <int S>
+template <int S, int CP>
 __device__ __forceinline__ void store_block(float *base, int64_t d, int ch, int64_t wide, int n0, int N,
-                                            const pair_t (&o)[S][2])
+                                            const pair_t (&o)[S][CP])
 {
-    float v[4][S];
+    float v[2 * CP][S];
 #pragma unroll
-    for (int i = 0; i < S; ++i) {
-        unpack2(o[i][0], v[0][i], v[1][i]);
-        unpack2(o[i][1], v[2][i], v[3][i]);
-    }
+    for (int i = 0; i < S; ++i)
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < CP; ++c) unpack2(o[i][c], v[2 * c][i], v[2 * c + 1][i]);
+#pragma unroll
+    for (int c = 0; c < 2 * CP; ++c)
         if (ch + c < wide) store_group<S>(base + (d + c) * N, n0, N, v[c]);
+}
+// A row's values of a thread's channels in shared memory.
+template <int CP>
+__device__ __forceinline__ void load_pairs(const float *from, pair_t (&o)[CP])
+{
+    if constexpr (CP == 2) {
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(from);
+        o[0] = v.x, o[1] = v.y;
+    } else {
+        o[0] = *reinterpret_cast<const pair_t *>(from);
+    }
 }
 
 __device__ __forceinline__ pair_t dup2(float a) { return pack2(a, a); }
 
-// s1 and s2 of four channels over LANES lanes (bits STRIDE ..): lane id ends
-// with the sums of channels id 4/LANES .. (or id / (LANES/4)) in a[0], b[0], ..
-template <int LANES, int STRIDE>
-__device__ __forceinline__ void halve_channels(float (&a)[4], float (&b)[4], int id)
+// s1 and s2 of V channels over LANES lanes (bits STRIDE ..): lane id ends
+// with the sums of channels id V/LANES .. (or id / (LANES/V)) in a[0], b[0], ..
+template <int LANES, int STRIDE, int V>
+__device__ __forceinline__ void halve_channels(float (&a)[V], float (&b)[V], int id)
 {
-    int w = 2;
+    int w = V / 2;
 #pragma unroll
     for (int m = LANES / 2; m > 0; m >>= 1, w >>= 1) {
         if (w > 0) {
@@ -161,57 +179,60 @@ template <typename T, int VEC, typename CV>
 struct BwdWarp {
     static constexpr int WCH = CV::kWarpCh, NP = CV::NP;
     float d[kTile][WCH], x[kTile][WCH], dy[kTile][WCH], slope[kTile][WCH];
-    float bc[kTile][2][NP];
-    float4 ck[kTile / kSub][4][32];                // states before each kSub rows, by lane
+    float4 ck[kTile / kSub][CV::C][32];                // states before each kSub rows, by lane
     float bias[WCH];
     T raw[3][kTile][VEC > 1 ? WCH : Words<T, WCH>::kPitch];   // the next tile's x, raw, dy as loaded
-    alignas(16) T rawbc[kTile][2][NP];
 };
 template <typename T, int VEC, typename CV>
 struct alignas(16) BwdShared {
     BwdWarp<T, VEC, CV> warp[CV::THREADS / 32];
+    float bc[kTile][2][CV::NP];                       // the tile's B and C
+    alignas(16) T rawbc[kTile][2][CV::NP];            // the next tile's as loaded
     float red[kTile][CV::THREADS / 32][2 * CV::NP];   // each warp's dB, then dC
     int first[kTile], last[kTile];
 };
 
+// Blocks that share an SM.
+template <typename CV>
+constexpr int backward_blocks() { return (CV::C == 2 ? 3 : 2) * (kThreads / CV::THREADS); }
+
 template <typename T, int VEC, typename CV>
-__global__ void __launch_bounds__(CV::THREADS, 2)
+__global__ void __launch_bounds__(CV::THREADS, backward_blocks<CV>())
 ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const float *agg_s,
                float *partB, float *partA, int mode)
 {
-    constexpr int S = CV::S, L = CV::L, NP = CV::NP, CH = CV::kCh, WCH = CV::kWarpCh, kWarps = CV::THREADS / 32;
+    constexpr int S = CV::S, L = CV::L, C = CV::C, CP = C / 2, NP = CV::NP, CH = CV::kCh, WCH = CV::kWarpCh, kWarps = CV::THREADS / 32;
     constexpr int kCols = WCH / VEC, kVecs = kTile * kCols, kPer = (kVecs + 31) / 32;
     constexpr int kCv = NP < 16 / int(sizeof(T)) ? NP : 16 / int(sizeof(T));   // values of a vector of B or C
-    constexpr int kBcCols = NP / kCv, kBcVecs = kTile * 2 * kBcCols, kBcPer = (kBcVecs + 31) / 32;
-    constexpr int kRowW = NP * int(sizeof(T)) / 4, kBcW = kTile * 2 * kRowW;   // words
+    constexpr int kBcCols = NP / kCv, kBcVecs = kTile * 2 * kBcCols, kBcPer = (kBcVecs + CV::THREADS - 1) / CV::THREADS;
     constexpr int kG = CV::kGroups;
-    static_assert(S == 4, "four states a thread");
+    static_assert(S == 4 && (C == 2 || C == 4), "four states of two or four channels a thread");
     extern __shared__ __align__(16) unsigned char shared_bytes[];
     BwdShared<T, VEC, CV> &block = *reinterpret_cast<BwdShared<T, VEC, CV> *>(shared_bytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     BwdWarp<T, VEC, CV> &sm = block.warp[warp];
     const Spot<CH> w(p, tl, ck);
     const int sl = lane / kG, cg = lane % kG, n0 = sl * S;
-    const int ch = cg * 4;                                       // of the warp's channels
+    const int ch = cg * C;                                       // of the warp's channels
     const int64_t dw = w.d0 + warp * WCH;                        // the warp's first channel
     const int wide = int(w.wide - warp * WCH < WCH ? w.wide - warp * WCH : WCH);   // its channels (may be <= 0)
     const bool vec_n = p.N % 4 == 0;
 
-    pair_t A2[S][2], ag[S][2], dA[S][2];
-    load_block<S>(p.A, dw + ch, ch, wide, n0, p.N, A2);
+    pair_t A2[S][CP], ag[S][CP], dA[S][CP];
+    load_block<S, CP>(p.A, dw + ch, ch, wide, n0, p.N, A2);
 #pragma unroll
     for (int i = 0; i < S; ++i)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < CP; ++c) {
             A2[i][c] = mul2(A2[i][c], dup2(kLog2eF));
             ag[i][c] = dA[i][c] = 0;
         }
     for (int i = lane; i < WCH; i += 32)
         sm.bias[i] = p.dt_bias != nullptr && i < wide ? p.dt_bias[dw + i] : 0.f;
     // the channels whose outputs are this lane's (lanes that share one: the first writes)
-    constexpr int kOut = L <= 4 ? 4 / L : 1;
-    const int oc = ch + (L <= 4 ? sl * kOut : sl / (L > 4 ? L / 4 : 1));
-    const bool writes = L <= 4 || sl % (L > 4 ? L / 4 : 1) == 0;
+    constexpr int kOut = L <= C ? C / L : 1, kSame = L > C ? L / C : 1;
+    const int oc = ch + (L <= C ? sl * kOut : sl / kSame);
+    const bool writes = sl % kSame == 0;
     float skip[kOut], sum_d[kOut], sum_b[kOut];
 #pragma unroll
     for (int o = 0; o < kOut; ++o) {
@@ -226,15 +247,15 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
         bool begin = true;
         for (; j > w.k; --j) {
             const int64_t at = (w.b * (ck.n - 1) + j - 1) * p.D;
-            pair_t v[S][2];
-            load_block<S>(agg_q + at * p.N, dw + ch, ch, wide, n0, p.N, v);
-            float ds[4];
+            pair_t v[S][CP];
+            load_block<S, CP>(agg_q + at * p.N, dw + ch, ch, wide, n0, p.N, v);
+            float ds[C];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) ds[c] = ch + c < wide ? agg_s[at + dw + ch + c] : 0.f;
+            for (int c = 0; c < C; ++c) ds[c] = ch + c < wide ? agg_s[at + dw + ch + c] : 0.f;
 #pragma unroll
             for (int i = 0; i < S; ++i)
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
+                for (int c = 0; c < CP; ++c)
                     ag[i][c] = begin ? v[i][c]
                                      : fma2(decay2(ds[2 * c], ds[2 * c + 1], A2[i][c]), ag[i][c], v[i][c]);
             begin = false;
@@ -265,22 +286,23 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
             fetch_words<T, WCH, kTile>(sm.raw[1], r0p, rf + t * p.ldraw, p.ldraw, rows, wide, lane);
             fetch_words<T, WCH, kTile>(sm.raw[2], y0p, yf + t * p.lddy, p.lddy, rows, wide, lane);
         }
-        if (mode == kBcVectors) {
+        if (mode == kBcValues) return;
 #pragma unroll
-            for (int i = 0; i < kBcPer; ++i) {
-                const int v = lane + i * 32, n = v % kBcCols * kCv, which = v / kBcCols % 2, row = v / kBcCols / 2;
-                const bool in = t + row < w.t1 && n < p.N;
-                const T *src = which == 0 ? bp + (t + row) * p.ldb + n : cp + (t + row) * p.ldc + n;
-                if (kCv * sizeof(T) == 16 && v < kBcVecs)
-                    cp_async16_or_zero(&sm.rawbc[row][which][n], in ? static_cast<const void *>(src) : p.Bm, in);
-            }
-        } else if (mode == kBcWords) {
-#pragma unroll 4
-            for (int v = lane; v < kBcW; v += 32) {
-                const int n = v % kRowW * (4 / int(sizeof(T))), which = v / kRowW % 2, row = v / kRowW / 2;
-                const bool in = t + row < w.t1 && n < p.N;
-                const T *src = which == 0 ? bp + (t + row) * p.ldb + n : cp + (t + row) * p.ldc + n;
-                cp_async4(&sm.rawbc[row][which][n], in ? static_cast<const void *>(src) : p.Bm, in ? 4 : 0);
+        for (int i = 0; i < kBcPer; ++i) {
+            const int v = tid + i * CV::THREADS, n = v % kBcCols * kCv, which = v / kBcCols % 2, row = v / kBcCols / 2;
+            if (v >= kBcVecs) continue;
+            const bool in = t + row < w.t1;
+            const T *src = which == 0 ? bp + (t + row) * p.ldb + n : cp + (t + row) * p.ldc + n;
+            T *to = &block.rawbc[row][which][n];
+            if (kCv * sizeof(T) == 16 && mode == kBcVectors) {
+                cp_async16_or_zero(to, in && n < p.N ? static_cast<const void *>(src) : p.Bm, in && n < p.N);
+            } else {
+                constexpr int kPer4 = 4 / int(sizeof(T));
+#pragma unroll
+                for (int e = 0; e < kCv; e += kPer4) {
+                    const bool ok = in && n + e < p.N;
+                    cp_async4(to + e, ok ? static_cast<const void *>(src + e) : p.Bm, ok ? 4 : 0);
+                }
             }
         }
     };
@@ -288,7 +310,7 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
     auto fetch_state = [&](int64_t t) {
         const float *o = p.saved_in + ((w.b * nseg + t / kSeg) * p.D + dw + ch) * p.N;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < C; ++c) {
             float4 *to = &sm.ck[0][c][lane];
             if (ch + c >= wide || n0 >= p.N) {
                 *to = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -301,35 +323,35 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
             }
         }
     };
-    pair_t h[S][2];
+    pair_t h[S][CP];
     auto get_state = [&](int i) {
-        const float4 a = sm.ck[i][0][lane], b = sm.ck[i][1][lane], c = sm.ck[i][2][lane], d = sm.ck[i][3][lane];
-        h[0][0] = pack2(a.x, b.x), h[0][1] = pack2(c.x, d.x);
-        h[1][0] = pack2(a.y, b.y), h[1][1] = pack2(c.y, d.y);
-        h[2][0] = pack2(a.z, b.z), h[2][1] = pack2(c.z, d.z);
-        h[3][0] = pack2(a.w, b.w), h[3][1] = pack2(c.w, d.w);
+#pragma unroll
+        for (int c = 0; c < CP; ++c) {
+            const float4 a = sm.ck[i][2 * c][lane], b = sm.ck[i][2 * c + 1][lane];
+            h[0][c] = pack2(a.x, b.x), h[1][c] = pack2(a.y, b.y);
+            h[2][c] = pack2(a.z, b.z), h[3][c] = pack2(a.w, b.w);
+        }
     };
     auto put_state = [&](int i) {
-        float a[4], b[4], c[4], d[4];
 #pragma unroll
-        for (int n = 0; n < S; ++n) {
-            unpack2(h[n][0], a[n], b[n]);
-            unpack2(h[n][1], c[n], d[n]);
+        for (int c = 0; c < CP; ++c) {
+            float4 a, b;
+            unpack2(h[0][c], a.x, b.x), unpack2(h[1][c], a.y, b.y);
+            unpack2(h[2][c], a.z, b.z), unpack2(h[3][c], a.w, b.w);
+            sm.ck[i][2 * c][lane] = a;
+            sm.ck[i][2 * c + 1][lane] = b;
         }
-        sm.ck[i][0][lane] = make_float4(a[0], a[1], a[2], a[3]);
-        sm.ck[i][1][lane] = make_float4(b[0], b[1], b[2], b[3]);
-        sm.ck[i][2][lane] = make_float4(c[0], c[1], c[2], c[3]);
-        sm.ck[i][3][lane] = make_float4(d[0], d[1], d[2], d[3]);
     };
 
     // A staged row's values for the thread: delta and u = delta x of its
     // channel pairs, and B of its states.
-    auto row_in = [&](int tt, pair_t (&dl)[2], pair_t (&u)[2], float (&bv)[4]) {
-        const ulonglong2 d2 = *reinterpret_cast<const ulonglong2 *>(&sm.d[tt][ch]);
-        const ulonglong2 x2 = *reinterpret_cast<const ulonglong2 *>(&sm.x[tt][ch]);
-        const float4 b4 = *reinterpret_cast<const float4 *>(&sm.bc[tt][0][n0]);
-        dl[0] = d2.x, dl[1] = d2.y;
-        u[0] = mul2(d2.x, x2.x), u[1] = mul2(d2.y, x2.y);
+    auto row_in = [&](int tt, pair_t (&dl)[CP], pair_t (&u)[CP], float (&bv)[4]) {
+        pair_t x[CP];
+        load_pairs<CP>(&sm.d[tt][ch], dl);
+        load_pairs<CP>(&sm.x[tt][ch], x);
+        const float4 b4 = *reinterpret_cast<const float4 *>(&block.bc[tt][0][n0]);
+#pragma unroll
+        for (int c = 0; c < CP; ++c) u[c] = mul2(dl[c], x[c]);
         bv[0] = b4.x, bv[1] = b4.y, bv[2] = b4.z, bv[3] = b4.w;
     };
 
@@ -340,7 +362,7 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
             if constexpr (kEdges) {
                 const int f = block.first[tt];
                 if (f >= 0)
-                    load_block<S>(p.h0 != nullptr ? p.h0 + int64_t(f) * p.D * p.N : nullptr, dw + ch, ch, wide, n0,
+                    load_block<S, CP>(p.h0 != nullptr ? p.h0 + int64_t(f) * p.D * p.N : nullptr, dw + ch, ch, wide, n0,
                                   p.N, h);
             }
         };
@@ -353,13 +375,13 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
             for (int i = 0; i < kSub; ++i) {
                 const int tt = (sb - 1) * kSub + i;
                 enter(tt);
-                pair_t dl[2], u[2];
+                pair_t dl[CP], u[CP];
                 float bv[4];
                 row_in(tt, dl, u, bv);
 #pragma unroll
                 for (int n = 0; n < S; ++n)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+                    for (int c = 0; c < CP; ++c)
                         h[n][c] = fma2(decay2(dl[c], A2[n][c]), h[n][c], mul2(u[c], dup2(bv[n])));
             }
             put_state(sb);
@@ -371,18 +393,18 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
                 if (t > w.t0) fetch_state(t - kTile);
                 cp_async_commit();
             }
-            pair_t a[kSub][S][2], ah[kSub][S][2];
+            pair_t a[kSub][S][CP], ah[kSub][S][CP];
 #pragma unroll
             for (int i = 0; i < kSub; ++i) {
                 const int tt = sb * kSub + i;
                 enter(tt);
-                pair_t dl[2], u[2];
+                pair_t dl[CP], u[CP];
                 float bv[4];
                 row_in(tt, dl, u, bv);
 #pragma unroll
                 for (int n = 0; n < S; ++n)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < CP; ++c) {
                         a[i][n][c] = decay2(dl[c], A2[n][c]);
                         ah[i][n][c] = mul2(a[i][n][c], h[n][c]);
                         h[n][c] = fma2(u[c], dup2(bv[n]), ah[i][n][c]);
@@ -393,24 +415,23 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
                 const int tt = sb * kSub + i;
                 if constexpr (kEdges) {
                     if (block.last[tt] >= 0)
-                        load_block<S>(p.dh_last != nullptr ? p.dh_last + int64_t(block.last[tt]) * p.D * p.N : nullptr,
+                        load_block<S, CP>(p.dh_last != nullptr ? p.dh_last + int64_t(block.last[tt]) * p.D * p.N : nullptr,
                                       dw + ch, ch, wide, n0, p.N, ag);
                 }
-                pair_t dl[2], u[2];
+                pair_t dl[CP], u[CP];
                 float bv[4];
                 row_in(tt, dl, u, bv);
-                const ulonglong2 y2 = *reinterpret_cast<const ulonglong2 *>(&sm.dy[tt][ch]);
-                const float4 c4 = *reinterpret_cast<const float4 *>(&sm.bc[tt][1][n0]);
+                pair_t dy[CP], s1[CP], s2[CP];
+                load_pairs<CP>(&sm.dy[tt][ch], dy);
+                const float4 c4 = *reinterpret_cast<const float4 *>(&block.bc[tt][1][n0]);
                 const float cv[4] = {c4.x, c4.y, c4.z, c4.w};
-                const pair_t dy[2] = {y2.x, y2.y};
-                pair_t s1[2], s2[2];
                 float bc[2 * S];
 #pragma unroll
                 for (int n = 0; n < S; ++n) {
                     const pair_t bn = dup2(bv[n]), cn = dup2(cv[n]);
                     pair_t db = 0, dc = 0;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
+                    for (int c = 0; c < CP; ++c) {
                         const pair_t g = fma2(cn, dy[c], ag[n][c]);
                         const pair_t hh = fma2(u[c], bn, ah[i][n][c]);
                         dc = c == 0 ? mul2(dy[c], hh) : fma2(dy[c], hh, dc);
@@ -429,7 +450,7 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
                 }
                 if constexpr (kEdges) {
                     if (p.dh0 != nullptr && block.first[tt] >= 0)
-                        store_block<S>(p.dh0 + int64_t(block.first[tt]) * p.D * p.N, dw + ch, ch, wide, n0, p.N, ag);
+                        store_block<S, CP>(p.dh0 + int64_t(block.first[tt]) * p.D * p.N, dw + ch, ch, wide, n0, p.N, ag);
                 }
                 // dB, dC over the warp's channel lanes
                 constexpr int kBcOut = 2 * S / kG > 0 ? 2 * S / kG : 1, kShare = kG / (2 * S) > 0 ? kG / (2 * S) : 1;
@@ -441,11 +462,12 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
                         block.red[tt][warp][(v0 + o) / S * NP + n0 + (v0 + o) % S] = bc[o];
                 }
                 // s1, s2 over the channel's state lanes, and the outputs
-                float s1v[4], s2v[4];
-                unpack2(s1[0], s1v[0], s1v[1]);
-                unpack2(s1[1], s1v[2], s1v[3]);
-                unpack2(s2[0], s2v[0], s2v[1]);
-                unpack2(s2[1], s2v[2], s2v[3]);
+                float s1v[C], s2v[C];
+#pragma unroll
+                for (int c = 0; c < CP; ++c) {
+                    unpack2(s1[c], s1v[2 * c], s1v[2 * c + 1]);
+                    unpack2(s2[c], s2v[2 * c], s2v[2 * c + 1]);
+                }
                 halve_channels<L, kG>(s1v, s2v, sl);
 #pragma unroll
                 for (int o = 0; o < kOut; ++o) {
@@ -535,21 +557,22 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
                 }
             }
         }
+        // the thread's vectors of B and C, which it copied itself
         if (mode != kBcValues) {
 #pragma unroll
             for (int i = 0; i < kBcPer; ++i) {
-                const int v = lane + i * 32;
+                const int v = tid + i * CV::THREADS;
                 if (v < kBcVecs) {
                     float o[kCv];
-                    load_vec<kCv>(&sm.rawbc[v / kBcCols / 2][v / kBcCols % 2][v % kBcCols * kCv], o);
-                    store_vec<kCv>(&sm.bc[v / kBcCols / 2][v / kBcCols % 2][v % kBcCols * kCv], o);
+                    load_vec<kCv>(&block.rawbc[v / kBcCols / 2][v / kBcCols % 2][v % kBcCols * kCv], o);
+                    store_vec<kCv>(&block.bc[v / kBcCols / 2][v / kBcCols % 2][v % kBcCols * kCv], o);
                 }
             }
         } else {
-            for (int e = lane; e < kTile * 2 * NP; e += 32) {
+            for (int e = tid; e < kTile * 2 * NP; e += CV::THREADS) {
                 const int n = e % NP, which = e / NP % 2, row = e / NP / 2;
                 const bool in = t + row < w.t1 && n < p.N;
-                sm.bc[row][which][n] =
+                block.bc[row][which][n] =
                     !in ? 0.f : load1(which == 0 ? bp + (t + row) * p.ldb + n : cp + (t + row) * p.ldc + n);
             }
         }
@@ -579,12 +602,12 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
     // a part is dA, then dDskip and ddt_bias
     float *part = partA + (w.b * ck.n + w.k) * p.D * (p.N + 2);
     if (p.N % 4 == 0 && p.D % 2 == 0) {
-        store_block<S>(part, dw + ch, ch, wide, n0, p.N, dA);
+        store_block<S, CP>(part, dw + ch, ch, wide, n0, p.N, dA);
     } else {   // parts that are not 16-byte aligned
 #pragma unroll
         for (int i = 0; i < S; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < C; ++c) {
                 float a, b;
                 unpack2(dA[i][c / 2], a, b);
                 if (ch + c < wide && n0 + i < p.N) part[(dw + ch + c) * p.N + n0 + i] = c % 2 ? b : a;
@@ -614,27 +637,30 @@ __global__ void __launch_bounds__(256) sum_bc_kernel(const float *part, int64_t 
     store1(o + rg * N + (v < N ? v : v - N), a);
 }
 
-// The gradients' chunks: four channels a thread, two blocks for each SM.
+// The gradients' threads: states of four channels, or, up to 8 states, of two,
+// whose registers let three blocks share an SM instead of two (2 x 4096 x 1024
+// channels of 8 states: 235 -> 162 us; of 16 it would be 821 -> 857, the sums
+// over lanes being of fewer values).  Blocks hold the tiles of 128 channels.
 inline int backward_lanes(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
-// Threads of a block: shared memory holds the tiles of 128 channels.
-constexpr int backward_threads(int L) { return L == 1 ? 32 : L == 2 ? 64 : kThreads; }
+constexpr int backward_channels(int L) { return L <= 2 ? 2 : 4; }
+constexpr int backward_threads(int L) { return L == 1 ? 64 : kThreads; }
 inline int64_t backward_tiles(int64_t D, int N, int G)
 {
     const int L = backward_lanes(N);
-    return ceil_div(D / G, backward_threads(L) / L * 4);
+    return ceil_div(D / G, backward_threads(L) / L * backward_channels(L));
 }
 
 inline Chunks backward_chunks(int64_t B, int64_t T, int64_t D, int N, int G)
 {
-    // measured: 152 blocks, and 304 blocks, a row each
-    static constexpr RowTime r{{0, 450, 714, 0}, 2, 0.2};
-    return cut_time(B * G * backward_tiles(D, N, G), T, r);
+    // measured: 1024 rows of 152, 304 and 456 blocks
+    static constexpr RowTime two{{0, 405, 495, 625}, 3, 0.2}, four{{0, 520, 705, 0}, 2, 0.2};
+    return cut_time(B * G * backward_tiles(D, N, G), T, backward_channels(backward_lanes(N)) == 2 ? two : four);
 }
 
 template <typename T, int VEC, int L>
 mg_status bwd(const SsmArgs &p, cudaStream_t s)
 {
-    using CV = Cover<4, L, 4, backward_threads(L)>;
+    using CV = Cover<4, L, backward_channels(L), backward_threads(L)>;
     const Tile t{backward_tiles(p.D, p.N, p.G), p.D / p.G};
     const Chunks ck = backward_chunks(p.B, p.T, p.D, p.N, p.G);
     const Seqs q = make_seqs(p.cu, p.B, p.T, p.nseq);
