@@ -606,3 +606,70 @@ def test_refusals(cuda_lib):
     assert e.value.status == mg.MG_ERR_UNSUPPORTED
     with pytest.raises(mg.MgScanError):
         mg.group_norm_fwd(x, z(8), eps=-1.0)
+
+
+# ------------------------------------------- rows that 16-byte vectors do not fit
+
+def _framed(t, before, after):
+    """The tensor inside wider rows whose other values are NaN (`before` keeps
+    the data's 16-byte alignment)."""
+    wide = torch.full((*t.shape[:-1], before + t.shape[-1] + after), float("nan"), dtype=t.dtype, device=DEV)
+    inner = wide[..., before:before + t.shape[-1]]
+    inner.copy_(t)
+    return inner
+
+
+@pytest.mark.parametrize("D,N,G", [(33, 16, 1), (129, 12, 1), (66, 6, 2), (45, 24, 3), (21, 33, 1), (70, 3, 1), (257, 8, 1)])
+@pytest.mark.parametrize("after", [1, 2, 7])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scan_rows_of_any_alignment(cuda_lib, D, N, G, after, dtype):
+    """Odd widths and row strides: the values between the rows, NaN here, reach
+    no result."""
+    c = Scan(cuda_lib, 2, 41, D, N, G=G, dtype=dtype, seed=D + after)
+    c.x, c.raw, c.dy = _framed(c.x, 8, after), _framed(c.raw, 0, after + 1), _framed(c.dy, 16, 2 * after)
+    c.check()
+
+
+@pytest.mark.parametrize("shape", [(9, 1001, 1), (5, 4097, 1), (300, 126, 2), (70, 250, 1), (33, 515, 5), (3, 2050, 1),
+                                   (40, 1024, 1), (40, 2048, 1), (90, 512, 1), (6, 1536, 1), (700, 128, 2)], ids=str)
+@pytest.mark.parametrize("gate", ["none", "after", "first"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_norm_group_widths(cuda_lib, shape, gate, dtype):
+    """Groups of every way to hold them: pairs of any alignment, one or two
+    vectors a thread, a part of a warp, a warp, a block."""
+    _norm(cuda_lib, *shape, dtype, gate, rms=gate == "first", seed=sum(shape), wide=shape[1] % 8 == 0)
+
+
+@pytest.mark.parametrize("D,G", [(1001, 7), (250, 1), (40, 8), (77, 1)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_norm_rows_among_nans(cuda_lib, D, G, dtype):
+    mg = cuda_lib
+    x, z, dy = (torch.randn(21, D, device=DEV).to(dtype) for _ in range(3))
+    w = torch.randn(D, device=DEV)
+    fx, fz, fdy = _framed(x, 8, 3), _framed(z, 16, 1), _framed(dy, 0, 5)
+    y, st = mg.group_norm_fwd(x, w, w, z, groups=G)
+    fy, fst = mg.group_norm_fwd(fx, w, w, fz, groups=G)
+    assert torch.equal(y, fy) and torch.equal(st, fst)
+    for a, b in zip(mg.group_norm_bwd(dy, st, x, w, w, z, groups=G), mg.group_norm_bwd(fdy, st, fx, w, w, fz, groups=G)):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("B,D,W", [(1, 1, 4), (5, 44, 4), (9, 1025, 3), (13, 514, 8), (4, 8, 1)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_conv_step_batches(cuda_lib, B, D, W, dtype):
+    """Batches that end inside a thread's rows, with idle rows among them."""
+    mg = cuda_lib
+    r = _rng(B + D)
+    x, nx = _dev(r.normal(size=(B, D)), dtype)
+    w, nw = _dev(r.normal(size=(D, W)))
+    b, nb = _dev(r.normal(size=D))
+    pool, npool = _dev(r.normal(size=(2 * B, W - 1, D)), dtype)
+    slots = r.permutation(2 * B)[:B]
+    slots[B // 2] = -1 if B > 1 else slots[0]
+    y = mg.causal_conv_step(x, w, pool, b, slots=torch.from_numpy(slots).to(DEV), out=_nan((B, D), dtype))
+    want, state = o.conv_step(nx, nw, nb, npool, slots)
+    scale = np.abs(nx * nw[:, -1]) + np.abs(nb)
+    for j in range(W - 1):
+        scale = scale + np.abs(nw[:, j]) * np.abs(npool[np.maximum(slots, 0), j])
+    _near("y", y, want, scale, W)
+    assert np.array_equal(_np(pool), state)
