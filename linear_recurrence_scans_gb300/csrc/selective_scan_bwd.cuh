@@ -37,10 +37,11 @@ namespace mg {
 // -> 838 us); the block's warps meet once a tile to add their dB and dC.
 //
 // 4 x 4096 x 2048 channels of 16 states take 780 us, 0.69e12 states a second:
-// 120 for the first pass, 630 here and 20 for the sums of the parts.  The
-// arithmetic bounds it (some 17 instructions a state, one of them an
-// exponential, twice over), at half the issue slots with two warps a
-// scheduler, which is what the registers of kSub rows leave.
+// 120 for the first pass, 620 here and 20 for the sums of the parts.
+// Instructions bound it: 23 a state (10 of them the formulas', each state's
+// exponential taken twice), at half the issue slots with two warps a
+// scheduler, which is what the registers of kSub rows leave.  (B and C kept
+// twice over as ready pairs: 847 us; u staged next to x: no change.)
 constexpr int kSub = 4;
 
 // v over LANES lanes (bits STRIDE .. of the lane index; `id` is the lane's
