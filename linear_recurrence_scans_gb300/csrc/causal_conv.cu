@@ -42,65 +42,57 @@ __device__ __forceinline__ Lanes<VEC> load_lanes(const T *from)
 // A thread's own ring of rows in shared memory, filled by asynchronous copies
 // kGroups - 1 groups ahead of the one at hand: what is in flight takes no
 // registers, and no other thread reads it, so nothing but the thread's own
-// copies is waited for.  Rows of 2 bytes, which no asynchronous copy moves,
-// are loaded when they are needed.
+// copies is waited for.  A single bf16 comes as the 4-byte word that it is a
+// half of, with the value before it, or alone (8 x 4096 x 1001 channels: 54
+// us and 93 for the gradients, where loads at the use took 64 and 120).
 template <typename T, int VEC>
 struct Ring {
-    static constexpr int kBytes = int(sizeof(T)) * VEC;
-    static constexpr bool kAsync = kBytes >= 4;
-    static constexpr size_t bytes(int threads) { return kAsync ? size_t(kGroups) * kUnroll * threads * kBytes : 0; }
-    T *mine;            // the thread's vector of ring row 0
-    const T *next;      // the next row to be copied (or loaded)
+    static constexpr bool kHalf = sizeof(T) * VEC == 2;
+    static constexpr int kBytes = kHalf ? 4 : int(sizeof(T)) * VEC;
+    static constexpr size_t bytes(int threads) { return size_t(kGroups) * kUnroll * threads * kBytes; }
+    unsigned char *mine;   // the thread's slot of ring row 0
+    const T *next;         // the next row to be copied
     int64_t ld;
-    Raw<T, VEC> here[kAsync ? 1 : kUnroll];   // the group at hand, where nothing is copied ahead
+    bool upper, turns;     // kHalf: a group's first row is an upper half; its rows take turns
     __device__ __forceinline__ Ring(unsigned char *base, const T *first, int64_t stride) : next(first), ld(stride)
     {
-        mine = reinterpret_cast<T *>(base) + (threadIdx.y * blockDim.x + threadIdx.x) * VEC;
+        mine = base + (threadIdx.y * blockDim.x + threadIdx.x) * kBytes;
+        upper = reinterpret_cast<uintptr_t>(first) % 4 != 0;
+        turns = stride % 2 != 0;
     }
-    __device__ __forceinline__ T *at(int row) const { return mine + row * kBlock * VEC; }
+    __device__ __forceinline__ unsigned char *at(int row) const { return mine + row * kBlock * kBytes; }
+    static_assert(kUnroll % 2 == 0, "a group begins like the first one");
+    __device__ __forceinline__ bool half(int i) const { return upper != (turns && i % 2 != 0); }
     // Starts the copies of the rows i0 .. of a run of n into ring group g.
     __device__ __forceinline__ void fetch(int g, int i0, int n)
     {
-        if constexpr (kAsync) {
 #pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                if (i0 + i < n) {
-                    if constexpr (kBytes == 16)
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" : : "r"(smem_addr(at(g * kUnroll + i))),
-                                     "l"(next) : "memory");
-                    else
-                        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" : : "r"(smem_addr(at(g * kUnroll + i))),
-                                     "l"(next), "n"(kBytes) : "memory");
-                }
-                next += ld;
+        for (int i = 0; i < kUnroll; ++i) {
+            if (i0 + i < n) {
+                const unsigned to = smem_addr(at(g * kUnroll + i));
+                if constexpr (kHalf)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" : : "r"(to),
+                                 "l"(half(i) ? next - 1 : next), "r"(half(i) ? 4 : 2) : "memory");
+                else if constexpr (kBytes == 16)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" : : "r"(to), "l"(next) : "memory");
+                else
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" : : "r"(to), "l"(next), "n"(kBytes)
+                                 : "memory");
             }
-        }
-    }
-    // The group at hand, rows i0 .. of a run of n.
-    __device__ __forceinline__ void open(int i0, int n)
-    {
-        if constexpr (!kAsync) {
-#pragma unroll
-            for (int i = 0; i < kUnroll; ++i) {
-                if (i0 + i < n) here[i].load(next);
-                next += ld;
-            }
+            next += ld;
         }
     }
     // Row i of ring group g, the group at hand.
     __device__ __forceinline__ Lanes<VEC> get(int g, int i) const
     {
-        if constexpr (kAsync) return load_lanes<T, VEC>(at(g * kUnroll + i));
-        else return vraw<T, VEC>(here[i]);
-    }
-    __device__ __forceinline__ Lanes<VEC> get_any(int g, int i) const   // i not known when compiled
-    {
-        if constexpr (kAsync) return load_lanes<T, VEC>(at(g * kUnroll + i));
-        Raw<T, VEC> r = here[0];
-#pragma unroll
-        for (int k = 1; k < (kAsync ? 1 : kUnroll); ++k)
-            if (i == k) r = here[k];
-        return vraw<T, VEC>(r);
+        if constexpr (kHalf) {
+            const unsigned w = *reinterpret_cast<const unsigned *>(at(g * kUnroll + i));
+            Lanes<VEC> v;
+            v.p[0] = __uint_as_float(half(i) ? w & 0xffff0000u : w << 16);
+            return v;
+        } else {
+            return load_lanes<T, VEC>(reinterpret_cast<const T *>(at(g * kUnroll + i)));
+        }
     }
 };
 
@@ -269,7 +261,6 @@ __global__ void __launch_bounds__(kBlock, kFwdPerSm) conv_fwd_kernel(ConvArgs p,
         ring.fetch(g == 0 ? kGroups - 1 : g - 1, i0 + (kGroups - 1) * kUnroll, n);
         cp_async_commit();
         cp_async_wait<kGroups - 1>();
-        ring.open(i0, n);
         if (i0 + kUnroll <= n && k.hi > i0 + kUnroll) {   // whole, inside one sequence
 #pragma unroll
             for (int i = 0; i < kUnroll; ++i) {
@@ -284,7 +275,7 @@ __global__ void __launch_bounds__(kBlock, kFwdPerSm) conv_fwd_kernel(ConvArgs p,
 #pragma unroll
                     for (int j = 0; j < W - 1; ++j) win[j + 1] = load_edge<T, VEC, W>(x0, k.s, j, D, d);
                 }
-                row(ring.get_any(g, i - i0), yp);
+                row(ring.get(g, i - i0), yp);
                 yp += D;
                 if (i + 1 == k.hi && x_last != nullptr) {
 #pragma unroll
@@ -383,9 +374,7 @@ __global__ void __launch_bounds__(kBlock, kBwdPerSm) conv_bwd_kernel(ConvArgs p,
             ring_g.fetch(g == 0 ? kGroups - 1 : g - 1, i0 + (kGroups - 1) * kUnroll, n);
             cp_async_commit();
             cp_async_wait<kGroups - 1>();
-            ring.open(i0, n);
-            ring_g.open(i0, n);
-            // whole, inside one sequence and the run, and no row before the
+                // whole, inside one sequence and the run, and no row before the
             // sequence is completed
             if (i0 + kUnroll <= own && k.hi > i0 + kUnroll && (k.lo < 0 || i0 - (W - 1) >= k.lo)) {
 #pragma unroll
@@ -409,7 +398,7 @@ __global__ void __launch_bounds__(kBlock, kBwdPerSm) conv_bwd_kernel(ConvArgs p,
                             acc[j + 1] = vset<VEC>(0.f);
                         }
                     }
-                    row(ring.get_any(g, i - i0), ring_g.get_any(g, i - i0), i < own);
+                    row(ring.get(g, i - i0), ring_g.get(g, i - i0), i < own);
                     emit(i - (W - 1), acc[0]);
                     dxp += D;
                     if (i + 1 == k.hi) {   // the sequence ends: the rest is complete too

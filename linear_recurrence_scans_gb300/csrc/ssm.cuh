@@ -306,14 +306,6 @@ __device__ __forceinline__ Lanes<VEC> vset(float c)
     for (int i = 0; i < VEC; ++i) f[i] = c;
     return vfrom<VEC>(f);
 }
-template <typename T, int VEC>
-__device__ __forceinline__ Lanes<VEC> vraw(const Raw<T, VEC> &x)
-{
-    float f[VEC];
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) f[i] = x[i];
-    return vfrom<VEC>(f);
-}
 // sigmoid as 1 / (1 + 2^(-v log2 e)): for v far below 0 the power is infinite
 // and the quotient 0.
 template <int VEC>
