@@ -496,6 +496,7 @@ __global__ void __launch_bounds__(256) sum_parts_kernel(const float *part, int64
                                                         SumOuts outs)
 {
     __shared__ float s[8][33];
+    after_previous();
     const int64_t i = int64_t(blockIdx.x) * 32 + threadIdx.x;
     float a = 0.f;
     if (i < stride) {
@@ -654,8 +655,7 @@ mg_status launch_sum_parts(const float *part, int64_t parts, std::initializer_li
         o.o[k++] = x;
         stride += x.n;
     }
-    sum_parts_kernel<<<unsigned(ceil_div(stride, 32)), dim3(32, 8), 0, s>>>(part, parts, stride, o);
-    return launched("sum over parts");
+    return launch_next("sum over parts", sum_parts_kernel, ceil_div(stride, 32), dim3(32, 8), 0, s, part, parts, stride, o);
 }
 
 }  // namespace mg

@@ -79,6 +79,7 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
     static_assert(C == 2 && WCH % VEC == 0 && kCols <= 32 && (VEC > 1 || kPer % 2 == 0), "staging");
     using Shared = FwdShared<T, VEC, WCH, NP, kFirst>;
     extern __shared__ __align__(16) unsigned char shared_bytes[];
+    if (kFirst) after_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     Shared &sm = reinterpret_cast<Shared *>(shared_bytes)[warp];
 
@@ -190,6 +191,7 @@ ssm_chunk_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, float *agg_h, float *agg
     // where the sequence ends, in rows from the chunk's first
     auto ends = [&]() { return kBack ? rowb + t1 - q.begin(s) : q.begin(s + 1) - (rowb + t0); };
     long long next = ends();
+    if (!kFirst) after_previous();   // the chunks' states
     {
         const long long lo = q.begin(s) - rowb;
         if (kBack ? q.begin(s + 1) - rowb <= t1 : lo >= t0) {
@@ -598,14 +600,18 @@ mg_status fwd_cover(const SsmArgs &p, cudaStream_t s)
     constexpr size_t sm2 = kThreads / 32 * sizeof(FwdShared<T, VEC, CV::kWarpCh, CV::NP, false>);
     MG_TRY(allow_shared<ssm_chunk_kernel<T, VEC, CV, kStates>>(sm1));
     MG_TRY(allow_shared<ssm_chunk_kernel<T, VEC, CV, kOutputs>>(sm2));
+    bool first = p.cu == nullptr;   // of the call's kernels
+    auto ours = [&](auto kernel, int64_t grid, size_t smem) {
+        constexpr const char *what = "mg_selective_scan_fwd";
+        if (!first) return launch_next(what, kernel, grid, kThreads, smem, s, p, q, t, ck, agg_h, agg_s, mode);
+        kernel<<<unsigned(grid), kThreads, smem, s>>>(p, q, t, ck, agg_h, agg_s, mode);
+        return launched(what);
+    };
     if (ck.n > 1) {
-        ssm_chunk_kernel<T, VEC, CV, kStates><<<unsigned(tiles * (ck.n - 1)), kThreads, sm1, s>>>(
-            p, q, t, ck, agg_h, agg_s, mode);
-        MG_TRY(launched("mg_selective_scan_fwd"));
+        MG_TRY(ours(ssm_chunk_kernel<T, VEC, CV, kStates>, tiles * (ck.n - 1), sm1));
+        first = false;
     }
-    ssm_chunk_kernel<T, VEC, CV, kOutputs><<<unsigned(tiles * ck.n), kThreads, sm2, s>>>(p, q, t, ck, agg_h, agg_s,
-                                                                                    mode);
-    return launched("mg_selective_scan_fwd");
+    return ours(ssm_chunk_kernel<T, VEC, CV, kOutputs>, tiles * ck.n, sm2);
 }
 
 template <typename T, int VEC, typename CV>
@@ -616,8 +622,11 @@ mg_status adjoint_cover(const SsmArgs &p, const Chunks &ck, float *agg_q, float 
     const Seqs q = make_seqs(p.cu, p.B, p.T, p.nseq);
     constexpr size_t sm = kThreads / 32 * sizeof(FwdShared<T, VEC, CV::kWarpCh, CV::NP, true>);
     MG_TRY(allow_shared<ssm_chunk_kernel<T, VEC, CV, kAdjoint>>(sm));
-    ssm_chunk_kernel<T, VEC, CV, kAdjoint><<<unsigned(t.tiles * p.G * p.B * (ck.n - 1)), kThreads, sm, s>>>(
-        p, q, t, ck, agg_q, agg_s, mode);
+    const int64_t grid = t.tiles * p.G * p.B * (ck.n - 1);
+    auto kernel = ssm_chunk_kernel<T, VEC, CV, kAdjoint>;
+    if (p.cu != nullptr)
+        return launch_next("mg_selective_scan_bwd", kernel, grid, kThreads, sm, s, p, q, t, ck, agg_q, agg_s, mode);
+    kernel<<<unsigned(grid), kThreads, sm, s>>>(p, q, t, ck, agg_q, agg_s, mode);
     return launched("mg_selective_scan_bwd");
 }
 

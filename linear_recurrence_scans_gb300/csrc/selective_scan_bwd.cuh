@@ -243,26 +243,6 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
 
     int s = q.of(w.rowb + w.t1 - 1);
     long long lo = q.begin(s) - w.rowb, hi = q.begin(s + 1) - w.rowb;
-    if (hi > w.t1) {   // the chunk's last sequence goes on: fold its later chunks
-        int64_t j = ((hi < p.T ? hi : p.T) - 1) / ck.len;
-        bool begin = true;
-        for (; j > w.k; --j) {
-            const int64_t at = (w.b * (ck.n - 1) + j - 1) * p.D;
-            pair_t v[S][CP];
-            load_block<S, CP>(agg_q + at * p.N, dw + ch, ch, wide, n0, p.N, v);
-            float ds[C];
-#pragma unroll
-            for (int c = 0; c < C; ++c) ds[c] = ch + c < wide ? agg_s[at + dw + ch + c] : 0.f;
-#pragma unroll
-            for (int i = 0; i < S; ++i)
-#pragma unroll
-                for (int c = 0; c < CP; ++c)
-                    ag[i][c] = begin ? v[i][c]
-                                     : fma2(decay2(ds[2 * c], ds[2 * c + 1], A2[i][c]), ag[i][c], v[i][c]);
-            begin = false;
-        }
-    }
-
     const T *x0p = static_cast<const T *>(p.x), *r0p = static_cast<const T *>(p.raw), *y0p = static_cast<const T *>(p.dy);
     const int64_t xf = w.rowb * p.ldx + dw, rf = w.rowb * p.ldraw + dw, yf = w.rowb * p.lddy + dw;
     const T *xp = x0p + xf, *rp = r0p + rf, *yp = y0p + yf;
@@ -491,6 +471,26 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
     fetch(t);
     fetch_state(t);
     cp_async_commit();
+    after_previous();   // the chunks' states
+    if (hi > w.t1) {   // the chunk's last sequence goes on: fold its later chunks
+        int64_t j = ((hi < p.T ? hi : p.T) - 1) / ck.len;
+        bool begin = true;
+        for (; j > w.k; --j) {
+            const int64_t at = (w.b * (ck.n - 1) + j - 1) * p.D;
+            pair_t v[S][CP];
+            load_block<S, CP>(agg_q + at * p.N, dw + ch, ch, wide, n0, p.N, v);
+            float ds[C];
+#pragma unroll
+            for (int c = 0; c < C; ++c) ds[c] = ch + c < wide ? agg_s[at + dw + ch + c] : 0.f;
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+#pragma unroll
+                for (int c = 0; c < CP; ++c)
+                    ag[i][c] = begin ? v[i][c]
+                                     : fma2(decay2(ds[2 * c], ds[2 * c + 1], A2[i][c]), ag[i][c], v[i][c]);
+            begin = false;
+        }
+    }
     for (; t >= w.t0; t -= kTile) {
         const int64_t end = t + kTile < w.t1 ? t + kTile : w.t1;
         cp_async_wait<0>();
@@ -629,6 +629,7 @@ __global__ void __launch_bounds__(256) sum_bc_kernel(const float *part, int64_t 
                                                      int N, T *dB, T *dC)
 {
     const int64_t n = rows_g * 2 * N, i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+    after_previous();
     if (i >= n) return;
     float a = 0.f;
     for (int64_t t = 0; t < tiles; ++t) a += part[t * n + i];
@@ -682,12 +683,16 @@ mg_status bwd(const SsmArgs &p, cudaStream_t s)
     constexpr size_t smem = sizeof(BwdShared<T, VEC, CV>);
     static_assert(smem <= kMostShared, "shared memory of a block");
     MG_TRY(allow_shared<ssm_bwd_kernel<T, VEC, CV>>(smem));
-    ssm_bwd_kernel<T, VEC, CV><<<unsigned(tiles * ck.n), CV::THREADS, smem, s>>>(p, q, t, ck, agg_q, agg_s, partB,
-                                                                             partA, mode);
-    MG_TRY(launched("mg_selective_scan_bwd"));
-    sum_bc_kernel<T><<<unsigned(ceil_div(rows_g * 2 * p.N, 256)), 256, 0, s>>>(
-        partB, t.tiles, rows_g, p.N, static_cast<T *>(p.dBm), static_cast<T *>(p.dCm));
-    MG_TRY(launched("mg_selective_scan_bwd"));
+    constexpr const char *what = "mg_selective_scan_bwd";
+    auto kernel = ssm_bwd_kernel<T, VEC, CV>;
+    if (ck.n > 1 || p.cu != nullptr) {   // not the call's first
+        MG_TRY(launch_next(what, kernel, tiles * ck.n, CV::THREADS, smem, s, p, q, t, ck, agg_q, agg_s, partB, partA, mode));
+    } else {
+        kernel<<<unsigned(tiles), CV::THREADS, smem, s>>>(p, q, t, ck, agg_q, agg_s, partB, partA, mode);
+        MG_TRY(launched(what));
+    }
+    MG_TRY(launch_next(what, sum_bc_kernel<T>, ceil_div(rows_g * 2 * p.N, 256), 256, 0, s, partB, t.tiles, rows_g, p.N,
+                       static_cast<T *>(p.dBm), static_cast<T *>(p.dCm)));
     return launch_sum_parts(partA, parts, {{p.dA, dn}, {p.dDskip, p.D}, {p.ddt_bias, p.D}}, s);
 }
 

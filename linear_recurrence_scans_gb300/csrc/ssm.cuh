@@ -115,6 +115,30 @@ inline mg_status launched(const char *what)
     return e == cudaSuccess ? MG_OK : fail(MG_ERR_LAUNCH, "%s: %s", what, cudaGetErrorString(e));
 }
 
+// Launches a kernel that is set up while the kernel before it in the stream,
+// one of the same call, comes to its end: until after_previous() it reads only
+// the call's inputs.  1 x 2048 x 2048 channels of 16 states: forward (two
+// kernels) 61 -> 58 us, gradients (four) 141 -> 133.  (Begun earlier, once the
+// other's last blocks run, the second's blocks gather on the SMs that are
+// free first: 74 us.)
+template <typename... P, typename... A>
+mg_status launch_next(const char *what, void (*kernel)(P...), int64_t grid, dim3 block, size_t smem, cudaStream_t s,
+                      const A &...args)
+{
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(unsigned(grid));
+    c.blockDim = block;
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = &early;
+    c.numAttrs = 1;
+    cudaLaunchKernelEx(&c, kernel, P(args)...);
+    return launched(what);
+}
+
 // Dynamic shared memory beyond the default 48 KB (which count static shared
 // memory too): allowed once for a kernel and device, up to what a block may
 // have.  The set-up costs as much as a launch.
@@ -138,6 +162,11 @@ mg_status allow_shared(size_t bytes)
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ---------------------------------------------------------- device side
+
+// Waits until the kernel before this one has ended and its writes are seen.
+// Every kernel that launch_next starts has every block come here, so that the
+// end of the last one means the end of all.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" : : : "memory"); }
 
 // One value of an activation tensor.
 __device__ __forceinline__ float load1(const float *p) { return *p; }

@@ -673,3 +673,38 @@ def test_conv_step_batches(cuda_lib, B, D, W, dtype):
         scale = scale + np.abs(nw[:, j]) * np.abs(npool[np.maximum(slots, 0), j])
     _near("y", y, want, scale, W)
     assert np.array_equal(_np(pool), state)
+
+
+@pytest.mark.parametrize("cu", [None, [0, 5, 5, 300, 700]])
+def test_graph_capture_of_a_training_step(cuda_lib, cu):
+    """Forward and gradients in a CUDA graph (several dependent kernels a call),
+    replayed on new inputs, equal the calls' own results."""
+    mg = cuda_lib
+    B, T, D, N = (1, 700, 200, 16) if cu else (3, 333, 200, 16)
+    x, dy = (torch.randn(B, T, D, device=DEV).bfloat16() for _ in range(2))
+    bc = torch.randn(B, T, 2 * N, device=DEV).bfloat16()
+    A, b, w = -torch.rand(D, N, device=DEV) - 0.1, torch.full((D,), -3.0, device=DEV), torch.randn(D, 4, device=DEV)
+    seqs = None if cu is None else torch.tensor(cu, dtype=torch.int64, device=DEV)
+
+    def step():
+        args = (x, x, A, bc[..., :N], bc[..., N:], b, b)
+        y, last, saved = mg.selective_scan_fwd(*args, save=True, cu_seqlens=seqs)
+        n, stats = mg.group_norm_fwd(y, b, b, x, groups=2)
+        return (y, last, n, *mg.selective_scan_bwd(dy, saved, *args, cu_seqlens=seqs),
+                *mg.group_norm_bwd(dy, stats, y, b, b, x, groups=2), *mg.causal_conv_bwd(dy, x, w, b, cu_seqlens=seqs))
+
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        step()   # the stream's workspace
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        got = step()
+    for _ in range(5):
+        x.normal_()
+        want = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(a is None or torch.equal(a, v) for a, v in zip(got, want))
+    mg.workspace_status()
