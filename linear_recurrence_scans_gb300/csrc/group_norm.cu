@@ -90,49 +90,86 @@ __device__ __forceinline__ Lanes<VEC> vact(const Lanes<VEC> &v, int silu, Lanes<
     return vmul<VEC>(v, s);
 }
 
-// Vectors of two values stand for groups and rows that 16-byte vectors do not
-// fit: they start at any value, and a group's last one may hold one value
-// (`count` of them; the other reads as 0 and is not written).
+// Vectors of half that (4 bf16, 2 float32) stand for groups and rows that
+// 16-byte vectors do not fit: they start at any value, and a group's last one
+// may hold fewer (`count`; the others read as 0 and are not written).
+template <typename T, int VEC>
+constexpr bool kRagged = VEC * sizeof(T) < 16;
 template <int VEC, typename T>
-__device__ __forceinline__ Lanes<VEC> vload(const T *from, int count)
+__device__ __forceinline__ Lanes<VEC> vload_any(const T *from, int count)
 {
     float f[VEC];
-    if constexpr (VEC == 2) {
-        f[0] = load1(from);
-        f[1] = count > 1 ? load1(from + 1) : 0.f;
-    } else {
-        load_vec<VEC>(from, f);
-    }
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) f[e] = e < count ? load1(from + e) : 0.f;
     return vfrom<VEC>(f);
 }
 template <int VEC, typename T>
-__device__ __forceinline__ void vstore(T *to, const Lanes<VEC> &v, int count)
+__device__ __forceinline__ void vstore_any(T *to, const Lanes<VEC> &v, int count)
 {
     float f[VEC];
     vto<VEC>(v, f);
-    if constexpr (VEC == 2) {
-        if (count > 1 && reinterpret_cast<uintptr_t>(to) % (2 * sizeof(T)) == 0) {
-            store_vec<2>(to, f);
+    const int lead = int(reinterpret_cast<uintptr_t>(to) / sizeof(T) % 2);   // a value before the first whole pair
+    if (count >= VEC) {
+        if (lead == 0) {
+#pragma unroll
+            for (int e = 0; e < VEC; e += 2) store_vec<2>(to + e, reinterpret_cast<const float (&)[2]>(f[e]));
         } else {
             store1(to, f[0]);
-            if (count > 1) store1(to + 1, f[1]);
+#pragma unroll
+            for (int e = 1; e + 1 < VEC; e += 2) store_vec<2>(to + e, reinterpret_cast<const float (&)[2]>(f[e]));
+            store1(to + VEC - 1, f[VEC - 1]);
         }
     } else {
+#pragma unroll
+        for (int e = 0; e + 1 < VEC; ++e)
+            if (e < count) store1(to + e, f[e]);
+    }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void vstore(T *to, const Lanes<VEC> &v, int count)
+{
+    if constexpr (kRagged<T, VEC>) {
+        vstore_any<VEC>(to, v, count);
+    } else {
+        float f[VEC];
+        vto<VEC>(v, f);
         store_out<VEC>(to, f);
+    }
+}
+// The values of a parameter, or sums, that go with a vector of T.
+template <typename T, int VEC>
+__device__ __forceinline__ Lanes<VEC> pload(const float *from, int count)
+{
+    if constexpr (kRagged<T, VEC>) return vload_any<VEC>(from, count);
+    float f[VEC];
+    load_vec<VEC>(from, f);
+    return vfrom<VEC>(f);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void pstore(float *to, const Lanes<VEC> &v, int count)
+{
+    if constexpr (kRagged<T, VEC>) {
+        vstore_any<VEC>(to, v, count);
+    } else {
+        float f[VEC];
+        vto<VEC>(v, f);
+        store_vec<VEC>(to, f);
     }
 }
 
 // A thread's vectors of the rows to come, K tensors of them: slots of shared
-// memory that only the thread's own copies fill.  Two values come as the
-// 4-byte words that hold them: two bf16 that start in the middle of a word as
-// its two words, of which the value before them (never the first of a tensor)
-// is dropped.  8192 rows of 7 groups of 143 bf16 take 68 us, and the gradients
-// 92; single values, loaded where they are used, took 63 and 192, and one
-// group of 1001 136 and 157, now 62 and 86.  Instructions bound these.
+// memory that only the thread's own copies fill.  Ragged vectors come as the
+// 4-byte words that hold them: 4 bf16 that start in the middle of a word as
+// three, of which the value before them (never the first of a tensor) is
+// dropped.  8192 rows of 1001 bf16 channels in one group take 56 us, the
+// gradients 75, in 7 groups 66 and 88 (as pairs 62 and 86, 68 and 93; single
+// values loaded where they are used 136 and 157, 63 and 192).  Instructions
+// bound these.
 template <typename T, int VEC, int NV, int K>
 struct Ahead {
-    static constexpr int kBytes = VEC == 2 ? 8 : int(sizeof(T)) * VEC;
-    static constexpr bool kAsync = NV <= (VEC == 2 ? 4 : 2);
+    static constexpr bool kRag = kRagged<T, VEC>;
+    static constexpr int kBytes = kRag && sizeof(T) == 4 ? 8 : 16;
+    static constexpr bool kAsync = NV * kBytes <= 32;
     static size_t bytes(int threads) { return kAsync ? size_t(kAhead) * K * NV * threads * kBytes : 0; }
     unsigned char *mine;
     __device__ __forceinline__ unsigned char *at(int slot, int k, int i) const
@@ -140,41 +177,41 @@ struct Ahead {
         return mine + size_t((slot * K + k) * NV + i) * blockDim.x * kBytes;
     }
     static __device__ __forceinline__ bool odd(const T *from) { return reinterpret_cast<uintptr_t>(from) % 4 != 0; }
-    static __device__ __forceinline__ void word(unsigned char *to, const void *from, int bytes)
-    {
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" : : "r"(smem_addr(to)), "l"(from), "r"(bytes)
-                     : "memory");
-    }
     __device__ __forceinline__ void fetch(int slot, int k, int i, const T *from, int count) const
     {
-        unsigned char *to = at(slot, k, i);
+        const unsigned to = smem_addr(at(slot, k, i));
         if constexpr (!kAsync) {
             return;
-        } else if constexpr (VEC > 2) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" : : "r"(smem_addr(to)), "l"(from) : "memory");
-        } else if constexpr (sizeof(T) == 4) {
-            word(to, from, 4);
-            word(to + 4, count > 1 ? from + 1 : from, count > 1 ? 4 : 0);
+        } else if constexpr (!kRag) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" : : "r"(to), "l"(from) : "memory");
         } else {
-            const T *first = reinterpret_cast<const T *>(reinterpret_cast<uintptr_t>(from) & ~uintptr_t(3));
-            const bool mid = first != from, two = count > 1;
-            word(to, first, mid || two ? 4 : 2);
-            word(to + 4, mid && two ? first + 2 : first, mid && two ? 2 : 0);
+            // the vector's bytes from the start of its first word
+            const int lead = odd(from) ? 2 : 0, all = lead + (count < VEC ? count : VEC) * int(sizeof(T));
+            const char *first = reinterpret_cast<const char *>(from) - lead;
+#pragma unroll
+            for (int b = 0; b < VEC * int(sizeof(T)) + (sizeof(T) == 2 ? 4 : 0); b += 4) {
+                const int n = all - b > 4 ? 4 : all - b;
+                if (b < VEC * int(sizeof(T)) || lead != 0)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" : : "r"(to + b),
+                                 "l"(n > 0 ? first + b : first), "r"(n > 0 ? n : 0) : "memory");
+            }
         }
     }
     __device__ __forceinline__ Lanes<VEC> get(int slot, int k, int i, const T *from, int count) const
     {
-        if constexpr (!kAsync) {
-            return vload<VEC>(from, count);
-        } else if constexpr (VEC == 2 && sizeof(T) == 2) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(at(slot, k, i));
-            const unsigned two = odd(from) ? __funnelshift_r(w.x, w.y, 16) : w.x;
+        if constexpr (!kAsync && kRag) {
+            return vload_any<VEC>(from, count);
+        } else if constexpr (kRag && sizeof(T) == 2) {
+            const uint4 w = *reinterpret_cast<const uint4 *>(at(slot, k, i));
+            const bool mid = odd(from);
+            const unsigned a = mid ? __funnelshift_r(w.x, w.y, 16) : w.x, b = mid ? __funnelshift_r(w.y, w.z, 16) : w.y;
             Lanes<VEC> v;
-            v.p[0] = pack2(__uint_as_float(two << 16), __uint_as_float(two & 0xffff0000u));
+            v.p[0] = pack2(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+            v.p[1] = pack2(__uint_as_float(b << 16), __uint_as_float(b & 0xffff0000u));
             return v;
         } else {
             float o[VEC];
-            load_vec<VEC>(reinterpret_cast<const T *>(at(slot, k, i)), o);
+            load_vec<VEC>(kAsync ? reinterpret_cast<const T *>(at(slot, k, i)) : from, o);
             return vfrom<VEC>(o);
         }
     }
@@ -198,7 +235,7 @@ struct Team {
 
 // SILU: 1 where the activation is known to be SiLU when compiled, else -1.
 template <typename T, int VEC, int NV, mg_gate GATE, int TEAM, int SILU>
-__global__ void __launch_bounds__(512, NV == 1 || (VEC == 2 && NV <= 4) ? 2 : 1)
+__global__ void __launch_bounds__(512, NV == 1 || (kRagged<T, VEC> && NV <= 4) ? 2 : 1)
 norm_fwd_kernel(NormArgs p, int team_size, int row_teams)
 {
     const int tpg = TEAM > 0 ? TEAM : team_size, silu = SILU == 1 ? 1 : p.silu;
@@ -220,8 +257,8 @@ norm_fwd_kernel(NormArgs p, int team_size, int row_teams)
         in[i] = team.live && c[i] < gs;
         w[i] = b[i] = vset<VEC>(0.f);
         if (in[i]) {
-            w[i] = vload<VEC>(p.w + team.d0 + c[i], gs - c[i]);
-            if (p.bias != nullptr) b[i] = vload<VEC>(p.bias + team.d0 + c[i], gs - c[i]);
+            w[i] = pload<T, VEC>(p.w + team.d0 + c[i], gs - c[i]);
+            if (p.bias != nullptr) b[i] = pload<T, VEC>(p.bias + team.d0 + c[i], gs - c[i]);
         }
     }
     const int64_t xs = row_teams * p.ldx, zs = row_teams * p.ldz, ys = row_teams * p.D;
@@ -266,15 +303,19 @@ norm_fwd_kernel(NormArgs p, int team_size, int row_teams)
             }
         }
         float mean = 0.f;
-        Lanes<VEC> first = vset<VEC>(1.f);
-        if constexpr (VEC == 2) first.p[0] = pack2(1.f, 0.f);
         if (!p.rms) mean = team_sum<TEAM>(sum, tpg, buf[0]) * inv;
         float sq = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
             if (in[i] && live) {
                 f[i] = vadd<VEC>(f[i], vset<VEC>(-mean));
-                if (VEC == 2 && c[i] + 1 == gs) f[i] = vmul<VEC>(f[i], first);
+                if (kRagged<T, VEC> && c[i] + VEC > gs) {   // no difference where there is no channel
+                    float v[VEC];
+                    vto<VEC>(f[i], v);
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) v[e] = c[i] + e < gs ? v[e] : 0.f;
+                    f[i] = vfrom<VEC>(v);
+                }
                 sq += vdot<VEC>(f[i], f[i]);
             }
         // (one sum a row: the buffers take turns)
@@ -287,7 +328,7 @@ norm_fwd_kernel(NormArgs p, int team_size, int row_teams)
                     Lanes<VEC> o = vfma<VEC>(vmul<VEC>(f[i], vset<VEC>(rstd)), w[i], b[i]);
                     if (GATE == MG_GATE_AFTER) o = vmul<VEC>(o, gate[i]);
                     if (GATE == MG_GATE_NONE) o = vact<VEC>(o, silu);
-                    vstore<VEC>(y + c[i], o, gs - c[i]);
+                    vstore<T, VEC>(y + c[i], o, gs - c[i]);
                 }
         }
         x += xs;
@@ -326,8 +367,8 @@ norm_bwd_kernel(NormArgs p, int team_size, int row_teams, float *part)
         in[i] = team.live && c[i] < gs;
         w[i] = b[i] = dw[i] = db[i] = vset<VEC>(0.f);
         if (in[i]) {
-            w[i] = vload<VEC>(p.w + team.d0 + c[i], gs - c[i]);
-            if (GATE != MG_GATE_FIRST && p.bias != nullptr) b[i] = vload<VEC>(p.bias + team.d0 + c[i], gs - c[i]);
+            w[i] = pload<T, VEC>(p.w + team.d0 + c[i], gs - c[i]);
+            if (GATE != MG_GATE_FIRST && p.bias != nullptr) b[i] = pload<T, VEC>(p.bias + team.d0 + c[i], gs - c[i]);
         }
     }
     const int64_t xs = row_teams * p.ldx, zs = row_teams * p.ldz, gst = row_teams * p.lddy, os = row_teams * p.D;
@@ -379,7 +420,7 @@ norm_bwd_kernel(NormArgs p, int team_size, int row_teams, float *part)
                 if (GATE != MG_GATE_FIRST) {
                     const Lanes<VEC> o = vfma<VEC>(n[i], w[i], b[i]);
                     if (GATE == MG_GATE_AFTER) {
-                        vstore<VEC>(static_cast<T *>(p.dz) + out + c[i], vmul<VEC>(vmul<VEC>(dov, o), gg[i]), gs - c[i]);
+                        vstore<T, VEC>(static_cast<T *>(p.dz) + out + c[i], vmul<VEC>(vmul<VEC>(dov, o), gg[i]), gs - c[i]);
                         dov = vmul<VEC>(dov, ga[i]);
                     } else {
                         Lanes<VEC> grad;
@@ -401,10 +442,10 @@ norm_bwd_kernel(NormArgs p, int team_size, int row_teams, float *part)
                 Lanes<VEC> dp = vadd<VEC>(vfma<VEC>(n[i], vset<VEC>(-m2), dn[i]), vset<VEC>(-m1));
                 dp = vmul<VEC>(dp, rstd);
                 if (GATE == MG_GATE_FIRST) {
-                    vstore<VEC>(static_cast<T *>(p.dz) + out + c[i], vmul<VEC>(dp, gg[i]), gs - c[i]);
+                    vstore<T, VEC>(static_cast<T *>(p.dz) + out + c[i], vmul<VEC>(dp, gg[i]), gs - c[i]);
                     dp = vmul<VEC>(dp, ga[i]);
                 }
-                vstore<VEC>(static_cast<T *>(p.dx) + out + c[i], dp, gs - c[i]);
+                vstore<T, VEC>(static_cast<T *>(p.dx) + out + c[i], dp, gs - c[i]);
             }
         x += xs;
         z += zs;
@@ -418,8 +459,8 @@ norm_bwd_kernel(NormArgs p, int team_size, int row_teams, float *part)
 #pragma unroll
     for (int i = 0; i < NV; ++i)
         if (in[i]) {
-            vstore<VEC>(to + c[i], dw[i], gs - c[i]);
-            vstore<VEC>(to + p.D + c[i], db[i], gs - c[i]);
+            pstore<T, VEC>(to + c[i], dw[i], gs - c[i]);
+            pstore<T, VEC>(to + p.D + c[i], db[i], gs - c[i]);
         }
 }
 
@@ -437,7 +478,7 @@ int team_for(int64_t gs, int vec, int nv)
 int block_for(int tpg) { return tpg > 32 ? tpg : 256; }
 
 // (vector width, vectors a thread, team) of a call.  Vectors are 16 bytes
-// where the group's width and the rows allow, else two values.
+// where the group's width and the rows allow, else half that, ragged.
 //
 // A thread takes two vectors where a group has more than 8 of them, which
 // leaves fewer threads to meet over its sums, and more only where 512 threads
@@ -447,10 +488,11 @@ int block_for(int tpg) { return tpg > 32 ? tpg : 256; }
 // than 256 (128 float32) channels: one group 397 to 366 us, 8 groups 297 to
 // 278, but 16 groups 256 to 276; 8192 rows of 32 float32 groups 135 to 118.
 //
-// Pairs take the fewest a thread whose team fits a warp, else at most
-// kPairTeam threads (8192 rows of 1001 channels: 62 us; with up to 512 87).
-// 8 x 512 float4 and 16 x 512 pairs hold the widest group, 16384 channels.
-constexpr int kPairTeam = 128;
+// Ragged vectors take the fewest a thread whose team fits a warp, else at most
+// kRaggedTeam threads (8192 rows of 1001 bf16 channels: 56 us; with up to 64
+// 62; of float32 65 and 90).  512 threads of 8 vectors (float32 pairs: 16)
+// hold the widest group, 16384 channels.
+constexpr int kRaggedTeam = 128;
 struct Shape {
     int vec, nv, tpg;
 };
@@ -458,16 +500,18 @@ Shape shape_for(mg_dtype dt, int64_t gs, bool aligned, bool backward)
 {
     const int full = dt == MG_F32 ? 4 : 8;
     Shape c;
-    c.vec = aligned && gs % full == 0 ? full : 2;
+    const bool whole = aligned && gs % full == 0;
+    c.vec = whole ? full : full / 2;
     const int most = c.vec == 2 ? 16 : 8, warp = 32, one = backward ? 4 * full : 8;
     auto fits = [&](int nv, int limit) {
         c.nv = nv;
         c.tpg = team_for(gs, c.vec, nv);
         return c.tpg <= limit;
     };
-    if (c.vec == 2) {
-        for (int limit : {warp, kPairTeam, kMaxTeam})
-            if (fits(1, limit) || fits(2, limit) || fits(4, limit)) return c;
+    if (!whole) {
+        for (int limit : {warp, kRaggedTeam, kMaxTeam})
+            if (fits(1, limit) || fits(2, limit) || (c.vec == 2 && fits(4, limit))) return c;
+        if (fits(4, kMaxTeam)) return c;
     } else if (fits(1, one) || fits(2, kMaxTeam) || fits(4, kMaxTeam)) {
         return c;
     }
@@ -516,7 +560,7 @@ mg_status norm_bwd_team(const NormArgs &p, int tpg, cudaStream_t s)
 // Groups of one or two 16-byte vectors a thread, gated or activated by SiLU,
 // have kernels for their team's size; the rest share one for any size.
 #define MG_NORM_TEAM(F)                                                              \
-    if constexpr (NV <= 2 && VEC > 2) {                                              \
+    if constexpr (NV <= 2 && !kRagged<T, VEC>) {                                     \
         if (p.silu) {                                                                \
             if (tpg == 8) return F<T, VEC, NV, GATE, 8, 1>(p, tpg, s);               \
             if (tpg == 16) return F<T, VEC, NV, GATE, 16, 1>(p, tpg, s);             \
@@ -583,8 +627,8 @@ mg_status norm_bwd(const NormArgs &p, int tpg, cudaStream_t s)
         MG_NORM_NV(F, bf16_t, 8)                                                         \
         return fail(MG_ERR_UNSUPPORTED, "group too wide");                               \
     }                                                                                    \
-    MG_NORM_NV(F, bf16_t, 2)                                                             \
-    return F<bf16_t, 2, 16>(p, c.tpg, s);
+    MG_NORM_NV(F, bf16_t, 4)                                                             \
+    return F<bf16_t, 4, 8>(p, c.tpg, s);
 
 }  // namespace
 

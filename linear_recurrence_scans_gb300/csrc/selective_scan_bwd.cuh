@@ -36,8 +36,8 @@ namespace mg {
 // shared memory for a second block: 2 x 4096 x 1024 channels of 64 states 1246
 // -> 838 us); the block's warps meet once a tile to add their dB and dC.
 //
-// 4 x 4096 x 2048 channels of 16 states take 780 us, 0.69e12 states a second:
-// 120 for the first pass, 620 here and 20 for the sums of the parts.
+// 4 x 4096 x 2048 channels of 16 states take 770 us, 0.70e12 states a second:
+// 120 for the first pass, 620 here and 18 for the sums of the parts.
 // Instructions bound it: 23 a state (10 of them the formulas', each state's
 // exponential taken twice), at half the issue slots with two warps a
 // scheduler, which is what the registers of kSub rows leave.  (B and C kept
