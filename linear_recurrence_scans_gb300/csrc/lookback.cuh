@@ -23,12 +23,14 @@
 //                       through the chunk engine (see record_tag)
 // A flag counts only if its epoch equals the launch's epoch, so stale flags
 // of earlier launches need no clearing.  The last CTA of every launch resets
-// the ticket and done counters and advances the epoch.  Where the flags of a
-// launch with more tiles overlay the data records of an earlier launch with
-// fewer, the old words are float pairs; the tag sets the top 13 bits, which
-// as the upper float of a pair is a negative quiet NaN with a non-zero
-// payload bit pattern that no arithmetic result has (the GPU's NaN is
-// 0x7fffffff), so no stale record reads as a flag of the running launch.
+// the ticket and done counters and advances the epoch.  Where the flags or the
+// records of a launch overlay what an earlier launch of this or another op
+// left, the old words are float pairs (the affine kernels' records, the mixer
+// operators' partial sums and states), flags or tagged words.  A flag sets the
+// top 13 bits, which as the upper float of a pair is a negative quiet NaN, and
+// a record's tag is a negative signalling NaN: patterns that no arithmetic
+// result has (the GPU's NaN is 0x7fffffff), so no stale float reads as a flag
+// or as a record of the running launch, whatever its value.
 //
 // Bounded waits.  A wait gives up after `max_polls` polls or `wait_limit_ns`
 // nanoseconds of %globaltimer, or as soon as another CTA of the SAME launch
@@ -66,6 +68,7 @@ struct Lookback {
     float *data;                 // op-specific per-tile records
     unsigned long long wait_limit_ns;
     unsigned int max_polls;
+    unsigned int lines;          // of 64 bytes, the whole workspace
     long long stall_tile;        // testing only: this tile never publishes (-1: none)
 };
 
@@ -142,15 +145,20 @@ __device__ __forceinline__ unsigned flag_status(unsigned long long v, unsigned l
 // reader whose relaxed load sees its own launch's tag in a word also sees the
 // value written with it, without first acquiring the record's flag: a chunk
 // can take its predecessor's inclusive prefix in one round trip as soon as the
-// words land (the flags still serve every other look-back step).  The tag's
-// top two bits are 01, so a tagged word never equals zero-filled memory or a
-// flag word (top 13 bits set), and tags of different launches on the same
-// workspace differ (the low 30 bits of the epoch).  The tile that the testing
-// option stalls writes tag 0, which no reader accepts, so its successors wait
-// on its flag as before.
-__device__ __forceinline__ unsigned launch_tag(unsigned long long epoch)
+// words land (the flags still serve every other look-back step).
+//
+// The tag read as a float is a negative signalling NaN (0xffa00000 up to
+// 0xffbfffff): no value that an op computes, not even the GPU's own NaN, has
+// its bits, and neither zero-filled memory nor a flag word (top 13 bits set)
+// does.  That leaves the low 21 bits of the epoch to tell launches apart: the
+// launch whose successor's bits begin again at 0 clears the workspace it was
+// given (finish_cta), so that no word of the cycle before is met.  The tile
+// that the testing option stalls writes tag 0, which no reader accepts, so its
+// successors wait on its flag as before.
+constexpr unsigned kTagNaN = 0xffa00000u, kTagEpochs = 1u << 21;
+__host__ __device__ __forceinline__ unsigned launch_tag(unsigned long long epoch)
 {
-    return 0x40000000u | unsigned(epoch & 0x3fffffffull);
+    return kTagNaN | (unsigned(epoch) & (kTagEpochs - 1u));
 }
 
 // The tag `tile` writes into its records.
@@ -315,6 +323,11 @@ __device__ __forceinline__ void publish(const Lookback &lb, size_t slot, unsigne
 
 // End of a CTA: count it; the launch's last CTA resets the ticket and done
 // counters and advances the epoch for the next launch on this workspace.
+// Where the tags' epochs begin again with that launch, it first clears all
+// behind the control block, whose older words would be taken for the next
+// launches'; every other CTA has counted itself behind its last access.  One
+// thread does it (15 ms for 64 MB): it comes up once in 2^21 launches, and a
+// loop of the whole CTA here cost the fused bf16 gradients 2% of every call.
 __device__ __forceinline__ void finish_cta(const Lookback &lb, unsigned long long epoch)
 {
     __syncthreads();
@@ -322,6 +335,14 @@ __device__ __forceinline__ void finish_cta(const Lookback &lb, unsigned long lon
         __threadfence();
         const unsigned prev = atomicAdd(&lb.ctl->done, 1u);
         if (prev == gridDim.x - 1) {
+            if ((unsigned(epoch + 1ull) & (kTagEpochs - 1u)) == 0u) {
+                uint4 *line = reinterpret_cast<uint4 *>(lb.ctl + 1);
+                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                __threadfence();
+#pragma unroll 1
+                for (unsigned i = kControlBytes / 64; i < lb.lines; ++i, line += 4)
+                    line[0] = line[1] = line[2] = line[3] = zero;
+            }
             lb.ctl->ticket = 0;
             lb.ctl->done = 0;
             lb.ctl->epoch = epoch + 1;

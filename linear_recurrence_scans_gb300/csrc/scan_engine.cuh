@@ -513,7 +513,7 @@ struct ChanPlan {
             return fail(MG_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", name,
                         ws_bytes_given, need);
         const ChanGeom g = geom(B, T, D);
-        const Lookback lb = make_lookback(ws, nt, o);
+        const Lookback lb = make_lookback(ws, ws_bytes_given, nt, o);
         constexpr size_t smem =
             (size_t(TY + 1) * Op::NS * DC +
              (op_stashes<Op>::value ? size_t(R) * Op::L * Op::NS * TX * TY * Op::VEC : 0)) *

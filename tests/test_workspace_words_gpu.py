@@ -1,0 +1,106 @@
+"""Workspaces that pass from op to op: what one op leaves there is never taken
+for a look-back record of a later one, whatever its values."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from linear_recurrence_scans_gb300 import workloads as wl
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+CONTROL = 256
+
+
+def _epoch(ws, value=None):
+    words = ws[8:16].view(torch.int64)
+    if value is not None:
+        words.fill_(value)
+    return int(words)
+
+
+def _scans(mg, ws_bytes):
+    """Calls that read tagged records, by name: f(ws) -> outputs."""
+    a, b, gA, gB = (t.to(DEV) for t in wl.mingru_linear(2, 4096, 256, seed=41))
+    A, Bc = mg.linear_scan_fwd(a, b)
+    lc, lv = (t.to(DEV) for t in wl.mingru_log(2, 4096, 256, seed=42))
+    x1, x2 = (t.to(DEV) for t in wl.mingru_x(2, 4096, 256, seed=43)[:2])
+    cu = torch.tensor([0, 7, 2100, 4096], device=DEV)
+    assert ws_bytes >= max(mg.linear_workspace_size(2, 4096, 256), mg.log_workspace_size(2, 4096, 256),
+                           mg.mingru_workspace_size(2, 4096, 256), mg.varlen_workspace_size(4096, 256))
+    return {
+        "linear": lambda ws: mg.linear_scan_fwd(a, b, ws=ws),
+        "linear bf16": lambda ws: mg.linear_scan_fwd(a.bfloat16(), b.bfloat16(), ws=ws),
+        "linear bwd": lambda ws: mg.linear_scan_bwd(a, A, Bc, gA, gB, ws=ws),
+        "log": lambda ws: (mg.parallel_scan_log_fwd(lc, lv, ws=ws),),
+        "mingru": lambda ws: mg.mingru_scan_fwd(x1, x2, ws=ws),
+        "varlen": lambda ws: mg.linear_scan_varlen_fwd(a[0], b[0], cu, ws=ws),
+    }
+
+
+def test_partial_sums_of_two_are_no_record(cuda_lib):
+    """Gradients of a norm whose upstream gradient is 1: every partial sum of its
+    bias gradient is 2.0 where a block has two rows.  The first scan on that
+    workspace does not take them for its predecessors' prefixes."""
+    mg = cuda_lib
+    x, z = (torch.randn(608, 4096, device=DEV).bfloat16() for _ in range(2))
+    w = torch.ones(4096, device=DEV)
+    _, stats = mg.group_norm_fwd(x, w, None, z, rms=True, gate_first=True)
+    size = 64 << 20
+    own = mg.new_workspace(size, DEV)
+    for name, scan in _scans(mg, size).items():
+        want = scan(own)
+        for _ in range(4):
+            ws = mg.new_workspace(size, DEV)
+            mg.group_norm_bwd(torch.ones_like(x), stats, x, w, None, z, rms=True, gate_first=True, ws=ws)
+            got = scan(ws)
+            assert all(torch.equal(p, q) for p, q in zip(got, want)), name
+            mg.workspace_status(ws)
+
+
+@pytest.mark.parametrize("value", [2.0, 2.0 + 2.0 ** -22, 0.0, -0.0, float("inf"), float("nan"), -float("inf")])
+def test_no_value_is_a_record(cuda_lib, value):
+    """The whole workspace behind its control block holds one float."""
+    mg = cuda_lib
+    size = 64 << 20
+    own = mg.new_workspace(size, DEV)
+    for name, scan in _scans(mg, size).items():
+        want = scan(own)
+        ws = mg.new_workspace(size, DEV)
+        for _ in range(2):
+            ws[CONTROL:].view(torch.float32).fill_(value)
+            got = scan(ws)
+            assert all(torch.equal(p, q) for p, q in zip(got, want)), (name, value)
+            mg.workspace_status(ws)
+
+
+def test_a_new_cycle_of_tags_meets_no_older_word(cuda_lib):
+    """The launch before the tags begin again clears the workspace: words of the
+    cycle before, with the next launch's own tag, are gone."""
+    mg = cuda_lib
+    size, cycle = 64 << 20, 1 << 21
+    own = mg.new_workspace(size, DEV)
+    a, b, _, _ = (t.to(DEV) for t in wl.mingru_linear(1, 200, 64, seed=44))
+    small = mg.linear_scan_fwd(a, b)
+    word = (mg.load().mg_testing_record_tag(cycle) - (1 << 32) << 32) | 0x40e00000   # 7.0, as int64
+    for name, scan in _scans(mg, size).items():
+        want = scan(own)
+        for first in ("small", "itself"):
+            ws = mg.new_workspace(size, DEV)
+            _epoch(ws, cycle - 1)
+            ws[CONTROL:].view(torch.int64).fill_(word)
+            got = mg.linear_scan_fwd(a, b, ws=ws) if first == "small" else scan(ws)
+            assert all(torch.equal(p, q) for p, q in zip(got, small if first == "small" else want)), (name, first)
+            assert _epoch(ws) == cycle and not ws[:8].any() and not ws[CONTROL:].any()
+            got = scan(ws)
+            assert all(torch.equal(p, q) for p, q in zip(got, want)), (name, first)
+            assert _epoch(ws) == cycle + 1
+            mg.workspace_status(ws)
+    Am, Bm, _, _ = wl.haar_affine(1, 300, 2, 16, 16, seed=45, grads=False)   # a kernel of its own
+    Am, Bm = Am.to(DEV), Bm.to(DEV)
+    ws = mg.new_workspace(size, DEV)
+    _epoch(ws, cycle - 1)
+    want = mg.affine_scan_fwd(Am, Bm)
+    for _ in range(2):
+        assert all(torch.equal(p, q) for p, q in zip(mg.affine_scan_fwd(Am, Bm, ws=ws), want))
+    assert _epoch(ws) == cycle + 1
