@@ -45,6 +45,12 @@ extern "C" {
 #endif
 
 /*
+ * Sizes.  A call has at most 2^36 values (rows x channels, and states), and no
+ * launch more than 2^31 - 1 blocks; beyond either MG_ERR_UNSUPPORTED is
+ * returned before any launch.
+ */
+
+/*
  * Short causal depthwise convolution with an activation:
  *   v_r[d] = bias[d] + sum_{k<W} w[d,k] x_{r-W+1+k}[d],
  *   y_r = silu(v_r) = v_r sigmoid(v_r) if silu, else v_r.

@@ -559,6 +559,7 @@ mg_status conv_fwd(const ConvArgs &p, cudaStream_t s)
 {
     const Seqs q = make_seqs(p.cu, p.B, p.T, p.nseq);
     const Cut c = cut(q.rows, p.D, VEC, 16, 152 * kFwdPerSm);
+    MG_TRY(check_grids("mg_causal_conv_fwd", {c.chan_blocks * c.row_blocks}));
     conv_fwd_kernel<T, VEC, W><<<unsigned(c.chan_blocks * c.row_blocks), c.block, Ring<T, VEC>::bytes(kBlock), s>>>(
         p, q, c.chan_blocks, c.run);
     return launched("mg_causal_conv_fwd");
@@ -569,6 +570,7 @@ mg_status conv_bwd(const ConvArgs &p, cudaStream_t s)
 {
     const Seqs q = make_seqs(p.cu, p.B, p.T, p.nseq);
     const Cut c = cut_bwd(q.rows, p.D, VEC);
+    MG_TRY(check_grids("mg_causal_conv_bwd", {c.chan_blocks * c.row_blocks, sum_parts_blocks(p.D * (W + 1))}));
     float *part = reinterpret_cast<float *>(static_cast<char *>(p.ws) + kControlBytes);
     constexpr size_t sums = kBlock * size_t(VEC * (W + 1)) * sizeof(float), rings = 2 * Ring<T, VEC>::bytes(kBlock);
     constexpr size_t smem = sums > rings ? sums : rings;
@@ -583,8 +585,7 @@ template <typename T, int VEC, int W>
 mg_status conv_step(const ConvStepArgs &p, cudaStream_t s)
 {
     const int64_t chan_blocks = ceil_div(ceil_div(p.D, VEC), 128), blocks = ceil_div(p.B, kTokens) * chan_blocks;
-    if (blocks > INT32_MAX)
-        return fail(MG_ERR_UNSUPPORTED, "mg_causal_conv_step: B = %lld, D = %lld", (long long)p.B, (long long)p.D);
+    MG_TRY(check_grids("mg_causal_conv_step", {blocks}));
     conv_step_kernel<T, VEC, W><<<unsigned(blocks), 128, 0, s>>>(p, unsigned(chan_blocks));
     return launched("mg_causal_conv_step");
 }
@@ -655,7 +656,7 @@ mg_status launch_sum_parts(const float *part, int64_t parts, std::initializer_li
         o.o[k++] = x;
         stride += x.n;
     }
-    return launch_next("sum over parts", sum_parts_kernel, ceil_div(stride, 32), dim3(32, 8), 0, s, part, parts, stride, o);
+    return launch_next("sum over parts", sum_parts_kernel, sum_parts_blocks(stride), dim3(32, 8), 0, s, part, parts, stride, o);
 }
 
 }  // namespace mg

@@ -536,6 +536,7 @@ mg_status norm_fwd_team(const NormArgs &p, int tpg, cudaStream_t s)
 {
     const int block = block_for(tpg);
     const int64_t rt = row_teams_for(p.M, p.G, tpg, kFwdWarps);
+    MG_TRY(check_grids("mg_group_norm_fwd", {ceil_div(rt * p.G, block / tpg)}));
     const size_t smem = Ahead<T, VEC, NV, GATE == MG_GATE_NONE ? 1 : 2>::bytes(block);
     MG_TRY(allow_shared<norm_fwd_kernel<T, VEC, NV, GATE, TEAM, SILU>>(smem));
     norm_fwd_kernel<T, VEC, NV, GATE, TEAM, SILU><<<unsigned(ceil_div(rt * p.G, block / tpg)), block, smem, s>>>(
@@ -548,6 +549,7 @@ mg_status norm_bwd_team(const NormArgs &p, int tpg, cudaStream_t s)
 {
     const int block = block_for(tpg);
     const int64_t rt = row_teams_for(p.M, p.G, tpg, kBwdWarps);
+    MG_TRY(check_grids("mg_group_norm_bwd", {ceil_div(rt * p.G, block / tpg), sum_parts_blocks(2 * p.D)}));
     float *part = reinterpret_cast<float *>(static_cast<char *>(p.ws) + kControlBytes);
     const size_t smem = Ahead<T, VEC, NV, GATE == MG_GATE_NONE ? 2 : 3>::bytes(block);
     MG_TRY(allow_shared<norm_bwd_kernel<T, VEC, NV, GATE, TEAM, SILU>>(smem));

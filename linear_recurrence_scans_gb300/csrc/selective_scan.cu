@@ -592,6 +592,7 @@ mg_status fwd_cover(const SsmArgs &p, cudaStream_t s)
     float *agg_h = reinterpret_cast<float *>(static_cast<char *>(p.ws) + kControlBytes);
     float *agg_s = agg_h + p.B * (ck.n - 1) * p.D * p.N;
     const int64_t tiles = t.tiles * p.G * p.B;
+    MG_TRY(check_grids("mg_selective_scan_fwd", {tiles * ck.n}));
     if (p.cu != nullptr) {
         const int64_t n = p.D * p.N;
         MG_TRY(launch_empty_sequences(q, p.h_last, p.h0, n, p.ws, s));
@@ -622,7 +623,7 @@ mg_status adjoint_cover(const SsmArgs &p, const Chunks &ck, float *agg_q, float 
     const Seqs q = make_seqs(p.cu, p.B, p.T, p.nseq);
     constexpr size_t sm = kThreads / 32 * sizeof(FwdShared<T, VEC, CV::kWarpCh, CV::NP, true>);
     MG_TRY(allow_shared<ssm_chunk_kernel<T, VEC, CV, kAdjoint>>(sm));
-    const int64_t grid = t.tiles * p.G * p.B * (ck.n - 1);
+    const int64_t grid = adjoint_blocks(p, ck);
     auto kernel = ssm_chunk_kernel<T, VEC, CV, kAdjoint>;
     if (p.cu != nullptr)
         return launch_next("mg_selective_scan_bwd", kernel, grid, kThreads, sm, s, p, q, t, ck, agg_q, agg_s, mode);
@@ -653,7 +654,8 @@ template <typename T, int L>
 mg_status step(const SsmStepArgs &p, cudaStream_t s)
 {
     const int64_t chan_blocks = ceil_div(p.D * L, kThreads), blocks = ceil_div(p.B, kTokens) * chan_blocks;
-    if (blocks > INT32_MAX || p.D > (int64_t(1) << 31) / L - kThreads)
+    MG_TRY(check_grids("mg_selective_scan_step", {blocks}));
+    if (p.D > (int64_t(1) << 31) / L - kThreads)
         return fail(MG_ERR_UNSUPPORTED, "mg_selective_scan_step: B = %lld, D = %lld", (long long)p.B, (long long)p.D);
     // rows of B and C as vectors of four
     const int bc_wide = p.N % 4 == 0 && p.ldb % 4 == 0 && p.ldc % 4 == 0;
@@ -682,6 +684,10 @@ mg_status launch_empty_sequences(const Seqs &q, float *dst, const float *src, in
     return launched("selective scan: empty sequences");
 }
 
+int64_t adjoint_blocks(const SsmArgs &p, const Chunks &ck)
+{
+    return forward_tiles(p.D, p.N, p.G) * p.G * p.B * (ck.n - 1);
+}
 mg_status launch_ssm_adjoint(const SsmArgs &p, mg_dtype dt, bool wide, const Chunks &ck, float *agg_q,
                              float *agg_s, cudaStream_t s)
 {

@@ -270,7 +270,8 @@ inline bool wide_rows(const SsmArgs &p, int vec)
 }
 
 // The gradients' first pass: q at the first row of chunks 1 .. ck.n-1, and
-// each one's sum of delta (selective_scan.cu).
+// each one's sum of delta, and its block count (selective_scan.cu).
+int64_t adjoint_blocks(const SsmArgs &p, const Chunks &ck);
 mg_status launch_ssm_adjoint(const SsmArgs &p, mg_dtype dt, bool wide, const Chunks &ck, float *agg_q,
                              float *agg_s, cudaStream_t s);
 

@@ -673,6 +673,9 @@ mg_status bwd(const SsmArgs &p, cudaStream_t s)
     float *agg_s = agg_q + p.B * (ck.n - 1) * dn;
     const int64_t tiles = t.tiles * p.G * p.B;
     const int mode = bc_mode<T>(p.N, p.ldb, p.ldc);
+    const int64_t bc_blocks = ceil_div(rows_g * 2 * p.N, 256);
+    MG_TRY(check_grids("mg_selective_scan_bwd", {tiles * ck.n, adjoint_blocks(p, ck), bc_blocks,
+                                                 sum_parts_blocks(p.D * (p.N + 2))}));
     if (p.cu != nullptr) {
         MG_TRY(launch_empty_sequences(q, p.dh0, p.dh_last, dn, p.ws, s));
     }
@@ -691,7 +694,7 @@ mg_status bwd(const SsmArgs &p, cudaStream_t s)
         kernel<<<unsigned(tiles), CV::THREADS, smem, s>>>(p, q, t, ck, agg_q, agg_s, partB, partA, mode);
         MG_TRY(launched(what));
     }
-    MG_TRY(launch_next(what, sum_bc_kernel<T>, ceil_div(rows_g * 2 * p.N, 256), 256, 0, s, partB, t.tiles, rows_g, p.N,
+    MG_TRY(launch_next(what, sum_bc_kernel<T>, bc_blocks, 256, 0, s, partB, t.tiles, rows_g, p.N,
                        static_cast<T *>(p.dBm), static_cast<T *>(p.dCm)));
     return launch_sum_parts(partA, parts, {{p.dA, dn}, {p.dDskip, p.D}, {p.ddt_bias, p.D}}, s);
 }

@@ -108,6 +108,17 @@ struct SumOut {
     int64_t n;
 };
 mg_status launch_sum_parts(const float *part, int64_t parts, std::initializer_list<SumOut> outs, cudaStream_t s);
+inline int64_t sum_parts_blocks(int64_t columns) { return (columns + 31) / 32; }
+
+// A call's block counts, all of them before its first launch: a grid holds
+// 2^31 - 1 blocks.
+inline mg_status check_grids(const char *what, std::initializer_list<int64_t> blocks)
+{
+    for (int64_t n : blocks)
+        if (n > INT32_MAX)
+            return fail(MG_ERR_UNSUPPORTED, "%s: %lld blocks in a launch, at most 2^31 - 1", what, (long long)n);
+    return MG_OK;
+}
 
 inline mg_status launched(const char *what)
 {
