@@ -184,7 +184,8 @@ typedef enum mg_gate {
  *   o = (p - mean) rstd w + bias
  *   y = o (MG_GATE_FIRST), o act(z) (MG_GATE_AFTER), act(o) (MG_GATE_NONE)
  * w, bias (D) float32 (bias may be NULL); y dense, type dt; stats (M, G, 2)
- * float32 (may be NULL) receives mean and rstd.
+ * float32 (may be NULL) receives mean and rstd.  Groups have at most 16384
+ * channels, and M G is below 2^31.
  */
 mg_status mg_group_norm_fwd(const void *x, int64_t ldx, const void *z, int64_t ldz, mg_dtype dt,
                             const float *w, const float *bias, double eps, int rms, mg_gate gate,

@@ -125,7 +125,8 @@ mg_status check_norm(const char *fn, int64_t M, int64_t D, int64_t G, mg_gate ga
         return fail(MG_ERR_UNSUPPORTED, "%s: groups of %lld channels, at most 16384", fn,
                     (long long)(D / G));
     MG_TRY(check_size(fn, M, D));
-    if (M > (int64_t(1) << 31) / G) return fail(MG_ERR_UNSUPPORTED, "%s: M G beyond 2^31", fn);
+    // the kernels count rows in 32 bits
+    if (M > INT32_MAX / G) return fail(MG_ERR_UNSUPPORTED, "%s: M G beyond 2^31 - 1", fn);
     return MG_OK;
 }
 

@@ -59,3 +59,13 @@ def test_token_blocks(lib):
     B, D = 1 << 33, 1
     _refused(lib, lib.mg_selective_scan_step(at(1), D, at(2), D, at(3), at(4), 1, at(5), 1, 0, None, None, 1, at(6), B,
                                              None, at(7), B, D, 1, 1, None))
+
+
+def test_norm_rows(lib):
+    """M G is held in 32 bits: 2^31 is one too many."""
+    for M, G in ((1 << 31, 1), (1 << 30, 2), (1 << 28, 8)):
+        fwd = lambda M: lib.mg_group_norm_fwd(at(1), G, None, G, 1, at(3), None, 1e-5, 0, 0, 1, at(4), None, M, G, G, None)  # noqa: E731
+        _refused(lib, fwd(M), b"M G")
+        _refused(lib, lib.mg_group_norm_bwd(at(1), G, at(2), at(3), G, None, G, 1, at(4), None, 0, 0, 1, at(5), None,
+                                            at(6), None, M, G, G, WS, WSB, None), b"M G")
+        assert lib.mg_group_norm_workspace_size(M, G, G) == 0 and lib.mg_group_norm_workspace_size(M - 1, G, G) > 0
