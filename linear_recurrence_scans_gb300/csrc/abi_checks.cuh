@@ -16,6 +16,7 @@ struct Buf {
     const char *name;
     bool output;
     bool optional = false;   // NULL allowed (the buffer is then not used)
+    size_t align = 16;
 };
 
 // NULL, alignment and overlap checks.  Outputs may overlap nothing.
@@ -24,8 +25,8 @@ inline mg_status check_bufs(const char *fn, std::initializer_list<Buf> bufs)
     for (const Buf &b : bufs) {
         if (b.p == nullptr && b.optional) continue;
         if (b.p == nullptr) return fail(MG_ERR_INVALID_ARG, "%s: %s is NULL", fn, b.name);
-        if (reinterpret_cast<uintptr_t>(b.p) % 16 != 0)
-            return fail(MG_ERR_INVALID_ARG, "%s: %s is not 16-byte aligned", fn, b.name);
+        if (reinterpret_cast<uintptr_t>(b.p) % b.align != 0)
+            return fail(MG_ERR_INVALID_ARG, "%s: %s is not %zu-byte aligned", fn, b.name, b.align);
     }
     for (const Buf &o : bufs) {
         if (!o.output || o.p == nullptr) continue;

@@ -59,8 +59,6 @@ mg_status check_slots(const char *fn, const int64_t *slots, int64_t nslots, int6
     if (slots == nullptr && nslots < B)
         return fail(MG_ERR_INVALID_ARG, "%s: %lld states for %lld rows without slots", fn,
                     (long long)nslots, (long long)B);
-    if (reinterpret_cast<uintptr_t>(slots) % 8 != 0)
-        return fail(MG_ERR_INVALID_ARG, "%s: slots is not 8-byte aligned", fn);
     return MG_OK;
 }
 
@@ -255,7 +253,7 @@ mg_status mg_causal_conv_step(const void *x, int64_t ldx, mg_dtype dt, const flo
     MG_TRY(check_bufs(fn, {{x, extent(B, ldx, D, es), "x", false},
                            {w, size_t(D) * W * 4, "w", false},
                            {bias, size_t(D) * 4, "bias", false, true},
-                           {slots, size_t(B) * 8, "slots", false, true},
+                           {slots, size_t(B) * 8, "slots", false, true, 8},
                            {state, pool, "state", true, pool == 0},
                            {y, size_t(B) * D * es, "y", true}}));
     ConvStepArgs p{};
@@ -424,7 +422,7 @@ mg_status mg_selective_scan_step(const void *x, int64_t ldx, const void *raw, in
                            {Cm, extent(B, ldc, G * N, es), "Cm", false},
                            {Dskip, size_t(D) * 4, "Dskip", false, true},
                            {dt_bias, size_t(D) * 4, "dt_bias", false, true},
-                           {slots, size_t(B) * 8, "slots", false, true},
+                           {slots, size_t(B) * 8, "slots", false, true, 8},
                            {state, pool, "state", true, pool == 0},
                            {y, size_t(B) * D * es, "y", true}}));
     SsmStepArgs p{};

@@ -221,7 +221,7 @@ def _slots(slots, state, B):
         return None, 0
     if not isinstance(slots, Tensor) or slots.dtype != torch.int64 or not slots.is_cuda or slots.shape != (B,):
         raise ValueError("slots must be a CUDA int64 tensor with one entry for each row")
-    if not slots.is_contiguous() or slots.data_ptr() & 15:
+    if not slots.is_contiguous():
         slots = slots.clone(memory_format=torch.contiguous_format)
     return slots, slots.data_ptr()
 
