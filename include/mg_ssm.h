@@ -32,6 +32,10 @@
  *   nslots >= B).  A row whose slot is negative or not below nslots is idle:
  *   its output is 0 and no state changes.  Rows of one call must use
  *   different slots.
+ * Infinities.  The selective scan's results are finite where the formulas' are;
+ *   where an infinite input makes them infinite they may be NaN instead (a sum
+ *   over states may take in states of 0 beside N, and a run of decays one
+ *   product that is 0 in float32: 0 times infinity).
  * Empty calls (no rows) return MG_OK; the states that a call returns are then
  *   the states that it was given.
  */

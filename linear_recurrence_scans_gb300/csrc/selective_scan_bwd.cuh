@@ -225,7 +225,8 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
     for (int i = 0; i < S; ++i)
 #pragma unroll
         for (int c = 0; c < CP; ++c) {
-            A2[i][c] = mul2(A2[i][c], dup2(kLog2eF));
+            // (a padded state's A is -1: with 0 an infinite delta would make its decay NaN, and with it s1)
+            A2[i][c] = n0 + i < p.N ? mul2(A2[i][c], dup2(kLog2eF)) : dup2(-1.f);
             ag[i][c] = dA[i][c] = 0;
         }
     for (int i = lane; i < WCH; i += 32)

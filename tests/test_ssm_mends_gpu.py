@@ -31,3 +31,57 @@ def test_slots_on_any_8_byte_boundary(cuda_lib):
                                       3, 24, 16, 1, torch.cuda.current_stream().cuda_stream) == mg.MG_OK
     assert torch.equal(y[0], wy[0]) and torch.equal(pools[0], want[0])
     assert torch.equal(mg.causal_conv_step(x, w, pools[1], slots=slots), wy[1]) and torch.equal(pools[1], want[1])
+
+
+def _same_finite(name, got, want, scale, count):
+    """Finite where the oracle is, and near it there."""
+    fin = np.isfinite(want)
+    assert np.array_equal(np.isfinite(_np(got)), fin), name
+    got = torch.where(torch.from_numpy(fin).to(DEV), got, torch.zeros_like(got))
+    _near(name, got, np.where(fin, want, 0.0), np.where(np.isfinite(scale), scale, 0.0), count)
+
+
+@pytest.mark.parametrize("N", [1, 3, 5, 12, 16, 24, 33, 48])
+@pytest.mark.parametrize("T,at", [(1, 0), (37, 20), (700, 3)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_infinite_inputs_with_any_number_of_states(cuda_lib, N, T, at, dtype):
+    """An infinite x or step reaches its own channel from that row on, whatever
+    the padding of the states."""
+    for which in ("x", "raw"):
+        c = Scan(cuda_lib, 1, T, 21, N, dtype=dtype, seed=N + T)
+        getattr(c, which)[0, at, 7] = float("inf")
+        getattr(c, "n" + which)[0, at, 7] = float("inf")
+        with np.errstate(invalid="ignore"):
+            wy, wl, _ = o.scan_fwd(*c.oracle_inputs(), c.sp)
+            sy, sl, _ = o.scan_fwd(*c.oracle_inputs(), c.sp, absolute=True)
+        assert not np.isfinite(wy[0, at:, 7]).any()
+        y, last, _ = c.forward()
+        _same_finite("y", y, wy, sy, T + N)
+        _same_finite("h_last", last, wl, sl, T + N)
+        if T == 1:
+            pool = c.h0.clone()
+            y = cuda_lib.selective_scan_step(c.x[:, 0], c.raw[:, 0], c.A, c.Bm[:, 0], c.Cm[:, 0], pool, c.Ds, c.bias)
+            _same_finite("token", y, wy[:, 0], sy[:, 0], 1 + N)
+            _same_finite("state", pool, wl, sl, 1 + N)
+
+
+@pytest.mark.parametrize("N", [1, 5, 12, 16, 24, 33])
+@pytest.mark.parametrize("T,at", [(37, 20), (700, 650)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradients_before_an_infinite_step(cuda_lib, N, T, at, dtype):
+    """An infinite step cuts the rows before it off: their gradients are finite
+    by the formulas, whatever the padding of the states."""
+    c = Scan(cuda_lib, 1, T, 21, N, dtype=dtype, seed=N + T)
+    c.raw[0, at, 7] = float("inf")
+    c.nraw[0, at, 7] = float("inf")
+    _, _, saved = c.forward()
+    got = c.backward(saved)
+    with np.errstate(invalid="ignore"):
+        more = (c.ndl, c.sp, c.softplus)
+        want = o.scan_bwd(c.ndy, *c.oracle_inputs(), *more)
+        scale = o.scan_bwd(c.ndy, *c.oracle_inputs(), *more, absolute=True)
+    counts = (T, T, 2 * T, T + 21, T + 21, T, 2 * T, T)
+    for name, g, w, s, n in zip(("dx", "ddt", "dA", "dB", "dC", "dD", "ddt_bias", "dh0"), got, want, scale, counts):
+        if name in ("dx", "ddt", "dB", "dC"):
+            assert np.isfinite(w[0, :at]).all()
+        _same_finite(name, g, w, s, n + N)
