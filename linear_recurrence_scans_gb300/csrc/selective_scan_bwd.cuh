@@ -89,13 +89,16 @@ struct Spot {
 };
 
 // The sequences at a tile's rows, found only for tiles that hold a first or
-// last row of one: the sequence that row starts / ends there, or -1.
+// last row of one: the sequence that row starts / ends there, or -1.  Rows past
+// the batch's end start from 0 (kNoRow): an infinite last state times their
+// adjoints of 0 would make dA NaN.
+constexpr int kNoRow = -2;
 __device__ __forceinline__ void edge_rows(const Seqs &q, int64_t rowb, int64_t ta, int rows,
                                           int (&first)[kTile], int (&last)[kTile])
 {
     const int i = threadIdx.x;
     if (i >= kTile) return;
-    int f = -1, e = -1;
+    int f = i < rows ? -1 : kNoRow, e = -1;
     if (i < rows) {
         const long long r = rowb + ta + i;
         const int s = q.of(r);
@@ -343,9 +346,9 @@ ssm_bwd_kernel(SsmArgs p, Seqs q, Tile tl, Chunks ck, const float *agg_q, const 
         auto enter = [&](int tt) {   // a sequence's first row starts from its h0
             if constexpr (kEdges) {
                 const int f = block.first[tt];
-                if (f >= 0)
-                    load_block<S, CP>(p.h0 != nullptr ? p.h0 + int64_t(f) * p.D * p.N : nullptr, dw + ch, ch, wide, n0,
-                                  p.N, h);
+                if (f != -1)
+                    load_block<S, CP>(f >= 0 && p.h0 != nullptr ? p.h0 + int64_t(f) * p.D * p.N : nullptr, dw + ch, ch,
+                                      wide, n0, p.N, h);
             }
         };
         const int rows = int(w.t1 - t);

@@ -85,3 +85,23 @@ def test_gradients_before_an_infinite_step(cuda_lib, N, T, at, dtype):
         if name in ("dx", "ddt", "dB", "dC"):
             assert np.isfinite(w[0, :at]).all()
         _same_finite(name, g, w, s, n + N)
+
+
+@pytest.mark.parametrize("N,G,cu", [(16, 1, None), (12, 3, None), (5, 1, [0, 3, 20, 37]), (16, 1, [0, 37, 37])], ids=str)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gradients_of_an_infinite_last_row(cuda_lib, N, G, cu, dtype):
+    """An infinite x in the batch's last row leaves dA finite by the formulas
+    (no row follows), also where that row is not the last of a tile."""
+    c = Scan(cuda_lib, 1 if cu else 2, 37, 21, N, G=G, cu=cu, dtype=dtype, seed=N)
+    c.x[-1, 36, 7] = float("inf")
+    c.nx[-1, 36, 7] = float("inf")
+    _, _, saved = c.forward()
+    got = c.backward(saved)
+    with np.errstate(invalid="ignore"):
+        more = (c.ndl, c.sp, c.softplus)
+        want = o.scan_bwd(c.ndy, *c.oracle_inputs(), *more)
+        scale = o.scan_bwd(c.ndy, *c.oracle_inputs(), *more, absolute=True)
+    assert np.isfinite(want[2]).all()
+    counts = (37, 37, 111, 58, 58, 74, 111, 37)
+    for name, g, w, s, n in zip(("dx", "ddt", "dA", "dB", "dC", "dD", "ddt_bias", "dh0"), got, want, scale, counts):
+        _same_finite(name, g, w, s, n + N)
