@@ -38,7 +38,8 @@ Every op accepts optional preallocated outputs (``out=(...)``), a workspace
 tensor (``ws=``, uint8, zero-filled before first use) and a stream
 (``stream=``, a ``torch.cuda.Stream``); by default outputs are allocated with
 ``torch.empty``, a cached per-(device, stream) workspace is used and the call
-is issued on the current stream.
+is issued on the current stream.  A workspace that a captured CUDA graph uses
+is kept for as long as the process runs.
 """
 from __future__ import annotations
 
@@ -221,6 +222,7 @@ def new_workspace(nbytes: int, device) -> torch.Tensor:
 
 
 _ws_cache: dict = {}
+_ws_captured: dict = {}   # workspaces whose addresses CUDA graphs hold, by address: never freed
 
 
 def _stream_handle(stream, device) -> int:
@@ -235,7 +237,11 @@ def _workspace(nbytes: int, device, stream_handle: int, ws):
         return ws
     key = (device.index, stream_handle)
     buf = _ws_cache.get(key)
+    capturing = torch.cuda.is_current_stream_capturing()
     if buf is None or buf.numel() < nbytes:
+        if capturing:
+            raise RuntimeError("a workspace cannot grow during a graph capture: run the op on the capture's stream "
+                               "once before it, or pass ws=")
         if buf is not None:
             # Kernels on the op's stream (which torch's allocator does not
             # track for this buffer) may still use the smaller workspace:
@@ -246,13 +252,16 @@ def _workspace(nbytes: int, device, stream_handle: int, ws):
         buf = new_workspace(int(nbytes * 1.25) + 4096, device)
         torch.cuda.current_stream(device).synchronize()
         _ws_cache[key] = buf
+    if capturing:
+        _ws_captured[buf.data_ptr()] = buf
     return buf
 
 
 def workspace_status(ws: torch.Tensor | None = None, stream=None) -> None:
     """Raise MgScanError(MG_ERR_TIMEOUT) if a look-back wait gave up on ``ws``
-    (default: every cached workspace) since the last check."""
-    bufs = [ws] if ws is not None else list(_ws_cache.values())
+    (default: every cached workspace, and those that captured graphs use) since
+    the last check."""
+    bufs = [ws] if ws is not None else list({b.data_ptr(): b for b in (*_ws_cache.values(), *_ws_captured.values())}.values())
     for b in bufs:
         _check(load().mg_workspace_status(b.data_ptr(), _stream_handle(stream, b.device)),
                "mg_workspace_status")

@@ -104,3 +104,42 @@ def test_a_new_cycle_of_tags_meets_no_older_word(cuda_lib):
     for _ in range(2):
         assert all(torch.equal(p, q) for p, q in zip(mg.affine_scan_fwd(Am, Bm, ws=ws), want))
     assert _epoch(ws) == cycle + 1
+
+
+def test_a_replayed_graph_writes_no_memory_of_others(cuda_lib):
+    """A graph captured on a stream's cached workspace, replayed after a larger
+    call replaced that workspace and other tensors took free memory."""
+    mg = cuda_lib
+    x, dt = torch.randn(2, 200, 96, device=DEV), torch.randn(2, 200, 96, device=DEV)
+    A, bc = -torch.rand(96, 16, device=DEV) - 0.1, torch.randn(2, 200, 16, device=DEV)
+    side = torch.cuda.Stream()
+    key = (0, side.cuda_stream)
+
+    def step():
+        y, _, saved = mg.selective_scan_fwd(x, dt, A, bc, bc, save=True)
+        return (y, *mg.selective_scan_bwd(y, saved, x, dt, A, bc, bc)[:5])
+
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        want = step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = step()
+    size = mg._ws_cache[key].numel()
+    with torch.cuda.stream(side):
+        big = torch.randn(4, 2048, 512, device=DEV)
+        mg.causal_conv_bwd(big, big, torch.randn(512, 8, device=DEV))
+        bb = torch.randn(4, 2048, 16, device=DEV)
+        y, _, saved = mg.selective_scan_fwd(big, big, -torch.rand(512, 16, device=DEV), bb, bb, save=True)
+        mg.selective_scan_bwd(y, saved, big, big, -torch.rand(512, 16, device=DEV), bb, bb)
+        assert mg._ws_cache[key].numel() > size
+        del y, saved, big, bb
+        others = [torch.full((n,), 7, dtype=torch.uint8, device=DEV) for n in (size, size // 2, size, 4 * size) * 4]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all((t == 7).all() for t in others)
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    mg.workspace_status()
