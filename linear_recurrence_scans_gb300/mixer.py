@@ -26,12 +26,29 @@ import linear_recurrence_scans_gb300 as mg
 
 
 class States:
-    """A pool of recurrent states: entry i belongs to one sequence."""
+    """A pool of recurrent states: entry i belongs to one sequence.  Behind the
+    pool lies an entry of zeros that stands for every slot outside it."""
 
     def __init__(self, mixer: "SelectiveMixer", count: int):
         m = mixer
-        self.conv = torch.zeros(count, m.taps - 1, m.channels, dtype=m.dtype, device=m.device)
-        self.scan = torch.zeros(count, m.channels, m.states, dtype=torch.float32, device=m.device)
+        self._conv = torch.zeros(count + 1, m.taps - 1, m.channels, dtype=m.dtype, device=m.device)
+        self._scan = torch.zeros(count + 1, m.channels, m.states, dtype=torch.float32, device=m.device)
+        self.conv, self.scan = self._conv[:count], self._scan[:count]
+
+    def _at(self, slots):
+        count = self.conv.shape[0]
+        return torch.where((slots >= 0) & (slots < count), slots, count)
+
+    def take(self, slots):
+        """Copies of the slots' (conv, scan) states, zeros for a slot outside the pool."""
+        at = self._at(slots)
+        return self._conv[at], self._scan[at]
+
+    def put(self, slots, conv, scan):
+        """Writes the slots' states; those of a slot outside the pool go nowhere."""
+        at = self._at(slots)
+        self._conv[at], self._scan[at] = conv, scan
+        self._conv[-1].zero_(), self._scan[-1].zero_()
 
 
 class SelectiveMixer:
@@ -73,14 +90,18 @@ class SelectiveMixer:
 
     def prompt(self, u, states=None, slots=None, cu_seqlens=None, save=False):
         """out (B,T,E) for whole sequences, dense or (B = 1) packed by
-        cu_seqlens.  With states and slots (one for each sequence) the
-        sequences go on from those states and leave their last ones there.
+        cu_seqlens.  With states the sequences go on from the entries slots[i]
+        of the pool (i without slots) and leave their last states there; a
+        sequence whose slot is not in the pool begins from zero and leaves none.
         save=True returns (out, what backward needs)."""
         p, D = self.p, self.channels
         xz = u @ p["in"]
         x, z = xz[..., :D], xz[..., D:]
-        x0 = states.conv[slots] if states is not None else None
-        h0 = states.scan[slots] if states is not None else None
+        x0 = h0 = None
+        if states is not None:
+            if slots is None:
+                slots = torch.arange(u.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1, device=u.device)
+            x0, h0 = states.take(slots)
         xc, x_last = mg.causal_conv_fwd(x, p["conv_w"], p["conv_b"], x0, cu_seqlens=cu_seqlens)
         low, dt, B, C = self._project(xc)
         A = -torch.exp(p["A_log"])
@@ -88,7 +109,7 @@ class SelectiveMixer:
                                                  cu_seqlens=cu_seqlens, save=save)
         o, stats = mg.group_norm_fwd(y, p["norm_w"], z=z, **self.norm)
         if states is not None:
-            states.conv[slots], states.scan[slots] = x_last, h_last
+            states.put(slots, x_last, h_last)
         out = o @ p["out"]
         return (out, (u, x, z, xc, low, dt, B, C, A, y, o, stats, saved, x0, h0, cu_seqlens)) if save else out
 

@@ -105,3 +105,24 @@ def test_gradients_of_an_infinite_last_row(cuda_lib, N, G, cu, dtype):
     counts = (37, 37, 111, 58, 58, 74, 111, 37)
     for name, g, w, s, n in zip(("dx", "ddt", "dA", "dB", "dC", "dD", "ddt_bias", "dh0"), got, want, scale, counts):
         _same_finite(name, g, w, s, n + N)
+
+
+def test_prompts_outside_the_pool_leave_it_alone(cuda_lib):
+    """The layer's prompts with idle slots: their outputs are those of fresh
+    sequences, and no entry of the pool changes for them."""
+    from linear_recurrence_scans_gb300.mixer import SelectiveMixer, States
+    m = SelectiveMixer(width=32, channels=48, states=16, dtype=F32, seed=2)
+    u = torch.randn(3, 9, 32, device=DEV)
+    fresh = m.prompt(u)
+    states = States(m, 3)
+    for t in (states.conv, states.scan):
+        t.normal_()
+    before = states.conv.clone(), states.scan.clone()
+    for _ in range(2):
+        out = m.prompt(u, states, torch.tensor([-1, 7, 1 << 40], device=DEV))
+        assert torch.equal(out, fresh)
+        assert torch.equal(states.conv, before[0]) and torch.equal(states.scan, before[1])
+    m.prompt(u, states, torch.tensor([-1, 2, 3], device=DEV))
+    assert torch.equal(states.scan[:2], before[1][:2]) and not torch.equal(states.scan[2], before[1][2])
+    y = m.token(u[:, 0], states, torch.tensor([2, -1, 0], device=DEV))
+    assert (y[1] == 0).all()
