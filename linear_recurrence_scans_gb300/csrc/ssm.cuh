@@ -226,21 +226,6 @@ __device__ __forceinline__ float softplus_f(float v)
     return fmaxf(v, 0.f) + log1p_unit(exp_neg(-fabsf(v)));
 }
 
-// softplus(v) and its derivative sigmoid(v).
-__device__ __forceinline__ float softplus_f(float v, float &sig)
-{
-    const float e = exp_neg(-fabsf(v)), r = rcp_fast(1.f + e);
-    sig = v >= 0.f ? r : e * r;
-    return fmaxf(v, 0.f) + log1p_unit(e);
-}
-
-// sigmoid(v) = e^min(v,0) / (1 + e^-|v|).
-__device__ __forceinline__ float sigmoid_f(float v)
-{
-    const float e = exp_neg(-fabsf(v));
-    return (v >= 0.f ? 1.f : e) * rcp_fast(1.f + e);
-}
-
 // ------------------------------------------------------- pairs of floats
 // Two float32 in one 64-bit register pair: one instruction multiplies and
 // adds both.
