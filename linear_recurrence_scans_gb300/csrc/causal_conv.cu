@@ -7,9 +7,12 @@
 // with the last W-1 inputs in registers, so each input is read once but for
 // the W-1 rows before its run.  At a sequence's first row the window is
 // loaded from the sequence's x0 (a select, so nothing of the sequence before
-// reaches it).  A value takes 2 W + 4 flops: memory bounds the kernels.  32768
-// x 4096 bf16 channels, W = 4, take 97 us forward, 5.5 TB/s, and 164 us for
-// the gradients, 4.9 TB/s; float32 reaches 5.7 and 5.1 TB/s at half the width.
+// reaches it).  A value takes 2 W + 4 flops: memory bounds the forward.  32768
+// x 4096 bf16 channels, W = 4, take 97 us forward with a cold L2, 5.5 TB/s, and
+// 164 us for the gradients, 4.9 TB/s; float32 reaches 5.7 and 5.1 TB/s at half
+// the width.  The gradients fill neither DRAM (55% at 2048 channels) nor the
+// issue slots (51%): their 128 registers leave 14 warps an SM, which wait for
+// their own results.
 #include "ssm.cuh"
 
 namespace mg {
@@ -44,7 +47,7 @@ __device__ __forceinline__ Lanes<VEC> load_lanes(const T *from)
 // registers, and no other thread reads it, so nothing but the thread's own
 // copies is waited for.  A single bf16 comes as the 4-byte word that it is a
 // half of, with the value before it, or alone (8 x 4096 x 1001 channels: 54
-// us and 93 for the gradients, where loads at the use took 64 and 120).
+// us and 91 for the gradients, where loads at the use took 64 and 120).
 template <typename T, int VEC>
 struct Ring {
     static constexpr bool kHalf = sizeof(T) * VEC == 2;
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(kBlock, kBwdPerSm) conv_bwd_kernel(ConvArgs p,
             ring_g.fetch(g == 0 ? kGroups - 1 : g - 1, i0 + (kGroups - 1) * kUnroll, n);
             cp_async_commit();
             cp_async_wait<kGroups - 1>();
-                // whole, inside one sequence and the run, and no row before the
+            // whole, inside one sequence and the run, and no row before the
             // sequence is completed
             if (i0 + kUnroll <= own && k.hi > i0 + kUnroll && (k.lo < 0 || i0 - (W - 1) >= k.lo)) {
 #pragma unroll
@@ -608,7 +611,7 @@ mg_status conv_step(const ConvStepArgs &p, cudaStream_t s)
 
 size_t conv_ws_bytes(int64_t B, int64_t T, int64_t D, int W)
 {
-    // the parts of either vector width
+    // the most parts of any vector width
     size_t need = 0;
     for (int vec : {1, 2, 4}) {
         const Cut c = cut_bwd(B * T, D, vec);

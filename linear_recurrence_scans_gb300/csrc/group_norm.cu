@@ -11,9 +11,10 @@
 // A team keeps its group and walks over rows: its weights stay in registers,
 // and its next rows arrive by asynchronous copies into each thread's own slots
 // of shared memory, kAhead rows ahead.  Memory bounds the forward, 32768 x 4096
-// bf16 channels in one group in 134 us, 6.0 TB/s, and nearly the gradients of
-// groups that a warp holds (the same in 16 groups: 5.2 TB/s); in wider
-// groups they wait at the row's barriers (one group of 4096: 3.7 TB/s).
+// bf16 channels in one group in 133 us with a cold L2, 6.1 TB/s, and nearly the
+// gradients of groups that a warp holds (the same in 16 groups: 258 us, 5.2
+// TB/s); in wider groups they wait at the row's barriers (one group of 4096:
+// 359 us, 3.7 TB/s).
 #include "ssm.cuh"
 
 namespace mg {
@@ -162,7 +163,7 @@ __device__ __forceinline__ void pstore(float *to, const Lanes<VEC> &v, int count
 // 4-byte words that hold them: 4 bf16 that start in the middle of a word as
 // three, of which the value before them (never the first of a tensor) is
 // dropped.  8192 rows of 1001 bf16 channels in one group take 56 us, the
-// gradients 75, in 7 groups 66 and 88 (as pairs 62 and 86, 68 and 93; single
+// gradients 75, in 7 groups 65 and 87 (as pairs 62 and 86, 68 and 93; single
 // values loaded where they are used 136 and 157, 63 and 192).  Instructions
 // bound these.
 template <typename T, int VEC, int NV, int K>

@@ -41,10 +41,13 @@ namespace {
 // shared memory for its 16 states' row (2.1 or 3.9 clocks for a warp's load,
 // by pattern), which is below that.
 //
-// 4 x 4096 x 2048 bf16 channels of 16 states take 284 us, 1.9e12 states a
-// second: 120 for the states at the chunks' ends, 163 for the outputs, 3.3e12
-// a second at three warps a scheduler, which the registers of 16 states a
-// thread allow.  The bytes would need 30 us.
+// 4 x 4096 x 2048 bf16 channels of 16 states take 287 us with a cold L2, 1.9e12
+// states a second: 121 for the states at the chunks' ends, the rest for the
+// outputs (178 where states are saved for the gradients).  The bytes would need
+// 30 us.  Of a warp's row of 512 states the formulas are 48 instructions in the
+// first pass and 56 in the second; executed are 89 and 124: staging, addresses,
+// conversions and the sum over lanes, in both passes.  Three warps a scheduler
+// (the registers of 16 states a thread) issue in 65 and 62% of the slots.
 constexpr int kRows = 8;    // rows of a stage
 constexpr int kRing = 4;    // stages in flight or in use
 

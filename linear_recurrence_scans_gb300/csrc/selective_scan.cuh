@@ -176,8 +176,8 @@ __device__ __forceinline__ void cp_async4(void *dst, const void *src, int bytes)
 }
 
 // (Loaded value by value where they are used instead, rows of 1001 bf16
-// channels took 386 us where they now take 141, and their gradients 568 for
-// 295: 2 x 4096 rows of 16 states.)
+// channels took 386 us where they now take 142, and their gradients 568 for
+// 288: 2 x 4096 rows of 16 states.)
 //
 // Starts the copies of the words of ROWS row segments: row r's first channel
 // is value first + r * ld of base, its channels `wide`, and rows from `rows`

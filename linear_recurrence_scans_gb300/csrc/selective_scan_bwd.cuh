@@ -36,8 +36,8 @@ namespace mg {
 // shared memory for a second block: 2 x 4096 x 1024 channels of 64 states 1246
 // -> 838 us); the block's warps meet once a tile to add their dB and dC.
 //
-// 4 x 4096 x 2048 channels of 16 states take 770 us, 0.70e12 states a second:
-// 120 for the first pass, 620 here and 18 for the sums of the parts.
+// 4 x 4096 x 2048 channels of 16 states take 775 us, 0.69e12 states a second:
+// 120 for the first pass, 616 here and 18 for the sums of the parts.
 // Instructions bound it: 23 a state (10 of them the formulas', each state's
 // exponential taken twice), at half the issue slots with two warps a
 // scheduler, which is what the registers of kSub rows leave.  (B and C kept
@@ -646,7 +646,8 @@ __global__ void __launch_bounds__(256) sum_bc_kernel(const float *part, int64_t 
 // The gradients' threads: states of four channels, or, up to 8 states, of two,
 // whose registers let three blocks share an SM instead of two (2 x 4096 x 1024
 // channels of 8 states: 235 -> 162 us; of 16 it would be 821 -> 857, the sums
-// over lanes being of fewer values).  Blocks hold the tiles of 128 channels.
+// over lanes being of fewer values).  A block holds 128 channels, 64 from 17
+// states on and 32 from 33 on.
 inline int backward_lanes(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
 constexpr int backward_channels(int L) { return L <= 2 ? 2 : 4; }
 constexpr int backward_threads(int L) { return L == 1 ? 64 : kThreads; }
