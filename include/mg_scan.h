@@ -37,11 +37,9 @@
  *   After that a workspace may be reused by any later call of any op and any
  *   size up to the one it was sized for, without clearing: each launch resets
  *   its own control words, and no value that a call computes and leaves there
- *   reads as another call's record.  Pass the workspace's whole size as
- *   ws_bytes: once in 2^21 launches the library clears what it is given, since
- *   the launch numbers in the records begin again.  One workspace serves one
- *   call at a time: calls that overlap on the GPU (two streams, or two threads)
- *   must use separate workspaces or they race.
+ *   reads as another call's record.  One workspace serves one call at a time:
+ *   calls that overlap on the GPU (two streams, or two threads) must use
+ *   separate workspaces or they race.
  * Streams.  Calls are asynchronous on `stream` (0 = the legacy default
  *   stream).  Argument errors are reported synchronously, before any launch,
  *   by the return value.  The device-side chunk look-back waits are bounded;
@@ -442,9 +440,10 @@ mg_status mg_testing_linear_scan_fwd_stall(const float *a, const float *b, float
                                            int64_t stall_tile, uint64_t wait_limit_ns,
                                            cudaStream_t stream);
 
-/* Testing: the upper half of the 64-bit words that the look-back records of a
- * workspace's launch number `epoch` consist of (the lower half is the value). */
-uint32_t mg_testing_record_tag(uint64_t epoch);
+/* Testing: the upper half of the 64-bit words at the even or odd places of the
+ * look-back records of a workspace's launch number `epoch` (the lower half is
+ * the value). */
+uint32_t mg_testing_record_tag(uint64_t epoch, int odd);
 
 #ifdef __cplusplus
 }

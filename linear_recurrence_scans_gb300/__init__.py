@@ -164,7 +164,7 @@ def load():
         lib.mg_testing_linear_scan_fwd_stall.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, sz,
                                                          i64, ctypes.c_uint64, vp]
         lib.mg_testing_linear_scan_fwd_stall.restype = st
-        lib.mg_testing_record_tag.argtypes = [ctypes.c_uint64]
+        lib.mg_testing_record_tag.argtypes = [ctypes.c_uint64, i32]
         lib.mg_testing_record_tag.restype = ctypes.c_uint32
         lib.mg_linear_scan_fwd_noalloc.argtypes = [vp, vp, i32, vp, vp, i64, i64, i64, vp]
         lib.mg_linear_scan_fwd_noalloc.restype = st

@@ -695,7 +695,7 @@ struct LanePlan {
         if (wsb < need)
             return fail(MG_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", name, wsb, need);
         const ChanGeom g = geom(B, T, n);
-        const Lookback lb = make_lookback(ws, wsb, nt, o);
+        const Lookback lb = make_lookback(ws, nt, o);
         static const cudaError_t attr = cudaFuncSetAttribute(
             affine_lane_kernel<Cf>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cf::SMEM));
         if (attr != cudaSuccess) return fail(MG_ERR_LAUNCH, "%s: %s", name, cudaGetErrorString(attr));
@@ -1208,7 +1208,7 @@ struct ColPlan {
         g.nJ = int(B * n);
         g.nC = int((T + Cf::TC - 1) / Cf::TC);
         g.n_tiles = unsigned(nt);
-        const Lookback lb = make_lookback(ws, wsb, nt, o);
+        const Lookback lb = make_lookback(ws, nt, o);
         if (Cf::SMEM > 48 * 1024) {
             static const cudaError_t attr = cudaFuncSetAttribute(
                 affine_col_kernel<Cf>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cf::SMEM));
@@ -1797,7 +1797,7 @@ struct MmaPlan {
         g.nJ = int(B * n);
         g.nC = int((T + Cf::TC - 1) / Cf::TC);
         g.n_tiles = unsigned(nt);
-        const Lookback lb = make_lookback(ws, wsb, nt, o);
+        const Lookback lb = make_lookback(ws, nt, o);
         if (Cf::SMEM > 48 * 1024) {
             static const cudaError_t attr = cudaFuncSetAttribute(
                 affine_mma_kernel<Cf>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(Cf::SMEM));

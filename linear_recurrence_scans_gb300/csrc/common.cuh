@@ -33,9 +33,8 @@ inline size_t tiled_ws_bytes(size_t n_tiles, size_t record_bytes)
            n_tiles * record_bytes;
 }
 
-// Build the device-side look-back view of a workspace of `bytes` for `n_tiles`
-// records.
-inline Lookback make_lookback(void *ws, size_t bytes, size_t n_tiles, const LaunchOpts &o)
+// Build the device-side look-back view of a workspace for `n_tiles` records.
+inline Lookback make_lookback(void *ws, size_t n_tiles, const LaunchOpts &o)
 {
     Lookback lb;
     char *base = static_cast<char *>(ws);
@@ -45,8 +44,6 @@ inline Lookback make_lookback(void *ws, size_t bytes, size_t n_tiles, const Laun
         base + kControlBytes + align_up(n_tiles * sizeof(unsigned long long), 256));
     lb.wait_limit_ns = o.wait_limit_ns;
     lb.max_polls = o.max_polls;
-    // (every layout ends on a line; 2^32 lines are more than the device has)
-    lb.lines = unsigned(bytes / 64 < UINT32_MAX ? bytes / 64 : UINT32_MAX);
     lb.stall_tile = o.stall_tile;
     return lb;
 }

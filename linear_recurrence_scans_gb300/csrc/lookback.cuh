@@ -20,7 +20,7 @@
 //                       kFlagTag | epoch << 2 | status
 //   then                per-tile data, op-specific (aggregate and prefix),
 //                       as tagged 64-bit words where the op's records go
-//                       through the chunk engine (see record_tag)
+//                       through the chunk engine (see Tags)
 // A flag counts only if its epoch equals the launch's epoch, so stale flags
 // of earlier launches need no clearing.  The last CTA of every launch resets
 // the ticket and done counters and advances the epoch.  Where the flags or the
@@ -68,7 +68,6 @@ struct Lookback {
     float *data;                 // op-specific per-tile records
     unsigned long long wait_limit_ns;
     unsigned int max_polls;
-    unsigned int lines;          // of 64 bytes, the whole workspace
     long long stall_tile;        // testing only: this tile never publishes (-1: none)
 };
 
@@ -150,22 +149,38 @@ __device__ __forceinline__ unsigned flag_status(unsigned long long v, unsigned l
 // The tag read as a float is a negative signalling NaN (0xffa00000 up to
 // 0xffbfffff): no value that an op computes, not even the GPU's own NaN, has
 // its bits, and neither zero-filled memory nor a flag word (top 13 bits set)
-// does.  That leaves the low 21 bits of the epoch to tell launches apart: the
-// launch whose successor's bits begin again at 0 clears the workspace it was
-// given (finish_cta), so that no word of the cycle before is met.  The tile
+// does.  That leaves 21 bits for the epoch.  Words at even places of a record
+// carry its low 21 bits, those at odd places the next 21, so that a record
+// whose words all match is one of the running launch or of 2^42 launches ago.
+// (Words of both, in the midst of the write of a record that an older one
+// 2^21 launches ago precedes, would have to part a 16-byte access.)  The tile
 // that the testing option stalls writes tag 0, which no reader accepts, so its
 // successors wait on its flag as before.
-constexpr unsigned kTagNaN = 0xffa00000u, kTagEpochs = 1u << 21;
-__host__ __device__ __forceinline__ unsigned launch_tag(unsigned long long epoch)
+constexpr unsigned kTagNaN = 0xffa00000u, kTagBits = 21;
+__host__ __device__ __forceinline__ unsigned launch_tag(unsigned long long epoch, unsigned odd)
 {
-    return kTagNaN | (unsigned(epoch) & (kTagEpochs - 1u));
+    return kTagNaN | (unsigned(epoch >> (odd != 0u ? kTagBits : 0u)) & ((1u << kTagBits) - 1u));
 }
 
-// The tag `tile` writes into its records.
-__device__ __forceinline__ unsigned record_tag(const Lookback &lb, unsigned long long epoch,
-                                               unsigned tile)
+// The tags of a launch's words, by the parity of their place.
+struct Tags {
+    unsigned even, odd;
+    // Of word v of a lane's VEC.
+    template <int VEC>
+    __device__ __forceinline__ unsigned of(int lane, int v) const
+    {
+        return ((VEC % 2 == 0 ? v : lane * VEC + v) & 1) != 0 ? odd : even;
+    }
+};
+__device__ __forceinline__ Tags launch_tags(unsigned long long epoch)
 {
-    return (long long)tile == lb.stall_tile ? 0u : launch_tag(epoch);
+    return Tags{launch_tag(epoch, 0u), launch_tag(epoch, 1u)};
+}
+
+// The tags `tile` writes into its records.
+__device__ __forceinline__ Tags record_tags(const Lookback &lb, unsigned long long epoch, unsigned tile)
+{
+    return (long long)tile == lb.stall_tile ? Tags{0u, 0u} : launch_tags(epoch);
 }
 
 __device__ __forceinline__ unsigned long long tag_word(unsigned tag, float x)
@@ -323,11 +338,6 @@ __device__ __forceinline__ void publish(const Lookback &lb, size_t slot, unsigne
 
 // End of a CTA: count it; the launch's last CTA resets the ticket and done
 // counters and advances the epoch for the next launch on this workspace.
-// Where the tags' epochs begin again with that launch, it first clears all
-// behind the control block, whose older words would be taken for the next
-// launches'; every other CTA has counted itself behind its last access.  One
-// thread does it (15 ms for 64 MB): it comes up once in 2^21 launches, and a
-// loop of the whole CTA here cost the fused bf16 gradients 2% of every call.
 __device__ __forceinline__ void finish_cta(const Lookback &lb, unsigned long long epoch)
 {
     __syncthreads();
@@ -335,14 +345,6 @@ __device__ __forceinline__ void finish_cta(const Lookback &lb, unsigned long lon
         __threadfence();
         const unsigned prev = atomicAdd(&lb.ctl->done, 1u);
         if (prev == gridDim.x - 1) {
-            if ((unsigned(epoch + 1ull) & (kTagEpochs - 1u)) == 0u) {
-                uint4 *line = reinterpret_cast<uint4 *>(lb.ctl + 1);
-                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                __threadfence();
-#pragma unroll 1
-                for (unsigned i = kControlBytes / 64; i < lb.lines; ++i, line += 4)
-                    line[0] = line[1] = line[2] = line[3] = zero;
-            }
             lb.ctl->ticket = 0;
             lb.ctl->done = 0;
             lb.ctl->epoch = epoch + 1;

@@ -716,7 +716,7 @@ mg_status mg_testing_linear_scan_fwd_stall(const float *a, const float *b, float
     return launch_linear_fwd(a, b, MG_F32, A, Bc, B, T, D, ws, ws_bytes, stream, o);
 }
 
-uint32_t mg_testing_record_tag(uint64_t epoch) { return launch_tag(epoch); }
+uint32_t mg_testing_record_tag(uint64_t epoch, int odd) { return launch_tag(epoch, odd != 0); }
 
 size_t mg_linear_scan_fwd_noalloc_max_scratch(void) { return kNoAllocScratchBytes; }
 

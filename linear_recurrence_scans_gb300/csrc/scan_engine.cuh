@@ -88,7 +88,7 @@ struct StashView {
 // ------------------------------------------------------------ the engine
 
 // Records: [slot][kind: aggregate, prefix][state][DC] tagged 64-bit words
-// (record_tag), one per float; a lane owns VEC consecutive words per state.
+// (Tags), one per float; a lane owns VEC consecutive words per state.
 template <class Op, int TX>
 __device__ __forceinline__ unsigned long long *chan_record(const Lookback &lb, size_t slot,
                                                            int kind, int s, int lane)
@@ -138,7 +138,7 @@ __device__ __forceinline__ constexpr bool keeps(int s)
 
 template <class Op, int TX, unsigned MASK = all_states<Op>()>
 __device__ __forceinline__ void put_record(const Lookback &lb, size_t slot, int kind, int lane,
-                                           const typename Op::S &x, unsigned tag)
+                                           const typename Op::S &x, Tags tags)
 {
 #pragma unroll
     for (int s = 0; s < Op::NS; ++s) {
@@ -147,10 +147,11 @@ __device__ __forceinline__ void put_record(const Lookback &lb, size_t slot, int 
         if constexpr (Op::VEC % 2 == 0) {
 #pragma unroll
             for (int v = 0; v < Op::VEC; v += 2)
-                st_relaxed_v2u64(p + v, tag_word(tag, x.v[s][v]), tag_word(tag, x.v[s][v + 1]));
+                st_relaxed_v2u64(p + v, tag_word(tags.even, x.v[s][v]), tag_word(tags.odd, x.v[s][v + 1]));
         } else {
 #pragma unroll
-            for (int v = 0; v < Op::VEC; ++v) st_relaxed_u64(p + v, tag_word(tag, x.v[s][v]));
+            for (int v = 0; v < Op::VEC; ++v)
+                st_relaxed_u64(p + v, tag_word(tags.of<Op::VEC>(lane, v), x.v[s][v]));
         }
     }
 }
@@ -188,16 +189,16 @@ __device__ __forceinline__ typename Op::S record_values(const RawRecord<Op> &r)
     return x;
 }
 
-// Whether every kept word of the lane's part carries `tag`.
+// Whether every kept word of the lane's part carries its tag.
 template <class Op, unsigned MASK = all_states<Op>()>
-__device__ __forceinline__ bool record_tagged(const RawRecord<Op> &r, unsigned tag)
+__device__ __forceinline__ bool record_tagged(const RawRecord<Op> &r, int lane, Tags tags)
 {
     bool ok = true;
 #pragma unroll
     for (int s = 0; s < Op::NS; ++s)
         if (keeps<MASK>(s)) {
 #pragma unroll
-            for (int v = 0; v < Op::VEC; ++v) ok &= unsigned(r.w[s][v] >> 32) == tag;
+            for (int v = 0; v < Op::VEC; ++v) ok &= unsigned(r.w[s][v] >> 32) == tags.of<Op::VEC>(lane, v);
         }
     return ok;
 }
@@ -230,6 +231,14 @@ struct op_tagged<Op, decltype(void(Op::kTagged))> {
     static constexpr bool value = MG_LB_TAGGED != 0 && Op::kTagged;
 };
 
+// The tags of a tile's records: those of an op that reads records under their
+// flags alone carry 0, which no reader accepts.
+template <class Op>
+__device__ __forceinline__ Tags tags_for(const Lookback &lb, unsigned long long epoch, unsigned tile)
+{
+    return op_tagged<Op>::value ? record_tags(lb, epoch, tile) : Tags{0u, 0u};
+}
+
 // First half of the look-back (one warp): publish this chunk's record as
 // early as possible.  Chunk 0 publishes its inclusive prefix (initial o cta)
 // at once; any other chunk publishes its aggregate, unless `peek` is set and
@@ -247,7 +256,7 @@ __device__ int publish_first(const typename Op::Args &args, const ChanGeom &g,
 {
     const int lane = threadIdx.x & 31;
     const size_t slot = size_t(c) * g.nJ + j;
-    const unsigned tag = record_tag(lb, epoch, tile);
+    const Tags tag = tags_for<Op>(lb, epoch, tile);
     if (c == 0) {
         if (lact)
             put_record<Op, TX, op_prefix_states<Op>::value>(
@@ -318,7 +327,7 @@ __device__ __forceinline__ typename Op::S look_back(const typename Op::Args &arg
 {
     constexpr unsigned PS = op_prefix_states<Op>::value;
     if (TAGGED && c > 0 &&
-        __all_sync(0xffffffffu, !lact || record_tagged<Op, PS>(pre, launch_tag(epoch))))
+        __all_sync(0xffffffffu, !lact || record_tagged<Op, PS>(pre, threadIdx.x & 31, launch_tags(epoch))))
         return lact ? record_values<Op, PS>(pre) : Op::identity();
     const int p0 = publish_first<Op, TX, PEEK>(args, g, lb, c, j, bb, ld, lact, lchan, tile, epoch,
                                                cta);
@@ -338,7 +347,7 @@ __device__ void publish_prefix(const ChanGeom &g, const Lookback &lb, int c, int
     if (lact)
         put_record<Op, TX, op_prefix_states<Op>::value>(lb, slot, 1, threadIdx.x & 31,
                                                         Op::combine(excl, cta),
-                                                        record_tag(lb, epoch, tile));
+                                                        tags_for<Op>(lb, epoch, tile));
     publish(lb, slot, kStatusPrefix, epoch, tile);
 }
 
@@ -513,7 +522,7 @@ struct ChanPlan {
             return fail(MG_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", name,
                         ws_bytes_given, need);
         const ChanGeom g = geom(B, T, D);
-        const Lookback lb = make_lookback(ws, ws_bytes_given, nt, o);
+        const Lookback lb = make_lookback(ws, nt, o);
         constexpr size_t smem =
             (size_t(TY + 1) * Op::NS * DC +
              (op_stashes<Op>::value ? size_t(R) * Op::L * Op::NS * TX * TY * Op::VEC : 0)) *

@@ -28,8 +28,12 @@ def _scans(mg, ws_bytes):
     cu = torch.tensor([0, 7, 2100, 4096], device=DEV)
     assert ws_bytes >= max(mg.linear_workspace_size(2, 4096, 256), mg.log_workspace_size(2, 4096, 256),
                            mg.mingru_workspace_size(2, 4096, 256), mg.varlen_workspace_size(4096, 256))
+    oa, ob, og = (t[..., :255].contiguous() for t in (a, b, gB))   # one channel a lane
+    oA, oBc = mg.linear_scan_fwd(oa, ob)
     return {
         "linear": lambda ws: mg.linear_scan_fwd(a, b, ws=ws),
+        "linear odd": lambda ws: mg.linear_scan_fwd(oa, ob, ws=ws),
+        "linear odd bwd": lambda ws: mg.linear_scan_bwd(oa, oA, oBc, og, og, ws=ws),
         "linear bf16": lambda ws: mg.linear_scan_fwd(a.bfloat16(), b.bfloat16(), ws=ws),
         "linear bwd": lambda ws: mg.linear_scan_bwd(a, A, Bc, gA, gB, ws=ws),
         "log": lambda ws: (mg.parallel_scan_log_fwd(lc, lv, ws=ws),),
@@ -74,36 +78,33 @@ def test_no_value_is_a_record(cuda_lib, value):
             mg.workspace_status(ws)
 
 
-def test_a_new_cycle_of_tags_meets_no_older_word(cuda_lib):
-    """The launch before the tags begin again clears the workspace: words of the
-    cycle before, with the next launch's own tag, are gone."""
+def _tagged_words(mg, ws, epoch, value):
+    """Fills the workspace behind its control block with `value` in words tagged
+    as those of launch `epoch`."""
+    bits = torch.tensor(value).view(torch.int32).item()
+    words = ws[CONTROL:].view(torch.int64).view(-1, 2)
+    for odd in (0, 1):
+        words[:, odd] = (mg.load().mg_testing_record_tag(epoch, odd) - (1 << 32) << 32) | bits
+
+
+@pytest.mark.parametrize("epoch", [(1 << 21) - 1, 1 << 21, 3 << 21, (1 << 42) - 2])
+def test_records_of_earlier_launches_are_not_taken(cuda_lib, epoch):
+    """Words of launches whose numbers agree with the running one's in the even
+    or in the odd places' bits; across the numbers at which these begin again."""
     mg = cuda_lib
-    size, cycle = 64 << 20, 1 << 21
+    size = 64 << 20
     own = mg.new_workspace(size, DEV)
-    a, b, _, _ = (t.to(DEV) for t in wl.mingru_linear(1, 200, 64, seed=44))
-    small = mg.linear_scan_fwd(a, b)
-    word = (mg.load().mg_testing_record_tag(cycle) - (1 << 32) << 32) | 0x40e00000   # 7.0, as int64
     for name, scan in _scans(mg, size).items():
         want = scan(own)
-        for first in ("small", "itself"):
+        for older in (epoch - (1 << 21), epoch - 1, epoch ^ 1, epoch ^ (1 << 41)):
             ws = mg.new_workspace(size, DEV)
-            _epoch(ws, cycle - 1)
-            ws[CONTROL:].view(torch.int64).fill_(word)
-            got = mg.linear_scan_fwd(a, b, ws=ws) if first == "small" else scan(ws)
-            assert all(torch.equal(p, q) for p, q in zip(got, small if first == "small" else want)), (name, first)
-            assert _epoch(ws) == cycle and not ws[:8].any() and not ws[CONTROL:].any()
-            got = scan(ws)
-            assert all(torch.equal(p, q) for p, q in zip(got, want)), (name, first)
-            assert _epoch(ws) == cycle + 1
+            _epoch(ws, epoch)
+            for k in range(2):
+                _tagged_words(mg, ws, (older + k) % (1 << 64), 7.0)
+                got = scan(ws)
+                assert all(torch.equal(p, q) for p, q in zip(got, want)), (name, older)
+            assert _epoch(ws) == epoch + 2
             mg.workspace_status(ws)
-    Am, Bm, _, _ = wl.haar_affine(1, 300, 2, 16, 16, seed=45, grads=False)   # a kernel of its own
-    Am, Bm = Am.to(DEV), Bm.to(DEV)
-    ws = mg.new_workspace(size, DEV)
-    _epoch(ws, cycle - 1)
-    want = mg.affine_scan_fwd(Am, Bm)
-    for _ in range(2):
-        assert all(torch.equal(p, q) for p, q in zip(mg.affine_scan_fwd(Am, Bm, ws=ws), want))
-    assert _epoch(ws) == cycle + 1
 
 
 def test_a_replayed_graph_writes_no_memory_of_others(cuda_lib):
