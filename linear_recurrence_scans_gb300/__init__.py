@@ -33,6 +33,8 @@ Ops (names of the C entry points; aliases with the names of the page
 
 * the selective state space mixer's operators, ``causal_conv_*``, ``selective_scan_*`` and
   ``group_norm_*`` (see ``ssm.py``)
+* the gated block's operators, ``gated_scan_*`` (a gated recurrence with a matrix state per head)
+  and ``rms_norm_*`` (with the residual's addition; see ``block.py``)
 
 Every op accepts optional preallocated outputs (``out=(...)``), a workspace
 tensor (``ws=``, uint8, zero-filled before first use) and a stream
@@ -180,8 +182,9 @@ def load():
                      "mg_linear_scan_varlen_bwd", "mg_affine_scan_h0_fwd",
                      "mg_affine_scan_h0_bwd", "mg_angle_scan_fwd", "mg_angle_scan_bwd"):
             getattr(lib, name).restype = st
-        from . import ssm
+        from . import block, ssm
         ssm.declare(lib)
+        block.declare(lib)
         _lib = lib
     return _lib
 
@@ -743,3 +746,10 @@ from .ssm import *  # noqa: E402,F401,F403
 
 __all__ += _ssm.__all__
 SYMBOLS += _ssm.SYMBOLS
+
+# The gated block's operators (gated_scan_*, rms_norm_*).
+from . import block as _block  # noqa: E402
+from .block import *  # noqa: E402,F401,F403
+
+__all__ += _block.__all__
+SYMBOLS += _block.SYMBOLS

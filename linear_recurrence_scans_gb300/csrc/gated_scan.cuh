@@ -1,0 +1,106 @@
+// Shared by the gated recurrence's kernels: chunks of rows, gates within a
+// chunk, the passes over chunks.
+#pragma once
+
+#include "block.cuh"
+
+namespace mg {
+
+// Gates below this count as this: exp(-128) is 0 in float32, and sums of a
+// chunk's gates keep their precision.
+constexpr float kLeastGate = -128.f;
+__device__ __forceinline__ float gate_of(float g) { return g < kLeastGate ? kLeastGate : g; }
+
+// A batch's chunks of up to L rows, none of them across two sequences.  Dense:
+// `per` in each sequence.  Packed: sequence s has the chunks first[s] ..
+// first[s+1]-1, a table that chunk_table() leaves in the workspace.
+struct Chunks {
+    Seqs q;
+    const int *first;
+    int per, L;
+    long long most;   // chunks that buffers have room for
+
+    struct One {
+        long long row;
+        int len, seq;
+    };
+    // Chunk c; len 0: there is none.
+    __device__ __forceinline__ One get(long long c) const
+    {
+        One o{0, 0, 0};
+        if (q.cu == nullptr) {
+            o.seq = int(c / per);
+            const long long at = (c - (long long)o.seq * per) * L;
+            o.row = (long long)o.seq * q.T + at;
+            o.len = int(q.T - at < L ? q.T - at : L);
+            return o;
+        }
+        if (c >= __ldg(first + q.nseq)) return o;
+        int lo = 0, hi = q.nseq;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (__ldg(first + mid) <= c) lo = mid; else hi = mid;
+        }
+        long long a, b;
+        bounds(lo, a, b);
+        o.seq = lo;
+        o.row = a + (c - __ldg(first + lo)) * L;
+        o.len = int(b - o.row < L ? b - o.row : L);
+        return o;
+    }
+    // Rows a .. b-1 of sequence s, inside the batch whatever cu holds.
+    __device__ __forceinline__ void bounds(int s, long long &a, long long &b) const
+    {
+        a = __ldg(q.cu + s), b = __ldg(q.cu + s + 1);
+        a = a < 0 ? 0 : a > q.rows ? q.rows : a;
+        b = b < a ? a : b > q.rows ? q.rows : b;
+    }
+    __device__ __forceinline__ long long begin(int s) const { return q.cu == nullptr ? (long long)s * per : __ldg(first + s); }
+    __device__ __forceinline__ long long end(int s) const { return begin(s + 1); }
+};
+
+// The most chunks that a batch can have.
+inline int64_t chunks_most(int64_t B, int64_t T, int64_t nseq, bool packed, int L)
+{
+    return packed ? T / L + (nseq < T ? nseq : T) : B * ceil_div(T, L);
+}
+
+// The workspace's parts: [control][first][totals][states][more].
+struct GatedWs {
+    int64_t chunks;
+    size_t first, totals, states, more;   // offsets
+};
+inline GatedWs gated_ws(int64_t B, int64_t T, int64_t H, int64_t N, int64_t P, int64_t nseq, bool packed, int L,
+                        bool states)
+{
+    GatedWs w{};
+    w.chunks = chunks_most(B, T, nseq, packed, L);
+    w.first = kControlBytes;
+    w.totals = w.first + align_up(packed ? size_t(nseq + 1) * 4 : 0, 256);
+    w.states = w.totals + align_up(size_t(w.chunks) * H * 4, 256);
+    w.more = w.states + (states ? align_up(size_t(w.chunks) * H * N * P * 4, 256) : 0);
+    return w;
+}
+
+// Packed batches: checks cu and fills the chunk table.
+mg_status launch_chunk_table(const Chunks &c, int *first, void *ws, cudaStream_t s);
+
+// Over the chunks of every sequence and head, in place: states[c] holds what
+// chunk c adds, and is left with what comes to it: the state before it
+// (forward), or the adjoint of the state behind it (backward = true), from
+// `from` (NULL: zero); `to` (may be NULL) gets what comes out at the end.
+// totals[c] is the sum of a chunk's gates.
+mg_status launch_over_chunks(const Chunks &c, float *states, const float *totals, const float *from, float *to, int H,
+                             int64_t NP, bool backward, cudaStream_t s);
+
+// The kernels' arguments.
+struct GatedCall {
+    GatedArgs a;
+    Chunks c;
+    float *totals, *states;      // states before each chunk
+    float *adjoints;             // of the states behind each chunk
+    float *partial;              // sums over some of a group's heads: dq, dk
+    int splits, heads;           // blocks for a group's heads, heads of each
+};
+
+}  // namespace mg

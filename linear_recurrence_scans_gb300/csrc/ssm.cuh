@@ -154,17 +154,17 @@ mg_status launch_next(const char *what, void (*kernel)(P...), int64_t grid, dim3
 // memory too): allowed once for a kernel and device, up to what a block may
 // have.  The set-up costs as much as a launch.
 constexpr size_t kMostShared = 226 * 1024;
-template <auto kKernel>
+template <auto kKernel, size_t kMost = kMostShared>
 mg_status allow_shared(size_t bytes)
 {
     if (bytes <= 40 * 1024) return MG_OK;
-    if (bytes > kMostShared) return fail(MG_ERR_UNSUPPORTED, "%zu bytes of shared memory", bytes);
+    if (bytes > kMost) return fail(MG_ERR_UNSUPPORTED, "%zu bytes of shared memory", bytes);
     static std::atomic<uint64_t> done{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
     if (e == cudaSuccess && (done.load() & bit) == 0) {
-        e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMostShared));
+        e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost));
         if (e == cudaSuccess) done.fetch_or(bit);
     }
     return e == cudaSuccess ? MG_OK : fail(MG_ERR_LAUNCH, "shared memory: %s", cudaGetErrorString(e));
