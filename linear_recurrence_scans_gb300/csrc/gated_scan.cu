@@ -26,36 +26,38 @@ namespace {
 
 // ------------------------------------------------------------ chunk table
 
-__global__ void __launch_bounds__(1024) chunk_table_kernel(const Chunks c, int *first, void *ws)
+// A block a cut.  Nothing of a cu that breaks the rules is used: its tables
+// name no chunks.
+__global__ void __launch_bounds__(1024) chunk_table_kernel(const Chunks c0, const Chunks c1, void *ws)
 {
     __shared__ int sums[32];
-    __shared__ long long base;
+    const Chunks &c = blockIdx.x == 0 ? c0 : c1;
+    int *first = const_cast<int *>(c.first);
     check_cu(c.q, error_word(ws), threadIdx.x, blockDim.x);
-    if (threadIdx.x == 0) base = 0;
-    __syncthreads();
+    bool bad = false;
+    for (int s = threadIdx.x; s < c.q.nseq; s += 1024) {
+        const long long a = __ldg(c.q.cu + s), b = __ldg(c.q.cu + s + 1);
+        bad = bad || b < a || (s == 0 && a != 0) || (s + 1 == c.q.nseq && b != c.q.rows);
+    }
+    bad = __syncthreads_or(bad);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int base = 0;
+    if (threadIdx.x == 0) first[0] = 0;
     for (int s0 = 0; s0 < c.q.nseq; s0 += 1024) {
         const int s = s0 + threadIdx.x;
-        long long a = 0, b = 0;
-        if (s < c.q.nseq) c.bounds(s, a, b);
-        const int n = int((b - a + c.L - 1) / c.L);
-        int v = n;
+        int v = s < c.q.nseq && !bad ? int((__ldg(c.q.cu + s + 1) - __ldg(c.q.cu + s) + c.L - 1) / c.L) : 0;
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(~0u, v, o);
             if (lane >= o) v += u;
         }
         if (lane == 31) sums[warp] = v;
         __syncthreads();
-        long long at = base;
-        for (int w = 0; w < warp; ++w) at += sums[w];
-        at += v;
-        // sequences that overlap (a cu that breaks the rules) stay within the room
-        if (s < c.q.nseq) {
-            if (s == 0) first[0] = 0;
-            first[s + 1] = int(at < c.most ? at : c.most);
+        int before = base;
+        for (int w = 0; w < 32; ++w) {
+            if (w < warp) before += sums[w];
+            base += sums[w];
         }
-        __syncthreads();
-        if (threadIdx.x == 1023) base = at;
+        if (s < c.q.nseq) first[s + 1] = before + v;
         __syncthreads();
     }
 }
@@ -79,6 +81,9 @@ __global__ void __launch_bounds__(256) over_chunks_kernel(const Chunks c, float 
 #pragma unroll
     for (int e = 0; e < VEC; ++e) s[e] = 0.f;
     if (from != nullptr) load_vec<VEC>(from + sh * NP + at, s);
+    // + 0: a caller's signalling NaN must not get into the workspace as it is
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) s[e] += 0.f;
     for (int64_t i0 = 0; i0 < hi - lo; i0 += kAhead) {
         float add[kAhead][VEC], decay[kAhead];
 #pragma unroll
@@ -143,13 +148,13 @@ __device__ __forceinline__ void clear(float (&acc)[MI][NJ])
 
 // `rows` x `cols` values, times `by`, as ROWS x CB with row stride LD; zeros
 // beside and below.
-template <int ROWS, int CB, int LD, typename T>
-__device__ __forceinline__ void load_tile(float *to, const T *from, int64_t ld, int rows, int cols, float by = 1.f)
+template <int ROWS, int CB, int LD>
+__device__ __forceinline__ void load_tile(float *to, const float *from, int64_t ld, int rows, int cols, float by = 1.f)
 {
 #pragma unroll 8
     for (int i = threadIdx.x; i < ROWS * CB; i += kThreads) {
         const int r = i / CB, c = i % CB;
-        to[r * LD + c] = r < rows && c < cols ? load1(from + r * ld + c) * by : 0.f;
+        to[r * LD + c] = r < rows && c < cols ? __ldg(from + r * ld + c) * by : 0.f;
     }
 }
 
@@ -179,7 +184,7 @@ __device__ __forceinline__ float span(const Gates &s, int i, int j)   // e^{G_i 
 __device__ __forceinline__ float span(const Gates &s, int i) { return expf(s.hi[i]) * (1.f + s.lo[i]); }
 
 // What a chunk adds to the state (to its adjoint with BACK), and its total gate.
-template <typename T, int NB, int PB, bool BACK>
+template <int NB, int PB, bool BACK>
 __global__ void __launch_bounds__(kThreads) gated_add_kernel(const GatedCall p)
 {
     extern __shared__ float sm[];
@@ -191,9 +196,9 @@ __global__ void __launch_bounds__(kThreads) gated_add_kernel(const GatedCall p)
     if (ch.len == 0) return;
     float *K = sm, *V = sm + kL * NB;
     load_gates(gates, a.g + ch.row * a.ldg + h, a.ldg, ch.len);
-    load_tile<kL, NB, NB>(K, static_cast<const T *>(BACK ? a.q : a.k) + ch.row * (BACK ? a.ldq : a.ldk) + grp * a.N,
+    load_tile<kL, NB, NB>(K, static_cast<const float *>(BACK ? a.q : a.k) + ch.row * (BACK ? a.ldq : a.ldk) + grp * a.N,
                           BACK ? a.ldq : a.ldk, ch.len, a.N, BACK ? a.scale : 1.f);
-    load_tile<kL, PB, PB>(V, static_cast<const T *>(BACK ? a.dout : a.v) + ch.row * (BACK ? a.lddo : a.ldv) + h * a.P,
+    load_tile<kL, PB, PB>(V, static_cast<const float *>(BACK ? a.dout : a.v) + ch.row * (BACK ? a.lddo : a.ldv) + h * a.P,
                           BACK ? a.lddo : a.ldv, ch.len, a.P);
     __syncthreads();
     for (int i = threadIdx.x; i < kL * PB; i += kThreads) V[i] *= BACK ? span(gates, i / PB) : span(gates, kL - 1, i / PB);
@@ -214,7 +219,7 @@ __global__ void __launch_bounds__(kThreads) gated_add_kernel(const GatedCall p)
 }
 
 // o of a chunk and head.
-template <typename T, int NB, int PB>
+template <int NB, int PB>
 __global__ void __launch_bounds__(kThreads) gated_out_kernel(const GatedCall p)
 {
     extern __shared__ float sm[];
@@ -227,9 +232,9 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(const GatedCall p)
     if (ch.len == 0) return;
     float *Q = sm, *K = Q + kL * LN, *V = K + kL * KN, *W = K;   // weights take K's place
     load_gates(gates, a.g + ch.row * a.ldg + h, a.ldg, ch.len);
-    load_tile<kL, NB, LN>(Q, static_cast<const T *>(a.q) + ch.row * a.ldq + grp * a.N, a.ldq, ch.len, a.N, a.scale);
-    load_tile<kL, NB, LN>(K, static_cast<const T *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
-    load_tile<kL, PB, PB>(V, static_cast<const T *>(a.v) + ch.row * a.ldv + h * a.P, a.ldv, ch.len, a.P);
+    load_tile<kL, NB, LN>(Q, static_cast<const float *>(a.q) + ch.row * a.ldq + grp * a.N, a.ldq, ch.len, a.N, a.scale);
+    load_tile<kL, NB, LN>(K, static_cast<const float *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
+    load_tile<kL, PB, PB>(V, static_cast<const float *>(a.v) + ch.row * a.ldv + h * a.P, a.ldv, ch.len, a.P);
     __syncthreads();
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     float w[4][4];
@@ -267,13 +272,13 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(const GatedCall p)
     }
     __syncthreads();
     mm<4, PB / 16, LP, 1, PB, 1>(acc, W, V, ch.len);
-    T *o = static_cast<T *>(a.o) + (ch.row * a.H + h) * a.P;
+    float *o = static_cast<float *>(a.o) + (ch.row * a.H + h) * a.P;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < PB / 16; ++j) {
             const int r = ty + 16 * i, q = tx + 16 * j;
-            if (r < ch.len && q < a.P) store1(o + int64_t(r) * a.H * a.P + q, acc[i][j]);
+            if (r < ch.len && q < a.P) o[int64_t(r) * a.H * a.P + q] = acc[i][j];
         }
 }
 
@@ -287,7 +292,7 @@ __device__ __forceinline__ float over_row(float v)
 
 // dv and dg of a chunk's heads, and dq and dk summed over them: a group's heads,
 // or a part of them whose sums then go to `partial`.
-template <typename T, int NB, int PB>
+template <int NB, int PB>
 __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
 {
     extern __shared__ float sm[];
@@ -301,8 +306,8 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
     if (ch.len == 0) return;
     float *Q = sm, *K = Q + kL * LN, *V = K + kL * LN, *dO = V + kL * LV, *W = dO + kL * LV, *dW = W + kL * LP, *St = dW + kL * LP;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    load_tile<kL, NB, LN>(Q, static_cast<const T *>(a.q) + ch.row * a.ldq + grp * a.N, a.ldq, ch.len, a.N);
-    load_tile<kL, NB, LN>(K, static_cast<const T *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
+    load_tile<kL, NB, LN>(Q, static_cast<const float *>(a.q) + ch.row * a.ldq + grp * a.N, a.ldq, ch.len, a.N);
+    load_tile<kL, NB, LN>(K, static_cast<const float *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
     const int per_group = a.H / a.G, h0 = split * p.heads, h1 = h0 + p.heads < per_group ? h0 + p.heads : per_group;
     float dq[4][NJ], dk[4][NJ];
     clear(dq), clear(dk);
@@ -310,8 +315,8 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
         const int h = grp * per_group + hh;
         __syncthreads();
         load_gates(gates, a.g + ch.row * a.ldg + h, a.ldg, ch.len);
-        load_tile<kL, PB, LV>(V, static_cast<const T *>(a.v) + ch.row * a.ldv + h * a.P, a.ldv, ch.len, a.P);
-        load_tile<kL, PB, LV>(dO, static_cast<const T *>(a.dout) + ch.row * a.lddo + h * a.P, a.lddo, ch.len, a.P, a.scale);
+        load_tile<kL, PB, LV>(V, static_cast<const float *>(a.v) + ch.row * a.ldv + h * a.P, a.ldv, ch.len, a.P);
+        load_tile<kL, PB, LV>(dO, static_cast<const float *>(a.dout) + ch.row * a.lddo + h * a.P, a.lddo, ch.len, a.P, a.scale);
         __syncthreads();
         {
             float s[4][4], d[4][4], cols[4] = {};
@@ -387,7 +392,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
                 }
             }
         }
-        T *out = static_cast<T *>(a.dv) + (ch.row * a.H + h) * a.P;
+        float *out = static_cast<float *>(a.dv) + (ch.row * a.H + h) * a.P;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int r = ty + 16 * i;
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
 #pragma unroll
             for (int j = 0; j < PJ; ++j) {
                 const int q = tx + 16 * j;
-                if (r < ch.len && q < a.P) store1(out + int64_t(r) * a.H * a.P + q, fmaf(tail, in_d[i][j], dv[i][j]));
+                if (r < ch.len && q < a.P) out[int64_t(r) * a.H * a.P + q] = fmaf(tail, in_d[i][j], dv[i][j]);
             }
             const float x = over_row(of_q[i]), y = over_row(of_k[i]);
             if (tx == 0) sum_row[r] += x, sum_key[r] = y;
@@ -433,8 +438,8 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
             if (r >= ch.len || n >= a.N) continue;
             const int64_t at = (ch.row + r) * a.G * a.N + grp * a.N + n;
             if (p.splits == 1) {
-                store1(static_cast<T *>(a.dq) + at, dq[i][j]);
-                store1(static_cast<T *>(a.dk) + at, dk[i][j]);
+                static_cast<float *>(a.dq)[at] = dq[i][j];
+                static_cast<float *>(a.dk)[at] = dk[i][j];
             } else {
                 float *part = p.partial + (int64_t(split) * 2 * a.B * a.T * a.G * a.N) + at;
                 part[0] = dq[i][j], part[a.B * a.T * a.G * a.N] = dk[i][j];
@@ -443,13 +448,12 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
 }
 
 // dq and dk from their parts.
-template <typename T>
-__global__ void __launch_bounds__(256) gated_join_kernel(const float *part, int splits, int64_t n, T *dq, T *dk)
+__global__ void __launch_bounds__(256) gated_join_kernel(const float *part, int splits, int64_t n, float *dq, float *dk)
 {
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < 2 * n; i += int64_t(gridDim.x) * 256) {
         float v = 0.f;
         for (int s = 0; s < splits; ++s) v += part[s * 2 * n + i];
-        store1(i < n ? dq + i : dk + (i - n), v);
+        *(i < n ? dq + i : dk + (i - n)) = v;
     }
 }
 
@@ -523,70 +527,65 @@ int splits_for(int64_t chunks, int H, int G)
     return int(ceil_div(per, heads));
 }
 
-template <typename T, int NB, int PB>
+template <int NB, int PB>
 mg_status fwd_sized(const GatedCall &p, cudaStream_t s)
 {
     const GatedArgs &a = p.a;
     const int64_t blocks = p.c.most * a.H;
     constexpr int LN = NB + 1, KN = LN > kL + 1 ? LN : kL + 1;
     constexpr size_t add = size_t(kL) * (NB + PB) * 4, out = size_t(kL) * (LN + KN + PB) * 4;
-    MG_TRY((allow_shared<gated_add_kernel<T, NB, PB, false>, kRoom>(add)));
-    MG_TRY((allow_shared<gated_out_kernel<T, NB, PB>, kRoom>(out)));
-    gated_add_kernel<T, NB, PB, false><<<unsigned(blocks), kThreads, add, s>>>(p);
+    MG_TRY((allow_shared<gated_add_kernel<NB, PB, false>, kRoom>(add)));
+    MG_TRY((allow_shared<gated_out_kernel<NB, PB>, kRoom>(out)));
+    gated_add_kernel<NB, PB, false><<<unsigned(blocks), kThreads, add, s>>>(p);
     MG_TRY(launched("mg_gated_scan_fwd"));
     MG_TRY(launch_over_chunks(p.c, p.states, p.totals, a.S0, a.S_last, a.H, int64_t(a.N) * a.P, false, s));
-    gated_out_kernel<T, NB, PB><<<unsigned(blocks), kThreads, out, s>>>(p);
+    gated_out_kernel<NB, PB><<<unsigned(blocks), kThreads, out, s>>>(p);
     return launched("mg_gated_scan_fwd");
 }
 
-template <typename T, int NB, int PB>
+template <int NB, int PB>
 mg_status bwd_sized(const GatedCall &p, cudaStream_t s)
 {
     const GatedArgs &a = p.a;
     const int64_t blocks = p.c.most * a.H, grads = p.c.most * a.G * p.splits;
     constexpr size_t add = size_t(kL) * (NB + PB) * 4;
     constexpr size_t grad = size_t(kL) * (2 * (NB + 1) + 2 * (PB + 1) + 2 * (kL + 1)) * 4 + size_t(NB < 64 ? NB : 64) * (PB + 1) * 4;
-    MG_TRY((allow_shared<gated_add_kernel<T, NB, PB, true>, kRoom>(add)));
-    MG_TRY((allow_shared<gated_grad_kernel<T, NB, PB>, kRoom>(grad)));
-    gated_add_kernel<T, NB, PB, true><<<unsigned(blocks), kThreads, add, s>>>(p);
+    MG_TRY((allow_shared<gated_add_kernel<NB, PB, true>, kRoom>(add)));
+    MG_TRY((allow_shared<gated_grad_kernel<NB, PB>, kRoom>(grad)));
+    gated_add_kernel<NB, PB, true><<<unsigned(blocks), kThreads, add, s>>>(p);
     MG_TRY(launched("mg_gated_scan_bwd"));
     MG_TRY(launch_over_chunks(p.c, p.adjoints, p.totals, a.dS_last, a.dS0, a.H, int64_t(a.N) * a.P, true, s));
-    gated_grad_kernel<T, NB, PB><<<unsigned(grads), kThreads, grad, s>>>(p);
+    gated_grad_kernel<NB, PB><<<unsigned(grads), kThreads, grad, s>>>(p);
     MG_TRY(launched("mg_gated_scan_bwd"));
     if (p.splits == 1) return MG_OK;
     const int64_t n = a.B * a.T * a.G * a.N, want = ceil_div(2 * n, 256);
-    gated_join_kernel<T><<<unsigned(want < 8192 ? want : 8192), 256, 0, s>>>(p.partial, p.splits, n, static_cast<T *>(a.dq), static_cast<T *>(a.dk));
+    gated_join_kernel<<<unsigned(want < 8192 ? want : 8192), 256, 0, s>>>(p.partial, p.splits, n, static_cast<float *>(a.dq), static_cast<float *>(a.dk));
     return launched("mg_gated_scan_bwd");
 }
 
-// F<T, NB, PB> for the sizes that hold N and P.
-#define MG_GATED_P(F, T, NB)                           \
-    if (p.a.P <= 32) return F<T, NB, 32>(p, s);        \
-    if (p.a.P <= 64) return F<T, NB, 64>(p, s);        \
-    return F<T, NB, 128>(p, s);
-#define MG_GATED(F, T)                                 \
-    if (p.a.N <= 32) { MG_GATED_P(F, T, 32) }          \
-    if (p.a.N <= 64) { MG_GATED_P(F, T, 64) }          \
-    MG_GATED_P(F, T, 128)
-template <typename T>
-mg_status fwd_typed(const GatedCall &p, cudaStream_t s) { MG_GATED(fwd_sized, T) }
-template <typename T>
-mg_status bwd_typed(const GatedCall &p, cudaStream_t s) { MG_GATED(bwd_sized, T) }
-
-int chunk_rows(mg_dtype) { return kL; }
+// F<NB, PB> for the sizes that hold N and P.
+#define MG_GATED_P(F, NB)                           \
+    if (p.a.P <= 32) return F<NB, 32>(p, s);        \
+    if (p.a.P <= 64) return F<NB, 64>(p, s);        \
+    return F<NB, 128>(p, s);
+#define MG_GATED(F)                                 \
+    if (p.a.N <= 32) { MG_GATED_P(F, 32) }          \
+    if (p.a.N <= 64) { MG_GATED_P(F, 64) }          \
+    MG_GATED_P(F, 128)
+mg_status fwd_any(const GatedCall &p, cudaStream_t s) { MG_GATED(fwd_sized) }
+mg_status bwd_any(const GatedCall &p, cudaStream_t s) { MG_GATED(bwd_sized) }
 
 // The call's chunks, checked against what a grid and the chunk table's 32-bit
 // counts hold.
-mg_status make_call(const GatedArgs &a, mg_dtype dt, bool bwd, GatedCall &p)
+mg_status make_call(const GatedArgs &a, bool bwd, GatedCall &p)
 {
     const bool packed = a.cu != nullptr;
-    const int L = chunk_rows(dt);
-    const GatedWs w = gated_ws(a.B, a.T, a.H, a.N, a.P, a.nseq, packed, L, bwd || a.saved == nullptr);
+    const GatedWs w = gated_ws(a.B, a.T, a.H, a.N, a.P, a.nseq, packed, kL, bwd || a.saved == nullptr);
     char *ws = static_cast<char *>(a.ws);
     p.a = a;
     p.c.q = make_seqs(a.cu, a.B, a.T, a.nseq);
     p.c.first = reinterpret_cast<const int *>(ws + w.first);
-    p.c.per = int(ceil_div(a.T, L)), p.c.L = L, p.c.most = w.chunks;
+    p.c.per = int(ceil_div(a.T, kL)), p.c.L = kL, p.c.most = w.chunks;
     p.totals = reinterpret_cast<float *>(ws + w.totals);
     float *states = reinterpret_cast<float *>(ws + w.states);
     p.states = bwd ? const_cast<float *>(a.saved_in) : a.saved != nullptr ? a.saved : states;
@@ -600,10 +599,10 @@ mg_status make_call(const GatedArgs &a, mg_dtype dt, bool bwd, GatedCall &p)
 
 }  // namespace
 
-mg_status launch_chunk_table(const Chunks &c, int *first, void *ws, cudaStream_t s)
+mg_status launch_chunk_tables(const Chunks &c, const Chunks &d, void *ws, cudaStream_t s)
 {
-    chunk_table_kernel<<<1, 1024, 0, s>>>(c, first, ws);
-    return launched("chunk table");
+    chunk_table_kernel<<<c.first == d.first ? 1 : 2, 1024, 0, s>>>(c, d, ws);
+    return launched("chunk tables");
 }
 
 mg_status launch_over_chunks(const Chunks &c, float *states, const float *totals, const float *from, float *to, int H,
@@ -620,31 +619,35 @@ mg_status launch_over_chunks(const Chunks &c, float *states, const float *totals
 
 size_t gated_saved_bytes(int64_t B, int64_t T, int64_t H, int64_t N, int64_t P, int64_t nseq, bool packed, mg_dtype dt)
 {
-    return size_t(chunks_most(B, T, nseq, packed, chunk_rows(dt))) * H * N * P * 4;
+    if (dt == MG_BF16) return gated_tc_saved_bytes(B, T, int(H), int(N), int(P), nseq, packed);
+    return size_t(chunks_most(B, T, nseq, packed, kL)) * H * N * P * 4;
 }
 
 size_t gated_ws_bytes(int64_t B, int64_t T, int64_t H, int64_t G, int64_t N, int64_t P, int64_t nseq, bool packed,
                       mg_dtype dt, bool bwd)
 {
-    const GatedWs w = gated_ws(B, T, H, N, P, nseq, packed, chunk_rows(dt), true);
+    if (dt == MG_BF16) return gated_tc_ws_bytes(B, T, int(H), int(G), int(N), int(P), nseq, packed, bwd);
+    const GatedWs w = gated_ws(B, T, H, N, P, nseq, packed, kL, true);
     const int splits = bwd ? splits_for(w.chunks, int(H), int(G)) : 1;
     return w.more + (splits > 1 ? size_t(splits) * 2 * B * T * G * N * 4 : 0);
 }
 
 mg_status launch_gated_fwd(const GatedArgs &a, mg_dtype dt, cudaStream_t s)
 {
+    if (dt == MG_BF16) return launch_gated_tc_fwd(a, s);
     GatedCall p{};
-    MG_TRY(make_call(a, dt, false, p));
-    if (a.cu != nullptr) MG_TRY(launch_chunk_table(p.c, const_cast<int *>(p.c.first), a.ws, s));
-    return dt == MG_F32 ? fwd_typed<float>(p, s) : fwd_typed<bf16_t>(p, s);
+    MG_TRY(make_call(a, false, p));
+    if (a.cu != nullptr) MG_TRY(launch_chunk_tables(p.c, p.c, a.ws, s));
+    return fwd_any(p, s);
 }
 
 mg_status launch_gated_bwd(const GatedArgs &a, mg_dtype dt, cudaStream_t s)
 {
+    if (dt == MG_BF16) return launch_gated_tc_bwd(a, s);
     GatedCall p{};
-    MG_TRY(make_call(a, dt, true, p));
-    if (a.cu != nullptr) MG_TRY(launch_chunk_table(p.c, const_cast<int *>(p.c.first), a.ws, s));
-    return dt == MG_F32 ? bwd_typed<float>(p, s) : bwd_typed<bf16_t>(p, s);
+    MG_TRY(make_call(a, true, p));
+    if (a.cu != nullptr) MG_TRY(launch_chunk_tables(p.c, p.c, a.ws, s));
+    return bwd_any(p, s);
 }
 
 mg_status launch_gated_step(const GatedStepArgs &p, mg_dtype dt, cudaStream_t s)

@@ -13,7 +13,8 @@ __device__ __forceinline__ float gate_of(float g) { return g < kLeastGate ? kLea
 
 // A batch's chunks of up to L rows, none of them across two sequences.  Dense:
 // `per` in each sequence.  Packed: sequence s has the chunks first[s] ..
-// first[s+1]-1, a table that chunk_table() leaves in the workspace.
+// first[s+1]-1, a table that launch_chunk_tables leaves in the workspace; of a
+// cu that breaks the rules there are none.
 struct Chunks {
     Seqs q;
     const int *first;
@@ -22,15 +23,16 @@ struct Chunks {
 
     struct One {
         long long row;
-        int len, seq;
+        int len, seq, idx;   // rows, sequence, place in it
     };
     // Chunk c; len 0: there is none.
     __device__ __forceinline__ One get(long long c) const
     {
-        One o{0, 0, 0};
+        One o{0, 0, 0, 0};
         if (q.cu == nullptr) {
             o.seq = int(c / per);
-            const long long at = (c - (long long)o.seq * per) * L;
+            o.idx = int(c - (long long)o.seq * per);
+            const long long at = (long long)o.idx * L;
             o.row = (long long)o.seq * q.T + at;
             o.len = int(q.T - at < L ? q.T - at : L);
             return o;
@@ -41,19 +43,12 @@ struct Chunks {
             const int mid = (lo + hi) >> 1;
             if (__ldg(first + mid) <= c) lo = mid; else hi = mid;
         }
-        long long a, b;
-        bounds(lo, a, b);
         o.seq = lo;
-        o.row = a + (c - __ldg(first + lo)) * L;
-        o.len = int(b - o.row < L ? b - o.row : L);
+        o.idx = int(c - __ldg(first + lo));
+        o.row = __ldg(q.cu + lo) + (long long)o.idx * L;
+        const long long left = __ldg(q.cu + lo + 1) - o.row;
+        o.len = int(left < L ? left : L);
         return o;
-    }
-    // Rows a .. b-1 of sequence s, inside the batch whatever cu holds.
-    __device__ __forceinline__ void bounds(int s, long long &a, long long &b) const
-    {
-        a = __ldg(q.cu + s), b = __ldg(q.cu + s + 1);
-        a = a < 0 ? 0 : a > q.rows ? q.rows : a;
-        b = b < a ? a : b > q.rows ? q.rows : b;
     }
     __device__ __forceinline__ long long begin(int s) const { return q.cu == nullptr ? (long long)s * per : __ldg(first + s); }
     __device__ __forceinline__ long long end(int s) const { return begin(s + 1); }
@@ -82,8 +77,8 @@ inline GatedWs gated_ws(int64_t B, int64_t T, int64_t H, int64_t N, int64_t P, i
     return w;
 }
 
-// Packed batches: checks cu and fills the chunk table.
-mg_status launch_chunk_table(const Chunks &c, int *first, void *ws, cudaStream_t s);
+// Packed batches: checks cu and fills the tables of two cuts of the batch.
+mg_status launch_chunk_tables(const Chunks &c, const Chunks &d, void *ws, cudaStream_t s);
 
 // Over the chunks of every sequence and head, in place: states[c] holds what
 // chunk c adds, and is left with what comes to it: the state before it
@@ -93,7 +88,13 @@ mg_status launch_chunk_table(const Chunks &c, int *first, void *ws, cudaStream_t
 mg_status launch_over_chunks(const Chunks &c, float *states, const float *totals, const float *from, float *to, int H,
                              int64_t NP, bool backward, cudaStream_t s);
 
-// The kernels' arguments.
+// bf16: tensor-core kernels (gated_tc.cu).
+size_t gated_tc_saved_bytes(int64_t B, int64_t T, int H, int N, int P, int64_t nseq, bool packed);
+size_t gated_tc_ws_bytes(int64_t B, int64_t T, int H, int G, int N, int P, int64_t nseq, bool packed, bool bwd);
+mg_status launch_gated_tc_fwd(const GatedArgs &a, cudaStream_t s);
+mg_status launch_gated_tc_bwd(const GatedArgs &a, cudaStream_t s);
+
+// The float32 kernels' arguments.
 struct GatedCall {
     GatedArgs a;
     Chunks c;

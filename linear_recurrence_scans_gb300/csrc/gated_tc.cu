@@ -1,0 +1,991 @@
+// Gated recurrence in bf16: chunks of 128 rows as tensor-core products (the
+// formulas are in gated_scan.cu).
+//
+// A call is three kernels.  A walk goes over the chunks of a segment (a few
+// chunks of a sequence and head) and leaves, for each chunk, the state that
+// the segment's earlier chunks give it; a pass over the segments adds up what
+// comes to each of them; then all chunks' rows are computed at once, each with
+// the state that it begins with: the walk's plus the decayed one of its segment.
+// Backwards the same with the adjoints, from the last chunk on.
+//
+// Rounding.  q, k, v and dout are bf16 as they are given, so their products are
+// exact in the tensor core's float32 sums.  A chunk's weights and the state are
+// rounded to bf16 where they meet an operand of the rows' outputs, which are
+// bf16 themselves (each term of an output has one of the two).  Where the result
+// is float32 (states, their adjoints, the gates' gradients) such a factor goes
+// in as the sum of three bf16 pieces, to 2^-24.  The smallest pieces are summed
+// first: the tensor core's sums lose up to a last bit of the sum at each step,
+// and the large piece first made dg's errors 1.2e-6 where they are 3e-7.
+#include "gated_scan.cuh"
+#include "umma.cuh"
+
+namespace mg {
+namespace {
+
+constexpr int kRows = 128;   // of a chunk: the rows of a tensor-core product
+
+// A chunk's gate sums as two floats.
+struct Gates128 {
+    float hi[kRows], lo[kRows];
+    __device__ __forceinline__ float span(float hi_i, float lo_i, int j) const { return exp_of((hi_i - hi[j]) + (lo_i - lo[j])); }
+    // e^x in two instructions.  The rounding of x log2 e costs a relative |x|
+    // 2^-24 of a weight that is e^x itself.
+    static __device__ __forceinline__ float exp_of(float x) { return ex2_ftz(x * kLog2eF); }
+};
+
+// x + y as two floats, exact but for the last bits of the lower ones.
+__device__ __forceinline__ void add_two(float &xh, float &xl, float yh, float yl)
+{
+    const float s = xh + yh, b = s - xh;
+    const float e = (xh - (s - b)) + (yh - b) + (xl + yl);
+    xh = s + e;
+    xl = e - (xh - s);
+}
+
+// One warp: a lane has the gates of rows 4 lane .. 4 lane + 3.
+__device__ __forceinline__ void sum_gates(const float (&g)[4], Gates128 &to)
+{
+    const int lane = threadIdx.x & 31;
+    float h[4], l[4];
+    h[0] = g[0], l[0] = 0.f;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) {
+        h[i] = h[i - 1], l[i] = l[i - 1];
+        add_two(h[i], l[i], g[i], 0.f);
+    }
+    float th = h[3], tl = l[3];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float uh = __shfl_up_sync(~0u, th, o), ul = __shfl_up_sync(~0u, tl, o);
+        if (lane >= o) add_two(th, tl, uh, ul);
+    }
+    const float bh = __shfl_up_sync(~0u, th, 1), bl = __shfl_up_sync(~0u, tl, 1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (lane > 0) add_two(h[i], l[i], bh, bl);
+        to.hi[4 * lane + i] = h[i], to.lo[4 * lane + i] = l[i];
+    }
+}
+__device__ __forceinline__ void fetch_gates(float (&g)[4], const float *from, int64_t ld, int len)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * (threadIdx.x & 31) + i;
+        g[i] = r < len ? gate_of(__ldg(from + r * ld)) : 0.f;
+    }
+}
+
+// The 8 values of a row from column 8 piece on, zeros beyond `cols`; where rows
+// are not aligned, value by value.
+template <bool VEC>
+__device__ __forceinline__ uint4 fetch_piece(const bf16_t *row, int piece, int cols, bool on)
+{
+    uint4 v = make_uint4(0, 0, 0, 0);
+    const int c = piece * 8;
+    if (!on || c >= cols) return v;
+    if constexpr (VEC) {
+        v = __ldg(reinterpret_cast<const uint4 *>(row + c));
+    } else {
+        unsigned w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = c + e < cols ? __ldg(&row[c + e].bits) : 0;
+        v = make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
+    }
+    return v;
+}
+
+// `len` rows of `cols` values into a tile of 128 rows, zeros beside and below.
+template <int PANELS, int THREADS, bool VEC>
+__device__ __forceinline__ void load_rows(unsigned tile, const bf16_t *from, int64_t ld, int len, int cols)
+{
+    constexpr int kPieces = PANELS * 8;
+#pragma unroll
+    for (int u = 0; u < kRows * kPieces / THREADS; ++u) {
+        const int id = threadIdx.x + THREADS * u, row = id / kPieces, piece = id % kPieces;
+        const unsigned at = tile_at(kRows, row, piece);
+        if constexpr (VEC) {
+            const bool on = row < len && piece * 8 < cols;
+            copy16(tile + at, on ? from + row * ld + piece * 8 : from, on);
+        } else {
+            st_tile(tile, at, fetch_piece<false>(from + row * ld, piece, cols, row < len));
+        }
+    }
+}
+
+// A tile's rows to global memory, `cols` of each.
+template <int PANELS, int THREADS, bool VEC>
+__device__ __forceinline__ void store_rows(bf16_t *to, int64_t ld, unsigned tile, int len, int cols)
+{
+    constexpr int kPieces = PANELS * 8;
+#pragma unroll
+    for (int u = 0; u < kRows * kPieces / THREADS; ++u) {
+        const int id = threadIdx.x + THREADS * u, row = id / kPieces, piece = id % kPieces;
+        if (row >= len || piece * 8 >= cols) continue;
+        const uint4 v = ld_tile(tile, tile_at(kRows, row, piece));
+        bf16_t *o = to + row * ld + piece * 8;
+        if constexpr (VEC) {
+            __stcs(reinterpret_cast<uint4 *>(o), v);
+        } else {
+            const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (piece * 8 + e < cols) o[e].bits = (unsigned short)(e & 1 ? w[e >> 1] >> 16 : w[e >> 1] & 0xffffu);
+        }
+    }
+}
+
+// 32 values of one row, rounded, into a tile from column 32 block on.
+__device__ __forceinline__ void put32(unsigned tile, int row, int block, const float (&v)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        st_tile(tile, tile_at(kRows, row, 4 * block + i),
+                make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                           pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7])));
+}
+
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8])
+{
+    const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[2 * i] = __uint_as_float(w[i] << 16), f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+}
+
+// States between the kernels lie as [P / 4][N][4] (zeros beyond P): a lane a
+// row of the accumulators, neighbouring lanes 16 bytes apart.
+__host__ __device__ constexpr int64_t state_size(int N, int P) { return int64_t((P + 3) / 4) * N * 4; }
+
+// A walk's results, for the states or for their adjoints.
+struct Walked {
+    float *local;    // [chunks][H][state]: of the segment's other chunks before (behind) the chunk
+    float *carry;    // [segments][H][state]: before (behind) the segment
+    float *reach;    // [chunks][H]: sum of the gates between the chunk and that end of its segment
+    float *totals;   // [segments][H]: of the segment's gates
+};
+
+struct TcCall {
+    GatedArgs a;
+    Chunks c, seg;   // chunks, and segments of m of them
+    int m;
+    Walked s, d;
+    float *partial;
+    int splits, heads;
+    bool starts;     // the first segments' carries may hold start states
+    unsigned *error;
+};
+
+// Where a chunk's state comes from.
+struct Source {
+    const float *local, *carry;   // NULL: nothing from there
+    float by;
+};
+template <bool BACK>
+__device__ __forceinline__ Source source_of(const TcCall &p, const Chunks::One &ch, int64_t c, int h)
+{
+    const Walked &w = BACK ? p.d : p.s;
+    const int64_t size = state_size(p.a.N, p.a.P);
+    const int count = int(p.c.end(ch.seq) - p.c.begin(ch.seq)), last = (count - 1) / p.m, seg = ch.idx / p.m;
+    const bool first = BACK ? ch.idx == count - 1 || ch.idx % p.m == p.m - 1 : ch.idx % p.m == 0;
+    const bool from_outside = BACK ? p.a.dS_last != nullptr : p.starts;
+    Source s;
+    s.local = first ? nullptr : w.local + (c * p.a.H + h) * size;
+    s.carry = !from_outside && seg == (BACK ? last : 0) ? nullptr : w.carry + ((p.seg.begin(ch.seq) + seg) * p.a.H + h) * size;
+    s.by = expf(w.reach[c * p.a.H + h]);
+    return s;
+}
+
+// 8 values of a state's row n from column 8 piece on.
+__device__ __forceinline__ void fetch_state(const Source &s, int n, int piece, int N, int P, float (&v)[8])
+{
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int quad = 2 * piece + q;
+        if (n < N && quad * 4 < P) {
+            const int64_t at = (int64_t(quad) * N + n) * 4;
+            if (s.local != nullptr) x = __ldg(reinterpret_cast<const float4 *>(s.local + at));
+            if (s.carry != nullptr) {
+                const float4 y = __ldg(reinterpret_cast<const float4 *>(s.carry + at));
+                x.x = fmaf(s.by, y.x, x.x), x.y = fmaf(s.by, y.y, x.y), x.z = fmaf(s.by, y.z, x.z), x.w = fmaf(s.by, y.w, x.w);
+            }
+        }
+        v[4 * q] = x.x, v[4 * q + 1] = x.y, v[4 * q + 2] = x.z, v[4 * q + 3] = x.w;
+    }
+}
+
+__device__ __forceinline__ void wait_or_tell(uint64_t *bar, unsigned phase, unsigned *error)
+{
+    if (!bar_wait(bar, phase)) atomicOr(error, kErrLookbackTimeout);
+}
+
+// ------------------------------------------------------------------- walk
+// A block: a segment, a head, 64 columns of its state, which stay in registers
+// (row n a lane, 32 columns a thread).  Each chunk adds K^T V~, the row weights
+// in V~'s three pieces; the next chunk's rows arrive meanwhile.
+
+constexpr int kWalkThreads = 256;
+
+template <int PN, bool VEC, bool BACK>
+__global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const TcCall p, int tiles)
+{
+    extern __shared__ __align__(1024) char sm[];
+    constexpr unsigned kK = PN * kRows * 128, kV = kRows * 128;
+    const GatedArgs &a = p.a;
+    const unsigned base = smem_addr(sm), tv = base + 2 * kK;
+    struct Small {
+        Gates128 g[2];
+        uint64_t bar;
+        unsigned tmem;
+    };
+    Small &sh = *reinterpret_cast<Small *>(sm + 2 * kK + 3 * kV);
+
+    const int tile = int(blockIdx.x % tiles), h = int(blockIdx.x / tiles % a.H), grp = h / (a.H / a.G);
+    const int64_t sg = int64_t(blockIdx.x) / tiles / a.H;
+    const Chunks::One s = p.seg.get(sg);
+    if (s.len == 0) return;
+    const Walked &w = BACK ? p.d : p.s;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int p0 = tile * 64, cols = a.P - p0 < 64 ? a.P - p0 : 64;
+    const int count = (s.len + kRows - 1) / kRows;
+    const int64_t c0 = p.c.begin(s.seq) + int64_t(s.idx) * p.m, size = state_size(a.N, a.P);
+    const bf16_t *kk = static_cast<const bf16_t *>(BACK ? a.q : a.k) + grp * a.N;
+    const bf16_t *vv = static_cast<const bf16_t *>(BACK ? a.dout : a.v) + h * a.P + p0;
+    const int64_t ldk = BACK ? a.ldq : a.ldk, ldv = BACK ? a.lddo : a.ldv;
+
+    if (warp == 0) tmem_take(&sh.tmem, 64);
+    if (tid == 0) bar_init(&sh.bar);
+    float g[4];
+    uint4 v[4];
+    const auto chunk_at = [&](int i) { return BACK ? count - 1 - i : i; };
+    const auto fetch = [&](int i) {   // chunk i of the walk: K into its buffer, V and gates into registers
+        const int ci = chunk_at(i), len = s.len - ci * kRows < kRows ? s.len - ci * kRows : kRows;
+        const int64_t row = s.row + int64_t(ci) * kRows;
+        load_rows<PN, kWalkThreads, VEC>(base + (i & 1) * kK, kk + row * ldk, ldk, len, a.N);
+        cp_async_commit();
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int r = (tid >> 3) + 32 * u;
+            v[u] = fetch_piece<VEC>(vv + (row + r) * ldv, tid & 7, cols, r < len);
+        }
+        if (warp == 0) fetch_gates(g, a.g + row * a.ldg + h, a.ldg, len);
+    };
+    fetch(0);
+    float S[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) S[i] = 0.f;
+    const int n = 32 * (warp & 3) + lane, quad0 = p0 / 4 + 8 * (warp >> 2);
+    const auto put = [&](float *to) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (n < a.N && (quad0 + q) * 4 < a.P)
+                *reinterpret_cast<float4 *>(to + (int64_t(quad0 + q) * a.N + n) * 4) = make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
+    };
+    float reach = 0.f;
+    for (int i = 0; i < count; ++i) {
+        Gates128 &gates = sh.g[i & 1];
+        if (warp == 0) sum_gates(g, gates);
+        cp_async_wait<0>();
+        __syncthreads();
+        const int64_t ch = (c0 + chunk_at(i)) * a.H + h;
+        if (tid == 0 && tile == 0) w.reach[ch] = reach;
+        if (i > 0) put(w.local + ch * size);
+        const float whole = gates.hi[kRows - 1], whole_lo = gates.lo[kRows - 1];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int r = (tid >> 3) + 32 * u;
+            const float by = BACK ? a.scale * Gates128::exp_of(gates.hi[r] + gates.lo[r]) : gates.span(whole, whole_lo, r);
+            float f[8];
+            unpack8(v[u], f);
+            unsigned x[3][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Pieces q = split3(f[2 * e] * by, f[2 * e + 1] * by);
+                x[0][e] = q.a, x[1][e] = q.b, x[2][e] = q.c;
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                st_tile(tv + k * kV, tile_at(kRows, r, tid & 7), make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]));
+        }
+        fence_tiles();
+        tmem_before_sync();
+        __syncthreads();
+        const unsigned acc = sh.tmem;
+        if (tid == 0) {
+            tmem_after_sync();
+            for (int k = 2; k >= 0; --k)
+                multiply(acc, Operand{base + (i & 1) * kK, kRows, true}, Operand{tv + k * kV, kRows, true}, 64, kRows / 16, k < 2);
+            bar_after_products(&sh.bar);
+        }
+        if (i + 1 < count) fetch(i + 1);
+        reach += whole + whole_lo;
+        const float decay = expf(whole) * (1.f + whole_lo);
+        wait_or_tell(&sh.bar, i & 1, p.error);
+        tmem_after_sync();
+        float add[32];
+        tmem_load(acc + (unsigned(32 * (warp & 3)) << 16) + 32 * (warp >> 2), add);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) S[e] = fmaf(decay, S[e], add[e]);
+    }
+    put(w.carry + (sg * a.H + h) * size);
+    if (tid == 0 && tile == 0) w.totals[sg * a.H + h] = reach;
+    tmem_before_sync();
+    __syncthreads();
+    if (warp == 0) tmem_free(sh.tmem, 64);
+}
+
+// ----------------------------------------------------- pass over segments
+// In place: carry holds what each segment leaves, and is left with what comes
+// to it, from `from` (N x P each; NULL: zero) and on to `to` (may be NULL).  A
+// thread a quad of a state's row.
+
+template <bool BACK>
+__global__ void __launch_bounds__(256) over_segments_kernel(const Chunks seg, const Walked w, const float *from, float *to,
+                                                            int H, int N, int P, int blocks_per)
+{
+    constexpr int kAhead = 8;
+    const int64_t sh = blockIdx.x / blocks_per;   // sequence and head
+    const int seq = int(sh / H), h = int(sh % H);
+    const int at = int(blockIdx.x % blocks_per) * 256 + threadIdx.x, quads = (P + 3) / 4;
+    if (at >= quads * N) return;
+    const int n = at % N, p0 = at / N * 4, cols = P - p0 < 4 ? P - p0 : 4;
+    const int64_t size = state_size(N, P), out = (sh * N + n) * P + p0;
+    const int64_t lo = seg.begin(seq), hi = seg.end(seq);
+    float s[4];
+    // + 0: a caller's signalling NaN must not get into the workspace as it is
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = from != nullptr && e < cols ? __ldg(from + out + e) + 0.f : 0.f;
+    for (int64_t i0 = 0; i0 < hi - lo; i0 += kAhead) {
+        float add[kAhead][4], gate[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (i0 + u >= hi - lo) continue;
+            const int64_t g = (BACK ? hi - 1 - i0 - u : lo + i0 + u) * H + h;
+            load_vec<4>(w.carry + g * size + int64_t(at) * 4, add[u]);
+            gate[u] = w.totals[g];
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (i0 + u >= hi - lo) continue;
+            const int64_t g = (BACK ? hi - 1 - i0 - u : lo + i0 + u) * H + h;
+            store_vec<4>(w.carry + g * size + int64_t(at) * 4, s);
+            const float d = expf(gate[u]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] = fmaf(d, s[e], add[u][e]);
+        }
+    }
+    if (to == nullptr) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < cols) to[out + e] = s[e];
+}
+
+// ------------------------------------------------------------------- rows
+// A block: o of a chunk and head.  Q K^T, weights, times V, and Q S beside it;
+// the weights take Q's place in shared memory and V takes K's, so that two blocks
+// fit an SM and one's products run under the other's loads and exponentials.
+
+constexpr int kRowThreads = 256;
+
+template <int PN, int PP, bool VEC>
+__global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const TcCall p)
+{
+    extern __shared__ __align__(1024) char sm[];
+    constexpr int NB = 64 * PN, PB = 64 * PP;
+    constexpr unsigned kQ = 2 * kRows * 128, kK = (PN > PP ? PN : PP) * kRows * 128, kS = PP * NB * 128;
+    const GatedArgs &a = p.a;
+    const unsigned tq = smem_addr(sm), tk = tq + kQ, ts = tk + kK;
+    struct Small {
+        Gates128 g;
+        uint64_t bar[2];
+        unsigned tmem;
+    };
+    Small &sh = *reinterpret_cast<Small *>(sm + kQ + kK + kS);
+    const int64_t c = blockIdx.x / a.H;
+    const int h = int(blockIdx.x % a.H), grp = h / (a.H / a.G);
+    const Chunks::One ch = p.c.get(c);
+    if (ch.len == 0) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (warp == 0) tmem_take(&sh.tmem, 256);
+    if (tid == 0) bar_init(&sh.bar[0]), bar_init(&sh.bar[1]);
+    load_rows<PN, kRowThreads, VEC>(tq, static_cast<const bf16_t *>(a.q) + ch.row * a.ldq + grp * a.N, a.ldq, ch.len, a.N);
+    load_rows<PN, kRowThreads, VEC>(tk, static_cast<const bf16_t *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
+    cp_async_commit();
+    uint4 v[4 * PP];
+    const bf16_t *vv = static_cast<const bf16_t *>(a.v) + ch.row * a.ldv + h * a.P;
+#pragma unroll
+    for (int u = 0; u < 4 * PP; ++u) {
+        const int id = tid + kRowThreads * u, r = id / (8 * PP);
+        v[u] = fetch_piece<VEC>(vv + r * a.ldv, id % (8 * PP), a.P, r < ch.len);
+    }
+    if (warp == 0) {
+        float g[4];
+        fetch_gates(g, a.g + ch.row * a.ldg + h, a.ldg, ch.len);
+        sum_gates(g, sh.g);
+    }
+    {   // the state, rounded: an operand of bf16 outputs
+        const Source s = source_of<false>(p, ch, c, h);
+#pragma unroll
+        for (int u = 0; u < NB * PP * 8 / kRowThreads; ++u) {
+            const int id = tid + kRowThreads * u, n = id % NB, piece = id / NB;
+            float f[8];
+            fetch_state(s, n, piece, a.N, a.P, f);
+            st_tile(ts, tile_at(NB, n, piece), make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
+        }
+    }
+    cp_async_wait<0>();
+    fence_tiles();
+    tmem_before_sync();
+    __syncthreads();
+    tmem_after_sync();
+    const unsigned acc = sh.tmem, acc_s = acc + 128, mine = unsigned(32 * (warp & 3)) << 16;
+    if (tid == 0) {
+        const int steps = (a.N + 15) / 16;
+        multiply(acc, Operand{tq, kRows, false}, Operand{tk, kRows, false}, kRows, steps, false);
+        bar_after_products(&sh.bar[0]);
+        multiply(acc_s, Operand{tq, kRows, false}, Operand{ts, NB, true}, PB, steps, false);
+        bar_after_products(&sh.bar[1]);
+    }
+    const int row = 32 * (warp & 3) + lane;
+    const float hi = sh.g.hi[row], lo = sh.g.lo[row];
+    wait_or_tell(&sh.bar[0], 0, p.error);
+    wait_or_tell(&sh.bar[1], 0, p.error);   // Q is read: the weights may take its place
+    tmem_after_sync();
+    // blocks of 32 columns, every second one to a warp; those above the diagonal are zeros
+#pragma unroll
+    for (int b = warp >> 2; b < 4; b += 2) {
+        float w[32];
+        if (b <= (warp & 3)) {
+            tmem_load(acc + mine + 32 * b, w);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+                const int j = 32 * b + e;
+                w[e] = j <= row ? w[e] * sh.g.span(hi, lo, j) : 0.f;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = 0.f;
+        }
+        put32(tq, row, b, w);
+    }
+#pragma unroll
+    for (int u = 0; u < 4 * PP; ++u) {
+        const int id = tid + kRowThreads * u;
+        st_tile(tk, tile_at(kRows, id / (8 * PP), id % (8 * PP)), v[u]);
+    }
+    fence_tiles();
+    tmem_before_sync();
+    __syncthreads();
+    if (tid == 0) {
+        tmem_after_sync();
+        multiply(acc, Operand{tq, kRows, false}, Operand{tk, kRows, true}, PB, (ch.len + 15) / 16, false);
+        bar_after_products(&sh.bar[0]);
+    }
+    const float up = Gates128::exp_of(hi + lo);
+    wait_or_tell(&sh.bar[0], 1, p.error);
+    tmem_after_sync();
+#pragma unroll
+    for (int b = warp >> 2; b < PB / 32; b += 2) {
+        float x[32], y[32];
+        tmem_load(acc + mine + 32 * b, x);
+        tmem_load(acc_s + mine + 32 * b, y);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) x[e] = a.scale * fmaf(up, y[e], x[e]);
+        put32(tk, row, b, x);
+    }
+    tmem_before_sync();
+    __syncthreads();
+    store_rows<PP, kRowThreads, VEC>(static_cast<bf16_t *>(a.o) + (ch.row * a.H + h) * a.P, int64_t(a.H) * a.P, tk, ch.len, a.P);
+    if (warp == 0) tmem_free(acc, 256);
+}
+
+// -------------------------------------------------------------- gradients
+// A block: a chunk, a group's heads (or a part of them), one after another: dv
+// and dg of each, dq and dk summed over them in tensor memory.
+
+constexpr int kGradThreads = 512;
+
+template <int PN, int PP>
+struct GradSmem {
+    static constexpr int NB = 64 * PN, PB = 64 * PP;
+    static constexpr unsigned kQ = PN * kRows * 128, kV = PP * kRows * 128, kState = PP * NB * 128, kW = 2 * kRows * 128;
+    static constexpr unsigned kX = 3 * kState > 2 * kW + 4096 ? 3 * kState : 2 * kW + 4096;
+    struct Small {
+        Gates128 g;
+        float after[kRows], key[kRows], dots[16];
+        uint64_t bar;
+        unsigned tmem;
+    };
+    static constexpr size_t bytes = 2 * kQ + 2 * kV + kX + sizeof(Small);
+};
+
+// Sums over a warp's 32 rows: lane l gets column l's.
+__device__ __forceinline__ float column_sums(float (&w)[32])
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int k = 0; k < o; ++k) {
+            const bool up = lane & o;
+            const float send = up ? w[k] : w[k + o], keep = up ? w[k + o] : w[k];
+            w[k] = keep + __shfl_xor_sync(~0u, send, o);
+        }
+    return w[0];
+}
+
+template <int PN, int PP, bool VEC>
+__global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const TcCall p)
+{
+    extern __shared__ __align__(1024) char sm[];
+    using M = GradSmem<PN, PP>;
+    constexpr int NB = M::NB, PB = M::PB;
+    const GatedArgs &a = p.a;
+    const unsigned tq = smem_addr(sm), tk = tq + M::kQ, tv = tk + M::kQ, to = tv + M::kV, tx = to + M::kV, tw = tx, tdw = tx + M::kW;
+    char *x_area = sm + 2 * M::kQ + 2 * M::kV;
+    float *row_part = reinterpret_cast<float *>(x_area + 2 * M::kW), *col_part = row_part + 4 * kRows;
+    auto &sh = *reinterpret_cast<typename M::Small *>(x_area + M::kX);
+
+    const int split = int(blockIdx.x % p.splits), grp = int(blockIdx.x / p.splits % a.G);
+    const int64_t c = int64_t(blockIdx.x) / p.splits / a.G;
+    const Chunks::One ch = p.c.get(c);
+    if (ch.len == 0) return;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rb = warp & 3, cb = warp >> 2, row = 32 * rb + lane;
+    if (warp == 0) tmem_take(&sh.tmem, 512);
+    if (tid == 0) bar_init(&sh.bar);
+    load_rows<PN, kGradThreads, VEC>(tq, static_cast<const bf16_t *>(a.q) + ch.row * a.ldq + grp * a.N, a.ldq, ch.len, a.N);
+    load_rows<PN, kGradThreads, VEC>(tk, static_cast<const bf16_t *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
+    const int per_group = a.H / a.G, h0 = split * p.heads, h1 = h0 + p.heads < per_group ? h0 + p.heads : per_group;
+    const int nsteps = (a.N + 15) / 16, psteps = (a.P + 15) / 16;
+    const unsigned mine = unsigned(32 * rb) << 16;
+    unsigned phase = 0, acc = 0;
+    const auto products_done = [&]() {
+        wait_or_tell(&sh.bar, phase, p.error);
+        phase ^= 1;
+        tmem_after_sync();
+    };
+    // writes of tiles and reads of accumulators before the next products
+    const auto before_products = [&]() {
+        fence_tiles();
+        tmem_before_sync();
+        __syncthreads();
+        tmem_after_sync();
+    };
+    // adds the column blocks' sums v for each row to to[row], block after block
+    const auto add_blocks = [&](float *to, float v, int blocks, bool fresh) {
+        for (int b = 0; b < blocks; ++b) {
+            if (cb == b) to[row] = (b == 0 && fresh ? 0.f : to[row]) + v;
+            __syncthreads();
+        }
+    };
+    for (int hh = h0; hh < h1; ++hh) {
+        const int h = grp * per_group + hh;
+        __syncthreads();   // the head before is done with its tiles
+        load_rows<PP, kGradThreads, VEC>(tv, static_cast<const bf16_t *>(a.v) + ch.row * a.ldv + h * a.P, a.ldv, ch.len, a.P);
+        load_rows<PP, kGradThreads, VEC>(to, static_cast<const bf16_t *>(a.dout) + ch.row * a.lddo + h * a.P, a.lddo, ch.len, a.P);
+        cp_async_commit();
+        if (warp == 0) {
+            float g[4];
+            fetch_gates(g, a.g + ch.row * a.ldg + h, a.ldg, ch.len);
+            sum_gates(g, sh.g);
+        }
+        const Source from_d = source_of<true>(p, ch, c, h), from_s = source_of<false>(p, ch, c, h);
+        cp_async_wait<0>();
+        before_products();
+        acc = sh.tmem;
+        const unsigned acc0 = acc, acc1 = acc + 128, acc_q = acc + 256, acc_k = acc + 384;
+        if (tid == 0) {
+            multiply(acc0, Operand{tq, kRows, false}, Operand{tk, kRows, false}, kRows, nsteps, false);
+            multiply(acc1, Operand{to, kRows, false}, Operand{tv, kRows, false}, kRows, psteps, false);
+            bar_after_products(&sh.bar);
+        }
+        const float hi = sh.g.hi[row], lo = sh.g.lo[row];
+        const float tail = sh.g.span(sh.g.hi[kRows - 1], sh.g.lo[kRows - 1], row), up = Gates128::exp_of(hi + lo);
+        products_done();
+        {   // weights, and what each pair of rows gives to the gates between them
+            float s[32], d[32];
+            float of_row = 0.f, of_col = 0.f;
+            if (cb <= rb) {
+                tmem_load(acc0 + mine + 32 * cb, s);
+                tmem_load(acc1 + mine + 32 * cb, d);
+                float both[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const int j = 32 * cb + e;
+                    const float by = a.scale * sh.g.span(hi, lo, j);
+                    d[e] = j <= row ? d[e] * by : 0.f;
+                    both[e] = j < row ? s[e] * d[e] : 0.f;
+                    s[e] = j <= row ? s[e] * by : 0.f;
+                    of_row += both[e];
+                }
+                of_col = column_sums(both);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) s[e] = d[e] = 0.f;
+            }
+            put32(tw, row, cb, s);
+            put32(tdw, row, cb, d);
+            row_part[cb * kRows + row] = of_row;
+            col_part[rb * kRows + 32 * cb + lane] = of_col;
+        }
+        before_products();
+        if (tid == 0) {
+            const bool add = hh > h0;
+            multiply(acc0, Operand{tw, kRows, true}, Operand{to, kRows, true}, PB, kRows / 16, false);
+            multiply(acc_q, Operand{tdw, kRows, false}, Operand{tk, kRows, true}, NB, kRows / 16, add);
+            multiply(acc_k, Operand{tdw, kRows, true}, Operand{tq, kRows, true}, NB, kRows / 16, add);
+            bar_after_products(&sh.bar);
+        }
+        if (tid < kRows) {
+            float x = 0.f;
+            for (int b = 0; b < 4; ++b) x += row_part[b * kRows + tid] - col_part[b * kRows + tid];
+            sh.after[tid] = x;
+        }
+        constexpr int kUnits = NB * PP * 8 / kGradThreads;
+        float st[kUnits][8];
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const int id = tid + kGradThreads * u;
+            fetch_state(from_d, id % NB, id / NB, a.N, a.P, st[u]);
+        }
+        products_done();
+        float dv[32];
+        if (cb < PB / 32) tmem_load(acc0 + mine + 32 * cb, dv);
+        __syncthreads();   // the sums of the weights are read: the adjoint may take their place
+        const auto put_state = [&]() {
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                const int id = tid + kGradThreads * u;
+                unsigned x[3][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const Pieces q = split3(st[u][2 * e], st[u][2 * e + 1]);
+                    x[0][e] = q.a, x[1][e] = q.b, x[2][e] = q.c;
+                }
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+                    st_tile(tx + k * M::kState, tile_at(NB, id % NB, id / NB), make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]));
+            }
+        };
+        put_state();
+        before_products();
+        if (tid == 0) {
+            multiply(acc0, Operand{tk, kRows, false}, Operand{tx, NB, true}, PB, nsteps, false);
+            for (int k = 2; k >= 0; --k)
+                multiply(acc1, Operand{tv, kRows, false}, Operand{tx + k * M::kState, NB, false}, NB, psteps, k < 2);
+            bar_after_products(&sh.bar);
+        }
+        products_done();
+        if (cb < PB / 32) {
+            float x[32];
+            tmem_load(acc0 + mine + 32 * cb, x);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = fmaf(tail, x[e], dv[e]);
+            put32(tv, row, cb, x);   // V is read
+        }
+        // the state before the chunk, and its product with the adjoint behind it
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const int id = tid + kGradThreads * u;
+            fetch_state(from_s, id % NB, id / NB, a.N, a.P, st[u]);
+        }
+        const auto take = [&](unsigned sums, float by, unsigned tile) {   // adds acc1's rows times `by`; their products with the tile's
+            float x[32], t[32], of = 0.f;
+            tmem_load(acc1 + mine + 32 * cb, x);
+            tmem_load(sums + mine + 32 * cb, t);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float f[8];
+                unpack8(ld_tile(tile, tile_at(kRows, row, 4 * cb + i)), f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float y = x[8 * i + e] * by;
+                    of = fmaf(y, f[e], of);
+                    t[8 * i + e] += y;
+                }
+            }
+            tmem_store(sums + mine + 32 * cb, t);
+            return of;
+        };
+        float of = 0.f;
+        if (cb < NB / 32) of = take(acc_k, tail, tk);
+        add_blocks(sh.key, of, NB / 32, true);
+        float dot = 0.f;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const int id = tid + kGradThreads * u;
+            const unsigned at = tile_at(NB, id % NB, id / NB);
+            float d[3][8];
+#pragma unroll
+            for (int k = 0; k < 3; ++k) unpack8(ld_tile(tx + k * M::kState, at), d[k]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dot = fmaf(st[u][e], d[0][e] + (d[1][e] + d[2][e]), dot);
+        }
+        put_state();   // each thread where it has just read
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
+        if (lane == 0) sh.dots[warp] = dot;
+        before_products();
+        if (tid == 0) {
+            for (int k = 2; k >= 0; --k)
+                multiply(acc1, Operand{to, kRows, false}, Operand{tx + k * M::kState, NB, false}, NB, psteps, k < 2);
+            bar_after_products(&sh.bar);
+        }
+        store_rows<PP, kGradThreads, VEC>(static_cast<bf16_t *>(a.dv) + (ch.row * a.H + h) * a.P, int64_t(a.H) * a.P, tv, ch.len, a.P);
+        products_done();
+        of = 0.f;
+        if (cb < NB / 32) of = take(acc_q, a.scale * up, tq);
+        add_blocks(sh.after, of, NB / 32, false);
+        if (warp == 0) {   // dg: four rows a lane
+            float x[4], z[4], after = 0.f, before = 0.f, whole = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = sh.after[4 * lane + i], z[i] = sh.key[4 * lane + i], after += x[i], before += z[i];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float u = __shfl_down_sync(~0u, after, o), v = __shfl_up_sync(~0u, before, o);
+                if (lane + o < 32) after += u;
+                if (lane >= o) before += v;
+            }
+            const float right = __shfl_down_sync(~0u, after, 1), left = __shfl_up_sync(~0u, before, 1);
+            after = lane < 31 ? right : 0.f, before = lane > 0 ? left : 0.f;   // of the lanes behind and before
+            for (int w = 0; w < 16; ++w) whole += sh.dots[w];
+            whole *= Gates128::exp_of(sh.g.hi[kRows - 1] + sh.g.lo[kRows - 1]);
+            float suffix[4];
+#pragma unroll
+            for (int i = 3; i >= 0; --i) suffix[i] = after += x[i];
+            float *dg = a.dg + ch.row * a.H + h;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 4 * lane + i;
+                if (r < ch.len) dg[int64_t(r) * a.H] = suffix[i] + before + whole;
+                before += z[i];
+            }
+        }
+    }
+    // dq and dk
+    __syncthreads();
+    tmem_after_sync();
+    const unsigned acc_q = acc + 256, acc_k = acc + 384;
+    if (cb < NB / 32) {
+        float x[32];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            tmem_load((k == 0 ? acc_q : acc_k) + mine + 32 * cb, x);
+            if (p.splits == 1) {
+                put32(tx + k * M::kW, row, cb, x);
+            } else {
+                const int quads = (a.N + 3) / 4;
+                float *to_part = p.partial + (((int64_t(split) * p.c.most + c) * a.G + grp) * 2 + k) * quads * kRows * 4;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (8 * cb + q < quads)
+                        *reinterpret_cast<float4 *>(to_part + (int64_t(8 * cb + q) * kRows + row) * 4) = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+            }
+        }
+    }
+    tmem_before_sync();
+    __syncthreads();
+    if (p.splits == 1) {
+        store_rows<PN, kGradThreads, VEC>(static_cast<bf16_t *>(a.dq) + (ch.row * a.G + grp) * a.N, int64_t(a.G) * a.N, tx, ch.len, a.N);
+        store_rows<PN, kGradThreads, VEC>(static_cast<bf16_t *>(a.dk) + (ch.row * a.G + grp) * a.N, int64_t(a.G) * a.N, tx + M::kW, ch.len, a.N);
+    }
+    if (warp == 0) tmem_free(acc, 512);
+}
+
+// dq and dk of a chunk and group from the parts of its heads: a thread a row's
+// quad, in the parts' order.
+__global__ void __launch_bounds__(256) gated_join_rows_kernel(const TcCall p)
+{
+    const GatedArgs &a = p.a;
+    const int quads = (a.N + 3) / 4, grp = int(blockIdx.x % a.G);
+    const int64_t c = blockIdx.x / a.G;
+    const Chunks::One ch = p.c.get(c);
+    for (int id = threadIdx.x; id < 2 * quads * kRows; id += 256) {
+        const int k = id / (quads * kRows), quad = id / kRows % quads, row = id % kRows;
+        if (row >= ch.len) continue;
+        float v[4] = {};
+        for (int s = 0; s < p.splits; ++s) {
+            float x[4];
+            load_vec<4>(p.partial + (((int64_t(s) * p.c.most + c) * a.G + grp) * 2 + k) * quads * kRows * 4 + int64_t(id % (quads * kRows)) * 4, x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += x[e];
+        }
+        bf16_t *o = static_cast<bf16_t *>(k == 0 ? a.dq : a.dk) + ((ch.row + row) * a.G + grp) * a.N + quad * 4;
+        if (a.N % 4 == 0) {
+            store_vec<4>(o, v);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (quad * 4 + e < a.N) store1(o + e, v[e]);
+        }
+    }
+}
+
+// ------------------------------------------------------------------- host
+
+// Chunks of a segment: few enough for about two blocks an SM over all segments.
+int segment_chunks(int64_t chunks, int H, int P)
+{
+    const int64_t walks = chunks * H * ceil_div(P, 64), want = 2 * 152;
+    const int64_t m = walks / want;
+    return int(m < 1 ? 1 : m > 64 ? 64 : m);
+}
+
+// Blocks for a group's heads: the gradients' blocks run one on an SM, in rounds
+// of a block's heads and about half a head's time for the group's own tiles.
+int grad_splits(int64_t chunks, int H, int G)
+{
+    const int per = H / G;
+    int best = 1;
+    double least = 1e300;
+    for (int heads = per; heads >= 1; --heads) {
+        const int splits = int(ceil_div(per, heads));
+        const double t = double(ceil_div(chunks * G * splits, 152)) * (heads + 0.5);
+        if (t < least * 0.999) least = t, best = splits;
+    }
+    return best;
+}
+
+struct Plan {
+    int64_t chunks, segments;
+    int m, splits;
+    size_t first, seg_first, local, carry, reach, totals, partial, end;   // of the workspace
+    size_t s_carry, s_reach, saved;                                       // of `saved`, whose local states come first
+};
+Plan plan_of(int64_t B, int64_t T, int H, int G, int N, int P, int64_t nseq, bool packed, bool bwd)
+{
+    Plan w{};
+    const size_t state = size_t(state_size(N, P)) * 4;
+    w.chunks = chunks_most(B, T, nseq, packed, kRows);
+    w.m = segment_chunks(w.chunks, H, P);
+    w.segments = chunks_most(B, T, nseq, packed, kRows * w.m);
+    w.splits = bwd ? grad_splits(w.chunks, H, G) : 1;
+    const size_t table = packed ? align_up(size_t(nseq + 1) * 4, 256) : 0;
+    w.first = kControlBytes, w.seg_first = w.first + table;
+    w.totals = w.seg_first + table;
+    w.local = w.totals + align_up(size_t(w.segments) * H * 4, 256);
+    w.carry = w.local + align_up(size_t(w.chunks) * H * state, 256);
+    w.reach = w.carry + align_up(size_t(w.segments) * H * state, 256);
+    w.partial = w.reach + align_up(size_t(w.chunks) * H * 4, 256);
+    w.end = w.partial + (w.splits > 1 ? size_t(w.splits) * w.chunks * G * 2 * ((N + 3) / 4) * kRows * 16 : 0);
+    w.s_carry = size_t(w.chunks) * H * state;
+    w.s_reach = w.s_carry + size_t(w.segments) * H * state;
+    w.saved = w.s_reach + align_up(size_t(w.chunks) * H * 4, 16);
+    return w;
+}
+
+template <bool BACK>
+mg_status over_segments(const TcCall &p, const float *from, float *to, cudaStream_t s)
+{
+    const GatedArgs &a = p.a;
+    const int per = int(ceil_div(int64_t((a.P + 3) / 4) * a.N, 256));
+    over_segments_kernel<BACK><<<unsigned(a.nseq * a.H * per), 256, 0, s>>>(p.seg, BACK ? p.d : p.s, from, to, a.H, a.N, a.P, per);
+    return launched("pass over segments");
+}
+
+template <int PN, bool VEC, bool BACK>
+mg_status walk(const TcCall &p, cudaStream_t s)
+{
+    constexpr size_t smem = 2 * PN * kRows * 128 + 3 * kRows * 128 + 2 * sizeof(Gates128) + 32;
+    MG_TRY((allow_shared<gated_walk_kernel<PN, VEC, BACK>>(smem)));
+    const int tiles = int(ceil_div(p.a.P, 64));
+    gated_walk_kernel<PN, VEC, BACK><<<unsigned(p.seg.most * p.a.H * tiles), kWalkThreads, smem, s>>>(p, tiles);
+    return launched("mg_gated_scan");
+}
+
+template <int PN, int PP, bool VEC>
+mg_status forward(const TcCall &p, cudaStream_t s)
+{
+    MG_TRY((walk<PN, VEC, false>(p, s)));
+    MG_TRY(over_segments<false>(p, p.a.S0, p.a.S_last, s));
+    constexpr size_t smem = 2 * kRows * 128 + (PN > PP ? PN : PP) * kRows * 128 + PP * PN * 64 * 128 + sizeof(Gates128) + 32;
+    MG_TRY((allow_shared<gated_rows_kernel<PN, PP, VEC>>(smem)));
+    gated_rows_kernel<PN, PP, VEC><<<unsigned(p.c.most * p.a.H), kRowThreads, smem, s>>>(p);
+    return launched("mg_gated_scan_fwd");
+}
+
+template <int PN, int PP, bool VEC>
+mg_status backward(const TcCall &p, cudaStream_t s)
+{
+    MG_TRY((walk<PN, VEC, true>(p, s)));
+    MG_TRY(over_segments<true>(p, p.a.dS_last, p.a.dS0, s));
+    constexpr size_t smem = GradSmem<PN, PP>::bytes;
+    MG_TRY((allow_shared<gated_grads_kernel<PN, PP, VEC>, 227 * 1024>(smem)));
+    gated_grads_kernel<PN, PP, VEC><<<unsigned(p.c.most * p.a.G * p.splits), kGradThreads, smem, s>>>(p);
+    MG_TRY(launched("mg_gated_scan_bwd"));
+    if (p.splits == 1) return MG_OK;
+    gated_join_rows_kernel<<<unsigned(p.c.most * p.a.G), 256, 0, s>>>(p);
+    return launched("mg_gated_scan_bwd");
+}
+
+mg_status make_call(const GatedArgs &a, bool bwd, TcCall &p, cudaStream_t s)
+{
+    const bool packed = a.cu != nullptr;
+    const Plan w = plan_of(a.B, a.T, a.H, a.G, a.N, a.P, a.nseq, packed, bwd);
+    char *ws = static_cast<char *>(a.ws);
+    const auto at = [&](size_t o) { return reinterpret_cast<float *>(ws + o); };
+    p.a = a, p.m = w.m;
+    p.c.q = p.seg.q = make_seqs(a.cu, a.B, a.T, a.nseq);
+    p.c.L = kRows, p.seg.L = kRows * w.m;
+    p.c.per = int(ceil_div(a.T, p.c.L)), p.seg.per = int(ceil_div(a.T, p.seg.L));
+    p.c.most = w.chunks, p.seg.most = w.segments;
+    p.c.first = reinterpret_cast<const int *>(ws + w.first), p.seg.first = reinterpret_cast<const int *>(ws + w.seg_first);
+    const Walked in_ws{at(w.local), at(w.carry), at(w.reach), at(w.totals)};
+    float *saved = bwd ? const_cast<float *>(a.saved_in) : a.saved;
+    if (saved != nullptr) p.s = Walked{saved, saved + w.s_carry / 4, saved + w.s_reach / 4, at(w.totals)};
+    else p.s = in_ws;
+    p.d = in_ws;
+    p.starts = bwd || a.S0 != nullptr;
+    p.partial = at(w.partial);
+    p.splits = w.splits, p.heads = int(ceil_div(a.H / a.G, w.splits));
+    p.error = &reinterpret_cast<Control *>(a.ws)->error;
+    MG_TRY(check_grids(bwd ? "mg_gated_scan_bwd" : "mg_gated_scan_fwd",
+                       {w.chunks * a.H, w.segments * a.H * ceil_div(a.P, 64), w.chunks * a.G * w.splits,
+                        a.nseq * a.H * ceil_div(int64_t((a.P + 3) / 4) * a.N, 256)}));
+    if (!packed) return MG_OK;
+    return launch_chunk_tables(p.c, p.seg, a.ws, s);
+}
+
+// Copies of 16 bytes where every row and head begins on such a boundary and
+// ends on one.
+bool by_pieces(const GatedArgs &a)
+{
+    const int64_t all = a.N | a.P | a.ldq | a.ldk | a.ldv | (a.dout != nullptr ? a.lddo : 0);
+    return all % 8 == 0;
+}
+
+#define MG_GATED_TC(F)                                                  \
+    const bool vec = by_pieces(a);                                      \
+    if (a.N <= 64) {                                                    \
+        if (a.P <= 64) return vec ? F<1, 1, true>(p, s) : F<1, 1, false>(p, s); \
+        return vec ? F<1, 2, true>(p, s) : F<1, 2, false>(p, s);        \
+    }                                                                   \
+    if (a.P <= 64) return vec ? F<2, 1, true>(p, s) : F<2, 1, false>(p, s); \
+    return vec ? F<2, 2, true>(p, s) : F<2, 2, false>(p, s);
+
+}  // namespace
+
+size_t gated_tc_saved_bytes(int64_t B, int64_t T, int H, int N, int P, int64_t nseq, bool packed)
+{
+    return plan_of(B, T, H, 1, N, P, nseq, packed, false).saved;
+}
+
+size_t gated_tc_ws_bytes(int64_t B, int64_t T, int H, int G, int N, int P, int64_t nseq, bool packed, bool bwd)
+{
+    return plan_of(B, T, H, G, N, P, nseq, packed, bwd).end;
+}
+
+mg_status launch_gated_tc_fwd(const GatedArgs &a, cudaStream_t s)
+{
+    TcCall p{};
+    MG_TRY(make_call(a, false, p, s));
+    MG_GATED_TC(forward)
+}
+
+mg_status launch_gated_tc_bwd(const GatedArgs &a, cudaStream_t s)
+{
+    TcCall p{};
+    MG_TRY(make_call(a, true, p, s));
+    MG_GATED_TC(backward)
+}
+
+}  // namespace mg
