@@ -42,11 +42,11 @@ __device__ __forceinline__ void add_two(float &xh, float &xl, float yh, float yl
     xl = e - (xh - s);
 }
 
-// One warp: a lane has the gates of rows 4 lane .. 4 lane + 3.
-__device__ __forceinline__ void sum_gates(const float (&g)[4], Gates128 &to)
+// One warp: a lane has the gates of rows 4 lane .. 4 lane + 3, and gets the sums
+// up to each of them.
+__device__ __forceinline__ void sum_gates(const float (&g)[4], float (&h)[4], float (&l)[4])
 {
     const int lane = threadIdx.x & 31;
-    float h[4], l[4];
     h[0] = g[0], l[0] = 0.f;
 #pragma unroll
     for (int i = 1; i < 4; ++i) {
@@ -61,10 +61,15 @@ __device__ __forceinline__ void sum_gates(const float (&g)[4], Gates128 &to)
     }
     const float bh = __shfl_up_sync(~0u, th, 1), bl = __shfl_up_sync(~0u, tl, 1);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i)
         if (lane > 0) add_two(h[i], l[i], bh, bl);
-        to.hi[4 * lane + i] = h[i], to.lo[4 * lane + i] = l[i];
-    }
+}
+__device__ __forceinline__ void sum_gates(const float (&g)[4], Gates128 &to)
+{
+    float h[4], l[4];
+    sum_gates(g, h, l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) to.hi[4 * (threadIdx.x & 31) + i] = h[i], to.lo[4 * (threadIdx.x & 31) + i] = l[i];
 }
 __device__ __forceinline__ void fetch_gates(float (&g)[4], const float *from, int64_t ld, int len)
 {
@@ -94,22 +99,31 @@ __device__ __forceinline__ uint4 fetch_piece(const bf16_t *row, int piece, int c
     return v;
 }
 
-// `len` rows of `cols` values into a tile of 128 rows, zeros beside and below.
-template <int PANELS, int THREADS, bool VEC>
+// `len` rows of `cols` values into a tile of 128 rows, value by value, zeros
+// beside and below.
+template <int PANELS, int THREADS>
 __device__ __forceinline__ void load_rows(unsigned tile, const bf16_t *from, int64_t ld, int len, int cols)
 {
     constexpr int kPieces = PANELS * 8;
 #pragma unroll
     for (int u = 0; u < kRows * kPieces / THREADS; ++u) {
         const int id = threadIdx.x + THREADS * u, row = id / kPieces, piece = id % kPieces;
-        const unsigned at = tile_at(kRows, row, piece);
-        if constexpr (VEC) {
-            const bool on = row < len && piece * 8 < cols;
-            copy16(tile + at, on ? from + row * ld + piece * 8 : from, on);
-        } else {
-            st_tile(tile, at, fetch_piece<false>(from + row * ld, piece, cols, row < len));
-        }
+        st_tile(tile, tile_at(kRows, row, piece), fetch_piece<false>(from + row * ld, piece, cols, row < len));
     }
+}
+
+// Zeros in a tile's rows from `len` on: a copy takes 128 rows, whoever's they are.
+template <int PANELS, int THREADS>
+__device__ __forceinline__ void clear_rows(unsigned tile, int len)
+{
+    for (int i = threadIdx.x; i < (kRows - len) * PANELS * 8; i += THREADS)
+        st_tile(tile, tile_at(kRows, len + i / (PANELS * 8), i % (PANELS * 8)), make_uint4(0, 0, 0, 0));
+}
+
+// Asks for memory (16-byte multiples) to be brought to L2.
+__device__ __forceinline__ void to_l2(const void *from, unsigned bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" : : "l"(from), "r"(bytes) : "memory");
 }
 
 // A tile's rows to global memory, `cols` of each.
@@ -134,12 +148,13 @@ __device__ __forceinline__ void store_rows(bf16_t *to, int64_t ld, unsigned tile
     }
 }
 
-// 32 values of one row, rounded, into a tile from column 32 block on.
-__device__ __forceinline__ void put32(unsigned tile, int row, int block, const float (&v)[32])
+// V values of one row, rounded, into a tile from column 8 piece on.
+template <int V>
+__device__ __forceinline__ void put(unsigned tile, int row, int piece, const float (&v)[V])
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        st_tile(tile, tile_at(kRows, row, 4 * block + i),
+    for (int i = 0; i < V / 8; ++i)
+        st_tile(tile, tile_at(kRows, row, piece + i),
                 make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]), pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
                            pack_bf16x2(v[8 * i + 4], v[8 * i + 5]), pack_bf16x2(v[8 * i + 6], v[8 * i + 7])));
 }
@@ -163,7 +178,8 @@ struct Walked {
     float *totals;   // [segments][H]: of the segment's gates
 };
 
-struct TcCall {
+struct alignas(64) TcCall {
+    CUtensorMap q, k, v, dout;   // where rows are aligned
     GatedArgs a;
     Chunks c, seg;   // chunks, and segments of m of them
     int m;
@@ -225,18 +241,21 @@ __device__ __forceinline__ void wait_or_tell(uint64_t *bar, unsigned phase, unsi
 
 constexpr int kWalkThreads = 256;
 
+struct WalkSmall {
+    float by[kRows];         // the weights of the chunk's rows
+    float whole, whole_lo;   // the sum of its gates
+    uint64_t bar, full[2];
+    unsigned tmem;
+};
+
 template <int PN, bool VEC, bool BACK>
-__global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const TcCall p, int tiles)
+__global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const __grid_constant__ TcCall p, int tiles)
 {
     extern __shared__ __align__(1024) char sm[];
     constexpr unsigned kK = PN * kRows * 128, kV = kRows * 128;
     const GatedArgs &a = p.a;
     const unsigned base = smem_addr(sm), tv = base + 2 * kK;
-    struct Small {
-        Gates128 g[2];
-        uint64_t bar;
-        unsigned tmem;
-    };
+    using Small = WalkSmall;
     Small &sh = *reinterpret_cast<Small *>(sm + 2 * kK + 3 * kV);
 
     const int tile = int(blockIdx.x % tiles), h = int(blockIdx.x / tiles % a.H), grp = h / (a.H / a.G);
@@ -248,28 +267,55 @@ __global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const TcCal
     const int p0 = tile * 64, cols = a.P - p0 < 64 ? a.P - p0 : 64;
     const int count = (s.len + kRows - 1) / kRows;
     const int64_t c0 = p.c.begin(s.seq) + int64_t(s.idx) * p.m, size = state_size(a.N, a.P);
-    const bf16_t *kk = static_cast<const bf16_t *>(BACK ? a.q : a.k) + grp * a.N;
+    const bf16_t *kk = static_cast<const bf16_t *>(BACK ? a.q : a.k) + grp * a.N;   // where K is loaded value by value
     const bf16_t *vv = static_cast<const bf16_t *>(BACK ? a.dout : a.v) + h * a.P + p0;
     const int64_t ldk = BACK ? a.ldq : a.ldk, ldv = BACK ? a.lddo : a.ldv;
 
     if (warp == 0) tmem_take(&sh.tmem, 64);
-    if (tid == 0) bar_init(&sh.bar);
+    if (tid == 0) bar_init(&sh.bar), bar_init(&sh.full[0]), bar_init(&sh.full[1]);
+    fence_tiles();
+    __syncthreads();
     float g[4];
     uint4 v[4];
     const auto chunk_at = [&](int i) { return BACK ? count - 1 - i : i; };
     const auto fetch = [&](int i) {   // chunk i of the walk: K into its buffer, V and gates into registers
         const int ci = chunk_at(i), len = s.len - ci * kRows < kRows ? s.len - ci * kRows : kRows;
         const int64_t row = s.row + int64_t(ci) * kRows;
-        load_rows<PN, kWalkThreads, VEC>(base + (i & 1) * kK, kk + row * ldk, ldk, len, a.N);
-        cp_async_commit();
+        if constexpr (VEC) {
+            if (tid == kWalkThreads - 32) {
+                bar_expect(&sh.full[i & 1], PN * kPanelBytes);
+                copy_tile<PN>(base + (i & 1) * kK, BACK ? p.q : p.k, grp, int(row), &sh.full[i & 1]);
+            }
+        } else {
+            load_rows<PN, kWalkThreads>(base + (i & 1) * kK, kk + row * ldk, ldk, len, a.N);
+        }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int r = (tid >> 3) + 32 * u;
             v[u] = fetch_piece<VEC>(vv + (row + r) * ldv, tid & 7, cols, r < len);
         }
-        if (warp == 0) fetch_gates(g, a.g + row * a.ldg + h, a.ldg, len);
+    };
+    // warp 0: the next chunk's gates, and the weights of the one whose gates it has
+    const auto next_gates = [&](int i) {
+        if (i >= count) return;
+        const int ci = chunk_at(i), len = s.len - ci * kRows < kRows ? s.len - ci * kRows : kRows;
+        fetch_gates(g, a.g + (s.row + int64_t(ci) * kRows) * a.ldg + h, a.ldg, len);
+    };
+    const auto weigh = [&]() {
+        float hi[4], lo[4];
+        sum_gates(g, hi, lo);
+        const float th = __shfl_sync(~0u, hi[3], 31), tl = __shfl_sync(~0u, lo[3], 31);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            sh.by[4 * lane + e] = BACK ? a.scale * Gates128::exp_of(hi[e] + lo[e]) : Gates128::exp_of((th - hi[e]) + (tl - lo[e]));
+        if (lane == 0) sh.whole = th, sh.whole_lo = tl;
     };
     fetch(0);
+    if (warp == 0) {
+        next_gates(0);
+        weigh();
+        next_gates(1);
+    }
     float S[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) S[i] = 0.f;
@@ -282,18 +328,20 @@ __global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const TcCal
     };
     float reach = 0.f;
     for (int i = 0; i < count; ++i) {
-        Gates128 &gates = sh.g[i & 1];
-        if (warp == 0) sum_gates(g, gates);
-        cp_async_wait<0>();
-        __syncthreads();
+        __syncthreads();   // the weights
+        if constexpr (VEC) {
+            const int left = s.len - chunk_at(i) * kRows;
+            wait_or_tell(&sh.full[i & 1], (i >> 1) & 1, p.error);
+            if (left < kRows) clear_rows<PN, kWalkThreads>(base + (i & 1) * kK, left);
+        }
         const int64_t ch = (c0 + chunk_at(i)) * a.H + h;
         if (tid == 0 && tile == 0) w.reach[ch] = reach;
         if (i > 0) put(w.local + ch * size);
-        const float whole = gates.hi[kRows - 1], whole_lo = gates.lo[kRows - 1];
+        const float whole = sh.whole, whole_lo = sh.whole_lo;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int r = (tid >> 3) + 32 * u;
-            const float by = BACK ? a.scale * Gates128::exp_of(gates.hi[r] + gates.lo[r]) : gates.span(whole, whole_lo, r);
+            const float by = sh.by[r];
             float f[8];
             unpack8(v[u], f);
             unsigned x[3][4];
@@ -316,7 +364,13 @@ __global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const TcCal
                 multiply(acc, Operand{base + (i & 1) * kK, kRows, true}, Operand{tv + k * kV, kRows, true}, 64, kRows / 16, k < 2);
             bar_after_products(&sh.bar);
         }
-        if (i + 1 < count) fetch(i + 1);
+        if (i + 1 < count) {
+            fetch(i + 1);
+            if (warp == 0) {   // everyone has read this chunk's
+                weigh();
+                next_gates(i + 2);
+            }
+        }
         reach += whole + whole_lo;
         const float decay = expf(whole) * (1.f + whole_lo);
         wait_or_tell(&sh.bar, i & 1, p.error);
@@ -351,9 +405,20 @@ __global__ void __launch_bounds__(256) over_segments_kernel(const Chunks seg, co
     const int64_t size = state_size(N, P), out = (sh * N + n) * P + p0;
     const int64_t lo = seg.begin(seq), hi = seg.end(seq);
     float s[4];
-    // + 0: a caller's signalling NaN must not get into the workspace as it is
 #pragma unroll
-    for (int e = 0; e < 4; ++e) s[e] = from != nullptr && e < cols ? __ldg(from + out + e) + 0.f : 0.f;
+    for (int e = 0; e < 4; ++e) s[e] = 0.f;
+    if (from != nullptr) {
+        if (P % 4 == 0) {
+            load_vec<4>(from + out, s);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (e < cols) s[e] = __ldg(from + out + e);
+        }
+        // + 0: a caller's signalling NaN must not get into the workspace as it is
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] += 0.f;
+    }
     for (int64_t i0 = 0; i0 < hi - lo; i0 += kAhead) {
         float add[kAhead][4], gate[kAhead];
 #pragma unroll
@@ -374,53 +439,80 @@ __global__ void __launch_bounds__(256) over_segments_kernel(const Chunks seg, co
         }
     }
     if (to == nullptr) return;
+    if (P % 4 == 0) {
+        store_vec<4>(to + out, s);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (e < cols) to[out + e] = s[e];
+        for (int e = 0; e < 4; ++e)
+            if (e < cols) to[out + e] = s[e];
+    }
 }
+
+// Within a chunk, weights e^{G_i - G_j}: pairs of rows in the same 32 take the
+// exponential; the others the product of e^{G_i - G_r} and e^{G_r - G_j}, r the
+// last of j's 32 rows, both at most 1: one exponential a row and block instead
+// of one a pair.
+struct Weights {
+    Gates128 g;
+    float to_end[kRows];   // e^{G_r - G_j}
+    // One warp, after sum_gates.
+    __device__ __forceinline__ void fill()
+    {
+        __syncwarp();
+        for (int b = 0; b < 4; ++b) {
+            const int j = 32 * b + (threadIdx.x & 31);
+            to_end[j] = g.span(g.hi[32 * b + 31], g.lo[32 * b + 31], j);
+        }
+    }
+};
 
 // ------------------------------------------------------------------- rows
 // A block: o of a chunk and head.  Q K^T, weights, times V, and Q S beside it;
 // the weights take Q's place in shared memory and V takes K's, so that two blocks
 // fit an SM and one's products run under the other's loads and exponentials.
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 512;
+
+struct RowsSmall {
+    Weights w;
+    uint64_t full[2], done[2];
+    unsigned tmem;
+};
 
 template <int PN, int PP, bool VEC>
-__global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const TcCall p)
+__global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid_constant__ TcCall p)
 {
     extern __shared__ __align__(1024) char sm[];
     constexpr int NB = 64 * PN, PB = 64 * PP;
-    constexpr unsigned kQ = 2 * kRows * 128, kK = (PN > PP ? PN : PP) * kRows * 128, kS = PP * NB * 128;
+    constexpr unsigned kQ = 2 * kPanelBytes, kK = (PN > PP ? PN : PP) * kPanelBytes, kS = PP * NB * 128;
     const GatedArgs &a = p.a;
     const unsigned tq = smem_addr(sm), tk = tq + kQ, ts = tk + kK;
-    struct Small {
-        Gates128 g;
-        uint64_t bar[2];
-        unsigned tmem;
-    };
+    using Small = RowsSmall;
     Small &sh = *reinterpret_cast<Small *>(sm + kQ + kK + kS);
     const int64_t c = blockIdx.x / a.H;
     const int h = int(blockIdx.x % a.H), grp = h / (a.H / a.G);
     const Chunks::One ch = p.c.get(c);
     if (ch.len == 0) return;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (warp == 0) tmem_take(&sh.tmem, 256);
-    if (tid == 0) bar_init(&sh.bar[0]), bar_init(&sh.bar[1]);
-    load_rows<PN, kRowThreads, VEC>(tq, static_cast<const bf16_t *>(a.q) + ch.row * a.ldq + grp * a.N, a.ldq, ch.len, a.N);
-    load_rows<PN, kRowThreads, VEC>(tk, static_cast<const bf16_t *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
-    cp_async_commit();
-    uint4 v[4 * PP];
-    const bf16_t *vv = static_cast<const bf16_t *>(a.v) + ch.row * a.ldv + h * a.P;
-#pragma unroll
-    for (int u = 0; u < 4 * PP; ++u) {
-        const int id = tid + kRowThreads * u, r = id / (8 * PP);
-        v[u] = fetch_piece<VEC>(vv + r * a.ldv, id % (8 * PP), a.P, r < ch.len);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rb = warp & 3, cb = warp >> 2, row = 32 * rb + lane;
+    if (tid == 32) {
+        bar_init(&sh.done[0]), bar_init(&sh.done[1]), bar_init(&sh.full[0]), bar_init(&sh.full[1]);
+        fence_tiles();
+        if constexpr (VEC) {
+            bar_expect(&sh.full[0], 2 * PN * kPanelBytes);
+            copy_tile<PN>(tq, p.q, grp, int(ch.row), &sh.full[0]);
+            copy_tile<PN>(tk, p.k, grp, int(ch.row), &sh.full[0]);
+        }
     }
     if (warp == 0) {
         float g[4];
         fetch_gates(g, a.g + ch.row * a.ldg + h, a.ldg, ch.len);
-        sum_gates(g, sh.g);
+        tmem_take(&sh.tmem, 256);
+        sum_gates(g, sh.w.g);
+        sh.w.fill();
+    }
+    if constexpr (!VEC) {
+        load_rows<PN, kRowThreads>(tq, static_cast<const bf16_t *>(a.q) + ch.row * a.ldq + grp * a.N, a.ldq, ch.len, a.N);
+        load_rows<PN, kRowThreads>(tk, static_cast<const bf16_t *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
     }
     {   // the state, rounded: an operand of bf16 outputs
         const Source s = source_of<false>(p, ch, c, h);
@@ -432,45 +524,68 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const TcCall
             st_tile(ts, tile_at(NB, n, piece), make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
         }
     }
-    cp_async_wait<0>();
+    if constexpr (VEC) {   // what the block that follows on this SM will read: 128 threads an operand
+        const int64_t next = int64_t(blockIdx.x) + 2 * 152, cn = next / a.H;
+        const int hn = int(next % a.H), what = tid >> 7, r = tid & 127;
+        if (cn < p.c.most) {
+            const Chunks::One n = p.c.get(cn);
+            if (r < n.len) {
+                if (what == 0) to_l2(static_cast<const bf16_t *>(a.q) + (n.row + r) * a.ldq + hn / (a.H / a.G) * a.N, 2 * a.N);
+                if (what == 1) to_l2(static_cast<const bf16_t *>(a.k) + (n.row + r) * a.ldk + hn / (a.H / a.G) * a.N, 2 * a.N);
+                if (what == 2) to_l2(static_cast<const bf16_t *>(a.v) + (n.row + r) * a.ldv + hn * a.P, 2 * a.P);
+                if (what == 3 && r == 0) {
+                    const Source f = source_of<false>(p, n, cn, hn);
+                    if (f.local != nullptr) to_l2(f.local, unsigned(state_size(a.N, a.P) * 4));
+                }
+            }
+        }
+    }
     fence_tiles();
     tmem_before_sync();
     __syncthreads();
     tmem_after_sync();
-    const unsigned acc = sh.tmem, acc_s = acc + 128, mine = unsigned(32 * (warp & 3)) << 16;
+    const unsigned acc = sh.tmem, acc_s = acc + 128, mine = unsigned(32 * rb) << 16;
     if (tid == 0) {
         const int steps = (a.N + 15) / 16;
+        // rows of K and Q behind the chunk only reach rows and columns that are not used
+        if constexpr (VEC) wait_or_tell(&sh.full[0], 0, p.error);
         multiply(acc, Operand{tq, kRows, false}, Operand{tk, kRows, false}, kRows, steps, false);
-        bar_after_products(&sh.bar[0]);
+        bar_after_products(&sh.done[0]);
         multiply(acc_s, Operand{tq, kRows, false}, Operand{ts, NB, true}, PB, steps, false);
-        bar_after_products(&sh.bar[1]);
+        bar_after_products(&sh.done[1]);
     }
-    const int row = 32 * (warp & 3) + lane;
-    const float hi = sh.g.hi[row], lo = sh.g.lo[row];
-    wait_or_tell(&sh.bar[0], 0, p.error);
-    wait_or_tell(&sh.bar[1], 0, p.error);   // Q is read: the weights may take its place
+    const float hi = sh.w.g.hi[row], lo = sh.w.g.lo[row];
+    wait_or_tell(&sh.done[0], 0, p.error);
+    if constexpr (VEC) {
+        if (tid == 32) {   // K is read
+            bar_expect(&sh.full[1], PP * kPanelBytes);
+            copy_tile<PP>(tk, p.v, h, int(ch.row), &sh.full[1]);
+        }
+    } else {
+        load_rows<PP, kRowThreads>(tk, static_cast<const bf16_t *>(a.v) + ch.row * a.ldv + h * a.P, a.ldv, ch.len, a.P);
+    }
     tmem_after_sync();
-    // blocks of 32 columns, every second one to a warp; those above the diagonal are zeros
-#pragma unroll
-    for (int b = warp >> 2; b < 4; b += 2) {
+    {   // a block of 32 columns a warp; those above the diagonal are zeros
         float w[32];
-        if (b <= (warp & 3)) {
-            tmem_load(acc + mine + 32 * b, w);
+        if (cb < rb) {
+            const float from = sh.w.g.span(hi, lo, 32 * cb + 31);
+            tmem_load(acc + mine + 32 * cb, w);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                const int j = 32 * b + e;
-                w[e] = j <= row ? w[e] * sh.g.span(hi, lo, j) : 0.f;
-            }
+            for (int e = 0; e < 32; ++e) w[e] *= from * sh.w.to_end[32 * cb + e];
+        } else if (cb == rb) {
+            tmem_load(acc + mine + 32 * cb, w);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) w[e] = e <= lane ? w[e] * sh.w.g.span(hi, lo, 32 * cb + e) : 0.f;
         } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) w[e] = 0.f;
         }
-        put32(tq, row, b, w);
+        wait_or_tell(&sh.done[1], 0, p.error);   // Q is read: the weights may take its place
+        put<32>(tq, row, 4 * cb, w);
     }
-#pragma unroll
-    for (int u = 0; u < 4 * PP; ++u) {
-        const int id = tid + kRowThreads * u;
-        st_tile(tk, tile_at(kRows, id / (8 * PP), id % (8 * PP)), v[u]);
+    if constexpr (VEC) {
+        wait_or_tell(&sh.full[1], 0, p.error);
+        if (ch.len < kRows) clear_rows<PP, kRowThreads>(tk, ch.len);
     }
     fence_tiles();
     tmem_before_sync();
@@ -478,19 +593,21 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const TcCall
     if (tid == 0) {
         tmem_after_sync();
         multiply(acc, Operand{tq, kRows, false}, Operand{tk, kRows, true}, PB, (ch.len + 15) / 16, false);
-        bar_after_products(&sh.bar[0]);
+        bar_after_products(&sh.done[0]);
     }
     const float up = Gates128::exp_of(hi + lo);
-    wait_or_tell(&sh.bar[0], 1, p.error);
+    wait_or_tell(&sh.done[0], 1, p.error);
     tmem_after_sync();
+    if (cb < PB / 32) {
 #pragma unroll
-    for (int b = warp >> 2; b < PB / 32; b += 2) {
-        float x[32], y[32];
-        tmem_load(acc + mine + 32 * b, x);
-        tmem_load(acc_s + mine + 32 * b, y);
+        for (int half = 0; half < 2; ++half) {
+            float x[16], y[16];
+            tmem_load(acc + mine + 32 * cb + 16 * half, x);
+            tmem_load(acc_s + mine + 32 * cb + 16 * half, y);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = a.scale * fmaf(up, y[e], x[e]);
-        put32(tk, row, b, x);
+            for (int e = 0; e < 16; ++e) x[e] = a.scale * fmaf(up, y[e], x[e]);
+            put<16>(tk, row, 4 * cb + 2 * half, x);
+        }
     }
     tmem_before_sync();
     __syncthreads();
@@ -500,22 +617,29 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const TcCall
 
 // -------------------------------------------------------------- gradients
 // A block: a chunk, a group's heads (or a part of them), one after another: dv
-// and dg of each, dq and dk summed over them in tensor memory.
+// and dg of each, dq and dk summed over them in tensor memory.  One block fits an
+// SM; the adjoint's and the state's pieces share a place (kX), which for N and
+// P above 64 is the weights' too.
 
 constexpr int kGradThreads = 512;
 
 template <int PN, int PP>
-struct GradSmem {
+struct Grad {
     static constexpr int NB = 64 * PN, PB = 64 * PP;
-    static constexpr unsigned kQ = PN * kRows * 128, kV = PP * kRows * 128, kState = PP * NB * 128, kW = 2 * kRows * 128;
-    static constexpr unsigned kX = 3 * kState > 2 * kW + 4096 ? 3 * kState : 2 * kW + 4096;
+    // N and P above 64: the adjoint's products come before the weights', straight
+    // into dk's sums, for a single head; else beside the weights' products.
+    static constexpr bool kFirst = PN == 2 && PP == 2;
+    static constexpr unsigned kQ = PN * kPanelBytes, kV = PP * kPanelBytes, kState = PP * NB * 128, kW = 2 * kPanelBytes;
+    static constexpr unsigned kX = 3 * kState;
+    static constexpr unsigned kTiles = 2 * kQ + 2 * kV + (kFirst ? kX : 2 * kW + kX);
     struct Small {
-        Gates128 g;
+        Weights w;
         float after[kRows], key[kRows], dots[16];
-        uint64_t bar;
+        uint64_t full[2], done[2];
         unsigned tmem;
+        float parts[kFirst ? 1 : 8 * kRows];   // sums of the weights, by blocks of 32 columns and of rows
     };
-    static constexpr size_t bytes = 2 * kQ + 2 * kV + kX + sizeof(Small);
+    static constexpr size_t bytes = kTiles + sizeof(Small);
 };
 
 // Sums over a warp's 32 rows: lane l gets column l's.
@@ -534,33 +658,49 @@ __device__ __forceinline__ float column_sums(float (&w)[32])
 }
 
 template <int PN, int PP, bool VEC>
-__global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const TcCall p)
+__global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __grid_constant__ TcCall p)
 {
     extern __shared__ __align__(1024) char sm[];
-    using M = GradSmem<PN, PP>;
+    using M = Grad<PN, PP>;
     constexpr int NB = M::NB, PB = M::PB;
     const GatedArgs &a = p.a;
-    const unsigned tq = smem_addr(sm), tk = tq + M::kQ, tv = tk + M::kQ, to = tv + M::kV, tx = to + M::kV, tw = tx, tdw = tx + M::kW;
-    char *x_area = sm + 2 * M::kQ + 2 * M::kV;
-    float *row_part = reinterpret_cast<float *>(x_area + 2 * M::kW), *col_part = row_part + 4 * kRows;
-    auto &sh = *reinterpret_cast<typename M::Small *>(x_area + M::kX);
+    const unsigned tq = smem_addr(sm), tk = tq + M::kQ, tv = tk + M::kQ, to = tv + M::kV, tw = to + M::kV, tdw = tw + M::kW;
+    const unsigned tx = M::kFirst ? tw : tdw + M::kW;
+    auto &sh = *reinterpret_cast<typename M::Small *>(sm + M::kTiles);
+    // beside the weights where they share their place with the pieces
+    float *row_part = M::kFirst ? reinterpret_cast<float *>(sm + 2 * M::kQ + 2 * M::kV + 2 * M::kW) : sh.parts, *col_part = row_part + 4 * kRows;
 
     const int split = int(blockIdx.x % p.splits), grp = int(blockIdx.x / p.splits % a.G);
     const int64_t c = int64_t(blockIdx.x) / p.splits / a.G;
     const Chunks::One ch = p.c.get(c);
     if (ch.len == 0) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rb = warp & 3, cb = warp >> 2, row = 32 * rb + lane;
-    if (warp == 0) tmem_take(&sh.tmem, 512);
-    if (tid == 0) bar_init(&sh.bar);
-    load_rows<PN, kGradThreads, VEC>(tq, static_cast<const bf16_t *>(a.q) + ch.row * a.ldq + grp * a.N, a.ldq, ch.len, a.N);
-    load_rows<PN, kGradThreads, VEC>(tk, static_cast<const bf16_t *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
     const int per_group = a.H / a.G, h0 = split * p.heads, h1 = h0 + p.heads < per_group ? h0 + p.heads : per_group;
+    const auto copy_head = [&](int h) {   // V and dO
+        bar_expect(&sh.full[1], 2 * PP * kPanelBytes);
+        copy_tile<PP>(tv, p.v, h, int(ch.row), &sh.full[1]);
+        copy_tile<PP>(to, p.dout, h, int(ch.row), &sh.full[1]);
+    };
+    if (tid == 32) {
+        bar_init(&sh.done[0]), bar_init(&sh.done[1]), bar_init(&sh.full[0]), bar_init(&sh.full[1]);
+        fence_tiles();
+        if constexpr (VEC) {
+            bar_expect(&sh.full[0], 2 * PN * kPanelBytes);
+            copy_tile<PN>(tq, p.q, grp, int(ch.row), &sh.full[0]);
+            copy_tile<PN>(tk, p.k, grp, int(ch.row), &sh.full[0]);
+        }
+    }
+    if (warp == 0) tmem_take(&sh.tmem, 512);
+    if constexpr (!VEC) {
+        load_rows<PN, kGradThreads>(tq, static_cast<const bf16_t *>(a.q) + ch.row * a.ldq + grp * a.N, a.ldq, ch.len, a.N);
+        load_rows<PN, kGradThreads>(tk, static_cast<const bf16_t *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
+    }
     const int nsteps = (a.N + 15) / 16, psteps = (a.P + 15) / 16;
     const unsigned mine = unsigned(32 * rb) << 16;
-    unsigned phase = 0, acc = 0;
-    const auto products_done = [&]() {
-        wait_or_tell(&sh.bar, phase, p.error);
-        phase ^= 1;
+    unsigned phase[2] = {0, 0}, acc0 = 0, acc1 = 0, acc_q = 0, acc_k = 0, acc_d = 0;
+    const auto products_done = [&](int b) {
+        wait_or_tell(&sh.done[b], phase[b], p.error);
+        phase[b] ^= 1;
         tmem_after_sync();
     };
     // writes of tiles and reads of accumulators before the next products
@@ -570,170 +710,244 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const TcCa
         __syncthreads();
         tmem_after_sync();
     };
-    // adds the column blocks' sums v for each row to to[row], block after block
-    const auto add_blocks = [&](float *to, float v, int blocks, bool fresh) {
+    // adds the column blocks' sums v of each row to to[row], block after block
+    const auto add_blocks = [&](float *sums, float v, int blocks, bool fresh) {
         for (int b = 0; b < blocks; ++b) {
-            if (cb == b) to[row] = (b == 0 && fresh ? 0.f : to[row]) + v;
+            if (cb == b) sums[row] = (b == 0 && fresh ? 0.f : sums[row]) + v;
             __syncthreads();
         }
     };
+    constexpr int kUnits = NB * PP * 8 / kGradThreads;
+    float st[kUnits][8];
+    const auto fetch_states = [&](const Source &from) {
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const int id = tid + kGradThreads * u;
+            fetch_state(from, id % NB, id / NB, a.N, a.P, st[u]);
+        }
+    };
+    const auto put_states = [&]() {   // as three pieces
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+            const int id = tid + kGradThreads * u;
+            unsigned x[3][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const Pieces q = split3(st[u][2 * e], st[u][2 * e + 1]);
+                x[0][e] = q.a, x[1][e] = q.b, x[2][e] = q.c;
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                st_tile(tx + k * M::kState, tile_at(NB, id % NB, id / NB), make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]));
+        }
+    };
+    const auto with_pieces = [&](unsigned acc, unsigned tile) {   // acc = tile (S or D)^T, the small pieces first
+        for (int k = 2; k >= 0; --k)
+            multiply(acc, Operand{tile, kRows, false}, Operand{tx + k * M::kState, NB, false}, NB, psteps, k < 2);
+    };
+    // Rows of `from` times `by`, added to those of `sums` (or in their place); their products with the tile's rows.
+    const auto take = [&](unsigned from, unsigned sums, float by, unsigned tile, bool add) {
+        float x[32], of = 0.f;
+        tmem_load(from + mine + 32 * cb, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float f[8];
+            unpack8(ld_tile(tile, tile_at(kRows, row, 4 * cb + i)), f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[8 * i + e] *= by;
+                of = fmaf(x[8 * i + e], f[e], of);
+            }
+        }
+        if (add) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float t[16];
+                tmem_load(sums + mine + 32 * cb + 16 * half, t);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[16 * half + e] += t[e];
+            }
+        }
+        tmem_store(sums + mine + 32 * cb, x);
+        return of;
+    };
     for (int hh = h0; hh < h1; ++hh) {
         const int h = grp * per_group + hh;
-        __syncthreads();   // the head before is done with its tiles
-        load_rows<PP, kGradThreads, VEC>(tv, static_cast<const bf16_t *>(a.v) + ch.row * a.ldv + h * a.P, a.ldv, ch.len, a.P);
-        load_rows<PP, kGradThreads, VEC>(to, static_cast<const bf16_t *>(a.dout) + ch.row * a.lddo + h * a.P, a.lddo, ch.len, a.P);
-        cp_async_commit();
+        if (hh > h0) {   // the head before is done with its tiles
+            fence_tiles();
+            __syncthreads();
+        }
+        if constexpr (VEC) {
+            if (tid == 32) copy_head(h);
+        } else {
+            load_rows<PP, kGradThreads>(tv, static_cast<const bf16_t *>(a.v) + ch.row * a.ldv + h * a.P, a.ldv, ch.len, a.P);
+            load_rows<PP, kGradThreads>(to, static_cast<const bf16_t *>(a.dout) + ch.row * a.lddo + h * a.P, a.lddo, ch.len, a.P);
+        }
         if (warp == 0) {
             float g[4];
             fetch_gates(g, a.g + ch.row * a.ldg + h, a.ldg, ch.len);
-            sum_gates(g, sh.g);
+            sum_gates(g, sh.w.g);
+            sh.w.fill();
         }
         const Source from_d = source_of<true>(p, ch, c, h), from_s = source_of<false>(p, ch, c, h);
-        cp_async_wait<0>();
+        // <S, D>: both in registers, D then stays
+        float dot = 0.f;
+        {
+            fetch_states(from_d);
+#pragma unroll
+            for (int u = 0; u < kUnits; ++u) {
+                const int id = tid + kGradThreads * u;
+                float s[8];
+                fetch_state(from_s, id % NB, id / NB, a.N, a.P, s);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dot = fmaf(s[e], st[u][e], dot);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
+        if (lane == 0) sh.dots[warp] = dot;
+        if constexpr (VEC) {   // the rows of the next head: of this block, or of the block that follows on the SM
+            const int64_t next = int64_t(blockIdx.x) + 152, cn = hh + 1 < h1 ? c : next / p.splits / a.G;
+            const int gn = hh + 1 < h1 ? grp : int(next / p.splits % a.G), hn = hh + 1 < h1 ? h + 1 : gn * per_group + int(next % p.splits) * p.heads;
+            const Chunks::One n = hh + 1 < h1 ? ch : cn < p.c.most ? p.c.get(cn) : Chunks::One{0, 0, 0, 0};
+            const int what = tid >> 7, r = tid & 127;
+            if (r < n.len) {
+                if (what == 0) to_l2(static_cast<const bf16_t *>(a.v) + (n.row + r) * a.ldv + hn * a.P, 2 * a.P);
+                if (what == 1) to_l2(static_cast<const bf16_t *>(a.dout) + (n.row + r) * a.lddo + hn * a.P, 2 * a.P);
+                if (what == 2 && hh + 1 == h1) to_l2(static_cast<const bf16_t *>(a.q) + (n.row + r) * a.ldq + gn * a.N, 2 * a.N);
+                if (what == 3 && hh + 1 == h1) to_l2(static_cast<const bf16_t *>(a.k) + (n.row + r) * a.ldk + gn * a.N, 2 * a.N);
+                if (what < 2 && r == 0) {
+                    const Source f = what == 0 ? source_of<true>(p, n, cn, hn) : source_of<false>(p, n, cn, hn);
+                    if (f.local != nullptr) to_l2(f.local, unsigned(state_size(a.N, a.P) * 4));
+                }
+            }
+        }
+        put_states();
+        if constexpr (VEC) {
+            if (hh == h0) wait_or_tell(&sh.full[0], 0, p.error);
+            wait_or_tell(&sh.full[1], (hh - h0) & 1, p.error);
+            if (ch.len < kRows) {   // rows of other chunks that came along
+                if (hh == h0) clear_rows<PN, kGradThreads>(tq, ch.len), clear_rows<PN, kGradThreads>(tk, ch.len);
+                clear_rows<PP, kGradThreads>(tv, ch.len), clear_rows<PP, kGradThreads>(to, ch.len);
+            }
+        }
         before_products();
-        acc = sh.tmem;
-        const unsigned acc0 = acc, acc1 = acc + 128, acc_q = acc + 256, acc_k = acc + 384;
+        acc0 = sh.tmem, acc1 = acc0 + 128, acc_q = acc0 + 256, acc_k = acc_q + NB;
+        acc_d = M::kFirst ? acc_q : PB == 64 ? acc0 + 64 : acc_k + NB;   // K D
         if (tid == 0) {
             multiply(acc0, Operand{tq, kRows, false}, Operand{tk, kRows, false}, kRows, nsteps, false);
             multiply(acc1, Operand{to, kRows, false}, Operand{tv, kRows, false}, kRows, psteps, false);
-            bar_after_products(&sh.bar);
-        }
-        const float hi = sh.g.hi[row], lo = sh.g.lo[row];
-        const float tail = sh.g.span(sh.g.hi[kRows - 1], sh.g.lo[kRows - 1], row), up = Gates128::exp_of(hi + lo);
-        products_done();
-        {   // weights, and what each pair of rows gives to the gates between them
-            float s[32], d[32];
-            float of_row = 0.f, of_col = 0.f;
-            if (cb <= rb) {
-                tmem_load(acc0 + mine + 32 * cb, s);
-                tmem_load(acc1 + mine + 32 * cb, d);
-                float both[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int j = 32 * cb + e;
-                    const float by = a.scale * sh.g.span(hi, lo, j);
-                    d[e] = j <= row ? d[e] * by : 0.f;
-                    both[e] = j < row ? s[e] * d[e] : 0.f;
-                    s[e] = j <= row ? s[e] * by : 0.f;
-                    of_row += both[e];
-                }
-                of_col = column_sums(both);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) s[e] = d[e] = 0.f;
+            bar_after_products(&sh.done[0]);
+            if constexpr (M::kFirst) {
+                with_pieces(acc_k, tv);
+                multiply(acc_d, Operand{tk, kRows, false}, Operand{tx, NB, true}, PB, nsteps, false);
+                bar_after_products(&sh.done[1]);
             }
-            put32(tw, row, cb, s);
-            put32(tdw, row, cb, d);
+        }
+        const float hi = sh.w.g.hi[row], lo = sh.w.g.lo[row];
+        const float tail = sh.w.g.span(sh.w.g.hi[kRows - 1], sh.w.g.lo[kRows - 1], row), up = Gates128::exp_of(hi + lo);
+        products_done(0);
+        // weights, and what each pair of rows gives to the gates between them
+        float of_row = 0.f, of_col = 0.f;
+        unsigned pw[16], pd[16];
+        if (cb <= rb) {
+            float both[32];
+            const float from = a.scale * sh.w.g.span(hi, lo, 32 * cb + 31);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float s[16], d[16];
+                tmem_load(acc0 + mine + 32 * cb + 16 * half, s);
+                tmem_load(acc1 + mine + 32 * cb + 16 * half, d);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int j = 16 * half + e;
+                    if (cb < rb) {
+                        const float by = from * sh.w.to_end[32 * cb + j];
+                        d[e] *= by;
+                        both[j] = s[e] * d[e];
+                        s[e] *= by;
+                    } else {
+                        const float by = j <= lane ? a.scale * sh.w.g.span(hi, lo, 32 * cb + j) : 0.f;
+                        d[e] = j <= lane ? d[e] * by : 0.f;
+                        both[j] = j < lane ? s[e] * d[e] : 0.f;
+                        s[e] = j <= lane ? s[e] * by : 0.f;
+                    }
+                    of_row += both[j];
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) pw[8 * half + e] = pack_bf16x2(s[2 * e], s[2 * e + 1]), pd[8 * half + e] = pack_bf16x2(d[2 * e], d[2 * e + 1]);
+            }
+            of_col = column_sums(both);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pw[e] = pd[e] = 0;
+        }
+        const auto put_weights = [&]() {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                st_tile(tw, tile_at(kRows, row, 4 * cb + i), make_uint4(pw[4 * i], pw[4 * i + 1], pw[4 * i + 2], pw[4 * i + 3]));
+                st_tile(tdw, tile_at(kRows, row, 4 * cb + i), make_uint4(pd[4 * i], pd[4 * i + 1], pd[4 * i + 2], pd[4 * i + 3]));
+            }
             row_part[cb * kRows + row] = of_row;
             col_part[rb * kRows + 32 * cb + lane] = of_col;
+        };
+        float dv[32];   // K D's part of dv
+        if constexpr (M::kFirst) {
+            products_done(1);
+            const float of = take(acc_k, acc_k, tail, tk, false);
+            tmem_load(acc_d + mine + 32 * cb, dv);
+            put_weights();   // the adjoint's pieces are read
+            add_blocks(sh.key, of, NB / 32, true);
+        } else {
+            put_weights();
         }
         before_products();
         if (tid == 0) {
             const bool add = hh > h0;
             multiply(acc0, Operand{tw, kRows, true}, Operand{to, kRows, true}, PB, kRows / 16, false);
             multiply(acc_q, Operand{tdw, kRows, false}, Operand{tk, kRows, true}, NB, kRows / 16, add);
-            multiply(acc_k, Operand{tdw, kRows, true}, Operand{tq, kRows, true}, NB, kRows / 16, add);
-            bar_after_products(&sh.bar);
+            multiply(acc_k, Operand{tdw, kRows, true}, Operand{tq, kRows, true}, NB, kRows / 16, add || M::kFirst);
+            if constexpr (!M::kFirst) {
+                multiply(acc_d, Operand{tk, kRows, false}, Operand{tx, NB, true}, PB, nsteps, false);
+                with_pieces(acc1, tv);
+            }
+            bar_after_products(&sh.done[0]);
         }
         if (tid < kRows) {
             float x = 0.f;
             for (int b = 0; b < 4; ++b) x += row_part[b * kRows + tid] - col_part[b * kRows + tid];
             sh.after[tid] = x;
         }
-        constexpr int kUnits = NB * PP * 8 / kGradThreads;
-        float st[kUnits][8];
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            const int id = tid + kGradThreads * u;
-            fetch_state(from_d, id % NB, id / NB, a.N, a.P, st[u]);
-        }
-        products_done();
-        float dv[32];
-        if (cb < PB / 32) tmem_load(acc0 + mine + 32 * cb, dv);
-        __syncthreads();   // the sums of the weights are read: the adjoint may take their place
-        const auto put_state = [&]() {
-#pragma unroll
-            for (int u = 0; u < kUnits; ++u) {
-                const int id = tid + kGradThreads * u;
-                unsigned x[3][4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const Pieces q = split3(st[u][2 * e], st[u][2 * e + 1]);
-                    x[0][e] = q.a, x[1][e] = q.b, x[2][e] = q.c;
-                }
-#pragma unroll
-                for (int k = 0; k < 3; ++k)
-                    st_tile(tx + k * M::kState, tile_at(NB, id % NB, id / NB), make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]));
-            }
-        };
-        put_state();
-        before_products();
-        if (tid == 0) {
-            multiply(acc0, Operand{tk, kRows, false}, Operand{tx, NB, true}, PB, nsteps, false);
-            for (int k = 2; k >= 0; --k)
-                multiply(acc1, Operand{tv, kRows, false}, Operand{tx + k * M::kState, NB, false}, NB, psteps, k < 2);
-            bar_after_products(&sh.bar);
-        }
-        products_done();
+        fetch_states(from_s);
+        products_done(0);
         if (cb < PB / 32) {
             float x[32];
             tmem_load(acc0 + mine + 32 * cb, x);
+            if constexpr (!M::kFirst) tmem_load(acc_d + mine + 32 * cb, dv);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = fmaf(tail, x[e], dv[e]);
-            put32(tv, row, cb, x);   // V is read
+            for (int e = 0; e < 32; ++e) x[e] = fmaf(tail, dv[e], x[e]);
+            put<32>(tv, row, 4 * cb, x);   // V is read
         }
-        // the state before the chunk, and its product with the adjoint behind it
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            const int id = tid + kGradThreads * u;
-            fetch_state(from_s, id % NB, id / NB, a.N, a.P, st[u]);
-        }
-        const auto take = [&](unsigned sums, float by, unsigned tile) {   // adds acc1's rows times `by`; their products with the tile's
-            float x[32], t[32], of = 0.f;
-            tmem_load(acc1 + mine + 32 * cb, x);
-            tmem_load(sums + mine + 32 * cb, t);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float f[8];
-                unpack8(ld_tile(tile, tile_at(kRows, row, 4 * cb + i)), f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float y = x[8 * i + e] * by;
-                    of = fmaf(y, f[e], of);
-                    t[8 * i + e] += y;
-                }
-            }
-            tmem_store(sums + mine + 32 * cb, t);
-            return of;
-        };
-        float of = 0.f;
-        if (cb < NB / 32) of = take(acc_k, tail, tk);
-        add_blocks(sh.key, of, NB / 32, true);
-        float dot = 0.f;
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            const int id = tid + kGradThreads * u;
-            const unsigned at = tile_at(NB, id % NB, id / NB);
-            float d[3][8];
-#pragma unroll
-            for (int k = 0; k < 3; ++k) unpack8(ld_tile(tx + k * M::kState, at), d[k]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dot = fmaf(st[u][e], d[0][e] + (d[1][e] + d[2][e]), dot);
-        }
-        put_state();   // each thread where it has just read
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
-        if (lane == 0) sh.dots[warp] = dot;
+        if constexpr (M::kFirst) __syncthreads();   // the sums of the weights are read
+        put_states();   // the adjoint's pieces and the weights are read
         before_products();
         if (tid == 0) {
-            for (int k = 2; k >= 0; --k)
-                multiply(acc1, Operand{to, kRows, false}, Operand{tx + k * M::kState, NB, false}, NB, psteps, k < 2);
-            bar_after_products(&sh.bar);
+            if constexpr (M::kFirst) {
+                with_pieces(acc1, to);
+            } else {
+                with_pieces(acc0, to);   // acc1 is read by now
+            }
+            bar_after_products(&sh.done[0]);
+        }
+        float of = 0.f;
+        if constexpr (!M::kFirst) {
+            if (cb < NB / 32) of = take(acc1, acc_k, tail, tk, true);
+            add_blocks(sh.key, of, NB / 32, true);
         }
         store_rows<PP, kGradThreads, VEC>(static_cast<bf16_t *>(a.dv) + (ch.row * a.H + h) * a.P, int64_t(a.H) * a.P, tv, ch.len, a.P);
-        products_done();
+        products_done(0);
         of = 0.f;
-        if (cb < NB / 32) of = take(acc_q, a.scale * up, tq);
+        if (cb < NB / 32) of = take(M::kFirst ? acc1 : acc0, acc_q, a.scale * up, tq, true);
         add_blocks(sh.after, of, NB / 32, false);
         if (warp == 0) {   // dg: four rows a lane
             float x[4], z[4], after = 0.f, before = 0.f, whole = 0.f;
@@ -748,7 +962,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const TcCa
             const float right = __shfl_down_sync(~0u, after, 1), left = __shfl_up_sync(~0u, before, 1);
             after = lane < 31 ? right : 0.f, before = lane > 0 ? left : 0.f;   // of the lanes behind and before
             for (int w = 0; w < 16; ++w) whole += sh.dots[w];
-            whole *= Gates128::exp_of(sh.g.hi[kRows - 1] + sh.g.lo[kRows - 1]);
+            whole *= Gates128::exp_of(sh.w.g.hi[kRows - 1] + sh.w.g.lo[kRows - 1]);
             float suffix[4];
 #pragma unroll
             for (int i = 3; i >= 0; --i) suffix[i] = after += x[i];
@@ -761,17 +975,16 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const TcCa
             }
         }
     }
-    // dq and dk
+    // dq and dk: through the weights' place
     __syncthreads();
     tmem_after_sync();
-    const unsigned acc_q = acc + 256, acc_k = acc + 384;
     if (cb < NB / 32) {
         float x[32];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             tmem_load((k == 0 ? acc_q : acc_k) + mine + 32 * cb, x);
             if (p.splits == 1) {
-                put32(tx + k * M::kW, row, cb, x);
+                put<32>(tw + k * M::kW, row, 4 * cb, x);
             } else {
                 const int quads = (a.N + 3) / 4;
                 float *to_part = p.partial + (((int64_t(split) * p.c.most + c) * a.G + grp) * 2 + k) * quads * kRows * 4;
@@ -785,21 +998,22 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const TcCa
     tmem_before_sync();
     __syncthreads();
     if (p.splits == 1) {
-        store_rows<PN, kGradThreads, VEC>(static_cast<bf16_t *>(a.dq) + (ch.row * a.G + grp) * a.N, int64_t(a.G) * a.N, tx, ch.len, a.N);
-        store_rows<PN, kGradThreads, VEC>(static_cast<bf16_t *>(a.dk) + (ch.row * a.G + grp) * a.N, int64_t(a.G) * a.N, tx + M::kW, ch.len, a.N);
+        store_rows<PN, kGradThreads, VEC>(static_cast<bf16_t *>(a.dq) + (ch.row * a.G + grp) * a.N, int64_t(a.G) * a.N, tw, ch.len, a.N);
+        store_rows<PN, kGradThreads, VEC>(static_cast<bf16_t *>(a.dk) + (ch.row * a.G + grp) * a.N, int64_t(a.G) * a.N, tw + M::kW, ch.len, a.N);
     }
-    if (warp == 0) tmem_free(acc, 512);
+    if (warp == 0) tmem_free(acc0, 512);
 }
 
 // dq and dk of a chunk and group from the parts of its heads: a thread a row's
 // quad, in the parts' order.
-__global__ void __launch_bounds__(256) gated_join_rows_kernel(const TcCall p)
+constexpr int kJoinBlocks = 8;   // for a chunk and group
+__global__ void __launch_bounds__(256) gated_join_rows_kernel(const __grid_constant__ TcCall p)
 {
     const GatedArgs &a = p.a;
-    const int quads = (a.N + 3) / 4, grp = int(blockIdx.x % a.G);
-    const int64_t c = blockIdx.x / a.G;
+    const int quads = (a.N + 3) / 4, grp = int(blockIdx.x / kJoinBlocks % a.G);
+    const int64_t c = blockIdx.x / kJoinBlocks / a.G;
     const Chunks::One ch = p.c.get(c);
-    for (int id = threadIdx.x; id < 2 * quads * kRows; id += 256) {
+    for (int id = int(blockIdx.x % kJoinBlocks) * 256 + threadIdx.x; id < 2 * quads * kRows; id += kJoinBlocks * 256) {
         const int k = id / (quads * kRows), quad = id / kRows % quads, row = id % kRows;
         if (row >= ch.len) continue;
         float v[4] = {};
@@ -822,19 +1036,27 @@ __global__ void __launch_bounds__(256) gated_join_rows_kernel(const TcCall p)
 
 // ------------------------------------------------------------------- host
 
-// Chunks of a segment: few enough for about two blocks an SM over all segments.
-int segment_chunks(int64_t chunks, int H, int P)
+// Chunks of a segment.  Two walks run on an SM, in rounds of a segment's chunks
+// and about one and a half more for a block's beginning and end.
+int segment_chunks(int64_t chunks, int64_t nseq, int H, int P)
 {
-    const int64_t walks = chunks * H * ceil_div(P, 64), want = 2 * 152;
-    const int64_t m = walks / want;
-    return int(m < 1 ? 1 : m > 64 ? 64 : m);
+    const int64_t blocks = H * ceil_div(P, 64), each = ceil_div(chunks, nseq > 0 ? nseq : 1);
+    int best = 1;
+    double least = 1e300;
+    for (int m = 1; m <= 64; ++m) {
+        const double t = double(ceil_div(nseq * ceil_div(each, m) * blocks, 2 * 152)) * (m + 1.5);
+        if (t < least * 0.999) least = t, best = m;
+    }
+    return best;
 }
 
 // Blocks for a group's heads: the gradients' blocks run one on an SM, in rounds
 // of a block's heads and about half a head's time for the group's own tiles.
-int grad_splits(int64_t chunks, int H, int G)
+// Above 64 values of both kinds a block takes one head.
+int grad_splits(int64_t chunks, int H, int G, int N, int P)
 {
     const int per = H / G;
+    if (N > 64 && P > 64) return per;
     int best = 1;
     double least = 1e300;
     for (int heads = per; heads >= 1; --heads) {
@@ -856,9 +1078,9 @@ Plan plan_of(int64_t B, int64_t T, int H, int G, int N, int P, int64_t nseq, boo
     Plan w{};
     const size_t state = size_t(state_size(N, P)) * 4;
     w.chunks = chunks_most(B, T, nseq, packed, kRows);
-    w.m = segment_chunks(w.chunks, H, P);
+    w.m = segment_chunks(w.chunks, nseq, H, P);
     w.segments = chunks_most(B, T, nseq, packed, kRows * w.m);
-    w.splits = bwd ? grad_splits(w.chunks, H, G) : 1;
+    w.splits = bwd ? grad_splits(w.chunks, H, G, N, P) : 1;
     const size_t table = packed ? align_up(size_t(nseq + 1) * 4, 256) : 0;
     w.first = kControlBytes, w.seg_first = w.first + table;
     w.totals = w.seg_first + table;
@@ -885,7 +1107,8 @@ mg_status over_segments(const TcCall &p, const float *from, float *to, cudaStrea
 template <int PN, bool VEC, bool BACK>
 mg_status walk(const TcCall &p, cudaStream_t s)
 {
-    constexpr size_t smem = 2 * PN * kRows * 128 + 3 * kRows * 128 + 2 * sizeof(Gates128) + 32;
+    constexpr size_t smem = 2 * PN * kRows * 128 + 3 * kRows * 128 + sizeof(WalkSmall);
+    static_assert(2 * (smem + 1024) <= 228 * 1024 || PN == 1, "two blocks an SM");
     MG_TRY((allow_shared<gated_walk_kernel<PN, VEC, BACK>>(smem)));
     const int tiles = int(ceil_div(p.a.P, 64));
     gated_walk_kernel<PN, VEC, BACK><<<unsigned(p.seg.most * p.a.H * tiles), kWalkThreads, smem, s>>>(p, tiles);
@@ -897,7 +1120,8 @@ mg_status forward(const TcCall &p, cudaStream_t s)
 {
     MG_TRY((walk<PN, VEC, false>(p, s)));
     MG_TRY(over_segments<false>(p, p.a.S0, p.a.S_last, s));
-    constexpr size_t smem = 2 * kRows * 128 + (PN > PP ? PN : PP) * kRows * 128 + PP * PN * 64 * 128 + sizeof(Gates128) + 32;
+    constexpr size_t smem = 2 * kPanelBytes + (PN > PP ? PN : PP) * kPanelBytes + PP * PN * 64 * 128 + sizeof(RowsSmall);
+    static_assert(2 * (smem + 1024) <= 228 * 1024, "two blocks an SM");
     MG_TRY((allow_shared<gated_rows_kernel<PN, PP, VEC>>(smem)));
     gated_rows_kernel<PN, PP, VEC><<<unsigned(p.c.most * p.a.H), kRowThreads, smem, s>>>(p);
     return launched("mg_gated_scan_fwd");
@@ -908,13 +1132,22 @@ mg_status backward(const TcCall &p, cudaStream_t s)
 {
     MG_TRY((walk<PN, VEC, true>(p, s)));
     MG_TRY(over_segments<true>(p, p.a.dS_last, p.a.dS0, s));
-    constexpr size_t smem = GradSmem<PN, PP>::bytes;
+    constexpr size_t smem = Grad<PN, PP>::bytes;
+    static_assert(smem <= 227 * 1024, "one block an SM");
     MG_TRY((allow_shared<gated_grads_kernel<PN, PP, VEC>, 227 * 1024>(smem)));
     gated_grads_kernel<PN, PP, VEC><<<unsigned(p.c.most * p.a.G * p.splits), kGradThreads, smem, s>>>(p);
     MG_TRY(launched("mg_gated_scan_bwd"));
     if (p.splits == 1) return MG_OK;
-    gated_join_rows_kernel<<<unsigned(p.c.most * p.a.G), 256, 0, s>>>(p);
+    gated_join_rows_kernel<<<unsigned(p.c.most * p.a.G * kJoinBlocks), 256, 0, s>>>(p);
     return launched("mg_gated_scan_bwd");
+}
+
+// Whole 16-byte pieces where every row and head begins and ends on such a
+// boundary; row numbers of copies are 32-bit.
+bool by_pieces(const GatedArgs &a)
+{
+    const int64_t all = a.N | a.P | a.ldq | a.ldk | a.ldv | (a.dout != nullptr ? a.lddo : 0);
+    return all % 8 == 0 && a.B * a.T <= INT32_MAX - kRows;
 }
 
 mg_status make_call(const GatedArgs &a, bool bwd, TcCall &p, cudaStream_t s)
@@ -939,18 +1172,17 @@ mg_status make_call(const GatedArgs &a, bool bwd, TcCall &p, cudaStream_t s)
     p.splits = w.splits, p.heads = int(ceil_div(a.H / a.G, w.splits));
     p.error = &reinterpret_cast<Control *>(a.ws)->error;
     MG_TRY(check_grids(bwd ? "mg_gated_scan_bwd" : "mg_gated_scan_fwd",
-                       {w.chunks * a.H, w.segments * a.H * ceil_div(a.P, 64), w.chunks * a.G * w.splits,
+                       {w.chunks * a.H, w.segments * a.H * ceil_div(a.P, 64), w.chunks * a.G * (w.splits > 1 && w.splits < kJoinBlocks ? kJoinBlocks : w.splits),
                         a.nseq * a.H * ceil_div(int64_t((a.P + 3) / 4) * a.N, 256)}));
+    if (by_pieces(a)) {
+        const int64_t rows = a.B * a.T;
+        MG_TRY(rows_map(&p.q, a.q, rows, a.G, a.N, a.ldq));
+        MG_TRY(rows_map(&p.k, a.k, rows, a.G, a.N, a.ldk));
+        MG_TRY(rows_map(&p.v, a.v, rows, a.H, a.P, a.ldv));
+        if (bwd) MG_TRY(rows_map(&p.dout, a.dout, rows, a.H, a.P, a.lddo));
+    }
     if (!packed) return MG_OK;
     return launch_chunk_tables(p.c, p.seg, a.ws, s);
-}
-
-// Copies of 16 bytes where every row and head begins on such a boundary and
-// ends on one.
-bool by_pieces(const GatedArgs &a)
-{
-    const int64_t all = a.N | a.P | a.ldq | a.ldk | a.ldv | (a.dout != nullptr ? a.lddo : 0);
-    return all % 8 == 0;
 }
 
 #define MG_GATED_TC(F)                                                  \

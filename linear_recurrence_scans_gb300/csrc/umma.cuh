@@ -2,6 +2,8 @@
 // tensor memory (tcgen05): tiles, descriptors, waits.
 #pragma once
 
+#include <cuda.h>
+
 #include "ssm.cuh"
 
 namespace mg {
@@ -32,6 +34,31 @@ __device__ __forceinline__ void copy16(unsigned to, const void *from, bool on)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" : : "r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
 }
+// A tensor of rows, heads of `cols` bf16 values in each, rows `ld` values apart,
+// for copies of a head's 64 columns of 128 rows: a panel of a tile, zeros where
+// columns or rows lie outside the tensor.  The address and all strides are
+// multiples of 16 bytes.
+mg_status rows_map(CUtensorMap *map, const void *base, int64_t rows, int64_t heads, int64_t cols, int64_t ld);
+
+constexpr unsigned kPanelBytes = 128 * 128;
+
+__device__ __forceinline__ void copy_panel(unsigned to, const CUtensorMap &map, int col, int head, int row, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+                 : : "r"(to), "l"(&map), "r"(col), "r"(head), "r"(row), "r"(smem_addr(bar)) : "memory");
+}
+template <int PANELS>
+__device__ __forceinline__ void copy_tile(unsigned to, const CUtensorMap &map, int head, int row, uint64_t *bar)
+{
+#pragma unroll
+    for (int i = 0; i < PANELS; ++i) copy_panel(to + i * kPanelBytes, map, 64 * i, head, row, bar);
+}
+// The one arrival of a barrier's phase, which ends when the bytes have come too.
+__device__ __forceinline__ void bar_expect(uint64_t *bar, unsigned bytes)
+{
+    asm volatile("{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" : : "r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+
 // Makes this thread's writes to shared memory seen by the tensor core.
 __device__ __forceinline__ void fence_tiles() { asm volatile("fence.proxy.async.shared::cta;" : : : "memory"); }
 
@@ -134,6 +161,18 @@ __device__ __forceinline__ void tmem_load(unsigned at, float (&v)[32])
     asm volatile("tcgen05.wait::ld.sync.aligned;" : : : "memory");
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_load(unsigned at, float (&v)[16])
+{
+    unsigned r[16];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(at) : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : : : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tmem_store(unsigned at, const float (&v)[32])
 {
