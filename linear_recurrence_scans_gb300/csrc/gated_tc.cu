@@ -190,10 +190,10 @@ struct alignas(64) TcCall {
     unsigned *error;
 };
 
-// Where a chunk's state comes from.
+// Where a chunk's state comes from: local + e^reach carry.
 struct Source {
     const float *local, *carry;   // NULL: nothing from there
-    float by;
+    const float *reach;
 };
 template <bool BACK>
 __device__ __forceinline__ Source source_of(const TcCall &p, const Chunks::One &ch, int64_t c, int h)
@@ -206,12 +206,13 @@ __device__ __forceinline__ Source source_of(const TcCall &p, const Chunks::One &
     Source s;
     s.local = first ? nullptr : w.local + (c * p.a.H + h) * size;
     s.carry = !from_outside && seg == (BACK ? last : 0) ? nullptr : w.carry + ((p.seg.begin(ch.seq) + seg) * p.a.H + h) * size;
-    s.by = expf(w.reach[c * p.a.H + h]);
+    s.reach = w.reach + c * p.a.H + h;
     return s;
 }
 
-// 8 values of a state's row n from column 8 piece on.
-__device__ __forceinline__ void fetch_state(const Source &s, int n, int piece, int N, int P, float (&v)[8])
+// 8 values of a state's row n from column 8 piece on; by = e^reach.
+__device__ __forceinline__ float reach_of(const Source &s) { return s.carry != nullptr ? expf(__ldg(s.reach)) : 0.f; }
+__device__ __forceinline__ void fetch_state(const Source &s, float by, int n, int piece, int N, int P, float (&v)[8])
 {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
@@ -222,7 +223,7 @@ __device__ __forceinline__ void fetch_state(const Source &s, int n, int piece, i
             if (s.local != nullptr) x = __ldg(reinterpret_cast<const float4 *>(s.local + at));
             if (s.carry != nullptr) {
                 const float4 y = __ldg(reinterpret_cast<const float4 *>(s.carry + at));
-                x.x = fmaf(s.by, y.x, x.x), x.y = fmaf(s.by, y.y, x.y), x.z = fmaf(s.by, y.z, x.z), x.w = fmaf(s.by, y.w, x.w);
+                x.x = fmaf(by, y.x, x.x), x.y = fmaf(by, y.y, x.y), x.z = fmaf(by, y.z, x.z), x.w = fmaf(by, y.w, x.w);
             }
         }
         v[4 * q] = x.x, v[4 * q + 1] = x.y, v[4 * q + 2] = x.z, v[4 * q + 3] = x.w;
@@ -516,11 +517,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
     }
     {   // the state, rounded: an operand of bf16 outputs
         const Source s = source_of<false>(p, ch, c, h);
+        const float by = reach_of(s);
 #pragma unroll
         for (int u = 0; u < NB * PP * 8 / kRowThreads; ++u) {
             const int id = tid + kRowThreads * u, n = id % NB, piece = id / NB;
             float f[8];
-            fetch_state(s, n, piece, a.N, a.P, f);
+            fetch_state(s, by, n, piece, a.N, a.P, f);
             st_tile(ts, tile_at(NB, n, piece), make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
         }
     }
@@ -621,7 +623,10 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
 // SM; the adjoint's and the state's pieces share a place (kX), which for N and
 // P above 64 is the weights' too.
 
-constexpr int kGradThreads = 512;
+constexpr int kGradThreads = 1024;
+// The warp that begins the products: rows 0 to 31 and columns 112 on, which have
+// no weights.
+constexpr int kMmaWarp = 28;
 
 template <int PN, int PP>
 struct Grad {
@@ -634,20 +639,22 @@ struct Grad {
     static constexpr unsigned kTiles = 2 * kQ + 2 * kV + (kFirst ? kX : 2 * kW + kX);
     struct Small {
         Weights w;
-        float after[kRows], key[kRows], dots[16];
+        float after[kRows], key[kRows], dots[32];
         uint64_t full[2], done[2];
         unsigned tmem;
-        float parts[kFirst ? 1 : 8 * kRows];   // sums of the weights, by blocks of 32 columns and of rows
+        float parts[kFirst ? 1 : 12 * kRows];   // sums by blocks of 16 columns and of 32 rows
     };
     static constexpr size_t bytes = kTiles + sizeof(Small);
 };
 
-// Sums over a warp's 32 rows: lane l gets column l's.
-__device__ __forceinline__ float column_sums(float (&w)[32])
+// Sums over a warp's 32 rows: lanes l and l + 16 get column l's.
+__device__ __forceinline__ float column_sums(float (&w)[16])
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int k = 0; k < 16; ++k) w[k] += __shfl_xor_sync(~0u, w[k], 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1)
 #pragma unroll
         for (int k = 0; k < o; ++k) {
             const bool up = lane & o;
@@ -668,7 +675,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
     const unsigned tx = M::kFirst ? tw : tdw + M::kW;
     auto &sh = *reinterpret_cast<typename M::Small *>(sm + M::kTiles);
     // beside the weights where they share their place with the pieces
-    float *row_part = M::kFirst ? reinterpret_cast<float *>(sm + 2 * M::kQ + 2 * M::kV + 2 * M::kW) : sh.parts, *col_part = row_part + 4 * kRows;
+    float *row_part = M::kFirst ? reinterpret_cast<float *>(sm + 2 * M::kQ + 2 * M::kV + 2 * M::kW) : sh.parts, *col_part = row_part + 8 * kRows;
+    float *key_part = M::kFirst ? col_part + 4 * kRows : row_part;
 
     const int split = int(blockIdx.x % p.splits), grp = int(blockIdx.x / p.splits % a.G);
     const int64_t c = int64_t(blockIdx.x) / p.splits / a.G;
@@ -710,26 +718,26 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         __syncthreads();
         tmem_after_sync();
     };
-    // adds the column blocks' sums v of each row to to[row], block after block
-    const auto add_blocks = [&](float *sums, float v, int blocks, bool fresh) {
-        for (int b = 0; b < blocks; ++b) {
-            if (cb == b) sums[row] = (b == 0 && fresh ? 0.f : sums[row]) + v;
-            __syncthreads();
-        }
+    // the sum of a row's parts, block after block
+    const auto of_blocks = [&](const float *part, int blocks) {
+        float v = 0.f;
+        for (int b = 0; b < blocks; ++b) v += part[b * kRows + tid];
+        return v;
     };
-    constexpr int kUnits = NB * PP * 8 / kGradThreads;
+    constexpr int kPieces = NB * PP * 8, kUnits = (kPieces + kGradThreads - 1) / kGradThreads;
     float st[kUnits][8];
-    const auto fetch_states = [&](const Source &from) {
+    const auto fetch_states = [&](const Source &from, float by) {
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int id = tid + kGradThreads * u;
-            fetch_state(from, id % NB, id / NB, a.N, a.P, st[u]);
+            if (id < kPieces) fetch_state(from, by, id % NB, id / NB, a.N, a.P, st[u]);
         }
     };
     const auto put_states = [&]() {   // as three pieces
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
             const int id = tid + kGradThreads * u;
+            if (id >= kPieces) continue;
             unsigned x[3][4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -747,12 +755,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
     };
     // Rows of `from` times `by`, added to those of `sums` (or in their place); their products with the tile's rows.
     const auto take = [&](unsigned from, unsigned sums, float by, unsigned tile, bool add) {
-        float x[32], of = 0.f;
-        tmem_load(from + mine + 32 * cb, x);
+        float x[16], of = 0.f;
+        tmem_load(from + mine + 16 * cb, x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             float f[8];
-            unpack8(ld_tile(tile, tile_at(kRows, row, 4 * cb + i)), f);
+            unpack8(ld_tile(tile, tile_at(kRows, row, 2 * cb + i)), f);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 x[8 * i + e] *= by;
@@ -760,15 +768,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             }
         }
         if (add) {
+            float t[16];
+            tmem_load(sums + mine + 16 * cb, t);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float t[16];
-                tmem_load(sums + mine + 32 * cb + 16 * half, t);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[16 * half + e] += t[e];
-            }
+            for (int e = 0; e < 16; ++e) x[e] += t[e];
         }
-        tmem_store(sums + mine + 32 * cb, x);
+        tmem_store(sums + mine + 16 * cb, x);
         return of;
     };
     for (int hh = h0; hh < h1; ++hh) {
@@ -783,22 +788,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             load_rows<PP, kGradThreads>(tv, static_cast<const bf16_t *>(a.v) + ch.row * a.ldv + h * a.P, a.ldv, ch.len, a.P);
             load_rows<PP, kGradThreads>(to, static_cast<const bf16_t *>(a.dout) + ch.row * a.lddo + h * a.P, a.lddo, ch.len, a.P);
         }
-        if (warp == 0) {
-            float g[4];
-            fetch_gates(g, a.g + ch.row * a.ldg + h, a.ldg, ch.len);
-            sum_gates(g, sh.w.g);
-            sh.w.fill();
-        }
+        float g[4];
+        if (warp == kMmaWarp) fetch_gates(g, a.g + ch.row * a.ldg + h, a.ldg, ch.len);
         const Source from_d = source_of<true>(p, ch, c, h), from_s = source_of<false>(p, ch, c, h);
+        const float by_d = reach_of(from_d), by_s = reach_of(from_s);
         // <S, D>: both in registers, D then stays
         float dot = 0.f;
         {
-            fetch_states(from_d);
+            fetch_states(from_d, by_d);
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
                 const int id = tid + kGradThreads * u;
+                if (id >= kPieces) continue;
                 float s[8];
-                fetch_state(from_s, id % NB, id / NB, a.N, a.P, s);
+                fetch_state(from_s, by_s, id % NB, id / NB, a.N, a.P, s);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) dot = fmaf(s[e], st[u][e], dot);
             }
@@ -811,7 +814,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             const int gn = hh + 1 < h1 ? grp : int(next / p.splits % a.G), hn = hh + 1 < h1 ? h + 1 : gn * per_group + int(next % p.splits) * p.heads;
             const Chunks::One n = hh + 1 < h1 ? ch : cn < p.c.most ? p.c.get(cn) : Chunks::One{0, 0, 0, 0};
             const int what = tid >> 7, r = tid & 127;
-            if (r < n.len) {
+            if (what < 4 && r < n.len) {
                 if (what == 0) to_l2(static_cast<const bf16_t *>(a.v) + (n.row + r) * a.ldv + hn * a.P, 2 * a.P);
                 if (what == 1) to_l2(static_cast<const bf16_t *>(a.dout) + (n.row + r) * a.lddo + hn * a.P, 2 * a.P);
                 if (what == 2 && hh + 1 == h1) to_l2(static_cast<const bf16_t *>(a.q) + (n.row + r) * a.ldq + gn * a.N, 2 * a.N);
@@ -821,6 +824,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
                     if (f.local != nullptr) to_l2(f.local, unsigned(state_size(a.N, a.P) * 4));
                 }
             }
+        }
+        if (warp == kMmaWarp) {
+            sum_gates(g, sh.w.g);
+            sh.w.fill();
         }
         put_states();
         if constexpr (VEC) {
@@ -834,7 +841,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         before_products();
         acc0 = sh.tmem, acc1 = acc0 + 128, acc_q = acc0 + 256, acc_k = acc_q + NB;
         acc_d = M::kFirst ? acc_q : PB == 64 ? acc0 + 64 : acc_k + NB;   // K D
-        if (tid == 0) {
+        if (tid == 32 * kMmaWarp) {
             multiply(acc0, Operand{tq, kRows, false}, Operand{tk, kRows, false}, kRows, nsteps, false);
             multiply(acc1, Operand{to, kRows, false}, Operand{tv, kRows, false}, kRows, psteps, false);
             bar_after_products(&sh.done[0]);
@@ -847,62 +854,56 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         const float hi = sh.w.g.hi[row], lo = sh.w.g.lo[row];
         const float tail = sh.w.g.span(sh.w.g.hi[kRows - 1], sh.w.g.lo[kRows - 1], row), up = Gates128::exp_of(hi + lo);
         products_done(0);
-        // weights, and what each pair of rows gives to the gates between them
+        // weights, and what each pair of rows gives to the gates between them: rows
+        // from 32 rb, columns from 16 cb
         float of_row = 0.f, of_col = 0.f;
-        unsigned pw[16], pd[16];
-        if (cb <= rb) {
-            float both[32];
-            const float from = a.scale * sh.w.g.span(hi, lo, 32 * cb + 31);
+        unsigned pw[8], pd[8];
+        if (cb <= 2 * rb + 1) {
+            float s[16], d[16];
+            tmem_load(acc0 + mine + 16 * cb, s);
+            tmem_load(acc1 + mine + 16 * cb, d);
+            const int first = 16 * cb - 32 * rb;   // columns up to lane - first reach the row
+            const float from = a.scale * (first < 0 ? sh.w.g.span(hi, lo, 32 * (cb >> 1) + 31) : 1.f);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float s[16], d[16];
-                tmem_load(acc0 + mine + 32 * cb + 16 * half, s);
-                tmem_load(acc1 + mine + 32 * cb + 16 * half, d);
+            for (int e = 0; e < 16; e += 2) {
+                float w[2];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int j = 16 * half + e;
-                    if (cb < rb) {
-                        const float by = from * sh.w.to_end[32 * cb + j];
-                        d[e] *= by;
-                        both[j] = s[e] * d[e];
-                        s[e] *= by;
-                    } else {
-                        const float by = j <= lane ? a.scale * sh.w.g.span(hi, lo, 32 * cb + j) : 0.f;
-                        d[e] = j <= lane ? d[e] * by : 0.f;
-                        both[j] = j < lane ? s[e] * d[e] : 0.f;
-                        s[e] = j <= lane ? s[e] * by : 0.f;
-                    }
-                    of_row += both[j];
+                for (int u = 0; u < 2; ++u) {
+                    const int j = e + u;
+                    float by = from * (first < 0 ? sh.w.to_end[16 * cb + j] : sh.w.g.span(hi, lo, 16 * cb + j));
+                    const bool in = first < 0 || first + j <= lane;
+                    w[u] = in ? s[j] * by : 0.f, d[j] = in ? d[j] * by : 0.f;
+                    s[j] = first < 0 || first + j < lane ? s[j] * d[j] : 0.f;
+                    of_row += s[j];
                 }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) pw[8 * half + e] = pack_bf16x2(s[2 * e], s[2 * e + 1]), pd[8 * half + e] = pack_bf16x2(d[2 * e], d[2 * e + 1]);
+                pw[e / 2] = pack_bf16x2(w[0], w[1]), pd[e / 2] = pack_bf16x2(d[e], d[e + 1]);
             }
-            of_col = column_sums(both);
+            of_col = column_sums(s);
         } else {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) pw[e] = pd[e] = 0;
+            for (int e = 0; e < 8; ++e) pw[e] = pd[e] = 0;
         }
         const auto put_weights = [&]() {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                st_tile(tw, tile_at(kRows, row, 4 * cb + i), make_uint4(pw[4 * i], pw[4 * i + 1], pw[4 * i + 2], pw[4 * i + 3]));
-                st_tile(tdw, tile_at(kRows, row, 4 * cb + i), make_uint4(pd[4 * i], pd[4 * i + 1], pd[4 * i + 2], pd[4 * i + 3]));
+            for (int i = 0; i < 2; ++i) {
+                st_tile(tw, tile_at(kRows, row, 2 * cb + i), make_uint4(pw[4 * i], pw[4 * i + 1], pw[4 * i + 2], pw[4 * i + 3]));
+                st_tile(tdw, tile_at(kRows, row, 2 * cb + i), make_uint4(pd[4 * i], pd[4 * i + 1], pd[4 * i + 2], pd[4 * i + 3]));
             }
             row_part[cb * kRows + row] = of_row;
-            col_part[rb * kRows + 32 * cb + lane] = of_col;
+            if (lane < 16) col_part[rb * kRows + 16 * cb + lane] = of_col;
         };
-        float dv[32];   // K D's part of dv
+        float dv[16];   // K D's part of dv
         if constexpr (M::kFirst) {
             products_done(1);
             const float of = take(acc_k, acc_k, tail, tk, false);
-            tmem_load(acc_d + mine + 32 * cb, dv);
+            tmem_load(acc_d + mine + 16 * cb, dv);
             put_weights();   // the adjoint's pieces are read
-            add_blocks(sh.key, of, NB / 32, true);
+            key_part[cb * kRows + row] = of;
         } else {
             put_weights();
         }
         before_products();
-        if (tid == 0) {
+        if (tid == 32 * kMmaWarp) {
             const bool add = hh > h0;
             multiply(acc0, Operand{tw, kRows, true}, Operand{to, kRows, true}, PB, kRows / 16, false);
             multiply(acc_q, Operand{tdw, kRows, false}, Operand{tk, kRows, true}, NB, kRows / 16, add);
@@ -914,41 +915,40 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             bar_after_products(&sh.done[0]);
         }
         if (tid < kRows) {
-            float x = 0.f;
-            for (int b = 0; b < 4; ++b) x += row_part[b * kRows + tid] - col_part[b * kRows + tid];
-            sh.after[tid] = x;
+            sh.after[tid] = of_blocks(row_part, 8) - of_blocks(col_part, 4);
+            if constexpr (M::kFirst) sh.key[tid] = of_blocks(key_part, 8);
         }
-        fetch_states(from_s);
+        fetch_states(from_s, by_s);
         products_done(0);
-        if (cb < PB / 32) {
-            float x[32];
-            tmem_load(acc0 + mine + 32 * cb, x);
-            if constexpr (!M::kFirst) tmem_load(acc_d + mine + 32 * cb, dv);
+        if (cb < PB / 16) {
+            float x[16];
+            tmem_load(acc0 + mine + 16 * cb, x);
+            if constexpr (!M::kFirst) tmem_load(acc_d + mine + 16 * cb, dv);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = fmaf(tail, dv[e], x[e]);
-            put<32>(tv, row, 4 * cb, x);   // V is read
+            for (int e = 0; e < 16; ++e) x[e] = fmaf(tail, dv[e], x[e]);
+            put<16>(tv, row, 2 * cb, x);   // V is read
         }
-        if constexpr (M::kFirst) __syncthreads();   // the sums of the weights are read
+        if constexpr (M::kFirst) __syncthreads();   // the parts of the sums are read
         put_states();   // the adjoint's pieces and the weights are read
         before_products();
-        if (tid == 0) {
-            if constexpr (M::kFirst) {
-                with_pieces(acc1, to);
-            } else {
-                with_pieces(acc0, to);   // acc1 is read by now
-            }
+        if (tid == 32 * kMmaWarp) {
+            with_pieces(M::kFirst ? acc1 : acc0, to);   // what was in these is read
             bar_after_products(&sh.done[0]);
         }
-        float of = 0.f;
         if constexpr (!M::kFirst) {
-            if (cb < NB / 32) of = take(acc1, acc_k, tail, tk, true);
-            add_blocks(sh.key, of, NB / 32, true);
+            if (cb < NB / 16) key_part[cb * kRows + row] = take(acc1, acc_k, tail, tk, true);
         }
         store_rows<PP, kGradThreads, VEC>(static_cast<bf16_t *>(a.dv) + (ch.row * a.H + h) * a.P, int64_t(a.H) * a.P, tv, ch.len, a.P);
         products_done(0);
-        of = 0.f;
-        if (cb < NB / 32) of = take(M::kFirst ? acc1 : acc0, acc_q, a.scale * up, tq, true);
-        add_blocks(sh.after, of, NB / 32, false);
+        if constexpr (!M::kFirst) {
+            __syncthreads();
+            if (tid < kRows) sh.key[tid] = of_blocks(key_part, NB / 16);
+            __syncthreads();
+        }
+        if (cb < NB / 16) row_part[cb * kRows + row] = take(M::kFirst ? acc1 : acc0, acc_q, a.scale * up, tq, true);
+        __syncthreads();
+        if (tid < kRows) sh.after[tid] += of_blocks(row_part, NB / 16);
+        __syncthreads();
         if (warp == 0) {   // dg: four rows a lane
             float x[4], z[4], after = 0.f, before = 0.f, whole = 0.f;
 #pragma unroll
@@ -961,7 +961,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             }
             const float right = __shfl_down_sync(~0u, after, 1), left = __shfl_up_sync(~0u, before, 1);
             after = lane < 31 ? right : 0.f, before = lane > 0 ? left : 0.f;   // of the lanes behind and before
-            for (int w = 0; w < 16; ++w) whole += sh.dots[w];
+            for (int w = 0; w < 32; ++w) whole += sh.dots[w];
             whole *= Gates128::exp_of(sh.w.g.hi[kRows - 1] + sh.w.g.lo[kRows - 1]);
             float suffix[4];
 #pragma unroll
@@ -978,20 +978,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
     // dq and dk: through the weights' place
     __syncthreads();
     tmem_after_sync();
-    if (cb < NB / 32) {
-        float x[32];
+    if (cb < NB / 16) {
+        float x[16];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            tmem_load((k == 0 ? acc_q : acc_k) + mine + 32 * cb, x);
+            tmem_load((k == 0 ? acc_q : acc_k) + mine + 16 * cb, x);
             if (p.splits == 1) {
-                put<32>(tw + k * M::kW, row, 4 * cb, x);
+                put<16>(tw + k * M::kW, row, 2 * cb, x);
             } else {
                 const int quads = (a.N + 3) / 4;
                 float *to_part = p.partial + (((int64_t(split) * p.c.most + c) * a.G + grp) * 2 + k) * quads * kRows * 4;
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    if (8 * cb + q < quads)
-                        *reinterpret_cast<float4 *>(to_part + (int64_t(8 * cb + q) * kRows + row) * 4) = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+                for (int q = 0; q < 4; ++q)
+                    if (4 * cb + q < quads)
+                        *reinterpret_cast<float4 *>(to_part + (int64_t(4 * cb + q) * kRows + row) * 4) = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
             }
         }
     }
@@ -1043,6 +1043,9 @@ int segment_chunks(int64_t chunks, int64_t nseq, int H, int P)
     const int64_t blocks = H * ceil_div(P, 64), each = ceil_div(chunks, nseq > 0 ? nseq : 1);
     int best = 1;
     double least = 1e300;
+#ifdef MG_GATED_M
+    return MG_GATED_M;
+#endif
     for (int m = 1; m <= 64; ++m) {
         const double t = double(ceil_div(nseq * ceil_div(each, m) * blocks, 2 * 152)) * (m + 1.5);
         if (t < least * 0.999) least = t, best = m;
