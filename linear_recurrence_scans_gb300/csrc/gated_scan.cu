@@ -190,8 +190,7 @@ __global__ void __launch_bounds__(kThreads) gated_add_kernel(const GatedCall p)
     extern __shared__ float sm[];
     __shared__ Gates gates;
     const GatedArgs &a = p.a;
-    const int64_t c = blockIdx.x / a.H;
-    const int h = int(blockIdx.x % a.H), grp = h / (a.H / a.G);
+    const int c = int(blockIdx.x / unsigned(a.H)), h = int(blockIdx.x % unsigned(a.H)), grp = h / (a.H / a.G);
     const Chunks::One ch = p.c.get(c);
     if (ch.len == 0) return;
     float *K = sm, *V = sm + kL * NB;
@@ -206,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) gated_add_kernel(const GatedCall p)
     float acc[NB / 16][PB / 16];
     clear(acc);
     mm<NB / 16, PB / 16, 1, NB, PB, 1>(acc, K, V, ch.len);
-    float *out = (BACK ? p.adjoints : p.states) + (c * a.H + h) * a.N * a.P;
+    float *out = (BACK ? p.adjoints : p.states) + (int64_t(c) * a.H + h) * a.N * a.P;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
 #pragma unroll
     for (int i = 0; i < NB / 16; ++i)
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) gated_add_kernel(const GatedCall p)
             const int n = ty + 16 * i, q = tx + 16 * j;
             if (n < a.N && q < a.P) out[n * a.P + q] = acc[i][j];
         }
-    if (threadIdx.x == 0) p.totals[c * a.H + h] = gates.hi[kL - 1];
+    if (threadIdx.x == 0) p.totals[int64_t(c) * a.H + h] = gates.hi[kL - 1];
 }
 
 // o of a chunk and head.
@@ -226,8 +225,7 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(const GatedCall p)
     __shared__ Gates gates;
     constexpr int LN = NB + 1, LP = kL + 1, KN = LN > LP ? LN : LP;
     const GatedArgs &a = p.a;
-    const int64_t c = blockIdx.x / a.H;
-    const int h = int(blockIdx.x % a.H), grp = h / (a.H / a.G);
+    const int c = int(blockIdx.x / unsigned(a.H)), h = int(blockIdx.x % unsigned(a.H)), grp = h / (a.H / a.G);
     const Chunks::One ch = p.c.get(c);
     if (ch.len == 0) return;
     float *Q = sm, *K = Q + kL * LN, *V = K + kL * KN, *W = K;   // weights take K's place
@@ -251,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(const GatedCall p)
     // Q S, straight from the state (L2): its rows are read by 16 lanes at once
     float acc[4][PB / 16];
     clear(acc);
-    const float *S = p.states + (c * a.H + h) * a.N * a.P;
+    const float *S = p.states + (int64_t(c) * a.H + h) * a.N * a.P;
 #pragma unroll 4
     for (int n = 0; n < a.N; ++n) {
         float x[4], y[PB / 16];
@@ -301,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
     constexpr int LN = NB + 1, LV = PB + 1, LP = kL + 1, HN = NB < 64 ? NB : 64, NJ = NB / 16, HJ = HN / 16, PJ = PB / 16;
     const GatedArgs &a = p.a;
     const int split = int(blockIdx.x % p.splits), grp = int(blockIdx.x / p.splits % a.G);
-    const int64_t c = int64_t(blockIdx.x) / p.splits / a.G;
+    const int c = int(blockIdx.x / unsigned(p.splits) / unsigned(a.G));
     const Chunks::One ch = p.c.get(c);
     if (ch.len == 0) return;
     float *Q = sm, *K = Q + kL * LN, *V = K + kL * LN, *dO = V + kL * LV, *W = dO + kL * LV, *dW = W + kL * LP, *St = dW + kL * LP;
@@ -352,7 +350,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
         clear(dv), clear(in_d);
         mm<4, PJ, 1, LP, LV, 1>(dv, W, dO, kL);
         float of_q[4] = {}, of_k[4] = {}, dot = 0.f;
-        const float *S = p.states + (c * a.H + h) * a.N * a.P, *D = p.adjoints + (c * a.H + h) * a.N * a.P;
+        const float *S = p.states + (int64_t(c) * a.H + h) * a.N * a.P, *D = p.adjoints + (int64_t(c) * a.H + h) * a.N * a.P;
 #pragma unroll
         for (int n0 = 0; n0 < NB; n0 += HN) {
             const int rows = a.N - n0 < HN ? a.N - n0 : HN;   // below 1: none
@@ -531,7 +529,7 @@ template <int NB, int PB>
 mg_status fwd_sized(const GatedCall &p, cudaStream_t s)
 {
     const GatedArgs &a = p.a;
-    const int64_t blocks = p.c.most * a.H;
+    const int64_t blocks = int64_t(p.c.most) * a.H;
     constexpr int LN = NB + 1, KN = LN > kL + 1 ? LN : kL + 1;
     constexpr size_t add = size_t(kL) * (NB + PB) * 4, out = size_t(kL) * (LN + KN + PB) * 4;
     MG_TRY((allow_shared<gated_add_kernel<NB, PB, false>, kRoom>(add)));
@@ -547,7 +545,7 @@ template <int NB, int PB>
 mg_status bwd_sized(const GatedCall &p, cudaStream_t s)
 {
     const GatedArgs &a = p.a;
-    const int64_t blocks = p.c.most * a.H, grads = p.c.most * a.G * p.splits;
+    const int64_t blocks = int64_t(p.c.most) * a.H, grads = int64_t(p.c.most) * a.G * p.splits;
     constexpr size_t add = size_t(kL) * (NB + PB) * 4;
     constexpr size_t grad = size_t(kL) * (2 * (NB + 1) + 2 * (PB + 1) + 2 * (kL + 1)) * 4 + size_t(NB < 64 ? NB : 64) * (PB + 1) * 4;
     MG_TRY((allow_shared<gated_add_kernel<NB, PB, true>, kRoom>(add)));
@@ -585,7 +583,7 @@ mg_status make_call(const GatedArgs &a, bool bwd, GatedCall &p)
     p.a = a;
     p.c.q = make_seqs(a.cu, a.B, a.T, a.nseq);
     p.c.first = reinterpret_cast<const int *>(ws + w.first);
-    p.c.per = int(ceil_div(a.T, kL)), p.c.L = kL, p.c.most = w.chunks;
+    p.c.per = int(ceil_div(a.T, kL)), p.c.L = kL, p.c.most = int(w.chunks);
     p.totals = reinterpret_cast<float *>(ws + w.totals);
     float *states = reinterpret_cast<float *>(ws + w.states);
     p.states = bwd ? const_cast<float *>(a.saved_in) : a.saved != nullptr ? a.saved : states;

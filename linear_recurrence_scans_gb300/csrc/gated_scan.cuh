@@ -19,19 +19,19 @@ struct Chunks {
     Seqs q;
     const int *first;
     int per, L;
-    long long most;   // chunks that buffers have room for
+    int most;   // chunks that buffers have room for
 
     struct One {
         long long row;
         int len, seq, idx;   // rows, sequence, place in it
     };
     // Chunk c; len 0: there is none.
-    __device__ __forceinline__ One get(long long c) const
+    __device__ __forceinline__ One get(int c) const
     {
         One o{0, 0, 0, 0};
         if (q.cu == nullptr) {
-            o.seq = int(c / per);
-            o.idx = int(c - (long long)o.seq * per);
+            o.seq = int(unsigned(c) / unsigned(per));
+            o.idx = c - o.seq * per;
             const long long at = (long long)o.idx * L;
             o.row = (long long)o.seq * q.T + at;
             o.len = int(q.T - at < L ? q.T - at : L);
@@ -44,14 +44,14 @@ struct Chunks {
             if (__ldg(first + mid) <= c) lo = mid; else hi = mid;
         }
         o.seq = lo;
-        o.idx = int(c - __ldg(first + lo));
+        o.idx = c - __ldg(first + lo);
         o.row = __ldg(q.cu + lo) + (long long)o.idx * L;
         const long long left = __ldg(q.cu + lo + 1) - o.row;
         o.len = int(left < L ? left : L);
         return o;
     }
-    __device__ __forceinline__ long long begin(int s) const { return q.cu == nullptr ? (long long)s * per : __ldg(first + s); }
-    __device__ __forceinline__ long long end(int s) const { return begin(s + 1); }
+    __device__ __forceinline__ int begin(int s) const { return q.cu == nullptr ? s * per : __ldg(first + s); }
+    __device__ __forceinline__ int end(int s) const { return begin(s + 1); }
 };
 
 // The most chunks that a batch can have.

@@ -168,7 +168,7 @@ __device__ __forceinline__ void unpack8(uint4 v, float (&f)[8])
 
 // States between the kernels lie as [P / 4][N][4] (zeros beyond P): a lane a
 // row of the accumulators, neighbouring lanes 16 bytes apart.
-__host__ __device__ constexpr int64_t state_size(int N, int P) { return int64_t((P + 3) / 4) * N * 4; }
+__host__ __device__ constexpr int state_size(int N, int P) { return (P + 3) / 4 * N * 4; }
 
 // A walk's results, for the states or for their adjoints.
 struct Walked {
@@ -187,27 +187,37 @@ struct alignas(64) TcCall {
     float *partial;
     int splits, heads;
     bool starts;     // the first segments' carries may hold start states
+    int state;       // values of a state
+    int next_c, next_h;   // chunks and heads from a block to the one that follows on its SM
     unsigned *error;
 };
 
-// Where a chunk's state comes from: local + e^reach carry.
+// Where a chunk's states come from, local + e^reach carry, but for the head.
+struct Place {
+    int c, seg;          // chunk, its segment
+    bool local, carry;   // whether there is anything
+};
+template <bool BACK>
+__device__ __forceinline__ Place place_of(const TcCall &p, const Chunks::One &ch, int c)
+{
+    const int begin = p.c.begin(ch.seq), count = p.c.end(ch.seq) - begin, seg = int(unsigned(ch.idx) / unsigned(p.m)), in = ch.idx - seg * p.m;
+    Place o;
+    o.c = c, o.seg = p.seg.begin(ch.seq) + seg;
+    o.local = BACK ? ch.idx != count - 1 && in != p.m - 1 : in != 0;
+    o.carry = BACK ? p.a.dS_last != nullptr || (seg + 1) * p.m < count : p.starts || seg > 0;
+    return o;
+}
 struct Source {
     const float *local, *carry;   // NULL: nothing from there
     const float *reach;
 };
 template <bool BACK>
-__device__ __forceinline__ Source source_of(const TcCall &p, const Chunks::One &ch, int64_t c, int h)
+__device__ __forceinline__ Source source_of(const TcCall &p, const Place &o, int h)
 {
     const Walked &w = BACK ? p.d : p.s;
-    const int64_t size = state_size(p.a.N, p.a.P);
-    const int count = int(p.c.end(ch.seq) - p.c.begin(ch.seq)), last = (count - 1) / p.m, seg = ch.idx / p.m;
-    const bool first = BACK ? ch.idx == count - 1 || ch.idx % p.m == p.m - 1 : ch.idx % p.m == 0;
-    const bool from_outside = BACK ? p.a.dS_last != nullptr : p.starts;
-    Source s;
-    s.local = first ? nullptr : w.local + (c * p.a.H + h) * size;
-    s.carry = !from_outside && seg == (BACK ? last : 0) ? nullptr : w.carry + ((p.seg.begin(ch.seq) + seg) * p.a.H + h) * size;
-    s.reach = w.reach + c * p.a.H + h;
-    return s;
+    const int64_t at = int64_t(o.c) * p.a.H + h;
+    return Source{o.local ? w.local + at * p.state : nullptr,
+                  o.carry ? w.carry + (int64_t(o.seg) * p.a.H + h) * p.state : nullptr, w.reach + at};
 }
 
 // 8 values of a state's row n from column 8 piece on; by = e^reach.
@@ -219,7 +229,7 @@ __device__ __forceinline__ void fetch_state(const Source &s, float by, int n, in
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
         const int quad = 2 * piece + q;
         if (n < N && quad * 4 < P) {
-            const int64_t at = (int64_t(quad) * N + n) * 4;
+            const int at = (quad * N + n) * 4;
             if (s.local != nullptr) x = __ldg(reinterpret_cast<const float4 *>(s.local + at));
             if (s.carry != nullptr) {
                 const float4 y = __ldg(reinterpret_cast<const float4 *>(s.carry + at));
@@ -259,15 +269,15 @@ __global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const __gri
     using Small = WalkSmall;
     Small &sh = *reinterpret_cast<Small *>(sm + 2 * kK + 3 * kV);
 
-    const int tile = int(blockIdx.x % tiles), h = int(blockIdx.x / tiles % a.H), grp = h / (a.H / a.G);
-    const int64_t sg = int64_t(blockIdx.x) / tiles / a.H;
+    const unsigned of = blockIdx.x / unsigned(tiles);
+    const int tile = int(blockIdx.x % unsigned(tiles)), h = int(of % unsigned(a.H)), grp = h / (a.H / a.G), sg = int(of / unsigned(a.H));
     const Chunks::One s = p.seg.get(sg);
     if (s.len == 0) return;
     const Walked &w = BACK ? p.d : p.s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int p0 = tile * 64, cols = a.P - p0 < 64 ? a.P - p0 : 64;
     const int count = (s.len + kRows - 1) / kRows;
-    const int64_t c0 = p.c.begin(s.seq) + int64_t(s.idx) * p.m, size = state_size(a.N, a.P);
+    const int c0 = p.c.begin(s.seq) + s.idx * p.m, size = p.state;
     const bf16_t *kk = static_cast<const bf16_t *>(BACK ? a.q : a.k) + grp * a.N;   // where K is loaded value by value
     const bf16_t *vv = static_cast<const bf16_t *>(BACK ? a.dout : a.v) + h * a.P + p0;
     const int64_t ldk = BACK ? a.ldq : a.ldk, ldv = BACK ? a.lddo : a.ldv;
@@ -325,7 +335,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const __gri
 #pragma unroll
         for (int q = 0; q < 8; ++q)
             if (n < a.N && (quad0 + q) * 4 < a.P)
-                *reinterpret_cast<float4 *>(to + (int64_t(quad0 + q) * a.N + n) * 4) = make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
+                *reinterpret_cast<float4 *>(to + ((quad0 + q) * a.N + n) * 4) = make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
     };
     float reach = 0.f;
     for (int i = 0; i < count; ++i) {
@@ -335,7 +345,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const __gri
             wait_or_tell(&sh.full[i & 1], (i >> 1) & 1, p.error);
             if (left < kRows) clear_rows<PN, kWalkThreads>(base + (i & 1) * kK, left);
         }
-        const int64_t ch = (c0 + chunk_at(i)) * a.H + h;
+        const int64_t ch = int64_t(c0 + chunk_at(i)) * a.H + h;
         if (tid == 0 && tile == 0) w.reach[ch] = reach;
         if (i > 0) put(w.local + ch * size);
         const float whole = sh.whole, whole_lo = sh.whole_lo;
@@ -381,8 +391,8 @@ __global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const __gri
 #pragma unroll
         for (int e = 0; e < 32; ++e) S[e] = fmaf(decay, S[e], add[e]);
     }
-    put(w.carry + (sg * a.H + h) * size);
-    if (tid == 0 && tile == 0) w.totals[sg * a.H + h] = reach;
+    put(w.carry + (int64_t(sg) * a.H + h) * size);
+    if (tid == 0 && tile == 0) w.totals[int64_t(sg) * a.H + h] = reach;
     tmem_before_sync();
     __syncthreads();
     if (warp == 0) tmem_free(sh.tmem, 64);
@@ -398,9 +408,10 @@ __global__ void __launch_bounds__(256) over_segments_kernel(const Chunks seg, co
                                                             int H, int N, int P, int blocks_per)
 {
     constexpr int kAhead = 8;
-    const int64_t sh = blockIdx.x / blocks_per;   // sequence and head
-    const int seq = int(sh / H), h = int(sh % H);
-    const int at = int(blockIdx.x % blocks_per) * 256 + threadIdx.x, quads = (P + 3) / 4;
+    const unsigned su = blockIdx.x / unsigned(blocks_per);   // sequence and head
+    const int seq = int(su / unsigned(H)), h = int(su % unsigned(H));
+    const int64_t sh = su;
+    const int at = int(blockIdx.x % unsigned(blocks_per)) * 256 + threadIdx.x, quads = (P + 3) / 4;
     if (at >= quads * N) return;
     const int n = at % N, p0 = at / N * 4, cols = P - p0 < 4 ? P - p0 : 4;
     const int64_t size = state_size(N, P), out = (sh * N + n) * P + p0;
@@ -490,8 +501,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
     const unsigned tq = smem_addr(sm), tk = tq + kQ, ts = tk + kK;
     using Small = RowsSmall;
     Small &sh = *reinterpret_cast<Small *>(sm + kQ + kK + kS);
-    const int64_t c = blockIdx.x / a.H;
-    const int h = int(blockIdx.x % a.H), grp = h / (a.H / a.G);
+    const int c = int(blockIdx.x / unsigned(a.H)), h = int(blockIdx.x % unsigned(a.H)), grp = h / (a.H / a.G);
     const Chunks::One ch = p.c.get(c);
     if (ch.len == 0) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rb = warp & 3, cb = warp >> 2, row = 32 * rb + lane;
@@ -516,7 +526,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
         load_rows<PN, kRowThreads>(tk, static_cast<const bf16_t *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
     }
     {   // the state, rounded: an operand of bf16 outputs
-        const Source s = source_of<false>(p, ch, c, h);
+        const Source s = source_of<false>(p, place_of<false>(p, ch, c), h);
         const float by = reach_of(s);
 #pragma unroll
         for (int u = 0; u < NB * PP * 8 / kRowThreads; ++u) {
@@ -527,17 +537,17 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
         }
     }
     if constexpr (VEC) {   // what the block that follows on this SM will read: 128 threads an operand
-        const int64_t next = int64_t(blockIdx.x) + 2 * 152, cn = next / a.H;
-        const int hn = int(next % a.H), what = tid >> 7, r = tid & 127;
-        if (cn < p.c.most) {
+        const int wrap = h + p.next_h >= a.H, cn = c + p.next_c + wrap, hn = h + p.next_h - (wrap ? a.H : 0), what = tid >> 7, r = tid & 127;
+        if (cn < p.c.most && (what < 3 || r == 0)) {
             const Chunks::One n = p.c.get(cn);
             if (r < n.len) {
-                if (what == 0) to_l2(static_cast<const bf16_t *>(a.q) + (n.row + r) * a.ldq + hn / (a.H / a.G) * a.N, 2 * a.N);
-                if (what == 1) to_l2(static_cast<const bf16_t *>(a.k) + (n.row + r) * a.ldk + hn / (a.H / a.G) * a.N, 2 * a.N);
+                const int gn = hn / (a.H / a.G);
+                if (what == 0) to_l2(static_cast<const bf16_t *>(a.q) + (n.row + r) * a.ldq + gn * a.N, 2 * a.N);
+                if (what == 1) to_l2(static_cast<const bf16_t *>(a.k) + (n.row + r) * a.ldk + gn * a.N, 2 * a.N);
                 if (what == 2) to_l2(static_cast<const bf16_t *>(a.v) + (n.row + r) * a.ldv + hn * a.P, 2 * a.P);
-                if (what == 3 && r == 0) {
-                    const Source f = source_of<false>(p, n, cn, hn);
-                    if (f.local != nullptr) to_l2(f.local, unsigned(state_size(a.N, a.P) * 4));
+                if (what == 3) {
+                    const Source f = source_of<false>(p, place_of<false>(p, n, cn), hn);
+                    if (f.local != nullptr) to_l2(f.local, unsigned(p.state) * 4);
                 }
             }
         }
@@ -678,10 +688,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
     float *row_part = M::kFirst ? reinterpret_cast<float *>(sm + 2 * M::kQ + 2 * M::kV + 2 * M::kW) : sh.parts, *col_part = row_part + 8 * kRows;
     float *key_part = M::kFirst ? col_part + 4 * kRows : row_part;
 
-    const int split = int(blockIdx.x % p.splits), grp = int(blockIdx.x / p.splits % a.G);
-    const int64_t c = int64_t(blockIdx.x) / p.splits / a.G;
+    const unsigned of_c = blockIdx.x / unsigned(p.splits);
+    const int split = int(blockIdx.x % unsigned(p.splits)), grp = int(of_c % unsigned(a.G)), c = int(of_c / unsigned(a.G));
     const Chunks::One ch = p.c.get(c);
     if (ch.len == 0) return;
+    const Place place_d = place_of<true>(p, ch, c), place_s = place_of<false>(p, ch, c);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rb = warp & 3, cb = warp >> 2, row = 32 * rb + lane;
     const int per_group = a.H / a.G, h0 = split * p.heads, h1 = h0 + p.heads < per_group ? h0 + p.heads : per_group;
     const auto copy_head = [&](int h) {   // V and dO
@@ -790,7 +801,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         }
         float g[4];
         if (warp == kMmaWarp) fetch_gates(g, a.g + ch.row * a.ldg + h, a.ldg, ch.len);
-        const Source from_d = source_of<true>(p, ch, c, h), from_s = source_of<false>(p, ch, c, h);
+        const Source from_d = source_of<true>(p, place_d, h), from_s = source_of<false>(p, place_s, h);
         const float by_d = reach_of(from_d), by_s = reach_of(from_s);
         // <S, D>: both in registers, D then stays
         float dot = 0.f;
@@ -810,18 +821,25 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
         if (lane == 0) sh.dots[warp] = dot;
         if constexpr (VEC) {   // the rows of the next head: of this block, or of the block that follows on the SM
-            const int64_t next = int64_t(blockIdx.x) + 152, cn = hh + 1 < h1 ? c : next / p.splits / a.G;
-            const int gn = hh + 1 < h1 ? grp : int(next / p.splits % a.G), hn = hh + 1 < h1 ? h + 1 : gn * per_group + int(next % p.splits) * p.heads;
-            const Chunks::One n = hh + 1 < h1 ? ch : cn < p.c.most ? p.c.get(cn) : Chunks::One{0, 0, 0, 0};
             const int what = tid >> 7, r = tid & 127;
-            if (what < 4 && r < n.len) {
-                if (what == 0) to_l2(static_cast<const bf16_t *>(a.v) + (n.row + r) * a.ldv + hn * a.P, 2 * a.P);
-                if (what == 1) to_l2(static_cast<const bf16_t *>(a.dout) + (n.row + r) * a.lddo + hn * a.P, 2 * a.P);
-                if (what == 2 && hh + 1 == h1) to_l2(static_cast<const bf16_t *>(a.q) + (n.row + r) * a.ldq + gn * a.N, 2 * a.N);
-                if (what == 3 && hh + 1 == h1) to_l2(static_cast<const bf16_t *>(a.k) + (n.row + r) * a.ldk + gn * a.N, 2 * a.N);
-                if (what < 2 && r == 0) {
-                    const Source f = what == 0 ? source_of<true>(p, n, cn, hn) : source_of<false>(p, n, cn, hn);
-                    if (f.local != nullptr) to_l2(f.local, unsigned(state_size(a.N, a.P) * 4));
+            if (hh + 1 < h1) {
+                if (what == 0 && r < ch.len) to_l2(static_cast<const bf16_t *>(a.v) + (ch.row + r) * a.ldv + (h + 1) * a.P, 2 * a.P);
+                if (what == 1 && r < ch.len) to_l2(static_cast<const bf16_t *>(a.dout) + (ch.row + r) * a.lddo + (h + 1) * a.P, 2 * a.P);
+                if (tid == 256 && place_d.local) to_l2(from_d.local + p.state, unsigned(p.state) * 4);
+                if (tid == 288 && place_s.local) to_l2(from_s.local + p.state, unsigned(p.state) * 4);
+            } else if (what < 4) {
+                const unsigned next = blockIdx.x + 152, of_n = next / unsigned(p.splits);
+                const int gn = int(of_n % unsigned(a.G)), cn = int(of_n / unsigned(a.G)), hn = gn * per_group + int(next % unsigned(p.splits)) * p.heads;
+                const Chunks::One n = cn < p.c.most ? p.c.get(cn) : Chunks::One{0, 0, 0, 0};
+                if (r < n.len) {
+                    if (what == 0) to_l2(static_cast<const bf16_t *>(a.v) + (n.row + r) * a.ldv + hn * a.P, 2 * a.P);
+                    if (what == 1) to_l2(static_cast<const bf16_t *>(a.dout) + (n.row + r) * a.lddo + hn * a.P, 2 * a.P);
+                    if (what == 2) to_l2(static_cast<const bf16_t *>(a.q) + (n.row + r) * a.ldq + gn * a.N, 2 * a.N);
+                    if (what == 3) to_l2(static_cast<const bf16_t *>(a.k) + (n.row + r) * a.ldk + gn * a.N, 2 * a.N);
+                    if (what < 2 && r == 0) {
+                        const Source f = what == 0 ? source_of<true>(p, place_of<true>(p, n, cn), hn) : source_of<false>(p, place_of<false>(p, n, cn), hn);
+                        if (f.local != nullptr) to_l2(f.local, unsigned(p.state) * 4);
+                    }
                 }
             }
         }
@@ -1010,8 +1028,7 @@ constexpr int kJoinBlocks = 8;   // for a chunk and group
 __global__ void __launch_bounds__(256) gated_join_rows_kernel(const __grid_constant__ TcCall p)
 {
     const GatedArgs &a = p.a;
-    const int quads = (a.N + 3) / 4, grp = int(blockIdx.x / kJoinBlocks % a.G);
-    const int64_t c = blockIdx.x / kJoinBlocks / a.G;
+    const int quads = (a.N + 3) / 4, grp = int(blockIdx.x / kJoinBlocks % unsigned(a.G)), c = int(blockIdx.x / kJoinBlocks / unsigned(a.G));
     const Chunks::One ch = p.c.get(c);
     for (int id = int(blockIdx.x % kJoinBlocks) * 256 + threadIdx.x; id < 2 * quads * kRows; id += kJoinBlocks * 256) {
         const int k = id / (quads * kRows), quad = id / kRows % quads, row = id % kRows;
@@ -1114,7 +1131,7 @@ mg_status walk(const TcCall &p, cudaStream_t s)
     static_assert(2 * (smem + 1024) <= 228 * 1024 || PN == 1, "two blocks an SM");
     MG_TRY((allow_shared<gated_walk_kernel<PN, VEC, BACK>>(smem)));
     const int tiles = int(ceil_div(p.a.P, 64));
-    gated_walk_kernel<PN, VEC, BACK><<<unsigned(p.seg.most * p.a.H * tiles), kWalkThreads, smem, s>>>(p, tiles);
+    gated_walk_kernel<PN, VEC, BACK><<<unsigned(int64_t(p.seg.most) * p.a.H * tiles), kWalkThreads, smem, s>>>(p, tiles);
     return launched("mg_gated_scan");
 }
 
@@ -1126,7 +1143,7 @@ mg_status forward(const TcCall &p, cudaStream_t s)
     constexpr size_t smem = 2 * kPanelBytes + (PN > PP ? PN : PP) * kPanelBytes + PP * PN * 64 * 128 + sizeof(RowsSmall);
     static_assert(2 * (smem + 1024) <= 228 * 1024, "two blocks an SM");
     MG_TRY((allow_shared<gated_rows_kernel<PN, PP, VEC>>(smem)));
-    gated_rows_kernel<PN, PP, VEC><<<unsigned(p.c.most * p.a.H), kRowThreads, smem, s>>>(p);
+    gated_rows_kernel<PN, PP, VEC><<<unsigned(int64_t(p.c.most) * p.a.H), kRowThreads, smem, s>>>(p);
     return launched("mg_gated_scan_fwd");
 }
 
@@ -1138,10 +1155,10 @@ mg_status backward(const TcCall &p, cudaStream_t s)
     constexpr size_t smem = Grad<PN, PP>::bytes;
     static_assert(smem <= 227 * 1024, "one block an SM");
     MG_TRY((allow_shared<gated_grads_kernel<PN, PP, VEC>, 227 * 1024>(smem)));
-    gated_grads_kernel<PN, PP, VEC><<<unsigned(p.c.most * p.a.G * p.splits), kGradThreads, smem, s>>>(p);
+    gated_grads_kernel<PN, PP, VEC><<<unsigned(int64_t(p.c.most) * p.a.G * p.splits), kGradThreads, smem, s>>>(p);
     MG_TRY(launched("mg_gated_scan_bwd"));
     if (p.splits == 1) return MG_OK;
-    gated_join_rows_kernel<<<unsigned(p.c.most * p.a.G * kJoinBlocks), 256, 0, s>>>(p);
+    gated_join_rows_kernel<<<unsigned(int64_t(p.c.most) * p.a.G * kJoinBlocks), 256, 0, s>>>(p);
     return launched("mg_gated_scan_bwd");
 }
 
@@ -1163,7 +1180,9 @@ mg_status make_call(const GatedArgs &a, bool bwd, TcCall &p, cudaStream_t s)
     p.c.q = p.seg.q = make_seqs(a.cu, a.B, a.T, a.nseq);
     p.c.L = kRows, p.seg.L = kRows * w.m;
     p.c.per = int(ceil_div(a.T, p.c.L)), p.seg.per = int(ceil_div(a.T, p.seg.L));
-    p.c.most = w.chunks, p.seg.most = w.segments;
+    p.c.most = int(w.chunks), p.seg.most = int(w.segments);
+    p.state = state_size(a.N, a.P);
+    p.next_c = 2 * 152 / a.H, p.next_h = 2 * 152 % a.H;   // two blocks of rows on an SM
     p.c.first = reinterpret_cast<const int *>(ws + w.first), p.seg.first = reinterpret_cast<const int *>(ws + w.seg_first);
     const Walked in_ws{at(w.local), at(w.carry), at(w.reach), at(w.totals)};
     float *saved = bwd ? const_cast<float *>(a.saved_in) : a.saved;
