@@ -179,7 +179,7 @@ struct Walked {
 };
 
 struct alignas(64) TcCall {
-    CUtensorMap q, k, v, dout;   // where rows are aligned
+    CUtensorMap q, k, v, dout, o, dq, dk, dv;   // where rows are aligned
     GatedArgs a;
     Chunks c, seg;   // chunks, and segments of m of them
     int m;
@@ -536,20 +536,16 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
             st_tile(ts, tile_at(NB, n, piece), make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
         }
     }
-    if constexpr (VEC) {   // what the block that follows on this SM will read: 128 threads an operand
-        const int wrap = h + p.next_h >= a.H, cn = c + p.next_c + wrap, hn = h + p.next_h - (wrap ? a.H : 0), what = tid >> 7, r = tid & 127;
-        if (cn < p.c.most && (what < 3 || r == 0)) {
-            const Chunks::One n = p.c.get(cn);
-            if (r < n.len) {
-                const int gn = hn / (a.H / a.G);
-                if (what == 0) to_l2(static_cast<const bf16_t *>(a.q) + (n.row + r) * a.ldq + gn * a.N, 2 * a.N);
-                if (what == 1) to_l2(static_cast<const bf16_t *>(a.k) + (n.row + r) * a.ldk + gn * a.N, 2 * a.N);
-                if (what == 2) to_l2(static_cast<const bf16_t *>(a.v) + (n.row + r) * a.ldv + hn * a.P, 2 * a.P);
-                if (what == 3) {
-                    const Source f = source_of<false>(p, place_of<false>(p, n, cn), hn);
-                    if (f.local != nullptr) to_l2(f.local, unsigned(p.state) * 4);
-                }
-            }
+    if (VEC && tid == 64) {   // what the block that follows on this SM will read
+        const int wrap = h + p.next_h >= a.H, cn = c + p.next_c + wrap, hn = h + p.next_h - (wrap ? a.H : 0);
+        const Chunks::One n = cn < p.c.most ? p.c.get(cn) : Chunks::One{0, 0, 0, 0};
+        if (n.len > 0) {
+            const int gn = hn / (a.H / a.G);
+            tile_to_l2<PN>(p.q, gn, int(n.row));
+            tile_to_l2<PN>(p.k, gn, int(n.row));
+            tile_to_l2<PP>(p.v, hn, int(n.row));
+            const Source f = source_of<false>(p, place_of<false>(p, n, cn), hn);
+            if (f.local != nullptr) to_l2(f.local, unsigned(p.state) * 4);
         }
     }
     fence_tiles();
@@ -621,9 +617,17 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
             put<16>(tk, row, 4 * cb + 2 * half, x);
         }
     }
+    fence_tiles();
     tmem_before_sync();
     __syncthreads();
-    store_rows<PP, kRowThreads, VEC>(static_cast<bf16_t *>(a.o) + (ch.row * a.H + h) * a.P, int64_t(a.H) * a.P, tk, ch.len, a.P);
+    if (VEC && ch.len == kRows) {
+        if (tid == 32) {
+            put_tile<PP>(p.o, tk, h, int(ch.row));
+            tiles_put();
+        }
+    } else {
+        store_rows<PP, kRowThreads, VEC>(static_cast<bf16_t *>(a.o) + (ch.row * a.H + h) * a.P, int64_t(a.H) * a.P, tk, ch.len, a.P);
+    }
     if (warp == 0) tmem_free(acc, 256);
 }
 
@@ -791,6 +795,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         const int h = grp * per_group + hh;
         if (hh > h0) {   // the head before is done with its tiles
             fence_tiles();
+            if (tid == 32) tiles_put();
             __syncthreads();
         }
         if constexpr (VEC) {
@@ -806,7 +811,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         // <S, D>: both in registers, D then stays
         float dot = 0.f;
         {
-            fetch_states(from_d, by_d);
+            fetch_states(from_d, by_d);   // D
 #pragma unroll
             for (int u = 0; u < kUnits; ++u) {
                 const int id = tid + kGradThreads * u;
@@ -820,26 +825,24 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
         if (lane == 0) sh.dots[warp] = dot;
-        if constexpr (VEC) {   // the rows of the next head: of this block, or of the block that follows on the SM
-            const int what = tid >> 7, r = tid & 127;
+        if (VEC && tid == 64) {   // what comes after this head: the block's next one, or the block that follows on the SM
             if (hh + 1 < h1) {
-                if (what == 0 && r < ch.len) to_l2(static_cast<const bf16_t *>(a.v) + (ch.row + r) * a.ldv + (h + 1) * a.P, 2 * a.P);
-                if (what == 1 && r < ch.len) to_l2(static_cast<const bf16_t *>(a.dout) + (ch.row + r) * a.lddo + (h + 1) * a.P, 2 * a.P);
-                if (tid == 256 && place_d.local) to_l2(from_d.local + p.state, unsigned(p.state) * 4);
-                if (tid == 288 && place_s.local) to_l2(from_s.local + p.state, unsigned(p.state) * 4);
-            } else if (what < 4) {
+                tile_to_l2<PP>(p.v, h + 1, int(ch.row));
+                tile_to_l2<PP>(p.dout, h + 1, int(ch.row));
+                if (place_d.local) to_l2(from_d.local + p.state, unsigned(p.state) * 4);
+                if (place_s.local) to_l2(from_s.local + p.state, unsigned(p.state) * 4);
+            } else {
                 const unsigned next = blockIdx.x + 152, of_n = next / unsigned(p.splits);
                 const int gn = int(of_n % unsigned(a.G)), cn = int(of_n / unsigned(a.G)), hn = gn * per_group + int(next % unsigned(p.splits)) * p.heads;
                 const Chunks::One n = cn < p.c.most ? p.c.get(cn) : Chunks::One{0, 0, 0, 0};
-                if (r < n.len) {
-                    if (what == 0) to_l2(static_cast<const bf16_t *>(a.v) + (n.row + r) * a.ldv + hn * a.P, 2 * a.P);
-                    if (what == 1) to_l2(static_cast<const bf16_t *>(a.dout) + (n.row + r) * a.lddo + hn * a.P, 2 * a.P);
-                    if (what == 2) to_l2(static_cast<const bf16_t *>(a.q) + (n.row + r) * a.ldq + gn * a.N, 2 * a.N);
-                    if (what == 3) to_l2(static_cast<const bf16_t *>(a.k) + (n.row + r) * a.ldk + gn * a.N, 2 * a.N);
-                    if (what < 2 && r == 0) {
-                        const Source f = what == 0 ? source_of<true>(p, place_of<true>(p, n, cn), hn) : source_of<false>(p, place_of<false>(p, n, cn), hn);
-                        if (f.local != nullptr) to_l2(f.local, unsigned(p.state) * 4);
-                    }
+                if (n.len > 0) {
+                    tile_to_l2<PN>(p.q, gn, int(n.row));
+                    tile_to_l2<PN>(p.k, gn, int(n.row));
+                    tile_to_l2<PP>(p.v, hn, int(n.row));
+                    tile_to_l2<PP>(p.dout, hn, int(n.row));
+                    const Source d = source_of<true>(p, place_of<true>(p, n, cn), hn), f = source_of<false>(p, place_of<false>(p, n, cn), hn);
+                    if (d.local != nullptr) to_l2(d.local, unsigned(p.state) * 4);
+                    if (f.local != nullptr) to_l2(f.local, unsigned(p.state) * 4);
                 }
             }
         }
@@ -956,7 +959,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         if constexpr (!M::kFirst) {
             if (cb < NB / 16) key_part[cb * kRows + row] = take(acc1, acc_k, tail, tk, true);
         }
-        store_rows<PP, kGradThreads, VEC>(static_cast<bf16_t *>(a.dv) + (ch.row * a.H + h) * a.P, int64_t(a.H) * a.P, tv, ch.len, a.P);
+        if (VEC && ch.len == kRows) {
+            if (tid == 32) put_tile<PP>(p.dv, tv, h, int(ch.row));
+        } else {
+            store_rows<PP, kGradThreads, VEC>(static_cast<bf16_t *>(a.dv) + (ch.row * a.H + h) * a.P, int64_t(a.H) * a.P, tv, ch.len, a.P);
+        }
         products_done(0);
         if constexpr (!M::kFirst) {
             __syncthreads();
@@ -1013,12 +1020,19 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             }
         }
     }
+    fence_tiles();
     tmem_before_sync();
     __syncthreads();
-    if (p.splits == 1) {
+    if (p.splits == 1 && VEC && ch.len == kRows) {
+        if (tid == 32) {
+            put_tile<PN>(p.dq, tw, grp, int(ch.row));
+            put_tile<PN>(p.dk, tw + M::kW, grp, int(ch.row));
+        }
+    } else if (p.splits == 1) {
         store_rows<PN, kGradThreads, VEC>(static_cast<bf16_t *>(a.dq) + (ch.row * a.G + grp) * a.N, int64_t(a.G) * a.N, tw, ch.len, a.N);
         store_rows<PN, kGradThreads, VEC>(static_cast<bf16_t *>(a.dk) + (ch.row * a.G + grp) * a.N, int64_t(a.G) * a.N, tw + M::kW, ch.len, a.N);
     }
+    if (tid == 32) tiles_put();
     if (warp == 0) tmem_free(acc0, 512);
 }
 
@@ -1201,7 +1215,14 @@ mg_status make_call(const GatedArgs &a, bool bwd, TcCall &p, cudaStream_t s)
         MG_TRY(rows_map(&p.q, a.q, rows, a.G, a.N, a.ldq));
         MG_TRY(rows_map(&p.k, a.k, rows, a.G, a.N, a.ldk));
         MG_TRY(rows_map(&p.v, a.v, rows, a.H, a.P, a.ldv));
-        if (bwd) MG_TRY(rows_map(&p.dout, a.dout, rows, a.H, a.P, a.lddo));
+        if (bwd) {
+            MG_TRY(rows_map(&p.dout, a.dout, rows, a.H, a.P, a.lddo));
+            MG_TRY(rows_map(&p.dq, a.dq, rows, a.G, a.N, int64_t(a.G) * a.N));
+            MG_TRY(rows_map(&p.dk, a.dk, rows, a.G, a.N, int64_t(a.G) * a.N));
+            MG_TRY(rows_map(&p.dv, a.dv, rows, a.H, a.P, int64_t(a.H) * a.P));
+        } else {
+            MG_TRY(rows_map(&p.o, a.o, rows, a.H, a.P, int64_t(a.H) * a.P));
+        }
     }
     if (!packed) return MG_OK;
     return launch_chunk_tables(p.c, p.seg, a.ws, s);

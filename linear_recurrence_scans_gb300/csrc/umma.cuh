@@ -53,6 +53,28 @@ __device__ __forceinline__ void copy_tile(unsigned to, const CUtensorMap &map, i
 #pragma unroll
     for (int i = 0; i < PANELS; ++i) copy_panel(to + i * kPanelBytes, map, 64 * i, head, row, bar);
 }
+// The same to L2 alone.
+template <int PANELS>
+__device__ __forceinline__ void tile_to_l2(const CUtensorMap &map, int head, int row)
+{
+#pragma unroll
+    for (int i = 0; i < PANELS; ++i)
+        asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
+                     : : "l"(&map), "r"(64 * i), "r"(head), "r"(row) : "memory");
+}
+// A tile's 128 rows to the tensor; columns beyond it are left out.
+template <int PANELS>
+__device__ __forceinline__ void put_tile(const CUtensorMap &map, unsigned from, int head, int row)
+{
+#pragma unroll
+    for (int i = 0; i < PANELS; ++i)
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                     : : "l"(&map), "r"(64 * i), "r"(head), "r"(row), "r"(from + i * kPanelBytes) : "memory");
+    asm volatile("cp.async.bulk.commit_group;" : : : "memory");
+}
+// Until this thread's put_tile have read shared memory.
+__device__ __forceinline__ void tiles_put() { asm volatile("cp.async.bulk.wait_group.read 0;" : : : "memory"); }
+
 // The one arrival of a barrier's phase, which ends when the bytes have come too.
 __device__ __forceinline__ void bar_expect(uint64_t *bar, unsigned bytes)
 {
