@@ -220,25 +220,42 @@ __device__ __forceinline__ Source source_of(const TcCall &p, const Place &o, int
                   o.carry ? w.carry + (int64_t(o.seg) * p.a.H + h) * p.state : nullptr, w.reach + at};
 }
 
-// 8 values of a state's row n from column 8 piece on; by = e^reach.
-__device__ __forceinline__ float reach_of(const Source &s) { return s.carry != nullptr ? expf(__ldg(s.reach)) : 0.f; }
-__device__ __forceinline__ void fetch_state(const Source &s, float by, int n, int piece, int N, int P, float (&v)[8])
+// A thread's pieces of a state, 8 values each: rows and columns of a tile of NB
+// rows, THREADS pieces on in each step (neighbouring lanes, neighbouring rows).
+template <int NB, int PP, int THREADS>
+struct Pieces8 {
+    static constexpr int kAll = NB * PP * 8, kMine = (kAll + THREADS - 1) / THREADS;
+    static __device__ __forceinline__ int row(int u) { return (threadIdx.x + THREADS * u) % NB; }
+    static __device__ __forceinline__ int piece(int u) { return (threadIdx.x + THREADS * u) / NB; }
+    static __device__ __forceinline__ bool mine(int u) { return kAll % THREADS == 0 || threadIdx.x + THREADS * u < kAll; }
+};
+
+// A thread's pieces of local + e^reach carry, zeros beside N and P.
+template <typename S>
+__device__ __forceinline__ void fetch_states(const Source &from, float by, int N, int P, float (&v)[S::kMine][8])
 {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int quad = 2 * piece + q;
-        if (n < N && quad * 4 < P) {
-            const int at = (quad * N + n) * 4;
-            if (s.local != nullptr) x = __ldg(reinterpret_cast<const float4 *>(s.local + at));
-            if (s.carry != nullptr) {
-                const float4 y = __ldg(reinterpret_cast<const float4 *>(s.carry + at));
-                x.x = fmaf(by, y.x, x.x), x.y = fmaf(by, y.y, x.y), x.z = fmaf(by, y.z, x.z), x.w = fmaf(by, y.w, x.w);
+    for (int u = 0; u < S::kMine; ++u)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[u][e] = 0.f;
+    const auto each = [&](const float *base, auto f) {
+#pragma unroll
+        for (int u = 0; u < S::kMine; ++u) {
+            const int n = S::row(u), col = S::piece(u) * 8, at = (2 * S::piece(u) * N + n) * 4;
+            if (S::mine(u) && n < N) {
+                if (col < P) f(*reinterpret_cast<const float4 *>(base + at), v[u], 0);
+                if (col + 4 < P) f(*reinterpret_cast<const float4 *>(base + at + 4 * N), v[u], 4);
             }
         }
-        v[4 * q] = x.x, v[4 * q + 1] = x.y, v[4 * q + 2] = x.z, v[4 * q + 3] = x.w;
-    }
+    };
+    if (from.local != nullptr)
+        each(from.local, [](const float4 x, float (&o)[8], int e) { o[e] = x.x, o[e + 1] = x.y, o[e + 2] = x.z, o[e + 3] = x.w; });
+    if (from.carry != nullptr)
+        each(from.carry, [by](const float4 x, float (&o)[8], int e) {
+            o[e] = fmaf(by, x.x, o[e]), o[e + 1] = fmaf(by, x.y, o[e + 1]), o[e + 2] = fmaf(by, x.z, o[e + 2]), o[e + 3] = fmaf(by, x.w, o[e + 3]);
+        });
 }
+__device__ __forceinline__ float reach_of(const Source &s) { return s.carry != nullptr ? expf(__ldg(s.reach)) : 0.f; }
 
 __device__ __forceinline__ void wait_or_tell(uint64_t *bar, unsigned phase, unsigned *error)
 {
@@ -372,7 +389,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const __gri
         if (tid == 0) {
             tmem_after_sync();
             for (int k = 2; k >= 0; --k)
-                multiply(acc, Operand{base + (i & 1) * kK, kRows, true}, Operand{tv + k * kV, kRows, true}, 64, kRows / 16, k < 2);
+                multiply(acc, Tile<kRows, true>{base + (i & 1) * kK}, Tile<kRows, true>{tv + k * kV}, 64, kRows / 16, k < 2);
             bar_after_products(&sh.bar);
         }
         if (i + 1 < count) {
@@ -527,14 +544,14 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
     }
     {   // the state, rounded: an operand of bf16 outputs
         const Source s = source_of<false>(p, place_of<false>(p, ch, c), h);
-        const float by = reach_of(s);
+        using Mine = Pieces8<NB, PP, kRowThreads>;
+        float f[Mine::kMine][8];
+        fetch_states<Mine>(s, reach_of(s), a.N, a.P, f);
 #pragma unroll
-        for (int u = 0; u < NB * PP * 8 / kRowThreads; ++u) {
-            const int id = tid + kRowThreads * u, n = id % NB, piece = id / NB;
-            float f[8];
-            fetch_state(s, by, n, piece, a.N, a.P, f);
-            st_tile(ts, tile_at(NB, n, piece), make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])));
-        }
+        for (int u = 0; u < Mine::kMine; ++u)
+            if (Mine::mine(u))
+                st_tile(ts, tile_at(NB, Mine::row(u), Mine::piece(u)),
+                        make_uint4(pack_bf16x2(f[u][0], f[u][1]), pack_bf16x2(f[u][2], f[u][3]), pack_bf16x2(f[u][4], f[u][5]), pack_bf16x2(f[u][6], f[u][7])));
     }
     if (VEC && tid == 64) {   // what the block that follows on this SM will read
         const int wrap = h + p.next_h >= a.H, cn = c + p.next_c + wrap, hn = h + p.next_h - (wrap ? a.H : 0);
@@ -557,9 +574,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
         const int steps = (a.N + 15) / 16;
         // rows of K and Q behind the chunk only reach rows and columns that are not used
         if constexpr (VEC) wait_or_tell(&sh.full[0], 0, p.error);
-        multiply(acc, Operand{tq, kRows, false}, Operand{tk, kRows, false}, kRows, steps, false);
+        multiply(acc, Tile<kRows, false>{tq}, Tile<kRows, false>{tk}, kRows, steps, false);
         bar_after_products(&sh.done[0]);
-        multiply(acc_s, Operand{tq, kRows, false}, Operand{ts, NB, true}, PB, steps, false);
+        multiply(acc_s, Tile<kRows, false>{tq}, Tile<NB, true>{ts}, PB, steps, false);
         bar_after_products(&sh.done[1]);
     }
     const float hi = sh.w.g.hi[row], lo = sh.w.g.lo[row];
@@ -600,7 +617,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
     __syncthreads();
     if (tid == 0) {
         tmem_after_sync();
-        multiply(acc, Operand{tq, kRows, false}, Operand{tk, kRows, true}, PB, (ch.len + 15) / 16, false);
+        multiply(acc, Tile<kRows, false>{tq}, Tile<kRows, true>{tk}, PB, (ch.len + 15) / 16, false);
         bar_after_products(&sh.done[0]);
     }
     const float up = Gates128::exp_of(hi + lo);
@@ -739,34 +756,26 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         for (int b = 0; b < blocks; ++b) v += part[b * kRows + tid];
         return v;
     };
-    constexpr int kPieces = NB * PP * 8, kUnits = (kPieces + kGradThreads - 1) / kGradThreads;
-    float st[kUnits][8];
-    const auto fetch_states = [&](const Source &from, float by) {
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            const int id = tid + kGradThreads * u;
-            if (id < kPieces) fetch_state(from, by, id % NB, id / NB, a.N, a.P, st[u]);
-        }
-    };
+    using Mine = Pieces8<NB, PP, kGradThreads>;
+    float st[Mine::kMine][8];
     const auto put_states = [&]() {   // as three pieces
 #pragma unroll
-        for (int u = 0; u < kUnits; ++u) {
-            const int id = tid + kGradThreads * u;
-            if (id >= kPieces) continue;
+        for (int u = 0; u < Mine::kMine; ++u) {
+            if (!Mine::mine(u)) continue;
             unsigned x[3][4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const Pieces q = split3(st[u][2 * e], st[u][2 * e + 1]);
                 x[0][e] = q.a, x[1][e] = q.b, x[2][e] = q.c;
             }
+            const unsigned at = tile_at(NB, Mine::row(u), Mine::piece(u));
 #pragma unroll
-            for (int k = 0; k < 3; ++k)
-                st_tile(tx + k * M::kState, tile_at(NB, id % NB, id / NB), make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]));
+            for (int k = 0; k < 3; ++k) st_tile(tx + k * M::kState, at, make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]));
         }
     };
     const auto with_pieces = [&](unsigned acc, unsigned tile) {   // acc = tile (S or D)^T, the small pieces first
         for (int k = 2; k >= 0; --k)
-            multiply(acc, Operand{tile, kRows, false}, Operand{tx + k * M::kState, NB, false}, NB, psteps, k < 2);
+            multiply(acc, Tile<kRows, false>{tile}, Tile<NB, false>{tx + k * M::kState}, NB, psteps, k < 2);
     };
     // Rows of `from` times `by`, added to those of `sums` (or in their place); their products with the tile's rows.
     const auto take = [&](unsigned from, unsigned sums, float by, unsigned tile, bool add) {
@@ -811,16 +820,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         // <S, D>: both in registers, D then stays
         float dot = 0.f;
         {
-            fetch_states(from_d, by_d);   // D
+            float other[Mine::kMine][8];
+            fetch_states<Mine>(from_d, by_d, a.N, a.P, st);
+            fetch_states<Mine>(from_s, by_s, a.N, a.P, other);
 #pragma unroll
-            for (int u = 0; u < kUnits; ++u) {
-                const int id = tid + kGradThreads * u;
-                if (id >= kPieces) continue;
-                float s[8];
-                fetch_state(from_s, by_s, id % NB, id / NB, a.N, a.P, s);
+            for (int u = 0; u < Mine::kMine; ++u)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dot = fmaf(s[e], st[u][e], dot);
-            }
+                for (int e = 0; e < 8; ++e) dot = fmaf(other[u][e], st[u][e], dot);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
@@ -863,12 +869,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         acc0 = sh.tmem, acc1 = acc0 + 128, acc_q = acc0 + 256, acc_k = acc_q + NB;
         acc_d = M::kFirst ? acc_q : PB == 64 ? acc0 + 64 : acc_k + NB;   // K D
         if (tid == 32 * kMmaWarp) {
-            multiply(acc0, Operand{tq, kRows, false}, Operand{tk, kRows, false}, kRows, nsteps, false);
-            multiply(acc1, Operand{to, kRows, false}, Operand{tv, kRows, false}, kRows, psteps, false);
+            multiply(acc0, Tile<kRows, false>{tq}, Tile<kRows, false>{tk}, kRows, nsteps, false);
+            multiply(acc1, Tile<kRows, false>{to}, Tile<kRows, false>{tv}, kRows, psteps, false);
             bar_after_products(&sh.done[0]);
             if constexpr (M::kFirst) {
                 with_pieces(acc_k, tv);
-                multiply(acc_d, Operand{tk, kRows, false}, Operand{tx, NB, true}, PB, nsteps, false);
+                multiply(acc_d, Tile<kRows, false>{tk}, Tile<NB, true>{tx}, PB, nsteps, false);
                 bar_after_products(&sh.done[1]);
             }
         }
@@ -926,11 +932,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         before_products();
         if (tid == 32 * kMmaWarp) {
             const bool add = hh > h0;
-            multiply(acc0, Operand{tw, kRows, true}, Operand{to, kRows, true}, PB, kRows / 16, false);
-            multiply(acc_q, Operand{tdw, kRows, false}, Operand{tk, kRows, true}, NB, kRows / 16, add);
-            multiply(acc_k, Operand{tdw, kRows, true}, Operand{tq, kRows, true}, NB, kRows / 16, add || M::kFirst);
+            multiply(acc0, Tile<kRows, true>{tw}, Tile<kRows, true>{to}, PB, kRows / 16, false);
+            multiply(acc_q, Tile<kRows, false>{tdw}, Tile<kRows, true>{tk}, NB, kRows / 16, add);
+            multiply(acc_k, Tile<kRows, true>{tdw}, Tile<kRows, true>{tq}, NB, kRows / 16, add || M::kFirst);
             if constexpr (!M::kFirst) {
-                multiply(acc_d, Operand{tk, kRows, false}, Operand{tx, NB, true}, PB, nsteps, false);
+                multiply(acc_d, Tile<kRows, false>{tk}, Tile<NB, true>{tx}, PB, nsteps, false);
                 with_pieces(acc1, tv);
             }
             bar_after_products(&sh.done[0]);
@@ -939,7 +945,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             sh.after[tid] = of_blocks(row_part, 8) - of_blocks(col_part, 4);
             if constexpr (M::kFirst) sh.key[tid] = of_blocks(key_part, 8);
         }
-        fetch_states(from_s, by_s);
+        fetch_states<Mine>(from_s, by_s, a.N, a.P, st);
         products_done(0);
         if (cb < PB / 16) {
             float x[16];

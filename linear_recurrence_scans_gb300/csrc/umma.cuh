@@ -101,6 +101,12 @@ __device__ __forceinline__ constexpr unsigned product(int n, bool a_mn, bool b_m
     return 1u << 4 | 1u << 7 | 1u << 10 | unsigned(a_mn) << 15 | unsigned(b_mn) << 16 | unsigned(n >> 3) << 17 | 8u << 24;
 }
 
+__device__ __forceinline__ void mma(unsigned acc, uint64_t a, uint64_t b, unsigned what)   // adds
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, 1, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 : : "r"(acc), "l"(a), "l"(b), "r"(what) : "memory");
+}
 __device__ __forceinline__ void mma(unsigned acc, uint64_t a, uint64_t b, unsigned what, bool add)
 {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -108,23 +114,29 @@ __device__ __forceinline__ void mma(unsigned acc, uint64_t a, uint64_t b, unsign
                  : : "r"(acc), "l"(a), "l"(b), "r"(what), "r"(unsigned(add)) : "memory");
 }
 
-// An operand tile for the steps of a product, 16 summed values each.
-struct Operand {
-    unsigned base, rows;   // rows of the tile, all of its panels
-    bool mn;
-    // K-major: step k is 32 bytes further in its panel of 4 steps.  Mn-major: 16
-    // rows further.
-    __device__ __forceinline__ uint64_t step(int k) const
-    {
-        return mn ? operand(base + k * 2048, rows * 128) : operand(base + (k >> 2) * rows * 128 + (k & 3) * 32);
-    }
+// An operand tile of R rows (all of its panels) for the steps of a product, 16
+// summed values each.
+template <int R, bool MN>
+struct Tile {
+    static constexpr bool mn = MN;
+    unsigned base;
+    __device__ __forceinline__ uint64_t first() const { return MN ? operand(base, R * 128) : operand(base); }
+    // What step k adds: k-major, 32 bytes in a panel of 4 steps; mn-major, 16 rows.
+    static __device__ __forceinline__ constexpr unsigned step(int k) { return (MN ? k * 2048 : (k >> 2) * R * 128 + (k & 3) * 32) >> 4; }
 };
 
-// acc (128 x n) (+)= A B over `steps` steps; one thread calls it.
-__device__ __forceinline__ void multiply(unsigned acc, Operand a, Operand b, int n, int steps, bool add)
+// acc (128 x n) (+)= A B over `steps` steps, 8 at most; one thread calls it.  A
+// step runs 32 cycles for each 64 columns, so its set-up is two additions (with
+// descriptors built anew for each, products took twice their time).
+template <typename A, typename B>
+__device__ __forceinline__ void multiply(unsigned acc, A a, B b, int n, int steps, bool add)
 {
-    const unsigned what = product(n, a.mn, b.mn);
-    for (int k = 0; k < steps; ++k) mma(acc, a.step(k), b.step(k), what, add || k > 0);
+    const unsigned what = product(n, A::mn, B::mn);
+    const uint64_t x = a.first(), y = b.first();
+    mma(acc, x, y, what, add);
+#pragma unroll
+    for (int k = 1; k < 8; ++k)
+        if (k < steps) mma(acc, x + A::step(k), y + B::step(k), what);
 }
 
 // ---------------------------------------------------- tensor memory, waits
