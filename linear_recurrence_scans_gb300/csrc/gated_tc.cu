@@ -24,7 +24,8 @@ namespace {
 
 constexpr int kRows = 128;   // of a chunk: the rows of a tensor-core product
 
-// A chunk's gate sums as two floats.
+// A chunk's gate sums as two floats.  The forward walk leaves them for the kernels
+// behind it.
 struct Gates128 {
     float hi[kRows], lo[kRows];
     __device__ __forceinline__ float span(float hi_i, float lo_i, int j) const { return exp_of((hi_i - hi[j]) + (lo_i - lo[j])); }
@@ -64,19 +65,12 @@ __device__ __forceinline__ void sum_gates(const float (&g)[4], float (&h)[4], fl
     for (int i = 0; i < 4; ++i)
         if (lane > 0) add_two(h[i], l[i], bh, bl);
 }
-__device__ __forceinline__ void sum_gates(const float (&g)[4], Gates128 &to)
-{
-    float h[4], l[4];
-    sum_gates(g, h, l);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) to.hi[4 * (threadIdx.x & 31) + i] = h[i], to.lo[4 * (threadIdx.x & 31) + i] = l[i];
-}
-__device__ __forceinline__ void fetch_gates(float (&g)[4], const float *from, int64_t ld, int len)
+__device__ __forceinline__ void fetch_gates(float (&g)[8], const float *from, int64_t ld, int len)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * (threadIdx.x & 31) + i;
-        g[i] = r < len ? gate_of(__ldg(from + r * ld)) : 0.f;
+        g[i] = r < len ? __ldg(from + r * ld) : 0.f;   // as they are: nothing waits for them yet
     }
 }
 
@@ -176,6 +170,7 @@ struct Walked {
     float *carry;    // [segments][H][state]: before (behind) the segment
     float *reach;    // [chunks][H]: sum of the gates between the chunk and that end of its segment
     float *totals;   // [segments][H]: of the segment's gates
+    float *sums;     // [chunks][H]: a chunk's Gates128
 };
 
 struct alignas(64) TcCall {
@@ -264,10 +259,10 @@ __device__ __forceinline__ void wait_or_tell(uint64_t *bar, unsigned phase, unsi
 
 // ------------------------------------------------------------------- walk
 // A block: a segment, a head, 64 columns of its state, which stay in registers
-// (row n a lane, 32 columns a thread).  Each chunk adds K^T V~, the row weights
+// (row n a lane, 16 columns a thread).  Each chunk adds K^T V~, the row weights
 // in V~'s three pieces; the next chunk's rows arrive meanwhile.
 
-constexpr int kWalkThreads = 256;
+constexpr int kWalkThreads = 512, kGateWarp = 4;
 
 struct WalkSmall {
     float by[kRows];         // the weights of the chunk's rows
@@ -303,72 +298,104 @@ __global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const __gri
     if (tid == 0) bar_init(&sh.bar), bar_init(&sh.full[0]), bar_init(&sh.full[1]);
     fence_tiles();
     __syncthreads();
-    float g[4];
-    uint4 v[4];
+    uint4 v[2];
     const auto chunk_at = [&](int i) { return BACK ? count - 1 - i : i; };
-    const auto fetch = [&](int i) {   // chunk i of the walk: K into its buffer, V and gates into registers
-        const int ci = chunk_at(i), len = s.len - ci * kRows < kRows ? s.len - ci * kRows : kRows;
+    // chunk i of the walk: K into its buffer, and what comes kFar chunks later to
+    // L2; V into registers
+    constexpr int kFar = 3;
+    const auto copy_k = [&](int i) {
+        if (i >= count) return;
+        const int ci = chunk_at(i);
         const int64_t row = s.row + int64_t(ci) * kRows;
         if constexpr (VEC) {
             if (tid == kWalkThreads - 32) {
                 bar_expect(&sh.full[i & 1], PN * kPanelBytes);
                 copy_tile<PN>(base + (i & 1) * kK, BACK ? p.q : p.k, grp, int(row), &sh.full[i & 1]);
+                if (i + kFar < count) {
+                    const int far = int(s.row) + chunk_at(i + kFar) * kRows;
+                    tile_to_l2<PN>(BACK ? p.q : p.k, grp, far);
+                    tile_to_l2<1>(BACK ? p.dout : p.v, h, far, p0);
+                }
             }
         } else {
-            load_rows<PN, kWalkThreads>(base + (i & 1) * kK, kk + row * ldk, ldk, len, a.N);
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int r = (tid >> 3) + 32 * u;
-            v[u] = fetch_piece<VEC>(vv + (row + r) * ldv, tid & 7, cols, r < len);
+            load_rows<PN, kWalkThreads>(base + (i & 1) * kK, kk + row * ldk, ldk, s.len - ci * kRows < kRows ? s.len - ci * kRows : kRows, a.N);
         }
     };
-    // warp 0: the next chunk's gates, and the weights of the one whose gates it has
-    const auto next_gates = [&](int i) {
+    const auto fetch_v = [&](int i) {
         if (i >= count) return;
         const int ci = chunk_at(i), len = s.len - ci * kRows < kRows ? s.len - ci * kRows : kRows;
-        fetch_gates(g, a.g + (s.row + int64_t(ci) * kRows) * a.ldg + h, a.ldg, len);
+        const bf16_t *from = vv + (s.row + int64_t(ci) * kRows) * ldv;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int r = (tid >> 3) + 64 * u;
+            v[u] = fetch_piece<VEC>(from + r * ldv, tid & 7, cols, r < len);
+        }
     };
-    const auto weigh = [&]() {
+    // One warp, not the one that begins the products: the next chunks' gates (their
+    // sums, where the forward walk has left them), and the weights of the next one.
+    float ahead[2][8];
+    const auto next_gates = [&](int i, float (&to)[8]) {
+        if (i >= count) return;
+        const int ci = chunk_at(i), len = s.len - ci * kRows < kRows ? s.len - ci * kRows : kRows;
+        if constexpr (BACK) {
+            const float *from = p.s.sums + (int64_t(c0 + ci) * a.H + h) * (2 * kRows) + 4 * lane;
+            const float4 x = __ldg(reinterpret_cast<const float4 *>(from)), y = __ldg(reinterpret_cast<const float4 *>(from + kRows));
+            to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w, to[4] = y.x, to[5] = y.y, to[6] = y.z, to[7] = y.w;
+        } else {
+            fetch_gates(to, a.g + (s.row + int64_t(ci) * kRows) * a.ldg + h, a.ldg, len);
+        }
+    };
+    const auto weigh = [&](int i, const float (&of)[8]) {
         float hi[4], lo[4];
-        sum_gates(g, hi, lo);
+        if constexpr (BACK) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) hi[e] = of[e], lo[e] = of[4 + e];
+        } else {
+            const float g[4] = {gate_of(of[0]), gate_of(of[1]), gate_of(of[2]), gate_of(of[3])};
+            sum_gates(g, hi, lo);
+            if (tile == 0) {
+                float *to = w.sums + (int64_t(c0 + chunk_at(i)) * a.H + h) * (2 * kRows) + 4 * lane;
+                store_vec<4>(to, hi), store_vec<4>(to + kRows, lo);
+            }
+        }
         const float th = __shfl_sync(~0u, hi[3], 31), tl = __shfl_sync(~0u, lo[3], 31);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             sh.by[4 * lane + e] = BACK ? a.scale * Gates128::exp_of(hi[e] + lo[e]) : Gates128::exp_of((th - hi[e]) + (tl - lo[e]));
         if (lane == 0) sh.whole = th, sh.whole_lo = tl;
     };
-    fetch(0);
-    if (warp == 0) {
-        next_gates(0);
-        weigh();
-        next_gates(1);
+    copy_k(0);
+    fetch_v(0);
+    if (warp == kGateWarp) {
+        next_gates(0, ahead[0]);
+        next_gates(1, ahead[1]);
+        weigh(0, ahead[0]);
+        next_gates(2, ahead[0]);
     }
-    float S[32];
+    float S[16];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) S[i] = 0.f;
-    const int n = 32 * (warp & 3) + lane, quad0 = p0 / 4 + 8 * (warp >> 2);
+    for (int i = 0; i < 16; ++i) S[i] = 0.f;
+    const int n = 32 * (warp & 3) + lane, quad0 = p0 / 4 + 4 * (warp >> 2);
     const auto put = [&](float *to) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
+        for (int q = 0; q < 4; ++q)
             if (n < a.N && (quad0 + q) * 4 < a.P)
                 *reinterpret_cast<float4 *>(to + ((quad0 + q) * a.N + n) * 4) = make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
     };
     float reach = 0.f;
     for (int i = 0; i < count; ++i) {
-        __syncthreads();   // the weights
+        __syncthreads();   // the weights; the other buffer's products are done
+        copy_k(i + 1);
         if constexpr (VEC) {
             const int left = s.len - chunk_at(i) * kRows;
             wait_or_tell(&sh.full[i & 1], (i >> 1) & 1, p.error);
             if (left < kRows) clear_rows<PN, kWalkThreads>(base + (i & 1) * kK, left);
         }
         const int64_t ch = int64_t(c0 + chunk_at(i)) * a.H + h;
-        if (tid == 0 && tile == 0) w.reach[ch] = reach;
-        if (i > 0) put(w.local + ch * size);
         const float whole = sh.whole, whole_lo = sh.whole_lo;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int r = (tid >> 3) + 32 * u;
+        for (int u = 0; u < 2; ++u) {
+            const int r = (tid >> 3) + 64 * u;
             const float by = sh.by[r];
             float f[8];
             unpack8(v[u], f);
@@ -382,6 +409,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const __gri
             for (int k = 0; k < 3; ++k)
                 st_tile(tv + k * kV, tile_at(kRows, r, tid & 7), make_uint4(x[k][0], x[k][1], x[k][2], x[k][3]));
         }
+        fetch_v(i + 1);
         fence_tiles();
         tmem_before_sync();
         __syncthreads();
@@ -392,21 +420,26 @@ __global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const __gri
                 multiply(acc, Tile<kRows, true>{base + (i & 1) * kK}, Tile<kRows, true>{tv + k * kV}, 64, kRows / 16, k < 2);
             bar_after_products(&sh.bar);
         }
-        if (i + 1 < count) {
-            fetch(i + 1);
-            if (warp == 0) {   // everyone has read this chunk's
-                weigh();
-                next_gates(i + 2);
+        if (i + 1 < count && warp == kGateWarp) {   // everyone has read this chunk's
+            if (i & 1) {
+                weigh(i + 1, ahead[0]);
+                next_gates(i + 3, ahead[0]);
+            } else {
+                weigh(i + 1, ahead[1]);
+                next_gates(i + 3, ahead[1]);
             }
         }
+        // while the products run: the state that came to the chunk
+        if (tid == 0 && tile == 0) w.reach[ch] = reach;
+        if (i > 0) put(w.local + ch * size);
         reach += whole + whole_lo;
         const float decay = expf(whole) * (1.f + whole_lo);
         wait_or_tell(&sh.bar, i & 1, p.error);
         tmem_after_sync();
-        float add[32];
-        tmem_load(acc + (unsigned(32 * (warp & 3)) << 16) + 32 * (warp >> 2), add);
+        float add[16];
+        tmem_load(acc + (unsigned(32 * (warp & 3)) << 16) + 16 * (warp >> 2), add);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) S[e] = fmaf(decay, S[e], add[e]);
+        for (int e = 0; e < 16; ++e) S[e] = fmaf(decay, S[e], add[e]);
     }
     put(w.carry + (int64_t(sg) * a.H + h) * size);
     if (tid == 0 && tile == 0) w.totals[int64_t(sg) * a.H + h] = reach;
@@ -481,13 +514,12 @@ __global__ void __launch_bounds__(256) over_segments_kernel(const Chunks seg, co
 // exponential; the others the product of e^{G_i - G_r} and e^{G_r - G_j}, r the
 // last of j's 32 rows, both at most 1: one exponential a row and block instead
 // of one a pair.
-struct Weights {
+struct alignas(16) Weights {
     Gates128 g;
     float to_end[kRows];   // e^{G_r - G_j}
-    // One warp, after sum_gates.
+    // One warp, once the sums are there.
     __device__ __forceinline__ void fill()
     {
-        __syncwarp();
         for (int b = 0; b < 4; ++b) {
             const int j = 32 * b + (threadIdx.x & 31);
             to_end[j] = g.span(g.hi[32 * b + 31], g.lo[32 * b + 31], j);
@@ -504,7 +536,7 @@ constexpr int kRowThreads = 512;
 
 struct RowsSmall {
     Weights w;
-    uint64_t full[2], done[2];
+    uint64_t full[2], done[2], gates;
     unsigned tmem;
 };
 
@@ -523,21 +555,22 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
     if (ch.len == 0) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rb = warp & 3, cb = warp >> 2, row = 32 * rb + lane;
     if (tid == 32) {
-        bar_init(&sh.done[0]), bar_init(&sh.done[1]), bar_init(&sh.full[0]), bar_init(&sh.full[1]);
+        bar_init(&sh.done[0]), bar_init(&sh.done[1]), bar_init(&sh.full[0]), bar_init(&sh.full[1]), bar_init(&sh.gates);
         fence_tiles();
+        bar_expect(&sh.gates, sizeof(Gates128));
+        copy_bytes(smem_addr(&sh.w.g), p.s.sums + (int64_t(c) * a.H + h) * (2 * kRows), sizeof(Gates128), &sh.gates);
         if constexpr (VEC) {
             bar_expect(&sh.full[0], 2 * PN * kPanelBytes);
             copy_tile<PN>(tq, p.q, grp, int(ch.row), &sh.full[0]);
             copy_tile<PN>(tk, p.k, grp, int(ch.row), &sh.full[0]);
         }
     }
-    if (warp == 0) {
-        float g[4];
-        fetch_gates(g, a.g + ch.row * a.ldg + h, a.ldg, ch.len);
-        tmem_take(&sh.tmem, 256);
-        sum_gates(g, sh.w.g);
+    __syncthreads();   // the barriers are set up
+    if (warp == 12) {  // a warp without weights
+        wait_or_tell(&sh.gates, 0, p.error);
         sh.w.fill();
     }
+    if (warp == 0) tmem_take(&sh.tmem, 256);
     if constexpr (!VEC) {
         load_rows<PN, kRowThreads>(tq, static_cast<const bf16_t *>(a.q) + ch.row * a.ldq + grp * a.N, a.ldq, ch.len, a.N);
         load_rows<PN, kRowThreads>(tk, static_cast<const bf16_t *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
@@ -579,6 +612,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
         multiply(acc_s, Tile<kRows, false>{tq}, Tile<NB, true>{ts}, PB, steps, false);
         bar_after_products(&sh.done[1]);
     }
+    wait_or_tell(&sh.gates, 0, p.error);
     const float hi = sh.w.g.hi[row], lo = sh.w.g.lo[row];
     wait_or_tell(&sh.done[0], 0, p.error);
     if constexpr (VEC) {
@@ -671,7 +705,7 @@ struct Grad {
     struct Small {
         Weights w;
         float after[kRows], key[kRows], dots[32];
-        uint64_t full[2], done[2];
+        uint64_t full[2], done[2], gates;
         unsigned tmem;
         float parts[kFirst ? 1 : 12 * kRows];   // sums by blocks of 16 columns and of 32 rows
     };
@@ -722,7 +756,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         copy_tile<PP>(to, p.dout, h, int(ch.row), &sh.full[1]);
     };
     if (tid == 32) {
-        bar_init(&sh.done[0]), bar_init(&sh.done[1]), bar_init(&sh.full[0]), bar_init(&sh.full[1]);
+        bar_init(&sh.done[0]), bar_init(&sh.done[1]), bar_init(&sh.full[0]), bar_init(&sh.full[1]), bar_init(&sh.gates);
         fence_tiles();
         if constexpr (VEC) {
             bar_expect(&sh.full[0], 2 * PN * kPanelBytes);
@@ -731,6 +765,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         }
     }
     if (warp == 0) tmem_take(&sh.tmem, 512);
+    __syncthreads();   // the barriers are set up
     if constexpr (!VEC) {
         load_rows<PN, kGradThreads>(tq, static_cast<const bf16_t *>(a.q) + ch.row * a.ldq + grp * a.N, a.ldq, ch.len, a.N);
         load_rows<PN, kGradThreads>(tk, static_cast<const bf16_t *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
@@ -813,8 +848,10 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             load_rows<PP, kGradThreads>(tv, static_cast<const bf16_t *>(a.v) + ch.row * a.ldv + h * a.P, a.ldv, ch.len, a.P);
             load_rows<PP, kGradThreads>(to, static_cast<const bf16_t *>(a.dout) + ch.row * a.lddo + h * a.P, a.lddo, ch.len, a.P);
         }
-        float g[4];
-        if (warp == kMmaWarp) fetch_gates(g, a.g + ch.row * a.ldg + h, a.ldg, ch.len);
+        if (tid == 32) {
+            bar_expect(&sh.gates, sizeof(Gates128));
+            copy_bytes(smem_addr(&sh.w.g), p.s.sums + (int64_t(c) * a.H + h) * (2 * kRows), sizeof(Gates128), &sh.gates);
+        }
         const Source from_d = source_of<true>(p, place_d, h), from_s = source_of<false>(p, place_s, h);
         const float by_d = reach_of(from_d), by_s = reach_of(from_s);
         // <S, D>: both in registers, D then stays
@@ -853,7 +890,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             }
         }
         if (warp == kMmaWarp) {
-            sum_gates(g, sh.w.g);
+            wait_or_tell(&sh.gates, (hh - h0) & 1, p.error);
             sh.w.fill();
         }
         put_states();
@@ -878,6 +915,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
                 bar_after_products(&sh.done[1]);
             }
         }
+        wait_or_tell(&sh.gates, (hh - h0) & 1, p.error);
         const float hi = sh.w.g.hi[row], lo = sh.w.g.lo[row];
         const float tail = sh.w.g.span(sh.w.g.hi[kRows - 1], sh.w.g.lo[kRows - 1], row), up = Gates128::exp_of(hi + lo);
         products_done(0);
@@ -1110,8 +1148,8 @@ int grad_splits(int64_t chunks, int H, int G, int N, int P)
 struct Plan {
     int64_t chunks, segments;
     int m, splits;
-    size_t first, seg_first, local, carry, reach, totals, partial, end;   // of the workspace
-    size_t s_carry, s_reach, saved;                                       // of `saved`, whose local states come first
+    size_t first, seg_first, local, carry, reach, totals, sums, partial, end;   // of the workspace
+    size_t s_carry, s_reach, s_sums, saved;                                       // of `saved`, whose local states come first
 };
 Plan plan_of(int64_t B, int64_t T, int H, int G, int N, int P, int64_t nseq, bool packed, bool bwd)
 {
@@ -1127,11 +1165,13 @@ Plan plan_of(int64_t B, int64_t T, int H, int G, int N, int P, int64_t nseq, boo
     w.local = w.totals + align_up(size_t(w.segments) * H * 4, 256);
     w.carry = w.local + align_up(size_t(w.chunks) * H * state, 256);
     w.reach = w.carry + align_up(size_t(w.segments) * H * state, 256);
-    w.partial = w.reach + align_up(size_t(w.chunks) * H * 4, 256);
+    w.sums = w.reach + align_up(size_t(w.chunks) * H * 4, 256);
+    w.partial = w.sums + size_t(w.chunks) * H * sizeof(Gates128);
     w.end = w.partial + (w.splits > 1 ? size_t(w.splits) * w.chunks * G * 2 * ((N + 3) / 4) * kRows * 16 : 0);
     w.s_carry = size_t(w.chunks) * H * state;
     w.s_reach = w.s_carry + size_t(w.segments) * H * state;
-    w.saved = w.s_reach + align_up(size_t(w.chunks) * H * 4, 16);
+    w.s_sums = w.s_reach + align_up(size_t(w.chunks) * H * 4, 16);
+    w.saved = w.s_sums + size_t(w.chunks) * H * sizeof(Gates128);
     return w;
 }
 
@@ -1204,9 +1244,9 @@ mg_status make_call(const GatedArgs &a, bool bwd, TcCall &p, cudaStream_t s)
     p.state = state_size(a.N, a.P);
     p.next_c = 2 * 152 / a.H, p.next_h = 2 * 152 % a.H;   // two blocks of rows on an SM
     p.c.first = reinterpret_cast<const int *>(ws + w.first), p.seg.first = reinterpret_cast<const int *>(ws + w.seg_first);
-    const Walked in_ws{at(w.local), at(w.carry), at(w.reach), at(w.totals)};
+    const Walked in_ws{at(w.local), at(w.carry), at(w.reach), at(w.totals), at(w.sums)};
     float *saved = bwd ? const_cast<float *>(a.saved_in) : a.saved;
-    if (saved != nullptr) p.s = Walked{saved, saved + w.s_carry / 4, saved + w.s_reach / 4, at(w.totals)};
+    if (saved != nullptr) p.s = Walked{saved, saved + w.s_carry / 4, saved + w.s_reach / 4, at(w.totals), saved + w.s_sums / 4};
     else p.s = in_ws;
     p.d = in_ws;
     p.starts = bwd || a.S0 != nullptr;

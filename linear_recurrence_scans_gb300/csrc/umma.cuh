@@ -53,14 +53,20 @@ __device__ __forceinline__ void copy_tile(unsigned to, const CUtensorMap &map, i
 #pragma unroll
     for (int i = 0; i < PANELS; ++i) copy_panel(to + i * kPanelBytes, map, 64 * i, head, row, bar);
 }
-// The same to L2 alone.
+// `bytes` of it (a multiple of 16) as they lie.
+__device__ __forceinline__ void copy_bytes(unsigned to, const void *from, unsigned bytes, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 : : "r"(to), "l"(from), "r"(bytes), "r"(smem_addr(bar)) : "memory");
+}
+// A tile to L2 alone.
 template <int PANELS>
-__device__ __forceinline__ void tile_to_l2(const CUtensorMap &map, int head, int row)
+__device__ __forceinline__ void tile_to_l2(const CUtensorMap &map, int head, int row, int col = 0)
 {
 #pragma unroll
     for (int i = 0; i < PANELS; ++i)
         asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];"
-                     : : "l"(&map), "r"(64 * i), "r"(head), "r"(row) : "memory");
+                     : : "l"(&map), "r"(col + 64 * i), "r"(head), "r"(row) : "memory");
 }
 // A tile's 128 rows to the tensor; columns beyond it are left out.
 template <int PANELS>
