@@ -17,7 +17,7 @@
 // over the chunks, and the outputs (all chunks at once); backwards the same
 // for the adjoints.  dg is summed inside its chunk: a running sum over the whole
 // sequence of q . dq - k . dk gives the same, but its rounding errors grow
-// with the length.  The sums G are taken in float64 and kept as two floats, so
+// with the length.  The sums G are taken and kept as two floats, so
 // that a row that forgets everything costs the differences behind it nothing.
 #include "gated_scan.cuh"
 
@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(256) over_chunks_kernel(const Chunks c, float 
                                                           const float *from, float *to, int H, int64_t NP,
                                                           int blocks_per)
 {
+    after_previous();
     constexpr int kAhead = 8;
     const int64_t sh = blockIdx.x / blocks_per;   // sequence and head
     const int seq = int(sh / H), h = int(sh % H);
@@ -109,31 +110,71 @@ __global__ void __launch_bounds__(256) over_chunks_kernel(const Chunks c, float 
 }
 
 // ---------------------------------------------------------- float32 kernels
-// Chunks of 64 rows in shared memory, 16 x 16 threads, each with an (i, j)
-// subset of a product's outputs: rows ty + 16 a, columns tx + 16 b.  The
-// arithmetic is float32 multiply-adds: bf16 tensor products of float32 values
+// Chunks of 64 rows in shared memory, 16 x 16 threads.  The arithmetic is float32 multiply-adds: bf16 tensor products of float32 values
 // would need six products of three-way splits, and tf32 ones three.
 
 constexpr int kL = 64, kThreads = 256;
+constexpr int kStaged = 4096;                  // values of a state in shared memory at a time, for the outputs
 constexpr size_t kRoom = kMostShared - 4096;   // beside a kernel's own gates and sums
 
-// acc[a][b] += sum_k A(ty + 16 a, k) B(k, tx + 16 b), both in shared memory
-// with constant strides.
-template <int MI, int NJ, int AI, int AK, int BK, int BJ>
+// Products of operands in shared memory.  A thread's rows are ty + 16 i; its
+// columns tx + 16 j, or for kQuads neighbouring ones, 4 (2) at a time, so that one
+// load brings them.  Operands whose rows run along the summed index are read 4
+// of its steps at a time: their row strides are 4 above a multiple of 32 values,
+// which spreads the 16 rows of a load over all banks.  (With single values
+// loaded, 8 loads for 16 multiply-adds, the loads bound the kernels.)
+enum Columns { kStrided, kQuads };
+template <Columns C, int NJ>
+__device__ __forceinline__ int column(int j)
+{
+    const int tx = threadIdx.x & 15;
+    return C == kStrided ? tx + 16 * j : NJ == 2 ? 2 * tx + j : 4 * tx + (j & 3) + 64 * (j >> 2);
+}
+
+// acc[i][j] += sum_k A(row i, k) B(k, column j).  AT: A lies as [k][row], else as
+// [row][k]; BT: B lies as [column][k] (columns kStrided), else as [k][column].
+// Not AT: K is rounded up to a multiple of 4, with zeros behind.
+template <int MI, int NJ, bool AT, bool BT, Columns C, int LA, int LB>
 __device__ __forceinline__ void mm(float (&acc)[MI][NJ], const float *A, const float *B, int K)
 {
-    const float *a = A + (threadIdx.x >> 4) * AI, *b = B + (threadIdx.x & 15) * BJ;
-#pragma unroll 4
-    for (int k = 0; k < K; ++k) {
-        float x[MI], y[NJ];
+    static_assert(!BT || (!AT && C == kStrided), "both along k");
+    const int ty = threadIdx.x >> 4;
+    constexpr int S = AT ? 1 : 4;
+#pragma unroll(AT ? 4 : 2)
+    for (int k = 0; k < K; k += S) {
+        float x[MI][S], y[S][NJ];
 #pragma unroll
-        for (int i = 0; i < MI; ++i) x[i] = a[k * AK + 16 * i * AI];
+        for (int i = 0; i < MI; ++i) {
+            if constexpr (AT) x[i][0] = A[k * LA + ty + 16 * i];
+            else load_vec<4>(A + (ty + 16 * i) * LA + k, x[i]);
+        }
+        if constexpr (BT) {
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) y[j] = b[k * BK + 16 * j * BJ];
+            for (int j = 0; j < NJ; ++j) {
+                float v[4];
+                load_vec<4>(B + column<C, NJ>(j) * LB + k, v);
 #pragma unroll
-        for (int i = 0; i < MI; ++i)
+                for (int u = 0; u < 4; ++u) y[u][j] = v[u];
+            }
+        } else {
 #pragma unroll
-            for (int j = 0; j < NJ; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+            for (int u = 0; u < S; ++u) {
+                constexpr int W = C == kStrided ? 1 : NJ == 2 ? 2 : 4;
+#pragma unroll
+                for (int j = 0; j < NJ; j += W) {
+                    float v[W];
+                    load_vec<W>(B + (k + u) * LB + column<C, NJ>(j), v);
+#pragma unroll
+                    for (int e = 0; e < W; ++e) y[u][j + e] = v[e];
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < S; ++u)
+#pragma unroll
+            for (int i = 0; i < MI; ++i)
+#pragma unroll
+                for (int j = 0; j < NJ; ++j) acc[i][j] = fmaf(x[i][u], y[u][j], acc[i][j]);
     }
 }
 
@@ -159,7 +200,7 @@ __device__ __forceinline__ void load_tile(float *to, const float *from, int64_t 
 }
 
 // Warp 0: a chunk's gate sums as two floats (rows behind the chunk have gate
-// 0), and their total.
+// 0).
 struct Gates {
     float hi[kL], lo[kL];
 };
@@ -167,15 +208,18 @@ __device__ __forceinline__ void load_gates(Gates &s, const float *g, int64_t ldg
 {
     if (threadIdx.x >= 32) return;
     const int i = 2 * threadIdx.x;
-    const double a = i < len ? gate_of(__ldg(g + i * ldg)) : 0.f, b = i + 1 < len ? gate_of(__ldg(g + (i + 1) * ldg)) : 0.f;
-    double v = a + b;
+    const float a = i < len ? gate_of(__ldg(g + i * ldg)) : 0.f, b = i + 1 < len ? gate_of(__ldg(g + (i + 1) * ldg)) : 0.f;
+    float h = a, l = 0.f;
+    add_two(h, l, b, 0.f);
     for (int o = 1; o < 32; o <<= 1) {
-        const double u = __shfl_up_sync(~0u, v, o);
-        if (int(threadIdx.x) >= o) v += u;
+        const float uh = __shfl_up_sync(~0u, h, o), ul = __shfl_up_sync(~0u, l, o);
+        if (int(threadIdx.x) >= o) add_two(h, l, uh, ul);
     }
-    s.hi[i + 1] = float(v), s.lo[i + 1] = float(v - s.hi[i + 1]);
-    v -= b;
-    s.hi[i] = float(v), s.lo[i] = float(v - s.hi[i]);
+    s.hi[i + 1] = h, s.lo[i + 1] = l;
+    float bh = __shfl_up_sync(~0u, h, 1), bl = __shfl_up_sync(~0u, l, 1);   // before the lane's own two
+    if (threadIdx.x == 0) bh = bl = 0.f;
+    add_two(bh, bl, a, 0.f);
+    s.hi[i] = bh, s.lo[i] = bl;
 }
 __device__ __forceinline__ float span(const Gates &s, int i, int j)   // e^{G_i - G_j}
 {
@@ -187,6 +231,7 @@ __device__ __forceinline__ float span(const Gates &s, int i) { return expf(s.hi[
 template <int NB, int PB, bool BACK>
 __global__ void __launch_bounds__(kThreads) gated_add_kernel(const GatedCall p)
 {
+    after_previous();
     extern __shared__ float sm[];
     __shared__ Gates gates;
     const GatedArgs &a = p.a;
@@ -200,18 +245,21 @@ __global__ void __launch_bounds__(kThreads) gated_add_kernel(const GatedCall p)
     load_tile<kL, PB, PB>(V, static_cast<const float *>(BACK ? a.dout : a.v) + ch.row * (BACK ? a.lddo : a.ldv) + h * a.P,
                           BACK ? a.lddo : a.ldv, ch.len, a.P);
     __syncthreads();
-    for (int i = threadIdx.x; i < kL * PB; i += kThreads) V[i] *= BACK ? span(gates, i / PB) : span(gates, kL - 1, i / PB);
+    __shared__ float by[kL];
+    if (threadIdx.x < kL) by[threadIdx.x] = BACK ? span(gates, threadIdx.x) : span(gates, kL - 1, threadIdx.x);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kL * PB; i += kThreads) V[i] *= by[i / PB];
     __syncthreads();
     float acc[NB / 16][PB / 16];
     clear(acc);
-    mm<NB / 16, PB / 16, 1, NB, PB, 1>(acc, K, V, ch.len);
+    mm<NB / 16, PB / 16, true, false, kQuads, NB, PB>(acc, K, V, ch.len);
     float *out = (BACK ? p.adjoints : p.states) + (int64_t(c) * a.H + h) * a.N * a.P;
-    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int ty = threadIdx.x >> 4;
 #pragma unroll
     for (int i = 0; i < NB / 16; ++i)
 #pragma unroll
         for (int j = 0; j < PB / 16; ++j) {
-            const int n = ty + 16 * i, q = tx + 16 * j;
+            const int n = ty + 16 * i, q = column<kQuads, PB / 16>(j);
             if (n < a.N && q < a.P) out[n * a.P + q] = acc[i][j];
         }
     if (threadIdx.x == 0) p.totals[int64_t(c) * a.H + h] = gates.hi[kL - 1];
@@ -221,14 +269,15 @@ __global__ void __launch_bounds__(kThreads) gated_add_kernel(const GatedCall p)
 template <int NB, int PB>
 __global__ void __launch_bounds__(kThreads) gated_out_kernel(const GatedCall p)
 {
+    after_previous();
     extern __shared__ float sm[];
     __shared__ Gates gates;
-    constexpr int LN = NB + 1, LP = kL + 1, KN = LN > LP ? LN : LP;
+    constexpr int LN = NB + 4, LP = kL + 4, KN = LN > LP ? LN : LP, SR = kStaged / PB < NB ? kStaged / PB : NB;
     const GatedArgs &a = p.a;
     const int c = int(blockIdx.x / unsigned(a.H)), h = int(blockIdx.x % unsigned(a.H)), grp = h / (a.H / a.G);
     const Chunks::One ch = p.c.get(c);
     if (ch.len == 0) return;
-    float *Q = sm, *K = Q + kL * LN, *V = K + kL * KN, *W = K;   // weights take K's place
+    float *Q = sm, *K = Q + kL * LN, *V = K + kL * KN, *St = V + kL * PB, *W = K;   // weights take K's place
     load_gates(gates, a.g + ch.row * a.ldg + h, a.ldg, ch.len);
     load_tile<kL, NB, LN>(Q, static_cast<const float *>(a.q) + ch.row * a.ldq + grp * a.N, a.ldq, ch.len, a.N, a.scale);
     load_tile<kL, NB, LN>(K, static_cast<const float *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
@@ -237,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(const GatedCall p)
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     float w[4][4];
     clear(w);
-    mm<4, 4, LN, 1, 1, LN>(w, Q, K, a.N);
+    mm<4, 4, false, true, kStrided, LN, LN>(w, Q, K, a.N);
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -246,21 +295,16 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(const GatedCall p)
             const int r = ty + 16 * i, q = tx + 16 * j;
             W[r * LP + q] = q <= r ? w[i][j] * span(gates, r, q) : 0.f;
         }
-    // Q S, straight from the state (L2): its rows are read by 16 lanes at once
+    // Q S, the state SR rows at a time
     float acc[4][PB / 16];
     clear(acc);
     const float *S = p.states + (int64_t(c) * a.H + h) * a.N * a.P;
-#pragma unroll 4
-    for (int n = 0; n < a.N; ++n) {
-        float x[4], y[PB / 16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = Q[(ty + 16 * i) * LN + n];
-#pragma unroll
-        for (int j = 0; j < PB / 16; ++j) y[j] = tx + 16 * j < a.P ? __ldg(S + n * a.P + tx + 16 * j) : 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < PB / 16; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+    for (int n0 = 0; n0 < a.N; n0 += SR) {
+        const int rows = a.N - n0 < SR ? a.N - n0 : SR;
+        if (n0 > 0) __syncthreads();
+        load_tile<SR, PB, PB>(St, S + n0 * a.P, a.P, rows, a.P);
+        __syncthreads();
+        mm<4, PB / 16, false, false, kQuads, LN, PB>(acc, Q + n0, St, rows);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -268,14 +312,13 @@ __global__ void __launch_bounds__(kThreads) gated_out_kernel(const GatedCall p)
 #pragma unroll
         for (int j = 0; j < PB / 16; ++j) acc[i][j] *= up;
     }
-    __syncthreads();
-    mm<4, PB / 16, LP, 1, PB, 1>(acc, W, V, ch.len);
+    mm<4, PB / 16, false, false, kQuads, LP, PB>(acc, W, V, ch.len);
     float *o = static_cast<float *>(a.o) + (ch.row * a.H + h) * a.P;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < PB / 16; ++j) {
-            const int r = ty + 16 * i, q = tx + 16 * j;
+            const int r = ty + 16 * i, q = column<kQuads, PB / 16>(j);
             if (r < ch.len && q < a.P) o[int64_t(r) * a.H * a.P + q] = acc[i][j];
         }
 }
@@ -293,10 +336,11 @@ __device__ __forceinline__ float over_row(float v)
 template <int NB, int PB>
 __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
 {
+    after_previous();
     extern __shared__ float sm[];
     __shared__ Gates gates;
     __shared__ float col[8][kL], sum_row[kL], sum_key[kL], through[8];
-    constexpr int LN = NB + 1, LV = PB + 1, LP = kL + 1, HN = NB < 64 ? NB : 64, NJ = NB / 16, HJ = HN / 16, PJ = PB / 16;
+    constexpr int LN = NB + 4, LV = PB + 4, LP = kL + 4, HN = NB < 64 ? NB : 64, NJ = NB / 16, HJ = HN / 16, PJ = PB / 16;
     const GatedArgs &a = p.a;
     const int split = int(blockIdx.x % p.splits), grp = int(blockIdx.x / p.splits % a.G);
     const int c = int(blockIdx.x / unsigned(p.splits) / unsigned(a.G));
@@ -319,8 +363,8 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
         {
             float s[4][4], d[4][4], cols[4] = {};
             clear(s), clear(d);
-            mm<4, 4, LN, 1, 1, LN>(s, Q, K, a.N);
-            mm<4, 4, LV, 1, 1, LV>(d, dO, V, a.P);
+            mm<4, 4, false, true, kStrided, LN, LN>(s, Q, K, a.N);
+            mm<4, 4, false, true, kStrided, LV, LV>(d, dO, V, a.P);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = ty + 16 * i;
@@ -344,11 +388,11 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
             }
         }
         __syncthreads();
-        mm<4, NJ, LP, 1, LN, 1>(dq, dW, K, kL);
-        mm<4, NJ, 1, LP, LN, 1>(dk, dW, Q, kL);
+        mm<4, NJ, false, false, kStrided, LP, LN>(dq, dW, K, kL);
+        mm<4, NJ, true, false, kStrided, LP, LN>(dk, dW, Q, kL);
         float dv[4][PJ], in_d[4][PJ];
         clear(dv), clear(in_d);
-        mm<4, PJ, 1, LP, LV, 1>(dv, W, dO, kL);
+        mm<4, PJ, true, false, kQuads, LP, LV>(dv, W, dO, kL);
         float of_q[4] = {}, of_k[4] = {}, dot = 0.f;
         const float *S = p.states + (int64_t(c) * a.H + h) * a.N * a.P, *D = p.adjoints + (int64_t(c) * a.H + h) * a.N * a.P;
 #pragma unroll
@@ -360,8 +404,8 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
             __syncthreads();
             float t[4][HJ];
             clear(t);
-            mm<4, HJ, LV, 1, 1, LV>(t, V, St, a.P);
-            mm<4, PJ, LN, 1, LV, 1>(in_d, K + n0, St, rows);
+            mm<4, HJ, false, true, kStrided, LV, LV>(t, V, St, a.P);
+            mm<4, PJ, false, false, kQuads, LN, LV>(in_d, K + n0, St, rows);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float tail = span(gates, kL - 1, ty + 16 * i);
@@ -378,7 +422,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
             load_tile<HN, PB, LV>(St, S + n0 * a.P, a.P, rows, a.P);
             __syncthreads();
             clear(t);
-            mm<4, HJ, LV, 1, 1, LV>(t, dO, St, a.P);
+            mm<4, HJ, false, true, kStrided, LV, LV>(t, dO, St, a.P);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float up = span(gates, ty + 16 * i);
@@ -397,7 +441,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
             const float tail = span(gates, kL - 1, r);
 #pragma unroll
             for (int j = 0; j < PJ; ++j) {
-                const int q = tx + 16 * j;
+                const int q = column<kQuads, PJ>(j);
                 if (r < ch.len && q < a.P) out[int64_t(r) * a.H * a.P + q] = fmaf(tail, in_d[i][j], dv[i][j]);
             }
             const float x = over_row(of_q[i]), y = over_row(of_k[i]);
@@ -448,6 +492,7 @@ __global__ void __launch_bounds__(kThreads) gated_grad_kernel(const GatedCall p)
 // dq and dk from their parts.
 __global__ void __launch_bounds__(256) gated_join_kernel(const float *part, int splits, int64_t n, float *dq, float *dk)
 {
+    after_previous();
     for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < 2 * n; i += int64_t(gridDim.x) * 256) {
         float v = 0.f;
         for (int s = 0; s < splits; ++s) v += part[s * 2 * n + i];
@@ -525,20 +570,27 @@ int splits_for(int64_t chunks, int H, int G)
     return int(ceil_div(per, heads));
 }
 
+// The call's first kernel, or the second where a chunk table comes before it.
+template <int NB, int PB, bool BACK>
+mg_status add_chunks(const GatedCall &p, int64_t blocks, size_t smem, cudaStream_t s)
+{
+    if (p.a.cu != nullptr) return launch_next("mg_gated_scan", gated_add_kernel<NB, PB, BACK>, blocks, dim3(kThreads), smem, s, p);
+    gated_add_kernel<NB, PB, BACK><<<unsigned(blocks), kThreads, smem, s>>>(p);
+    return launched("mg_gated_scan");
+}
+
 template <int NB, int PB>
 mg_status fwd_sized(const GatedCall &p, cudaStream_t s)
 {
     const GatedArgs &a = p.a;
     const int64_t blocks = int64_t(p.c.most) * a.H;
-    constexpr int LN = NB + 1, KN = LN > kL + 1 ? LN : kL + 1;
-    constexpr size_t add = size_t(kL) * (NB + PB) * 4, out = size_t(kL) * (LN + KN + PB) * 4;
+    constexpr int LN = NB + 4, KN = LN > kL + 4 ? LN : kL + 4;
+    constexpr size_t add = size_t(kL) * (NB + PB) * 4, out = (size_t(kL) * (LN + KN + PB) + kStaged) * 4;
     MG_TRY((allow_shared<gated_add_kernel<NB, PB, false>, kRoom>(add)));
     MG_TRY((allow_shared<gated_out_kernel<NB, PB>, kRoom>(out)));
-    gated_add_kernel<NB, PB, false><<<unsigned(blocks), kThreads, add, s>>>(p);
-    MG_TRY(launched("mg_gated_scan_fwd"));
+    MG_TRY((add_chunks<NB, PB, false>(p, blocks, add, s)));
     MG_TRY(launch_over_chunks(p.c, p.states, p.totals, a.S0, a.S_last, a.H, int64_t(a.N) * a.P, false, s));
-    gated_out_kernel<NB, PB><<<unsigned(blocks), kThreads, out, s>>>(p);
-    return launched("mg_gated_scan_fwd");
+    return launch_next("mg_gated_scan_fwd", gated_out_kernel<NB, PB>, blocks, dim3(kThreads), out, s, p);
 }
 
 template <int NB, int PB>
@@ -547,18 +599,16 @@ mg_status bwd_sized(const GatedCall &p, cudaStream_t s)
     const GatedArgs &a = p.a;
     const int64_t blocks = int64_t(p.c.most) * a.H, grads = int64_t(p.c.most) * a.G * p.splits;
     constexpr size_t add = size_t(kL) * (NB + PB) * 4;
-    constexpr size_t grad = size_t(kL) * (2 * (NB + 1) + 2 * (PB + 1) + 2 * (kL + 1)) * 4 + size_t(NB < 64 ? NB : 64) * (PB + 1) * 4;
+    constexpr size_t grad = size_t(kL) * (2 * (NB + 4) + 2 * (PB + 4) + 2 * (kL + 4)) * 4 + size_t(NB < 64 ? NB : 64) * (PB + 4) * 4;
     MG_TRY((allow_shared<gated_add_kernel<NB, PB, true>, kRoom>(add)));
     MG_TRY((allow_shared<gated_grad_kernel<NB, PB>, kRoom>(grad)));
-    gated_add_kernel<NB, PB, true><<<unsigned(blocks), kThreads, add, s>>>(p);
-    MG_TRY(launched("mg_gated_scan_bwd"));
+    MG_TRY((add_chunks<NB, PB, true>(p, blocks, add, s)));
     MG_TRY(launch_over_chunks(p.c, p.adjoints, p.totals, a.dS_last, a.dS0, a.H, int64_t(a.N) * a.P, true, s));
-    gated_grad_kernel<NB, PB><<<unsigned(grads), kThreads, grad, s>>>(p);
-    MG_TRY(launched("mg_gated_scan_bwd"));
+    MG_TRY(launch_next("mg_gated_scan_bwd", gated_grad_kernel<NB, PB>, grads, dim3(kThreads), grad, s, p));
     if (p.splits == 1) return MG_OK;
     const int64_t n = a.B * a.T * a.G * a.N, want = ceil_div(2 * n, 256);
-    gated_join_kernel<<<unsigned(want < 8192 ? want : 8192), 256, 0, s>>>(p.partial, p.splits, n, static_cast<float *>(a.dq), static_cast<float *>(a.dk));
-    return launched("mg_gated_scan_bwd");
+    return launch_next("mg_gated_scan_bwd", gated_join_kernel, want < 8192 ? want : 8192, dim3(256), 0, s, p.partial, p.splits, n,
+                       static_cast<float *>(a.dq), static_cast<float *>(a.dk));
 }
 
 // F<NB, PB> for the sizes that hold N and P.
@@ -608,11 +658,9 @@ mg_status launch_over_chunks(const Chunks &c, float *states, const float *totals
 {
     const int vec = NP % 4 == 0 ? 4 : 1;
     const int per = int(ceil_div(NP, 256 * vec));
-    const unsigned blocks = unsigned(int64_t(c.q.nseq) * H * per);
     auto *kernel = vec == 4 ? (backward ? over_chunks_kernel<4, true> : over_chunks_kernel<4, false>)
                             : (backward ? over_chunks_kernel<1, true> : over_chunks_kernel<1, false>);
-    kernel<<<blocks, 256, 0, s>>>(c, states, totals, from, to, H, NP, per);
-    return launched("pass over chunks");
+    return launch_next("pass over chunks", kernel, int64_t(c.q.nseq) * H * per, dim3(256), 0, s, c, states, totals, from, to, H, NP, per);
 }
 
 size_t gated_saved_bytes(int64_t B, int64_t T, int64_t H, int64_t N, int64_t P, int64_t nseq, bool packed, mg_dtype dt)

@@ -11,6 +11,15 @@ namespace mg {
 constexpr float kLeastGate = -128.f;
 __device__ __forceinline__ float gate_of(float g) { return g < kLeastGate ? kLeastGate : g; }
 
+// x + y as two floats, exact but for the last bits of the lower ones.
+__device__ __forceinline__ void add_two(float &xh, float &xl, float yh, float yl)
+{
+    const float s = xh + yh, b = s - xh;
+    const float e = (xh - (s - b)) + (yh - b) + (xl + yl);
+    xh = s + e;
+    xl = e - (xh - s);
+}
+
 // A batch's chunks of up to L rows, none of them across two sequences.  Dense:
 // `per` in each sequence.  Packed: sequence s has the chunks first[s] ..
 // first[s+1]-1, a table that launch_chunk_tables leaves in the workspace; of a

@@ -27,21 +27,12 @@ constexpr int kRows = 128;   // of a chunk: the rows of a tensor-core product
 // A chunk's gate sums as two floats.  The forward walk leaves them for the kernels
 // behind it.
 struct Gates128 {
-    float hi[kRows], lo[kRows];
+    alignas(16) float hi[kRows], lo[kRows];   // copied as they lie
     __device__ __forceinline__ float span(float hi_i, float lo_i, int j) const { return exp_of((hi_i - hi[j]) + (lo_i - lo[j])); }
     // e^x in two instructions.  The rounding of x log2 e costs a relative |x|
     // 2^-24 of a weight that is e^x itself.
     static __device__ __forceinline__ float exp_of(float x) { return ex2_ftz(x * kLog2eF); }
 };
-
-// x + y as two floats, exact but for the last bits of the lower ones.
-__device__ __forceinline__ void add_two(float &xh, float &xl, float yh, float yl)
-{
-    const float s = xh + yh, b = s - xh;
-    const float e = (xh - (s - b)) + (yh - b) + (xl + yl);
-    xh = s + e;
-    xl = e - (xh - s);
-}
 
 // One warp: a lane has the gates of rows 4 lane .. 4 lane + 3, and gets the sums
 // up to each of them.
@@ -274,6 +265,7 @@ struct WalkSmall {
 template <int PN, bool VEC, bool BACK>
 __global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const __grid_constant__ TcCall p, int tiles)
 {
+    after_previous();
     extern __shared__ __align__(1024) char sm[];
     constexpr unsigned kK = PN * kRows * 128, kV = kRows * 128;
     const GatedArgs &a = p.a;
@@ -457,6 +449,7 @@ template <bool BACK>
 __global__ void __launch_bounds__(256) over_segments_kernel(const Chunks seg, const Walked w, const float *from, float *to,
                                                             int H, int N, int P, int blocks_per)
 {
+    after_previous();
     constexpr int kAhead = 8;
     const unsigned su = blockIdx.x / unsigned(blocks_per);   // sequence and head
     const int seq = int(su / unsigned(H)), h = int(su % unsigned(H));
@@ -514,7 +507,7 @@ __global__ void __launch_bounds__(256) over_segments_kernel(const Chunks seg, co
 // exponential; the others the product of e^{G_i - G_r} and e^{G_r - G_j}, r the
 // last of j's 32 rows, both at most 1: one exponential a row and block instead
 // of one a pair.
-struct alignas(16) Weights {
+struct Weights {
     Gates128 g;
     float to_end[kRows];   // e^{G_r - G_j}
     // One warp, once the sums are there.
@@ -543,6 +536,7 @@ struct RowsSmall {
 template <int PN, int PP, bool VEC>
 __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid_constant__ TcCall p)
 {
+    after_previous();
     extern __shared__ __align__(1024) char sm[];
     constexpr int NB = 64 * PN, PB = 64 * PP;
     constexpr unsigned kQ = 2 * kPanelBytes, kK = (PN > PP ? PN : PP) * kPanelBytes, kS = PP * NB * 128;
@@ -732,6 +726,7 @@ __device__ __forceinline__ float column_sums(float (&w)[16])
 template <int PN, int PP, bool VEC>
 __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __grid_constant__ TcCall p)
 {
+    after_previous();
     extern __shared__ __align__(1024) char sm[];
     using M = Grad<PN, PP>;
     constexpr int NB = M::NB, PB = M::PB;
@@ -1085,6 +1080,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
 constexpr int kJoinBlocks = 8;   // for a chunk and group
 __global__ void __launch_bounds__(256) gated_join_rows_kernel(const __grid_constant__ TcCall p)
 {
+    after_previous();
     const GatedArgs &a = p.a;
     const int quads = (a.N + 3) / 4, grp = int(blockIdx.x / kJoinBlocks % unsigned(a.G)), c = int(blockIdx.x / kJoinBlocks / unsigned(a.G));
     const Chunks::One ch = p.c.get(c);
@@ -1180,8 +1176,8 @@ mg_status over_segments(const TcCall &p, const float *from, float *to, cudaStrea
 {
     const GatedArgs &a = p.a;
     const int per = int(ceil_div(int64_t((a.P + 3) / 4) * a.N, 256));
-    over_segments_kernel<BACK><<<unsigned(a.nseq * a.H * per), 256, 0, s>>>(p.seg, BACK ? p.d : p.s, from, to, a.H, a.N, a.P, per);
-    return launched("pass over segments");
+    return launch_next("pass over segments", over_segments_kernel<BACK>, a.nseq * a.H * per, dim3(256), 0, s, p.seg, BACK ? p.d : p.s, from, to,
+                       a.H, a.N, a.P, per);
 }
 
 template <int PN, bool VEC, bool BACK>
@@ -1191,7 +1187,9 @@ mg_status walk(const TcCall &p, cudaStream_t s)
     static_assert(2 * (smem + 1024) <= 228 * 1024 || PN == 1, "two blocks an SM");
     MG_TRY((allow_shared<gated_walk_kernel<PN, VEC, BACK>>(smem)));
     const int tiles = int(ceil_div(p.a.P, 64));
-    gated_walk_kernel<PN, VEC, BACK><<<unsigned(int64_t(p.seg.most) * p.a.H * tiles), kWalkThreads, smem, s>>>(p, tiles);
+    const int64_t blocks = int64_t(p.seg.most) * p.a.H * tiles;
+    if (p.a.cu != nullptr) return launch_next("mg_gated_scan", gated_walk_kernel<PN, VEC, BACK>, blocks, dim3(kWalkThreads), smem, s, p, tiles);
+    gated_walk_kernel<PN, VEC, BACK><<<unsigned(blocks), kWalkThreads, smem, s>>>(p, tiles);   // the call's first kernel
     return launched("mg_gated_scan");
 }
 
@@ -1203,8 +1201,7 @@ mg_status forward(const TcCall &p, cudaStream_t s)
     constexpr size_t smem = 2 * kPanelBytes + (PN > PP ? PN : PP) * kPanelBytes + PP * PN * 64 * 128 + sizeof(RowsSmall);
     static_assert(2 * (smem + 1024) <= 228 * 1024, "two blocks an SM");
     MG_TRY((allow_shared<gated_rows_kernel<PN, PP, VEC>>(smem)));
-    gated_rows_kernel<PN, PP, VEC><<<unsigned(int64_t(p.c.most) * p.a.H), kRowThreads, smem, s>>>(p);
-    return launched("mg_gated_scan_fwd");
+    return launch_next("mg_gated_scan_fwd", gated_rows_kernel<PN, PP, VEC>, int64_t(p.c.most) * p.a.H, dim3(kRowThreads), smem, s, p);
 }
 
 template <int PN, int PP, bool VEC>
@@ -1215,11 +1212,9 @@ mg_status backward(const TcCall &p, cudaStream_t s)
     constexpr size_t smem = Grad<PN, PP>::bytes;
     static_assert(smem <= 227 * 1024, "one block an SM");
     MG_TRY((allow_shared<gated_grads_kernel<PN, PP, VEC>, 227 * 1024>(smem)));
-    gated_grads_kernel<PN, PP, VEC><<<unsigned(int64_t(p.c.most) * p.a.G * p.splits), kGradThreads, smem, s>>>(p);
-    MG_TRY(launched("mg_gated_scan_bwd"));
+    MG_TRY(launch_next("mg_gated_scan_bwd", gated_grads_kernel<PN, PP, VEC>, int64_t(p.c.most) * p.a.G * p.splits, dim3(kGradThreads), smem, s, p));
     if (p.splits == 1) return MG_OK;
-    gated_join_rows_kernel<<<unsigned(int64_t(p.c.most) * p.a.G * kJoinBlocks), 256, 0, s>>>(p);
-    return launched("mg_gated_scan_bwd");
+    return launch_next("mg_gated_scan_bwd", gated_join_rows_kernel, int64_t(p.c.most) * p.a.G * kJoinBlocks, dim3(256), 0, s, p);
 }
 
 // Whole 16-byte pieces where every row and head begins and ends on such a
