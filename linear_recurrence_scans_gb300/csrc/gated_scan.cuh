@@ -7,9 +7,10 @@
 namespace mg {
 
 // Gates below this count as this: exp(-128) is 0 in float32, and sums of a
-// chunk's gates keep their precision.
+// chunk's gates keep their precision.  (+ 0: a caller's signalling NaN must not
+// get into the workspace as it is.)
 constexpr float kLeastGate = -128.f;
-__device__ __forceinline__ float gate_of(float g) { return g < kLeastGate ? kLeastGate : g; }
+__device__ __forceinline__ float gate_of(float g) { return (g < kLeastGate ? kLeastGate : g) + 0.f; }
 
 // x + y as two floats, exact but for the last bits of the lower ones.
 __device__ __forceinline__ void add_two(float &xh, float &xl, float yh, float yl)

@@ -164,7 +164,7 @@ struct Walked {
     float *sums;     // [chunks][H]: a chunk's Gates128
 };
 
-struct alignas(64) TcCall {
+struct TcCall {
     CUtensorMap q, k, v, dout, o, dq, dk, dv;   // where rows are aligned
     GatedArgs a;
     Chunks c, seg;   // chunks, and segments of m of them
@@ -1114,9 +1114,6 @@ int segment_chunks(int64_t chunks, int64_t nseq, int H, int P)
     const int64_t blocks = H * ceil_div(P, 64), each = ceil_div(chunks, nseq > 0 ? nseq : 1);
     int best = 1;
     double least = 1e300;
-#ifdef MG_GATED_M
-    return MG_GATED_M;
-#endif
     for (int m = 1; m <= 64; ++m) {
         const double t = double(ceil_div(nseq * ceil_div(each, m) * blocks, 2 * 152)) * (m + 1.5);
         if (t < least * 0.999) least = t, best = m;

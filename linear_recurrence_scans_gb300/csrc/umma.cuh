@@ -29,11 +29,6 @@ __device__ __forceinline__ uint4 ld_tile(unsigned base, unsigned at)
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(base + at) : "memory");
     return v;
 }
-// 16 bytes from global memory, without a register; zeros where `on` is false.
-__device__ __forceinline__ void copy16(unsigned to, const void *from, bool on)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" : : "r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
-}
 // A tensor of rows, heads of `cols` bf16 values in each, rows `ld` values apart,
 // for copies of a head's 64 columns of 128 rows: a panel of a tile, zeros where
 // columns or rows lie outside the tensor.  The address and all strides are
