@@ -20,6 +20,11 @@ Cases (inputs seeded, resident on cuda:0 before the first launch):
                                  the states saved for the gradients)
   conv_fwd / conv_bwd            short causal convolution, B=8 T=4096 D=2048 W=4, bf16
   norm_fwd / norm_bwd            group norm of 32768 rows x 2048, 16 groups, gated, bf16
+  gated_fwd / gated_bwd          gated scan, B=4 T=4096, 16 heads of 128 keys x 128 values,
+                                 each with its own q and k, bf16 (forward with what the
+                                 gradients need)
+  rms_fwd / rms_quant / rms_bwd  RMS norm of 32768 rows x 2048 with a residual, bf16; its
+                                 8-bit output in blocks of 128; its gradients
 
 Every case runs its op `repeats` times (default 3) after one set-up call of
 the forward op where the backward needs the forward's outputs.  Each input is
@@ -37,7 +42,8 @@ from linear_recurrence_scans_gb300 import workloads as wl
 CASES = ("linear_fwd", "linear_bwd", "linear_bf16_fwd", "linear_bf16_bwd", "log_fwd", "log_bwd",
          "affine4_fwd", "affine4_bwd", "affine16_fwd", "affine16_bwd", "mingru_bf16_fwd",
          "mingru_bf16_bwd", "varlen_fwd", "varlen_bwd", "angle_fwd", "angle_bwd",
-         "selective_fwd", "selective_bwd", "conv_fwd", "conv_bwd", "norm_fwd", "norm_bwd")
+         "selective_fwd", "selective_bwd", "conv_fwd", "conv_bwd", "norm_fwd", "norm_bwd",
+         "gated_fwd", "gated_bwd", "rms_fwd", "rms_quant", "rms_bwd")
 
 
 def main(argv):
@@ -83,6 +89,28 @@ def main(argv):
                 mg.group_norm_fwd(x, g, b, z, groups=16, out=(y, stats))
             else:
                 mg.group_norm_bwd(dy, stats, x, g, b, z, groups=16)
+    elif case.startswith("gated"):
+        gen = torch.Generator(dev).manual_seed(0)
+        q, k, v, do = (torch.randn(4, 4096, 16, 128, device=dev, generator=gen).to(torch.bfloat16) for _ in range(4))
+        g = torch.nn.functional.logsigmoid(2 + torch.randn(4, 4096, 16, device=dev, generator=gen))
+        o, S_last, saved = mg.gated_scan_fwd(q, k, v, g, scale=128 ** -0.5, save=True)
+        for _ in range(reps):
+            if case.endswith("fwd"):
+                mg.gated_scan_fwd(q, k, v, g, scale=128 ** -0.5, save=True, out=(o, S_last, saved))
+            else:
+                mg.gated_scan_bwd(do, saved, q, k, v, g, scale=128 ** -0.5)
+    elif case.startswith("rms"):
+        gen = torch.Generator(dev).manual_seed(0)
+        x, residual, dy, dr = (torch.randn(32768, 2048, device=dev, generator=gen).to(torch.bfloat16) for _ in range(4))
+        w = torch.randn(2048, device=dev, generator=gen)
+        y, r, rstd = mg.rms_norm_fwd(x, w, residual)
+        for _ in range(reps):
+            if case == "rms_fwd":
+                mg.rms_norm_fwd(x, w, residual, out=(y, r, rstd))
+            elif case == "rms_quant":
+                mg.rms_norm_quant(x, w, residual, block=128)
+            else:
+                mg.rms_norm_bwd(dy, rstd, r, w, dr)
     elif case.startswith("mingru"):
         x1, x2, _, gBc = wl.mingru_x(4, 8192, 4096, seed=0, device=dev, in_dtype=torch.bfloat16)
         _, Bc = mg.mingru_scan_fwd(x1, x2, want_A=False)
