@@ -29,6 +29,16 @@ constexpr int kRows = 128;   // of a chunk: the rows of a tensor-core product
 struct Gates128 {
     alignas(16) float hi[kRows], lo[kRows];   // copied as they lie
     __device__ __forceinline__ float span(float hi_i, float lo_i, int j) const { return exp_of((hi_i - hi[j]) + (lo_i - lo[j])); }
+    // The four of j .. j + 3, j a multiple of 4, zeros from `count` of them on: the
+    // exponent is what is selected, so that no element is a branch of its own (as
+    // branches these took 3300 cycles of a block's 26000, and other pairs' 800).
+    __device__ __forceinline__ void spans(float hi_i, float lo_i, int j, int count, float (&by)[4]) const
+    {
+        const float4 h = *reinterpret_cast<const float4 *>(hi + j), l = *reinterpret_cast<const float4 *>(lo + j);
+        const float x[4] = {(hi_i - h.x) + (lo_i - l.x), (hi_i - h.y) + (lo_i - l.y), (hi_i - h.z) + (lo_i - l.z), (hi_i - h.w) + (lo_i - l.w)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) by[e] = exp_of(e < count ? x[e] : -INFINITY);
+    }
     // e^x in two instructions.  The rounding of x log2 e costs a relative |x|
     // 2^-24 of a weight that is e^x itself.
     static __device__ __forceinline__ float exp_of(float x) { return ex2_ftz(x * kLog2eF); }
@@ -236,12 +246,12 @@ __device__ __forceinline__ void fetch_states(const Source &from, float by, int N
     };
     if (from.local != nullptr)
         each(from.local, [](const float4 x, float (&o)[8], int e) { o[e] = x.x, o[e + 1] = x.y, o[e + 2] = x.z, o[e + 3] = x.w; });
-    if (from.carry != nullptr)
-        each(from.carry, [by](const float4 x, float (&o)[8], int e) {
-            o[e] = fmaf(by, x.x, o[e]), o[e + 1] = fmaf(by, x.y, o[e + 1]), o[e + 2] = fmaf(by, x.z, o[e + 2]), o[e + 3] = fmaf(by, x.w, o[e + 3]);
-        });
+    if (from.carry == nullptr) return;
+    each(from.carry, [by](const float4 x, float (&o)[8], int e) {
+        o[e] = fmaf(by, x.x, o[e]), o[e + 1] = fmaf(by, x.y, o[e + 1]), o[e + 2] = fmaf(by, x.z, o[e + 2]), o[e + 3] = fmaf(by, x.w, o[e + 3]);
+    });
 }
-__device__ __forceinline__ float reach_of(const Source &s) { return s.carry != nullptr ? expf(__ldg(s.reach)) : 0.f; }
+__device__ __forceinline__ float reach_of(const Source &s) { return s.carry != nullptr ? __ldg(s.reach) : 0.f; }
 
 __device__ __forceinline__ void wait_or_tell(uint64_t *bar, unsigned phase, unsigned *error)
 {
@@ -573,7 +583,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
         const Source s = source_of<false>(p, place_of<false>(p, ch, c), h);
         using Mine = Pieces8<NB, PP, kRowThreads>;
         float f[Mine::kMine][8];
-        fetch_states<Mine>(s, reach_of(s), a.N, a.P, f);
+        fetch_states<Mine>(s, expf(reach_of(s)), a.N, a.P, f);
 #pragma unroll
         for (int u = 0; u < Mine::kMine; ++u)
             if (Mine::mine(u))
@@ -628,7 +638,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
         } else if (cb == rb) {
             tmem_load(acc + mine + 32 * cb, w);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) w[e] = e <= lane ? w[e] * sh.w.g.span(hi, lo, 32 * cb + e) : 0.f;
+            for (int e = 0; e < 32; e += 4) {
+                float by[4];
+                sh.w.g.spans(hi, lo, 32 * cb + e, lane + 1 - e, by);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) w[e + u] = (e + u <= lane ? w[e + u] : 0.f) * by[u];
+            }
         } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) w[e] = 0.f;
@@ -698,8 +713,8 @@ struct Grad {
     static constexpr unsigned kTiles = 2 * kQ + 2 * kV + (kFirst ? kX : 2 * kW + kX);
     struct Small {
         Weights w;
-        float after[kRows], key[kRows], dots[32];
-        uint64_t full[2], done[2], gates;
+        float after[kRows], key[kRows], dots[32], end[2];
+        uint64_t full[2], done[2], gates, adjoint;
         unsigned tmem;
         float parts[kFirst ? 1 : 12 * kRows];   // sums by blocks of 16 columns and of 32 rows
     };
@@ -738,21 +753,35 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
     float *row_part = M::kFirst ? reinterpret_cast<float *>(sm + 2 * M::kQ + 2 * M::kV + 2 * M::kW) : sh.parts, *col_part = row_part + 8 * kRows;
     float *key_part = M::kFirst ? col_part + 4 * kRows : row_part;
 
-    const unsigned of_c = blockIdx.x / unsigned(p.splits);
-    const int split = int(blockIdx.x % unsigned(p.splits)), grp = int(of_c % unsigned(a.G)), c = int(of_c / unsigned(a.G));
+    // the parts of a group's heads one after another: the last, maybe smaller, ones fill up the SMs
+    const unsigned all = unsigned(p.c.most) * unsigned(a.G), of_c = blockIdx.x % all;
+    const int split = int(blockIdx.x / all), grp = int(of_c % unsigned(a.G)), c = int(of_c / unsigned(a.G));
     const Chunks::One ch = p.c.get(c);
     if (ch.len == 0) return;
     const Place place_d = place_of<true>(p, ch, c), place_s = place_of<false>(p, ch, c);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rb = warp & 3, cb = warp >> 2, row = 32 * rb + lane;
-    const int per_group = a.H / a.G, h0 = split * p.heads, h1 = h0 + p.heads < per_group ? h0 + p.heads : per_group;
-    const auto copy_head = [&](int h) {   // V and dO
-        bar_expect(&sh.full[1], 2 * PP * kPanelBytes);
-        copy_tile<PP>(tv, p.v, h, int(ch.row), &sh.full[1]);
-        copy_tile<PP>(to, p.dout, h, int(ch.row), &sh.full[1]);
+    const int per_group = a.H / a.G, h0 = split * p.heads, h1 = M::kFirst ? h0 + 1 : h0 + p.heads < per_group ? h0 + p.heads : per_group;
+    // V, dO, gate sums and (into the weights' place) the adjoint's two parts
+    const auto copy_head = [&](int h) {
+        if constexpr (VEC) {
+            bar_expect(&sh.full[1], 2 * PP * kPanelBytes);
+            copy_tile<PP>(tv, p.v, h, int(ch.row), &sh.full[1]);
+            copy_tile<PP>(to, p.dout, h, int(ch.row), &sh.full[1]);
+        }
+        bar_expect(&sh.gates, sizeof(Gates128));
+        copy_bytes(smem_addr(&sh.w.g), p.s.sums + (int64_t(c) * a.H + h) * (2 * kRows), sizeof(Gates128), &sh.gates);
+        if constexpr (!M::kFirst) {
+            const Source d = source_of<true>(p, place_d, h);
+            const unsigned bytes = unsigned(p.state) * 4;
+            if (place_d.local || place_d.carry) bar_expect(&sh.adjoint, bytes * (unsigned(place_d.local) + unsigned(place_d.carry)));
+            if (place_d.local) copy_bytes(tw, d.local, bytes, &sh.adjoint);
+            if (place_d.carry) copy_bytes(tdw, d.carry, bytes, &sh.adjoint);
+        }
     };
     if (tid == 32) {
-        bar_init(&sh.done[0]), bar_init(&sh.done[1]), bar_init(&sh.full[0]), bar_init(&sh.full[1]), bar_init(&sh.gates);
+        bar_init(&sh.done[0]), bar_init(&sh.done[1]), bar_init(&sh.full[0]), bar_init(&sh.full[1]), bar_init(&sh.gates), bar_init(&sh.adjoint);
         fence_tiles();
+        copy_head(grp * per_group + h0);
         if constexpr (VEC) {
             bar_expect(&sh.full[0], 2 * PN * kPanelBytes);
             copy_tile<PN>(tq, p.q, grp, int(ch.row), &sh.full[0]);
@@ -788,6 +817,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
     };
     using Mine = Pieces8<NB, PP, kGradThreads>;
     float st[Mine::kMine][8];
+    float reach_d = reach_of(source_of<true>(p, place_d, grp * per_group + h0)), reach_s = reach_of(source_of<false>(p, place_s, grp * per_group + h0));
     const auto put_states = [&]() {   // as three pieces
 #pragma unroll
         for (int u = 0; u < Mine::kMine; ++u) {
@@ -832,37 +862,34 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
     };
     for (int hh = h0; hh < h1; ++hh) {
         const int h = grp * per_group + hh;
-        if (hh > h0) {   // the head before is done with its tiles
-            fence_tiles();
-            if (tid == 32) tiles_put();
-            __syncthreads();
-        }
-        if constexpr (VEC) {
-            if (tid == 32) copy_head(h);
-        } else {
+        if constexpr (!VEC) {   // the head before is done with its tiles
             load_rows<PP, kGradThreads>(tv, static_cast<const bf16_t *>(a.v) + ch.row * a.ldv + h * a.P, a.ldv, ch.len, a.P);
             load_rows<PP, kGradThreads>(to, static_cast<const bf16_t *>(a.dout) + ch.row * a.lddo + h * a.P, a.lddo, ch.len, a.P);
         }
-        if (tid == 32) {
-            bar_expect(&sh.gates, sizeof(Gates128));
-            copy_bytes(smem_addr(&sh.w.g), p.s.sums + (int64_t(c) * a.H + h) * (2 * kRows), sizeof(Gates128), &sh.gates);
-        }
         const Source from_d = source_of<true>(p, place_d, h), from_s = source_of<false>(p, place_s, h);
-        const float by_d = reach_of(from_d), by_s = reach_of(from_s);
-        // <S, D>: both in registers, D then stays
-        float dot = 0.f;
-        {
-            float other[Mine::kMine][8];
+        const float by_d = expf(reach_d), by_s = expf(reach_s);
+        if constexpr (M::kFirst) {
             fetch_states<Mine>(from_d, by_d, a.N, a.P, st);
+        } else {
+            if (place_d.local || place_d.carry) wait_or_tell(&sh.adjoint, (hh - h0) & 1, p.error);
+            const float *copied = reinterpret_cast<const float *>(sm + (tw - tq));
+            fetch_states<Mine>(Source{place_d.local ? copied : nullptr, place_d.carry ? copied + M::kW / 4 : nullptr, nullptr}, by_d, a.N, a.P, st);
+        }
+        float dot = 0.f;   // <S, D>
+        const auto put_dot = [&]() {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
+            if (lane == 0) sh.dots[warp] = dot;
+        };
+        if constexpr (M::kFirst) {   // D's pieces make room before S comes for good
+            float other[Mine::kMine][8];
             fetch_states<Mine>(from_s, by_s, a.N, a.P, other);
 #pragma unroll
             for (int u = 0; u < Mine::kMine; ++u)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) dot = fmaf(other[u][e], st[u][e], dot);
+            put_dot();
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(~0u, dot, o);
-        if (lane == 0) sh.dots[warp] = dot;
         if (VEC && tid == 64) {   // what comes after this head: the block's next one, or the block that follows on the SM
             if (hh + 1 < h1) {
                 tile_to_l2<PP>(p.v, h + 1, int(ch.row));
@@ -870,9 +897,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
                 if (place_d.local) to_l2(from_d.local + p.state, unsigned(p.state) * 4);
                 if (place_s.local) to_l2(from_s.local + p.state, unsigned(p.state) * 4);
             } else {
-                const unsigned next = blockIdx.x + 152, of_n = next / unsigned(p.splits);
-                const int gn = int(of_n % unsigned(a.G)), cn = int(of_n / unsigned(a.G)), hn = gn * per_group + int(next % unsigned(p.splits)) * p.heads;
-                const Chunks::One n = cn < p.c.most ? p.c.get(cn) : Chunks::One{0, 0, 0, 0};
+                const unsigned next = blockIdx.x + 152, of_n = next % all;
+                const int gn = int(of_n % unsigned(a.G)), cn = int(of_n / unsigned(a.G)), hn = gn * per_group + int(next / all) * p.heads;
+                const Chunks::One n = next < gridDim.x ? p.c.get(cn) : Chunks::One{0, 0, 0, 0};
                 if (n.len > 0) {
                     tile_to_l2<PN>(p.q, gn, int(n.row));
                     tile_to_l2<PN>(p.k, gn, int(n.row));
@@ -887,6 +914,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         if (warp == kMmaWarp) {
             wait_or_tell(&sh.gates, (hh - h0) & 1, p.error);
             sh.w.fill();
+            if (lane == 0) sh.end[(hh - h0) & 1] = Gates128::exp_of(sh.w.g.hi[kRows - 1] + sh.w.g.lo[kRows - 1]);
         }
         put_states();
         if constexpr (VEC) {
@@ -916,27 +944,38 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         products_done(0);
         // weights, and what each pair of rows gives to the gates between them: rows
         // from 32 rb, columns from 16 cb
-        float of_row = 0.f, of_col = 0.f;
+        float of_row = 0.f, of_col = 0.f, last = 0.f;
         unsigned pw[8], pd[8];
         if (cb <= 2 * rb + 1) {
             float s[16], d[16];
             tmem_load(acc0 + mine + 16 * cb, s);
             tmem_load(acc1 + mine + 16 * cb, d);
             const int first = 16 * cb - 32 * rb;   // columns up to lane - first reach the row
-            const float from = a.scale * (first < 0 ? sh.w.g.span(hi, lo, 32 * (cb >> 1) + 31) : 1.f);
+            if (first < 0) {   // all of them
+                const float from = a.scale * sh.w.g.span(hi, lo, 32 * (cb >> 1) + 31);
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-                float w[2];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int j = e + u;
-                    float by = from * (first < 0 ? sh.w.to_end[16 * cb + j] : sh.w.g.span(hi, lo, 16 * cb + j));
-                    const bool in = first < 0 || first + j <= lane;
-                    w[u] = in ? s[j] * by : 0.f, d[j] = in ? d[j] * by : 0.f;
-                    s[j] = first < 0 || first + j < lane ? s[j] * d[j] : 0.f;
-                    of_row += s[j];
+                for (int j = 0; j < 16; ++j) {
+                    const float by = from * sh.w.to_end[16 * cb + j], w = s[j] * by;
+                    d[j] *= by, s[j] *= d[j], of_row += s[j];
+                    if (j & 1) pw[j / 2] = pack_bf16x2(last, w), pd[j / 2] = pack_bf16x2(d[j - 1], d[j]);
+                    last = w;
                 }
-                pw[e / 2] = pack_bf16x2(w[0], w[1]), pd[e / 2] = pack_bf16x2(d[e], d[e + 1]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    float by[4];
+                    sh.w.g.spans(hi, lo, 16 * cb + e, lane + 1 - first - e, by);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int j = e + u;
+                        const bool in = first + j <= lane;   // what is behind may be a NaN
+                        by[u] *= a.scale;
+                        const float w = (in ? s[j] : 0.f) * by[u];
+                        d[j] = (in ? d[j] : 0.f) * by[u], s[j] = (first + j < lane ? s[j] : 0.f) * d[j], of_row += s[j];
+                        if (j & 1) pw[j / 2] = pack_bf16x2(last, w), pd[j / 2] = pack_bf16x2(d[j - 1], d[j]);
+                        last = w;
+                    }
+                }
             }
             of_col = column_sums(s);
         } else {
@@ -979,6 +1018,18 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             if constexpr (M::kFirst) sh.key[tid] = of_blocks(key_part, 8);
         }
         fetch_states<Mine>(from_s, by_s, a.N, a.P, st);
+        if constexpr (!M::kFirst) {   // D is the sum of its pieces
+#pragma unroll
+            for (int u = 0; u < Mine::kMine; ++u) {
+                if (!Mine::mine(u)) continue;
+                float x[3][8];
+#pragma unroll
+                for (int k = 0; k < 3; ++k) unpack8(ld_tile(tx + k * M::kState, tile_at(NB, Mine::row(u), Mine::piece(u))), x[k]);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dot = fmaf(st[u][e], x[0][e] + (x[1][e] + x[2][e]), dot);
+            }
+            put_dot();
+        }
         products_done(0);
         if (cb < PB / 16) {
             float x[16];
@@ -1003,9 +1054,20 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         } else {
             store_rows<PP, kGradThreads, VEC>(static_cast<bf16_t *>(a.dv) + (ch.row * a.H + h) * a.P, int64_t(a.H) * a.P, tv, ch.len, a.P);
         }
+        if constexpr (!M::kFirst) {
+            if (hh + 1 < h1) {   // of the next head
+                if (place_d.carry) reach_d = __ldg(from_d.reach + 1);
+                if (place_s.carry) reach_s = __ldg(from_s.reach + 1);
+            }
+        }
         products_done(0);
         if constexpr (!M::kFirst) {
+            fence_tiles();
             __syncthreads();
+            if (tid == 32 && hh + 1 < h1) {   // all places are free but Q's and K's
+                tiles_put();
+                copy_head(h + 1);
+            }
             if (tid < kRows) sh.key[tid] = of_blocks(key_part, NB / 16);
             __syncthreads();
         }
@@ -1026,7 +1088,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             const float right = __shfl_down_sync(~0u, after, 1), left = __shfl_up_sync(~0u, before, 1);
             after = lane < 31 ? right : 0.f, before = lane > 0 ? left : 0.f;   // of the lanes behind and before
             for (int w = 0; w < 32; ++w) whole += sh.dots[w];
-            whole *= Gates128::exp_of(sh.w.g.hi[kRows - 1] + sh.w.g.lo[kRows - 1]);
+            whole *= sh.end[(hh - h0) & 1];
             float suffix[4];
 #pragma unroll
             for (int i = 3; i >= 0; --i) suffix[i] = after += x[i];
@@ -1121,26 +1183,35 @@ int segment_chunks(int64_t chunks, int64_t nseq, int H, int P)
     return best;
 }
 
-// Blocks for a group's heads: the gradients' blocks run one on an SM, in rounds
-// of a block's heads and about half a head's time for the group's own tiles.
-// Above 64 values of both kinds a block takes one head.
-int grad_splits(int64_t chunks, int H, int G, int N, int P)
+// Heads of a block of the gradients, of a group's: such blocks run one on an SM,
+// each for its heads' time and about half a head's for the group's own tiles.  A
+// group's last block may have fewer heads; those come after all others and run
+// where the others' last round leaves SMs.  Above 64 values of both kinds a
+// block takes one head.  (2x4096x32x128x64, G 1: 14, 14 and 4 heads of 32 in
+// two blocks' time less than 16 and 16: KEPT.)
+int grad_heads(int64_t chunks, int H, int G, int N, int P)
 {
     const int per = H / G;
-    if (N > 64 && P > 64) return per;
-    int best = 1;
+    if (N > 64 && P > 64) return 1;
+    const int64_t groups = chunks * G;
+    int best = per;
     double least = 1e300;
     for (int heads = per; heads >= 1; --heads) {
-        const int splits = int(ceil_div(per, heads));
-        const double t = double(ceil_div(chunks * G * splits, 152)) * (heads + 0.5);
-        if (t < least * 0.999) least = t, best = splits;
+        const int rest = per % heads;
+        const int64_t full = groups * (per / heads), rounds = full / 152, last = full % 152;
+        double t = double(rounds + (last > 0)) * (heads + 0.5);
+        if (rest > 0) {
+            const int64_t fit = last > 0 ? (152 - last) * int64_t((heads + 0.5) / (rest + 0.5)) : 0;
+            if (groups > fit) t += double(ceil_div(groups - fit, 152)) * (rest + 0.5);
+        }
+        if (t < least * 0.999) least = t, best = heads;
     }
     return best;
 }
 
 struct Plan {
     int64_t chunks, segments;
-    int m, splits;
+    int m, heads, splits;
     size_t first, seg_first, local, carry, reach, totals, sums, partial, end;   // of the workspace
     size_t s_carry, s_reach, s_sums, saved;                                       // of `saved`, whose local states come first
 };
@@ -1151,7 +1222,8 @@ Plan plan_of(int64_t B, int64_t T, int H, int G, int N, int P, int64_t nseq, boo
     w.chunks = chunks_most(B, T, nseq, packed, kRows);
     w.m = segment_chunks(w.chunks, nseq, H, P);
     w.segments = chunks_most(B, T, nseq, packed, kRows * w.m);
-    w.splits = bwd ? grad_splits(w.chunks, H, G, N, P) : 1;
+    w.heads = bwd ? grad_heads(w.chunks, H, G, N, P) : H / G;
+    w.splits = int(ceil_div(H / G, w.heads));
     const size_t table = packed ? align_up(size_t(nseq + 1) * 4, 256) : 0;
     w.first = kControlBytes, w.seg_first = w.first + table;
     w.totals = w.seg_first + table;
@@ -1243,7 +1315,7 @@ mg_status make_call(const GatedArgs &a, bool bwd, TcCall &p, cudaStream_t s)
     p.d = in_ws;
     p.starts = bwd || a.S0 != nullptr;
     p.partial = at(w.partial);
-    p.splits = w.splits, p.heads = int(ceil_div(a.H / a.G, w.splits));
+    p.splits = w.splits, p.heads = w.heads;
     p.error = &reinterpret_cast<Control *>(a.ws)->error;
     MG_TRY(check_grids(bwd ? "mg_gated_scan_bwd" : "mg_gated_scan_fwd",
                        {w.chunks * a.H, w.segments * a.H * ceil_div(a.P, 64), w.chunks * a.G * (w.splits > 1 && w.splits < kJoinBlocks ? kJoinBlocks : w.splits),
