@@ -1186,9 +1186,9 @@ int segment_chunks(int64_t chunks, int64_t nseq, int H, int P)
 // Heads of a block of the gradients, of a group's: such blocks run one on an SM,
 // each for its heads' time and about half a head's for the group's own tiles.  A
 // group's last block may have fewer heads; those come after all others and run
-// where the others' last round leaves SMs.  Above 64 values of both kinds a
-// block takes one head.  (2x4096x32x128x64, G 1: 14, 14 and 4 heads of 32 in
-// two blocks' time less than 16 and 16: KEPT.)
+// where the others' last round leaves SMs (2x4096 rows, a group of 32 heads of
+// 128 x 64: parts of 14, 14 and 4 heads 155 us and 12 for joining them, two of 16
+// 174 and 10).  Above 64 values of both kinds a block takes one head.
 int grad_heads(int64_t chunks, int H, int G, int N, int P)
 {
     const int per = H / G;

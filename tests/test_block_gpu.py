@@ -445,3 +445,91 @@ def test_refusals(cuda_lib):
               lambda: mg.rms_norm_fwd(x, w, out=(x, None, None))):
         with pytest.raises(mg.MgScanError):
             f()
+
+
+# --------------------------------------- blocks of several heads, big buffers
+
+@pytest.mark.parametrize("sizes", [(20, 129, 5, 1, 16, 8), (20, 129, 5, 1, 17, 9), (20, 129, 5, 1, 72, 16), (20, 129, 5, 1, 16, 72),
+                                   (20, 129, 9, 1, 40, 24), (20, 128, 18, 2, 8, 8)], ids=str)
+def test_groups_of_heads_in_parts(cuda_lib, sizes):
+    """Batches whose gradients take a group's heads in parts of several, the last
+    one smaller, with and without rows on 16-byte boundaries."""
+    Scan(cuda_lib, *sizes, dtype=BF16, seed=31).check()
+
+
+def test_groups_of_heads_in_parts_packed(cuda_lib):
+    cu = [0] + list(np.cumsum([129, 1, 0, 128, 257, 300] * 4))
+    Scan(cuda_lib, 1, int(cu[-1]), 9, 1, 24, 16, dtype=BF16, cu=[int(x) for x in cu], seed=32).check()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_two_calls_at_once(cuda_lib, dtype):
+    """Different inputs on two streams, the calls of both in flight together."""
+    mg, n = cuda_lib, 6
+    cases = [Scan(mg, 2, 300, 4, 2, 64, 64, dtype=dtype, seed=33 + i) for i in range(2)]
+    norms = [_norm_case(500, 384, dtype, 0, 35 + i) for i in range(2)]
+
+    def calls(c, norm):
+        x, res, w, dy, dr = norm
+        oo, last, saved = mg.gated_scan_fwd(c.q, c.k, c.v, c.g, c.S0, scale=c.scale, save=True)
+        _, r, rstd = mg.rms_norm_fwd(x, w, res)
+        return [oo, last, *mg.gated_scan_bwd(c.do, saved, c.q, c.k, c.v, c.g, c.S0, c.dl, scale=c.scale), *mg.rms_norm_bwd(dy, rstd, r, w, dr)]
+
+    want = [calls(c, x) for c, x in zip(cases, norms)]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(n):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(calls(cases[i], norms[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for g in got[i] for a, b in zip(g, want[i]))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_rows_far_apart(cuda_lib, dtype):
+    """Row offsets beyond 2^31 values: the same bits as from dense rows."""
+    mg, T, H, N, P = cuda_lib, 2200, 2, 24, 40
+    wide = torch.empty(1, T, 1 << 20, dtype=dtype, device=DEV)
+    gen = torch.Generator(DEV).manual_seed(37)
+    at, far = 0, []
+    for width in (N, N, P, P):
+        part = wide[..., at:at + H * width]
+        part.copy_(torch.randn(1, T, H * width, generator=gen, device=DEV))
+        far.append(part.unflatten(-1, (H, width)))
+        at += H * width
+    g = torch.nn.functional.logsigmoid(torch.randn(1, T, H, generator=gen, device=DEV) + 2)
+    got = []
+    for q, k, v, do in (far, [t.contiguous() for t in far]):
+        oo, last, saved = mg.gated_scan_fwd(q, k, v, g, save=True)
+        got.append([oo, last, *mg.gated_scan_bwd(do, saved, q, k, v, g)[:4]])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    x, res, dy = (wide[0, :, i * 96:(i + 1) * 96] for i in range(1, 4))
+    w = torch.randn(96, generator=gen, device=DEV)
+    for t in (x, res, dy):
+        t.normal_(generator=gen)
+    got = []
+    for a, b, c in ((x, res, dy), tuple(t.contiguous() for t in (x, res, dy))):
+        y, r, rstd = mg.rms_norm_fwd(a, w, b)
+        q8, sc, _ = mg.rms_norm_quant(a, w, b, block=32)
+        got.append([y, r, rstd, q8.view(torch.uint8), sc, *mg.rms_norm_bwd(c, rstd, r, w, b)])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_a_pool_of_many_states(cuda_lib):
+    """Slots whose states begin beyond 2^31 values."""
+    mg, H, N, P = cuda_lib, 32, 128, 128
+    pool = torch.empty(4100, H, N, P, device=DEV)
+    slots = torch.tensor([4099, 0, -1, 4096, 1 << 40], device=DEV)
+    gen = torch.Generator(DEV).manual_seed(38)
+    q, k = (torch.randn(5, 4, N, generator=gen, device=DEV) for _ in range(2))
+    v, g = torch.randn(5, H, P, generator=gen, device=DEV), -torch.rand(5, H, generator=gen, device=DEV)
+    own = torch.randn(5, H, N, P, generator=gen, device=DEV)
+    for i in (0, 1, 3):
+        pool[slots[i]] = own[i]
+    want = mg.gated_scan_step(q, k, v, g, own, scale=0.1)
+    got = mg.gated_scan_step(q, k, v, g, pool, slots=slots, scale=0.1)
+    assert torch.equal(got[[0, 1, 3]], want[[0, 1, 3]]) and not got[[2, 4]].any()
+    assert all(torch.equal(pool[slots[i]], own[i]) for i in (0, 1, 3))
