@@ -333,46 +333,52 @@ __global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const __gri
             v[u] = fetch_piece<VEC>(from + r * ldv, tid & 7, cols, r < len);
         }
     };
-    // One warp, not the one that begins the products: the next chunks' gates (their
-    // sums, where the forward walk has left them), and the weights of the next one.
-    float ahead[2][8];
-    const auto next_gates = [&](int i, float (&to)[8]) {
+    // Two warps, not the one that begins the products, take the chunks' gates in
+    // turn: one adds up those of the chunk after the next, while the other turns
+    // the next one's sums into weights and asks for the gates of its chunk behind
+    // (one warp with both took longer than the products: walks of 64 and 60 us at
+    // 4x4096x16x128x128, now 62 and 57).  Backwards the forward walk's sums are there.
+    const int turn = warp - kGateWarp;   // chunks of this parity, if 0 or 1
+    float gates[8];
+    const auto next_gates = [&](int i) {
         if (i >= count) return;
         const int ci = chunk_at(i), len = s.len - ci * kRows < kRows ? s.len - ci * kRows : kRows;
         if constexpr (BACK) {
             const float *from = p.s.sums + (int64_t(c0 + ci) * a.H + h) * (2 * kRows) + 4 * lane;
             const float4 x = __ldg(reinterpret_cast<const float4 *>(from)), y = __ldg(reinterpret_cast<const float4 *>(from + kRows));
-            to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w, to[4] = y.x, to[5] = y.y, to[6] = y.z, to[7] = y.w;
+            gates[0] = x.x, gates[1] = x.y, gates[2] = x.z, gates[3] = x.w, gates[4] = y.x, gates[5] = y.y, gates[6] = y.z, gates[7] = y.w;
         } else {
-            fetch_gates(to, a.g + (s.row + int64_t(ci) * kRows) * a.ldg + h, a.ldg, len);
+            fetch_gates(gates, a.g + (s.row + int64_t(ci) * kRows) * a.ldg + h, a.ldg, len);
         }
     };
-    const auto weigh = [&](int i, const float (&of)[8]) {
-        float hi[4], lo[4];
-        if constexpr (BACK) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) hi[e] = of[e], lo[e] = of[4 + e];
-        } else {
-            const float g[4] = {gate_of(of[0]), gate_of(of[1]), gate_of(of[2]), gate_of(of[3])};
+    const auto add_gates = [&]() {
+        if constexpr (!BACK) {
+            const float g[4] = {gate_of(gates[0]), gate_of(gates[1]), gate_of(gates[2]), gate_of(gates[3])};
+            float hi[4], lo[4];
             sum_gates(g, hi, lo);
-            if (tile == 0) {
-                float *to = w.sums + (int64_t(c0 + chunk_at(i)) * a.H + h) * (2 * kRows) + 4 * lane;
-                store_vec<4>(to, hi), store_vec<4>(to + kRows, lo);
-            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) gates[e] = hi[e], gates[4 + e] = lo[e];
         }
-        const float th = __shfl_sync(~0u, hi[3], 31), tl = __shfl_sync(~0u, lo[3], 31);
+    };
+    const auto weigh = [&](int i) {
+        if (i >= count) return;
+        if (!BACK && tile == 0) {
+            float *to = w.sums + (int64_t(c0 + chunk_at(i)) * a.H + h) * (2 * kRows) + 4 * lane;
+            *reinterpret_cast<float4 *>(to) = make_float4(gates[0], gates[1], gates[2], gates[3]);
+            *reinterpret_cast<float4 *>(to + kRows) = make_float4(gates[4], gates[5], gates[6], gates[7]);
+        }
+        const float th = __shfl_sync(~0u, gates[3], 31), tl = __shfl_sync(~0u, gates[7], 31);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            sh.by[4 * lane + e] = BACK ? a.scale * Gates128::exp_of(hi[e] + lo[e]) : Gates128::exp_of((th - hi[e]) + (tl - lo[e]));
+            sh.by[4 * lane + e] = BACK ? a.scale * Gates128::exp_of(gates[e] + gates[4 + e]) : Gates128::exp_of((th - gates[e]) + (tl - gates[4 + e]));
         if (lane == 0) sh.whole = th, sh.whole_lo = tl;
     };
     copy_k(0);
     fetch_v(0);
-    if (warp == kGateWarp) {
-        next_gates(0, ahead[0]);
-        next_gates(1, ahead[1]);
-        weigh(0, ahead[0]);
-        next_gates(2, ahead[0]);
+    if (turn == 0 || turn == 1) {
+        next_gates(turn);
+        if (turn < count) add_gates();
+        if (turn == 0) weigh(0), next_gates(2);
     }
     float S[16];
 #pragma unroll
@@ -422,14 +428,11 @@ __global__ void __launch_bounds__(kWalkThreads, 2) gated_walk_kernel(const __gri
                 multiply(acc, Tile<kRows, true>{base + (i & 1) * kK}, Tile<kRows, true>{tv + k * kV}, 64, kRows / 16, k < 2);
             bar_after_products(&sh.bar);
         }
-        if (i + 1 < count && warp == kGateWarp) {   // everyone has read this chunk's
-            if (i & 1) {
-                weigh(i + 1, ahead[0]);
-                next_gates(i + 3, ahead[0]);
-            } else {
-                weigh(i + 1, ahead[1]);
-                next_gates(i + 3, ahead[1]);
-            }
+        if (turn == ((i + 1) & 1)) {   // everyone has read this chunk's
+            weigh(i + 1);
+            next_gates(i + 3);
+        } else if (turn == (i & 1) && i + 2 < count) {
+            add_gates();
         }
         // while the products run: the state that came to the chunk
         if (tid == 0 && tile == 0) w.reach[ch] = reach;
