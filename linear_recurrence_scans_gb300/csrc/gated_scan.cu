@@ -19,6 +19,14 @@
 // sequence of q . dq - k . dk gives the same, but its rounding errors grow
 // with the length.  The sums G are taken and kept as two floats, so
 // that a row that forgets everything costs the differences behind it nothing.
+//
+// The float32 kernels multiply with FFMA (the tensor cores' 10 or 7 bits would
+// take three to nine products for float32's) in chunks of 64 rows, by blocks of
+// 256 threads that hold a 64 x 64 product in 4 x 4 values each.  At 5003 rows in
+// one packed batch x 6 heads x 80 x 48 a call takes 75 us (2.8 us of bytes):
+// 510 blocks of each kernel are less than two rounds, and a block's chain of
+// loads, products and barriers is what it takes; 25 us for what chunks add, 40
+// for the outputs.  3x509x6x24x40 with gradients: 77 us for seven launches.
 #include "gated_scan.cuh"
 
 namespace mg {
@@ -502,6 +510,9 @@ __global__ void __launch_bounds__(256) gated_join_kernel(const float *part, int 
 
 // ------------------------------------------------------------------ tokens
 
+// Bytes bound it: the state is read and written once (256 x 32 heads of 128 x 64:
+// 82 us, 6.6 TB/s; one row of 16 heads of 128 x 128: 6.7 us, the latency of a launch
+// and of a load and a store).
 // A block takes a row's head: a state of N x P, walked by rows of P values, VEC
 // a thread; the threads beside each other in P share an n, and the others' sums
 // are joined at the end.

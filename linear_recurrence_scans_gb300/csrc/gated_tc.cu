@@ -262,6 +262,12 @@ __device__ __forceinline__ void wait_or_tell(uint64_t *bar, unsigned phase, unsi
 // A block: a segment, a head, 64 columns of its state, which stay in registers
 // (row n a lane, 16 columns a thread).  Each chunk adds K^T V~, the row weights
 // in V~'s three pieces; the next chunk's rows arrive meanwhile.
+//
+// 62 us at 4x4096x16x128x128 (209 MB, 3.4 TB/s; tensor pipe 20%).  A step is a
+// chain, V into pieces, products, the state, of about 7000 cycles, the same with
+// one block on an SM as with two; two blocks hide half of each other's.  Segments
+// cut the walks (of 32 chunks here) so that all SMs have two: with whole
+// sequences 107 us where segments took 67.
 
 constexpr int kWalkThreads = 512, kGateWarp = 4;
 
@@ -537,6 +543,10 @@ struct Weights {
 // A block: o of a chunk and head.  Q K^T, weights, times V, and Q S beside it;
 // the weights take Q's place in shared memory and V takes K's, so that two blocks
 // fit an SM and one's products run under the other's loads and exponentials.
+//
+// 77 us at 4x4096x16x128x128 (268 MB, 3.5 TB/s; tensor pipe 15%): a block's chain
+// of set-up, state, products, weights, products and output takes 21000 cycles, of
+// which loads are 7000.
 
 constexpr int kRowThreads = 512;
 
@@ -699,6 +709,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
 // and dg of each, dq and dk summed over them in tensor memory.  One block fits an
 // SM; the adjoint's and the state's pieces share a place (kX), which for N and
 // P above 64 is the weights' too.
+//
+// 237 us at 4x4096x16x128x128 (500 MB, 2.1 TB/s; tensor pipe 19%), 155 us at
+// 2x4096x32x128x64 with shared q and k.  28000 and 22000 cycles a head: loads of
+// states 8500 (and 1500, where the next head's adjoint is copied ahead), products
+// 6000 and 4000, the rest weights, pieces and sums over rows between barriers;
+// shared memory is full with one block, so that nothing else runs beside them.
 
 constexpr int kGradThreads = 1024;
 // The warp that begins the products: rows 0 to 31 and columns 112 on, which have
