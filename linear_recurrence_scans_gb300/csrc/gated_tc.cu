@@ -263,7 +263,7 @@ __device__ __forceinline__ void wait_or_tell(uint64_t *bar, unsigned phase, unsi
 // (row n a lane, 16 columns a thread).  Each chunk adds K^T V~, the row weights
 // in V~'s three pieces; the next chunk's rows arrive meanwhile.
 //
-// 62 us at 4x4096x16x128x128 (209 MB, 3.4 TB/s; tensor pipe 20%).  A step is a
+// 62 us at 4x4096x16x128x128 (264 MB, 4.3 TB/s; tensor pipe 21%).  A step is a
 // chain, V into pieces, products, the state, of about 7000 cycles, the same with
 // one block on an SM as with two; two blocks hide half of each other's.  Segments
 // cut the walks (of 32 chunks here) so that all SMs have two: with whole
@@ -544,9 +544,9 @@ struct Weights {
 // the weights take Q's place in shared memory and V takes K's, so that two blocks
 // fit an SM and one's products run under the other's loads and exponentials.
 //
-// 77 us at 4x4096x16x128x128 (268 MB, 3.5 TB/s; tensor pipe 15%): a block's chain
-// of set-up, state, products, weights, products and output takes 21000 cycles, of
-// which loads are 7000.
+// 77 us at 4x4096x16x128x128 (403 MB, 5.2 TB/s of 6.8; tensor pipe 14%): memory,
+// and a block's chain of set-up, state, products, weights, products and output,
+// 21000 cycles of which two blocks hide half.
 
 constexpr int kRowThreads = 512;
 
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
 // SM; the adjoint's and the state's pieces share a place (kX), which for N and
 // P above 64 is the weights' too.
 //
-// 237 us at 4x4096x16x128x128 (500 MB, 2.1 TB/s; tensor pipe 19%), 155 us at
+// 237 us at 4x4096x16x128x128 (738 MB, 3.1 TB/s; tensor pipe 19%), 155 us at
 // 2x4096x32x128x64 with shared q and k.  28000 and 22000 cycles a head: loads of
 // states 8500 (and 1500, where the next head's adjoint is copied ahead), products
 // 6000 and 4000, the rest weights, pieces and sums over rows between barriers;

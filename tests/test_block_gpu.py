@@ -533,3 +533,22 @@ def test_a_pool_of_many_states(cuda_lib):
     got = mg.gated_scan_step(q, k, v, g, pool, slots=slots, scale=0.1)
     assert torch.equal(got[[0, 1, 3]], want[[0, 1, 3]]) and not got[[2, 4]].any()
     assert all(torch.equal(pool[slots[i]], own[i]) for i in (0, 1, 3))
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_signalling_nans_do_not_pass_through_a_workspace(cuda_lib, dtype):
+    """Gates and states whose bits are those of a look-back record's tag, then a
+    scan that looks back in the same workspace: its results are a fresh one's."""
+    mg = cuda_lib
+    c = Scan(mg, 1, 700, 4, 2, 32, 32, dtype=dtype, seed=39)
+    a, b = torch.rand(2, 700, 96, device=DEV), torch.randn(2, 700, 96, device=DEV)
+    want = mg.linear_scan_fwd(a, b)
+    size = max(mg.load().mg_gated_scan_workspace_size(1, 700, 4, 2, 32, 32, 1, 0, mg._DT[dtype], back) for back in (0, 1))
+    ws = mg.new_workspace(max(size, mg.linear_workspace_size(2, 700, 96)), device=DEV)
+    for epoch in range(1, 5):
+        for t in (c.g, c.S0, c.dl):
+            t.view(torch.int32).fill_((0xffa00000 | epoch) - (1 << 32))
+        _, _, saved = mg.gated_scan_fwd(c.q, c.k, c.v, c.g, c.S0, scale=c.scale, save=True, ws=ws)
+        mg.gated_scan_bwd(c.do, saved, c.q, c.k, c.v, c.g, c.S0, c.dl, scale=c.scale, ws=ws)
+        got = mg.linear_scan_fwd(a, b, ws=ws)
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
