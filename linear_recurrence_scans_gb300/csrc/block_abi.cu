@@ -76,6 +76,7 @@ size_t mg_gated_scan_saved_size(int64_t B, int64_t T, int64_t H, int64_t N, int6
     if (check_type(fn, dt) != MG_OK || check_gated(fn, B, T, H, 1, N, P) != MG_OK || nseq < 0 ||
         nseq > INT32_MAX - 1 || B * T / 64 + nseq > INT32_MAX)
         return 0;
+    if (B == 0 || T == 0 || H == 0) return 0;
     return gated_saved_bytes(B, T, H, N, P, nseq, packed != 0, dt);
 }
 
