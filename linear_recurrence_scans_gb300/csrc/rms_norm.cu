@@ -15,6 +15,7 @@
 #include <type_traits>
 
 #include "block.cuh"
+#include "flat_rows.h"
 #include "umma.cuh"
 
 namespace mg {
@@ -103,8 +104,9 @@ struct Held {
         }
     }
     // The same of a row that lies in shared memory from its 16-byte boundary on,
-    // `shift` values before it; `rest`: the row itself, for what the copy left out.
-    __device__ __forceinline__ void take(const T *copy, int shift, int i, int D, const T *rest, bool last)
+    // `shift` values before it; `rest`: the row itself, for the piece that the copy
+    // left out, from value `stop` on.
+    __device__ __forceinline__ void take(const T *copy, int shift, int i, int D, const T *rest, int stop)
     {
         if constexpr (R != kSingle) {
 #pragma unroll
@@ -112,7 +114,7 @@ struct Held {
                 const int at = i + c * LV;
                 if (R != kFlat || (at >= 0 && at + LV <= D)) {
                     w[c].load(copy + at + shift);
-                } else if (last) {
+                } else if (at >= stop) {
                     edge(w[c], rest, at, D);
                 } else {
                     edge(w[c], copy + shift, at, D);
@@ -322,9 +324,9 @@ __global__ void __launch_bounds__(WARP ? 256 : 1024, 1) rms_fwd_kernel(const Rms
 // Gradients: teams walk over rows and keep their channels' sums for dw; a block
 // leaves one row of sums.  The next STAGES rows come by bulk copies into shared
 // memory, so that a row's barrier does not hold up its successors: a flat row from
-// the 16-byte boundary before it to the one behind it.  (A row ahead in registers:
-// 125 us for 32768 x 2048 bf16 rows; 16-byte asynchronous copies by all threads:
-// 116 us, and 160 for 16384 x 2048 float32 ones.)  The teams' number is a multiple
+// the 16-byte boundary before it to the one behind it (flat_rows.h).  (A row ahead
+// in registers: 125 us for 32768 x 2048 bf16 rows; 16-byte asynchronous copies by
+// all threads: 116 us, and 160 for 16384 x 2048 float32 ones.)  The teams' number is a multiple
 // of 8, so that a team's rows all begin at the same place between two boundaries.
 // Single values are loaded as they are needed.
 template <typename T, Rows R, int NV, bool WARP, int STAGES, int MOST>
@@ -345,10 +347,8 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? 2 : 1) rms_bwd_kernel(cons
     const auto slot = [&](int stage, int k) { return reinterpret_cast<T *>(ring + (warp * STAGES + stage) * stage_bytes + k * slot_bytes); };
     const auto fetch = [&](int stage, int64_t r) {   // one thread of the team
         if (R == kSingle || r >= p.M) return;
-        // what lies in the row's 16-byte pieces, but for the array's last one if that is not whole
-        const int64_t end = r * p.D + p.D, whole = R == kFlat && r + 1 == p.M ? end / kWide<T> * kWide<T> : (end + kWide<T> - 1) / kWide<T> * kWide<T>;
-        const int64_t begin = r * p.D - shift;
-        const unsigned bytes = R == kFlat ? (whole > begin ? unsigned((whole - begin) * sizeof(T)) : 0) : unsigned(D * sizeof(T));
+        const int64_t pieces = flat_copy_end(r, p.D, p.M, kWide<T>) - flat_copy_begin(r, p.D, kWide<T>);
+        const unsigned bytes = R == kFlat ? (pieces > 0 ? unsigned(pieces * sizeof(T)) : 0) : unsigned(D * sizeof(T));
         bar_expect(&full[warp][stage], bytes * (p.dr != nullptr ? 3 : 2));
         if (bytes == 0) return;
         copy_bytes(smem_addr(slot(stage, 0)), static_cast<const T *>(p.dy) + r * p.lddy - shift, bytes, &full[warp][stage]);
@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? 2 : 1) rms_bwd_kernel(cons
         }
         const T *gdy = static_cast<const T *>(p.dy) + row * p.lddy, *gx = static_cast<const T *>(p.x) + row * p.ldx;
         const T *gdr = p.dr != nullptr ? static_cast<const T *>(p.dr) + row * p.lddr : nullptr;
+        const int stop = R == kFlat ? int(flat_copy_end(row, p.D, p.M, kWide<T>) - row * p.D) : D;
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -391,9 +392,8 @@ __global__ void __launch_bounds__(MOST, MOST == 256 ? 2 : 1) rms_bwd_kernel(cons
                 dy[i].load(gdy, at, D), x[i].load(gx, at, D);
                 if (gdr != nullptr) dr[i].load(gdr, at, D);
             } else {
-                const bool last = row + 1 == p.M;
-                dy[i].take(slot(stage, 0), shift, at, D, gdy, last), x[i].take(slot(stage, 1), shift, at, D, gx, last);
-                if (gdr != nullptr) dr[i].take(slot(stage, 2), shift, at, D, gdr, last);
+                dy[i].take(slot(stage, 0), shift, at, D, gdy, stop), x[i].take(slot(stage, 1), shift, at, D, gx, stop);
+                if (gdr != nullptr) dr[i].take(slot(stage, 2), shift, at, D, gdr, stop);
             }
             if (!kKeepW) load_w<R>(p.w, at, D, w[0]);
 #pragma unroll

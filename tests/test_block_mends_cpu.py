@@ -2,6 +2,8 @@
 sizes of nothing, copies' ranges, calls by name (no GPU needed)."""
 from __future__ import annotations
 
+import subprocess
+
 import pytest
 
 import linear_recurrence_scans_gb300 as mg
@@ -22,3 +24,34 @@ def test_sizes_of_nothing(lib, B, T, H, dt):
         assert lib.mg_gated_scan_saved_size(B, T, H, 16, 16, B, packed, dt) == 0
         for bwd in (0, 1):
             assert lib.mg_gated_scan_workspace_size(B, T, H, 1, 16, 16, B, packed, dt, bwd) == 256
+
+
+FLAT = r"""
+#include "flat_rows.h"
+#include <cstdio>
+int main()
+{
+    long bad = 0;
+    for (int wide = 4; wide <= 8; wide += 4)
+        for (long D = 1; D < 200; ++D)
+            for (long M = 1; M < 70; ++M)
+                for (long r = 0; r < M; ++r) {
+                    const long b = mg::flat_copy_begin(r, D, wide), e = mg::flat_copy_end(r, D, M, wide);
+                    bad += b % wide != 0 || e % wide != 0 || b < 0 || b > r * D;
+                    if (e > b) bad += e > M * D || e - b > D + 2 * wide - 2;      // the array's end; a slot's room
+                    // what is left out: less than a piece, of the array's last one
+                    for (long v = r * D; v < (r + 1) * D; ++v)
+                        if (v >= e) bad += v < M * D / wide * wide;
+                }
+    std::printf("%ld\n", bad);
+}
+"""
+
+
+def test_copies_of_flat_rows_stay_in_the_array(tmp_path):
+    """The ranges that the norm's gradients copy (csrc/flat_rows.h), compiled as
+    the kernels compile them."""
+    from linear_recurrence_scans_gb300 import _build
+    (tmp_path / "flat.cpp").write_text(FLAT)
+    subprocess.run(["g++", "-std=c++17", "-I", _build.CSRC, "-o", tmp_path / "flat", tmp_path / "flat.cpp"], check=True)
+    assert subprocess.run([tmp_path / "flat"], capture_output=True, text=True, check=True).stdout == "0\n"

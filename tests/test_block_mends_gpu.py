@@ -1,8 +1,12 @@
-"""GPU checks of the gated block's operators beside test_block_gpu.py's."""
+"""GPU checks of the gated block's operators beside test_block_gpu.py's, whose
+tolerances they take where they name none."""
 from __future__ import annotations
 
 import pytest
 import torch
+
+from oracle import block as o
+from test_block_gpu import _near, _np
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -21,3 +25,23 @@ def test_no_heads(cuda_lib, dtype):
     nan = lambda: torch.full_like(q, float("nan"))  # noqa: E731
     dq, dk, dv, dg, _ = mg.gated_scan_bwd(v, saved, q, q, v, g, out=(nan(), nan(), None, None, None))
     assert not dq.any() and not dk.any() and dv.shape == v.shape and dg.shape == g.shape
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("D", range(1, 10))
+def test_gradients_of_narrow_rows(cuda_lib, D, dtype):
+    """Rows narrower than a 16-byte piece, several of them in the array's last
+    one; behind each array lie NaNs."""
+    mg = cuda_lib
+    for M in (1, 2, 3, 5, 10, 11, 37, 64, 701):
+        def rows():
+            wide = torch.full((M * D + 64,), float("nan"), device=DEV, dtype=dtype)
+            wide[:M * D].copy_(torch.randn(M * D, device=DEV))
+            return wide[:M * D].view(M, D)
+        torch.manual_seed(100 * D + M)
+        dy, r, dr, w = rows(), rows(), rows(), 1 + 0.1 * torch.randn(D, device=DEV)
+        rstd = mg.rms_norm_fwd(r, w)[2]
+        dx, dw = mg.rms_norm_bwd(dy, rstd, r, w, dr)
+        args = (*(_np(t) for t in (dy, r, w)), 1e-5, _np(dr))
+        for name, a, b, s in zip(("dx", "dw"), (dx, dw), o.norm_bwd(*args), o.norm_bwd(*args, absolute=True)):
+            _near(name, a, b, s, D if name == "dx" else M)
