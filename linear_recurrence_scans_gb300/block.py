@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import struct
 
 import torch
@@ -42,18 +43,25 @@ MAX_HEAD = 128                      # values of a head's q, k and v
 BLOCKS = (32, 64, 128, 256)         # channels that may share a scale
 _E4M3 = torch.float8_e4m3fn
 
+
 def _on_its_device(f):
     """Makes a call on its stream, where one is given, and with its first
-    tensor's device current."""
+    tensor's device current; adds the argument `stream`."""
+    shown = inspect.signature(f)
+    first = next(iter(shown.parameters))
+
     @functools.wraps(f)
-    def call(x, *args, stream=None, **more):
+    def call(*args, stream=None, **more):
+        x = args[0] if args else more.get(first)
         if stream is not None:
             with torch.cuda.stream(stream):
-                return call(x, *args, **more)
+                return call(*args, **more)
         if isinstance(x, Tensor) and x.is_cuda and x.get_device() != torch.cuda.current_device():
             with torch.cuda.device(x.device):
-                return f(x, *args, **more)
-        return f(x, *args, **more)
+                return f(*args, **more)
+        return f(*args, **more)
+    call.__signature__ = shown.replace(parameters=[*shown.parameters.values(),
+                                                   inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return call
 
 

@@ -2,9 +2,11 @@
 sizes of nothing, copies' ranges, calls by name (no GPU needed)."""
 from __future__ import annotations
 
+import inspect
 import subprocess
 
 import pytest
+import torch
 
 import linear_recurrence_scans_gb300 as mg
 
@@ -55,3 +57,20 @@ def test_copies_of_flat_rows_stay_in_the_array(tmp_path):
     (tmp_path / "flat.cpp").write_text(FLAT)
     subprocess.run(["g++", "-std=c++17", "-I", _build.CSRC, "-o", tmp_path / "flat", tmp_path / "flat.cpp"], check=True)
     assert subprocess.run([tmp_path / "flat"], capture_output=True, text=True, check=True).stdout == "0\n"
+
+
+CALLS = ("gated_scan_fwd", "gated_scan_bwd", "gated_scan_step", "rms_norm_fwd", "rms_norm_quant", "rms_norm_bwd")
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_every_argument_has_its_name(name):
+    """What the signature shows may be given by name, the first tensor and the
+    stream too: the call gets as far as its checks of tensors."""
+    f = getattr(mg, name)
+    shown = inspect.signature(f).parameters
+    assert "stream" in shown
+    tensors = {n: torch.zeros(1, 1, 1, 1) for n, p in shown.items() if p.default is inspect.Parameter.empty}
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
+        f(**tensors, stream=None)
+    with pytest.raises(TypeError, match="missing"):
+        f()

@@ -45,3 +45,27 @@ def test_gradients_of_narrow_rows(cuda_lib, D, dtype):
         args = (*(_np(t) for t in (dy, r, w)), 1e-5, _np(dr))
         for name, a, b, s in zip(("dx", "dw"), (dx, dw), o.norm_bwd(*args), o.norm_bwd(*args, absolute=True)):
             _near(name, a, b, s, D if name == "dx" else M)
+
+
+def test_calls_by_name(cuda_lib):
+    """Every argument by its name gives the bits of the same call by position."""
+    mg = cuda_lib
+    q, k, do, v = (torch.randn(1, 9, 2, 8, device=DEV) for _ in range(4))
+    g, S0, side = -torch.rand(1, 9, 2, device=DEV), torch.randn(1, 2, 8, 8, device=DEV), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    want, got = mg.gated_scan_fwd(q, k, v, g, S0, save=True), mg.gated_scan_fwd(q=q, k=k, v=v, g=g, S0=S0, save=True, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    want, got = mg.gated_scan_bwd(do, want[2], q, k, v, g, S0), mg.gated_scan_bwd(do=do, saved=want[2], q=q, k=k, v=v, g=g, S0=S0)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    pools = S0.clone(), S0.clone()
+    row = dict(q=q[:, 0], k=k[:, 0], v=v[:, 0], g=g[:, 0])
+    assert torch.equal(mg.gated_scan_step(*row.values(), pools[0]), mg.gated_scan_step(**row, state=pools[1])) and torch.equal(*pools)
+    x, w, residual = torch.randn(4, 64, device=DEV), torch.rand(64, device=DEV), torch.randn(4, 64, device=DEV)
+    want, got = mg.rms_norm_fwd(x, w, residual), mg.rms_norm_fwd(x=x, w=w, residual=residual)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    _, r, rstd = want
+    want, got = mg.rms_norm_bwd(x, rstd, r, w), mg.rms_norm_bwd(dy=x, rstd=rstd, r=r, w=w)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    want, got = mg.rms_norm_quant(x, w, residual), mg.rms_norm_quant(x=x, w=w, residual=residual)
+    assert all(torch.equal(a.float(), b.float()) for a, b in zip(got, want))
