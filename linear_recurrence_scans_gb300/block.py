@@ -54,6 +54,8 @@ def _on_its_device(f):
     def call(*args, stream=None, **more):
         x = args[0] if args else more.get(first)
         if stream is not None:
+            if isinstance(x, Tensor) and x.is_cuda and stream.device != x.device:
+                raise ValueError("the stream must be on the tensors' device")
             with torch.cuda.stream(stream):
                 return call(*args, **more)
         if isinstance(x, Tensor) and x.is_cuda and x.get_device() != torch.cuda.current_device():

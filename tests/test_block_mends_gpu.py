@@ -69,3 +69,14 @@ def test_calls_by_name(cuda_lib):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     want, got = mg.rms_norm_quant(x, w, residual), mg.rms_norm_quant(x=x, w=w, residual=residual)
     assert all(torch.equal(a.float(), b.float()) for a, b in zip(got, want))
+
+
+def test_a_stream_of_another_device_is_refused(cuda_lib):
+    """The call would run on its tensors' device, behind none of that stream's work."""
+    class Other:
+        device, cuda_stream = torch.device("cuda", torch.cuda.device_count()), 0
+    x, w = torch.randn(4, 64, device=DEV), torch.rand(64, device=DEV)
+    with pytest.raises(ValueError, match="stream must be on"):
+        cuda_lib.rms_norm_fwd(x, w, stream=Other())
+    with pytest.raises(ValueError, match="stream must be on"):
+        cuda_lib.rms_norm_fwd(x=x, w=w, stream=Other())
