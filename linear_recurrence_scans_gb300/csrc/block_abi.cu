@@ -1,5 +1,7 @@
 // The C entry points of mg_block.h: argument validation (all of it before any
 // launch) and the calls without rows.
+#include <cmath>
+
 #include "abi_calls.cuh"
 #include "block.cuh"
 
@@ -29,9 +31,10 @@ mg_status check_gated_seqs(const char *fn, const int64_t *cu, int64_t nseq, int6
     return check_size(fn, nseq, H * N * P);
 }
 
+// A factor that the kernels take as a float.
 mg_status check_scale(const char *fn, double v, const char *name)
 {
-    return v - v == 0.0 ? MG_OK : fail(MG_ERR_INVALID_ARG, "%s: %s must be finite", fn, name);
+    return std::isfinite(float(v)) ? MG_OK : fail(MG_ERR_INVALID_ARG, "%s: %s must be finite in float32", fn, name);
 }
 
 mg_status check_rms(const char *fn, int64_t M, int64_t D)
@@ -50,8 +53,8 @@ mg_status check_rms_in(const char *fn, const void *res, int64_t ldx, int64_t ldr
     if (res != nullptr) MG_TRY(check_ld(fn, "res", ldres, D));
     if (M > 0 && D > 0 && (res == nullptr) != (r == nullptr))
         return fail(MG_ERR_INVALID_ARG, "%s: r goes with res", fn);
-    if (!(eps >= 0.0) || eps - eps != 0.0) return fail(MG_ERR_INVALID_ARG, "%s: eps must be finite and not negative", fn);
-    return MG_OK;
+    if (eps < 0.0) return fail(MG_ERR_INVALID_ARG, "%s: eps must not be negative", fn);
+    return check_scale(fn, eps, "eps");
 }
 
 }  // namespace

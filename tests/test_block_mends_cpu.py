@@ -74,3 +74,21 @@ def test_every_argument_has_its_name(name):
         f(**tensors, stream=None)
     with pytest.raises(TypeError, match="missing"):
         f()
+
+
+@pytest.mark.parametrize("value", [1e39, -1e39, 3.5e38, float("inf"), float("nan")])
+def test_factors_beyond_float32(lib, value):
+    """scale and eps are float32 in the kernels: what is infinite there is refused."""
+    at = lambda i: (1 << 40) + (i << 34)  # noqa: E731
+    size = (2, 6, 4, 2, 4, 3)
+    fwd = lib.mg_gated_scan_fwd(at(1), 8, at(2), 8, at(3), 12, at(4), 4, 0, value, None, None, 2, at(5), at(6), None, *size, at(7), 1 << 30, None)
+    assert fwd == mg.MG_ERR_INVALID_ARG and b"scale" in lib.mg_last_error_detail()
+    bwd = lib.mg_gated_scan_bwd(at(1), 12, at(2), at(3), 8, at(4), 8, at(5), 12, at(6), 4, 0, value, None, None, 2, at(7), at(8), at(9), at(10), None,
+                                *size, at(11), 1 << 30, None)
+    assert bwd == mg.MG_ERR_INVALID_ARG and b"scale" in lib.mg_last_error_detail()
+    step = lib.mg_gated_scan_step(at(1), 8, at(2), 8, at(3), 12, at(4), 4, 0, value, at(5), 4, at(6), at(7), 2, 4, 2, 4, 3, None)
+    assert step == mg.MG_ERR_INVALID_ARG and b"scale" in lib.mg_last_error_detail()
+    norm = lib.mg_rms_norm_fwd(at(1), 64, None, 64, 0, at(3), value, at(4), None, None, 6, 64, None)
+    assert norm == mg.MG_ERR_INVALID_ARG and b"eps" in lib.mg_last_error_detail()
+    quant = lib.mg_rms_norm_quant(at(1), 64, None, 64, 0, at(3), value, at(4), at(5), None, 32, 6, 64, None)
+    assert quant == mg.MG_ERR_INVALID_ARG and b"eps" in lib.mg_last_error_detail()
