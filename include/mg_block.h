@@ -81,7 +81,7 @@ mg_status mg_gated_scan_step(const void *q, int64_t ldq, const void *k, int64_t 
                              cudaStream_t stream);
 
 /*
- * Root-mean-square norm behind a residual's addition, rows of D <= 16384
+ * Root-mean-square norm behind a residual's addition, rows of 1 <= D <= 16384
  * channels:
  *   r = x + res, rounded to dt (r = x without res),  y = r rstd w,
  *   rstd = (mean(r^2) + eps)^(-1/2)

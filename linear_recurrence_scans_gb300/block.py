@@ -257,7 +257,7 @@ def _norm_in(x, w, residual, out):
     if w is None:
         raise ValueError("w must be (D,)")
     _together(x, residual, w, *(out or ()))
-    return (x, residual, w), (px, ldx, pr, ldr, _DT[x.dtype], pw), x.numel() // D if D else 0, D
+    return (x, residual, w), (px, ldx, pr, ldr, _DT[x.dtype], pw), x.shape[:-1].numel(), D
 
 
 @_on_its_device

@@ -53,6 +53,7 @@ mg_status check_rms_in(const char *fn, const void *res, int64_t ldx, int64_t ldr
     if (res != nullptr) MG_TRY(check_ld(fn, "res", ldres, D));
     if (M > 0 && D > 0 && (res == nullptr) != (r == nullptr))
         return fail(MG_ERR_INVALID_ARG, "%s: r goes with res", fn);
+    if (M > 0 && D == 0) return fail(MG_ERR_INVALID_ARG, "%s: rows without channels have no mean", fn);
     if (eps < 0.0) return fail(MG_ERR_INVALID_ARG, "%s: eps must not be negative", fn);
     return check_scale(fn, eps, "eps");
 }
@@ -209,7 +210,7 @@ mg_status mg_rms_norm_fwd(const void *x, int64_t ldx, const void *res, int64_t l
     MG_TRY(check_type(fn, dt));
     MG_TRY(check_rms(fn, M, D));
     MG_TRY(check_rms_in(fn, res, ldx, ldres, r, eps, M, D));
-    if (M == 0 || D == 0) return MG_OK;
+    if (M == 0) return MG_OK;
     const size_t es = esize(dt), n = size_t(M) * D * es;
     const bool in_place = res != nullptr && res == r && ldres == D;
     MG_TRY(check_bufs(fn, {{x, extent(M, ldx, D, es), "x", false},
@@ -239,7 +240,7 @@ mg_status mg_rms_norm_quant(const void *x, int64_t ldx, const void *res, int64_t
     if (block != 0 && D % block != 0)
         return fail(MG_ERR_INVALID_ARG, "%s: D = %lld is not a multiple of the block of %lld", fn, (long long)D,
                     (long long)block);
-    if (M == 0 || D == 0) return MG_OK;
+    if (M == 0) return MG_OK;
     const size_t es = esize(dt), n = size_t(M) * D;
     const bool in_place = res != nullptr && res == r && ldres == D;
     MG_TRY(check_bufs(fn, {{x, extent(M, ldx, D, es), "x", false},

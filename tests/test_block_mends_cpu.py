@@ -92,3 +92,13 @@ def test_factors_beyond_float32(lib, value):
     assert norm == mg.MG_ERR_INVALID_ARG and b"eps" in lib.mg_last_error_detail()
     quant = lib.mg_rms_norm_quant(at(1), 64, None, 64, 0, at(3), value, at(4), at(5), None, 32, 6, 64, None)
     assert quant == mg.MG_ERR_INVALID_ARG and b"eps" in lib.mg_last_error_detail()
+
+
+def test_rows_without_channels(lib):
+    """They have no mean: refused, as their statistics would stay unwritten."""
+    at = lambda i: (1 << 40) + (i << 34)  # noqa: E731
+    assert lib.mg_rms_norm_fwd(at(1), 0, None, 0, 0, at(2), 1e-5, at(3), None, at(4), 6, 0, None) == mg.MG_ERR_INVALID_ARG
+    assert b"channels" in lib.mg_last_error_detail()
+    assert lib.mg_rms_norm_quant(at(1), 0, None, 0, 1, at(2), 1e-5, at(3), at(4), None, 0, 6, 0, None) == mg.MG_ERR_INVALID_ARG
+    assert lib.mg_rms_norm_fwd(None, 0, None, 0, 0, None, 1e-5, None, None, None, 0, 0, None) == mg.MG_OK
+    assert lib.mg_rms_norm_fwd(None, 64, None, 64, 0, None, 1e-5, None, None, None, 0, 64, None) == mg.MG_OK

@@ -80,3 +80,13 @@ def test_a_stream_of_another_device_is_refused(cuda_lib):
         cuda_lib.rms_norm_fwd(x, w, stream=Other())
     with pytest.raises(ValueError, match="stream must be on"):
         cuda_lib.rms_norm_fwd(x=x, w=w, stream=Other())
+
+
+def test_rows_without_channels(cuda_lib):
+    mg = cuda_lib
+    x, w = torch.empty(3, 0, device=DEV), torch.empty(0, device=DEV)
+    with pytest.raises(mg.MgScanError, match="channels"):
+        mg.rms_norm_fwd(x, w)
+    with pytest.raises(mg.MgScanError, match="channels"):
+        mg.rms_norm_quant(x, w, x)
+    assert mg.rms_norm_fwd(torch.empty(2, 0, 8, device=DEV), torch.rand(8, device=DEV))[2].shape == (2, 0)
