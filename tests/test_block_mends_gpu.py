@@ -2,11 +2,12 @@
 tolerances they take where they name none."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
 from oracle import block as o
-from test_block_gpu import _near, _np
+from test_block_gpu import SIZES, Scan, _near, _np
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -90,3 +91,44 @@ def test_rows_without_channels(cuda_lib):
     with pytest.raises(mg.MgScanError, match="channels"):
         mg.rms_norm_quant(x, w, x)
     assert mg.rms_norm_fwd(torch.empty(2, 0, 8, device=DEV), torch.rand(8, device=DEV))[2].shape == (2, 0)
+
+
+# ------------------------------------------------------- the gates' gradients
+
+def _near_dg(c, dg, heads=slice(None)):
+    """Each head's dg as a whole.  dg_t is a sum over the rows of t's chunk of the
+    products q_n dq_n and k_n dk_n, each of which carries errors of its own, of no
+    common sign: together 2^-24 sqrt(count) of the products' norm; 4 times that.
+    The bound is far below dg itself, or the check would say nothing."""
+    H = c.nv.shape[2]
+    q, k = (np.repeat(x, H // x.shape[2], 2) for x in (c.nq, c.nk))
+    dq, dk, _, want, _ = o.scan_bwd(c.ndo, q, k, c.nv, c.ng, c.scale, c.nS0, c.ndl, c.sp)
+    squares, near = ((q * dq) ** 2 + (k * dk) ** 2).sum(-1), np.zeros_like(want)
+    chunk = 128 if c.dtype == BF16 else 64
+    for b, lo, hi in c.sp:
+        for at in range(lo, hi, chunk):
+            end = min(hi, at + chunk)
+            near[b, at:end] = squares[b, at:end].sum(0)
+    norm = lambda x: np.sqrt((x ** 2).sum((0, 1)))  # noqa: E731
+    bound, size = 2.0 ** -22 * np.sqrt(c.count) * norm(np.sqrt(near)), norm(want)
+    assert (bound < 1e-3 * size).all(), (bound / size).max()
+    off = norm(_np(dg) - want)
+    assert (off <= bound).all(), (off / bound).max()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("sizes", SIZES, ids=lambda s: "x".join(map(str, s)))
+def test_gates_gradients_as_a_whole(cuda_lib, sizes, dtype):
+    for gates in ("mixed", "none"):
+        c = Scan(cuda_lib, *sizes, dtype=dtype, seed=sum(sizes), gates=gates)
+        _near_dg(c, c.backward(c.forward()[2])[3])
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+def test_gates_gradients_as_a_whole_elsewhere(cuda_lib, dtype):
+    """Packed sequences, no states, many rows, heads in parts."""
+    for c in (Scan(cuda_lib, 1, 300, 4, 2, 72, 80, dtype=dtype, cu=[0, 0, 5, 5, 6, 134, 134, 263, 300], seed=40),
+              Scan(cuda_lib, 2, 150, 2, 1, 48, 64, dtype=dtype, state=False, dl=False, seed=41),
+              Scan(cuda_lib, 1, 1500, 2, 1, 80, 96, dtype=dtype, gates="mild", seed=42),
+              Scan(cuda_lib, 20, 129, 9, 1, 40, 24, dtype=dtype, seed=43)):
+        _near_dg(c, c.backward(c.forward()[2])[3])
