@@ -132,3 +132,73 @@ def test_gates_gradients_as_a_whole_elsewhere(cuda_lib, dtype):
               Scan(cuda_lib, 1, 1500, 2, 1, 80, 96, dtype=dtype, gates="mild", seed=42),
               Scan(cuda_lib, 20, 129, 9, 1, 40, 24, dtype=dtype, seed=43)):
         _near_dg(c, c.backward(c.forward()[2])[3])
+
+
+# --------------------------------------------- segments of many chunks (bf16)
+
+def _segments(mg, B, T, H, N, P, nseq, packed):
+    """How many segments the bf16 kernels cut a batch into, from what they save:
+    states of every chunk and segment, a float and two times 128 sums a chunk."""
+    state = -(-P // 4) * 4 * N
+    chunks = T // 128 + min(nseq, T) if packed else B * -(-T // 128)
+    rest = mg.load().mg_gated_scan_saved_size(B, T, H, N, P, nseq, packed, mg.MG_BF16) - chunks * H * (state * 4 + 1024) - -(-chunks * H * 4 // 16) * 16
+    assert rest % (H * state * 4) == 0
+    return rest // (H * state * 4)
+
+
+# heads' sizes: both above 64, with rows on 16-byte boundaries and without; one of them; none
+LONG = [(52, 1100, 2, 1, 128, 128), (52, 1100, 2, 2, 72, 72), (52, 1100, 2, 1, 71, 65), (104, 700, 2, 1, 128, 64), (52, 700, 2, 2, 40, 128),
+        (104, 700, 2, 1, 64, 64), (104, 700, 2, 2, 33, 17)]
+
+
+def _repeated(c, times, cu=None):
+    """The case's batch `times` times over: what every copy must give is the same."""
+    def more(x):
+        return None if x is None else torch.cat([x] * times, 1 if cu is not None and x.shape[0] == 1 and x is not c.S0 and x is not c.dl else 0)
+    args = [more(x) for x in (c.q, c.k, c.v, c.g, c.S0)]
+    kw = dict(scale=c.scale, cu_seqlens=cu)
+    oo, last, saved = c.mg.gated_scan_fwd(*args, **kw, save=True)
+    out = [oo, last, *c.mg.gated_scan_bwd(more(c.do), saved, *args, more(c.dl), **kw)]
+    plain = c.mg.gated_scan_fwd(*args, **kw)
+    assert torch.equal(plain[0], oo) and torch.equal(plain[1], last)
+    ones = []
+    for i, x in enumerate(out):
+        if x is None:
+            ones.append(None)
+            continue
+        parts = x.chunk(times, 1 if cu is not None and i not in (1, 6) else 0)
+        assert all(torch.equal(p, parts[0]) for p in parts[1:]), i
+        ones.append(parts[0])
+    return ones
+
+
+def _check_all(c, got):
+    want = [*o.scan_fwd(*c.args(), c.sp)[:2], *o.scan_bwd(c.ndo, *c.args(), c.ndl, c.sp)]
+    size = [*o.scan_fwd(*c.args(), c.sp, absolute=True)[:2], *o.scan_bwd(c.ndo, *c.args(), c.ndl, c.sp, absolute=True)]
+    for name, a, b, s in zip(("o", "S_last", "dq", "dk", "dv", "dg", "dS0"), got, want, size):
+        if a is not None:
+            _near(name, a, b, s, c.count + 128, name in ("o", "dq", "dk", "dv"))
+    _near_dg(c, got[5])
+
+
+@pytest.mark.parametrize("state", [True, False], ids=["states", "zeros"])
+@pytest.mark.parametrize("sizes", LONG, ids=lambda s: "x".join(map(str, s)))
+def test_segments_of_many_chunks(cuda_lib, sizes, state):
+    """Walks of six to nine chunks, the last one ragged, in one segment a sequence."""
+    B, T, H, G, N, P = sizes
+    assert _segments(cuda_lib, B, T, H, N, P, B, 0) == B
+    c = Scan(cuda_lib, 2, T, H, G, N, P, dtype=BF16, seed=sum(sizes), gates="mild", state=state, dl=state)
+    _check_all(c, _repeated(c, B // 2))
+
+
+@pytest.mark.parametrize("sizes", [(2, 1, 128, 128), (2, 2, 72, 72), (2, 1, 71, 65), (4, 2, 128, 64), (4, 1, 24, 40)], ids=lambda s: "x".join(map(str, s)))
+def test_segments_of_many_chunks_packed(cuda_lib, sizes):
+    """Sequences of one row to eleven chunks, most of them in a segment or two."""
+    H, G, N, P = sizes
+    lens, times = [1100, 1, 700, 0, 1400, 129], 12
+    cu = [0, *np.cumsum(lens)]
+    c = Scan(cuda_lib, 1, int(cu[-1]), H, G, N, P, dtype=BF16, cu=[int(x) for x in cu], seed=sum(sizes), gates="mild")
+    whole = torch.tensor([0, *np.cumsum(lens * times)], dtype=torch.int64, device=DEV)
+    T, n = int(whole[-1]), len(lens) * times
+    assert _segments(cuda_lib, 1, T, H, N, P, n, 1) - n <= T // (5 * 128)   # segments of five chunks or more
+    _check_all(c, _repeated(c, times, whole))
