@@ -13,6 +13,9 @@
  * Gates.  g (B,T,H), row stride ldg, is float32 whatever dt is: the logarithm
  *   of a row's decay, meant to be <= 0.  A gate below -128 counts as -128 (its
  *   decay, 2.6e-56, is 0 in float32); -inf forgets everything.
+ * Arithmetic.  Products of bf16 calls run on the tensor cores with float32 sums:
+ *   a factor that is no input (weights, states) goes in as bf16 pieces that add up
+ *   to 2^-16 of it where the result is an activation, to 2^-24 where it is float32.
  * Not-a-numbers.  The recurrence works on chunks of rows: an infinity or NaN in
  *   a row may make NaN of the rows of the same sequence and head after it, and
  *   of those before it in the same chunk of 128 rows (backwards the other way

@@ -9,13 +9,15 @@
 // Backwards the same with the adjoints, from the last chunk on.
 //
 // Rounding.  q, k, v and dout are bf16 as they are given, so their products are
-// exact in the tensor core's float32 sums.  A chunk's weights and the state are
-// rounded to bf16 where they meet an operand of the rows' outputs, which are
-// bf16 themselves (each term of an output has one of the two).  Where the result
-// is float32 (states, their adjoints, the gates' gradients) such a factor goes
-// in as the sum of three bf16 pieces, to 2^-24.  The smallest pieces are summed
-// first: the tensor core's sums lose up to a last bit of the sum at each step,
-// and the large piece first made dg's errors 1.2e-6 where they are 3e-7.
+// exact in the tensor core's float32 sums.  What they are multiplied with (a
+// chunk's weights, the state, its adjoint) goes in as a sum of bf16 pieces, two
+// where the result is bf16 (to 2^-16, so that the rounding at the store is the
+// only one that counts: with one piece o, dq, dk and dv were off by 2.3e-3 of
+// their norm where that rounding alone is 1.7e-3), three where it is float32
+// (states, their adjoints, the gates' gradients; to 2^-24).  There the smallest
+// pieces are summed first: the tensor core's sums lose up to a last bit of the sum
+// at each step, and the large piece first made dg's errors 1.2e-6 where they are
+// 3e-7.
 #include "gated_scan.cuh"
 #include "umma.cuh"
 
@@ -541,14 +543,16 @@ struct Weights {
 
 // ------------------------------------------------------------------- rows
 // A block: o of a chunk and head.  Q K^T, weights, times V, and Q S beside it;
-// the weights take Q's place in shared memory and V takes K's, so that two blocks
-// fit an SM and one's products run under the other's loads and exponentials.
+// the weights take Q's and the state's places in shared memory and V takes K's, so
+// that two blocks fit an SM and one's products run under the other's loads and
+// exponentials.  A state of 128 x 128 has room for one piece at a time.
 //
-// 77 us at 4x4096x16x128x128 (403 MB, 5.2 TB/s of 6.8; tensor pipe 14%): memory,
-// and a block's chain of set-up, state, products, weights, products and output,
-// 21000 cycles of which two blocks hide half.
+// 82 us at 4x4096x16x128x128 (403 MB, 4.9 TB/s of 6.8; 77 us with one piece of each
+// factor): memory, and a block's chain of set-up, state, products, weights,
+// products and output, of which two blocks hide half.
 
 constexpr int kRowThreads = 512;
+constexpr unsigned kRowsS = 2 * kPanelBytes;   // the state's place, then the weights' second pieces'
 
 struct RowsSmall {
     Weights w;
@@ -562,7 +566,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
     after_previous();
     extern __shared__ __align__(1024) char sm[];
     constexpr int NB = 64 * PN, PB = 64 * PP;
-    constexpr unsigned kQ = 2 * kPanelBytes, kK = (PN > PP ? PN : PP) * kPanelBytes, kS = PP * NB * 128;
+    constexpr unsigned kQ = 2 * kPanelBytes, kK = (PN > PP ? PN : PP) * kPanelBytes, kS = kRowsS;
     const GatedArgs &a = p.a;
     const unsigned tq = smem_addr(sm), tk = tq + kQ, ts = tk + kK;
     using Small = RowsSmall;
@@ -592,16 +596,22 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
         load_rows<PN, kRowThreads>(tq, static_cast<const bf16_t *>(a.q) + ch.row * a.ldq + grp * a.N, a.ldq, ch.len, a.N);
         load_rows<PN, kRowThreads>(tk, static_cast<const bf16_t *>(a.k) + ch.row * a.ldk + grp * a.N, a.ldk, ch.len, a.N);
     }
-    {   // the state, rounded: an operand of bf16 outputs
+    using Mine = Pieces8<NB, PP, kRowThreads>;
+    constexpr unsigned kState = PP * NB * 128;
+    constexpr bool kBoth = 2 * kState <= kS;   // both pieces of the state have room at once
+    uint4 rest[Mine::kMine];   // else the second ones wait until the first ones are read
+    {
         const Source s = source_of<false>(p, place_of<false>(p, ch, c), h);
-        using Mine = Pieces8<NB, PP, kRowThreads>;
         float f[Mine::kMine][8];
         fetch_states<Mine>(s, expf(reach_of(s)), a.N, a.P, f);
 #pragma unroll
-        for (int u = 0; u < Mine::kMine; ++u)
-            if (Mine::mine(u))
-                st_tile(ts, tile_at(NB, Mine::row(u), Mine::piece(u)),
-                        make_uint4(pack_bf16x2(f[u][0], f[u][1]), pack_bf16x2(f[u][2], f[u][3]), pack_bf16x2(f[u][4], f[u][5]), pack_bf16x2(f[u][6], f[u][7])));
+        for (int u = 0; u < Mine::kMine; ++u) {
+            uint4 v;
+            split2(f[u], v, rest[u]);
+            if (!Mine::mine(u)) continue;
+            st_tile(ts, tile_at(NB, Mine::row(u), Mine::piece(u)), v);
+            if constexpr (kBoth) st_tile(ts + kState, tile_at(NB, Mine::row(u), Mine::piece(u)), rest[u]);
+        }
     }
     if (VEC && tid == 64) {   // what the block that follows on this SM will read
         const int wrap = h + p.next_h >= a.H, cn = c + p.next_c + wrap, hn = h + p.next_h - (wrap ? a.H : 0);
@@ -626,7 +636,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
         if constexpr (VEC) wait_or_tell(&sh.full[0], 0, p.error);
         multiply(acc, Tile<kRows, false>{tq}, Tile<kRows, false>{tk}, kRows, steps, false);
         bar_after_products(&sh.done[0]);
-        multiply(acc_s, Tile<kRows, false>{tq}, Tile<NB, true>{ts}, PB, steps, false);
+        if constexpr (kBoth) multiply(acc_s, Tile<kRows, false>{tq}, Tile<NB, true>{ts + kState}, PB, steps, false);
+        multiply(acc_s, Tile<kRows, false>{tq}, Tile<NB, true>{ts}, PB, steps, kBoth);
         bar_after_products(&sh.done[1]);
     }
     wait_or_tell(&sh.gates, 0, p.error);
@@ -639,6 +650,18 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
         }
     } else {
         load_rows<PP, kRowThreads>(tk, static_cast<const bf16_t *>(a.v) + ch.row * a.ldv + h * a.P, a.ldv, ch.len, a.P);
+    }
+    if constexpr (!kBoth) {
+        wait_or_tell(&sh.done[1], 0, p.error);   // the first pieces are read
+#pragma unroll
+        for (int u = 0; u < Mine::kMine; ++u)
+            if (Mine::mine(u)) st_tile(ts, tile_at(NB, Mine::row(u), Mine::piece(u)), rest[u]);
+        fence_tiles();
+        __syncthreads();
+        if (tid == 0) {
+            multiply(acc_s, Tile<kRows, false>{tq}, Tile<NB, true>{ts}, PB, (a.N + 15) / 16, true);
+            bar_after_products(&sh.done[1]);
+        }
     }
     tmem_after_sync();
     {   // a block of 32 columns a warp; those above the diagonal are zeros
@@ -657,12 +680,15 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
 #pragma unroll
                 for (int u = 0; u < 4; ++u) w[e + u] = (e + u <= lane ? w[e + u] : 0.f) * by[u];
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) w[e] = 0.f;
         }
-        wait_or_tell(&sh.done[1], 0, p.error);   // Q is read: the weights may take its place
-        put<32>(tq, row, 4 * cb, w);
+        wait_or_tell(&sh.done[1], kBoth ? 0 : 1, p.error);   // Q and the state are read: the weights may take their places
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint4 v = make_uint4(0, 0, 0, 0), more = v;
+            if (cb <= rb) split2(w + 8 * i, v, more);
+            st_tile(tq, tile_at(kRows, row, 4 * cb + i), v);
+            st_tile(ts, tile_at(kRows, row, 4 * cb + i), more);
+        }
     }
     if constexpr (VEC) {
         wait_or_tell(&sh.full[1], 0, p.error);
@@ -673,7 +699,8 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
     __syncthreads();
     if (tid == 0) {
         tmem_after_sync();
-        multiply(acc, Tile<kRows, false>{tq}, Tile<kRows, true>{tk}, PB, (ch.len + 15) / 16, false);
+        multiply(acc, Tile<kRows, false>{ts}, Tile<kRows, true>{tk}, PB, (ch.len + 15) / 16, false);
+        multiply(acc, Tile<kRows, false>{tq}, Tile<kRows, true>{tk}, PB, (ch.len + 15) / 16, true);
         bar_after_products(&sh.done[0]);
     }
     const float up = Gates128::exp_of(hi + lo);
@@ -710,11 +737,12 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
 // SM; the adjoint's and the state's pieces share a place (kX), which for N and
 // P above 64 is the weights' too.
 //
-// 237 us at 4x4096x16x128x128 (738 MB, 3.1 TB/s; tensor pipe 19%), 155 us at
-// 2x4096x32x128x64 with shared q and k.  28000 and 22000 cycles a head: loads of
-// states 8500 (and 1500, where the next head's adjoint is copied ahead), products
-// 6000 and 4000, the rest weights, pieces and sums over rows between barriers;
-// shared memory is full with one block, so that nothing else runs beside them.
+// 258 us at 4x4096x16x128x128 (738 MB, 2.9 TB/s), 182 us at 2x4096x32x128x64 with
+// shared q and k (with one piece of the weights 237 and 155): 18.4 and 12.5 us a
+// head, of which the products' steps are 8200 and 5400 cycles; the rest is loads
+// of states (the next head's adjoint is copied ahead), weights, pieces and sums
+// over rows between barriers; shared memory is full with one block, so that
+// nothing else runs beside them.
 
 constexpr int kGradThreads = 1024;
 // The warp that begins the products: rows 0 to 31 and columns 112 on, which have
@@ -953,7 +981,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             bar_after_products(&sh.done[0]);
             if constexpr (M::kFirst) {
                 with_pieces(acc_k, tv);
-                multiply(acc_d, Tile<kRows, false>{tk}, Tile<NB, true>{tx}, PB, nsteps, false);
+                for (int k = 1; k >= 0; --k)
+                    multiply(acc_d, Tile<kRows, false>{tk}, Tile<NB, true>{tx + k * M::kState}, PB, nsteps, k < 1);
                 bar_after_products(&sh.done[1]);
             }
         }
@@ -963,10 +992,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
         products_done(0);
         // weights, and what each pair of rows gives to the gates between them: rows
         // from 32 rb, columns from 16 cb
-        float of_row = 0.f, of_col = 0.f, last = 0.f;
-        unsigned pw[8], pd[8];
+        float of_row = 0.f, of_col = 0.f, w[16], d[16];
         if (cb <= 2 * rb + 1) {
-            float s[16], d[16];
+            float s[16];
             tmem_load(acc0 + mine + 16 * cb, s);
             tmem_load(acc1 + mine + 16 * cb, d);
             const int first = 16 * cb - 32 * rb;   // columns up to lane - first reach the row
@@ -974,10 +1002,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
                 const float from = a.scale * sh.w.g.span(hi, lo, 32 * (cb >> 1) + 31);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    const float by = from * sh.w.to_end[16 * cb + j], w = s[j] * by;
-                    d[j] *= by, s[j] *= d[j], of_row += s[j];
-                    if (j & 1) pw[j / 2] = pack_bf16x2(last, w), pd[j / 2] = pack_bf16x2(d[j - 1], d[j]);
-                    last = w;
+                    const float by = from * sh.w.to_end[16 * cb + j];
+                    w[j] = s[j] * by, d[j] *= by, s[j] *= d[j], of_row += s[j];
                 }
             } else {
 #pragma unroll
@@ -989,53 +1015,73 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
                         const int j = e + u;
                         const bool in = first + j <= lane;   // what is behind may be a NaN
                         by[u] *= a.scale;
-                        const float w = (in ? s[j] : 0.f) * by[u];
+                        w[j] = (in ? s[j] : 0.f) * by[u];
                         d[j] = (in ? d[j] : 0.f) * by[u], s[j] = (first + j < lane ? s[j] : 0.f) * d[j], of_row += s[j];
-                        if (j & 1) pw[j / 2] = pack_bf16x2(last, w), pd[j / 2] = pack_bf16x2(d[j - 1], d[j]);
-                        last = w;
                     }
                 }
             }
             of_col = column_sums(s);
         } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) pw[e] = pd[e] = 0;
+            for (int e = 0; e < 16; ++e) w[e] = d[e] = 0.f;
         }
+        // the weights' two pieces, the second ones kept for later
+        uint4 w_rest[2], d_rest[2];
         const auto put_weights = [&]() {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                st_tile(tw, tile_at(kRows, row, 2 * cb + i), make_uint4(pw[4 * i], pw[4 * i + 1], pw[4 * i + 2], pw[4 * i + 3]));
-                st_tile(tdw, tile_at(kRows, row, 2 * cb + i), make_uint4(pd[4 * i], pd[4 * i + 1], pd[4 * i + 2], pd[4 * i + 3]));
+                uint4 v;
+                split2(w + 8 * i, v, w_rest[i]);
+                st_tile(tw, tile_at(kRows, row, 2 * cb + i), v);
+                split2(d + 8 * i, v, d_rest[i]);
+                st_tile(tdw, tile_at(kRows, row, 2 * cb + i), v);
             }
             row_part[cb * kRows + row] = of_row;
             if (lane < 16) col_part[rb * kRows + 16 * cb + lane] = of_col;
         };
+        const auto put_rest = [&](unsigned tile, const uint4 (&v)[2]) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) st_tile(tile, tile_at(kRows, row, 2 * cb + i), v[i]);
+        };
         float dv[16];   // K D's part of dv
+        // where the weights' second pieces lie
+        const unsigned tw2 = M::kFirst ? tv : tw, tdw2 = M::kFirst ? tdw + M::kW : tdw;
+        const auto sum_parts = [&]() {
+            if (tid < kRows) sh.after[tid] = of_blocks(row_part, 8) - of_blocks(col_part, 4);
+            if (M::kFirst && tid < kRows) sh.key[tid] = of_blocks(key_part, 8);
+        };
         if constexpr (M::kFirst) {
             products_done(1);
-            const float of = take(acc_k, acc_k, tail, tk, false);
+            put_weights();   // the adjoint's pieces are read, and V
+            put_rest(tw2, w_rest);
+            key_part[cb * kRows + row] = take(acc_k, acc_k, tail, tk, false);
             tmem_load(acc_d + mine + 16 * cb, dv);
-            put_weights();   // the adjoint's pieces are read
-            key_part[cb * kRows + row] = of;
+            __syncthreads();
+            sum_parts();
+            __syncthreads();
+            put_rest(tdw2, d_rest);
         } else {
             put_weights();
         }
         before_products();
         if (tid == 32 * kMmaWarp) {
             const bool add = hh > h0;
-            multiply(acc0, Tile<kRows, true>{tw}, Tile<kRows, true>{to}, PB, kRows / 16, false);
-            multiply(acc_q, Tile<kRows, false>{tdw}, Tile<kRows, true>{tk}, NB, kRows / 16, add);
+            if constexpr (M::kFirst) {
+                multiply(acc0, Tile<kRows, true>{tw2}, Tile<kRows, true>{to}, PB, kRows / 16, false);
+                multiply(acc_q, Tile<kRows, false>{tdw2}, Tile<kRows, true>{tk}, NB, kRows / 16, false);
+                multiply(acc_k, Tile<kRows, true>{tdw2}, Tile<kRows, true>{tq}, NB, kRows / 16, true);
+            }
+            multiply(acc0, Tile<kRows, true>{tw}, Tile<kRows, true>{to}, PB, kRows / 16, M::kFirst);
+            multiply(acc_q, Tile<kRows, false>{tdw}, Tile<kRows, true>{tk}, NB, kRows / 16, add || M::kFirst);
             multiply(acc_k, Tile<kRows, true>{tdw}, Tile<kRows, true>{tq}, NB, kRows / 16, add || M::kFirst);
             if constexpr (!M::kFirst) {
-                multiply(acc_d, Tile<kRows, false>{tk}, Tile<NB, true>{tx}, PB, nsteps, false);
+                for (int k = 1; k >= 0; --k)
+                    multiply(acc_d, Tile<kRows, false>{tk}, Tile<NB, true>{tx + k * M::kState}, PB, nsteps, k < 1);
                 with_pieces(acc1, tv);
             }
             bar_after_products(&sh.done[0]);
         }
-        if (tid < kRows) {
-            sh.after[tid] = of_blocks(row_part, 8) - of_blocks(col_part, 4);
-            if constexpr (M::kFirst) sh.key[tid] = of_blocks(key_part, 8);
-        }
+        if constexpr (!M::kFirst) sum_parts();
         fetch_states<Mine>(from_s, by_s, a.N, a.P, st);
         if constexpr (!M::kFirst) {   // D is the sum of its pieces
 #pragma unroll
@@ -1050,6 +1096,21 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             put_dot();
         }
         products_done(0);
+        if constexpr (!M::kFirst) {   // the weights' second pieces: in the first ones' places, where zeros stay
+            if (cb <= 2 * rb + 1) put_rest(tw2, w_rest), put_rest(tdw2, d_rest);
+            put_states();   // the adjoint's pieces are read
+            before_products();
+            if (tid == 32 * kMmaWarp) {
+                multiply(acc0, Tile<kRows, true>{tw2}, Tile<kRows, true>{to}, PB, kRows / 16, true);
+                multiply(acc_k, Tile<kRows, true>{tdw2}, Tile<kRows, true>{tq}, NB, kRows / 16, true);
+                bar_after_products(&sh.done[0]);
+            }
+            if (hh + 1 < h1) {   // of the next head
+                if (place_d.carry) reach_d = __ldg(from_d.reach + 1);
+                if (place_s.carry) reach_s = __ldg(from_s.reach + 1);
+            }
+            products_done(0);
+        }
         if (cb < PB / 16) {
             float x[16];
             tmem_load(acc0 + mine + 16 * cb, x);
@@ -1058,11 +1119,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             for (int e = 0; e < 16; ++e) x[e] = fmaf(tail, dv[e], x[e]);
             put<16>(tv, row, 2 * cb, x);   // V is read
         }
-        if constexpr (M::kFirst) __syncthreads();   // the parts of the sums are read
-        put_states();   // the adjoint's pieces and the weights are read
+        if constexpr (M::kFirst) put_states();   // the adjoint's pieces and the weights are read
         before_products();
         if (tid == 32 * kMmaWarp) {
             with_pieces(M::kFirst ? acc1 : acc0, to);   // what was in these is read
+            if constexpr (!M::kFirst) multiply(acc_q, Tile<kRows, false>{tdw2}, Tile<kRows, true>{tk}, NB, kRows / 16, true);
             bar_after_products(&sh.done[0]);
         }
         if constexpr (!M::kFirst) {
@@ -1072,12 +1133,6 @@ __global__ void __launch_bounds__(kGradThreads, 1) gated_grads_kernel(const __gr
             if (tid == 32) put_tile<PP>(p.dv, tv, h, int(ch.row));
         } else {
             store_rows<PP, kGradThreads, VEC>(static_cast<bf16_t *>(a.dv) + (ch.row * a.H + h) * a.P, int64_t(a.H) * a.P, tv, ch.len, a.P);
-        }
-        if constexpr (!M::kFirst) {
-            if (hh + 1 < h1) {   // of the next head
-                if (place_d.carry) reach_d = __ldg(from_d.reach + 1);
-                if (place_s.carry) reach_s = __ldg(from_s.reach + 1);
-            }
         }
         products_done(0);
         if constexpr (!M::kFirst) {
@@ -1286,7 +1341,7 @@ mg_status forward(const TcCall &p, cudaStream_t s)
 {
     MG_TRY((walk<PN, VEC, false>(p, s)));
     MG_TRY(over_segments<false>(p, p.a.S0, p.a.S_last, s));
-    constexpr size_t smem = 2 * kPanelBytes + (PN > PP ? PN : PP) * kPanelBytes + PP * PN * 64 * 128 + sizeof(RowsSmall);
+    constexpr size_t smem = 2 * kPanelBytes + (PN > PP ? PN : PP) * kPanelBytes + kRowsS + sizeof(RowsSmall);
     static_assert(2 * (smem + 1024) <= 228 * 1024, "two blocks an SM");
     MG_TRY((allow_shared<gated_rows_kernel<PN, PP, VEC>>(smem)));
     return launch_next("mg_gated_scan_fwd", gated_rows_kernel<PN, PP, VEC>, int64_t(p.c.most) * p.a.H, dim3(kRowThreads), smem, s, p);

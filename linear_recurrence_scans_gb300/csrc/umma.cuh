@@ -222,7 +222,25 @@ __device__ __forceinline__ void tmem_store(unsigned at, const float (&v)[16])
     asm volatile("tcgen05.wait::st.sync.aligned;" : : : "memory");
 }
 
-// -------------------------------------------------------- bf16 in 3 pieces
+// -------------------------------------------------------- bf16 in pieces
+
+// v = a + b with bf16 a, b to 2^-16 of v, two values at a time.
+struct Halves {
+    unsigned a, b;
+};
+__device__ __forceinline__ Halves split2(float x, float y)
+{
+    Halves p;
+    p.a = pack_bf16x2(x, y);
+    p.b = pack_bf16x2(x - __uint_as_float(p.a << 16), y - __uint_as_float(p.a & 0xffff0000u));
+    return p;
+}
+// Eight of them.
+__device__ __forceinline__ void split2(const float *v, uint4 &a, uint4 &b)
+{
+    const Halves p = split2(v[0], v[1]), q = split2(v[2], v[3]), r = split2(v[4], v[5]), s = split2(v[6], v[7]);
+    a = make_uint4(p.a, q.a, r.a, s.a), b = make_uint4(p.b, q.b, r.b, s.b);
+}
 
 // v = a + b + c with bf16 a, b, c to 2^-24 of v, two values at a time.
 struct Pieces {

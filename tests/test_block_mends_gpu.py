@@ -202,3 +202,21 @@ def test_segments_of_many_chunks_packed(cuda_lib, sizes):
     T, n = int(whole[-1]), len(lens) * times
     assert _segments(cuda_lib, 1, T, H, N, P, n, 1) - n <= T // (5 * 128)   # segments of five chunks or more
     _check_all(c, _repeated(c, times, whole))
+
+
+# ------------------------------------------------------- one rounding (bf16)
+
+@pytest.mark.parametrize("sizes", [(2, 300, 2, 1, 128, 128), (2, 300, 2, 2, 71, 65), (2, 300, 4, 2, 128, 64), (2, 300, 2, 1, 40, 128), (2, 300, 4, 1, 64, 64),
+                                   (2, 300, 4, 2, 23, 41), (20, 129, 9, 1, 40, 24)], ids=lambda s: "x".join(map(str, s)))
+def test_activations_are_rounded_once(cuda_lib, sizes):
+    """o, dq, dk and dv have the error of the exact values rounded at their store.
+    What their sums lose besides is 2^-16 of a term at a time, of no common sign:
+    2^-8 of the rounding's error, in quadrature 2^-17; some values near a border go
+    to the other side.  1% is ample; a rounding of operands of its own adds 41%."""
+    for state in (True, False):
+        c = Scan(cuda_lib, *sizes, dtype=BF16, seed=50 + sum(sizes), gates="mild", state=state, dl=state)
+        oo, _, saved = c.forward()
+        want = [o.scan_fwd(*c.args(), c.sp)[0], *o.scan_bwd(c.ndo, *c.args(), c.ndl, c.sp)[:3]]
+        for name, got, exact in zip(("o", "dq", "dk", "dv"), [oo, *c.backward(saved)[:3]], want):
+            once = np.linalg.norm(_np(torch.from_numpy(exact).bfloat16()) - exact)
+            assert np.linalg.norm(_np(got) - exact) <= 1.01 * once, (name, np.linalg.norm(_np(got) - exact) / once)
