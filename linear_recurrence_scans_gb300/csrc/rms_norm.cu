@@ -492,10 +492,10 @@ Rows rows_for(int64_t D, std::initializer_list<int64_t> lds)
 }
 
 // A warp takes rows of up to 4 vectors a lane (2 in the gradients, which hold more
-// for each), a block wider ones: 2 vectors a thread while that leaves 1024
-// threads at most, else 4 (single values: 4, 8 or 16).  One vector a thread was
-// slower: 8 bits of 32768 x 4096 bf16 rows 201 us against 167.  A flat row may
-// have a vector more than it fills.
+// for each), a block wider ones: 2 vectors a thread (single values: 4, 8 or 16).
+// One vector a thread was slower: 8 bits of 32768 x 4096 bf16 rows 201 us against
+// 167.  A flat row may have a vector more than it fills, which for the widest (from
+// 16378 channels on) is one more than 1024 threads hold: 4 a thread.
 Shape shape_for(Rows r, int64_t D, bool bwd)
 {
     const int64_t n = r == kSingle ? D : r == kFlat ? (D + 14) / 8 : D / 8;
@@ -557,24 +557,30 @@ mg_status bwd_most(const RmsArgs &p, const Shape &c, const Ring &r, cudaStream_t
     return launch_next("mg_rms_norm_bwd", rms_sum_kernel, ceil_div(p.D, 32), dim3(32, 32), 0, s, part, blocks, p.D, p.dw);
 }
 
-// Stages, and registers for the threads that the block has.
+// Stages, and registers for the threads that the block has, of those that a type's
+// rows come to (ring_for, shape_for).
 template <typename T, Rows R, int NV, bool WARP>
 mg_status bwd(const RmsArgs &p, const Shape &c, cudaStream_t s)
 {
+    constexpr bool kF32 = sizeof(T) == 4;
     const Ring r = ring_for(R, c, p.D, sizeof(T));
     if constexpr (R == kSingle) {
-        if (!WARP && c.threads > 512) return bwd_most<T, R, NV, WARP, 1, 1024>(p, c, r, s);
+        if constexpr (NV == 16)
+            if (c.threads > 512) return bwd_most<T, R, NV, WARP, 1, 1024>(p, c, r, s);
         return bwd_most<T, R, NV, WARP, 1, 512>(p, c, r, s);
+    } else if constexpr (WARP) {
+        if constexpr (kF32 && NV == 2)
+            if (r.stages == 2) return bwd_most<T, R, NV, WARP, 2, 256>(p, c, r, s);
+        return bwd_most<T, R, NV, WARP, 3, 256>(p, c, r, s);
+    } else if constexpr (NV == 4) {
+        return bwd_most<T, R, NV, WARP, kF32 ? 1 : 2, 1024>(p, c, r, s);
     } else {
-        if constexpr (!WARP) {
-            if (c.threads > 512) {
-                if (r.stages == 1) return bwd_most<T, R, NV, WARP, 1, 1024>(p, c, r, s);
-                return bwd_most<T, R, NV, WARP, 2, 1024>(p, c, r, s);
-            }
-            if (r.stages == 2) return bwd_most<T, R, NV, WARP, 2, 512>(p, c, r, s);
+        if constexpr (kF32)
+            if (r.stages == 1) return bwd_most<T, R, NV, WARP, 1, 1024>(p, c, r, s);
+        if (c.threads > 512) return bwd_most<T, R, NV, WARP, 2, 1024>(p, c, r, s);
+        if (r.stages == 2) return bwd_most<T, R, NV, WARP, 2, 512>(p, c, r, s);
+        if constexpr (!kF32)
             if (c.threads > 256) return bwd_most<T, R, NV, WARP, 3, 512>(p, c, r, s);
-        }
-        if (r.stages == 2) return bwd_most<T, R, NV, WARP, 2, 256>(p, c, r, s);
         return bwd_most<T, R, NV, WARP, 3, 256>(p, c, r, s);
     }
 }
@@ -589,8 +595,9 @@ mg_status fwd_shape(const RmsArgs &p, cudaStream_t s)
         return fwd<T, R, 4, true, Q>(p, c, s);
     }
     if constexpr (R != kSingle) {
-        if (c.nv == 2) return fwd<T, R, 2, false, Q>(p, c, s);
-        return fwd<T, R, 4, false, Q>(p, c, s);
+        if constexpr (R == kFlat)
+            if (c.nv == 4) return fwd<T, R, 4, false, Q>(p, c, s);
+        return fwd<T, R, 2, false, Q>(p, c, s);
     } else {
         if (c.nv == 4) return fwd<T, R, 4, false, Q>(p, c, s);
         if (c.nv == 8) return fwd<T, R, 8, false, Q>(p, c, s);
@@ -607,8 +614,9 @@ mg_status bwd_shape(const RmsArgs &p, cudaStream_t s)
         return bwd<T, R, 2, true>(p, c, s);
     }
     if constexpr (R != kSingle) {
-        if (c.nv == 2) return bwd<T, R, 2, false>(p, c, s);
-        return bwd<T, R, 4, false>(p, c, s);
+        if constexpr (R == kFlat)
+            if (c.nv == 4) return bwd<T, R, 4, false>(p, c, s);
+        return bwd<T, R, 2, false>(p, c, s);
     } else {
         if (c.nv == 4) return bwd<T, R, 4, false>(p, c, s);
         if (c.nv == 8) return bwd<T, R, 8, false>(p, c, s);

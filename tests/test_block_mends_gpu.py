@@ -220,3 +220,26 @@ def test_activations_are_rounded_once(cuda_lib, sizes):
         for name, got, exact in zip(("o", "dq", "dk", "dv"), [oo, *c.backward(saved)[:3]], want):
             once = np.linalg.norm(_np(torch.from_numpy(exact).bfloat16()) - exact)
             assert np.linalg.norm(_np(got) - exact) <= 1.01 * once, (name, np.linalg.norm(_np(got) - exact) / once)
+
+
+# -------------------------------------------------- launches of the norm
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS)
+@pytest.mark.parametrize("pad", [0, 3, 8])
+def test_norm_on_both_sides_of_each_launch(cuda_lib, dtype, pad):
+    """Widths around those where the kernels' shape changes: vectors a thread,
+    threads a block, rows copied ahead; and some between."""
+    mg = cuda_lib
+    edges = [32, 64, 128, 256, 498, 512, 1024, 2768, 4096, 5544, 8192, 8520, 16376]
+    widths = sorted({d + i for d in edges for i in (-8, -1, 0, 1, 2, 8) if 0 < d + i <= 16384} | {9, 700, 1111, 3001, 6000, 7001, 10000, 12345, 16378, 16383, 16384})
+    torch.manual_seed(60 + pad)
+    for D in widths:
+        x, res, dy, dr = (torch.randn(3, D + pad, device=DEV).to(dtype)[:, :D] for _ in range(4))
+        w = 1 + 0.1 * torch.randn(D, device=DEV)
+        y, r, rstd = mg.rms_norm_fwd(x, w, res)
+        dx, dw = mg.rms_norm_bwd(dy, rstd, r, w, dr)
+        args = (*(_np(t) for t in (dy, r, w)), 1e-5, _np(dr))
+        want = o.norm_fwd(_np(r), _np(w), 1e-5)[0]
+        _near(("y", D), y, want, np.abs(want), 8)
+        for name, a, b, s in zip(("dx", "dw"), (dx, dw), o.norm_bwd(*args), o.norm_bwd(*args, absolute=True)):
+            _near((name, D), a, b, s, D if name == "dx" else 3)
