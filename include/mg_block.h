@@ -47,7 +47,7 @@ mg_status mg_gated_scan_fwd(const void *q, int64_t ldq, const void *k, int64_t l
 
 /* Bytes of the workspace of mg_gated_scan_fwd (of mg_gated_scan_bwd with
  * bwd != 0) and of `saved`, for nseq sequences, packed or dense (0: invalid or
- * unsupported sizes). */
+ * unsupported sizes; nothing is saved of a batch without rows or heads either). */
 size_t mg_gated_scan_workspace_size(int64_t B, int64_t T, int64_t H, int64_t G, int64_t N,
                                     int64_t P, int64_t nseq, int packed, mg_dtype dt, int bwd);
 size_t mg_gated_scan_saved_size(int64_t B, int64_t T, int64_t H, int64_t N, int64_t P,

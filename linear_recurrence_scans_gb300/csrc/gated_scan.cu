@@ -511,8 +511,9 @@ __global__ void __launch_bounds__(256) gated_join_kernel(const float *part, int 
 // ------------------------------------------------------------------ tokens
 
 // Bytes bound it: the state is read and written once (256 x 32 heads of 128 x 64:
-// 82 us, 6.6 TB/s; one row of 16 heads of 128 x 128: 6.7 us, the latency of a launch
-// and of a load and a store).
+// 82 us, 6.6 TB/s).  One row of 16 heads of 128 x 128 takes 6.7 us: the latency of a
+// launch, and of a thread's four rounds of loads and stores, one behind the other,
+// on 16 of the SMs.
 // A block takes a row's head: a state of N x P, walked by rows of P values, VEC
 // a thread; the threads beside each other in P share an n, and the others' sums
 // are joined at the end.

@@ -265,11 +265,13 @@ __device__ __forceinline__ void wait_or_tell(uint64_t *bar, unsigned phase, unsi
 // (row n a lane, 16 columns a thread).  Each chunk adds K^T V~, the row weights
 // in V~'s three pieces; the next chunk's rows arrive meanwhile.
 //
-// 62 us at 4x4096x16x128x128 (264 MB, 4.3 TB/s; tensor pipe 21%).  A step is a
-// chain, V into pieces, products, the state, of about 7000 cycles, the same with
-// one block on an SM as with two; two blocks hide half of each other's.  Segments
-// cut the walks (of 32 chunks here) so that all SMs have two: with whole
-// sequences 107 us where segments took 67.
+// 62 us at 4x4096x16x128x128 (264 MB, 4.3 TB/s; tensor pipe 21%).  A step, V into
+// pieces, products, the state, is about 7000 cycles, the same with one block on an
+// SM as with two.  Only the state itself needs the step before; what makes the
+// steps a chain is that V's pieces have one place and each step two barriers.  Two
+// blocks hide half of each other's.  Segments cut the walks (of 32 chunks here, into
+// 256 blocks) so that most SMs have two: with whole sequences 107 us where segments
+// took 67.
 
 constexpr int kWalkThreads = 512, kGateWarp = 4;
 
@@ -735,7 +737,9 @@ __global__ void __launch_bounds__(kRowThreads, 2) gated_rows_kernel(const __grid
 // A block: a chunk, a group's heads (or a part of them), one after another: dv
 // and dg of each, dq and dk summed over them in tensor memory.  One block fits an
 // SM; the adjoint's and the state's pieces share a place (kX), which for N and
-// P above 64 is the weights' too.
+// P above 64 is the weights' too, with V's for what is left of them.  Else the
+// weights have a place for one piece at a time, and the second pieces' products
+// come between the first ones' and the state's.
 //
 // 258 us at 4x4096x16x128x128 (738 MB, 2.9 TB/s), 182 us at 2x4096x32x128x64 with
 // shared q and k (with one piece of the weights 237 and 155): 18.4 and 12.5 us a
